@@ -9,6 +9,7 @@
 //    every score within ~3e-4 of exact;
 //  * CUDA cores (simt.cu) for fp32 calls and any other shape; their intermediates
 //    are fp32.
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -16,6 +17,7 @@
 #include <algorithm>
 
 #include "mla_internal.h"
+#include "paged.h"
 #include "tc.h"
 #include "tc_internal.h"
 
@@ -56,6 +58,7 @@ float scale_of(const mla_dims *d) {
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }   // the paged calls' index arrays
 
 struct Range {
     uintptr_t lo, hi;
@@ -1049,6 +1052,150 @@ mla_status mla_lse_combine(mla_dtype out_dtype, int n_splits, int rows, int D, c
     g_last_path = 1;
     return cuda_status(launch_lse_combine(ty_of(out_dtype), n_splits, rows, D, part_out, part_lse, out, lse,
                                           (cudaStream_t)cuda_stream));
+}
+
+// ------------------------------------------------------------------ paged cache ----
+mla_status mla_paged_tables(int B, int page_size, int max_pages, int n_free, int n_tokens, const int *past_lens,
+                            const int *new_lens, const int *free_pages, int *block_table, int *kv_lens, int *cu_tokens,
+                            int *slots, int *positions, int *counts, void *cuda_stream) {
+    if (B < 0 || B > PAGED_MAX_BATCH || page_size < 1 || max_pages < 1 || n_free < 0 || n_tokens < 0 ||
+        (long)max_pages * page_size > INT_MAX)
+        return MLA_ERR_SHAPE;
+    const size_t e = sizeof(int);
+    Range in[] = {rng(past_lens, B * e), rng(new_lens, B * e), rng(free_pages, n_free * e)};
+    Range outs[] = {rng(block_table, (size_t)B * max_pages * e), rng(kv_lens, B * e), rng(cu_tokens, (B + 1) * e),
+                    rng(slots, n_tokens * e), rng(positions, n_tokens * e), rng(counts, 2 * e)};
+    if (!cu_tokens || !counts || (B && (!past_lens || !new_lens || !block_table || !kv_lens)) ||
+        (n_free && !free_pages) || (n_tokens && (!slots || !positions)))
+        return MLA_ERR_NULL;
+    for (const Range &r : in)
+        if (!aligned4((void *)r.lo)) return MLA_ERR_ALIGN;
+    for (const Range &r : outs)
+        if (!aligned4((void *)r.lo)) return MLA_ERR_ALIGN;
+    mla_status st = check_alias(in, 3, outs, 6);
+    if (st != MLA_OK) return st;
+    g_last_path = 1;
+    return cuda_status(launch_paged_tables(B, page_size, max_pages, n_free, n_tokens, past_lens, new_lens, free_pages,
+                                           block_table, kv_lens, cu_tokens, slots, positions, counts,
+                                           (cudaStream_t)cuda_stream));
+}
+
+mla_status mla_paged_append(const mla_dims *dims, mla_dtype dtype, int n_tokens, int num_pages, int page_size,
+                            const void *c_kv, long c_stride, const void *k_pe, long k_stride, const void *rms_w,
+                            const int *slots, const int *positions, void *c_cache, void *kpe_cache, void *cuda_stream) {
+    mla_status st = check_dims(dims);
+    if (st != MLA_OK) return st;
+    if (!valid_dtype(dtype)) return MLA_ERR_DTYPE;
+    const int Dk = dims->d_kv, Dr = dims->d_rope;
+    if (n_tokens < 0 || num_pages < 1 || page_size < 1 || (long)num_pages * page_size > INT_MAX || c_stride < Dk ||
+        k_stride < Dr || c_stride > INT_MAX || k_stride > INT_MAX)
+        return MLA_ERR_SHAPE;
+    if (Dr > 640) return MLA_ERR_UNSUPPORTED;
+    if (n_tokens == 0) return MLA_OK;
+    const void *ptrs[] = {c_kv, k_pe, rms_w, c_cache, kpe_cache};
+    for (const void *q : ptrs)
+        if (!q) return MLA_ERR_NULL;
+    if (!slots || !positions) return MLA_ERR_NULL;
+    for (const void *q : ptrs)
+        if (!aligned16(q)) return MLA_ERR_ALIGN;
+    if (!aligned4(slots) || !aligned4(positions)) return MLA_ERR_ALIGN;
+    const size_t es = ty_size(ty_of(dtype)), n_slots = (size_t)num_pages * page_size;
+    Range in[] = {rng(c_kv, ((size_t)(n_tokens - 1) * c_stride + Dk) * es),
+                  rng(k_pe, ((size_t)(n_tokens - 1) * k_stride + Dr) * es), rng(rms_w, Dk * es),
+                  rng(slots, n_tokens * sizeof(int)), rng(positions, n_tokens * sizeof(int))};
+    Range outs[] = {rng(c_cache, n_slots * Dk * es), rng(kpe_cache, n_slots * Dr * es)};
+    st = check_alias(in, 5, outs, 2);
+    if (st != MLA_OK) return st;
+    g_last_path = 1;
+    return cuda_status(launch_paged_append(ty_of(dtype), n_tokens, (long)n_slots, Dk, Dr, dims->rope_base, dims->rms_eps,
+                                           c_kv, c_stride, k_pe, k_stride, rms_w, slots, positions, c_cache, kpe_cache,
+                                           (cudaStream_t)cuda_stream));
+}
+
+namespace {
+mla_status paged_decode_shape(const mla_dims *d, mla_dtype dt, int B, int page_size, int max_pages, PagedDecode *p) {
+    mla_status st = check_dims(d);
+    if (st != MLA_OK) return st;
+    if (!valid_dtype(dt)) return MLA_ERR_DTYPE;
+    if (B < 0 || page_size < 1 || max_pages < 1 || (long)max_pages * page_size > INT_MAX ||
+        ((long)B + 3) * d->n_heads > INT_MAX)
+        return MLA_ERR_SHAPE;
+    p->B = B;
+    p->H = d->n_heads;
+    p->Dk = d->d_kv;
+    p->Dn = d->d_nope;
+    p->Dr = d->d_rope;
+    p->Dv = d->d_v;
+    if (p->Dk + p->Dr > 640 || p->Dk > 512 || p->Dn > 1024) return MLA_ERR_UNSUPPORTED;
+    p->page = page_size;
+    p->max_pages = max_pages;
+    p->ty = ty_of(dt);
+    p->scale = scale_of(d);
+    p->base = d->rope_base;
+    p->row_tile = 16;
+    p->row_tiles = (p->H + 15) / 16;
+    p->tile = 32;
+    p->workers = 152;
+    p->min_tiles = 2;
+    return MLA_OK;
+}
+
+size_t paged_decode_ws(PagedDecode *p, void *base) {
+    Carve c;
+    c.base = (char *)base;
+    const size_t rows = (size_t)p->B * p->H, slots = (size_t)p->workers + (size_t)p->B * p->row_tiles;
+    p->tile_off = (long *)c.take(((size_t)p->B + 1) * sizeof(long));
+    p->qabs = c.take(rows * p->Dk * 4);
+    p->qpe = c.take(rows * p->Dr * 4);
+    p->po = (float *)c.take(slots * p->row_tile * p->Dk * 4);
+    p->pl = (float *)c.take(slots * p->row_tile * 4);
+    return align_up(c.off, 256);
+}
+}  // namespace
+
+size_t mla_paged_decode_workspace(const mla_dims *dims, mla_dtype dtype, int B, int page_size, int max_pages) {
+    PagedDecode p{};
+    if (paged_decode_shape(dims, dtype, B, page_size, max_pages, &p) != MLA_OK || B == 0) return 0;
+    return paged_decode_ws(&p, nullptr);
+}
+
+mla_status mla_paged_decode(const mla_dims *dims, mla_dtype dtype, int B, int num_pages, int page_size, int max_pages,
+                            const void *q_nope, const void *q_pe, const void *c_cache, const void *kpe_cache,
+                            const int *block_table, const int *kv_lens, const void *w_kv_b, void *out, float *lse,
+                            void *workspace, size_t workspace_bytes, void *cuda_stream) {
+    PagedDecode p{};
+    mla_status st = paged_decode_shape(dims, dtype, B, page_size, max_pages, &p);
+    if (st != MLA_OK) return st;
+    if (num_pages < 1 || (long)num_pages * page_size > INT_MAX) return MLA_ERR_SHAPE;
+    if (B == 0) return MLA_OK;
+    const void *ptrs[] = {q_nope, q_pe, c_cache, kpe_cache, w_kv_b, out, lse, workspace};
+    for (const void *q : ptrs)
+        if (!q) return MLA_ERR_NULL;
+    if (!block_table || !kv_lens) return MLA_ERR_NULL;
+    for (const void *q : ptrs)
+        if (!aligned16(q)) return MLA_ERR_ALIGN;
+    if (!aligned4(block_table) || !aligned4(kv_lens)) return MLA_ERR_ALIGN;
+    const size_t need = paged_decode_ws(&p, workspace);
+    if (workspace_bytes < need) return MLA_ERR_WORKSPACE;
+    const size_t es = ty_size(p.ty), rows = (size_t)B * p.H, keys = (size_t)num_pages * page_size;
+    Range in[] = {rng(q_nope, rows * p.Dn * es), rng(q_pe, rows * p.Dr * es), rng(c_cache, keys * p.Dk * es),
+                  rng(kpe_cache, keys * p.Dr * es), rng(block_table, (size_t)B * max_pages * sizeof(int)),
+                  rng(kv_lens, B * sizeof(int)), rng(w_kv_b, (size_t)p.H * (p.Dn + p.Dv) * p.Dk * es)};
+    Range outs[] = {rng(out, rows * p.Dv * es), rng(lse, rows * 4), rng(workspace, need)};
+    st = check_alias(in, 7, outs, 3);
+    if (st != MLA_OK) return st;
+    p.num_pages = num_pages;
+    p.q_nope = q_nope;
+    p.q_pe = q_pe;
+    p.c_cache = c_cache;
+    p.kpe_cache = kpe_cache;
+    p.w = w_kv_b;
+    p.table = block_table;
+    p.lens = kv_lens;
+    p.out = out;
+    p.lse = lse;
+    g_last_path = 1;
+    return cuda_status(paged_decode_simt(p, (cudaStream_t)cuda_stream));
 }
 
 const char *mla_status_string(mla_status s) {

@@ -1,0 +1,41 @@
+// paged.h -- host interface of the paged-cache kernels (paged.cu, paged_simt.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace mla {
+
+constexpr int PAGED_MAX_BATCH = 16384;   // requests of one mla_paged_tables call (its prefix sums stay in shared memory)
+
+cudaError_t launch_paged_tables(int B, int page, int max_pages, int n_free, int n_tokens, const int *past,
+                                const int *fresh, const int *free_pages, int *table, int *kv_lens, int *cu, int *slots,
+                                int *positions, int *counts, cudaStream_t st);
+
+// c rows at c + t * c_stride elements, k rows at k + t * k_stride.
+cudaError_t launch_paged_append(int ty, int T, long n_slots, int Dk, int Dr, float base, float eps, const void *c,
+                                long c_stride, const void *k, long k_stride, const void *w, const int *slots,
+                                const int *positions, void *c_cache, void *kpe_cache, cudaStream_t st);
+
+// One decode call.  A work item is (request b, row tile of `row_tile` heads); its keys are cut
+// into tiles of `tile` keys, all items' tiles are numbered through, and worker c of W takes tiles
+// [c T / W, (c + 1) T / W).  The part of item i that worker c computes goes to partial slot
+// c + i: unique, because going along the tiles every cut raises c or i.
+struct PagedDecode {
+    int B, H, Dk, Dn, Dr, Dv;
+    int num_pages, page, max_pages;
+    int ty;
+    float scale, base;
+    const void *q_nope, *q_pe, *c_cache, *kpe_cache, *w;
+    const int *table, *lens;
+    void *out;
+    float *lse;
+    int row_tile, row_tiles, tile;   // heads per item, items per request, keys per tile
+    int workers, min_tiles;          // most workers, fewest tiles that make one worker more
+    long *tile_off;                  // [B + 1] first tile of request b, for one row tile
+    void *qabs, *qpe;                // absorbed and rotated queries
+    float *po, *pl;                  // partials [workers + B row_tiles][row_tile][Dk], [..][row_tile]
+};
+cudaError_t paged_decode_simt(const PagedDecode &p, cudaStream_t st);
+
+}  // namespace mla

@@ -1,0 +1,110 @@
+// paged_common.cuh -- device code shared by the paged-cache kernels: rotation angles, the
+// division of a ragged batch among workers, element access.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "mla_internal.h"
+#include "paged.h"
+
+namespace mla {
+namespace paged {
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// RoPE angles in turns, as 64-bit fixed point: frequency t turns base^(-2t/Dr) / (2 pi) per
+// position, kept modulo one turn in 64 bits.  pos * turns modulo 2^64 is then the angle's exact
+// fraction of a turn (to pos * 2^-53 of the frequency's own rounding), at any 32-bit position and
+// without a double-precision operation on the device.
+constexpr int MAX_HALF = 320;   // d_rope <= 640
+struct Turns {
+    unsigned long long v[MAX_HALF];
+};
+__device__ __forceinline__ float2 turn_cs(unsigned long long turns, int pos) {
+    const long long x = (long long)(turns * (unsigned long long)(long long)pos);
+    float s, c;
+    sincospif((float)(int)(x >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31 half turns
+    return make_float2(c, s);
+}
+
+// Workers that take part for T tiles, and the first tile of worker c.
+__device__ __forceinline__ int active_workers(const PagedDecode &p, long T) {
+    const long w = (T + p.min_tiles - 1) / p.min_tiles;
+    return (int)(w < p.workers ? w : p.workers);
+}
+// The worker whose range holds tile t: the largest c with floor(c T / W) <= t.
+__device__ __forceinline__ int worker_of(long t, long T, int W) { return (int)(((t + 1) * W - 1) / T); }
+
+// A request's keys: its length cut to what its table row can hold.
+__device__ __forceinline__ int keys_of(const PagedDecode &p, int b) {
+    const int cap = p.max_pages * p.page;   // checked to fit by the caller
+    return min(max(p.lens[b], 0), cap);
+}
+
+// The tile prefix sums of all requests, by one block of NT threads.
+template <int NT>
+__device__ void plan_block(const PagedDecode &p) {
+    __shared__ long warp_tot[NT / 32];
+    const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
+    long carry = 0;
+    for (int b0 = 0; b0 < p.B; b0 += NT) {
+        const int b = b0 + tid;
+        const long n = b < p.B ? (keys_of(p, b) + p.tile - 1) / p.tile : 0;
+        long x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) warp_tot[wp] = x;
+        __syncthreads();
+        long before = carry, all = carry;
+#pragma unroll
+        for (int i = 0; i < NT / 32; ++i) {
+            if (i < wp) before += warp_tot[i];
+            all += warp_tot[i];
+        }
+        if (b < p.B) p.tile_off[b] = before + x - n;
+        carry = all;
+        __syncthreads();
+    }
+    if (tid == 0) p.tile_off[p.B] = carry;
+}
+
+// The request whose tiles (for all its row tiles) hold tile t < T.
+__device__ __forceinline__ int request_of(const PagedDecode &p, long t) {
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {   // the last b whose first tile is <= t: empty requests before it share that tile
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(p.tile_off + mid) * p.row_tiles <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+}  // namespace paged
+
+// The frequencies of Turns for one base and width (host).
+void paged_turns(float base, int Dr, unsigned long long *v);
+
+}  // namespace mla

@@ -1,0 +1,315 @@
+// paged_simt.cu -- one-token decode over the paged latent cache on the CUDA cores: fp32, and bf16
+// at dimensions or page sizes that the tensor-core kernels do not take.  fp32 arithmetic.
+//
+// Three launches: absorb (q_abs = W_K^T q_nope, the query's rotation, the division of the batch
+// among the workers), attention (each worker walks its key tiles with the running maximum and sum
+// of the softmax and writes one normalised partial per request it met), join (the partials'
+// log-sum-exp merge and out = W_V o).
+#include <algorithm>
+
+#include "paged_common.cuh"
+
+namespace mla {
+namespace {
+
+using namespace paged;
+
+constexpr int NT = 256;         // threads
+constexpr int HT = 16;          // heads per work item
+constexpr int KT = 32;          // keys per tile
+constexpr int DK_MAX = 512, DQ_MAX = 640;
+constexpr int BT = 4;           // requests per block of the two weight products
+
+// ------------------------------------------------------------------------ absorb ----
+// Block (h, group of BT requests): a thread owns latent dims and walks the rows of W_K(h), each
+// weight read once per group.  One block more forms the tile prefix sums.
+template <typename T>
+__global__ void __launch_bounds__(NT) paged_absorb_simt_kernel(const __grid_constant__ PagedDecode p,
+                                                               const __grid_constant__ Turns turns) {
+    extern __shared__ float sm[];
+    const int tid = threadIdx.x;
+    const int groups = (p.B + BT - 1) / BT;
+    if (blockIdx.x == (unsigned)(groups * p.H)) {
+        plan_block<NT>(p);
+        return;
+    }
+    const int h = blockIdx.x / groups, b0 = (blockIdx.x % groups) * BT, nb = min(BT, p.B - b0);
+    for (int i = tid; i < BT * p.Dn; i += NT) {
+        const int j = i / p.Dn, n = i % p.Dn;
+        sm[i] = j < nb ? to_f<T>(((const T *)p.q_nope)[((long)(b0 + j) * p.H + h) * p.Dn + n]) : 0.f;
+    }
+    const int half = p.Dr / 2;
+    for (int i = tid; i < nb * half; i += NT) {   // the query sits at its request's last key
+        const int j = i / half, t = i % half;
+        const long row = (long)(b0 + j) * p.H + h;
+        const float2 cs = turn_cs(turns.v[t], keys_of(p, b0 + j) - 1);
+        const T *x = (const T *)p.q_pe + row * p.Dr;
+        const float x0 = to_f<T>(x[t]), x1 = to_f<T>(x[t + half]);
+        float *y = (float *)p.qpe + row * p.Dr;
+        y[t] = x0 * cs.x - x1 * cs.y;
+        y[t + half] = x1 * cs.x + x0 * cs.y;
+    }
+    __syncthreads();
+    const T *w = (const T *)p.w + (long)h * (p.Dn + p.Dv) * p.Dk;
+    for (int d = tid; d < p.Dk; d += NT) {
+        float acc[BT] = {};
+        for (int n = 0; n < p.Dn; ++n) {
+            const float v = to_f<T>(w[(long)n * p.Dk + d]);
+#pragma unroll
+            for (int j = 0; j < BT; ++j) acc[j] = fmaf(v, sm[j * p.Dn + n], acc[j]);
+        }
+        for (int j = 0; j < nb; ++j) ((float *)p.qabs)[((long)(b0 + j) * p.H + h) * p.Dk + d] = acc[j];
+    }
+}
+
+// --------------------------------------------------------------------- attention ----
+// Scores: 16 heads x 32 keys of a tile; the 640 query dims are cut among the 8 warps in chunks of
+// four, each lane holding 4 heads x 4 keys, and the warps' sums meet in shared memory (eight
+// 16-byte shared loads feed 64 FMAs).  Values: a thread owns two latent dims of every head.
+struct Lay {   // shared memory, in floats
+    int dqp, q, k, s, flag, total;
+};
+__host__ __device__ inline Lay layout(int Dq) {
+    Lay l;
+    l.dqp = (Dq + 3) / 4 * 4 + 4;   // row pitch: rows four banks apart
+    l.q = 0;
+    l.k = HT * l.dqp;
+    l.s = l.k + KT * l.dqp;
+    l.flag = l.s + 8 * HT * KT;
+    l.total = l.flag + KT + 3 * HT;
+    return l;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_constant__ PagedDecode p) {
+    extern __shared__ float sm[];
+    const int Dq = p.Dk + p.Dr;
+    const Lay L = layout(Dq);
+    float *sQ = sm + L.q, *sK = sm + L.k, *sS = sm + L.s;
+    int *sRow = (int *)(sm + L.flag);                   // the keys' cache rows, -1 = no key
+    float *sM = sm + L.flag + KT, *sL = sM + HT, *sA = sL + HT;   // running maximum, sum, rescale
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const long total = p.tile_off[p.B] * p.row_tiles;
+    if (total == 0) return;
+    const int W = active_workers(p, total);
+    if ((int)blockIdx.x >= W) return;
+    long t = (long)blockIdx.x * total / W;
+    const long tend = (long)(blockIdx.x + 1) * total / W;
+    const int chunks = (Dq + 3) / 4;
+    while (t < tend) {
+        const int b = request_of(p, t);
+        const long first = p.tile_off[b], per = p.tile_off[b + 1] - first;
+        const int rt = (int)((t - first * p.row_tiles) / per);
+        const long k0 = (t - first * p.row_tiles) % per;        // first tile of the item here
+        const long k1 = min(per, k0 + tend - t);
+        const int keys = keys_of(p, b), h0 = rt * HT, nh = min(HT, p.H - h0);
+        __syncthreads();
+        for (int i = tid; i < HT * L.dqp; i += NT) {
+            const int h = i / L.dqp, d = i % L.dqp;
+            float v = 0.f;
+            if (h < nh && d < Dq) {
+                const long row = (long)b * p.H + h0 + h;
+                v = d < p.Dk ? ((const float *)p.qabs)[row * p.Dk + d] : ((const float *)p.qpe)[row * p.Dr + d - p.Dk];
+            }
+            sQ[i] = v;
+        }
+        if (tid < HT) {
+            sM[tid] = -INFINITY;
+            sL[tid] = 0.f;
+        }
+        float o[HT][2];
+#pragma unroll
+        for (int h = 0; h < HT; ++h) o[h][0] = o[h][1] = 0.f;
+        for (long kt = k0; kt < k1; ++kt) {
+            const int key0 = (int)kt * KT;
+            __syncthreads();   // the previous tile has been read
+            if (tid < KT) {
+                int row = -1;
+                const int key = key0 + tid;
+                if (key < keys) {
+                    const int id = p.table[(long)b * p.max_pages + key / p.page];
+                    if (id >= 0 && id < p.num_pages) row = id * p.page + key % p.page;
+                }
+                sRow[tid] = row;
+            }
+            __syncthreads();
+            for (int k = warp; k < KT; k += NT / 32) {   // a warp per key row; absent keys as zeros
+                const int row = sRow[k];
+                const T *c = (const T *)p.c_cache + (long)row * p.Dk, *r = (const T *)p.kpe_cache + (long)row * p.Dr;
+                for (int d = lane; d < L.dqp; d += 32) {
+                    float v = 0.f;
+                    if (row >= 0 && d < Dq) v = d < p.Dk ? to_f<T>(c[d]) : to_f<T>(r[d - p.Dk]);
+                    sK[k * L.dqp + d] = v;
+                }
+            }
+            __syncthreads();
+            {
+                const int hg = lane >> 3, kg = lane & 7;   // heads 4 hg .., keys kg, kg + 8, ..
+                float acc[4][4] = {};
+                for (int c = warp; c < chunks; c += NT / 32) {
+                    float4 q[4], k[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) q[i] = *(const float4 *)(sQ + (4 * hg + i) * L.dqp + 4 * c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) k[i] = *(const float4 *)(sK + (kg + 8 * i) * L.dqp + 4 * c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            acc[i][j] = fmaf(q[i].x, k[j].x, acc[i][j]);
+                            acc[i][j] = fmaf(q[i].y, k[j].y, acc[i][j]);
+                            acc[i][j] = fmaf(q[i].z, k[j].z, acc[i][j]);
+                            acc[i][j] = fmaf(q[i].w, k[j].w, acc[i][j]);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sS[(warp * HT + 4 * hg + i) * KT + kg + 8 * j] = acc[i][j];
+            }
+            __syncthreads();
+            for (int h = warp; h < HT; h += NT / 32) {   // a warp per head, a lane per key
+                float s = 0.f;
+#pragma unroll
+                for (int w = 0; w < NT / 32; ++w) s += sS[(w * HT + h) * KT + lane];
+                s = sRow[lane] >= 0 ? s * p.scale : -INFINITY;
+                float m = s;
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                const float mo = sM[h], mn = fmaxf(mo, m);
+                const float e = s == -INFINITY ? 0.f : expf(s - mn);   // a NaN score stays one
+                const float sum = warp_sum(e);
+                __syncwarp();
+                sS[h * KT + lane] = e;   // warp w's own slice of head h is read; slice 0 takes P
+                if (lane == 0) {
+                    const float al = mo == -INFINITY ? 0.f : expf(mo - mn);
+                    sM[h] = mn;
+                    sL[h] = sL[h] * al + sum;
+                    sA[h] = al;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < HT; ++h) {
+                o[h][0] *= sA[h];
+                o[h][1] *= sA[h];
+            }
+            if (2 * tid < p.Dk) {
+                for (int k = 0; k < KT; k += 4) {
+                    float2 v[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = *(const float2 *)(sK + (k + j) * L.dqp + 2 * tid);
+#pragma unroll
+                    for (int h = 0; h < HT; ++h) {
+                        const float4 w = *(const float4 *)(sS + h * KT + k);
+                        o[h][0] = fmaf(w.x, v[0].x, fmaf(w.y, v[1].x, fmaf(w.z, v[2].x, fmaf(w.w, v[3].x, o[h][0]))));
+                        o[h][1] = fmaf(w.x, v[0].y, fmaf(w.y, v[1].y, fmaf(w.z, v[2].y, fmaf(w.w, v[3].y, o[h][1]))));
+                    }
+                }
+            }
+        }
+        const long slot = (long)blockIdx.x + (long)b * p.row_tiles + rt;
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+            const float inv = sL[h] == 0.f ? 0.f : 1.f / sL[h];
+            float *po = p.po + (slot * HT + h) * p.Dk + 2 * tid;
+            if (h < nh && 2 * tid < p.Dk) {
+                po[0] = o[h][0] * inv;
+                if (2 * tid + 1 < p.Dk) po[1] = o[h][1] * inv;
+            }
+        }
+        if (tid < nh) p.pl[slot * HT + tid] = sL[tid] == 0.f ? -INFINITY : sM[tid] + logf(sL[tid]);
+        t += k1 - k0;
+    }
+}
+
+// -------------------------------------------------------------------------- join ----
+template <typename T>
+__global__ void __launch_bounds__(NT) paged_join_simt_kernel(const __grid_constant__ PagedDecode p) {
+    extern __shared__ float sm[];   // o [BT][Dk]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int groups = (p.B + BT - 1) / BT;
+    const int h = blockIdx.x / groups, b0 = (blockIdx.x % groups) * BT, nb = min(BT, p.B - b0);
+    const int rt = h / p.row_tile, r = h % p.row_tile;
+    const long total = p.tile_off[p.B] * p.row_tiles;
+    const int W = total ? active_workers(p, total) : 0;
+    for (int j = 0; j < nb; ++j) {
+        const int b = b0 + j;
+        const long per = p.tile_off[b + 1] - p.tile_off[b], first = p.tile_off[b] * p.row_tiles + rt * per;
+        const long item = (long)b * p.row_tiles + rt;
+        float m = -INFINITY, sum = 0.f;
+        int c0 = 0, c1 = -1;
+        if (per > 0) {
+            c0 = worker_of(first, total, W);
+            c1 = worker_of(first + per - 1, total, W);
+            for (int c = c0; c <= c1; ++c) m = fmaxf(m, p.pl[(c + item) * p.row_tile + r]);
+            for (int c = c0; c <= c1; ++c) {
+                const float x = p.pl[(c + item) * p.row_tile + r];
+                if (x != -INFINITY) sum += expf(x - m);
+            }
+        }
+        const float lse = sum == 0.f ? -INFINITY : m + logf(sum);
+        for (int d = tid; d < p.Dk; d += NT) {
+            float o = 0.f;
+            if (sum != 0.f)
+                for (int c = c0; c <= c1; ++c) {
+                    const long s = (c + item) * p.row_tile + r;
+                    if (p.pl[s] != -INFINITY) o = fmaf(expf(p.pl[s] - lse), p.po[s * p.Dk + d], o);
+                }
+            sm[j * p.Dk + d] = o;
+        }
+        if (tid == 0) p.lse[(long)b * p.H + h] = lse;
+    }
+    __syncthreads();
+    const T *w = (const T *)p.w + ((long)h * (p.Dn + p.Dv) + p.Dn) * p.Dk;
+    for (int v = warp; v < p.Dv; v += NT / 32) {
+        float acc[BT] = {};
+        for (int d = lane; d < p.Dk; d += 32) {
+            const float x = to_f<T>(w[(long)v * p.Dk + d]);
+#pragma unroll
+            for (int j = 0; j < BT; ++j)
+                if (j < nb) acc[j] = fmaf(x, sm[j * p.Dk + d], acc[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < BT; ++j) {
+            const float s = warp_sum(acc[j]);
+            if (lane == 0 && j < nb) ((T *)p.out)[((long)(b0 + j) * p.H + h) * p.Dv + v] = from_f<T>(s);
+        }
+    }
+}
+
+template <typename T>
+cudaError_t decode_simt(const PagedDecode &p, cudaStream_t st) {
+    Turns turns{};
+    paged_turns(p.base, p.Dr, turns.v);
+    const unsigned blocks = (unsigned)((p.B + BT - 1) / BT) * (unsigned)p.H;
+    const size_t s1 = (size_t)BT * p.Dn * 4, s2 = (size_t)layout(p.Dk + p.Dr).total * 4, s3 = (size_t)BT * p.Dk * 4;
+    cudaError_t e;
+    if ((e = cudaFuncSetAttribute(paged_absorb_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1)) != cudaSuccess)
+        return e;
+    if ((e = cudaFuncSetAttribute(paged_attn_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2)) != cudaSuccess)
+        return e;
+    {
+        ProfScope ps("paged_absorb", st);
+        paged_absorb_simt_kernel<T><<<blocks + 1, NT, s1, st>>>(p, turns);
+    }
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    {
+        ProfScope ps("paged_attn", st);
+        paged_attn_simt_kernel<T><<<p.workers, NT, s2, st>>>(p);
+    }
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    {
+        ProfScope ps("paged_join", st);
+        paged_join_simt_kernel<T><<<blocks, NT, s3, st>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t paged_decode_simt(const PagedDecode &p, cudaStream_t st) {
+    return p.ty == TY_F32 ? decode_simt<float>(p, st) : decode_simt<__nv_bfloat16>(p, st);
+}
+
+}  // namespace mla

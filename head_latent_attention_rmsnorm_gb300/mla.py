@@ -6,7 +6,8 @@ Two layers, argument marshalling only:
   ``mla_status_string``, ``mla_check_device_error``: the C entry points under their
   own names, taking integers for pointers and sizes.
 * ``latent_attn_fwd``, ``absorbed_attn_fwd``, ``decode_splitkv``, ``lse_combine``,
-  ``tpla_decode``, ``rmsnorm``, ``rmsnorm_bwd``:
+  ``tpla_decode``, ``rmsnorm``, ``rmsnorm_bwd``, ``paged_tables``, ``paged_append``,
+  ``paged_decode``:
   the same calls taking torch tensors; they allocate any output or workspace the
   caller did not pass (through torch's allocator, so the CUDA caching allocator sees
   every byte) and raise :class:`MlaError` on a non-OK status.
@@ -16,8 +17,11 @@ is missing this module raises on first use; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -99,6 +103,14 @@ def lib() -> ctypes.CDLL:
         L.mla_rmsnorm_bwd.restype = _i
         L.mla_rmsnorm_bwd_workspace.argtypes = [_i, ctypes.c_long, _i, _i]
         L.mla_rmsnorm_bwd_workspace.restype = _sz
+        L.mla_paged_tables.argtypes = [_i] * 5 + [_vp] * 10
+        L.mla_paged_tables.restype = _i
+        L.mla_paged_append.argtypes = ([D, _i, _i, _i, _i, _vp, ctypes.c_long, _vp, ctypes.c_long] + [_vp] * 6)
+        L.mla_paged_append.restype = _i
+        L.mla_paged_decode.argtypes = [D, _i, _i, _i, _i, _i] + [_vp] * 10 + [_sz, _vp]
+        L.mla_paged_decode.restype = _i
+        L.mla_paged_decode_workspace.argtypes = [D, _i, _i, _i, _i]
+        L.mla_paged_decode_workspace.restype = _sz
         L.mla_status_string.argtypes = [_i]
         L.mla_status_string.restype = ctypes.c_char_p
         L.mla_check_device_error.argtypes = [_vp]
@@ -194,6 +206,22 @@ def mla_rmsnorm_bwd_workspace(*args) -> int:
     return lib().mla_rmsnorm_bwd_workspace(*args)
 
 
+def mla_paged_tables(*args) -> int:
+    return lib().mla_paged_tables(*args)
+
+
+def mla_paged_append(*args) -> int:
+    return lib().mla_paged_append(*args)
+
+
+def mla_paged_decode(*args) -> int:
+    return lib().mla_paged_decode(*args)
+
+
+def mla_paged_decode_workspace(*args) -> int:
+    return lib().mla_paged_decode_workspace(*args)
+
+
 def mla_status_string(status: int) -> str:
     return lib().mla_status_string(status).decode()
 
@@ -217,7 +245,8 @@ def set_path_override(mode: int) -> None:
 KERNELS = ("prep", "latent_prep", "rope_table", "rope_rows", "convert", "gemm_simt", "attn_simt", "lse_combine",
            "tc_gemm", "tc_attn", "tc_latent_attn", "tc_decode_attn", "transpose", "rmsnorm", "rmsnorm_bwd", "tpla_expand",
            "tpla_combine", "wait_probe", "tc_fused_attn", "bwd_rowdot", "attn_bwd_simt", "bwd_rows",
-           "bwd_prep", "tc_bwd_dkv", "tc_bwd_dq")
+           "bwd_prep", "tc_bwd_dkv", "tc_bwd_dq", "paged_tables", "paged_append", "paged_absorb", "paged_attn",
+           "paged_join")
 
 
 def launch_count() -> int:
@@ -533,4 +562,173 @@ def lse_combine(part_out, part_lse, *, out_dtype=torch.float32, out=None, lse=No
     st = mla_lse_combine(_dt(out), n, rows, D, _ptr(part_out), _ptr(part_lse), _ptr(out), _ptr(lse),
                          _stream(stream))
     _check(st, "mla_lse_combine")
+    return out, lse
+
+
+# ------------------------------------------------------------------- paged cache ----
+def _on(device: torch.device):
+    """The tensors' device made current for the call: the library launches on the current
+    device, and the default stream is that device's current one."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _shape(name: str, t, shape: tuple, dtype: torch.dtype, device: torch.device) -> None:
+    _expect(name, t, math.prod(shape), dtype, device)
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), shape))
+
+
+class PagedTables(NamedTuple):
+    kv_lens: torch.Tensor      # [B] tokens each request holds after the step
+    cu_tokens: torch.Tensor    # [B + 1] prefix sums of the new lengths
+    slots: torch.Tensor        # [n_tokens] slot of each token row, -1 for none
+    positions: torch.Tensor    # [n_tokens]
+    counts: torch.Tensor       # [2] pages taken, pages needed
+
+
+def paged_tables(past_lens, new_lens, free_pages, block_table, *, page_size, n_tokens=None, kv_lens=None,
+                 cu_tokens=None, slots=None, positions=None, counts=None, stream=None) -> PagedTables:
+    """One step's block tables and slot map (all int32) from the requests' lengths; the new
+    pages are entered into ``block_table`` [B, max_pages] in place.  ``n_tokens``: rows of the
+    step's token arrays (default: those of ``slots``), at least the sum of ``new_lens``."""
+    dev = _device(block_table)
+    if block_table.dim() != 2 or block_table.shape[1] < 1:
+        raise ValueError("block_table must be [B, max_pages]")
+    B, max_pages = block_table.shape
+    if n_tokens is None:
+        if slots is None:
+            raise ValueError("n_tokens or slots is required")
+        n_tokens = slots.numel()
+    i32 = torch.int32
+    if not isinstance(free_pages, torch.Tensor):
+        raise TypeError("free_pages: expected a torch.Tensor, got %s" % type(free_pages).__name__)
+    n_free = free_pages.numel()
+    for name, t, shape in (("block_table", block_table, (B, max_pages)), ("past_lens", past_lens, (B,)),
+                           ("new_lens", new_lens, (B,)), ("free_pages", free_pages, (n_free,)),
+                           ("kv_lens", kv_lens, (B,)), ("cu_tokens", cu_tokens, (B + 1,)),
+                           ("slots", slots, (n_tokens,)), ("positions", positions, (n_tokens,)),
+                           ("counts", counts, (2,))):
+        _shape(name, t, shape, i32, dev)
+    if past_lens is None or new_lens is None:
+        raise TypeError("past_lens and new_lens are required")
+    with _on(dev):
+        if kv_lens is None:
+            kv_lens = torch.empty(B, dtype=i32, device=dev)
+        if cu_tokens is None:
+            cu_tokens = torch.empty(B + 1, dtype=i32, device=dev)
+        if slots is None:
+            slots = torch.empty(n_tokens, dtype=i32, device=dev)
+        if positions is None:
+            positions = torch.empty(n_tokens, dtype=i32, device=dev)
+        if counts is None:
+            counts = torch.empty(2, dtype=i32, device=dev)
+        st = lib().mla_paged_tables(B, page_size, max_pages, n_free, n_tokens, _ptr(past_lens), _ptr(new_lens),
+                                    _ptr(free_pages), _ptr(block_table), _ptr(kv_lens), _ptr(cu_tokens), _ptr(slots),
+                                    _ptr(positions), _ptr(counts), _stream(stream))
+    _check(st, "mla_paged_tables")
+    return PagedTables(kv_lens, cu_tokens, slots, positions, counts)
+
+
+def _cache_checks(d, c_cache, kpe_cache, tdt, dev):
+    if c_cache.dim() != 3:
+        raise ValueError("c_cache must be [num_pages, page_size, d_kv]")
+    num_pages, page = c_cache.shape[:2]
+    _shape("c_cache", c_cache, (num_pages, page, d.d_kv), tdt, dev)
+    _shape("kpe_cache", kpe_cache, (num_pages, page, d.d_rope), tdt, dev)
+    if kpe_cache is None:
+        raise TypeError("kpe_cache is required")
+    return num_pages, page
+
+
+def _rows(name, t, n, width, dtype, device) -> int:
+    """A matrix of n rows whose elements lie together, at any row pitch: returns the pitch."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: expected a torch.Tensor, got %s" % (name, type(t).__name__))
+    if t.device != device:
+        raise ValueError("%s: on %s, the call's tensors are on %s" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
+    if tuple(t.shape) != (n, width):
+        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), (n, width)))
+    if n < 2:
+        pitch = width
+    else:
+        pitch = t.stride(0)
+    if (width > 1 and t.stride(1) != 1) or pitch < width:
+        raise ValueError("%s: a row's elements must be adjacent and rows must not overlap" % name)
+    return pitch
+
+
+def paged_append(d: Dims, c_kv, k_pe, rms_w, slots, positions, c_cache, kpe_cache, *, stream=None):
+    """Write the tokens' normalised latent and rotated key band into their slots of the paged
+    cache, in place.  ``c_kv`` [n, d_kv] and ``k_pe`` [n, d_rope] may be column ranges of wider
+    rows.  Returns (c_cache, kpe_cache)."""
+    dev = _device(c_kv)
+    dt = _dt(c_kv)
+    if c_kv.dim() != 2:
+        raise ValueError("c_kv must be [n_tokens, d_kv]")
+    n, tdt = c_kv.shape[0], c_kv.dtype
+    num_pages, page = _cache_checks(d, c_cache, kpe_cache, tdt, dev)
+    cs = _rows("c_kv", c_kv, n, d.d_kv, tdt, dev)
+    ks = _rows("k_pe", k_pe, n, d.d_rope, tdt, dev)
+    for name, t, shape, ty in (("rms_w", rms_w, (d.d_kv,), tdt), ("slots", slots, (n,), torch.int32),
+                               ("positions", positions, (n,), torch.int32)):
+        if t is None:
+            raise TypeError("%s is required" % name)
+        _shape(name, t, shape, ty, dev)
+    with _on(dev):
+        st = lib().mla_paged_append(ctypes.byref(d), dt, n, num_pages, page, c_kv.data_ptr(), cs, k_pe.data_ptr(), ks,
+                                    _ptr(rms_w), _ptr(slots), _ptr(positions), _ptr(c_cache), _ptr(kpe_cache),
+                                    _stream(stream))
+    _check(st, "mla_paged_append")
+    return c_cache, kpe_cache
+
+
+def paged_decode_workspace(d: Dims, c_cache, block_table) -> torch.Tensor:
+    """A workspace for :func:`paged_decode` calls with this cache and table, one call at a time."""
+    dt = _dt(c_cache)
+    n = lib().mla_paged_decode_workspace(ctypes.byref(d), dt, block_table.shape[0], c_cache.shape[1],
+                                         block_table.shape[1])
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=c_cache.device)
+
+
+def paged_decode(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, w_kv_b, *, out=None, lse=None,
+                 workspace=None, stream=None):
+    """Latent decode of one query per request over the paged cache; ``kv_lens`` and
+    ``block_table`` (int32) stay on the device.  Returns (out, lse)."""
+    dev = _device(q_nope)
+    dt = _dt(q_nope)
+    tdt = q_nope.dtype
+    if q_nope.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q_nope must be [B, n_heads, d_nope] and block_table [B, max_pages]")
+    B, H = q_nope.shape[0], d.n_heads
+    max_pages = block_table.shape[1]
+    num_pages, page = _cache_checks(d, c_cache, kpe_cache, tdt, dev)
+    for name, t, shape, ty in (("q_nope", q_nope, (B, H, d.d_nope), tdt), ("q_pe", q_pe, (B, H, d.d_rope), tdt),
+                               ("block_table", block_table, (B, max_pages), torch.int32),
+                               ("kv_lens", kv_lens, (B,), torch.int32)):
+        if t is None:
+            raise TypeError("%s is required" % name)
+        _shape(name, t, shape, ty, dev)
+    if w_kv_b is None:
+        raise TypeError("w_kv_b is required")
+    _expect("w_kv_b", w_kv_b, H * (d.d_nope + d.d_v) * d.d_kv, tdt, dev)
+    _shape("out", out, (B, H, d.d_v), tdt, dev)
+    _shape("lse", lse, (B, H), torch.float32, dev)
+    with _on(dev):
+        if out is None:
+            out = torch.empty(B, H, d.d_v, dtype=tdt, device=dev)
+        if lse is None:
+            lse = torch.empty(B, H, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = paged_decode_workspace(d, c_cache, block_table)
+        else:
+            _workspace(0, dev, workspace)
+        st = lib().mla_paged_decode(ctypes.byref(d), dt, B, num_pages, page, max_pages, _ptr(q_nope), _ptr(q_pe),
+                                    _ptr(c_cache), _ptr(kpe_cache), _ptr(block_table), _ptr(kv_lens), _ptr(w_kv_b),
+                                    _ptr(out), _ptr(lse), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "mla_paged_decode")
     return out, lse

@@ -253,6 +253,73 @@ mla_status mla_lse_combine(mla_dtype out_dtype, int n_splits, int rows, int D,
                            const float *part_out, const float *part_lse, void *out, float *lse,
                            void *cuda_stream);
 
+/*
+ * Paged latent cache.  A cache of num_pages pages of page_size tokens:
+ *   c_cache [num_pages, page_size, d_kv]   kpe_cache [num_pages, page_size, d_rope]
+ * (num_pages * page_size < 2^31; byte offsets may pass 2^32).  A request's token at position p
+ * lies in slot block_table[b][p / page_size] * page_size + p % page_size, where row b of
+ * block_table [B, max_pages] (int32) holds the ids of its pages.  A step of a server is
+ * mla_paged_tables (which pages and slots the new tokens take), mla_paged_append (their
+ * rows written) and mla_paged_decode (one query per request attends); all three take the lengths
+ * from device memory, so the calls may be captured once and replayed as requests grow.  Their int32
+ * arrays need 4-byte alignment only (a slice of a list of free pages may start anywhere).
+ *
+ * mla_paged_tables: one step's tables from the requests' lengths.  past_lens [B]: tokens that a
+ * request holds already; new_lens [B]: tokens it gains; free_pages [n_free]: ids of free pages,
+ * taken from the front in the order of the requests.
+ *   block_table [B, max_pages]  in and out: a request's new pages are entered behind the
+ *                               ceil(past / page_size) that it holds; no other entry is touched
+ *   kv_lens [B]                 tokens that the request holds afterwards
+ *   cu_tokens [B + 1]           exclusive prefix sums of new_lens: rows cu_tokens[b] .. of the
+ *                               step's token arrays are request b's
+ *   slots [n_tokens]            the slot of each token row, -1 for one without (below)
+ *   positions [n_tokens]        the token's position in its request
+ *   counts [2]                  pages taken from free_pages, pages that the step needed
+ * Rows behind the last token (cu_tokens[B] <= row < n_tokens, a padded step) get slot -1 and
+ * position 0.  A token gets no slot (-1), and kv_lens stops before it, when its row would be
+ * past n_tokens, its position past max_pages * page_size, or free_pages has run out
+ * (counts[1] > counts[0]).  Negative lengths count as 0, a past length above what a table row holds
+ * as that.  A negative entry among a request's held pages gives its tokens slot -1.
+ * 0 <= B <= 16384; arrays of no elements may be NULL.  Page ids are copied as they are.
+ */
+mla_status mla_paged_tables(int B, int page_size, int max_pages, int n_free, int n_tokens, const int *past_lens,
+                            const int *new_lens, const int *free_pages, int *block_table, int *kv_lens, int *cu_tokens,
+                            int *slots, int *positions, int *counts, void *cuda_stream);
+
+/*
+ * Cache write of n_tokens tokens: c_cache[slots[t]] = RMSNorm(c_kv[t]) * rms_w (dims.rms_eps) and
+ * kpe_cache[slots[t]] = RoPE(k_pe[t], positions[t]) (any int32 position).  c_kv rows lie c_stride
+ * elements apart, k_pe rows k_stride (both may be column ranges of one projection's output);
+ * every other tensor is dense.  A slot outside [0, num_pages * page_size) is skipped, and no other
+ * row of the cache is touched.  Slots must be distinct: of two tokens with one slot
+ * either's elements may remain.  Uses d_kv, d_rope (<= 640), rope_base and rms_eps of dims.
+ */
+mla_status mla_paged_append(const mla_dims *dims, mla_dtype dtype, int n_tokens, int num_pages, int page_size,
+                            const void *c_kv, long c_stride, const void *k_pe, long k_stride, const void *rms_w,
+                            const int *slots, const int *positions, void *c_cache, void *kpe_cache, void *cuda_stream);
+
+/*
+ * Decode over the paged cache: mla_decode_splitkv with a length and a block table per request.
+ * One query per request, at position kv_lens[b] - 1, all n_heads heads, absorbed-form scores over
+ * keys 0 .. kv_lens[b] - 1.
+ *   q_nope [B, H, d_nope]   q_pe [B, H, d_rope] (not rotated)   block_table [B, max_pages]
+ *   kv_lens [B]   w_kv_b as above   out [B, H, d_v]   lse (fp32) [B, H]
+ * A request of length 0 gives out 0 and lse -inf; a length outside [0, max_pages * page_size]
+ * counts as the nearer end.  Slots at or behind a request's length are never looked at, whatever they
+ * hold (NaN included), nor are table entries behind its last page.  A page id outside
+ * [0, num_pages) stands for no keys: the positions it would hold get no weight.
+ * Key tiles of the whole batch are divided evenly among the GPU's SMs whatever the
+ * lengths are, and the parts of a request merged by the log-sum-exp rescale; results do not depend on
+ * timing (the same bits for the same call).  d_kv <= 512, d_kv + d_rope <= 640, d_nope <= 1024
+ * (MLA_ERR_UNSUPPORTED otherwise).  The workspace belongs to one call at a time: calls that may overlap
+ * (other streams, graphs replayed side by side) each need their own.
+ */
+mla_status mla_paged_decode(const mla_dims *dims, mla_dtype dtype, int B, int num_pages, int page_size, int max_pages,
+                            const void *q_nope, const void *q_pe, const void *c_cache, const void *kpe_cache,
+                            const int *block_table, const int *kv_lens, const void *w_kv_b, void *out, float *lse,
+                            void *workspace, size_t workspace_bytes, void *cuda_stream);
+size_t mla_paged_decode_workspace(const mla_dims *dims, mla_dtype dtype, int B, int page_size, int max_pages);
+
 /* Workspace bytes the matching call needs (0 on invalid arguments). */
 size_t mla_latent_attn_workspace(const mla_dims *dims, mla_dtype dtype, int B, int s_q, int s_kv,
                                  int q_offset, int causal, int head_count, int head_shard);
@@ -350,7 +417,8 @@ mla_status mla_decode_splitkv_noalloc(const mla_dims *dims, mla_dtype dtype, int
  *   "convert", "gemm_simt", "attn_simt", "lse_combine", "tc_gemm", "tc_attn",
  *   "tc_latent_attn", "tc_decode_attn", "transpose", "rmsnorm", "rmsnorm_bwd", "tpla_expand",
  *   "tpla_combine", "wait_probe", "tc_fused_attn", "bwd_rowdot",
- *   "attn_bwd_simt", "bwd_rows", "bwd_prep", "tc_bwd_dkv", "tc_bwd_dq".
+ *   "attn_bwd_simt", "bwd_rows", "bwd_prep", "tc_bwd_dkv", "tc_bwd_dq",
+ *   "paged_tables", "paged_append", "paged_absorb", "paged_attn", "paged_join".
  * mla_profile_reset: forgets recorded events, keeps recording on/off as it was.
  * Launches from several host threads are recorded safely; call enable, reset and the
  * queries between computations, not while another thread's calls are in flight.
