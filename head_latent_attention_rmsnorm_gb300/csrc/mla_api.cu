@@ -1132,11 +1132,19 @@ mla_status paged_decode_shape(const mla_dims *d, mla_dtype dt, int B, int page_s
     p->ty = ty_of(dt);
     p->scale = scale_of(d);
     p->base = d->rope_base;
-    p->row_tile = 16;
-    p->row_tiles = (p->H + 15) / 16;
-    p->tile = 32;
-    p->workers = 152;
-    p->min_tiles = 2;
+    p->tc = dt == MLA_BF16 && g_path_override != 1 && paged_tc_supported(p->Dk, p->Dn, p->Dr, p->Dv, page_size);
+    if (p->tc) {
+        p->row_tile = std::min(p->H, 128);
+        p->tile = PAGED_TC_TILE;
+        p->workers = PAGED_TC_WORKERS;
+        p->min_tiles = 3;
+    } else {
+        p->row_tile = 16;
+        p->tile = 32;
+        p->workers = 152;
+        p->min_tiles = 2;
+    }
+    p->row_tiles = (p->H + p->row_tile - 1) / p->row_tile;
     return MLA_OK;
 }
 
@@ -1194,8 +1202,8 @@ mla_status mla_paged_decode(const mla_dims *dims, mla_dtype dtype, int B, int nu
     p.lens = kv_lens;
     p.out = out;
     p.lse = lse;
-    g_last_path = 1;
-    return cuda_status(paged_decode_simt(p, (cudaStream_t)cuda_stream));
+    g_last_path = p.tc ? 2 : 1;
+    return cuda_status(p.tc ? paged_decode_tc(p, (cudaStream_t)cuda_stream) : paged_decode_simt(p, (cudaStream_t)cuda_stream));
 }
 
 const char *mla_status_string(mla_status s) {

@@ -25,6 +25,7 @@ struct PagedDecode {
     int B, H, Dk, Dn, Dr, Dv;
     int num_pages, page, max_pages;
     int ty;
+    bool tc;                         // the tensor-core form
     float scale, base;
     const void *q_nope, *q_pe, *c_cache, *kpe_cache, *w;
     const int *table, *lens;
@@ -37,5 +38,11 @@ struct PagedDecode {
     float *po, *pl;                  // partials [workers + B row_tiles][row_tile][Dk], [..][row_tile]
 };
 cudaError_t paged_decode_simt(const PagedDecode &p, cudaStream_t st);
+
+// The tensor-core form (bf16): these dimensions and page size, any number of heads.
+constexpr int PAGED_TC_WORKERS = 76, PAGED_TC_TILE = 80;   // pairs of SMs, keys per tile
+bool paged_tc_supported(int Dk, int Dn, int Dr, int Dv, int page);
+cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st);
+cudaError_t paged_tc_read_and_clear_error(unsigned *flags, cudaStream_t st);
 
 }  // namespace mla

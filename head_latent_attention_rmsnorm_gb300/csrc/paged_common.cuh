@@ -96,7 +96,7 @@ __device__ __forceinline__ int request_of(const PagedDecode &p, long t) {
     int lo = 0, hi = p.B - 1;
     while (lo < hi) {   // the last b whose first tile is <= t: empty requests before it share that tile
         const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(p.tile_off + mid) * p.row_tiles <= t) lo = mid;
+        if (__ldcg(p.tile_off + mid) * p.row_tiles <= t) lo = mid;
         else hi = mid - 1;
     }
     return lo;

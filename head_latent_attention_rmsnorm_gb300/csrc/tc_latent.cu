@@ -34,6 +34,7 @@
 #include <algorithm>
 
 #include "mla_internal.h"
+#include "paged.h"
 #include "tc.h"
 #include "tc_common.cuh"
 #include "tc_internal.h"
@@ -627,6 +628,7 @@ cudaError_t tc_read_and_clear_error(unsigned int *flags, cudaStream_t st) {
     if (e == cudaSuccess) e = tc_fused_read_and_clear_error(flags, st);
     if (e == cudaSuccess) e = tc_bwd_read_and_clear_error(flags, st);
     if (e == cudaSuccess) e = simt_read_and_clear_error(flags, st);
+    if (e == cudaSuccess) e = paged_tc_read_and_clear_error(flags, st);
     return e;
 }
 
