@@ -1059,7 +1059,7 @@ mla_status mla_paged_tables(int B, int page_size, int max_pages, int n_free, int
                             const int *new_lens, const int *free_pages, int *block_table, int *kv_lens, int *cu_tokens,
                             int *slots, int *positions, int *counts, void *cuda_stream) {
     if (B < 0 || B > PAGED_MAX_BATCH || page_size < 1 || max_pages < 1 || n_free < 0 || n_tokens < 0 ||
-        (long)max_pages * page_size > INT_MAX)
+        (long)max_pages * page_size > 1 << 30)
         return MLA_ERR_SHAPE;
     const size_t e = sizeof(int);
     Range in[] = {rng(past_lens, B * e), rng(new_lens, B * e), rng(free_pages, n_free * e)};
@@ -1117,7 +1117,7 @@ mla_status paged_decode_shape(const mla_dims *d, mla_dtype dt, int B, int page_s
     mla_status st = check_dims(d);
     if (st != MLA_OK) return st;
     if (!valid_dtype(dt)) return MLA_ERR_DTYPE;
-    if (B < 0 || page_size < 1 || max_pages < 1 || (long)max_pages * page_size > INT_MAX ||
+    if (B < 0 || page_size < 1 || max_pages < 1 || (long)max_pages * page_size > 1 << 30 ||
         ((long)B + 3) * d->n_heads > INT_MAX)
         return MLA_ERR_SHAPE;
     p->B = B;
@@ -1153,6 +1153,10 @@ size_t paged_decode_ws(PagedDecode *p, void *base) {
     c.base = (char *)base;
     const size_t rows = (size_t)p->B * p->H, slots = (size_t)p->workers + (size_t)p->B * p->row_tiles;
     p->tile_off = (long *)c.take(((size_t)p->B + 1) * sizeof(long));
+    if (p->tc) {
+        p->parts = (PagedPart *)c.take(slots * sizeof(PagedPart));
+        p->first = (int *)c.take((size_t)p->workers * 2 * sizeof(int));
+    }
     p->qabs = c.take(rows * p->Dk * 4);
     p->qpe = c.take(rows * p->Dr * 4);
     p->po = (float *)c.take(slots * p->row_tile * p->Dk * 4);

@@ -21,6 +21,11 @@ cudaError_t launch_paged_append(int ty, int T, long n_slots, int Dk, int Dr, flo
 // into tiles of `tile` keys, all items' tiles are numbered through, and worker c of W takes tiles
 // [c T / W, (c + 1) T / W).  The part of item i that worker c computes goes to partial slot
 // c + i: unique, because going along the tiles every cut raises c or i.
+struct alignas(16) PagedPart {   // what a worker computes of one item
+    int b, rt, k0, nt;           // request, row tile, first key tile, key tiles
+    int keys, next;              // the request's length; distance to the worker's next part, 0 for none
+    int pad[2];
+};
 struct PagedDecode {
     int B, H, Dk, Dn, Dr, Dv;
     int num_pages, page, max_pages;
@@ -34,13 +39,15 @@ struct PagedDecode {
     int row_tile, row_tiles, tile;   // heads per item, items per request, keys per tile
     int workers, min_tiles;          // most workers, fewest tiles that make one worker more
     long *tile_off;                  // [B + 1] first tile of request b, for one row tile
+    PagedPart *parts;                // [slots], the tensor-core form's
+    int *first;                      // [2][workers]: a worker's first part, its number of tiles
     void *qabs, *qpe;                // absorbed and rotated queries
     float *po, *pl;                  // partials [workers + B row_tiles][row_tile][Dk], [..][row_tile]
 };
 cudaError_t paged_decode_simt(const PagedDecode &p, cudaStream_t st);
 
 // The tensor-core form (bf16): these dimensions and page size, any number of heads.
-constexpr int PAGED_TC_WORKERS = 76, PAGED_TC_TILE = 80;   // pairs of SMs, keys per tile
+constexpr int PAGED_TC_WORKERS = 76, PAGED_TC_TILE = 64;   // pairs of SMs, keys per tile
 bool paged_tc_supported(int Dk, int Dn, int Dr, int Dv, int page);
 cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st);
 cudaError_t paged_tc_read_and_clear_error(unsigned *flags, cudaStream_t st);

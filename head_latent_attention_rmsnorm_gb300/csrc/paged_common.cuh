@@ -61,7 +61,18 @@ __device__ __forceinline__ int keys_of(const PagedDecode &p, int b) {
     return min(max(p.lens[b], 0), cap);
 }
 
-// The tile prefix sums of all requests, by one block of NT threads.
+// The request whose tiles (for all its row tiles) hold tile t < T.
+__device__ __forceinline__ int request_of(const PagedDecode &p, long t) {
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {   // the last b whose first tile is <= t: empty requests before it share that tile
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.tile_off[mid] * p.row_tiles <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// The tile prefix sums of all requests and the workers' parts, by one block of NT threads.
 template <int NT>
 __device__ void plan_block(const PagedDecode &p) {
     __shared__ long warp_tot[NT / 32];
@@ -89,17 +100,42 @@ __device__ void plan_block(const PagedDecode &p) {
         __syncthreads();
     }
     if (tid == 0) p.tile_off[p.B] = carry;
-}
-
-// The request whose tiles (for all its row tiles) hold tile t < T.
-__device__ __forceinline__ int request_of(const PagedDecode &p, long t) {
-    int lo = 0, hi = p.B - 1;
-    while (lo < hi) {   // the last b whose first tile is <= t: empty requests before it share that tile
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldcg(p.tile_off + mid) * p.row_tiles <= t) lo = mid;
-        else hi = mid - 1;
+    if (!p.parts) return;
+    __syncthreads();
+    // the parts: item (b, rt) is cut where a worker's share ends
+    const long total = carry * p.row_tiles;
+    const int W = total ? active_workers(p, total) : 0;
+    for (int c = tid; c < p.workers; c += NT) {
+        int f = 0, n = 0;
+        if (c < W) {
+            const long t0 = c * total / W;
+            n = (int)((c + 1) * total / W - t0);
+            const int b = request_of(p, t0);
+            f = c + b * p.row_tiles + (int)((t0 - p.tile_off[b] * p.row_tiles) / (p.tile_off[b + 1] - p.tile_off[b]));
+        }
+        p.first[c] = f;
+        p.first[p.workers + c] = n;
     }
-    return lo;
+    for (long item = tid; item < (long)p.B * p.row_tiles; item += NT) {
+        const int b = (int)(item / p.row_tiles), rt = (int)(item % p.row_tiles);
+        const long o = p.tile_off[b], per = p.tile_off[b + 1] - o, i0 = o * p.row_tiles + rt * per;
+        if (per == 0) continue;
+        for (int c = worker_of(i0, total, W), c1 = worker_of(i0 + per - 1, total, W); c <= c1; ++c) {
+            const long s0 = max(c * total / W, i0), end = (c + 1) * total / W, s1 = min(end, i0 + per);
+            PagedPart x{};
+            x.b = b;
+            x.rt = rt;
+            x.k0 = (int)(s0 - i0);
+            x.nt = (int)(s1 - s0);
+            x.keys = keys_of(p, b);
+            if (s1 < end) {   // the worker goes on with the next item that has tiles
+                x.next = 1;
+                if (rt == p.row_tiles - 1)
+                    for (int e = b + 1; p.tile_off[e + 1] == p.tile_off[e]; ++e) x.next += p.row_tiles;
+            }
+            p.parts[c + item] = x;
+        }
+    }
 }
 
 }  // namespace paged

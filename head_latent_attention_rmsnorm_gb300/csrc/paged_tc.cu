@@ -88,6 +88,7 @@ struct Absorb {
     PagedDecode p;
     bf16 *qhi, *qlo, *rhi, *rlo;   // [B][H][512], [B][H][64]
     int groups, group;             // groups of `group` requests
+    int rot_blocks;                // blocks 1 .. rot_blocks rotate the queries; block 0 divides the batch
     Turns turns;
 };
 
@@ -97,11 +98,41 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
     const PagedDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
-    if (blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.x == 0) {
         plan_block<128>(p);
         return;
     }
-    int u = blockIdx.x;
+    if ((int)blockIdx.x <= a.rot_blocks) {
+        // the queries' rotation: a warp per request and 32 heads, a lane per pair of dims, the angle
+        // formed once
+        const int i = ((int)blockIdx.x - 1) * 4 + warp, per = (p.H + 31) / 32, b = i / per, h0 = i % per * 32;
+        if (b >= p.B) return;
+        const float2 cs = turn_cs(a.turns.v[lane], keys_of(p, b) - 1);
+        const int h1 = min(h0 + 32, p.H);
+        for (int h = h0; h < h1; h += 8) {
+            uint16_t x0[8], x1[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint16_t *x = (const uint16_t *)p.q_pe + ((long)b * p.H + min(h + j, h1 - 1)) * DR + lane;
+                x0[j] = x[0];
+                x1[j] = x[32];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (h + j >= h1) break;
+                const long o = ((long)b * p.H + h + j) * DR + lane;
+                const float f0 = __uint_as_float((uint32_t)x0[j] << 16), f1 = __uint_as_float((uint32_t)x1[j] << 16);
+                uint32_t hi, lo;
+                split2(f0 * cs.x - f1 * cs.y, f1 * cs.x + f0 * cs.y, hi, lo);
+                ((uint16_t *)a.rhi)[o] = (uint16_t)hi;
+                ((uint16_t *)a.rhi)[o + 32] = (uint16_t)(hi >> 16);
+                ((uint16_t *)a.rlo)[o] = (uint16_t)lo;
+                ((uint16_t *)a.rlo)[o + 32] = (uint16_t)(lo >> 16);
+            }
+        }
+        return;
+    }
+    int u = (int)blockIdx.x - 1 - a.rot_blocks;
     const int dc = u & 3;
     u >>= 2;
     const int grp = u % a.groups, h = u / a.groups;
@@ -112,21 +143,18 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
         cp16(sw + n * AB_PITCH + c * 16, w + (long)n * DK + c * 8);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    // the query's rotation: this block's share of its requests
-    for (int i = tid; i < (b1 - b0) * (DR / 2); i += 128) {
-        const int b = b0 + (i >> 5), t = i & 31;
-        if ((b & 3) != dc) continue;
-        const long row = ((long)b * p.H + h) * DR;
-        const float2 cs = turn_cs(a.turns.v[t], keys_of(p, b) - 1);
-        const bf16 *x = (const bf16 *)p.q_pe + row;
-        const float x0 = __bfloat162float(x[t]), x1 = __bfloat162float(x[t + 32]);
-        uint32_t hi, lo;
-        split2(x0 * cs.x - x1 * cs.y, x1 * cs.x + x0 * cs.y, hi, lo);
-        ((uint16_t *)a.rhi)[row + t] = (uint16_t)hi;
-        ((uint16_t *)a.rhi)[row + t + 32] = (uint16_t)(hi >> 16);
-        ((uint16_t *)a.rlo)[row + t] = (uint16_t)lo;
-        ((uint16_t *)a.rlo)[row + t + 32] = (uint16_t)(lo >> 16);
-    }
+    const int g = lane >> 2, t = lane & 3;
+    uint4 qn[4];
+    auto fetch = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qn[i] = make_uint4(0, 0, 0, 0);
+        if (b + g < b1) {
+            const uint4 *src = (const uint4 *)((const bf16 *)p.q_nope + ((long)(b + g) * p.H + h) * DN + t * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qn[i] = __ldg(src + i);
+        }
+    };
+    fetch(b0);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     // step s of the sum: k = 2t, 2t + 1 is dim 32 t + 4 s + {0, 1}, k = 2t + 8, + 9 the next two
@@ -140,16 +168,11 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
             for (int s = 0; s < 8; ++s)   // matrices: (dims 0-7, k 0-7), (dims 8-15, k 0-7), (.., k 8-15) x 2
                 ldsm4_t(A[m][s], smem_u32(sw + (krow + 4 * s) * AB_PITCH + (warp * 32 + m * 16 + (mi & 1) * 8) * 2));
     }
-    const int g = lane >> 2, t = lane & 3;
     for (int b = b0; b < b1; b += 8) {
         uint4 q[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = make_uint4(0, 0, 0, 0);
-        if (b + g < b1) {
-            const uint4 *src = (const uint4 *)((const bf16 *)p.q_nope + ((long)(b + g) * p.H + h) * DN + t * 32);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = __ldg(src + i);
-        }
+        for (int i = 0; i < 4; ++i) q[i] = qn[i];
+        fetch(b + 8);   // the next eight requests
         float d[2][4] = {};
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
@@ -183,206 +206,306 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
 }
 
 // -------------------------------------------------------------------------- join ----
-// out[b, h, :] = W_V(h) sum_c w_c o_c: block (head, 64 value dims, 16 requests).  A warp holds its
-// 16 rows of W_V in registers (loaded before the wait for the attention), the block merges the
-// partials into shared memory as bf16 hi + lo, and two m16n8k16 products per step take both halves.
-// A step's 16 summed dims are permuted alike in A and B: lane t of a row owns dims 64 i + 16 t ..
-// + 15, four dims a step.
-constexpr int JB = 16, JROWS = 64, JPITCH = DK * 2 + 16, JMAXC = 80;
+// out[b, h, :] = W_V(h) sum_c w_c o_c: block (head, 16 requests), a warp per 16 value dims.  The
+// block merges the partials into shared memory as bf16 hi + lo, and two m16n8k16 products per step
+// take both halves.  A step's 16 summed dims are permuted alike in A and B: lane t of a row owns
+// dims 64 i + 16 t .. + 15, four dims a step, so its weights are 16-byte loads straight from W_V
+// (brought into L2 before the wait for the attention: the cache stream leaves none of it there).
+constexpr int JB = 16, JNT = 256, JPITCH = DK * 2 + 16, JMAXC = 80;
 
-__global__ void __launch_bounds__(128) paged_join_tc_kernel(const __grid_constant__ PagedDecode p) {
+__global__ void __launch_bounds__(JNT, 2) paged_join_tc_kernel(const __grid_constant__ PagedDecode p, const bf16 *qlo) {
     __shared__ __align__(16) uint8_t so[2][JB * JPITCH];
-    __shared__ float sw[JB][JMAXC];
-    __shared__ int sc[JB][2];   // first worker, number of parts
+    __shared__ float sw[JB][JMAXC];   // the parts' weights
+    __shared__ int sc[JB][2];         // first worker, number of parts
+    __shared__ float sl[JB], sd[4][JB];   // log-sum-exp without the q_lo term; the warps' shares of q_lo . o
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    int u = blockIdx.x;
-    const int vc = u & 1;
-    u >>= 1;
-    const int nb_groups = (p.B + JB - 1) / JB, h = u / nb_groups, b0 = (u % nb_groups) * JB, nb = min(JB, p.B - b0);
-    const int rt = h / p.row_tile, r = h % p.row_tile;
-    const bf16 *w = (const bf16 *)p.w + ((long)h * (DN + DV) + DN + vc * JROWS + warp * 16) * DK;
-    uint4 A[8][2][2];   // [64-dim piece][row g, g + 8][16-byte half]
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) A[i][m][q] = __ldg((const uint4 *)(w + (long)(g + 8 * m) * DK + 64 * i + 16 * t + 8 * q));
+    const int nb_groups = (p.B + JB - 1) / JB, h = blockIdx.x / nb_groups, b0 = (blockIdx.x % nb_groups) * JB;
+    const int nb = min(JB, p.B - b0), rt = h / p.row_tile, r = h % p.row_tile;
+    const bf16 *w = (const bf16 *)p.w + ((long)h * (DN + DV) + DN) * DK;
+    if (tid == 0 && b0 == 0) l2_prefetch(w, DV * DK * 2);
+    w += (warp * 16 + g) * DK + 16 * t;
     pdl_wait();
     const long total = p.tile_off[p.B] * p.row_tiles;
     const int W = total ? active_workers(p, total) : 0;
-    for (int j = warp; j < nb; j += 4) {   // a warp per request: the parts' weights
+#pragma unroll 1
+    for (int j = warp; j < JB; j += JNT / 32) {   // a warp per request
         const int b = b0 + j;
-        const long per = p.tile_off[b + 1] - p.tile_off[b], first = p.tile_off[b] * p.row_tiles + rt * per;
-        const long item = (long)b * p.row_tiles + rt;
         int c0 = 0, n = 0;
-        if (per > 0) {
-            c0 = worker_of(first, total, W);
-            n = worker_of(first + per - 1, total, W) - c0 + 1;
+        if (j < nb) {
+            const long o0 = p.tile_off[b], per = p.tile_off[b + 1] - o0, first = o0 * p.row_tiles + rt * per;
+            const float *pl = p.pl + ((long)b * p.row_tiles + rt) * p.row_tile + r;
+            if (per > 0) {
+                c0 = worker_of(first, total, W);
+                n = worker_of(first + per - 1, total, W) - c0 + 1;
+            }
+            float m = -INFINITY, s = 0.f;
+            for (int i = lane; i < n; i += 32) {
+                const float x = pl[(long)(c0 + i) * p.row_tile];
+                sw[j][i] = x;
+                m = fmaxf(m, x);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+            for (int i = lane; i < n; i += 32) {
+                const float x = sw[j][i], e = x == -INFINITY ? 0.f : expf(x - m);
+                sw[j][i] = e;
+                s += e;
+            }
+            s = warp_sum(s);
+            const float inv = s == 0.f ? 0.f : 1.f / s;
+            for (int i = lane; i < n; i += 32) sw[j][i] *= inv;
+            if (lane == 0) sl[j] = s == 0.f ? -INFINITY : m + logf(s);
         }
-        float x[3], m = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            x[i] = lane + 32 * i < n ? p.pl[(c0 + lane + 32 * i + item) * p.row_tile + r] : -INFINITY;
-            m = fmaxf(m, x[i]);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            x[i] = x[i] == -INFINITY ? 0.f : expf(x[i] - m);
-            s += x[i];
-        }
-        s = warp_sum(s);
-        const float inv = s == 0.f ? 0.f : 1.f / s;
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (lane + 32 * i < n) sw[j][lane + 32 * i] = x[i] * inv;
         if (lane == 0) {
             sc[j][0] = c0;
             sc[j][1] = n;
-            if (vc == 0) p.lse[(long)b * p.H + h] = s == 0.f ? -INFINITY : m + logf(s);
         }
     }
     __syncthreads();
-    for (int j = 0; j < JB; ++j) {   // a thread per four latent dims
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j < nb) {
+    // the merge: a thread per four latent dims of every other request, four requests and up to four
+    // parts of each in flight
+    const int d4 = tid & 127, half = tid >> 7;
+    const long pitch = (long)p.row_tile * (DK / 4);
+#pragma unroll 1
+    for (int j0 = half; j0 < (nb <= 8 ? 8 : 16); j0 += 8) {
+        const float4 *src[4];
+        float4 o[4];
+        int n[4], most = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = j0 + 2 * i;
             const long s0 = sc[j][0] + (long)(b0 + j) * p.row_tiles + rt;
-            const int n = sc[j][1];
-            const float4 *src = (const float4 *)(p.po + (s0 * p.row_tile + r) * DK) + tid;
-            const long pitch = (long)p.row_tile * (DK / 4);
-#pragma unroll 4
-            for (int c = 0; c < n; ++c) {
-                const float wt = sw[j][c];
-                const float4 v = __ldcg(src + c * pitch);
-                o.x = fmaf(wt, v.x, o.x);
-                o.y = fmaf(wt, v.y, o.y);
-                o.z = fmaf(wt, v.z, o.z);
-                o.w = fmaf(wt, v.w, o.w);
+            src[i] = (const float4 *)(p.po + (s0 * p.row_tile + r) * DK) + d4;
+            n[i] = sc[j][1];
+            most = max(most, n[i]);
+            o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 1
+        for (int c0 = 0; c0 < most; c0 += 4) {
+            float4 v[4][4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c0 + c < n[i]) v[i][c] = __ldcg(src[i] + (c0 + c) * pitch);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c0 + c < n[i]) {
+                        const float x = sw[j0 + 2 * i][c0 + c];
+                        o[i].x = fmaf(x, v[i][c].x, o[i].x);
+                        o[i].y = fmaf(x, v[i][c].y, o[i].y);
+                        o[i].z = fmaf(x, v[i][c].z, o[i].z);
+                        o[i].w = fmaf(x, v[i][c].w, o[i].w);
+                    }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = j0 + 2 * i;
+            uint32_t h0, l0, h1, l1;
+            split2(o[i].x, o[i].y, h0, l0);
+            split2(o[i].z, o[i].w, h1, l1);
+            *(uint2 *)(so[0] + j * JPITCH + d4 * 8) = make_uint2(h0, h1);
+            *(uint2 *)(so[1] + j * JPITCH + d4 * 8) = make_uint2(l0, l1);
+            if (j < nb) {   // the log-sum-exp's q_lo term: this warp's 128 dims
+                const uint2 q = __ldcg((const uint2 *)(qlo + ((long)(b0 + j) * p.H + h) * DK) + d4);
+                float dot = o[i].x * __uint_as_float(q.x << 16) + o[i].y * __uint_as_float(q.x & 0xffff0000u);
+                dot += o[i].z * __uint_as_float(q.y << 16) + o[i].w * __uint_as_float(q.y & 0xffff0000u);
+                dot = warp_sum(dot);
+                if (lane == 0) sd[warp & 3][j] = dot;
             }
         }
-        uint32_t h0, l0, h1, l1;
-        split2(o.x, o.y, h0, l0);
-        split2(o.z, o.w, h1, l1);
-        *(uint2 *)(so[0] + j * JPITCH + tid * 8) = make_uint2(h0, h1);
-        *(uint2 *)(so[1] + j * JPITCH + tid * 8) = make_uint2(l0, l1);
     }
     __syncthreads();
+    if (tid < nb)
+        p.lse[(long)(b0 + tid) * p.H + h] = sl[tid] + p.scale * ((sd[0][tid] + sd[1][tid]) + (sd[2][tid] + sd[3][tid]));
     float d[2][4] = {};
+    uint4 An[2][2];   // [row g, g + 8][16-byte half] of the next 64 dims
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        if (8 * n >= nb) break;
+    for (int e = 0; e < 4; ++e) An[e & 1][e >> 1] = __ldg((const uint4 *)(w + (e & 1) * 8 * DK + (e >> 1) * 8));
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+        uint4 A[2][2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int e = 0; e < 4; ++e) {
+            A[e & 1][e >> 1] = An[e & 1][e >> 1];
+            if (i < 7) An[e & 1][e >> 1] = __ldg((const uint4 *)(w + (e & 1) * 8 * DK + 64 * (i + 1) + (e >> 1) * 8));
+        }
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const uint4 bh = *(const uint4 *)(so[0] + (8 * n + g) * JPITCH + (64 * i + 16 * t + 8 * q) * 2);
-                const uint4 bl = *(const uint4 *)(so[1] + (8 * n + g) * JPITCH + (64 * i + 16 * t + 8 * q) * 2);
-                const uint32_t a0[4] = {A[i][0][q].x, A[i][1][q].x, A[i][0][q].y, A[i][1][q].y};
-                const uint32_t a1[4] = {A[i][0][q].z, A[i][1][q].z, A[i][0][q].w, A[i][1][q].w};
+        for (int q = 0; q < 2; ++q) {
+            const uint32_t a0[4] = {A[0][q].x, A[1][q].x, A[0][q].y, A[1][q].y};
+            const uint32_t a1[4] = {A[0][q].z, A[1][q].z, A[0][q].w, A[1][q].w};
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                if (n && nb <= 8) break;
+                const int at = (8 * n + g) * JPITCH + (64 * i + 16 * t + 8 * q) * 2;
+                const uint4 bh = *(const uint4 *)(so[0] + at), bl = *(const uint4 *)(so[1] + at);
                 mma_16816(d[n], a0, bh.x, bh.y);
                 mma_16816(d[n], a0, bl.x, bl.y);
                 mma_16816(d[n], a1, bh.z, bh.w);
                 mma_16816(d[n], a1, bl.z, bl.w);
             }
+        }
     }
     // d[n][..]: value dims g, g + 8 of the warp's 16, requests 8 n + 2t, + 1
     __syncthreads();
-    bf16 *ss = (bf16 *)so[0];   // [request][64 dims + pad]
+    bf16 *ss = (bf16 *)so[0];   // [request][128 dims + pad]
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            ss[(8 * n + 2 * t + (e & 1)) * 72 + warp * 16 + g + 8 * (e >> 1)] = __float2bfloat16_rn(d[n][e]);
+            ss[(8 * n + 2 * t + (e & 1)) * 136 + warp * 16 + g + 8 * (e >> 1)] = __float2bfloat16_rn(d[n][e]);
     __syncthreads();
-    const int j = tid >> 3, c = tid & 7;
-    if (j < nb)
-        *(uint4 *)((bf16 *)p.out + ((long)(b0 + j) * p.H + h) * DV + vc * JROWS + c * 8) = *(const uint4 *)(ss + j * 72 + c * 8);
+    const int j = tid >> 4, c = tid & 15;
+    if (j < nb) *(uint4 *)((bf16 *)p.out + ((long)(b0 + j) * p.H + h) * DV + c * 8) = *(const uint4 *)(ss + j * 136 + c * 8);
 }
 
 // --------------------------------------------------------------------- attention ----
-constexpr int ROWS = 128, NK = 80, NTHREADS = 384;
-constexpr int NGRP = NK / 8;   // row groups of a tile
-constexpr int KST = 2, KGRP = 3, VST = 2, NPB = 2;
-constexpr int PF1 = 4;         // key tiles prefetched into L2 ahead of rank 1's loads
+constexpr int ROWS = 128, NK = 64, NTHREADS = 576;
+constexpr int NGRP = NK / 8;            // row groups of a tile
+constexpr int KST = 2, KGRP = 3;        // rank 0: tile stages, block groups of a stage
+constexpr int VSL = 5;                  // rank 1: slots of half a tile (256 latent dims)
+constexpr int NPB = 2;                  // P slots of rank 1 = staging slots of rank 0
 constexpr uint32_t ATOM = 1024;
 // rank 0 stage: groups of 64-dim blocks {0-2}, {3-5}, {6-7}, each [row group][block][8 rows], then the
 // key band [row group][8 rows]
-constexpr uint32_t KG0 = 0, KG1 = NGRP * 3 * ATOM, KG2 = 2 * KG1, KG3 = KG2 + NGRP * 2 * ATOM;
-constexpr uint32_t KSTAGE = KG3 + NGRP * ATOM, VSTAGE = NGRP * 8 * ATOM;
-constexpr uint32_t P_BLK1 = 16384, P_BYTES = 16384 + 4096;
+constexpr uint32_t KG1 = NGRP * 3 * ATOM, KG2 = 2 * KG1, KG3 = KG2 + NGRP * 2 * ATOM, KSTAGE = KG3 + NGRP * ATOM;
+constexpr uint32_t VHALF = NGRP * 4 * ATOM;   // [row group][block][8 rows]
+// One P transfer: P [128 heads][64 keys] bf16 as the K-major A operand of P C, then the per-head
+// extras: rescale factor, 1/l and m + log2(l) (both on a part's last tile), a flag per lane quarter.
+constexpr uint32_t P_BYTES = 16384;
 constexpr uint32_t X_ALPHA = 0, X_INVL = 512, X_LSE = 1024, X_FLAG = 1536, X_BYTES = X_FLAG + 16;
-constexpr uint32_t XOFF = P_BYTES, XSLOT = 22528;
-constexpr uint32_t OFF_STG = KST * KSTAGE, OFF_EXT = OFF_STG + NPB * P_BYTES, EXT_STRIDE = 1664;
+constexpr uint32_t XOFF = P_BYTES, XSLOT = 18432, EXT_STRIDE = 1664;
+// rank 0: key stages, two query boxes, P staging, extras, row maxima [tile parity][half][row], row sums
+constexpr uint32_t OFF_Q = KST * KSTAGE, OFF_STG = OFF_Q + 2 * 16384, OFF_EXT = OFF_STG + NPB * P_BYTES;
 constexpr uint32_t OFF_RED = OFF_EXT + NPB * EXT_STRIDE, OFF_SUM = OFF_RED + 2 * 2 * ROWS * 4;
-constexpr uint32_t OFF_PB = VST * VSTAGE, OFF_RED1 = OFF_PB + NPB * XSLOT;
-constexpr uint32_t QB_OFF = 8 * 4096;
-constexpr uint32_t END0 = OFF_SUM + 2 * ROWS * 4, END1 = OFF_RED1 + 2 * ROWS * 4;
+// rank 1: latent slots, P slots, 1/l of each row for the epilogue's other warps [part parity][row], the
+// epilogue's transposes (2 KB a warp)
+constexpr uint32_t OFF_PB = VSL * VHALF, OFF_INV = OFF_PB + NPB * XSLOT, OFF_OUT = OFF_INV + 2 * ROWS * 4;
+constexpr uint32_t END0 = OFF_SUM + 2 * ROWS * 4, END1 = OFF_OUT + 8 * 2048;
 constexpr uint32_t OFF_BAR = END0 > END1 ? END0 : END1;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 512;
-constexpr uint32_t T_S = 0, T_Q = 2 * NK, T_QP = T_Q + 256, T_QL = T_QP + 32;
+constexpr uint32_t T_S = 0, T_Q = 2 * NK;   // rank 0's TMEM columns: S buffers; 32 per 64 query dims (10 blocks)
 constexpr float RESCALE_LOG2 = 8.0f;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-static_assert(10 * 16384 <= KST * KSTAGE, "the query block fits the key stages");
-static_assert(QB_OFF + 8 * 16384 <= OFF_PB, "epilogue staging fits the latent stages");
-static_assert(OFF_STG % 1024 == 0 && P_BYTES % 1024 == 0 && OFF_PB % 1024 == 0 && XSLOT % 1024 == 0, "swizzle atoms");
+static_assert(KSTAGE % 1024 == 0 && OFF_STG % 1024 == 0 && OFF_PB % 1024 == 0 && XSLOT % 1024 == 0, "swizzle atoms");
 static_assert(XOFF + X_BYTES <= XSLOT && X_BYTES <= EXT_STRIDE && OFF_EXT % 16 == 0, "P transfer layout");
-static_assert(T_QL + 32 <= 512, "TMEM budget of rank 0");
+static_assert(T_Q + 320 <= 512, "TMEM budget of rank 0");
+// Barriers, by index; the same places in both CTAs.
+enum : int {
+    B_GFULL = 0,                 // rank 0 [stage][group]: boxes landed / read by the MMAs
+    B_GEMPTY = B_GFULL + 6,
+    B_SFULL = B_GEMPTY + 6,      // rank 0 [buffer]: scores done / drained by the softmax
+    B_SFREE = B_SFULL + 2,
+    B_STAGED = B_SFREE + 2,      // rank 0 [slot]: P staged / its copy has read it
+    B_STGFREE = B_STAGED + 2,
+    B_QFULL = B_STGFREE + 2,     // rank 0 [slot]: query box landed / moved to TMEM
+    B_QEMPTY = B_QFULL + 2,
+    B_QREADY = B_QEMPTY + 2,     // rank 0: the part's queries in TMEM / no longer read by MMAs
+    B_QFREE = B_QREADY + 1,
+    B_PEMPTY = B_QFREE + 1,      // both [slot]: P consumed (one multicast commit completes it in both)
+    B_PFULL = B_PEMPTY + 2,      // rank 1 [slot]: P and extras landed / O rescaled for it
+    B_PCREADY = B_PFULL + 2,
+    B_VFULL = B_PCREADY + 2,     // rank 1 [slot]: half a tile landed / read by the MMAs
+    B_VEMPTY = B_VFULL + VSL,
+    B_OFINAL = B_VEMPTY + VSL,   // rank 1: the part's O complete / read
+    B_EPIDONE = B_OFINAL + 1,
+    B_COUNT = B_EPIDONE + 1
+};
+__device__ __forceinline__ uint32_t arrivals(int i) {
+    if (i >= B_SFREE && i < B_STGFREE) return 8;   // one per softmax warp
+    if ((i >= B_QEMPTY && i <= B_QREADY) || (i >= B_PCREADY && i < B_VFULL)) return 4;
+    if (i == B_QFREE) return 2;
+    return i == B_EPIDONE ? 8 : 1;
+}
 
+struct Maps {
+    CUtensorMap k3, k2, v, r;   // boxes of a unit's rows: blocks 0-2 / 3-5, blocks 6-7, four blocks, key band
+    CUtensorMap v8;             // eight rows, four blocks
+    CUtensorMap qh, rh, rl;     // queries [B][H][512], [B][H][64] twice
+};
 struct Attn {
     PagedDecode p;
-    int box_rows;            // rows of a cache box: 8 or 16
+    int q_rows;                 // rows of the query boxes
+    uint32_t page_mul, page_shift;   // division by the page size
     float scale_log2;
     uint32_t idesc_s, idesc_pv;
 };
 
-// The cluster's walk over its share of the tiles, a part (one item's consecutive tiles) at a time.
-struct Walk {
-    long left;               // tiles of the share from this part on
-    int b, rt, k0, nt;       // request, row tile, first tile and number of tiles of the part
-    int keys;                // the request's length
-    __device__ __forceinline__ void part(const PagedDecode &p, long from) {
-        const int per = (int)(p.tile_off[b + 1] - p.tile_off[b]);
-        k0 = (int)from;
-        nt = (int)min((long)(per - k0), left);
-        keys = keys_of(p, b);
-    }
-    __device__ __forceinline__ void begin(const PagedDecode &p, long t, long n) {
-        left = n;
-        nt = 0;
-        if (n <= 0) return;
-        b = request_of(p, t);
-        const long first = p.tile_off[b], per = p.tile_off[b + 1] - first, o = t - first * p.row_tiles;
-        rt = (int)(o / per);
-        part(p, o % per);
-    }
-    __device__ __forceinline__ bool next(const PagedDecode &p) {
-        left -= nt;
-        if (left <= 0) return false;
-        if (++rt == p.row_tiles) {
-            rt = 0;
-            do ++b;
-            while (p.tile_off[b + 1] == p.tile_off[b]);
+// Code size counts here: it is fetched through the L2 that the cache streams through, and what a role
+// runs seldom comes from DRAM each time.  Hence parts as a list (PagedPart) made once, waits
+// whose slow side is one function, rolled loops around small bodies.  The same kernel at 95 KB of
+// code took 1.4 us a tile where 82 KB took 1.0.
+
+// x / page for 0 <= x < 2^31 (round-up multiplier; the sum cannot overflow as the high product is < x).
+__device__ __forceinline__ int page_of(const Attn &a, int x) {
+    return (int)((__umulhi(a.page_mul, (uint32_t)x) + (uint32_t)x) >> a.page_shift);
+}
+// The cache row of key `key` of the part's request, -1 for none (behind the end, a bad page id).
+__device__ __forceinline__ int row_of(const Attn &a, const PagedPart &w, int key) {
+    if (key >= w.keys) return -1;
+    const int col = page_of(a, key);
+    const int id = __ldg(a.p.table + (long)w.b * a.p.max_pages + col);
+    return (unsigned)id < (unsigned)a.p.num_pages ? id * a.p.page + (key - col * a.p.page) : -1;
+}
+
+// The cache rows of the part's units, a window of 64 units in two registers of the warp: fetched 32
+// at a time, tiles ahead of their use (under the cache stream a table entry takes longer than a tile
+// to arrive).
+template <int UNIT>
+struct Rows {
+    int cur, nxt, base;   // units base + lane, base + 32 + lane; base < 0 before the first tile
+    // The row of unit `lane` of tile i (lanes below NK / UNIT; a tile never straddles the registers).
+    __device__ __forceinline__ int tile(const Attn &a, const PagedPart &w, int i, int lane) {
+        constexpr int N = NK / UNIT;
+        while (i * N - base >= 32) {   // once in 32 units; twice for the first tile
+            base += 32;
+            cur = nxt;
+            const int u = base + 32 + lane;
+            nxt = u < w.nt * N ? row_of(a, w, w.k0 * NK + u * UNIT) : -1;
         }
-        part(p, 0);
-        return true;
+        return __shfl_sync(FULL, cur, (i * N + lane - base) & 31);
     }
 };
-
-// The cache row of key `key`, -1 for none (behind the end, a page id outside the cache).
-__device__ __forceinline__ int row_of(const PagedDecode &p, const Walk &w, int key) {
-    if (key >= w.keys) return -1;
-    const int col = key / p.page;
-    const int id = __ldg(p.table + (long)w.b * p.max_pages + col);
-    return (unsigned)id < (unsigned)p.num_pages ? id * p.page + (key - col * p.page) : -1;
-}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Bounded waits.  A kernel of this file lasts milliseconds (every byte that the GPU holds, read once);
+// KERNEL_NS after its start a wait records the timeout and gives up, as does every other wait of the
+// CTA.
+constexpr uint64_t KERNEL_NS = 4000000000ull;
+struct Ctl {
+    unsigned long long deadline;
+    int abort;
+};
+__device__ __noinline__ bool gave_up(Ctl *c) {
+    if (((volatile Ctl *)c)->abort) return true;
+    if (global_ns() < ((volatile Ctl *)c)->deadline) return false;
+    atomicOr(&g_paged_tc_err, ERR_WAIT_TIMEOUT);
+    ((volatile Ctl *)c)->abort = 1;
+    return true;
+}
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, Ctl *c) {
+    for (uint32_t n = 1; !(CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)); ++n)
+        if ((n & 63) == 0 && gave_up(c)) return false;
+    return true;
+}
+__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, Ctl *c) {
+    return __all_sync(FULL, wait_for(bar, parity, c));
 }
 
 __device__ void settle() {   // after an abandoned wait: loads in flight land before the CTA leaves
@@ -391,87 +514,38 @@ __device__ void settle() {   // after an abandoned wait: loads in flight land be
     }
 }
 
+template <int UNIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
-    paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mK3, const __grid_constant__ CUtensorMap mK2,
-                         const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mR,
-                         const __grid_constant__ CUtensorMap mQh, const __grid_constant__ CUtensorMap mQl,
-                         const __grid_constant__ CUtensorMap mRh, const __grid_constant__ CUtensorMap mRl,
-                         const __grid_constant__ CUtensorMap mP, const __grid_constant__ Attn a) {
+    paged_attn_tc_kernel(const __grid_constant__ Maps m, const __grid_constant__ Attn a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023) {   // no room to align by hand; the same answer in every CTA
         if (threadIdx.x == 0) atomicOr(&g_paged_tc_err, 2u);
         return;
     }
+    constexpr int UNITS = NK / UNIT, NRG = UNIT / 8;   // units of a tile, row groups of a unit
     uint64_t *bars = (uint64_t *)(smem + OFF_BAR);
+    Ctl *ctl = (Ctl *)(bars + B_COUNT);
+    uint32_t *tslot = (uint32_t *)(ctl + 1);
+    static_assert(B_COUNT * 8 + sizeof(Ctl) + 4 <= 512, "barrier area");
     const PagedDecode &p = a.p;
-    // rank 0
-    uint64_t *s_free = bars, *stg_free = bars + 2, *s_full = bars + 4, *staged = bars + 6;
-    uint64_t *grp_full = bars + 8, *grp_empty = bars + 14;   // [stage][group]
-    uint64_t *q_full = bars + 20, *q_ready = bars + 21, *q_seen = bars + 22;
-    // both: P slot consumed by its P C MMAs (one multicast commit completes it in both CTAs)
-    uint64_t *p_empty = bars + 24;
-    // rank 1
-    uint64_t *p_full = bars + 26, *pc_ready = bars + 28, *v_full = bars + 30, *v_empty = bars + 32;
-    uint64_t *o_final = bars + 34, *qb_full = bars + 35, *epi_done = bars + 36;
-    volatile int *prog = (volatile int *)(bars + 38);
-    uint32_t *tslot = (uint32_t *)(bars + 39);
-    volatile int *abort = (volatile int *)(tslot + 1);
-    unsigned *err = &g_paged_tc_err;
-    float *red = (float *)(smem + OFF_RED), *sums = (float *)(smem + OFF_SUM);
-
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
 
-    if (tid == 0) {
-        if (rank == 0) {
-            for (int s = 0; s < 2; ++s) {
-                mbar_init(&s_free[s], 8);
-                mbar_init(&stg_free[s], 1);
-                mbar_init(&s_full[s], 1);
-                mbar_init(&staged[s], 8);
-            }
-            for (int i = 0; i < KST * KGRP; ++i) {
-                mbar_init(&grp_full[i], 1);
-                mbar_init(&grp_empty[i], 1);
-            }
-            mbar_init(q_full, 1);
-            mbar_init(q_ready, 8);
-            mbar_init(q_seen, 2);
-        } else {
-            for (int s = 0; s < 2; ++s) {
-                mbar_init(&p_full[s], 1);
-                mbar_init(&pc_ready[s], 4);
-                mbar_init(&v_full[s], 1);
-                mbar_init(&v_empty[s], 1);
-            }
-            mbar_init(o_final, 1);
-            mbar_init(qb_full, 1);
-            mbar_init(epi_done, 8);
+    if (warp == 0) {
+        for (int i = lane; i < B_COUNT; i += 32) mbar_init(&bars[i], arrivals(i));
+        if (lane == 0) {
+            ctl->abort = 0;
+            ctl->deadline = global_ns() + KERNEL_NS;
         }
-        for (int s = 0; s < NPB; ++s) mbar_init(&p_empty[s], 1);
-        *abort = 0;
-        *prog = 0;
         fence_mbar_init();
-        if (rank == 0) {
-            for (int s = 0; s < 2; ++s)
-                for (int i = 0; i < 8; ++i) mbar_arrive(&s_free[s]);
-        } else {
-            for (int s = 0; s < NPB; ++s) mbar_arrive_expect_tx(&p_full[s], P_BYTES + X_BYTES);
-        }
+        __syncwarp();
+        if (rank == 1 && lane < NPB) mbar_arrive_expect_tx(&bars[B_PFULL + lane], P_BYTES + X_BYTES);   // armed for its first transfer
     }
     if (warp == 1) {
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
-    if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&mK3);
-        tma_prefetch_desc(&mK2);
-        tma_prefetch_desc(&mV);
-        tma_prefetch_desc(&mR);
-        tma_prefetch_desc(&mQh);
-        tma_prefetch_desc(&mQl);
-        tma_prefetch_desc(&mP);
-    }
+    if (warp == 2 && lane < 8) tma_prefetch_desc((const CUtensorMap *)&m + lane);
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // both CTAs' barriers exist before any cross-CTA arrival
@@ -480,407 +554,387 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     pdl_wait();
     pdl_launch_dependents();
 
-    // this cluster's share of the tiles
-    const int worker = blockIdx.x >> 1;
-    long n_all = 0;
-    Walk w{};
-    {
-        const long total = __ldcg(p.tile_off + p.B) * p.row_tiles;
-        const int W = active_workers(p, total);
-        if (worker < W) {
-            const long t0 = worker * total / W, t1 = (worker + 1) * total / W;
-            n_all = t1 - t0;
-            w.begin(p, t0, n_all);
-        }
-    }
-    const bool work = n_all > 0;
+    // this cluster's parts: a list from the division of the batch
+    const PagedPart *part = p.parts + __ldcg(p.first + (blockIdx.x >> 1));
+    const int n_all = __ldcg(p.first + p.workers + (blockIdx.x >> 1));   // tiles
+    PagedPart w{};
+    bool more = n_all > 0;
+    auto load = [&]() {
+        const int4 x = __ldcg((const int4 *)part), y = __ldcg((const int4 *)part + 1);
+        w.b = x.x;
+        w.rt = x.y;
+        w.k0 = x.z;
+        w.nt = x.w;
+        w.keys = y.x;
+        w.next = y.y;
+    };
+    if (more) load();
+    auto next = [&]() {
+        more = w.next > 0;
+        part += w.next;
+        if (more) load();
+    };
+    const int none = (int)((p.num_pages * (long)p.page) >> 3);   // a row group outside the cache: zeros
 
     if (rank == 0) {
-        if (warp == 0) {
-            // ---------------------------------------------------------------- TMA producer
-            // a lane per cache box; the whole warp waits
-            const int nbox = NK / a.box_rows, nrg = a.box_rows >> 3, none = (p.num_pages * (long)p.page) >> 3;
-            int n = 0, seg = 0;
-            bool go = work;
-            while (go) {
-                // the key stages hold the query block until it is in TMEM: free once the last
-                // part's score MMAs have read them
-                for (int m = n > 2 ? n - 2 : 0; m < n && go; ++m)
-                    for (int g = 0; g < KGRP && go; ++g)
-                        go = __all_sync(FULL, mbar_wait(&grp_empty[(m & 1) * KGRP + g], (m >> 1) & 1, abort, err));
-                if (go && seg > 0) go = __all_sync(FULL, mbar_wait(q_seen, (seg - 1) & 1, abort, err));
-                if (!go) break;
-                if (lane == 0) {
-                    const int r0 = w.rt * ROWS;
-                    mbar_arrive_expect_tx(q_full, 10 * 16384);
-                    for (int i = 0; i < 8; ++i) tma_load_3d(smem + i * 16384, &mQh, q_full, 64 * i, r0, w.b);
-                    tma_load_3d(smem + 8 * 16384, &mRh, q_full, 0, r0, w.b);
-                    tma_load_3d(smem + 9 * 16384, &mRl, q_full, 0, r0, w.b);
-                }
-                int row = lane < nbox ? row_of(p, w, w.k0 * NK + lane * a.box_rows) : -1;
-                go = __all_sync(FULL, mbar_wait(q_ready, seg & 1, abort, err));
-                for (int i = 0; i < w.nt && go; ++i, ++n) {
+        if (warp == 0 || warp == 12 || warp == 13) {
+            // ------------------------------------------------- TMA producers, a warp per block group
+            // a lane per unit of the tile's rows; the whole warp waits.  A group's refill costs the time
+            // from its last MMA to the issue of its boxes, hence a warp for each.
+            const int g = warp == 0 ? 0 : warp - 11;
+            int n = 0;
+            bool go = true;
+            for (; more && go; next()) {
+                Rows<UNIT> rows{-1, -1, -64};
+#pragma unroll 1
+                for (int i = 0; i < w.nt; ++i, ++n) {
                     const int s = n & 1;
-                    uint8_t *dst = smem + s * KSTAGE;
-                    const int rg = row >= 0 ? row >> 3 : none;
-                    for (int g = 0; g < KGRP; ++g) {
-                        uint64_t *full = &grp_full[s * KGRP + g];
-                        if (i >= KST) go = __all_sync(FULL, mbar_wait(&grp_empty[s * KGRP + g], ((n >> 1) - 1) & 1, abort, err));
-                        if (!go) break;
-                        if (lane == 0) mbar_arrive_expect_tx(full, NGRP * 3 * ATOM);
-                        __syncwarp();
-                        if (lane < nbox) {
-                            const uint32_t o = lane * nrg;
-                            if (g < 2) {
-                                tma_load_4d(dst + (g == 0 ? KG0 : KG1) + o * 3 * ATOM, &mK3, full, 0, 0, 3 * g, rg);
-                            } else {
-                                tma_load_4d(dst + KG2 + o * 2 * ATOM, &mK2, full, 0, 0, 6, rg);
-                                tma_load_2d(dst + KG3 + o * ATOM, &mR, full, 0, rg * 8);
-                            }
-                        }
+                    uint8_t *dst = smem + s * KSTAGE + g * KG1 + lane * NRG * (g < 2 ? 3 : 2) * ATOM;
+                    uint64_t *full = &bars[B_GFULL + s * KGRP + g];
+                    const int row = rows.tile(a, w, i, lane), rg = row >= 0 ? row >> 3 : none;
+                    go = wait_all(&bars[B_GEMPTY + s * KGRP + g], ((n >> 1) & 1) ^ 1, ctl);   // a fresh barrier passes
+                    if (!go) break;
+                    if (lane == 0) mbar_arrive_expect_tx(full, NGRP * 3 * ATOM);
+                    if (lane < UNITS) {
+                        tma_load_4d(dst, g < 2 ? &m.k3 : &m.k2, full, 0, 0, 3 * g, rg);
+                        if (g == 2) tma_load_2d(smem + s * KSTAGE + KG3 + lane * NRG * ATOM, &m.r, full, 0, rg * 8);
                     }
-                    if (i + 1 < w.nt && lane < nbox) row = row_of(p, w, (w.k0 + i + 1) * NK + lane * a.box_rows);
                     __syncwarp();
                 }
-                ++seg;
-                go = go && w.next(p);
             }
         } else if (warp == 1 || warp == 11) {
             // --------------------- S = Q K^T issuers: warp 1 even tiles, warp 11 odd tiles
             int n = 0, seg = 0;
-            const int mine = warp == 1 ? 0 : 1;
-            bool ok = work;
-            while (ok) {
-                ok = __all_sync(FULL, mbar_wait(q_ready, seg & 1, abort, err));
-                if (!ok) break;
-                if (lane == 0) mbar_arrive(q_seen);
+            const int s = warp == 1 ? 0 : 1;
+            const uint32_t base = smem_u32(smem + s * KSTAGE), dt = tmem + T_S + s * NK;
+            bool ok = true;
+            for (; more && ok; next(), ++seg) {
+                ok = wait_all(&bars[B_QREADY], seg & 1, ctl);
+#pragma unroll 1
                 for (int i = 0; i < w.nt && ok; ++i, ++n) {
-                    if ((n & 1) != mine) continue;
-                    const int s = n & 1;
+                    if ((n & 1) != s) continue;
                     const uint32_t ph = (n >> 1) & 1;
-                    ok = __all_sync(FULL, mbar_wait(&s_free[s], ph, abort, err));
-                    const uint32_t base = smem_u32(smem + s * KSTAGE), dt = tmem + T_S + s * NK, at = tmem + T_Q;
-                    const uint64_t d0 = sdesc_sw128(base + KG0, 16, 3 * ATOM), d1 = sdesc_sw128(base + KG1, 16, 3 * ATOM);
-                    const uint64_t d2 = sdesc_sw128(base + KG2, 16, 2 * ATOM), d3 = sdesc_sw128(base + KG3, 16, ATOM);
-#pragma unroll
+                    ok = wait_all(&bars[B_SFREE + s], ph ^ 1, ctl);
+#pragma unroll 1
                     for (int g = 0; g < KGRP; ++g) {
-                        ok = ok && __all_sync(FULL, mbar_wait(&grp_full[s * KGRP + g], ph, abort, err));
+                        ok = ok && wait_all(&bars[B_GFULL + s * KGRP + g], ph, ctl);
                         if (!ok) break;
                         tc_fence_after();
                         if (elect_one()) {
-                            const uint64_t dg = g == 0 ? d0 : (g == 1 ? d1 : d2);
+                            // blocks of 64 dims: latent 0-7 (q_hi), then the key band twice (hi, lo)
+                            uint64_t d = sdesc_sw128(base + g * KG1, 16, (g < 2 ? 3 : 2) * ATOM);
+                            const int j1 = g < 2 ? 3 * g + 3 : 10;
+#pragma unroll 1
+                            for (int j = 3 * g; j < j1; ++j) {
+                                if (j >= 8) d = sdesc_sw128(base + KG3, 16, ATOM);
 #pragma unroll
-                            for (int kk = 12 * g; kk < 12 * g + 12 && kk < 32; ++kk)   // latent, q_hi
-                                mma_ts(dt, at + kk * 8, dg + (uint64_t)(((kk >> 2) - 3 * g) * (ATOM >> 4) + 2 * (kk & 3)),
-                                       a.idesc_s, kk != 0);
-                            if (g == KGRP - 1) {
-#pragma unroll
-                                for (int kk = 0; kk < 8; ++kk)   // key band: hi, then lo
-                                    mma_ts(dt, tmem + (kk < 4 ? T_QP : T_QL) + (kk & 3) * 8, d3 + (uint64_t)(2 * (kk & 3)),
-                                           a.idesc_s, 1);
+                                for (int q = 0; q < 4; ++q)
+                                    mma_ts(dt, tmem + T_Q + j * 32 + q * 8, d + 2 * q, a.idesc_s, (j | q) != 0);
+                                d += ATOM >> 4;
                             }
-                            mma_commit(&grp_empty[s * KGRP + g]);
-                            if (g == KGRP - 1) mma_commit(&s_full[s]);
+                            mma_commit(&bars[B_GEMPTY + s * KGRP + g]);
+                            if (g == KGRP - 1) mma_commit(&bars[B_SFULL + s]);
                         }
                         __syncwarp();
                     }
                 }
-                ++seg;
-                ok = ok && w.next(p);
+                // this warp's last score MMAs of the part: the queries may be replaced
+                if (ok && elect_one()) mma_commit(&bars[B_QFREE]);
+                __syncwarp();
             }
         } else if (warp >= 2 && warp < 10) {
             // ---------------------------------------------------------- softmax warps
-            // two threads per head: warps 2-5 take keys 0-39 of a tile, warps 6-9 keys 40-79
+            // two threads per head: warps 2-5 take keys 0-31 of a tile, warps 6-9 keys 32-63.  An
+            // abandoned wait clears `ok`; the walk goes on without waiting, so that both warps of a row
+            // reach every barrier.
             const int quad = warp & 3, row = quad * 32 + lane, h = (warp - 2) >> 2;
-            const uint32_t lb = tmem + ((uint32_t)(quad * 32) << 16);
+            const uint32_t sbase = tmem + ((uint32_t)(quad * 32) << 16) + T_S + h * (NK / 2);
             const float c = a.scale_log2;
+            float *red = (float *)(smem + OFF_RED) + row, *sums = (float *)(smem + OFF_SUM) + row;
             constexpr int HK = NK / 2;
-            // an abandoned wait clears `ok`; the walk goes on without waiting, so that both warps of a
-            // row reach every barrier
-            int n = 0, seg = 0;
+            int n = 0;
             bool ok = true;
-            for (bool more = work; more; more = w.next(p), ++seg) {
+            for (; more; next()) {
                 // a warp whose 32 rows are all behind the last head only keeps the barriers
                 const bool act = w.rt * ROWS + quad * 32 < p.H;
-                ok = __all_sync(FULL, ok && mbar_wait(q_full, seg & 1, abort, err));
-                if (ok && act) {
-                    tc_fence_after();
-                    // this head's queries into TMEM, 32 values per step: hi of the latent (steps
-                    // 0-15), hi and lo of the band (16-17, 18-19); a step is half a 128-byte row of
-                    // a box; the head's two threads take ten steps each
-                    for (int st = 10 * h; st < 10 * h + 10; ++st) {
-                        const uint8_t *box = smem + (st < 16 ? (st >> 1) : 8 + ((st - 16) >> 1)) * 16384 + row * 128;
-                        uint32_t v[16];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint4 x = *(const uint4 *)(box + ((((st & 1) * 4 + e) ^ (row & 7)) << 4));
-                            v[4 * e] = x.x;
-                            v[4 * e + 1] = x.y;
-                            v[4 * e + 2] = x.z;
-                            v[4 * e + 3] = x.w;
-                        }
-                        tmem_st16(lb + (st < 16 ? T_Q + st * 16 : T_QP + (st - 16) * 16), v);
-                    }
-                    tmem_st_wait();
+                // whether every page of the part has an id inside the cache
+                bool sound = true;
+                {
+                    const int c0 = page_of(a, w.k0 * NK), c1 = page_of(a, min(w.keys, (w.k0 + w.nt) * NK) - 1);
+                    const int *ids = p.table + (long)w.b * p.max_pages;
+#pragma unroll 2
+                    for (int col = c0 + lane; col <= c1; col += 32) sound = sound && (unsigned)__ldg(ids + col) < (unsigned)p.num_pages;
+                    sound = __all_sync(FULL, sound);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_ready);
-                float m = -INFINITY, l = 0.f;
-                // bit g of a tile's mask: its row group g holds keys
-                int have = lane < NGRP ? row_of(p, w, w.k0 * NK + lane * 8) : -1;
+                float top = -INFINITY, l = 0.f;   // running maximum (scaled, log2 units), this half's sum
+#pragma unroll 1
                 for (int i = 0; i < w.nt; ++i, ++n) {
                     const int s = n & 1;
-                    const unsigned groups = __ballot_sync(FULL, have >= 0);
-                    if (i + 1 < w.nt) have = lane < NGRP ? row_of(p, w, (w.k0 + i + 1) * NK + lane * 8) : -1;
-                    ok = __all_sync(FULL, ok && mbar_wait(&s_full[s], (n >> 1) & 1, abort, err));
+                    const uint32_t ph = (n >> 1) & 1;
+                    // bit g of the mask: row group g holds keys (looked up only where some page does not)
+                    unsigned groups = (1u << NGRP) - 1;
+                    if (!sound) groups = __ballot_sync(FULL, lane < NGRP && row_of(a, w, (w.k0 + i) * NK + lane * 8) >= 0);
+                    ok = __all_sync(FULL, ok && wait_for(&bars[B_SFULL + s], ph, ctl));
                     tc_fence_after();
-                    uint32_t sa[32], sb[8];
-                    if (act) {   // half 0: columns 0-31, 32-39; half 1: columns 40-47, 48-79
-                        const uint32_t base = lb + T_S + s * NK + h * HK;
-                        if (h == 0) {
-                            tmem_ld32(base, sa);
-                            tmem_ld8(base + 32, sb);
-                        } else {
-                            tmem_ld8(base, sb);
-                            tmem_ld32(base + 8, sa);
-                        }
+                    uint32_t sa[HK];
+                    if (act) {
+                        tmem_ld32(sbase + s * NK, sa);
                         tmem_ld_wait();
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_free[s]);
+                    if (lane == 0) mbar_arrive(&bars[B_SFREE + s]);
                     uint8_t *ext = smem + OFF_EXT + s * EXT_STRIDE;
+                    // staging slot s: its copy of tile n - 2 has read it (a fresh barrier passes)
+                    ok = __all_sync(FULL, ok && wait_for(&bars[B_STGFREE + s], ph ^ 1, ctl));
+                    bool rescaled = false;
                     if (act) {
-                        float x[HK];
-#pragma unroll
-                        for (int e = 0; e < HK; ++e)
-                            x[e] = __uint_as_float(h == 0 ? (e < 32 ? sa[e] : sb[e - 32]) : (e < 8 ? sb[e] : sa[e - 8]));
                         const int key0 = (w.k0 + i) * NK + h * HK;
                         if (groups != (1u << NGRP) - 1 || key0 + HK > w.keys) {
+                            const int end = w.keys - key0;
+                            groups >>= 4 * h;
 #pragma unroll
                             for (int e = 0; e < HK; ++e)
-                                if (key0 + e >= w.keys || !((groups >> (5 * h + (e >> 3))) & 1)) x[e] = -INFINITY;
+                                if (e >= end || !((groups >> (e >> 3)) & 1)) sa[e] = 0xff800000u;   // -inf
                         }
-                        float mx[8];
+                        float mx[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) mx[e] = x[e];
+                        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(sa[e]), __uint_as_float(sa[e + 4]));
 #pragma unroll
-                        for (int e = 8; e < HK; ++e) mx[e & 7] = fmaxf(mx[e & 7], x[e]);
-                        float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                         fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-                        red[(s * 2 + h) * ROWS + row] = mt;
+                        for (int e = 8; e < HK; e += 8)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(sa[e + q]), __uint_as_float(sa[e + q + 4])));
+                        float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        red[(s * 2 + h) * ROWS] = mt;
                         named_bar_sync(1 + quad, 64);   // the two warps of these 32 heads
-                        mt = fmaxf(mt, red[(s * 2 + (h ^ 1)) * ROWS + row]) * c;
-                        const bool need = mt > m + RESCALE_LOG2;
+                        mt = fmaxf(mt, red[(s * 2 + (h ^ 1)) * ROWS]) * c;
+                        // O is rescaled only when the maximum grows by more than 2^8 (both threads of a
+                        // row decide alike from the same numbers)
+                        const bool need = mt > top + RESCALE_LOG2;
                         float alpha = 1.f;
                         if (need) {
-                            alpha = m == -INFINITY ? 0.f : ex2(m - mt);
-                            m = mt;
+                            alpha = top == -INFINITY ? 0.f : ex2(top - mt);
+                            top = mt;
                         }
-                        l *= alpha;
-                        const float m_eff = m == -INFINITY ? 0.f : m;
-                        float ra[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                        uint32_t pk[HK / 2];
+                        rescaled = __any_sync(FULL, need && i > 0);
+                        const float m_eff = top == -INFINITY ? 0.f : top;
+                        float ra[4] = {0.f, 0.f, 0.f, 0.f};
+                        uint8_t *stg = smem + OFF_STG + s * P_BYTES + row * 128;
 #pragma unroll
-                        for (int e = 0; e < HK / 2; ++e) {
-                            const float p0 = ex2(fmaf(x[2 * e], c, -m_eff)), p1 = ex2(fmaf(x[2 * e + 1], c, -m_eff));
-                            ra[e & 7] += p0 + p1;
-                            pk[e] = pack_bf16(p0, p1);
+                        for (int q = 0; q < HK / 8; ++q) {
+                            uint32_t pk[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float p0 = ex2(fmaf(__uint_as_float(sa[8 * q + 2 * e]), c, -m_eff));
+                                const float p1 = ex2(fmaf(__uint_as_float(sa[8 * q + 2 * e + 1]), c, -m_eff));
+                                ra[e] += p0 + p1;
+                                pk[e] = pack_bf16(p0, p1);
+                            }
+                            *(uint4 *)(stg + (((h * (HK / 8) + q) ^ (row & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                         }
-                        l += ((ra[0] + ra[1]) + (ra[2] + ra[3])) + ((ra[4] + ra[5]) + (ra[6] + ra[7]));
-                        const bool rescaled = __any_sync(FULL, need && i > 0);
-                        // staging slot s: its copy of tile n - 2 has read it
-                        if (n >= 2) ok = __all_sync(FULL, ok && mbar_wait(&stg_free[s], ((n >> 1) - 1) & 1, abort, err));
+                        l = l * alpha + ((ra[0] + ra[1]) + (ra[2] + ra[3]));
                         if (i == w.nt - 1) {   // the row's sum, with the partner's half
-                            sums[h * ROWS + row] = l;
+                            sums[h * ROWS] = l;
                             named_bar_sync(1 + quad, 64);
-                            const float lt = l + sums[(h ^ 1) * ROWS + row];
+                            const float lt = l + sums[(h ^ 1) * ROWS];
                             if (h == 0) {
                                 ((float *)(ext + X_INVL))[row] = lt == 0.f ? 0.f : 1.f / lt;
                                 ((float *)(ext + X_LSE))[row] = lt == 0.f ? -INFINITY : m_eff + log2f(lt);
                             }
                         }
-                        uint8_t *stg = smem + OFF_STG + s * P_BYTES;
-#pragma unroll
-                        for (int q = 0; q < HK / 8; ++q) {
-                            const int j = h * (HK / 8) + q;
-                            uint8_t *dst = j < 8 ? stg + row * 128 + ((j ^ (row & 7)) << 4)
-                                                 : stg + P_BLK1 + row * 32 + (((j - 8) ^ ((row >> 2) & 1)) << 4);
-                            *(uint4 *)dst = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
-                        }
-                        if (h == 0) {
-                            ((float *)(ext + X_ALPHA))[row] = alpha;
-                            if (lane == 0) ((uint32_t *)(ext + X_FLAG))[quad] = rescaled ? 1u : 0u;
-                        }
-                        fence_proxy_async_smem();
-                    } else {
-                        if (n >= 2) ok = __all_sync(FULL, ok && mbar_wait(&stg_free[s], ((n >> 1) - 1) & 1, abort, err));
-                        if (h == 0 && lane == 0) ((uint32_t *)(ext + X_FLAG))[quad] = 0u;
-                        fence_proxy_async_smem();
+                        if (h == 0) ((float *)(ext + X_ALPHA))[row] = alpha;
                     }
+                    if (h == 0 && lane == 0) ((uint32_t *)(ext + X_FLAG))[quad] = rescaled ? 1u : 0u;
+                    fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&staged[s]);
+                    if (lane == 0) mbar_arrive(&bars[B_STAGED + s]);
                 }
             }
         } else if (warp == 10) {
             // ------------------------------- copier: staged P and extras -> rank 1
             if (lane == 0) {
                 const uint32_t peer_slot0 = map_peer(smem_u32(smem + OFF_PB), 1);
-                const uint32_t peer_full0 = map_peer(smem_u32(p_full), 1);   // armed by rank 1 itself
+                const uint32_t peer_full0 = map_peer(smem_u32(&bars[B_PFULL]), 1);   // armed by rank 1 itself
+#pragma unroll 1
                 for (int n = 0; n < n_all; ++n) {
                     const int s = n & 1;
-                    if (!mbar_wait(&staged[s], (n >> 1) & 1, abort, err)) break;
-                    if (n >= NPB && !mbar_wait_cluster(&p_empty[s], ((n >> 1) - 1) & 1, abort, err)) break;
+                    const uint32_t ph = (n >> 1) & 1;
+                    if (!wait_for(&bars[B_STAGED + s], ph, ctl)) break;
+                    if (!wait_for<true>(&bars[B_PEMPTY + s], ph ^ 1, ctl)) break;   // (passes at first)
                     const uint32_t dst = peer_slot0 + s * XSLOT, bar = peer_full0 + s * 8;
                     bulk_copy_to_peer(dst, smem + OFF_STG + s * P_BYTES, P_BYTES, bar);
                     bulk_copy_to_peer(dst + XOFF, smem + OFF_EXT + s * EXT_STRIDE, X_BYTES, bar);
                     bulk_commit();
                     bulk_wait_read<0>();
-                    mbar_arrive(&stg_free[s]);
+                    mbar_arrive(&bars[B_STGFREE + s]);
                 }
                 bulk_wait_all();   // nothing in flight into the peer at exit
+            }
+        } else {
+            // ------------------------------- queries into TMEM (warps 14-17, a thread per head)
+            // boxes of 64 dims x 128 heads through two slots: hi of the latent (boxes 0-7), hi and lo
+            // of the band (8, 9); the next part's first two land before the last part's MMAs are done
+            const int quad = warp & 3, row = quad * 32 + lane;
+            const uint32_t dst = tmem + ((uint32_t)(quad * 32) << 16) + T_Q;
+            int seg = 0, at = 0;   // `at`: boxes so far
+            bool ok = true;
+            for (; more && ok; next(), ++seg) {
+                const bool act = w.rt * ROWS + quad * 32 < p.H;
+#pragma unroll 1
+                for (int j = -2; j < 10 && ok; ++j) {   // box j out of its slot, box j + 2 into it
+                    if (j == 0 && seg > 0) {
+                        ok = wait_all(&bars[B_QFREE], (seg - 1) & 1, ctl);
+                        tc_fence_after();
+                    }
+                    if (j >= 0) {
+                        const int k = (at + j) & 1;
+                        ok = __all_sync(FULL, ok && wait_for(&bars[B_QFULL + k], ((at + j) >> 1) & 1, ctl));
+                        if (ok && act) {
+                            const uint8_t *box = smem + OFF_Q + k * 16384 + row * 128;
+                            uint32_t v[32];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const uint4 x = *(const uint4 *)(box + ((e ^ (row & 7)) << 4));
+                                v[4 * e] = x.x;
+                                v[4 * e + 1] = x.y;
+                                v[4 * e + 2] = x.z;
+                                v[4 * e + 3] = x.w;
+                            }
+                            tmem_st32(dst + j * 32, v);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars[B_QEMPTY + k]);
+                    }
+                    if (warp == 14 && lane == 0 && j + 2 < 10) {
+                        const int f = at + j + 2, k = f & 1;
+                        if (wait_for(&bars[B_QEMPTY + k], ((f >> 1) & 1) ^ 1, ctl)) {
+                            mbar_arrive_expect_tx(&bars[B_QFULL + k], 128 * a.q_rows);
+                            tma_load_3d(smem + OFF_Q + k * 16384, j < 6 ? &m.qh : (j == 6 ? &m.rh : &m.rl), &bars[B_QFULL + k],
+                                        j < 6 ? 64 * (j + 2) : 0, w.rt * ROWS, w.b);
+                        }
+                    }
+                    __syncwarp();
+                }
+                at += 10;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_QREADY]);
             }
         }
     } else {
         if (warp == 0) {
             // ------------------------------------------------ TMA producer (latent rows)
-            const int nbox = NK / a.box_rows, nrg = a.box_rows >> 3, none = (p.num_pages * (long)p.page) >> 3;
-            int n = 0, seg = 0;
-            bool go = work;
-            while (go) {
-                // the previous part's epilogue has left the stages
-                if (seg > 0) go = __all_sync(FULL, mbar_wait(epi_done, (seg - 1) & 1, abort, err));
-                int row = lane < nbox ? row_of(p, w, w.k0 * NK + lane * a.box_rows) : -1;
-                for (int i = 0; i < w.nt && go; ++i, ++n) {
-                    const int s = n & 1;
-                    if (n >= VST) go = __all_sync(FULL, mbar_wait(&v_empty[s], ((n >> 1) - 1) & 1, abort, err));
-                    if (!go) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&v_full[s], VSTAGE);
-                    __syncwarp();
-                    if (lane < nbox)
-                        tma_load_4d(smem + s * VSTAGE + lane * nrg * 8 * ATOM, &mV, &v_full[s], 0, 0, 0, row >= 0 ? row >> 3 : none);
-                    if (lane == 0) *prog = n + 1;   // paces the prefetching warp
-                    if (i + 1 < w.nt && lane < nbox) row = row_of(p, w, (w.k0 + i + 1) * NK + lane * a.box_rows);
-                }
-                // once the part's last P C MMAs are done its q_lo block goes to the stages
-                go = go && __all_sync(FULL, mbar_wait(o_final, seg & 1, abort, err));
-                if (!go) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(qb_full, 8 * 16384);
-                    for (int i = 0; i < 8; ++i) tma_load_3d(smem + QB_OFF + i * 16384, &mQl, qb_full, 64 * i, w.rt * ROWS, w.b);
-                }
-                __syncwarp();
-                ++seg;
-                go = w.next(p);
-            }
-        } else if (warp == 10) {
-            // ------------------------------- L2 prefetch of the key tiles rank 0 loads next
-            const int nbox = NK / a.box_rows;
-            const uint64_t t0 = global_ns();
-            uint64_t last = t0;
-            int n = 0, seen = 0;
-            bool go = work;
-            while (go) {
-                for (int i = 0; i < w.nt && go; ++i, ++n) {
-                    const int row = lane < nbox ? row_of(p, w, (w.k0 + i) * NK + lane * a.box_rows) : -1;
-                    while (*prog < n - PF1 + 1) {   // rank 1's loads of tile n - PF1 are issued
-                        const int now = *prog;
-                        if (now != seen) {
-                            seen = now;
-                            last = global_ns();
+            int slot = 0;
+            uint32_t ph = 1;   // a fresh barrier's previous phase counts as complete
+            bool go = true;
+            for (; more && go; next()) {
+                Rows<UNIT> rows{-1, -1, -64};
+#pragma unroll 1
+                for (int i = 0; i < w.nt && go; ++i) {
+                    const int row = rows.tile(a, w, i, lane), end = w.keys - (w.k0 + i) * NK;
+                    // a request's last tile goes by row groups, with zeros behind the last one with keys
+                    const bool whole = end >= NK;
+                    const int first = __shfl_sync(FULL, row, lane / NRG);
+                    int rg = whole ? row : (first >= 0 && 8 * lane < end ? first + lane % NRG * 8 : -1);
+                    rg = rg >= 0 ? rg >> 3 : none;
+                    const int boxes = whole ? UNITS : NGRP;
+                    const uint32_t off = lane * (whole ? NRG : 1) * 4 * ATOM;
+#pragma unroll 1
+                    for (int hf = 0; hf < 2 && go; ++hf) {
+                        go = wait_all(&bars[B_VEMPTY + slot], ph, ctl);
+                        if (!go) break;
+                        uint64_t *full = &bars[B_VFULL + slot];
+                        if (lane == 0) mbar_arrive_expect_tx(full, VHALF);
+                        if (lane < boxes) tma_load_4d(smem + slot * VHALF + off, whole ? &m.v : &m.v8, full, 0, 0, 4 * hf, rg);
+                        __syncwarp();
+                        if (++slot == VSL) {
+                            slot = 0;
+                            ph ^= 1;
                         }
-                        if (*abort || global_ns() - last > WAIT_NS) {
-                            go = false;
-                            break;
-                        }
-                        __nanosleep(128);
-                    }
-                    go = __all_sync(FULL, go);
-                    if (!go) break;
-                    if (row >= 0) {
-                        l2_prefetch((const bf16 *)p.c_cache + (long)row * DK, a.box_rows * DK * 2);
-                        l2_prefetch((const bf16 *)p.kpe_cache + (long)row * DR, a.box_rows * DR * 2);
                     }
                 }
-                go = go && w.next(p);
             }
         } else if (warp == 1) {
             // ---------------------------------------------------- O += P C issuer
-            int n = 0, seg = 0;
-            bool ok = work;
-            while (ok) {
-                if (seg > 0) ok = __all_sync(FULL, mbar_wait(epi_done, (seg - 1) & 1, abort, err));   // O has been read
+            int n = 0, seg = 0, slot = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (; more && ok; next(), ++seg) {
+                ok = wait_all(&bars[B_EPIDONE], (seg & 1) ^ 1, ctl);   // the last part's O has been read
+#pragma unroll 1
                 for (int i = 0; i < w.nt && ok; ++i, ++n) {
                     const int s = n & 1;
-                    ok = __all_sync(FULL, mbar_wait(&v_full[s], (n >> 1) & 1, abort, err));
-                    if (!ok) break;
                     const int end = w.keys - (w.k0 + i) * NK;   // rows of the tile in front of the request's end
-                    if (end < NK && (end & (a.box_rows - 1))) {
-                        // rows behind the end in its box: zeros, whatever the cache holds there
-                        for (int r = end; r < (end | (a.box_rows - 1)) + 1; ++r)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int j = lane + 32 * e;
-                                *(uint4 *)(smem + s * VSTAGE + (r >> 3) * 8 * ATOM + (j >> 3) * ATOM + (r & 7) * 128 + (j & 7) * 16) =
+#pragma unroll 1
+                    for (int hf = 0; hf < 2 && ok; ++hf) {
+                        ok = wait_all(&bars[B_VFULL + slot], ph, ctl);
+                        uint8_t *vs = smem + slot * VHALF;
+                        if (end < NK && (end & 7)) {
+                            // rows behind the end in its row group: zeros, whatever the cache holds there
+#pragma unroll 1
+                            for (int r = end; r & 7; ++r)
+                                *(uint4 *)(vs + (r >> 3) * 4 * ATOM + (lane >> 3) * ATOM + (r & 7) * 128 + (lane & 7) * 16) =
                                     make_uint4(0, 0, 0, 0);
-                            }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    ok = __all_sync(FULL, mbar_wait(&pc_ready[s], (n >> 1) & 1, abort, err));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint8_t *slot = smem + OFF_PB + s * XSLOT;
-                    const uint64_t pa0 = sdesc_kmajor(slot), pa1 = sdesc_kmajor_sw32(slot + P_BLK1);
-                    const uint64_t vb = sdesc_sw128(smem_u32(smem + s * VSTAGE), ATOM, 8 * ATOM);   // MN-major
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < NK / 16; ++kk) {   // 16 keys per step, 256 latent dims per MMA
-                            const uint64_t pa = kk < 4 ? pa0 + (uint64_t)(2 * kk) : pa1;
-                            const uint32_t acc = (i | kk) != 0;
-                            mma_ss(tmem, pa, vb + (uint64_t)(kk * (16 * ATOM >> 4)), a.idesc_pv, acc);
-                            mma_ss(tmem + 256, pa, vb + (uint64_t)((kk * 16 * ATOM + 4 * ATOM) >> 4), a.idesc_pv, acc);
+                            fence_proxy_async_smem();
+                            __syncwarp();
                         }
-                        mma_commit(&v_empty[s]);
-                        mma_commit_mc(&p_empty[s], 3);
+                        ok = __all_sync(FULL, ok && (hf || wait_for(&bars[B_PCREADY + s], (n >> 1) & 1, ctl)));
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t pa = sdesc_kmajor(smem + OFF_PB + s * XSLOT);
+                            const uint64_t vb = sdesc_sw128(smem_u32(vs), ATOM, 4 * ATOM);   // MN-major
+#pragma unroll
+                            for (int kk = 0; kk < NK / 16; ++kk)   // 16 keys per step, 256 latent dims per MMA
+                                mma_ss(tmem + hf * 256, pa + (uint64_t)(2 * kk), vb + (uint64_t)(kk * (8 * ATOM >> 4)), a.idesc_pv,
+                                       (i | kk) != 0);
+                            mma_commit(&bars[B_VEMPTY + slot]);
+                            if (hf) mma_commit_mc(&bars[B_PEMPTY + s], 3);
+                        }
+                        __syncwarp();
+                        if (++slot == VSL) {
+                            slot = 0;
+                            ph ^= 1;
+                        }
                     }
-                    __syncwarp();
                 }
-                if (!ok) break;
-                if (elect_one()) mma_commit(o_final);
+                if (ok && elect_one()) mma_commit(&bars[B_OFINAL]);
                 __syncwarp();
-                ++seg;
-                ok = w.next(p);
             }
         } else if (warp >= 2 && warp < 10) {
             // ------------------------ row rescale (warps 2-5) + epilogue (warps 2-9)
             const int quad = warp & 3, row = quad * 32 + lane, g = (warp - 2) >> 2;
             const uint32_t lb = tmem + ((uint32_t)(quad * 32) << 16);
-            float *red1 = (float *)(smem + OFF_RED1);
+            float *invs = (float *)(smem + OFF_INV) + row;
             int n = 0, seg = 0;
             bool ok = true;   // as in the softmax warps: every barrier is reached
-            for (bool more = work; more; more = w.next(p), ++seg) {
+            for (; more; next(), ++seg) {
                 const bool act = w.rt * ROWS + quad * 32 < p.H;
-                float inv_l = 0.f, lse2 = -INFINITY;
+                const long slot = part - p.parts;
                 if (g == 0) {
+                    float lse2 = -INFINITY, inv_l = 0.f;
+#pragma unroll 1
                     for (int i = 0; i < w.nt && ok; ++i, ++n) {
                         const int s = n & 1;
-                        ok = __all_sync(FULL, mbar_wait_cluster(&p_full[s], (n >> 1) & 1, abort, err));
+                        const uint32_t ph = (n >> 1) & 1;
+                        ok = __all_sync(FULL, wait_for<true>(&bars[B_PFULL + s], ph, ctl));
                         // slot s's previous use is over (its transfer waited for that), so the
                         // parity tests below are at most one phase behind
-                        if (ok && n >= NPB) ok = __all_sync(FULL, mbar_wait(&p_empty[s], ((n >> 1) - 1) & 1, abort, err));
+                        ok = __all_sync(FULL, ok && wait_for(&bars[B_PEMPTY + s], ph ^ 1, ctl));
                         if (!ok) break;
-                        if (warp == 2 && lane == 0 && n + NPB < n_all) mbar_arrive_expect_tx(&p_full[s], P_BYTES + X_BYTES);
+                        if (warp == 2 && lane == 0 && n + NPB < n_all) mbar_arrive_expect_tx(&bars[B_PFULL + s], P_BYTES + X_BYTES);
                         const uint8_t *xs = smem + OFF_PB + s * XSLOT + XOFF;
-                        const uint32_t *fl = (const uint32_t *)(xs + X_FLAG);
-                        if ((fl[0] | fl[1] | fl[2] | fl[3]) != 0u) {   // the same answer in every thread; i > 0
+                        const uint4 fl = *(const uint4 *)(xs + X_FLAG);
+                        if ((fl.x | fl.y | fl.z | fl.w) != 0u) {   // the same answer in every thread; i > 0
                             // O holds tile n - 1's product before it is rescaled
-                            ok = __all_sync(FULL, mbar_wait(&p_empty[s ^ 1], ((n - 1) >> 1) & 1, abort, err));
+                            ok = wait_all(&bars[B_PEMPTY + (s ^ 1)], ((n - 1) >> 1) & 1, ctl);
                             if (!ok) break;
                             tc_fence_after();
                             const float al = act ? ((const float *)(xs + X_ALPHA))[row] : 1.f;
                             if (__any_sync(FULL, al != 1.f)) {
+#pragma unroll 1
                                 for (int cc = 0; cc < 16; ++cc) {
                                     uint32_t o[32];
                                     tmem_ld32(lb + cc * 32, o);
@@ -898,77 +952,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                             lse2 = ((const float *)(xs + X_LSE))[row];
                         }
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&pc_ready[s]);
+                        if (lane == 0) mbar_arrive(&bars[B_PCREADY + s]);
                     }
+                    invs[(seg & 1) * ROWS] = inv_l;
+                    if (ok && w.rt * ROWS + row < p.H) p.pl[slot * p.row_tile + row] = lse2 * 0.69314718055994531f;
                 }
-                // ---- epilogue: the part's normalised output (warps 2-5 latent dims 0-255, 6-9
-                // dims 256-511) and its log-sum-exp with the first-order term of q_lo
-                if (g == 0) red1[ROWS + row] = inv_l;
-                named_bar_sync(6, 256);
-                if (g == 1) inv_l = red1[ROWS + row];
-                ok = __all_sync(FULL, ok && mbar_wait(o_final, seg & 1, abort, err));
-                ok = __all_sync(FULL, ok && mbar_wait(qb_full, seg & 1, abort, err));
+                // ---- epilogue: the part's normalised output, 256 latent dims per warp: 16 columns of 32
+                // heads at a time, turned in shared memory so that a store writes whole 64-byte pieces
+                named_bar_sync(1 + quad, 64);   // the two warps of these 32 heads
+                const float inv_l = invs[(seg & 1) * ROWS];
+                ok = __all_sync(FULL, ok && wait_for(&bars[B_OFINAL], seg & 1, ctl));
                 tc_fence_after();
-                const long slot = worker + (long)w.b * p.row_tiles + w.rt;
-                float dot[4] = {0.f, 0.f, 0.f, 0.f};
                 if (ok && act) {
-                    // 32 x 32 fp32 blocks, 128-byte swizzled, written by TMA tile stores (rows behind
-                    // the last head lie outside the map)
-                    uint8_t *buf = smem + (warp - 2) * 4096;
-                    const int d0 = 256 * g;
+                    uint8_t *buf = smem + OFF_OUT + (warp - 2) * 2048;
+                    const int live = min(32, p.H - (w.rt * ROWS + quad * 32));
+                    float *po = p.po + (slot * p.row_tile + quad * 32 + (lane >> 2)) * DK + 256 * g + (lane & 3) * 4;
 #pragma unroll 1
-                    for (int cc = 0; cc < 8; ++cc) {
-                        uint32_t o[32];
-                        tmem_ld32(lb + d0 + cc * 32, o);
+                    for (int cc = 0; cc < 16; ++cc, po += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(lb + 256 * g + cc * 16, o);
                         tmem_ld_wait();
-                        float ov[32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) ov[e] = __uint_as_float(o[e]) * inv_l;
-                        if (cc >= 1) {
-                            if (lane == 0) bulk_wait_read<0>();
-                            __syncwarp();
-                        }
-#pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            *(float4 *)(buf + lane * 128 + ((v ^ (lane & 7)) << 4)) =
-                                make_float4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
-                        fence_proxy_async_smem();
+                        for (int e = 0; e < 4; ++e)   // 16-byte piece e of row `lane` at piece e ^ (row / 2 mod 4)
+                            *(float4 *)(buf + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
+                                make_float4(__uint_as_float(o[4 * e]) * inv_l, __uint_as_float(o[4 * e + 1]) * inv_l,
+                                            __uint_as_float(o[4 * e + 2]) * inv_l, __uint_as_float(o[4 * e + 3]) * inv_l);
                         __syncwarp();
-                        if (lane == 0) {   // columns in 16-bit units of the map
-                            asm volatile(
-                                "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"((uint64_t)&mP),
-                                "r"(smem_u32(buf)), "r"((d0 + 32 * cc) * 2), "r"(quad * 32), "r"((int)slot)
-                                : "memory");
-                            bulk_commit();
-                        }
-                        const int od = d0 + 32 * cc;
-                        const uint8_t *qr = smem + QB_OFF + (od >> 6) * 16384 + row * 128;
+                        float4 v[4];
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const uint4 x = *(const uint4 *)(qr + (((((od >> 5) & 1) * 4 + v) ^ (row & 7)) << 4));
-                            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                dot[e] = fmaf(__uint_as_float(u[e] << 16), ov[8 * v + 2 * e], dot[e]);
-                                dot[e] = fmaf(__uint_as_float(u[e] & 0xffff0000u), ov[8 * v + 2 * e + 1], dot[e]);
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = 8 * e + (lane >> 2);
+                            v[e] = *(const float4 *)(buf + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
                         }
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (8 * e + (lane >> 2) < live) *(float4 *)(po + 8 * e * DK) = v[e];
                     }
-                    if (lane == 0) bulk_wait_all();
-                }
-                if (g == 1) red1[row] = (dot[0] + dot[1]) + (dot[2] + dot[3]);
-                named_bar_sync(7, 256);
-                if (g == 0 && ok && w.rt * ROWS + row < p.H) {
-                    const float corr = ((dot[0] + dot[1]) + (dot[2] + dot[3]) + red1[row]) * a.scale_log2;
-                    p.pl[slot * p.row_tile + row] = lse2 == -INFINITY ? -INFINITY : (lse2 + corr) * 0.69314718055994531f;
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(epi_done);
+                if (lane == 0) mbar_arrive(&bars[B_EPIDONE]);
             }
         }
     }
-    if (tid == 0 && *abort) settle();
+    __syncwarp();
+    if (tid == 0 && ((volatile Ctl *)ctl)->abort) settle();
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // the peer may still address this CTA's barriers and slots until here
@@ -1000,7 +1029,6 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     using ull = unsigned long long;
     cudaError_t e;
     const ull rows = (ull)p.num_pages * p.page, heads = (ull)p.B * p.H;
-    const unsigned br = p.page % 16 == 0 ? 16 : 8;
     Absorb ab{};
     ab.p = p;
     ab.qhi = (bf16 *)p.qabs;
@@ -1012,54 +1040,55 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     ab.groups = std::max(1, std::min(want, most));
     ab.group = ((p.B + ab.groups - 1) / ab.groups + 7) / 8 * 8;
     ab.groups = (p.B + ab.group - 1) / ab.group;
+    ab.rot_blocks = (int)(((long)p.B * ((p.H + 31) / 32) + 3) / 4);
     paged_turns(p.base, DR, ab.turns.v);
 
-    CUtensorMap mK3, mK2, mV, mR, mQh, mQl, mRh, mRl, mP;
-    {
-        const ull d[4] = {64, 8, 8, rows / 8}, s[3] = {1024, 128, 8192};
-        const unsigned b3[4] = {64, 8, 3, br / 8}, b2[4] = {64, 8, 2, br / 8}, b8[4] = {64, 8, 8, br / 8};
-        if ((e = make_tma_map(&mK3, p.c_cache, 4, d, s, b3)) != cudaSuccess) return e;
-        if ((e = make_tma_map(&mK2, p.c_cache, 4, d, s, b2)) != cudaSuccess) return e;
-        if ((e = make_tma_map(&mV, p.c_cache, 4, d, s, b8)) != cudaSuccess) return e;
-        const ull dr[2] = {64, rows}, sr[1] = {128};
-        const unsigned bb[2] = {64, br};
-        if ((e = make_tma_map(&mR, p.kpe_cache, 2, dr, sr, bb)) != cudaSuccess) return e;
-    }
-    {
-        const unsigned bq[3] = {64, ROWS, 1};
-        const ull d[3] = {DK, (ull)p.H, (ull)p.B}, s[2] = {DK * 2, (ull)p.H * DK * 2};
-        if ((e = make_tma_map(&mQh, ab.qhi, 3, d, s, bq)) != cudaSuccess) return e;
-        if ((e = make_tma_map(&mQl, ab.qlo, 3, d, s, bq)) != cudaSuccess) return e;
-        const ull dr[3] = {DR, (ull)p.H, (ull)p.B}, sr[2] = {DR * 2, (ull)p.H * DR * 2};
-        if ((e = make_tma_map(&mRh, ab.rhi, 3, dr, sr, bq)) != cudaSuccess) return e;
-        if ((e = make_tma_map(&mRl, ab.rlo, 3, dr, sr, bq)) != cudaSuccess) return e;
-        // the fp32 partials as 16-bit units: [slots][row_tile][1024], boxes of 32 rows x 32 values
-        const ull slots = (ull)p.workers + (ull)p.B * p.row_tiles;
-        const ull dp[3] = {2 * DK, (ull)p.row_tile, slots}, sp[2] = {DK * 4, (ull)p.row_tile * DK * 4};
-        const unsigned bp[3] = {64, 32, 1};
-        if ((e = make_tma_map(&mP, p.po, 3, dp, sp, bp)) != cudaSuccess) return e;
-    }
     Attn at{};
+    int unit = NK;   // rows that always share a page: the largest power of two up to a tile that divides one
+    while (p.page % unit) unit /= 2;
+    at.q_rows = std::min(ROWS, (p.H + 31) / 32 * 32);
+    Maps m{};
+    {
+        const ull d[4] = {64, 8, 8, rows / 8}, s[3] = {1024, 128, 8192}, dr[2] = {64, rows}, sr[1] = {128};
+        const unsigned g = (unsigned)unit / 8;
+        const unsigned b3[4] = {64, 8, 3, g}, b2[4] = {64, 8, 2, g}, b8[4] = {64, 8, 4, g}, br[2] = {64, 8 * g};
+        if ((e = make_tma_map(&m.k3, p.c_cache, 4, d, s, b3)) != cudaSuccess) return e;
+        if ((e = make_tma_map(&m.k2, p.c_cache, 4, d, s, b2)) != cudaSuccess) return e;
+        if ((e = make_tma_map(&m.v, p.c_cache, 4, d, s, b8)) != cudaSuccess) return e;
+        if ((e = make_tma_map(&m.r, p.kpe_cache, 2, dr, sr, br)) != cudaSuccess) return e;
+        const unsigned b1[4] = {64, 8, 4, 1};
+        if ((e = make_tma_map(&m.v8, p.c_cache, 4, d, s, b1)) != cudaSuccess) return e;
+    }
+    {
+        const unsigned bq[3] = {64, (unsigned)at.q_rows, 1};
+        const ull d[3] = {DK, (ull)p.H, (ull)p.B}, s[2] = {DK * 2, (ull)p.H * DK * 2};
+        if ((e = make_tma_map(&m.qh, ab.qhi, 3, d, s, bq)) != cudaSuccess) return e;
+        const ull dr[3] = {DR, (ull)p.H, (ull)p.B}, sr[2] = {DR * 2, (ull)p.H * DR * 2};
+        if ((e = make_tma_map(&m.rh, ab.rhi, 3, dr, sr, bq)) != cudaSuccess) return e;
+        if ((e = make_tma_map(&m.rl, ab.rlo, 3, dr, sr, bq)) != cudaSuccess) return e;
+    }
     at.p = p;
-    at.box_rows = (int)br;
+    while ((1u << at.page_shift) < (unsigned)p.page) ++at.page_shift;
+    at.page_mul = (uint32_t)((((ull)1 << 32) * (((ull)1 << at.page_shift) - p.page)) / p.page + 1);
     at.scale_log2 = p.scale * 1.4426950408889634f;
     at.idesc_s = idesc_f16(128, NK, false);
     at.idesc_pv = idesc_f16(128, 256, false, true);
-    if ((e = cudaFuncSetAttribute(paged_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess)
+    auto attn = unit == 64 ? paged_attn_tc_kernel<64> : unit == 32 ? paged_attn_tc_kernel<32> : unit == 16 ? paged_attn_tc_kernel<16> : paged_attn_tc_kernel<8>;
+    if ((e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess)
         return e;
     {
         ProfScope ps("paged_absorb", st);
-        paged_absorb_tc_kernel<<<(unsigned)(p.H * 4 * ab.groups + 1), 128, 0, st>>>(ab);
+        paged_absorb_tc_kernel<<<(unsigned)(p.H * 4 * ab.groups + 1 + ab.rot_blocks), 128, 0, st>>>(ab);
     }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     {
         ProfScope ps("paged_attn", st);
-        e = launch_after(paged_attn_tc_kernel, 2 * p.workers, NTHREADS, SMEM_BYTES, st, mK3, mK2, mV, mR, mQh, mQl, mRh, mRl, mP, at);
+        e = launch_after(attn, 2 * p.workers, NTHREADS, SMEM_BYTES, st, m, at);
     }
     if (e != cudaSuccess) return e;
     {
         ProfScope ps("paged_join", st);
-        e = launch_after(paged_join_tc_kernel, (unsigned)(p.H * 2 * ((p.B + JB - 1) / JB)), 128, 0, st, p);
+        e = launch_after(paged_join_tc_kernel, (unsigned)(p.H * ((p.B + JB - 1) / JB)), JNT, 0, st, p, (const bf16 *)ab.qlo);
     }
     return e;
 }

@@ -256,7 +256,7 @@ mla_status mla_lse_combine(mla_dtype out_dtype, int n_splits, int rows, int D,
 /*
  * Paged latent cache.  A cache of num_pages pages of page_size tokens:
  *   c_cache [num_pages, page_size, d_kv]   kpe_cache [num_pages, page_size, d_rope]
- * (num_pages * page_size < 2^31; byte offsets may pass 2^32).  A request's token at position p
+ * (num_pages * page_size < 2^31, max_pages * page_size <= 2^30; byte offsets may pass 2^32).  A request's token at position p
  * lies in slot block_table[b][p / page_size] * page_size + p % page_size, where row b of
  * block_table [B, max_pages] (int32) holds the ids of its pages.  A step of a server is
  * mla_paged_tables (which pages and slots the new tokens take), mla_paged_append (their
