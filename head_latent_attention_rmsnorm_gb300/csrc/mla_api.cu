@@ -1156,10 +1156,16 @@ size_t paged_decode_ws(PagedDecode *p, void *base) {
     if (p->tc) {
         p->parts = (PagedPart *)c.take(slots * sizeof(PagedPart));
         p->first = (int *)c.take((size_t)p->workers * 2 * sizeof(int));
+        p->spans = (int2 *)c.take((size_t)p->B * p->row_tiles * sizeof(int2));
     }
     p->qabs = c.take(rows * p->Dk * 4);
     p->qpe = c.take(rows * p->Dr * 4);
-    p->po = (float *)c.take(slots * p->row_tile * p->Dk * 4);
+    if (p->tc) {
+        p->po = (__half *)c.take(slots * p->row_tile * p->Dk * 2);
+        p->pscale = (float *)c.take(slots * p->row_tile * 2 * 4);
+    } else {
+        p->po32 = (float *)c.take(slots * p->row_tile * p->Dk * 4);
+    }
     p->pl = (float *)c.take(slots * p->row_tile * 4);
     return align_up(c.off, 256);
 }

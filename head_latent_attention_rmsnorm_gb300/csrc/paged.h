@@ -1,6 +1,7 @@
 // paged.h -- host interface of the paged-cache kernels (paged.cu, paged_simt.cu).
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -41,8 +42,12 @@ struct PagedDecode {
     long *tile_off;                  // [B + 1] first tile of request b, for one row tile
     PagedPart *parts;                // [slots], the tensor-core form's
     int *first;                      // [2][workers]: a worker's first part, its number of tiles
+    int2 *spans;                     // [B row_tiles]: an item's first part, its number of parts
     void *qabs, *qpe;                // absorbed and rotated queries
-    float *po, *pl;                  // partials [workers + B row_tiles][row_tile][Dk], [..][row_tile]
+    // partials [slots][row_tile][Dk] and their log-sum-exps [slots][row_tile], slots = workers + B row_tiles:
+    // fp32, or fp16 times a scale per half row [slots][row_tile][2] in the tensor-core form
+    float *po32, *pl, *pscale;
+    __half *po;
 };
 cudaError_t paged_decode_simt(const PagedDecode &p, cudaStream_t st);
 

@@ -102,38 +102,55 @@ __device__ void plan_block(const PagedDecode &p) {
     if (tid == 0) p.tile_off[p.B] = carry;
     if (!p.parts) return;
     __syncthreads();
-    // the parts: item (b, rt) is cut where a worker's share ends
+    // The parts begin where a worker's share begins and where an item does (one may be both): a thread
+    // per beginning finds its part's worker, item and end.
     const long total = carry * p.row_tiles;
     const int W = total ? active_workers(p, total) : 0;
-    for (int c = tid; c < p.workers; c += NT) {
-        int f = 0, n = 0;
-        if (c < W) {
-            const long t0 = c * total / W;
-            n = (int)((c + 1) * total / W - t0);
-            const int b = request_of(p, t0);
-            f = c + b * p.row_tiles + (int)((t0 - p.tile_off[b] * p.row_tiles) / (p.tile_off[b + 1] - p.tile_off[b]));
-        }
-        p.first[c] = f;
-        p.first[p.workers + c] = n;
-    }
-    for (long item = tid; item < (long)p.B * p.row_tiles; item += NT) {
-        const int b = (int)(item / p.row_tiles), rt = (int)(item % p.row_tiles);
-        const long o = p.tile_off[b], per = p.tile_off[b + 1] - o, i0 = o * p.row_tiles + rt * per;
-        if (per == 0) continue;
-        for (int c = worker_of(i0, total, W), c1 = worker_of(i0 + per - 1, total, W); c <= c1; ++c) {
-            const long s0 = max(c * total / W, i0), end = (c + 1) * total / W, s1 = min(end, i0 + per);
-            PagedPart x{};
-            x.b = b;
-            x.rt = rt;
-            x.k0 = (int)(s0 - i0);
-            x.nt = (int)(s1 - s0);
-            x.keys = keys_of(p, b);
-            if (s1 < end) {   // the worker goes on with the next item that has tiles
-                x.next = 1;
-                if (rt == p.row_tiles - 1)
-                    for (int e = b + 1; p.tile_off[e + 1] == p.tile_off[e]; ++e) x.next += p.row_tiles;
+    const long items = (long)p.B * p.row_tiles;
+    for (long k = tid; k < p.workers + items; k += NT) {
+        const bool worker = k < p.workers;
+        long t0 = 0;
+        int b = 0, c = (int)k, rt = 0;
+        if (worker) {
+            if (c >= W) {
+                p.first[c] = p.first[p.workers + c] = 0;
+                continue;
             }
-            p.parts[c + item] = x;
+            t0 = c * total / W;
+            b = request_of(p, t0);
+        } else {
+            b = (int)((k - p.workers) / p.row_tiles);
+            rt = (int)((k - p.workers) % p.row_tiles);
+        }
+        const long o = p.tile_off[b], per = p.tile_off[b + 1] - o;
+        if (per == 0) {
+            p.spans[k - p.workers] = make_int2(0, 0);
+            continue;
+        }
+        if (worker) {
+            rt = (int)((t0 - o * p.row_tiles) / per);
+        } else {
+            t0 = o * p.row_tiles + rt * per;
+            c = worker_of(t0, total, W);
+            p.spans[k - p.workers] = make_int2(c + (int)(k - p.workers), worker_of(t0 + per - 1, total, W) - c + 1);
+        }
+        const long i0 = o * p.row_tiles + rt * per, i1 = i0 + per, end = (c + 1) * total / W, t1 = min(end, i1);
+        const int item = b * p.row_tiles + rt;
+        PagedPart x{};
+        x.b = b;
+        x.rt = rt;
+        x.k0 = (int)(t0 - i0);
+        x.nt = (int)(t1 - t0);
+        x.keys = keys_of(p, b);
+        if (t1 < end) {   // the worker goes on with the next item that has tiles
+            x.next = 1;
+            if (rt == p.row_tiles - 1)
+                for (int e = b + 1; p.tile_off[e + 1] == p.tile_off[e]; ++e) x.next += p.row_tiles;
+        }
+        p.parts[c + item] = x;
+        if (worker) {
+            p.first[c] = c + item;
+            p.first[p.workers + c] = (int)(end - t0);
         }
     }
 }

@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
             const float inv = sL[h] == 0.f ? 0.f : 1.f / sL[h];
-            float *po = p.po + (slot * HT + h) * p.Dk + 2 * tid;
+            float *po = p.po32 + (slot * HT + h) * p.Dk + 2 * tid;
             if (h < nh && 2 * tid < p.Dk) {
                 po[0] = o[h][0] * inv;
                 if (2 * tid + 1 < p.Dk) po[1] = o[h][1] * inv;
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(NT) paged_join_simt_kernel(const __grid_consta
             if (sum != 0.f)
                 for (int c = c0; c <= c1; ++c) {
                     const long s = (c + item) * p.row_tile + r;
-                    if (p.pl[s] != -INFINITY) o = fmaf(expf(p.pl[s] - lse), p.po[s * p.Dk + d], o);
+                    if (p.pl[s] != -INFINITY) o = fmaf(expf(p.pl[s] - lse), p.po32[s * p.Dk + d], o);
                 }
             sm[j * p.Dk + d] = o;
         }

@@ -34,6 +34,7 @@
 // keeps q to 2^-17.  P is bf16 (relative 2^-8 on the weights of an average; the sums take the
 // unrounded ones).  Partials are fp32.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
@@ -215,8 +216,8 @@ constexpr int JB = 16, JNT = 256, JPITCH = DK * 2 + 16, JMAXC = 80;
 
 __global__ void __launch_bounds__(JNT, 2) paged_join_tc_kernel(const __grid_constant__ PagedDecode p, const bf16 *qlo) {
     __shared__ __align__(16) uint8_t so[2][JB * JPITCH];
-    __shared__ float sw[JB][JMAXC];   // the parts' weights
-    __shared__ int sc[JB][2];         // first worker, number of parts
+    __shared__ float sw[2][JB][JMAXC];   // the parts' weights for either half of the dims
+    __shared__ int sc[JB][2];         // first part, number of parts
     __shared__ float sl[JB], sd[4][JB];   // log-sum-exp without the q_lo term; the warps' shares of q_lo . o
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int nb_groups = (p.B + JB - 1) / JB, h = blockIdx.x / nb_groups, b0 = (blockIdx.x % nb_groups) * JB;
@@ -225,39 +226,41 @@ __global__ void __launch_bounds__(JNT, 2) paged_join_tc_kernel(const __grid_cons
     if (tid == 0 && b0 == 0) l2_prefetch(w, DV * DK * 2);
     w += (warp * 16 + g) * DK + 16 * t;
     pdl_wait();
-    const long total = p.tile_off[p.B] * p.row_tiles;
-    const int W = total ? active_workers(p, total) : 0;
 #pragma unroll 1
     for (int j = warp; j < JB; j += JNT / 32) {   // a warp per request
-        const int b = b0 + j;
-        int c0 = 0, n = 0;
+        int s0 = 0, n = 0;
         if (j < nb) {
-            const long o0 = p.tile_off[b], per = p.tile_off[b + 1] - o0, first = o0 * p.row_tiles + rt * per;
-            const float *pl = p.pl + ((long)b * p.row_tiles + rt) * p.row_tile + r;
-            if (per > 0) {
-                c0 = worker_of(first, total, W);
-                n = worker_of(first + per - 1, total, W) - c0 + 1;
-            }
-            float m = -INFINITY, s = 0.f;
-            for (int i = lane; i < n; i += 32) {
-                const float x = pl[(long)(c0 + i) * p.row_tile];
-                sw[j][i] = x;
-                m = fmaxf(m, x);
+            const int2 sp = __ldcg(p.spans + (long)(b0 + j) * p.row_tiles + rt);
+            s0 = sp.x;
+            n = sp.y;
+            const float *pl = p.pl + (long)s0 * p.row_tile + r;
+            const float2 *ps = (const float2 *)p.pscale + (long)s0 * p.row_tile + r;
+            float x[3], m = -INFINITY, s = 0.f;   // up to 96 parts
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                x[i] = lane + 32 * i < n ? __ldcg(pl + (long)(lane + 32 * i) * p.row_tile) : -INFINITY;
+                m = fmaxf(m, x[i]);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-            for (int i = lane; i < n; i += 32) {
-                const float x = sw[j][i], e = x == -INFINITY ? 0.f : expf(x - m);
-                sw[j][i] = e;
-                s += e;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                x[i] = x[i] == -INFINITY ? 0.f : expf(x[i] - m);
+                s += x[i];
             }
             s = warp_sum(s);
             const float inv = s == 0.f ? 0.f : 1.f / s;
-            for (int i = lane; i < n; i += 32) sw[j][i] *= inv;
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (lane + 32 * i < n) {
+                    const float2 sc2 = __ldcg(ps + (long)(lane + 32 * i) * p.row_tile);
+                    sw[0][j][lane + 32 * i] = x[i] * inv * sc2.x;
+                    sw[1][j][lane + 32 * i] = x[i] * inv * sc2.y;
+                }
             if (lane == 0) sl[j] = s == 0.f ? -INFINITY : m + logf(s);
         }
         if (lane == 0) {
-            sc[j][0] = c0;
+            sc[j][0] = s0;
             sc[j][1] = n;
         }
     }
@@ -268,21 +271,20 @@ __global__ void __launch_bounds__(JNT, 2) paged_join_tc_kernel(const __grid_cons
     const long pitch = (long)p.row_tile * (DK / 4);
 #pragma unroll 1
     for (int j0 = half; j0 < (nb <= 8 ? 8 : 16); j0 += 8) {
-        const float4 *src[4];
+        const uint2 *src[4];
         float4 o[4];
         int n[4], most = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int j = j0 + 2 * i;
-            const long s0 = sc[j][0] + (long)(b0 + j) * p.row_tiles + rt;
-            src[i] = (const float4 *)(p.po + (s0 * p.row_tile + r) * DK) + d4;
+            src[i] = (const uint2 *)(p.po + ((long)sc[j][0] * p.row_tile + r) * DK) + d4;
             n[i] = sc[j][1];
             most = max(most, n[i]);
             o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll 1
         for (int c0 = 0; c0 < most; c0 += 4) {
-            float4 v[4][4];
+            uint2 v[4][4];
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -293,11 +295,12 @@ __global__ void __launch_bounds__(JNT, 2) paged_join_tc_kernel(const __grid_cons
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (c0 + c < n[i]) {
-                        const float x = sw[j0 + 2 * i][c0 + c];
-                        o[i].x = fmaf(x, v[i][c].x, o[i].x);
-                        o[i].y = fmaf(x, v[i][c].y, o[i].y);
-                        o[i].z = fmaf(x, v[i][c].z, o[i].z);
-                        o[i].w = fmaf(x, v[i][c].w, o[i].w);
+                        const float x = sw[d4 >> 6][j0 + 2 * i][c0 + c];
+                        const float2 f0 = __half22float2(*(const __half2 *)&v[i][c].x), f1 = __half22float2(*(const __half2 *)&v[i][c].y);
+                        o[i].x = fmaf(x, f0.x, o[i].x);
+                        o[i].y = fmaf(x, f0.y, o[i].y);
+                        o[i].z = fmaf(x, f1.x, o[i].z);
+                        o[i].w = fmaf(x, f1.y, o[i].w);
                     }
         }
 #pragma unroll
@@ -362,11 +365,15 @@ __global__ void __launch_bounds__(JNT, 2) paged_join_tc_kernel(const __grid_cons
 }
 
 // --------------------------------------------------------------------- attention ----
-constexpr int ROWS = 128, NK = 64, NTHREADS = 576;
+constexpr int ROWS = 128, NK = 64, NTHREADS = 608;
 constexpr int NGRP = NK / 8;            // row groups of a tile
 constexpr int KST = 2, KGRP = 3;        // rank 0: tile stages, block groups of a stage
-constexpr int VSL = 5;                  // rank 1: slots of half a tile (256 latent dims)
+constexpr int VSL = 4;                  // rank 1: slots of half a tile (256 latent dims)
 constexpr int NPB = 2;                  // P slots of rank 1 = staging slots of rank 0
+#ifndef PFD
+#define PFD 4
+#endif
+constexpr int PF = PFD;                 // tiles prefetched into L2 ahead of rank 1's loads
 constexpr uint32_t ATOM = 1024;
 // rank 0 stage: groups of 64-dim blocks {0-2}, {3-5}, {6-7}, each [row group][block][8 rows], then the
 // key band [row group][8 rows]
@@ -377,13 +384,13 @@ constexpr uint32_t VHALF = NGRP * 4 * ATOM;   // [row group][block][8 rows]
 constexpr uint32_t P_BYTES = 16384;
 constexpr uint32_t X_ALPHA = 0, X_INVL = 512, X_LSE = 1024, X_FLAG = 1536, X_BYTES = X_FLAG + 16;
 constexpr uint32_t XOFF = P_BYTES, XSLOT = 18432, EXT_STRIDE = 1664;
-// rank 0: key stages, two query boxes, P staging, extras, row maxima [tile parity][half][row], row sums
-constexpr uint32_t OFF_Q = KST * KSTAGE, OFF_STG = OFF_Q + 2 * 16384, OFF_EXT = OFF_STG + NPB * P_BYTES;
+// rank 0: key stages (between parts: query boxes 0-8), query box 9, P staging, extras, row maxima [tile parity][half][row], row sums
+constexpr uint32_t OFF_Q = KST * KSTAGE, OFF_STG = OFF_Q + 16384, OFF_EXT = OFF_STG + NPB * P_BYTES;
 constexpr uint32_t OFF_RED = OFF_EXT + NPB * EXT_STRIDE, OFF_SUM = OFF_RED + 2 * 2 * ROWS * 4;
 // rank 1: latent slots, P slots, 1/l of each row for the epilogue's other warps [part parity][row], the
-// epilogue's transposes (2 KB a warp)
+// epilogue's transposes (4 KB a warp)
 constexpr uint32_t OFF_PB = VSL * VHALF, OFF_INV = OFF_PB + NPB * XSLOT, OFF_OUT = OFF_INV + 2 * ROWS * 4;
-constexpr uint32_t END0 = OFF_SUM + 2 * ROWS * 4, END1 = OFF_OUT + 8 * 2048;
+constexpr uint32_t END0 = OFF_SUM + 2 * ROWS * 4, END1 = OFF_OUT + 8 * 4096;
 constexpr uint32_t OFF_BAR = END0 > END1 ? END0 : END1;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 512;
 constexpr uint32_t T_S = 0, T_Q = 2 * NK;   // rank 0's TMEM columns: S buffers; 32 per 64 query dims (10 blocks)
@@ -392,6 +399,7 @@ static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 static_assert(KSTAGE % 1024 == 0 && OFF_STG % 1024 == 0 && OFF_PB % 1024 == 0 && XSLOT % 1024 == 0, "swizzle atoms");
 static_assert(XOFF + X_BYTES <= XSLOT && X_BYTES <= EXT_STRIDE && OFF_EXT % 16 == 0, "P transfer layout");
 static_assert(T_Q + 320 <= 512, "TMEM budget of rank 0");
+static_assert(5 * 16384 >= KSTAGE && 9 * 16384 <= KST * KSTAGE, "query boxes in the key stages");
 // Barriers, by index; the same places in both CTAs.
 enum : int {
     B_GFULL = 0,                 // rank 0 [stage][group]: boxes landed / read by the MMAs
@@ -400,9 +408,9 @@ enum : int {
     B_SFREE = B_SFULL + 2,
     B_STAGED = B_SFREE + 2,      // rank 0 [slot]: P staged / its copy has read it
     B_STGFREE = B_STAGED + 2,
-    B_QFULL = B_STGFREE + 2,     // rank 0 [slot]: query box landed / moved to TMEM
-    B_QEMPTY = B_QFULL + 2,
-    B_QREADY = B_QEMPTY + 2,     // rank 0: the part's queries in TMEM / no longer read by MMAs
+    B_QFULL = B_STGFREE + 2,     // rank 0: the part's query boxes landed
+    B_KFREE = B_QFULL + 1,       // rank 0 [stage]: the boxes there are in TMEM
+    B_QREADY = B_KFREE + 2,      // rank 0: the part's queries in TMEM / no longer read by MMAs
     B_QFREE = B_QREADY + 1,
     B_PEMPTY = B_QFREE + 1,      // both [slot]: P consumed (one multicast commit completes it in both)
     B_PFULL = B_PEMPTY + 2,      // rank 1 [slot]: P and extras landed / O rescaled for it
@@ -415,7 +423,7 @@ enum : int {
 };
 __device__ __forceinline__ uint32_t arrivals(int i) {
     if (i >= B_SFREE && i < B_STGFREE) return 8;   // one per softmax warp
-    if ((i >= B_QEMPTY && i <= B_QREADY) || (i >= B_PCREADY && i < B_VFULL)) return 4;
+    if ((i >= B_KFREE && i <= B_QREADY) || (i >= B_PCREADY && i < B_VFULL)) return 4;
     if (i == B_QFREE) return 2;
     return i == B_EPIDONE ? 8 : 1;
 }
@@ -474,14 +482,6 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-        "[%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
 
 // Bounded waits.  A kernel of this file lasts milliseconds (every byte that the GPU holds, read once);
 // KERNEL_NS after its start a wait records the timeout and gives up, as does every other wait of the
@@ -526,7 +526,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     uint64_t *bars = (uint64_t *)(smem + OFF_BAR);
     Ctl *ctl = (Ctl *)(bars + B_COUNT);
     uint32_t *tslot = (uint32_t *)(ctl + 1);
-    static_assert(B_COUNT * 8 + sizeof(Ctl) + 4 <= 512, "barrier area");
+    volatile int *prog = (volatile int *)(tslot + 1);   // rank 1: tiles whose latent loads have begun
+    static_assert(B_COUNT * 8 + sizeof(Ctl) + 8 <= 512, "barrier area");
     const PagedDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
@@ -535,6 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         for (int i = lane; i < B_COUNT; i += 32) mbar_init(&bars[i], arrivals(i));
         if (lane == 0) {
             ctl->abort = 0;
+            *prog = 0;
             ctl->deadline = global_ns() + KERNEL_NS;
         }
         fence_mbar_init();
@@ -582,9 +584,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             // a lane per unit of the tile's rows; the whole warp waits.  A group's refill costs the time
             // from its last MMA to the issue of its boxes, hence a warp for each.
             const int g = warp == 0 ? 0 : warp - 11;
-            int n = 0;
+            int n = 0, seg = 0;
             bool go = true;
-            for (; more && go; next()) {
+            for (; more && go; next(), ++seg) {
                 Rows<UNIT> rows{-1, -1, -64};
 #pragma unroll 1
                 for (int i = 0; i < w.nt; ++i, ++n) {
@@ -592,7 +594,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     uint8_t *dst = smem + s * KSTAGE + g * KG1 + lane * NRG * (g < 2 ? 3 : 2) * ATOM;
                     uint64_t *full = &bars[B_GFULL + s * KGRP + g];
                     const int row = rows.tile(a, w, i, lane), rg = row >= 0 ? row >> 3 : none;
-                    go = wait_all(&bars[B_GEMPTY + s * KGRP + g], ((n >> 1) & 1) ^ 1, ctl);   // a fresh barrier passes
+                    // a part's first tiles go where its queries were, the others behind the MMAs of two tiles ago
+                    go = wait_all(i < KST ? &bars[B_KFREE + s] : &bars[B_GEMPTY + s * KGRP + g],
+                                  i < KST ? seg & 1 : ((n >> 1) & 1) ^ 1, ctl);
                     if (!go) break;
                     if (lane == 0) mbar_arrive_expect_tx(full, NGRP * 3 * ATOM);
                     if (lane < UNITS) {
@@ -771,52 +775,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 }
                 bulk_wait_all();   // nothing in flight into the peer at exit
             }
+        } else if (warp == 18) {
+            // ------------------------------- the parts' query boxes: 64 dims x 128 heads each, hi of the latent
+            // (0-7), hi and lo of the band (8, 9), all in flight at once in the key stages, which the
+            // last part's MMAs have left
+            int seg = 0;
+            bool go = lane == 0;
+            for (; more && go; next(), ++seg) {
+                go = wait_for(&bars[B_QFREE], (seg & 1) ^ 1, ctl);   // (passes at first)
+                if (!go) break;
+                mbar_arrive_expect_tx(&bars[B_QFULL], 10 * 128 * a.q_rows);
+#pragma unroll 1
+                for (int j = 0; j < 10; ++j)
+                    tma_load_3d(smem + (j < 9 ? j * 16384 : OFF_Q), j < 8 ? &m.qh : (j == 8 ? &m.rh : &m.rl), &bars[B_QFULL],
+                                j < 8 ? 64 * j : 0, w.rt * ROWS, w.b);
+            }
         } else {
             // ------------------------------- queries into TMEM (warps 14-17, a thread per head)
-            // boxes of 64 dims x 128 heads through two slots: hi of the latent (boxes 0-7), hi and lo
-            // of the band (8, 9); the next part's first two land before the last part's MMAs are done
             const int quad = warp & 3, row = quad * 32 + lane;
             const uint32_t dst = tmem + ((uint32_t)(quad * 32) << 16) + T_Q;
-            int seg = 0, at = 0;   // `at`: boxes so far
+            int seg = 0;
             bool ok = true;
             for (; more && ok; next(), ++seg) {
                 const bool act = w.rt * ROWS + quad * 32 < p.H;
+                ok = wait_all(&bars[B_QFULL], seg & 1, ctl);
+                tc_fence_after();   // (the boxes landed behind the commit of the last part's MMAs)
 #pragma unroll 1
-                for (int j = -2; j < 10 && ok; ++j) {   // box j out of its slot, box j + 2 into it
-                    if (j == 0 && seg > 0) {
-                        ok = wait_all(&bars[B_QFREE], (seg - 1) & 1, ctl);
-                        tc_fence_after();
-                    }
-                    if (j >= 0) {
-                        const int k = (at + j) & 1;
-                        ok = __all_sync(FULL, ok && wait_for(&bars[B_QFULL + k], ((at + j) >> 1) & 1, ctl));
-                        if (ok && act) {
-                            const uint8_t *box = smem + OFF_Q + k * 16384 + row * 128;
-                            uint32_t v[32];
+                for (int j = 0; j < 10 && ok; ++j) {
+                    const uint8_t *box = smem + (j < 9 ? j * 16384 : OFF_Q) + row * 128;
+                    uint32_t v[32];
+                    if (act) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const uint4 x = *(const uint4 *)(box + ((e ^ (row & 7)) << 4));
-                                v[4 * e] = x.x;
-                                v[4 * e + 1] = x.y;
-                                v[4 * e + 2] = x.z;
-                                v[4 * e + 3] = x.w;
-                            }
-                            tmem_st32(dst + j * 32, v);
+                        for (int e = 0; e < 8; ++e) {
+                            const uint4 x = *(const uint4 *)(box + ((e ^ (row & 7)) << 4));
+                            v[4 * e] = x.x;
+                            v[4 * e + 1] = x.y;
+                            v[4 * e + 2] = x.z;
+                            v[4 * e + 3] = x.w;
                         }
+                        tmem_st32(dst + j * 32, v);
+                    }
+                    if (j == 4 || j == 8) {   // boxes 0-4 cover the first stage
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars[B_QEMPTY + k]);
+                        if (lane == 0) mbar_arrive(&bars[B_KFREE + (j == 8)]);
                     }
-                    if (warp == 14 && lane == 0 && j + 2 < 10) {
-                        const int f = at + j + 2, k = f & 1;
-                        if (wait_for(&bars[B_QEMPTY + k], ((f >> 1) & 1) ^ 1, ctl)) {
-                            mbar_arrive_expect_tx(&bars[B_QFULL + k], 128 * a.q_rows);
-                            tma_load_3d(smem + OFF_Q + k * 16384, j < 6 ? &m.qh : (j == 6 ? &m.rh : &m.rl), &bars[B_QFULL + k],
-                                        j < 6 ? 64 * (j + 2) : 0, w.rt * ROWS, w.b);
-                        }
-                    }
-                    __syncwarp();
                 }
-                at += 10;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -826,7 +829,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     } else {
         if (warp == 0) {
             // ------------------------------------------------ TMA producer (latent rows)
-            int slot = 0;
+            int n = 0, slot = 0;
             uint32_t ph = 1;   // a fresh barrier's previous phase counts as complete
             bool go = true;
             for (; more && go; next()) {
@@ -834,6 +837,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
                 for (int i = 0; i < w.nt && go; ++i) {
                     const int row = rows.tile(a, w, i, lane), end = w.keys - (w.k0 + i) * NK;
+                    *prog = ++n;   // paces the prefetching warp
                     // a request's last tile goes by row groups, with zeros behind the last one with keys
                     const bool whole = end >= NK;
                     const int first = __shfl_sync(FULL, row, lane / NRG);
@@ -854,6 +858,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                             ph ^= 1;
                         }
                     }
+                }
+            }
+        } else if (warp == 10) {
+            // ------------------------------- L2 prefetch of the tiles that rank 0 loads next
+            // two tiles of key stages per cluster in flight do not cover DRAM's latency: tile n is
+            // asked for when rank 1, which trails, loads tile n - PF
+            int n = 0;
+            bool go = true;
+            for (; more && go; next()) {
+                Rows<UNIT> rows{-1, -1, -64};
+#pragma unroll 1
+                for (int i = 0; i < w.nt && go; ++i, ++n) {
+                    const int row = rows.tile(a, w, i, lane);
+                    for (uint32_t k = 1; *prog < n - PF && go; ++k) {
+                        __nanosleep(128);
+                        if ((k & 1023) == 0 && gave_up(ctl)) go = false;
+                    }
+                    go = __all_sync(FULL, go);
+                    if (row >= 0 && lane < UNITS) {
+                        l2_prefetch((const bf16 *)p.c_cache + (long)row * DK, UNIT * DK * 2);
+                        l2_prefetch((const bf16 *)p.kpe_cache + (long)row * DR, UNIT * DR * 2);
+                    }
+                    __syncwarp();
                 }
             }
         } else if (warp == 1) {
@@ -957,37 +984,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     invs[(seg & 1) * ROWS] = inv_l;
                     if (ok && w.rt * ROWS + row < p.H) p.pl[slot * p.row_tile + row] = lse2 * 0.69314718055994531f;
                 }
-                // ---- epilogue: the part's normalised output, 256 latent dims per warp: 16 columns of 32
-                // heads at a time, turned in shared memory so that a store writes whole 64-byte pieces
+                // ---- epilogue: the part's normalised output, 256 latent dims per warp: 64 columns of 32
+                // heads at a time, turned in shared memory so that a store writes whole 128-byte lines.
+                // An SM stores about 27 bytes a cycle, so 128 heads in fp32 took 4.8 us; fp16 with a
+                // power of two per half row (|x| <= 2^15, half a step 2^-12 of the value) halves that,
+                // at an error an eighth of the bf16 result's own.
                 named_bar_sync(1 + quad, 64);   // the two warps of these 32 heads
                 const float inv_l = invs[(seg & 1) * ROWS];
                 ok = __all_sync(FULL, ok && wait_for(&bars[B_OFINAL], seg & 1, ctl));
                 tc_fence_after();
                 if (ok && act) {
-                    uint8_t *buf = smem + OFF_OUT + (warp - 2) * 2048;
                     const int live = min(32, p.H - (w.rt * ROWS + quad * 32));
-                    float *po = p.po + (slot * p.row_tile + quad * 32 + (lane >> 2)) * DK + 256 * g + (lane & 3) * 4;
+                    // the row's largest value here sets its power of two
+                    float big = 0.f;
 #pragma unroll 1
-                    for (int cc = 0; cc < 16; ++cc, po += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(lb + 256 * g + cc * 16, o);
+                    for (int cc = 0; cc < 8; ++cc) {
+                        uint32_t o[32];
+                        tmem_ld32(lb + 256 * g + 32 * cc, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)   // 16-byte piece e of row `lane` at piece e ^ (row / 2 mod 4)
-                            *(float4 *)(buf + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
-                                make_float4(__uint_as_float(o[4 * e]) * inv_l, __uint_as_float(o[4 * e + 1]) * inv_l,
-                                            __uint_as_float(o[4 * e + 2]) * inv_l, __uint_as_float(o[4 * e + 3]) * inv_l);
-                        __syncwarp();
-                        float4 v[4];
+                        for (int e = 0; e < 32; ++e) big = fmaxf(big, fabsf(__uint_as_float(o[e])));
+                    }
+                    const int ex = (int)(__float_as_uint(big * inv_l) >> 23);   // 0 for a row of zeros, 255 for infinity
+                    const float up = ex == 0 || ex == 255 ? 1.f : __uint_as_float((uint32_t)min(268 - ex, 254) << 23);
+                    if (lane < live) p.pscale[(slot * p.row_tile + quad * 32 + lane) * 2 + g] = 1.f / up;
+                    const float f = inv_l * up;
+                    uint8_t *buf = smem + OFF_OUT + (warp - 2) * 4096;
+                    const int r = lane >> 3;
+                    __half *po = p.po + (slot * p.row_tile + quad * 32 + r) * DK + 256 * g + (lane & 7) * 8;
+#pragma unroll 1
+                    for (int cc = 0; cc < 4; ++cc, po += 64) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int r = 8 * e + (lane >> 2);
-                            v[e] = *(const float4 *)(buf + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t o[32];
+                            tmem_ld32(lb + 256 * g + 64 * cc + 32 * k, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {   // 16-byte piece 4 k + e of row `lane` at piece .. ^ (row mod 8)
+                                uint32_t h[4];
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    h[q] = pack_f16(__uint_as_float(o[8 * e + 2 * q]) * f, __uint_as_float(o[8 * e + 2 * q + 1]) * f);
+                                *(uint4 *)(buf + lane * 128 + (((4 * k + e) ^ (lane & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                            }
                         }
                         __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (8 * e + (lane >> 2) < live) *(float4 *)(po + 8 * e * DK) = v[e];
+                        for (int e = 0; e < 8; ++e) {   // rows 4 e + r
+                            const uint4 v = *(const uint4 *)(buf + (4 * e + r) * 128 + (((lane & 7) ^ ((4 * e + r) & 7)) << 4));
+                            if (4 * e + r < live) *(uint4 *)(po + 4 * e * DK) = v;
+                        }
+                        __syncwarp();
                     }
                 }
                 tc_fence_before();
@@ -1035,8 +1082,8 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     ab.qlo = ab.qhi + heads * DK;
     ab.rhi = (bf16 *)p.qpe;
     ab.rlo = ab.rhi + heads * DR;
-    // at least two blocks per SM, where the batch has that many groups of eight
-    const int want = (2 * 152 + 4 * p.H - 1) / (4 * p.H), most = (p.B + 7) / 8;
+    // about five blocks per SM (what their shared memory allows), where the batch has that many groups of eight
+    const int want = (5 * 152 + 4 * p.H - 1) / (4 * p.H), most = (p.B + 7) / 8;
     ab.groups = std::max(1, std::min(want, most));
     ab.group = ((p.B + ab.groups - 1) / ab.groups + 7) / 8 * 8;
     ab.groups = (p.B + ab.group - 1) / ab.group;
