@@ -61,53 +61,26 @@ __device__ __forceinline__ int keys_of(const PagedDecode &p, int b) {
     return min(max(p.lens[b], 0), cap);
 }
 
-// The request whose tiles (for all its row tiles) hold tile t < T.
-__device__ __forceinline__ int request_of(const PagedDecode &p, long t) {
+// The request whose tiles (for all its row tiles) hold tile t < T; `off`: the prefix sums.
+template <typename I>
+__device__ __forceinline__ int request_of(const PagedDecode &p, const I *off, long t) {
     int lo = 0, hi = p.B - 1;
     while (lo < hi) {   // the last b whose first tile is <= t: empty requests before it share that tile
         const int mid = (lo + hi + 1) >> 1;
-        if (p.tile_off[mid] * p.row_tiles <= t) lo = mid;
+        if ((long)off[mid] * p.row_tiles <= t) lo = mid;
         else hi = mid - 1;
     }
     return lo;
 }
 
-// The tile prefix sums of all requests and the workers' parts, by one block of NT threads.
-template <int NT>
-__device__ void plan_block(const PagedDecode &p) {
-    __shared__ long warp_tot[NT / 32];
-    const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
-    long carry = 0;
-    for (int b0 = 0; b0 < p.B; b0 += NT) {
-        const int b = b0 + tid;
-        const long n = b < p.B ? (keys_of(p, b) + p.tile - 1) / p.tile : 0;
-        long x = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) warp_tot[wp] = x;
-        __syncthreads();
-        long before = carry, all = carry;
-#pragma unroll
-        for (int i = 0; i < NT / 32; ++i) {
-            if (i < wp) before += warp_tot[i];
-            all += warp_tot[i];
-        }
-        if (b < p.B) p.tile_off[b] = before + x - n;
-        carry = all;
-        __syncthreads();
-    }
-    if (tid == 0) p.tile_off[p.B] = carry;
-    if (!p.parts) return;
-    __syncthreads();
-    // The parts begin where a worker's share begins and where an item does (one may be both): a thread
-    // per beginning finds its part's worker, item and end.
-    const long total = carry * p.row_tiles;
+// The parts begin where a worker's share begins and where an item does (one may be both): a thread per
+// beginning finds its part's worker, item and end.
+template <int NT, typename I>
+__device__ void plan_parts(const PagedDecode &p, const I *off, long total) {
     const int W = total ? active_workers(p, total) : 0;
     const long items = (long)p.B * p.row_tiles;
-    for (long k = tid; k < p.workers + items; k += NT) {
+#pragma unroll 1
+    for (long k = threadIdx.x; k < p.workers + items; k += NT) {
         const bool worker = k < p.workers;
         long t0 = 0;
         int b = 0, c = (int)k, rt = 0;
@@ -117,12 +90,12 @@ __device__ void plan_block(const PagedDecode &p) {
                 continue;
             }
             t0 = c * total / W;
-            b = request_of(p, t0);
+            b = request_of(p, off, t0);
         } else {
             b = (int)((k - p.workers) / p.row_tiles);
             rt = (int)((k - p.workers) % p.row_tiles);
         }
-        const long o = p.tile_off[b], per = p.tile_off[b + 1] - o;
+        const long o = off[b], per = off[b + 1] - o;
         if (per == 0) {
             p.spans[k - p.workers] = make_int2(0, 0);
             continue;
@@ -145,7 +118,7 @@ __device__ void plan_block(const PagedDecode &p) {
         if (t1 < end) {   // the worker goes on with the next item that has tiles
             x.next = 1;
             if (rt == p.row_tiles - 1)
-                for (int e = b + 1; p.tile_off[e + 1] == p.tile_off[e]; ++e) x.next += p.row_tiles;
+                for (int e = b + 1; off[e + 1] == off[e]; ++e) x.next += p.row_tiles;
         }
         p.parts[c + item] = x;
         if (worker) {
@@ -153,6 +126,49 @@ __device__ void plan_block(const PagedDecode &p) {
             p.first[p.workers + c] = (int)(end - t0);
         }
     }
+}
+
+// The tile prefix sums of all requests and the workers' parts, by one block of NT threads; `room`
+// ints of shared memory keep the sums at hand where they fit.
+template <int NT>
+__device__ void plan_block(const PagedDecode &p, int *sm = nullptr, int room = 0) {
+    __shared__ long warp_tot[NT / 32];
+    const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
+    const bool near = p.B < room && (long)p.B * ((p.max_pages * (long)p.page + p.tile - 1) / p.tile) < 1l << 31;
+    long carry = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B; b0 += NT) {
+        const int b = b0 + tid;
+        const long n = b < p.B ? (keys_of(p, b) + p.tile - 1) / p.tile : 0;
+        long x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) warp_tot[wp] = x;
+        __syncthreads();
+        long before = carry, all = carry;
+#pragma unroll
+        for (int i = 0; i < NT / 32; ++i) {
+            if (i < wp) before += warp_tot[i];
+            all += warp_tot[i];
+        }
+        if (b < p.B) {
+            if (near) sm[b] = (int)(before + x - n);
+            else p.tile_off[b] = before + x - n;
+        }
+        carry = all;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        if (near) sm[p.B] = (int)carry;
+        else p.tile_off[p.B] = carry;
+    }
+    if (!p.parts) return;
+    __syncthreads();
+    if (near) plan_parts<NT>(p, sm, carry * p.row_tiles);
+    else plan_parts<NT>(p, p.tile_off, carry * p.row_tiles);
 }
 
 }  // namespace paged

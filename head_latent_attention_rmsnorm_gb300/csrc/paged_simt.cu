@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
     const long tend = (long)(blockIdx.x + 1) * total / W;
     const int chunks = (Dq + 3) / 4;
     while (t < tend) {
-        const int b = request_of(p, t);
+        const int b = request_of(p, p.tile_off, t);
         const long first = p.tile_off[b], per = p.tile_off[b + 1] - first;
         const int rt = (int)((t - first * p.row_tiles) / per);
         const long k0 = (t - first * p.row_tiles) % per;        // first tile of the item here

@@ -67,6 +67,11 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
 }
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
 __device__ __forceinline__ void cp16(void *dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -80,10 +85,11 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
 // q[b, h, :] = W_K(h)^T q_nope[b, h, :]: streams 16 KB x heads x 8 of weights for B x 128 x 512
 // multiply-adds a head, so it is bound by the weights' bytes until B is in the hundreds; the
 // products run on mma.sync (M = latent dims, N = requests: eight per step, no padding to 128
-// rows).  Block (head, 128 latent dims, group of requests): the weight block by cp.async, then in
-// registers as A fragments, eight requests at a time against it.  The order of the 128 summed
-// dims is permuted the same way in A and B so that a lane's share of q is 64 contiguous bytes.
-constexpr int AB_DIMS = 128, AB_PITCH = AB_DIMS * 2 + 16;
+// rows).  Block (head, 128 latent dims, group of up to 64 requests): the weight block and the group's
+// queries by cp.async, all in flight at once; the weights then stay in registers as A fragments.
+constexpr int AB_DIMS = 128, AB_PITCH = 256 + 16, AB_GROUP = 64;
+constexpr int AB_OUT = 40;              // halves per request of a warp's staging (32 dims + pad)
+constexpr int AB_SMEM = DN * AB_PITCH + AB_GROUP * AB_PITCH + 4 * 2 * 8 * AB_OUT * 2;
 
 struct Absorb {
     PagedDecode p;
@@ -93,97 +99,87 @@ struct Absorb {
     Turns turns;
 };
 
+// The queries' rotation: a warp per request and 32 heads, a lane per pair of dims, the angle formed once.
+__device__ void rotate_queries(const Absorb &a, int i, int lane) {
+    const PagedDecode &p = a.p;
+    const int per = (p.H + 31) / 32, b = i / per, h0 = i % per * 32;
+    if (b >= p.B) return;
+    const float2 cs = turn_cs(a.turns.v[lane], keys_of(p, b) - 1);
+    const int h1 = min(h0 + 32, p.H);
+#pragma unroll 1
+    for (int h = h0; h < h1; h += 8) {
+        uint16_t x0[8], x1[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint16_t *x = (const uint16_t *)p.q_pe + ((long)b * p.H + min(h + j, h1 - 1)) * DR + lane;
+            x0[j] = x[0];
+            x1[j] = x[32];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (h + j >= h1) break;
+            const long o = ((long)b * p.H + h + j) * DR + lane;
+            const float f0 = __uint_as_float((uint32_t)x0[j] << 16), f1 = __uint_as_float((uint32_t)x1[j] << 16);
+            uint32_t hi, lo;
+            split2(f0 * cs.x - f1 * cs.y, f1 * cs.x + f0 * cs.y, hi, lo);
+            ((uint16_t *)a.rhi)[o] = (uint16_t)hi;
+            ((uint16_t *)a.rhi)[o + 32] = (uint16_t)(hi >> 16);
+            ((uint16_t *)a.rlo)[o] = (uint16_t)lo;
+            ((uint16_t *)a.rlo)[o + 32] = (uint16_t)(lo >> 16);
+        }
+    }
+}
+
 __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_constant__ Absorb a) {
-    __shared__ __align__(16) uint8_t sw[DN * AB_PITCH];
-    __shared__ __align__(16) uint32_t st[4][2][8][20];   // per warp: hi / lo, 8 requests x 32 dims (+ pad)
+    extern __shared__ __align__(16) uint8_t sm[];
     const PagedDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
     if (blockIdx.x == 0) {
-        plan_block<128>(p);
+        plan_block<128>(p, (int *)sm, AB_SMEM / 4);
         return;
     }
     if ((int)blockIdx.x <= a.rot_blocks) {
-        // the queries' rotation: a warp per request and 32 heads, a lane per pair of dims, the angle
-        // formed once
-        const int i = ((int)blockIdx.x - 1) * 4 + warp, per = (p.H + 31) / 32, b = i / per, h0 = i % per * 32;
-        if (b >= p.B) return;
-        const float2 cs = turn_cs(a.turns.v[lane], keys_of(p, b) - 1);
-        const int h1 = min(h0 + 32, p.H);
-        for (int h = h0; h < h1; h += 8) {
-            uint16_t x0[8], x1[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint16_t *x = (const uint16_t *)p.q_pe + ((long)b * p.H + min(h + j, h1 - 1)) * DR + lane;
-                x0[j] = x[0];
-                x1[j] = x[32];
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (h + j >= h1) break;
-                const long o = ((long)b * p.H + h + j) * DR + lane;
-                const float f0 = __uint_as_float((uint32_t)x0[j] << 16), f1 = __uint_as_float((uint32_t)x1[j] << 16);
-                uint32_t hi, lo;
-                split2(f0 * cs.x - f1 * cs.y, f1 * cs.x + f0 * cs.y, hi, lo);
-                ((uint16_t *)a.rhi)[o] = (uint16_t)hi;
-                ((uint16_t *)a.rhi)[o + 32] = (uint16_t)(hi >> 16);
-                ((uint16_t *)a.rlo)[o] = (uint16_t)lo;
-                ((uint16_t *)a.rlo)[o + 32] = (uint16_t)(lo >> 16);
-            }
-        }
+        rotate_queries(a, ((int)blockIdx.x - 1) * 4 + warp, lane);
         return;
     }
+    uint8_t *sw = sm, *sq = sm + DN * AB_PITCH;
     int u = (int)blockIdx.x - 1 - a.rot_blocks;
     const int dc = u & 3;
     u >>= 2;
     const int grp = u % a.groups, h = u / a.groups;
-    const int b0 = grp * a.group, b1 = min(b0 + a.group, p.B);
+    const int b0 = grp * a.group, nb = min(a.group, p.B - b0);
     const bf16 *w = (const bf16 *)p.w + (long)h * (DN + DV) * DK + dc * AB_DIMS;
-    for (int i = tid; i < DN * (AB_DIMS / 8); i += 128) {
-        const int n = i >> 4, c = i & 15;
-        cp16(sw + n * AB_PITCH + c * 16, w + (long)n * DK + c * 8);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    const int g = lane >> 2, t = lane & 3;
-    uint4 qn[4];
-    auto fetch = [&](int b) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) qn[i] = make_uint4(0, 0, 0, 0);
-        if (b + g < b1) {
-            const uint4 *src = (const uint4 *)((const bf16 *)p.q_nope + ((long)(b + g) * p.H + h) * DN + t * 32);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) qn[i] = __ldg(src + i);
-        }
-    };
-    fetch(b0);
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    for (int i = tid; i < nb * 16; i += 128)
+        cp16(sq + (i >> 4) * AB_PITCH + (i & 15) * 16, (const bf16 *)p.q_nope + ((long)(b0 + (i >> 4)) * p.H + h) * DN + (i & 15) * 8);
+#pragma unroll 4
+    for (int i = tid; i < DN * (AB_DIMS / 8); i += 128)
+        cp16(sw + (i >> 4) * AB_PITCH + (i & 15) * 16, w + (long)(i >> 4) * DK + (i & 15) * 8);
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
     __syncthreads();
-    // step s of the sum: k = 2t, 2t + 1 is dim 32 t + 4 s + {0, 1}, k = 2t + 8, + 9 the next two
     uint32_t A[2][8][4];
-    {
-        const int mi = lane >> 3, r = lane & 7;   // matrix of the x4 load, its row k
-        const int krow = (r >> 1) * 32 + (r & 1) + ((mi >> 1) ? 2 : 0);
+    const int mi = lane >> 3, r = lane & 7;   // matrix of an x4 load, its row
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int s = 0; s < 8; ++s)   // matrices: (dims 0-7, k 0-7), (dims 8-15, k 0-7), (.., k 8-15) x 2
-                ldsm4_t(A[m][s], smem_u32(sw + (krow + 4 * s) * AB_PITCH + (warp * 32 + m * 16 + (mi & 1) * 8) * 2));
-    }
-    for (int b = b0; b < b1; b += 8) {
-        uint4 q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = qn[i];
-        fetch(b + 8);   // the next eight requests
+        for (int s = 0; s < 8; ++s)   // matrices: (dims 0-7, k 0-7), (dims 8-15, k 0-7), the same of k 8-15
+            ldsm4_t(A[m][s], smem_u32(sw + (16 * s + (mi >> 1) * 8 + r) * AB_PITCH + (warp * 32 + m * 16 + (mi & 1) * 8) * 2));
+    const int g = lane >> 2, t = lane & 3;
+    uint16_t *sh = (uint16_t *)(sq + AB_GROUP * AB_PITCH) + warp * 2 * 8 * AB_OUT, *sl = sh + 8 * AB_OUT;
+#pragma unroll 1
+    for (int b = 0; b < nb; b += 8) {   // (rows behind the group's last request are not read back)
         float d[2][4] = {};
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            const uint4 v = q[s >> 1];
-            const uint32_t k0 = (s & 1) ? v.z : v.x, k1 = (s & 1) ? v.w : v.y;
-            mma_16816(d[0], A[0][s], k0, k1);
-            mma_16816(d[1], A[1][s], k0, k1);
+        for (int s = 0; s < 4; ++s) {   // 32 of the summed dims
+            uint32_t q[4];
+            ldsm4(q, smem_u32(sq + (b + r) * AB_PITCH + (32 * s + mi * 8) * 2));
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                mma_16816(d[m], A[m][2 * s], q[0], q[1]);
+                mma_16816(d[m], A[m][2 * s + 1], q[2], q[3]);
+            }
         }
         // d[m][..]: dim 16 m + g (+ 8), requests 2t, 2t + 1
-        uint16_t *sh = (uint16_t *)&st[warp][0][0][0], *sl = (uint16_t *)&st[warp][1][0][0];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -191,56 +187,91 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
                 uint32_t hi, lo;
                 split2(d[m][2 * e], d[m][2 * e + 1], hi, lo);
                 const int dim = 16 * m + 8 * e + g;
-                sh[(2 * t) * 40 + dim] = (uint16_t)hi;
-                sh[(2 * t + 1) * 40 + dim] = (uint16_t)(hi >> 16);
-                sl[(2 * t) * 40 + dim] = (uint16_t)lo;
-                sl[(2 * t + 1) * 40 + dim] = (uint16_t)(lo >> 16);
+                sh[(2 * t) * AB_OUT + dim] = (uint16_t)hi;
+                sh[(2 * t + 1) * AB_OUT + dim] = (uint16_t)(hi >> 16);
+                sl[(2 * t) * AB_OUT + dim] = (uint16_t)lo;
+                sl[(2 * t + 1) * AB_OUT + dim] = (uint16_t)(lo >> 16);
             }
         __syncwarp();
-        if (b + g < b1) {   // 8 requests x 64 bytes: a 16-byte piece per lane
-            const long o = ((long)(b + g) * p.H + h) * DK + dc * AB_DIMS + warp * 32 + t * 8;
-            *(uint4 *)(a.qhi + o) = *(const uint4 *)&st[warp][0][g][t * 4];
-            *(uint4 *)(a.qlo + o) = *(const uint4 *)&st[warp][1][g][t * 4];
+        if (b + g < nb) {   // 8 requests x 64 bytes: a 16-byte piece per lane
+            const long o = ((long)(b0 + b + g) * p.H + h) * DK + dc * AB_DIMS + warp * 32 + t * 8;
+            *(uint4 *)(a.qhi + o) = *(const uint4 *)(sh + g * AB_OUT + t * 8);
+            *(uint4 *)(a.qlo + o) = *(const uint4 *)(sl + g * AB_OUT + t * 8);
         }
         __syncwarp();
     }
 }
 
 // -------------------------------------------------------------------------- join ----
-// out[b, h, :] = W_V(h) sum_c w_c o_c: block (head, 16 requests), a warp per 16 value dims.  The
-// block merges the partials into shared memory as bf16 hi + lo, and two m16n8k16 products per step
-// take both halves.  A step's 16 summed dims are permuted alike in A and B: lane t of a row owns
-// dims 64 i + 16 t .. + 15, four dims a step, so its weights are 16-byte loads straight from W_V
-// (brought into L2 before the wait for the attention: the cache stream leaves none of it there).
-constexpr int JB = 16, JNT = 256, JPITCH = DK * 2 + 16, JMAXC = 80;
+// out[b, h, :] = W_V(h) sum_c w_c o_c: a block holds W_V(h) in shared memory and walks groups of 32
+// requests (one block per SM, so that the weights cross the L2 once per block).  Latency is what it
+// spends, so each phase has its loads in flight at once: W_V(h) lands while the rest runs (the
+// attention's last tiles brought it into L2); a warp per request forms the parts' weights; the
+// merge runs over eight groups of 128 threads (a thread per four latent dims), which share out the
+// requests, or, for up to four requests, their parts; the product (bf16 hi + lo of o against W_V,
+// m16n8k16) runs over eight warps of 16 value dims for each quarter of the 512 dims.  A step's
+// 16 summed dims are permuted alike in A and B (lane t of a row owns dims 64 i + 16 t .. + 15, four
+// dims a step), so both come by 16-byte loads.
+constexpr int JB = 32, JNT = 1024, JPITCH = DK * 2 + 16, JMAXC = 80;
+constexpr int JO = DV * JPITCH;                // W_V
+constexpr int JW = JO + 2 * JB * JPITCH;       // o as bf16 hi + lo; before it the groups' sums (7 x 4 x 512 fp32),
+                                               // after it the quarters' products [3][request][132]
+constexpr int JSMEM = JW + 2 * JB * JMAXC * 4; // the parts' weights for either half of the dims
+static_assert(2 * JB * JPITCH >= 7 * 4 * DK * 4 && 2 * JB * JPITCH >= 3 * JB * 132 * 4, "the join's exchanges");
+static_assert(PAGED_TC_WORKERS <= JMAXC && JMAXC <= 96, "parts of an item");
 
-__global__ void __launch_bounds__(JNT, 2) paged_join_tc_kernel(const __grid_constant__ PagedDecode p, const bf16 *qlo) {
-    __shared__ __align__(16) uint8_t so[2][JB * JPITCH];
-    __shared__ float sw[2][JB][JMAXC];   // the parts' weights for either half of the dims
-    __shared__ int sc[JB][2];         // first part, number of parts
-    __shared__ float sl[JB], sd[4][JB];   // log-sum-exp without the q_lo term; the warps' shares of q_lo . o
+__global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_constant__ PagedDecode p, const bf16 *qlo, int per_head) {
+    extern __shared__ __align__(16) uint8_t sm[];
+    __shared__ int sc[JB][2];            // first part, number of parts
+    __shared__ float sl[JB], sd[4][JB];  // log-sum-exp without the q_lo term; the warps' shares of q_lo . o
+    __shared__ uint64_t bar;
+    __shared__ int abort;
+    uint8_t *so = sm + JO;
+    float (*sw)[JB][JMAXC] = (float (*)[JB][JMAXC])(sm + JW);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int nb_groups = (p.B + JB - 1) / JB, h = blockIdx.x / nb_groups, b0 = (blockIdx.x % nb_groups) * JB;
-    const int nb = min(JB, p.B - b0), rt = h / p.row_tile, r = h % p.row_tile;
-    const bf16 *w = (const bf16 *)p.w + ((long)h * (DN + DV) + DN) * DK;
-    if (tid == 0 && b0 == 0) l2_prefetch(w, DV * DK * 2);
-    w += (warp * 16 + g) * DK + 16 * t;
+    const int h = blockIdx.x / per_head, rt = h / p.row_tile, r = h % p.row_tile;
+    const long pitch = (long)p.row_tile * (DK / 4);
+    bool ok = true;
+    if (tid == 0) {
+        mbar_init(&bar, 1);
+        abort = 0;
+        fence_mbar_init();
+        mbar_arrive_expect_tx(&bar, DV * DK * 2);
+    }
+    __syncthreads();
+    if (tid < DV) bulk_load(sm + tid * JPITCH, (const bf16 *)p.w + ((long)h * (DN + DV) + DN + tid) * DK, DK * 2, &bar);
     pdl_wait();
 #pragma unroll 1
-    for (int j = warp; j < JB; j += JNT / 32) {   // a warp per request
-        int s0 = 0, n = 0;
-        if (j < nb) {
-            const int2 sp = __ldcg(p.spans + (long)(b0 + j) * p.row_tiles + rt);
-            s0 = sp.x;
-            n = sp.y;
-            const float *pl = p.pl + (long)s0 * p.row_tile + r;
-            const float2 *ps = (const float2 *)p.pscale + (long)s0 * p.row_tile + r;
-            float x[3], m = -INFINITY, s = 0.f;   // up to 96 parts
+    for (int b0 = (int)(blockIdx.x % per_head) * JB; b0 < p.B; b0 += per_head * JB) {
+        const int nb = min(JB, p.B - b0);
+        const int d4 = tid & 127, q8 = tid >> 7;
+        const bool few = nb <= 4;                                // the groups share out parts, not requests
+        const int j0 = few ? 0 : q8, dj = few ? 1 : 8, c0 = few ? q8 : 0, dc = few ? 8 : 1;
+        uint2 ql[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = j0 + dj * i;
+            ql[i] = j < nb ? __ldcg((const uint2 *)(qlo + ((long)(b0 + j) * p.H + h) * DK) + d4) : make_uint2(0, 0);
+        }
+        {   // a warp per request: the weights of its parts (up to 96)
+            int s0 = 0, n = 0;
+            if (warp < nb) {
+                const int2 sp = __ldcg(p.spans + (long)(b0 + warp) * p.row_tiles + rt);
+                s0 = sp.x;
+                n = sp.y;
+            }
+            const long at = (long)s0 * p.row_tile + r;
+            float x[3], m = -INFINITY, s = 0.f;
+            float2 up[3];
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
-                x[i] = lane + 32 * i < n ? __ldcg(pl + (long)(lane + 32 * i) * p.row_tile) : -INFINITY;
-                m = fmaxf(m, x[i]);
+                const long k = at + (long)(lane + 32 * i) * p.row_tile;
+                const bool in = lane + 32 * i < n;
+                x[i] = in ? __ldcg(p.pl + k) : -INFINITY;
+                up[i] = in ? __ldcg((const float2 *)p.pscale + k) : make_float2(0.f, 0.f);
             }
+#pragma unroll
+            for (int i = 0; i < 3; ++i) m = fmaxf(m, x[i]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
 #pragma unroll
@@ -253,115 +284,126 @@ __global__ void __launch_bounds__(JNT, 2) paged_join_tc_kernel(const __grid_cons
 #pragma unroll
             for (int i = 0; i < 3; ++i)
                 if (lane + 32 * i < n) {
-                    const float2 sc2 = __ldcg(ps + (long)(lane + 32 * i) * p.row_tile);
-                    sw[0][j][lane + 32 * i] = x[i] * inv * sc2.x;
-                    sw[1][j][lane + 32 * i] = x[i] * inv * sc2.y;
+                    sw[0][warp][lane + 32 * i] = x[i] * inv * up[i].x;
+                    sw[1][warp][lane + 32 * i] = x[i] * inv * up[i].y;
                 }
-            if (lane == 0) sl[j] = s == 0.f ? -INFINITY : m + logf(s);
+            if (lane == 0) {
+                sc[warp][0] = s0;
+                sc[warp][1] = n;
+                sl[warp] = s == 0.f ? -INFINITY : m + logf(s);
+            }
         }
-        if (lane == 0) {
-            sc[j][0] = s0;
-            sc[j][1] = n;
-        }
-    }
-    __syncthreads();
-    // the merge: a thread per four latent dims of every other request, four requests and up to four
-    // parts of each in flight
-    const int d4 = tid & 127, half = tid >> 7;
-    const long pitch = (long)p.row_tile * (DK / 4);
-#pragma unroll 1
-    for (int j0 = half; j0 < (nb <= 8 ? 8 : 16); j0 += 8) {
-        const uint2 *src[4];
+        __syncthreads();
         float4 o[4];
-        int n[4], most = 0;
+        {
+            const uint2 *src[4];
+            int n[4], most = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = j0 + 2 * i;
-            src[i] = (const uint2 *)(p.po + ((long)sc[j][0] * p.row_tile + r) * DK) + d4;
-            n[i] = sc[j][1];
-            most = max(most, n[i]);
-            o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+            for (int i = 0; i < 4; ++i) {
+                const int j = j0 + dj * i;
+                src[i] = (const uint2 *)(p.po + ((long)sc[j][0] * p.row_tile + r) * DK) + d4;
+                n[i] = sc[j][1];
+                most = max(most, n[i]);
+                o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
 #pragma unroll 1
-        for (int c0 = 0; c0 < most; c0 += 4) {
-            uint2 v[4][4];
+            for (int c = c0; c < most; c += 2 * dc) {
+                uint2 v[4][2];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c0 + c < n[i]) v[i][c] = __ldcg(src[i] + (c0 + c) * pitch);
+                    for (int i = 0; i < 4; ++i)
+                        if (c + u * dc < n[i]) v[i][u] = __ldcg(src[i] + (c + u * dc) * pitch);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c0 + c < n[i]) {
-                        const float x = sw[d4 >> 6][j0 + 2 * i][c0 + c];
-                        const float2 f0 = __half22float2(*(const __half2 *)&v[i][c].x), f1 = __half22float2(*(const __half2 *)&v[i][c].y);
-                        o[i].x = fmaf(x, f0.x, o[i].x);
-                        o[i].y = fmaf(x, f0.y, o[i].y);
-                        o[i].z = fmaf(x, f1.x, o[i].z);
-                        o[i].w = fmaf(x, f1.y, o[i].w);
+                    for (int i = 0; i < 4; ++i)
+                        if (c + u * dc < n[i]) {
+                            const float x = sw[d4 >> 6][j0 + dj * i][c + u * dc];
+                            const float2 f0 = __half22float2(*(const __half2 *)&v[i][u].x), f1 = __half22float2(*(const __half2 *)&v[i][u].y);
+                            o[i].x = fmaf(x, f0.x, o[i].x);
+                            o[i].y = fmaf(x, f0.y, o[i].y);
+                            o[i].z = fmaf(x, f1.x, o[i].z);
+                            o[i].w = fmaf(x, f1.y, o[i].w);
+                        }
+            }
+        }
+        if (few) {   // the groups' sums meet in the first
+            float4 *x = (float4 *)so;
+            if (q8 > 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[((q8 - 1) * 4 + i) * 128 + d4] = o[i];
+            __syncthreads();
+            if (q8 == 0)
+#pragma unroll 1
+                for (int k = 0; k < 7; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 v = x[(k * 4 + i) * 128 + d4];
+                        o[i].x += v.x;
+                        o[i].y += v.y;
+                        o[i].z += v.z;
+                        o[i].w += v.w;
                     }
+            __syncthreads();
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int j = j0 + 2 * i;
+            const int j = few ? 4 * q8 + i : j0 + dj * i;   // (few: the other groups bring rows of zeros)
+            if (few && q8 > 0) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             uint32_t h0, l0, h1, l1;
             split2(o[i].x, o[i].y, h0, l0);
             split2(o[i].z, o[i].w, h1, l1);
-            *(uint2 *)(so[0] + j * JPITCH + d4 * 8) = make_uint2(h0, h1);
-            *(uint2 *)(so[1] + j * JPITCH + d4 * 8) = make_uint2(l0, l1);
-            if (j < nb) {   // the log-sum-exp's q_lo term: this warp's 128 dims
-                const uint2 q = __ldcg((const uint2 *)(qlo + ((long)(b0 + j) * p.H + h) * DK) + d4);
-                float dot = o[i].x * __uint_as_float(q.x << 16) + o[i].y * __uint_as_float(q.x & 0xffff0000u);
-                dot += o[i].z * __uint_as_float(q.y << 16) + o[i].w * __uint_as_float(q.y & 0xffff0000u);
-                dot = warp_sum(dot);
-                if (lane == 0) sd[warp & 3][j] = dot;
-            }
+            *(uint2 *)(so + j * JPITCH + d4 * 8) = make_uint2(h0, h1);
+            *(uint2 *)(so + (JB + j) * JPITCH + d4 * 8) = make_uint2(l0, l1);
+            // the log-sum-exp's q_lo term: this warp's 128 dims
+            float dot = o[i].x * __uint_as_float(ql[i].x << 16) + o[i].y * __uint_as_float(ql[i].x & 0xffff0000u);
+            dot += o[i].z * __uint_as_float(ql[i].y << 16) + o[i].w * __uint_as_float(ql[i].y & 0xffff0000u);
+            dot = warp_sum(dot);
+            if (lane == 0) sd[warp & 3][j] = dot;
         }
-    }
-    __syncthreads();
-    if (tid < nb)
-        p.lse[(long)(b0 + tid) * p.H + h] = sl[tid] + p.scale * ((sd[0][tid] + sd[1][tid]) + (sd[2][tid] + sd[3][tid]));
-    float d[2][4] = {};
-    uint4 An[2][2];   // [row g, g + 8][16-byte half] of the next 64 dims
+        ok = ok && mbar_wait(&bar, 0, (volatile int *)&abort, &g_paged_tc_err);   // W_V is here
+        __syncthreads();
+        if (tid < nb)
+            p.lse[(long)(b0 + tid) * p.H + h] = sl[tid] + p.scale * ((sd[0][tid] + sd[1][tid]) + (sd[2][tid] + sd[3][tid]));
+        float d[4][4] = {};
+        const int kq = warp >> 3, v0 = (warp & 7) * 16 + g;
+        const uint8_t *wa = sm + v0 * JPITCH + (128 * kq + 16 * t) * 2, *ob = so + g * JPITCH + (128 * kq + 16 * t) * 2;
+#pragma unroll 1
+        for (int i = 0; i < 4 && ok; ++i) {   // 16-byte pieces of the lane's dims: two of either 64
+            const int at = (i >> 1) * 128 + (i & 1) * 16;
+            const uint4 x = *(const uint4 *)(wa + at), y = *(const uint4 *)(wa + 8 * JPITCH + at);
+            const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) An[e & 1][e >> 1] = __ldg((const uint4 *)(w + (e & 1) * 8 * DK + (e >> 1) * 8));
-#pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
-        uint4 A[2][2];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            A[e & 1][e >> 1] = An[e & 1][e >> 1];
-            if (i < 7) An[e & 1][e >> 1] = __ldg((const uint4 *)(w + (e & 1) * 8 * DK + 64 * (i + 1) + (e >> 1) * 8));
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint32_t a0[4] = {A[0][q].x, A[1][q].x, A[0][q].y, A[1][q].y};
-            const uint32_t a1[4] = {A[0][q].z, A[1][q].z, A[0][q].w, A[1][q].w};
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                if (n && nb <= 8) break;
-                const int at = (8 * n + g) * JPITCH + (64 * i + 16 * t + 8 * q) * 2;
-                const uint4 bh = *(const uint4 *)(so[0] + at), bl = *(const uint4 *)(so[1] + at);
+            for (int n = 0; n < 4; ++n) {
+                if (8 * n >= nb) break;
+                const uint4 bh = *(const uint4 *)(ob + 8 * n * JPITCH + at), bl = *(const uint4 *)(ob + (JB + 8 * n) * JPITCH + at);
                 mma_16816(d[n], a0, bh.x, bh.y);
                 mma_16816(d[n], a0, bl.x, bl.y);
                 mma_16816(d[n], a1, bh.z, bh.w);
                 mma_16816(d[n], a1, bl.z, bl.w);
             }
         }
+        // d[n][..]: value dims v0, v0 + 8, requests 8 n + 2t, + 1; the quarters meet where o was
+        __syncthreads();
+        float *ss = (float *)so + (2 * t) * 132 + v0;   // [quarter][request][128 dims + pad]
+        if (kq > 0)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ss[((kq - 1) * JB + 8 * (e >> 2) + (e & 1)) * 132 + 8 * (e >> 1 & 1)] = d[e >> 2][e & 3];
+        __syncthreads();
+        if (kq == 0)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                float *x = ss + (8 * (e >> 2) + (e & 1)) * 132 + 8 * (e >> 1 & 1);
+                x[0] += d[e >> 2][e & 3] + (x[JB * 132] + x[2 * JB * 132]);
+            }
+        __syncthreads();
+        if (warp < nb && ok) {
+            const float4 v = *(const float4 *)((float *)so + warp * 132 + lane * 4);
+            *(uint2 *)((bf16 *)p.out + ((long)(b0 + warp) * p.H + h) * DV + lane * 4) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        }
+        __syncthreads();
     }
-    // d[n][..]: value dims g, g + 8 of the warp's 16, requests 8 n + 2t, + 1
-    __syncthreads();
-    bf16 *ss = (bf16 *)so[0];   // [request][128 dims + pad]
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            ss[(8 * n + 2 * t + (e & 1)) * 136 + warp * 16 + g + 8 * (e >> 1)] = __float2bfloat16_rn(d[n][e]);
-    __syncthreads();
-    const int j = tid >> 4, c = tid & 15;
-    if (j < nb) *(uint4 *)((bf16 *)p.out + ((long)(b0 + j) * p.H + h) * DV + c * 8) = *(const uint4 *)(ss + j * 136 + c * 8);
 }
 
 // --------------------------------------------------------------------- attention ----
@@ -883,6 +925,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     __syncwarp();
                 }
             }
+            // the share is asked for: now this cluster's share of W_V, which the join reads next, in
+            // pieces of 16 KB
+            for (int i = (blockIdx.x >> 1) + p.workers * lane; i < p.H * (DV * DK * 2 / 16384) && go; i += p.workers * 32)
+                l2_prefetch((const bf16 *)p.w + ((long)(i >> 3) * (DN + DV) + DN + (i & 7) * 16) * DK, 16384);
         } else if (warp == 1) {
             // ---------------------------------------------------- O += P C issuer
             int n = 0, seg = 0, slot = 0;
@@ -1082,9 +1128,9 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     ab.qlo = ab.qhi + heads * DK;
     ab.rhi = (bf16 *)p.qpe;
     ab.rlo = ab.rhi + heads * DR;
-    // about five blocks per SM (what their shared memory allows), where the batch has that many groups of eight
-    const int want = (5 * 152 + 4 * p.H - 1) / (4 * p.H), most = (p.B + 7) / 8;
-    ab.groups = std::max(1, std::min(want, most));
+    // at least two blocks per SM, where the batch has that many groups of eight
+    const int want = (2 * 152 + 4 * p.H - 1) / (4 * p.H), most = (p.B + 7) / 8;
+    ab.groups = std::max((p.B + AB_GROUP - 1) / AB_GROUP, std::min(want, most));
     ab.group = ((p.B + ab.groups - 1) / ab.groups + 7) / 8 * 8;
     ab.groups = (p.B + ab.group - 1) / ab.group;
     ab.rot_blocks = (int)(((long)p.B * ((p.H + 31) / 32) + 3) / 4);
@@ -1120,12 +1166,16 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     at.scale_log2 = p.scale * 1.4426950408889634f;
     at.idesc_s = idesc_f16(128, NK, false);
     at.idesc_pv = idesc_f16(128, 256, false, true);
+    if ((e = cudaFuncSetAttribute(paged_absorb_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM)) != cudaSuccess)
+        return e;
+    if ((e = cudaFuncSetAttribute(paged_join_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, JSMEM)) != cudaSuccess) return e;
+    const int per_head = std::max(1, std::min((p.B + JB - 1) / JB, 2 * p.workers / p.H));   // one wave of join blocks
     auto attn = unit == 64 ? paged_attn_tc_kernel<64> : unit == 32 ? paged_attn_tc_kernel<32> : unit == 16 ? paged_attn_tc_kernel<16> : paged_attn_tc_kernel<8>;
     if ((e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess)
         return e;
     {
         ProfScope ps("paged_absorb", st);
-        paged_absorb_tc_kernel<<<(unsigned)(p.H * 4 * ab.groups + 1 + ab.rot_blocks), 128, 0, st>>>(ab);
+        paged_absorb_tc_kernel<<<(unsigned)(p.H * 4 * ab.groups + 1 + ab.rot_blocks), 128, AB_SMEM, st>>>(ab);
     }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     {
@@ -1135,7 +1185,7 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     {
         ProfScope ps("paged_join", st);
-        e = launch_after(paged_join_tc_kernel, (unsigned)(p.H * ((p.B + JB - 1) / JB)), JNT, 0, st, p, (const bf16 *)ab.qlo);
+        e = launch_after(paged_join_tc_kernel, (unsigned)(p.H * per_head), JNT, JSMEM, st, p, (const bf16 *)ab.qlo, per_head);
     }
     return e;
 }
