@@ -1118,7 +1118,7 @@ mla_status paged_decode_shape(const mla_dims *d, mla_dtype dt, int B, int page_s
     if (st != MLA_OK) return st;
     if (!valid_dtype(dt)) return MLA_ERR_DTYPE;
     if (B < 0 || page_size < 1 || max_pages < 1 || (long)max_pages * page_size > 1 << 30 ||
-        ((long)B + 3) * d->n_heads > INT_MAX)
+        ((long)B + 3) * d->n_heads > INT_MAX / 4 || ((long)B + 3) / 4 * d->n_heads * (((long)d->d_v + 31) / 32) > INT_MAX)
         return MLA_ERR_SHAPE;
     p->B = B;
     p->H = d->n_heads;
@@ -1142,7 +1142,7 @@ mla_status paged_decode_shape(const mla_dims *d, mla_dtype dt, int B, int page_s
         p->row_tile = 16;
         p->tile = 32;
         p->workers = 152;
-        p->min_tiles = 2;
+        p->min_tiles = 1;
     }
     p->row_tiles = (p->H + p->row_tile - 1) / p->row_tile;
     return MLA_OK;

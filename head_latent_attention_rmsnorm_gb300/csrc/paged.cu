@@ -7,43 +7,39 @@
 
 namespace mla {
 
-void paged_turns(float base, int Dr, unsigned long long *v) {
-    for (int t = 0; t < Dr / 2; ++t) {
-        const double f = pow((double)base, -2.0 * t / Dr) / 6.283185307179586476925286766559;
-        v[t] = (unsigned long long)ldexp(f - floor(f), 64);
+using namespace paged;
+
+const unsigned long long *paged_turns(float base, int Dr) {
+    static thread_local unsigned long long v[MAX_HALF];
+    static thread_local float last_base = 0.f;
+    static thread_local int last_dr = 0;
+    if (last_base != base || last_dr != Dr) {
+        for (int t = 0; t < Dr / 2; ++t) {
+            const double f = pow((double)base, -2.0 * t / Dr) / 6.283185307179586476925286766559;
+            v[t] = (unsigned long long)ldexp(f - floor(f), 64);
+        }
+        last_base = base;
+        last_dr = Dr;
     }
+    return v;
 }
 
 namespace {
 
-using namespace paged;
-
 // ------------------------------------------------------------------------ tables ----
 // Each block forms both prefix sums (tokens, pages taken) over all requests in its own shared
-// memory and then fills its share of the token and page rows; no block waits for another.
-constexpr int TB = 1024;
-
+// memory and then fills its share of the token and page rows; no block waits for another.  The rows
+// are found by binary search in shared memory; everything per row is 32-bit arithmetic, with the
+// division by the page size as a multiplication (64-bit divisions took 9 of 15 us at 2001 requests
+// and half a million tokens).
 struct Tables {
     int B, page, max_pages, n_free, n_tokens;
+    Divisor by_page;
     const int *past, *fresh, *free_pages;
     int *table, *kv_lens, *cu, *slots, *positions, *counts;
 };
 
 __device__ __forceinline__ int sat(long v) { return (int)min(v, 2147483647l); }
-
-struct Request {
-    int past, have;   // tokens and pages held before
-    long placed, extra;
-};
-__device__ __forceinline__ Request request(const Tables &a, int b, long cu) {
-    const long cap = (long)a.max_pages * a.page;
-    Request r;
-    r.past = (int)min((long)max(a.past[b], 0), cap);
-    r.placed = max(min(min((long)a.fresh[b], (long)a.n_tokens - cu), cap - r.past), 0l);
-    r.have = (r.past + a.page - 1) / a.page;
-    r.extra = (r.past + r.placed + a.page - 1) / a.page - r.have;
-    return r;
-}
 
 // Exclusive prefix of one value per thread over the block; the total in `all`.
 __device__ __forceinline__ long block_scan(long n, long *warp_tot, long &all) {
@@ -67,30 +63,42 @@ __device__ __forceinline__ long block_scan(long n, long *warp_tot, long &all) {
     return before + x - n;
 }
 
-__global__ void __launch_bounds__(TB) paged_tables_kernel(Tables a) {
+// The last of n requests whose prefix is <= x.
+__device__ __forceinline__ int owner(const int *prefix, int n, int x) {
+    int lo = 0;
+    while (n > 1) {
+        const int half = n >> 1;
+        if (prefix[lo + half] <= x) lo += half;
+        n -= half;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(1024) paged_tables_kernel(const __grid_constant__ Tables a) {
     extern __shared__ int sm[];
-    __shared__ long warp_tot[TB / 32];
-    int *cu = sm, *off = sm + a.B + 1;
-    const int tid = threadIdx.x;
+    __shared__ long warp_tot[32];
+    int *cu = sm, *off = cu + a.B + 1, *past = off + a.B + 1;
+    const int tid = threadIdx.x, cap = a.max_pages * a.page;
     long tok = 0, pages = 0;
-    for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {   // the last request's successor holds the totals
+    for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
         const int b = b0 + tid;
+        const bool in = b < a.B;
+        const int p0 = in ? min(max(a.past[b], 0), cap) : 0, fresh = in ? max(a.fresh[b], 0) : 0;
         long all;
-        const long n = b < a.B ? max(a.fresh[b], 0) : 0;
-        const long c = tok + block_scan(n, warp_tot, all);
+        const long c = tok + block_scan(fresh, warp_tot, all);
         tok += all;
-        Request r{};
-        if (b < a.B) r = request(a, b, c);
-        const long o = pages + block_scan(r.extra, warp_tot, all);
+        const int placed = max((int)min(min((long)fresh, (long)a.n_tokens - c), (long)(cap - p0)), 0);
+        const int have = quotient(a.by_page, p0 + a.page - 1), extra = quotient(a.by_page, p0 + placed + a.page - 1) - have;
+        const long o = pages + block_scan(extra, warp_tot, all);
         pages += all;
-        if (b < a.B) {
+        if (in) {
             cu[b] = sat(c);
             off[b] = sat(o);
+            past[b] = p0;
             if (blockIdx.x == 0) {
-                const long got = min(max((long)a.n_free - o, 0l), r.extra);
+                const int got = (int)min(max((long)a.n_free - o, 0l), (long)extra);
                 a.cu[b] = sat(c);
-                a.kv_lens[b] = (int)(got == r.extra ? r.past + r.placed
-                                                    : max((long)r.past, (r.have + got) * (long)a.page));
+                a.kv_lens[b] = got == extra ? p0 + placed : max(p0, (have + got) * a.page);
             }
         }
     }
@@ -104,42 +112,28 @@ __global__ void __launch_bounds__(TB) paged_tables_kernel(Tables a) {
         }
     }
     __syncthreads();
-    const long step = (long)gridDim.x * blockDim.x;
+    const long step = (long)gridDim.x * blockDim.x, first = (long)blockIdx.x * blockDim.x + tid;
     // pages: entry e of the free list goes to the request whose prefix range holds e
-    const long taken = min((long)off[a.B], (long)a.n_free);
-    for (long e = (long)blockIdx.x * blockDim.x + tid; e < taken; e += step) {
-        int lo = 0, hi = a.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (off[mid] <= e) lo = mid;
-            else hi = mid - 1;
-        }
-        const Request r = request(a, lo, cu[lo]);
-        a.table[(long)lo * a.max_pages + r.have + (e - off[lo])] = a.free_pages[e];
+    const int taken = min(off[a.B], a.n_free), tokens = min(cu[a.B], a.n_tokens);
+    for (long e = first; e < taken; e += step) {
+        const int b = owner(off, a.B, (int)e);
+        const int have = quotient(a.by_page, past[b] + a.page - 1);
+        a.table[(long)b * a.max_pages + have + ((int)e - off[b])] = a.free_pages[e];
     }
-    // tokens
-    for (long t = (long)blockIdx.x * blockDim.x + tid; t < a.n_tokens; t += step) {
+    // tokens; rows behind the last one belong to no request
+    for (long t = first; t < a.n_tokens; t += step) {
         int slot = -1, pos = 0;
-        if (t < cu[a.B]) {
-            int lo = 0, hi = a.B - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (cu[mid] <= t) lo = mid;
-                else hi = mid - 1;
-            }
-            const Request r = request(a, lo, cu[lo]);
-            const long i = t - cu[lo], at = r.past + i;
-            pos = sat(at);
-            if (i < r.placed) {
-                const int col = (int)(at / a.page), in = (int)(at % a.page);
+        if (t < tokens) {
+            const int b = owner(cu, a.B, (int)t), p0 = past[b];
+            const unsigned at = (unsigned)p0 + (unsigned)((int)t - cu[b]);   // below 2^30 + 2^31
+            pos = (int)min(at, 2147483647u);
+            if (at < (unsigned)cap) {
+                const int col = quotient(a.by_page, pos), have = quotient(a.by_page, p0 + a.page - 1);
+                const long e = (long)off[b] + col - have;
                 int id = -1;
-                if (col < r.have) {
-                    id = a.table[(long)lo * a.max_pages + col];
-                } else {
-                    const long e = (long)off[lo] + col - r.have;
-                    if (e < a.n_free) id = a.free_pages[e];
-                }
-                const long s = (long)id * a.page + in;
+                if (col < have) id = a.table[(long)b * a.max_pages + col];
+                else if (e < a.n_free) id = a.free_pages[e];
+                const long s = (long)id * a.page + (pos - col * a.page);
                 if (id >= 0 && s <= 2147483647l) slot = (int)s;
             }
         }
@@ -158,33 +152,111 @@ struct Append {
     const void *c, *k, *w;
     const int *slots, *positions;
     void *c_cache, *kpe_cache;
-    Turns turns;
 };
 
+template <typename T, typename TU>
+__device__ __forceinline__ void rotate_row(const Append &a, const TU &turns, long t, long slot, int lane) {
+    const int half = a.Dr / 2, pos = a.positions[t];
+    const T *k = (const T *)a.k + t * a.k_stride;
+    T *o = (T *)a.kpe_cache + slot * a.Dr;
+    for (int i = lane; i < half; i += 32) {
+        const float x = to_f<T>(k[i]), y = to_f<T>(k[i + half]);
+        const float2 cs = turn_cs(turns.v[i], pos);
+        o[i] = from_f<T>(x * cs.x - y * cs.y);
+        o[i + half] = from_f<T>(y * cs.x + x * cs.y);
+    }
+}
+
+// Any width and row pitch.
 template <typename T>
-__global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ Append a) {
-    const int lane = threadIdx.x & 31, half = a.Dr / 2;
-    const long warp = ((long)blockIdx.x * blockDim.x + threadIdx.x) >> 5, nwarps = ((long)gridDim.x * blockDim.x) >> 5;
-    for (long t = warp; t < a.T; t += nwarps) {
-        const long slot = a.slots[t];
-        if (slot < 0 || slot >= a.n_slots) continue;
-        const int pos = a.positions[t];
-        const T *c = (const T *)a.c + t * a.c_stride, *k = (const T *)a.k + t * a.k_stride, *w = (const T *)a.w;
-        T *co = (T *)a.c_cache + slot * a.Dk, *ko = (T *)a.kpe_cache + slot * a.Dr;
-        float s = 0.f;
-        for (int d = lane; d < a.Dk; d += 32) {
-            const float v = to_f<T>(c[d]);
-            s = fmaf(v, v, s);
+__global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ Append a, const __grid_constant__ Turns turns) {
+    const int lane = threadIdx.x & 31;
+    const long t = ((long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    if (t >= a.T) return;
+    const long slot = a.slots[t];
+    if (slot < 0 || slot >= a.n_slots) return;
+    const T *c = (const T *)a.c + t * a.c_stride, *w = (const T *)a.w;
+    T *co = (T *)a.c_cache + slot * a.Dk;
+    float s = 0.f;
+    for (int d = lane; d < a.Dk; d += 32) {
+        const float v = to_f<T>(c[d]);
+        s = fmaf(v, v, s);
+    }
+    const float r = 1.f / sqrtf(warp_sum(s) / (float)a.Dk + a.eps);
+    for (int d = lane; d < a.Dk; d += 32) co[d] = from_f<T>(to_f<T>(c[d]) * r * to_f<T>(w[d]));
+    rotate_row<T>(a, turns, t, slot, lane);
+}
+
+// 16-byte pieces: rows of a whole number of pieces, up to 32 NC, held in registers between the sum and
+// the write; one read and one write of every byte.  16384 tokens of 512 + 64 bf16: 13.3 us by single
+// elements.
+template <typename T, int NC, typename TU>
+__global__ void __launch_bounds__(256) paged_append_vec_kernel(const __grid_constant__ Append a, const __grid_constant__ TU turns) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const int lane = threadIdx.x & 31, pieces = a.Dk / E;
+    const long t = ((long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    if (t >= a.T) return;
+    const long slot = a.slots[t];
+    const uint4 *c = (const uint4 *)((const T *)a.c + t * a.c_stride), *w = (const uint4 *)a.w;
+    uint4 x[NC], y[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+        if (lane + 32 * i < pieces) {
+            x[i] = __ldcs(c + lane + 32 * i);
+            y[i] = __ldg(w + lane + 32 * i);
+        } else {
+            x[i] = y[i] = make_uint4(0, 0, 0, 0);
         }
-        const float r = 1.f / sqrtf(warp_sum(s) / (float)a.Dk + a.eps);
-        for (int d = lane; d < a.Dk; d += 32) co[d] = from_f<T>(to_f<T>(c[d]) * r * to_f<T>(w[d]));
-        for (int i = lane; i < half; i += 32) {
-            const float2 cs = turn_cs(a.turns.v[i], pos);
-            const float x = to_f<T>(k[i]), y = to_f<T>(k[i + half]);
-            ko[i] = from_f<T>(x * cs.x - y * cs.y);
-            ko[i + half] = from_f<T>(y * cs.x + x * cs.y);
+    if (slot < 0 || slot >= a.n_slots) return;
+    float f[NC][E], s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        alignas(16) T v[E];
+        *(uint4 *)v = x[i];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            f[i][e] = to_f<T>(v[e]);
+            s = fmaf(f[i][e], f[i][e], s);
         }
     }
+    const float r = 1.f / sqrtf(warp_sum(s) / (float)a.Dk + a.eps);
+    uint4 *o = (uint4 *)((T *)a.c_cache + slot * a.Dk);
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+        if (lane + 32 * i < pieces) {
+            alignas(16) T v[E];
+            *(uint4 *)v = y[i];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = from_f<T>(f[i][e] * r * to_f<T>(v[e]));
+            o[lane + 32 * i] = *(const uint4 *)v;
+        }
+    rotate_row<T>(a, turns, t, slot, lane);
+}
+
+template <typename T, int NC>
+void append_vec(const Append &a, const unsigned long long *v, cudaStream_t st) {
+    const unsigned blocks = (unsigned)(((long)a.T + 7) / 8);
+    if (a.Dr <= 64) {
+        Turns64 turns{};
+        std::copy(v, v + a.Dr / 2, turns.v);
+        paged_append_vec_kernel<T, NC><<<blocks, 256, 0, st>>>(a, turns);
+    } else {
+        Turns turns{};
+        std::copy(v, v + a.Dr / 2, turns.v);
+        paged_append_vec_kernel<T, NC><<<blocks, 256, 0, st>>>(a, turns);
+    }
+}
+
+template <typename T>
+void append(const Append &a, const unsigned long long *v, cudaStream_t st) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const int pieces = a.Dk % E == 0 && a.c_stride % E == 0 ? a.Dk / E : 0;
+    if (pieces > 0 && pieces <= 32) return append_vec<T, 1>(a, v, st);
+    if (pieces > 0 && pieces <= 64) return append_vec<T, 2>(a, v, st);
+    if (pieces > 0 && pieces <= 128) return append_vec<T, 4>(a, v, st);
+    Turns turns{};
+    std::copy(v, v + a.Dr / 2, turns.v);
+    paged_append_kernel<T><<<(unsigned)(((long)a.T + 7) / 8), 256, 0, st>>>(a, turns);
 }
 
 }  // namespace
@@ -192,25 +264,29 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
 cudaError_t launch_paged_tables(int B, int page, int max_pages, int n_free, int n_tokens, const int *past,
                                 const int *fresh, const int *free_pages, int *table, int *kv_lens, int *cu, int *slots,
                                 int *positions, int *counts, cudaStream_t st) {
-    Tables a{B, page, max_pages, n_free, n_tokens, past, fresh, free_pages, table, kv_lens, cu, slots, positions, counts};
-    const int smem = 2 * (B + 1) * (int)sizeof(int);
-    const int blocks = (int)std::min(152l, std::max(1l, ((long)n_tokens + TB - 1) / TB));
-    cudaError_t e = cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    Tables a{B, page, max_pages, n_free, n_tokens, divisor(page), past, fresh, free_pages, table, kv_lens, cu, slots, positions, counts};
+    const int smem = (3 * B + 2) * (int)sizeof(int);
+    // a block per 1024 rows, one per SM at most; small steps in a small block (fewer warps to bring together)
+    const long rows = std::max((long)n_tokens, (long)B);
+    const int threads = rows <= 128 ? 128 : rows <= 512 ? 256 : 1024;
+    const int blocks = (int)std::min(152l, std::max(1l, (rows + threads - 1) / threads));
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
     ProfScope ps("paged_tables", st);
-    paged_tables_kernel<<<blocks, TB, smem, st>>>(a);
+    paged_tables_kernel<<<blocks, threads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 cudaError_t launch_paged_append(int ty, int T, long n_slots, int Dk, int Dr, float base, float eps, const void *c,
                                 long c_stride, const void *k, long k_stride, const void *w, const int *slots,
                                 const int *positions, void *c_cache, void *kpe_cache, cudaStream_t st) {
-    Append a{T, Dk, Dr, n_slots, c_stride, k_stride, eps, c, k, w, slots, positions, c_cache, kpe_cache, {}};
-    paged_turns(base, Dr, a.turns.v);
-    const int blocks = (int)std::min(152l * 8, ((long)T + 7) / 8);
+    Append a{T, Dk, Dr, n_slots, c_stride, k_stride, eps, c, k, w, slots, positions, c_cache, kpe_cache};
+    const unsigned long long *v = paged_turns(base, Dr);
     ProfScope ps("paged_append", st);
-    if (ty == TY_F32) paged_append_kernel<float><<<blocks, 256, 0, st>>>(a);
-    else paged_append_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(a);
+    if (ty == TY_F32) append<float>(a, v, st);
+    else append<__nv_bfloat16>(a, v, st);
     return cudaGetLastError();
 }
 

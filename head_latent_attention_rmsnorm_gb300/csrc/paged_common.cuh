@@ -37,14 +37,32 @@ __device__ __forceinline__ float warp_sum(float v) {
 // fraction of a turn (to pos * 2^-53 of the frequency's own rounding), at any 32-bit position and
 // without a double-precision operation on the device.
 constexpr int MAX_HALF = 320;   // d_rope <= 640
-struct Turns {
-    unsigned long long v[MAX_HALF];
+template <int N>
+struct TurnsOf {
+    unsigned long long v[N];
 };
+using Turns = TurnsOf<MAX_HALF>;
+using Turns64 = TurnsOf<32>;    // d_rope <= 64: a tenth of the launch's parameters
 __device__ __forceinline__ float2 turn_cs(unsigned long long turns, int pos) {
     const long long x = (long long)(turns * (unsigned long long)(long long)pos);
     float s, c;
     sincospif((float)(int)(x >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31 half turns
     return make_float2(c, s);
+}
+
+// x / d for 0 <= x < 2^31 by a multiplication (round-up multiplier; the sum cannot overflow, as the high
+// product is at most x).
+struct Divisor {
+    uint32_t mul, shift;
+};
+__device__ __forceinline__ int quotient(const Divisor &d, int x) {
+    return (int)((__umulhi(d.mul, (uint32_t)x) + (uint32_t)x) >> d.shift);
+}
+inline Divisor divisor(int d) {
+    Divisor r{0, 0};
+    while ((1u << r.shift) < (unsigned)d) ++r.shift;
+    r.mul = (uint32_t)((((unsigned long long)1 << 32) * (((unsigned long long)1 << r.shift) - d)) / d + 1);
+    return r;
 }
 
 // Workers that take part for T tiles, and the first tile of worker c.
@@ -173,7 +191,7 @@ __device__ void plan_block(const PagedDecode &p, int *sm = nullptr, int room = 0
 
 }  // namespace paged
 
-// The frequencies of Turns for one base and width (host).
-void paged_turns(float base, int Dr, unsigned long long *v);
+// The frequencies for one base and width (host), kept for the next call of the thread with the same two.
+const unsigned long long *paged_turns(float base, int Dr);
 
 }  // namespace mla

@@ -19,46 +19,72 @@ constexpr int HT = 16;          // heads per work item
 constexpr int KT = 32;          // keys per tile
 constexpr int DK_MAX = 512, DQ_MAX = 640;
 constexpr int BT = 4;           // requests per block of the two weight products
+constexpr int DC = 128;         // latent dims of an absorb block
+constexpr int VC = 32;          // value dims of a join block
 
 // ------------------------------------------------------------------------ absorb ----
-// Block (h, group of BT requests): a thread owns latent dims and walks the rows of W_K(h), each
-// weight read once per group.  One block more forms the tile prefix sums.
+// Block (head, DC latent dims, group of BT requests): the warps share out the rows of W_K(h), a lane
+// holds four dims 32 apart, and the warps' sums meet in shared memory.  The grid is cut that fine
+// because few heads over few requests are a matter of latency: every weight load of a block is in
+// flight at once.  One block more forms the tile prefix sums.
 template <typename T>
 __global__ void __launch_bounds__(NT) paged_absorb_simt_kernel(const __grid_constant__ PagedDecode p,
                                                                const __grid_constant__ Turns turns) {
-    extern __shared__ float sm[];
-    const int tid = threadIdx.x;
-    const int groups = (p.B + BT - 1) / BT;
-    if (blockIdx.x == (unsigned)(groups * p.H)) {
+    extern __shared__ float sm[];   // q [BT][Dn], sums [8 warps][BT][DC]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int groups = (p.B + BT - 1) / BT, chunks = (p.Dk + DC - 1) / DC;
+    if (blockIdx.x == 0) {
         plan_block<NT>(p);
         return;
     }
-    const int h = blockIdx.x / groups, b0 = (blockIdx.x % groups) * BT, nb = min(BT, p.B - b0);
+    int u = blockIdx.x - 1;
+    const int ch = u % chunks;
+    u /= chunks;
+    const int h = u / groups, b0 = (u % groups) * BT, nb = min(BT, p.B - b0), d0 = ch * DC;
     for (int i = tid; i < BT * p.Dn; i += NT) {
         const int j = i / p.Dn, n = i % p.Dn;
         sm[i] = j < nb ? to_f<T>(((const T *)p.q_nope)[((long)(b0 + j) * p.H + h) * p.Dn + n]) : 0.f;
     }
-    const int half = p.Dr / 2;
-    for (int i = tid; i < nb * half; i += NT) {   // the query sits at its request's last key
-        const int j = i / half, t = i % half;
-        const long row = (long)(b0 + j) * p.H + h;
-        const float2 cs = turn_cs(turns.v[t], keys_of(p, b0 + j) - 1);
-        const T *x = (const T *)p.q_pe + row * p.Dr;
-        const float x0 = to_f<T>(x[t]), x1 = to_f<T>(x[t + half]);
-        float *y = (float *)p.qpe + row * p.Dr;
-        y[t] = x0 * cs.x - x1 * cs.y;
-        y[t + half] = x1 * cs.x + x0 * cs.y;
+    if (ch == 0) {   // the query sits at its request's last key
+        const int half = p.Dr / 2;
+        for (int i = tid; i < nb * half; i += NT) {
+            const int j = i / half, t = i % half;
+            const long row = (long)(b0 + j) * p.H + h;
+            const float2 cs = turn_cs(turns.v[t], keys_of(p, b0 + j) - 1);
+            const T *x = (const T *)p.q_pe + row * p.Dr;
+            const float x0 = to_f<T>(x[t]), x1 = to_f<T>(x[t + half]);
+            float *y = (float *)p.qpe + row * p.Dr;
+            y[t] = x0 * cs.x - x1 * cs.y;
+            y[t + half] = x1 * cs.x + x0 * cs.y;
+        }
     }
     __syncthreads();
-    const T *w = (const T *)p.w + (long)h * (p.Dn + p.Dv) * p.Dk;
-    for (int d = tid; d < p.Dk; d += NT) {
-        float acc[BT] = {};
-        for (int n = 0; n < p.Dn; ++n) {
-            const float v = to_f<T>(w[(long)n * p.Dk + d]);
+    const T *w = (const T *)p.w + (long)h * (p.Dn + p.Dv) * p.Dk + d0 + lane;
+    float acc[BT][4] = {};
+#pragma unroll 8
+    for (int n = warp; n < p.Dn; n += NT / 32) {
+        float v[4];
 #pragma unroll
-            for (int j = 0; j < BT; ++j) acc[j] = fmaf(v, sm[j * p.Dn + n], acc[j]);
+        for (int k = 0; k < 4; ++k) v[k] = d0 + lane + 32 * k < p.Dk ? to_f<T>(w[(long)n * p.Dk + 32 * k]) : 0.f;
+#pragma unroll
+        for (int j = 0; j < BT; ++j) {
+            const float q = sm[j * p.Dn + n];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[j][k] = fmaf(v[k], q, acc[j][k]);
         }
-        for (int j = 0; j < nb; ++j) ((float *)p.qabs)[((long)(b0 + j) * p.H + h) * p.Dk + d] = acc[j];
+    }
+    float *sum = sm + BT * p.Dn;
+#pragma unroll
+    for (int j = 0; j < BT; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[(warp * BT + j) * DC + lane + 32 * k] = acc[j][k];
+    __syncthreads();
+    for (int i = tid; i < BT * DC; i += NT) {
+        const int j = i / DC, d = i % DC;
+        float x = 0.f;
+#pragma unroll
+        for (int k = 0; k < NT / 32; ++k) x += sum[(k * BT + j) * DC + d];
+        if (j < nb && d0 + d < p.Dk) ((float *)p.qabs)[((long)(b0 + j) * p.H + h) * p.Dk + d0 + d] = x;
     }
 }
 
@@ -80,6 +106,13 @@ __host__ __device__ inline Lay layout(int Dq) {
     return l;
 }
 
+__device__ __forceinline__ float4 load4(const float *p) { return __ldg((const float4 *)p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 x = __ldg((const uint2 *)p);
+    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                       __uint_as_float(x.y & 0xffff0000u));
+}
+
 template <typename T>
 __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_constant__ PagedDecode p) {
     extern __shared__ float sm[];
@@ -96,6 +129,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
     long t = (long)blockIdx.x * total / W;
     const long tend = (long)(blockIdx.x + 1) * total / W;
     const int chunks = (Dq + 3) / 4;
+    const bool four = p.Dk % 4 == 0 && p.Dr % 4 == 0;
     while (t < tend) {
         const int b = request_of(p, p.tile_off, t);
         const long first = p.tile_off[b], per = p.tile_off[b + 1] - first;
@@ -133,13 +167,35 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
                 sRow[tid] = row;
             }
             __syncthreads();
-            for (int k = warp; k < KT; k += NT / 32) {   // a warp per key row; absent keys as zeros
-                const int row = sRow[k];
-                const T *c = (const T *)p.c_cache + (long)row * p.Dk, *r = (const T *)p.kpe_cache + (long)row * p.Dr;
-                for (int d = lane; d < L.dqp; d += 32) {
-                    float v = 0.f;
-                    if (row >= 0 && d < Dq) v = d < p.Dk ? to_f<T>(c[d]) : to_f<T>(r[d - p.Dk]);
-                    sK[k * L.dqp + d] = v;
+            if (four) {   // rows of whole groups of four: a lane per group, a warp's four rows in flight
+                const int ck = p.Dk / 4, cr = p.Dr / 4;
+                for (int i0 = lane; i0 < ck + cr; i0 += 64) {
+                    float4 v[KT / 8][2];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int k = 0; k < KT / 8; ++k) {
+                            const int row = sRow[warp + 8 * k], i = i0 + 32 * q;
+                            v[k][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (row >= 0 && i < ck + cr)
+                                v[k][q] = i < ck ? load4((const T *)p.c_cache + (long)row * p.Dk + 4 * i)
+                                                 : load4((const T *)p.kpe_cache + (long)row * p.Dr + 4 * (i - ck));
+                        }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int k = 0; k < KT / 8; ++k)
+                            if (i0 + 32 * q < ck + cr) *(float4 *)(sK + (warp + 8 * k) * L.dqp + 4 * (i0 + 32 * q)) = v[k][q];
+                }
+            } else {
+                for (int k = warp; k < KT; k += NT / 32) {   // a warp per key row; absent keys as zeros
+                    const int row = sRow[k];
+                    const T *c = (const T *)p.c_cache + (long)row * p.Dk, *r = (const T *)p.kpe_cache + (long)row * p.Dr;
+                    for (int d = lane; d < L.dqp; d += 32) {
+                        float v = 0.f;
+                        if (row >= 0 && d < Dq) v = d < p.Dk ? to_f<T>(c[d]) : to_f<T>(r[d - p.Dk]);
+                        sK[k * L.dqp + d] = v;
+                    }
                 }
             }
             __syncthreads();
@@ -224,66 +280,92 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
 }
 
 // -------------------------------------------------------------------------- join ----
+// Block (head, VC value dims, group of BT requests): the parts' weights, their merge (a thread per
+// latent dim and two requests), then a warp per four rows of W_V.
+constexpr int JP = 160;   // parts of an item at most (the workers)
+
 template <typename T>
 __global__ void __launch_bounds__(NT) paged_join_simt_kernel(const __grid_constant__ PagedDecode p) {
     extern __shared__ float sm[];   // o [BT][Dk]
+    __shared__ float sw[BT][JP];
+    __shared__ long ss[BT];
+    __shared__ int sn[BT];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int groups = (p.B + BT - 1) / BT;
-    const int h = blockIdx.x / groups, b0 = (blockIdx.x % groups) * BT, nb = min(BT, p.B - b0);
+    const int groups = (p.B + BT - 1) / BT, chunks = (p.Dv + VC - 1) / VC;
+    int u = blockIdx.x;
+    const int ch = u % chunks;
+    u /= chunks;
+    const int h = u / groups, b0 = (u % groups) * BT, nb = min(BT, p.B - b0);
     const int rt = h / p.row_tile, r = h % p.row_tile;
-    const long total = p.tile_off[p.B] * p.row_tiles;
-    const int W = total ? active_workers(p, total) : 0;
-    for (int j = 0; j < nb; ++j) {
-        const int b = b0 + j;
-        const long per = p.tile_off[b + 1] - p.tile_off[b], first = p.tile_off[b] * p.row_tiles + rt * per;
-        const long item = (long)b * p.row_tiles + rt;
-        float m = -INFINITY, sum = 0.f;
-        int c0 = 0, c1 = -1;
-        if (per > 0) {
-            c0 = worker_of(first, total, W);
-            c1 = worker_of(first + per - 1, total, W);
-            for (int c = c0; c <= c1; ++c) m = fmaxf(m, p.pl[(c + item) * p.row_tile + r]);
-            for (int c = c0; c <= c1; ++c) {
-                const float x = p.pl[(c + item) * p.row_tile + r];
-                if (x != -INFINITY) sum += expf(x - m);
+    if (warp < BT) {
+        const int b = b0 + warp;
+        long s0 = 0;
+        int n = 0;
+        if (warp < nb) {
+            const long total = p.tile_off[p.B] * p.row_tiles;
+            const long per = p.tile_off[b + 1] - p.tile_off[b], first = p.tile_off[b] * p.row_tiles + rt * per;
+            if (per > 0) {
+                const int W = active_workers(p, total), c0 = worker_of(first, total, W);
+                n = worker_of(first + per - 1, total, W) - c0 + 1;
+                s0 = c0 + (long)b * p.row_tiles + rt;
             }
         }
-        const float lse = sum == 0.f ? -INFINITY : m + logf(sum);
-        for (int d = tid; d < p.Dk; d += NT) {
-            float o = 0.f;
-            if (sum != 0.f)
-                for (int c = c0; c <= c1; ++c) {
-                    const long s = (c + item) * p.row_tile + r;
-                    if (p.pl[s] != -INFINITY) o = fmaf(expf(p.pl[s] - lse), p.po32[s * p.Dk + d], o);
-                }
-            sm[j * p.Dk + d] = o;
+        const float *pl = p.pl + s0 * p.row_tile + r;
+        float m = -INFINITY, sum = 0.f;
+        for (int c = lane; c < n; c += 32) m = fmaxf(m, pl[(long)c * p.row_tile]);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        for (int c = lane; c < n; c += 32) {
+            const float x = pl[(long)c * p.row_tile];
+            sum += sw[warp][c] = x == -INFINITY ? 0.f : expf(x - m);
         }
-        if (tid == 0) p.lse[(long)b * p.H + h] = lse;
+        sum = warp_sum(sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        for (int c = lane; c < n; c += 32) sw[warp][c] *= inv;
+        if (lane == 0) {
+            ss[warp] = s0;
+            sn[warp] = n;
+            if (ch == 0 && warp < nb) p.lse[(long)b * p.H + h] = sum == 0.f ? -INFINITY : m + logf(sum);
+        }
     }
     __syncthreads();
-    const T *w = (const T *)p.w + ((long)h * (p.Dn + p.Dv) + p.Dn) * p.Dk;
-    for (int v = warp; v < p.Dv; v += NT / 32) {
-        float acc[BT] = {};
-        for (int d = lane; d < p.Dk; d += 32) {
-            const float x = to_f<T>(w[(long)v * p.Dk + d]);
+    for (int i = tid; i < BT * p.Dk; i += NT) {
+        const int j = i / p.Dk, d = i % p.Dk;
+        const float *po = p.po32 + (ss[j] * p.row_tile + r) * p.Dk + d;
+        const long pitch = (long)p.row_tile * p.Dk;
+        float o = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < sn[j]; ++c) o = fmaf(sw[j][c], po[c * pitch], o);
+        sm[i] = o;
+    }
+    __syncthreads();
+    const int v0 = ch * VC + warp * 4;
+    const T *w = (const T *)p.w + ((long)h * (p.Dn + p.Dv) + p.Dn + v0) * p.Dk;
+    float acc[4][BT] = {};
+#pragma unroll 4
+    for (int d = lane; d < p.Dk; d += 32)
 #pragma unroll
-            for (int j = 0; j < BT; ++j)
-                if (j < nb) acc[j] = fmaf(x, sm[j * p.Dk + d], acc[j]);
+        for (int k = 0; k < 4; ++k) {
+            const float x = v0 + k < p.Dv ? to_f<T>(w[(long)k * p.Dk + d]) : 0.f;
+#pragma unroll
+            for (int j = 0; j < BT; ++j) acc[k][j] = fmaf(x, sm[j * p.Dk + d], acc[k][j]);
         }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int j = 0; j < BT; ++j) {
-            const float s = warp_sum(acc[j]);
-            if (lane == 0 && j < nb) ((T *)p.out)[((long)(b0 + j) * p.H + h) * p.Dv + v] = from_f<T>(s);
+            const float x = warp_sum(acc[k][j]);
+            if (lane == 0 && j < nb && v0 + k < p.Dv) ((T *)p.out)[((long)(b0 + j) * p.H + h) * p.Dv + v0 + k] = from_f<T>(x);
         }
-    }
 }
 
 template <typename T>
 cudaError_t decode_simt(const PagedDecode &p, cudaStream_t st) {
     Turns turns{};
-    paged_turns(p.base, p.Dr, turns.v);
-    const unsigned blocks = (unsigned)((p.B + BT - 1) / BT) * (unsigned)p.H;
-    const size_t s1 = (size_t)BT * p.Dn * 4, s2 = (size_t)layout(p.Dk + p.Dr).total * 4, s3 = (size_t)BT * p.Dk * 4;
+    std::copy_n(paged_turns(p.base, p.Dr), p.Dr / 2, turns.v);
+    const unsigned units = (unsigned)((p.B + BT - 1) / BT) * (unsigned)p.H;
+    const unsigned blocks = units * (unsigned)((p.Dk + DC - 1) / DC), jblocks = units * (unsigned)((p.Dv + VC - 1) / VC);
+    const size_t s1 = ((size_t)BT * p.Dn + (size_t)NT / 32 * BT * DC) * 4, s2 = (size_t)layout(p.Dk + p.Dr).total * 4, s3 = (size_t)BT * p.Dk * 4;
     cudaError_t e;
     if ((e = cudaFuncSetAttribute(paged_absorb_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1)) != cudaSuccess)
         return e;
@@ -301,7 +383,7 @@ cudaError_t decode_simt(const PagedDecode &p, cudaStream_t st) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     {
         ProfScope ps("paged_join", st);
-        paged_join_simt_kernel<T><<<blocks, NT, s3, st>>>(p);
+        paged_join_simt_kernel<T><<<jblocks, NT, s3, st>>>(p);
     }
     return cudaGetLastError();
 }

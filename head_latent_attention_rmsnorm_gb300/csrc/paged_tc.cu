@@ -96,7 +96,7 @@ struct Absorb {
     bf16 *qhi, *qlo, *rhi, *rlo;   // [B][H][512], [B][H][64]
     int groups, group;             // groups of `group` requests
     int rot_blocks;                // blocks 1 .. rot_blocks rotate the queries; block 0 divides the batch
-    Turns turns;
+    Turns64 turns;
 };
 
 // The queries' rotation: a warp per request and 32 heads, a lane per pair of dims, the angle formed once.
@@ -478,7 +478,7 @@ struct Maps {
 struct Attn {
     PagedDecode p;
     int q_rows;                 // rows of the query boxes
-    uint32_t page_mul, page_shift;   // division by the page size
+    Divisor by_page;
     float scale_log2;
     uint32_t idesc_s, idesc_pv;
 };
@@ -488,14 +488,10 @@ struct Attn {
 // whose slow side is one function, rolled loops around small bodies.  The same kernel at 95 KB of
 // code took 1.4 us a tile where 82 KB took 1.0.
 
-// x / page for 0 <= x < 2^31 (round-up multiplier; the sum cannot overflow as the high product is < x).
-__device__ __forceinline__ int page_of(const Attn &a, int x) {
-    return (int)((__umulhi(a.page_mul, (uint32_t)x) + (uint32_t)x) >> a.page_shift);
-}
 // The cache row of key `key` of the part's request, -1 for none (behind the end, a bad page id).
 __device__ __forceinline__ int row_of(const Attn &a, const PagedPart &w, int key) {
     if (key >= w.keys) return -1;
-    const int col = page_of(a, key);
+    const int col = quotient(a.by_page, key);
     const int id = __ldg(a.p.table + (long)w.b * a.p.max_pages + col);
     return (unsigned)id < (unsigned)a.p.num_pages ? id * a.p.page + (key - col * a.p.page) : -1;
 }
@@ -706,7 +702,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 // whether every page of the part has an id inside the cache
                 bool sound = true;
                 {
-                    const int c0 = page_of(a, w.k0 * NK), c1 = page_of(a, min(w.keys, (w.k0 + w.nt) * NK) - 1);
+                    const int c0 = quotient(a.by_page, w.k0 * NK), c1 = quotient(a.by_page, min(w.keys, (w.k0 + w.nt) * NK) - 1);
                     const int *ids = p.table + (long)w.b * p.max_pages;
 #pragma unroll 2
                     for (int col = c0 + lane; col <= c1; col += 32) sound = sound && (unsigned)__ldg(ids + col) < (unsigned)p.num_pages;
@@ -1134,7 +1130,7 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     ab.group = ((p.B + ab.groups - 1) / ab.groups + 7) / 8 * 8;
     ab.groups = (p.B + ab.group - 1) / ab.group;
     ab.rot_blocks = (int)(((long)p.B * ((p.H + 31) / 32) + 3) / 4);
-    paged_turns(p.base, DR, ab.turns.v);
+    std::copy_n(paged_turns(p.base, DR), DR / 2, ab.turns.v);
 
     Attn at{};
     int unit = NK;   // rows that always share a page: the largest power of two up to a tile that divides one
@@ -1161,8 +1157,7 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
         if ((e = make_tma_map(&m.rl, ab.rlo, 3, dr, sr, bq)) != cudaSuccess) return e;
     }
     at.p = p;
-    while ((1u << at.page_shift) < (unsigned)p.page) ++at.page_shift;
-    at.page_mul = (uint32_t)((((ull)1 << 32) * (((ull)1 << at.page_shift) - p.page)) / p.page + 1);
+    at.by_page = divisor(p.page);
     at.scale_log2 = p.scale * 1.4426950408889634f;
     at.idesc_s = idesc_f16(128, NK, false);
     at.idesc_pv = idesc_f16(128, 256, false, true);

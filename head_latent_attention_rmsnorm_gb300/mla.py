@@ -17,7 +17,6 @@ is missing this module raises on first use; there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -566,18 +565,33 @@ def lse_combine(part_out, part_lse, *, out_dtype=torch.float32, out=None, lse=No
 
 
 # ------------------------------------------------------------------- paged cache ----
-def _on(device: torch.device):
-    """The tensors' device made current for the call: the library launches on the current
-    device, and the default stream is that device's current one."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+# A serving step makes these three calls for every layer, and a small step's kernels last a few
+# microseconds: the checks are one expression per tensor, and only a failed one finds out why.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _shape(name: str, t, shape: tuple, dtype: torch.dtype, device: torch.device) -> None:
+def _need(name: str, t, shape: tuple, dtype: torch.dtype, device: torch.device) -> int:
+    """The address of a tensor of exactly this shape and dtype, dense, on the call's device."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: expected a torch.Tensor, got %s" % (name, type(t).__name__))
     _expect(name, t, math.prod(shape), dtype, device)
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), shape))
+    raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), shape))
+
+
+def _launch(device: torch.device, stream, fn, where: str, *args) -> None:
+    """The call with the tensors' device current (the library launches on the current device; the
+    default stream is that device's current one)."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
+    if st != 0:
+        raise MlaError(st, where)
 
 
 class PagedTables(NamedTuple):
@@ -601,45 +615,37 @@ def paged_tables(past_lens, new_lens, free_pages, block_table, *, page_size, n_t
         if slots is None:
             raise ValueError("n_tokens or slots is required")
         n_tokens = slots.numel()
-    i32 = torch.int32
     if not isinstance(free_pages, torch.Tensor):
         raise TypeError("free_pages: expected a torch.Tensor, got %s" % type(free_pages).__name__)
     n_free = free_pages.numel()
-    for name, t, shape in (("block_table", block_table, (B, max_pages)), ("past_lens", past_lens, (B,)),
-                           ("new_lens", new_lens, (B,)), ("free_pages", free_pages, (n_free,)),
-                           ("kv_lens", kv_lens, (B,)), ("cu_tokens", cu_tokens, (B + 1,)),
-                           ("slots", slots, (n_tokens,)), ("positions", positions, (n_tokens,)),
-                           ("counts", counts, (2,))):
-        _shape(name, t, shape, i32, dev)
-    if past_lens is None or new_lens is None:
-        raise TypeError("past_lens and new_lens are required")
-    with _on(dev):
-        if kv_lens is None:
-            kv_lens = torch.empty(B, dtype=i32, device=dev)
-        if cu_tokens is None:
-            cu_tokens = torch.empty(B + 1, dtype=i32, device=dev)
-        if slots is None:
-            slots = torch.empty(n_tokens, dtype=i32, device=dev)
-        if positions is None:
-            positions = torch.empty(n_tokens, dtype=i32, device=dev)
-        if counts is None:
-            counts = torch.empty(2, dtype=i32, device=dev)
-        st = lib().mla_paged_tables(B, page_size, max_pages, n_free, n_tokens, _ptr(past_lens), _ptr(new_lens),
-                                    _ptr(free_pages), _ptr(block_table), _ptr(kv_lens), _ptr(cu_tokens), _ptr(slots),
-                                    _ptr(positions), _ptr(counts), _stream(stream))
-    _check(st, "mla_paged_tables")
+    i32 = torch.int32
+    if kv_lens is None:
+        kv_lens = torch.empty(B, dtype=i32, device=dev)
+    if cu_tokens is None:
+        cu_tokens = torch.empty(B + 1, dtype=i32, device=dev)
+    if slots is None:
+        slots = torch.empty(n_tokens, dtype=i32, device=dev)
+    if positions is None:
+        positions = torch.empty(n_tokens, dtype=i32, device=dev)
+    if counts is None:
+        counts = torch.empty(2, dtype=i32, device=dev)
+    rows = (B,)
+    _launch(dev, stream, lib().mla_paged_tables, "mla_paged_tables", B, page_size, max_pages, n_free, n_tokens,
+            _need("past_lens", past_lens, rows, i32, dev), _need("new_lens", new_lens, rows, i32, dev),
+            _need("free_pages", free_pages, (n_free,), i32, dev),
+            _need("block_table", block_table, (B, max_pages), i32, dev), _need("kv_lens", kv_lens, rows, i32, dev),
+            _need("cu_tokens", cu_tokens, (B + 1,), i32, dev), _need("slots", slots, (n_tokens,), i32, dev),
+            _need("positions", positions, (n_tokens,), i32, dev), _need("counts", counts, (2,), i32, dev))
     return PagedTables(kv_lens, cu_tokens, slots, positions, counts)
 
 
-def _cache_checks(d, c_cache, kpe_cache, tdt, dev):
-    if c_cache.dim() != 3:
+def _cache(d, c_cache, kpe_cache, tdt, dev):
+    """(num_pages, page_size, address of c_cache, of kpe_cache)."""
+    if not isinstance(c_cache, torch.Tensor) or c_cache.dim() != 3:
         raise ValueError("c_cache must be [num_pages, page_size, d_kv]")
-    num_pages, page = c_cache.shape[:2]
-    _shape("c_cache", c_cache, (num_pages, page, d.d_kv), tdt, dev)
-    _shape("kpe_cache", kpe_cache, (num_pages, page, d.d_rope), tdt, dev)
-    if kpe_cache is None:
-        raise TypeError("kpe_cache is required")
-    return num_pages, page
+    num_pages, page, _ = c_cache.shape
+    return (num_pages, page, _need("c_cache", c_cache, (num_pages, page, d.d_kv), tdt, dev),
+            _need("kpe_cache", kpe_cache, (num_pages, page, d.d_rope), tdt, dev))
 
 
 def _rows(name, t, n, width, dtype, device) -> int:
@@ -650,13 +656,12 @@ def _rows(name, t, n, width, dtype, device) -> int:
         raise ValueError("%s: on %s, the call's tensors are on %s" % (name, t.device, device))
     if t.dtype != dtype:
         raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
-    if tuple(t.shape) != (n, width):
+    if t.shape != (n, width):
         raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), (n, width)))
+    pitch, step = t.stride()
     if n < 2:
         pitch = width
-    else:
-        pitch = t.stride(0)
-    if (width > 1 and t.stride(1) != 1) or pitch < width:
+    if (width > 1 and step != 1) or pitch < width:
         raise ValueError("%s: a row's elements must be adjacent and rows must not overlap" % name)
     return pitch
 
@@ -666,23 +671,17 @@ def paged_append(d: Dims, c_kv, k_pe, rms_w, slots, positions, c_cache, kpe_cach
     cache, in place.  ``c_kv`` [n, d_kv] and ``k_pe`` [n, d_rope] may be column ranges of wider
     rows.  Returns (c_cache, kpe_cache)."""
     dev = _device(c_kv)
-    dt = _dt(c_kv)
+    dt, tdt = _dt(c_kv), c_kv.dtype
     if c_kv.dim() != 2:
         raise ValueError("c_kv must be [n_tokens, d_kv]")
-    n, tdt = c_kv.shape[0], c_kv.dtype
-    num_pages, page = _cache_checks(d, c_cache, kpe_cache, tdt, dev)
+    n = c_kv.shape[0]
+    num_pages, page, cp, kp = _cache(d, c_cache, kpe_cache, tdt, dev)
     cs = _rows("c_kv", c_kv, n, d.d_kv, tdt, dev)
     ks = _rows("k_pe", k_pe, n, d.d_rope, tdt, dev)
-    for name, t, shape, ty in (("rms_w", rms_w, (d.d_kv,), tdt), ("slots", slots, (n,), torch.int32),
-                               ("positions", positions, (n,), torch.int32)):
-        if t is None:
-            raise TypeError("%s is required" % name)
-        _shape(name, t, shape, ty, dev)
-    with _on(dev):
-        st = lib().mla_paged_append(ctypes.byref(d), dt, n, num_pages, page, c_kv.data_ptr(), cs, k_pe.data_ptr(), ks,
-                                    _ptr(rms_w), _ptr(slots), _ptr(positions), _ptr(c_cache), _ptr(kpe_cache),
-                                    _stream(stream))
-    _check(st, "mla_paged_append")
+    rows, i32 = (n,), torch.int32
+    _launch(dev, stream, lib().mla_paged_append, "mla_paged_append", d, dt, n, num_pages, page, c_kv.data_ptr(), cs,
+            k_pe.data_ptr(), ks, _need("rms_w", rms_w, (d.d_kv,), tdt, dev), _need("slots", slots, rows, i32, dev),
+            _need("positions", positions, rows, i32, dev), cp, kp)
     return c_cache, kpe_cache
 
 
@@ -699,36 +698,27 @@ def paged_decode(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens
     """Latent decode of one query per request over the paged cache; ``kv_lens`` and
     ``block_table`` (int32) stay on the device.  Returns (out, lse)."""
     dev = _device(q_nope)
-    dt = _dt(q_nope)
-    tdt = q_nope.dtype
-    if q_nope.dim() != 3 or block_table.dim() != 2:
+    dt, tdt = _dt(q_nope), q_nope.dtype
+    if q_nope.dim() != 3 or not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("q_nope must be [B, n_heads, d_nope] and block_table [B, max_pages]")
-    B, H = q_nope.shape[0], d.n_heads
+    B, H, i32 = q_nope.shape[0], d.n_heads, torch.int32
     max_pages = block_table.shape[1]
-    num_pages, page = _cache_checks(d, c_cache, kpe_cache, tdt, dev)
-    for name, t, shape, ty in (("q_nope", q_nope, (B, H, d.d_nope), tdt), ("q_pe", q_pe, (B, H, d.d_rope), tdt),
-                               ("block_table", block_table, (B, max_pages), torch.int32),
-                               ("kv_lens", kv_lens, (B,), torch.int32)):
-        if t is None:
-            raise TypeError("%s is required" % name)
-        _shape(name, t, shape, ty, dev)
-    if w_kv_b is None:
-        raise TypeError("w_kv_b is required")
+    num_pages, page, cp, kp = _cache(d, c_cache, kpe_cache, tdt, dev)
+    if not isinstance(w_kv_b, torch.Tensor):
+        raise TypeError("w_kv_b: expected a torch.Tensor, got %s" % type(w_kv_b).__name__)
     _expect("w_kv_b", w_kv_b, H * (d.d_nope + d.d_v) * d.d_kv, tdt, dev)
-    _shape("out", out, (B, H, d.d_v), tdt, dev)
-    _shape("lse", lse, (B, H), torch.float32, dev)
-    with _on(dev):
-        if out is None:
-            out = torch.empty(B, H, d.d_v, dtype=tdt, device=dev)
-        if lse is None:
-            lse = torch.empty(B, H, dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = paged_decode_workspace(d, c_cache, block_table)
-        else:
-            _workspace(0, dev, workspace)
-        st = lib().mla_paged_decode(ctypes.byref(d), dt, B, num_pages, page, max_pages, _ptr(q_nope), _ptr(q_pe),
-                                    _ptr(c_cache), _ptr(kpe_cache), _ptr(block_table), _ptr(kv_lens), _ptr(w_kv_b),
-                                    _ptr(out), _ptr(lse), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "mla_paged_decode")
+    ptrs = (_need("q_nope", q_nope, (B, H, d.d_nope), tdt, dev), _need("q_pe", q_pe, (B, H, d.d_rope), tdt, dev), cp, kp,
+            _need("block_table", block_table, (B, max_pages), i32, dev), _need("kv_lens", kv_lens, (B,), i32, dev),
+            w_kv_b.data_ptr())
+    if out is None:
+        out = torch.empty(B, H, d.d_v, dtype=tdt, device=dev)
+    if lse is None:
+        lse = torch.empty(B, H, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = paged_decode_workspace(d, c_cache, block_table)
+    else:
+        _workspace(0, dev, workspace)
+    _launch(dev, stream, lib().mla_paged_decode, "mla_paged_decode", d, dt, B, num_pages, page, max_pages, *ptrs,
+            _need("out", out, (B, H, d.d_v), tdt, dev), _need("lse", lse, (B, H), torch.float32, dev), _ptr(workspace),
+            workspace.numel() * workspace.element_size())
     return out, lse

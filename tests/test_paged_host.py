@@ -166,12 +166,19 @@ def test_row_pitch_check():
         f(None)
 
 
-def test_shape_check():
+def test_tensor_check():
     cpu = torch.device("cpu")
     x = torch.zeros(4, 6)
-    mla._shape("x", x, (4, 6), torch.float32, cpu)
-    mla._shape("x", None, (4, 6), torch.float32, cpu)
-    with pytest.raises(ValueError, match="shape"):
-        mla._shape("x", x, (6, 4), torch.float32, cpu)
+    assert mla._need("x", x, (4, 6), torch.float32, cpu) == x.data_ptr()
+    with pytest.raises(ValueError, match="x: shape"):
+        mla._need("x", x, (6, 4), torch.float32, cpu)
+    with pytest.raises(ValueError, match="x: 24 elements, expected 20"):
+        mla._need("x", x, (4, 5), torch.float32, cpu)
     with pytest.raises(ValueError, match="contiguous"):
-        mla._shape("x", torch.zeros(6, 4).t(), (4, 6), torch.float32, cpu)
+        mla._need("x", torch.zeros(6, 4).t(), (4, 6), torch.float32, cpu)
+    with pytest.raises(TypeError, match="dtype"):
+        mla._need("x", x.double(), (4, 6), torch.float32, cpu)
+    with pytest.raises(ValueError, match="on cpu"):
+        mla._need("x", x, (4, 6), torch.float32, torch.device("cuda", 0))
+    with pytest.raises(TypeError, match="expected a torch.Tensor"):
+        mla._need("x", None, (4, 6), torch.float32, cpu)
