@@ -1137,7 +1137,7 @@ mla_status paged_decode_shape(const mla_dims *d, mla_dtype dt, int B, int page_s
         p->row_tile = std::min(p->H, 128);
         p->tile = PAGED_TC_TILE;
         p->workers = PAGED_TC_WORKERS;
-        p->min_tiles = 3;
+        p->min_tiles = 2;
     } else {
         p->row_tile = 16;
         p->tile = 32;

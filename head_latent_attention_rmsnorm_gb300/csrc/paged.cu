@@ -74,6 +74,8 @@ __device__ __forceinline__ int owner(const int *prefix, int n, int x) {
     return lo;
 }
 
+// PER: token rows of a thread.
+template <int PER>
 __global__ void __launch_bounds__(1024) paged_tables_kernel(const __grid_constant__ Tables a) {
     extern __shared__ int sm[];
     __shared__ long warp_tot[32];
@@ -120,25 +122,42 @@ __global__ void __launch_bounds__(1024) paged_tables_kernel(const __grid_constan
         const int have = quotient(a.by_page, past[b] + a.page - 1);
         a.table[(long)b * a.max_pages + have + ((int)e - off[b])] = a.free_pages[e];
     }
-    // tokens; rows behind the last one belong to no request
-    for (long t = first; t < a.n_tokens; t += step) {
-        int slot = -1, pos = 0;
-        if (t < tokens) {
-            const int b = owner(cu, a.B, (int)t), p0 = past[b];
+    // tokens, PER neighbours to a thread: one search, then a walk; rows behind the last token belong to no
+    // request
+    const bool wide = PER == 4 && (((uintptr_t)a.slots | (uintptr_t)a.positions) & 15) == 0;
+    for (long t4 = first * PER; t4 < a.n_tokens; t4 += step * PER) {
+        int slot[PER], pos[PER];
+        int b = t4 < tokens ? owner(cu, a.B, (int)t4) : 0;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const long t = t4 + k;
+            slot[k] = -1;
+            pos[k] = 0;
+            if (t >= tokens) continue;
+            while (cu[b + 1] <= t) ++b;
+            const int p0 = past[b];
             const unsigned at = (unsigned)p0 + (unsigned)((int)t - cu[b]);   // below 2^30 + 2^31
-            pos = (int)min(at, 2147483647u);
-            if (at < (unsigned)cap) {
-                const int col = quotient(a.by_page, pos), have = quotient(a.by_page, p0 + a.page - 1);
-                const long e = (long)off[b] + col - have;
-                int id = -1;
-                if (col < have) id = a.table[(long)b * a.max_pages + col];
-                else if (e < a.n_free) id = a.free_pages[e];
-                const long s = (long)id * a.page + (pos - col * a.page);
-                if (id >= 0 && s <= 2147483647l) slot = (int)s;
-            }
+            pos[k] = (int)min(at, 2147483647u);
+            if (at >= (unsigned)cap) continue;
+            const int col = quotient(a.by_page, pos[k]), have = quotient(a.by_page, p0 + a.page - 1);
+            const long e = (long)off[b] + col - have;
+            int id = -1;
+            if (col < have) id = a.table[(long)b * a.max_pages + col];
+            else if (e < a.n_free) id = a.free_pages[e];
+            const long s = (long)id * a.page + (pos[k] - col * a.page);
+            if (id >= 0 && s <= 2147483647l) slot[k] = (int)s;
         }
-        a.slots[t] = slot;
-        a.positions[t] = pos;
+        if (wide && t4 + 4 <= a.n_tokens) {
+            *(int4 *)(a.slots + t4) = make_int4(slot[0], slot[PER / 4], slot[PER / 2], slot[PER - 1]);
+            *(int4 *)(a.positions + t4) = make_int4(pos[0], pos[PER / 4], pos[PER / 2], pos[PER - 1]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+                if (t4 + k < a.n_tokens) {
+                    a.slots[t4 + k] = slot[k];
+                    a.positions[t4 + k] = pos[k];
+                }
+        }
     }
 }
 
@@ -266,16 +285,20 @@ cudaError_t launch_paged_tables(int B, int page, int max_pages, int n_free, int 
                                 int *positions, int *counts, cudaStream_t st) {
     Tables a{B, page, max_pages, n_free, n_tokens, divisor(page), past, fresh, free_pages, table, kv_lens, cu, slots, positions, counts};
     const int smem = (3 * B + 2) * (int)sizeof(int);
-    // a block per 1024 rows, one per SM at most; small steps in a small block (fewer warps to bring together)
-    const long rows = std::max((long)n_tokens, (long)B);
+    // A block per 1024 threads, one per SM at most, small steps in a small block (fewer warps to bring
+    // together); four rows a thread once one a thread would fill the GPU (half a million tokens of 2001
+    // requests: 10.6 against 12.0 us; 66 thousand of eight: 6.9 against 5.4 us).
+    const bool four = n_tokens > 152 * 1024;
+    const long rows = std::max(four ? ((long)n_tokens + 3) / 4 : (long)n_tokens, (long)B);
     const int threads = rows <= 128 ? 128 : rows <= 512 ? 256 : 1024;
     const int blocks = (int)std::min(152l, std::max(1l, (rows + threads - 1) / threads));
+    auto kern = four ? paged_tables_kernel<4> : paged_tables_kernel<1>;
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
     ProfScope ps("paged_tables", st);
-    paged_tables_kernel<<<blocks, threads, smem, st>>>(a);
+    kern<<<blocks, threads, smem, st>>>(a);
     return cudaGetLastError();
 }
 

@@ -65,13 +65,14 @@ inline Divisor divisor(int d) {
     return r;
 }
 
-// Workers that take part for T tiles, and the first tile of worker c.
-__device__ __forceinline__ int active_workers(const PagedDecode &p, long T) {
-    const long w = (T + p.min_tiles - 1) / p.min_tiles;
-    return (int)(w < p.workers ? w : p.workers);
+// Tiles of a worker's share of T: worker c takes [c q, (c + 1) q).  Whole tiles, the same for all but the
+// last, so that shares end where requests do as often as they can (a request's last part and the
+// next one's first in one share cost some 5 us more than a tile each: 16 requests of 1000 keys went
+// from 31 to 27 us against shares of T / W).
+__device__ __forceinline__ long share_of(const PagedDecode &p, long T) {
+    const long q = (T + p.workers - 1) / p.workers;
+    return q > p.min_tiles ? q : p.min_tiles;
 }
-// The worker whose range holds tile t: the largest c with floor(c T / W) <= t.
-__device__ __forceinline__ int worker_of(long t, long T, int W) { return (int)(((t + 1) * W - 1) / T); }
 
 // A request's keys: its length cut to what its table row can hold.
 __device__ __forceinline__ int keys_of(const PagedDecode &p, int b) {
@@ -95,7 +96,7 @@ __device__ __forceinline__ int request_of(const PagedDecode &p, const I *off, lo
 // beginning finds its part's worker, item and end.
 template <int NT, typename I>
 __device__ void plan_parts(const PagedDecode &p, const I *off, long total) {
-    const int W = total ? active_workers(p, total) : 0;
+    const long q = share_of(p, total);
     const long items = (long)p.B * p.row_tiles;
 #pragma unroll 1
     for (long k = threadIdx.x; k < p.workers + items; k += NT) {
@@ -103,11 +104,11 @@ __device__ void plan_parts(const PagedDecode &p, const I *off, long total) {
         long t0 = 0;
         int b = 0, c = (int)k, rt = 0;
         if (worker) {
-            if (c >= W) {
+            if (c * q >= total) {
                 p.first[c] = p.first[p.workers + c] = 0;
                 continue;
             }
-            t0 = c * total / W;
+            t0 = c * q;
             b = request_of(p, off, t0);
         } else {
             b = (int)((k - p.workers) / p.row_tiles);
@@ -122,10 +123,10 @@ __device__ void plan_parts(const PagedDecode &p, const I *off, long total) {
             rt = (int)((t0 - o * p.row_tiles) / per);
         } else {
             t0 = o * p.row_tiles + rt * per;
-            c = worker_of(t0, total, W);
-            p.spans[k - p.workers] = make_int2(c + (int)(k - p.workers), worker_of(t0 + per - 1, total, W) - c + 1);
+            c = (int)(t0 / q);
+            p.spans[k - p.workers] = make_int2(c + (int)(k - p.workers), (int)((t0 + per - 1) / q) - c + 1);
         }
-        const long i0 = o * p.row_tiles + rt * per, i1 = i0 + per, end = (c + 1) * total / W, t1 = min(end, i1);
+        const long i0 = o * p.row_tiles + rt * per, i1 = i0 + per, end = min((c + 1) * q, total), t1 = min(end, i1);
         const int item = b * p.row_tiles + rt;
         PagedPart x{};
         x.b = b;

@@ -123,11 +123,9 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
     float *sM = sm + L.flag + KT, *sL = sM + HT, *sA = sL + HT;   // running maximum, sum, rescale
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long total = p.tile_off[p.B] * p.row_tiles;
-    if (total == 0) return;
-    const int W = active_workers(p, total);
-    if ((int)blockIdx.x >= W) return;
-    long t = (long)blockIdx.x * total / W;
-    const long tend = (long)(blockIdx.x + 1) * total / W;
+    const long q = share_of(p, total);
+    long t = blockIdx.x * q;
+    const long tend = min(t + q, total);
     const int chunks = (Dq + 3) / 4;
     const bool four = p.Dk % 4 == 0 && p.Dr % 4 == 0;
     while (t < tend) {
@@ -305,8 +303,8 @@ __global__ void __launch_bounds__(NT) paged_join_simt_kernel(const __grid_consta
             const long total = p.tile_off[p.B] * p.row_tiles;
             const long per = p.tile_off[b + 1] - p.tile_off[b], first = p.tile_off[b] * p.row_tiles + rt * per;
             if (per > 0) {
-                const int W = active_workers(p, total), c0 = worker_of(first, total, W);
-                n = worker_of(first + per - 1, total, W) - c0 + 1;
+                const long q = share_of(p, total), c0 = first / q;
+                n = (int)((first + per - 1) / q - c0) + 1;
                 s0 = c0 + (long)b * p.row_tiles + rt;
             }
         }

@@ -32,7 +32,8 @@
 // latent term shifts a part's log-sum-exp by scale q_lo . o to first order, which the epilogue
 // adds (the second order is half the variance of scale q_lo . c_j, ~1e-6 at unit scale).  q_lo
 // keeps q to 2^-17.  P is bf16 (relative 2^-8 on the weights of an average; the sums take the
-// unrounded ones).  Partials are fp32.
+// unrounded ones); up to 64 heads, what that rounding leaves goes through the idle rows 64 on, at no
+// cost in MMAs.  Partials are fp16 with a power of two per half row.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -552,7 +553,8 @@ __device__ void settle() {   // after an abandoned wait: loads in flight land be
     }
 }
 
-template <int UNIT>
+// PAIRED (up to 64 heads): the rows behind the heads, 64 on, carry P's low halves.
+template <int UNIT, bool PAIRED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     paged_attn_tc_kernel(const __grid_constant__ Maps m, const __grid_constant__ Attn a) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -614,6 +616,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         part += w.next;
         if (more) load();
     };
+    constexpr bool paired = PAIRED;
     const int none = (int)((p.num_pages * (long)p.page) >> 3);   // a row group outside the cache: zeros
 
     if (rank == 0) {
@@ -762,18 +765,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                         rescaled = __any_sync(FULL, need && i > 0);
                         const float m_eff = top == -INFINITY ? 0.f : top;
                         float ra[4] = {0.f, 0.f, 0.f, 0.f};
-                        uint8_t *stg = smem + OFF_STG + s * P_BYTES + row * 128;
+                        uint8_t *stg = smem + OFF_STG + s * P_BYTES + row * 128;   // (row + 64: the same swizzle)
 #pragma unroll
                         for (int q = 0; q < HK / 8; ++q) {
-                            uint32_t pk[4];
+                            uint32_t pk[4], lo[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const float p0 = ex2(fmaf(__uint_as_float(sa[8 * q + 2 * e]), c, -m_eff));
                                 const float p1 = ex2(fmaf(__uint_as_float(sa[8 * q + 2 * e + 1]), c, -m_eff));
                                 ra[e] += p0 + p1;
                                 pk[e] = pack_bf16(p0, p1);
+                                if (paired) lo[e] = pack_bf16(p0 - __uint_as_float(pk[e] << 16), p1 - __uint_as_float(pk[e] & 0xffff0000u));
                             }
-                            *(uint4 *)(stg + (((h * (HK / 8) + q) ^ (row & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                            uint4 *at = (uint4 *)(stg + (((h * (HK / 8) + q) ^ (row & 7)) << 4));
+                            at[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                            if (paired) at[64 * 128 / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         }
                         l = l * alpha + ((ra[0] + ra[1]) + (ra[2] + ra[3]));
                         if (i == w.nt - 1) {   // the row's sum, with the partner's half
@@ -785,7 +791,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                                 ((float *)(ext + X_LSE))[row] = lt == 0.f ? -INFINITY : m_eff + log2f(lt);
                             }
                         }
-                        if (h == 0) ((float *)(ext + X_ALPHA))[row] = alpha;
+                        if (h == 0) {
+                            ((float *)(ext + X_ALPHA))[row] = alpha;
+                            if (paired) ((float *)(ext + X_ALPHA))[row + 64] = alpha;
+                        }
                     }
                     if (h == 0 && lane == 0) ((uint32_t *)(ext + X_FLAG))[quad] = rescaled ? 1u : 0u;
                     fence_proxy_async_smem();
@@ -981,6 +990,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             bool ok = true;   // as in the softmax warps: every barrier is reached
             for (; more; next(), ++seg) {
                 const bool act = w.rt * ROWS + quad * 32 < p.H;
+                const bool acc = act || (paired && quad >= 2 && (quad - 2) * 32 < p.H);   // rows that O is kept for
                 const long slot = part - p.parts;
                 if (g == 0) {
                     float lse2 = -INFINITY, inv_l = 0.f;
@@ -1001,7 +1011,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                             ok = wait_all(&bars[B_PEMPTY + (s ^ 1)], ((n - 1) >> 1) & 1, ctl);
                             if (!ok) break;
                             tc_fence_after();
-                            const float al = act ? ((const float *)(xs + X_ALPHA))[row] : 1.f;
+                            const float al = acc ? ((const float *)(xs + X_ALPHA))[row] : 1.f;
                             if (__any_sync(FULL, al != 1.f)) {
 #pragma unroll 1
                                 for (int cc = 0; cc < 16; ++cc) {
@@ -1024,7 +1034,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                         if (lane == 0) mbar_arrive(&bars[B_PCREADY + s]);
                     }
                     invs[(seg & 1) * ROWS] = inv_l;
-                    if (ok && w.rt * ROWS + row < p.H) p.pl[slot * p.row_tile + row] = lse2 * 0.69314718055994531f;
+                    if (ok && act && w.rt * ROWS + row < p.H) p.pl[slot * p.row_tile + row] = lse2 * 0.69314718055994531f;
                 }
                 // ---- epilogue: the part's normalised output, 256 latent dims per warp: 64 columns of 32
                 // heads at a time, turned in shared memory so that a store writes whole 128-byte lines.
@@ -1035,7 +1045,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 const float inv_l = invs[(seg & 1) * ROWS];
                 ok = __all_sync(FULL, ok && wait_for(&bars[B_OFINAL], seg & 1, ctl));
                 tc_fence_after();
-                if (ok && act) {
+                if (paired && acc && !act) {
+                    // O of P's low halves, for the warp 64 rows in front, 32 columns at a time
+                    uint8_t *buf = smem + OFF_OUT + (warp - 2) * 4096 + lane * 128;
+#pragma unroll 1
+                    for (int cc = 0; cc < 8; ++cc) {
+                        uint32_t o[32];
+                        tmem_ld32(lb + 256 * g + 32 * cc, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *(uint4 *)(buf + ((e ^ (lane & 7)) << 4)) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        named_bar_sync(5 + 2 * (quad - 2) + g, 64);   // there
+                        named_bar_sync(5 + 2 * (quad - 2) + g, 64);   // added
+                    }
+                }
+                if (act) {   // (an abandoned wait leaves rubbish here, and the error word)
                     const int live = min(32, p.H - (w.rt * ROWS + quad * 32));
                     // the row's largest value here sets its power of two
                     float big = 0.f;
@@ -1061,6 +1086,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                             uint32_t o[32];
                             tmem_ld32(lb + 256 * g + 64 * cc + 32 * k, o);
                             tmem_ld_wait();
+                            if (paired) {
+                                const uint8_t *lo = smem + OFF_OUT + (4 * g + quad) * 4096 + lane * 128;
+                                named_bar_sync(5 + 2 * quad + g, 64);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const float4 x = *(const float4 *)(lo + ((e ^ (lane & 7)) << 4));
+                                    o[4 * e] = __float_as_uint(__uint_as_float(o[4 * e]) + x.x);
+                                    o[4 * e + 1] = __float_as_uint(__uint_as_float(o[4 * e + 1]) + x.y);
+                                    o[4 * e + 2] = __float_as_uint(__uint_as_float(o[4 * e + 2]) + x.z);
+                                    o[4 * e + 3] = __float_as_uint(__uint_as_float(o[4 * e + 3]) + x.w);
+                                }
+                                named_bar_sync(5 + 2 * quad + g, 64);
+                            }
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {   // 16-byte piece 4 k + e of row `lane` at piece .. ^ (row mod 8)
                                 uint32_t h[4];
@@ -1165,7 +1203,14 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
         return e;
     if ((e = cudaFuncSetAttribute(paged_join_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, JSMEM)) != cudaSuccess) return e;
     const int per_head = std::max(1, std::min((p.B + JB - 1) / JB, 2 * p.workers / p.H));   // one wave of join blocks
-    auto attn = unit == 64 ? paged_attn_tc_kernel<64> : unit == 32 ? paged_attn_tc_kernel<32> : unit == 16 ? paged_attn_tc_kernel<16> : paged_attn_tc_kernel<8>;
+    auto attn = p.H <= 64 ? (unit == 64   ? paged_attn_tc_kernel<64, true>
+                             : unit == 32 ? paged_attn_tc_kernel<32, true>
+                             : unit == 16 ? paged_attn_tc_kernel<16, true>
+                                          : paged_attn_tc_kernel<8, true>)
+                          : (unit == 64   ? paged_attn_tc_kernel<64, false>
+                             : unit == 32 ? paged_attn_tc_kernel<32, false>
+                             : unit == 16 ? paged_attn_tc_kernel<16, false>
+                                          : paged_attn_tc_kernel<8, false>);
     if ((e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess)
         return e;
     {

@@ -567,28 +567,29 @@ def lse_combine(part_out, part_lse, *, out_dtype=torch.float32, out=None, lse=No
 # ------------------------------------------------------------------- paged cache ----
 # A serving step makes these three calls for every layer, and a small step's kernels last a few
 # microseconds: the checks are one expression per tensor, and only a failed one finds out why.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _need(name: str, t, shape: tuple, dtype: torch.dtype, device: torch.device) -> int:
-    """The address of a tensor of exactly this shape and dtype, dense, on the call's device."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
-            and t.is_contiguous()):
-        return t.data_ptr()
+def _need(name: str, t, shape: tuple, dtype: torch.dtype, index: int) -> int:
+    """The address of a tensor of exactly this shape and dtype, dense, on CUDA device ``index``."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s: expected a torch.Tensor, got %s" % (name, type(t).__name__))
-    _expect(name, t, math.prod(shape), dtype, device)
+    _expect(name, t, math.prod(shape), dtype, torch.device("cuda", index))
     raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), shape))
 
 
-def _launch(device: torch.device, stream, fn, where: str, *args) -> None:
+def _launch(index: int, stream, fn, where: str, *args) -> None:
     """The call with the tensors' device current (the library launches on the current device; the
     default stream is that device's current one)."""
-    index = device.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         st = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             st = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
     if st != 0:
         raise MlaError(st, where)
@@ -629,31 +630,31 @@ def paged_tables(past_lens, new_lens, free_pages, block_table, *, page_size, n_t
         positions = torch.empty(n_tokens, dtype=i32, device=dev)
     if counts is None:
         counts = torch.empty(2, dtype=i32, device=dev)
-    rows = (B,)
-    _launch(dev, stream, lib().mla_paged_tables, "mla_paged_tables", B, page_size, max_pages, n_free, n_tokens,
-            _need("past_lens", past_lens, rows, i32, dev), _need("new_lens", new_lens, rows, i32, dev),
-            _need("free_pages", free_pages, (n_free,), i32, dev),
-            _need("block_table", block_table, (B, max_pages), i32, dev), _need("kv_lens", kv_lens, rows, i32, dev),
-            _need("cu_tokens", cu_tokens, (B + 1,), i32, dev), _need("slots", slots, (n_tokens,), i32, dev),
-            _need("positions", positions, (n_tokens,), i32, dev), _need("counts", counts, (2,), i32, dev))
+    rows, at = (B,), block_table.get_device()
+    _launch(at, stream, lib().mla_paged_tables, "mla_paged_tables", B, page_size, max_pages, n_free, n_tokens,
+            _need("past_lens", past_lens, rows, i32, at), _need("new_lens", new_lens, rows, i32, at),
+            _need("free_pages", free_pages, (n_free,), i32, at),
+            _need("block_table", block_table, (B, max_pages), i32, at), _need("kv_lens", kv_lens, rows, i32, at),
+            _need("cu_tokens", cu_tokens, (B + 1,), i32, at), _need("slots", slots, (n_tokens,), i32, at),
+            _need("positions", positions, (n_tokens,), i32, at), _need("counts", counts, (2,), i32, at))
     return PagedTables(kv_lens, cu_tokens, slots, positions, counts)
 
 
-def _cache(d, c_cache, kpe_cache, tdt, dev):
+def _cache(d, c_cache, kpe_cache, tdt, at):
     """(num_pages, page_size, address of c_cache, of kpe_cache)."""
     if not isinstance(c_cache, torch.Tensor) or c_cache.dim() != 3:
         raise ValueError("c_cache must be [num_pages, page_size, d_kv]")
     num_pages, page, _ = c_cache.shape
-    return (num_pages, page, _need("c_cache", c_cache, (num_pages, page, d.d_kv), tdt, dev),
-            _need("kpe_cache", kpe_cache, (num_pages, page, d.d_rope), tdt, dev))
+    return (num_pages, page, _need("c_cache", c_cache, (num_pages, page, d.d_kv), tdt, at),
+            _need("kpe_cache", kpe_cache, (num_pages, page, d.d_rope), tdt, at))
 
 
-def _rows(name, t, n, width, dtype, device) -> int:
+def _rows(name, t, n, width, dtype, index) -> int:
     """A matrix of n rows whose elements lie together, at any row pitch: returns the pitch."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s: expected a torch.Tensor, got %s" % (name, type(t).__name__))
-    if t.device != device:
-        raise ValueError("%s: on %s, the call's tensors are on %s" % (name, t.device, device))
+    if t.get_device() != index:
+        raise ValueError("%s: on %s, the call's tensors are on CUDA device %d" % (name, t.device, index))
     if t.dtype != dtype:
         raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.shape != (n, width):
@@ -670,18 +671,18 @@ def paged_append(d: Dims, c_kv, k_pe, rms_w, slots, positions, c_cache, kpe_cach
     """Write the tokens' normalised latent and rotated key band into their slots of the paged
     cache, in place.  ``c_kv`` [n, d_kv] and ``k_pe`` [n, d_rope] may be column ranges of wider
     rows.  Returns (c_cache, kpe_cache)."""
-    dev = _device(c_kv)
-    dt, tdt = _dt(c_kv), c_kv.dtype
+    _device(c_kv)
+    dt, tdt, at = _dt(c_kv), c_kv.dtype, c_kv.get_device()
     if c_kv.dim() != 2:
         raise ValueError("c_kv must be [n_tokens, d_kv]")
     n = c_kv.shape[0]
-    num_pages, page, cp, kp = _cache(d, c_cache, kpe_cache, tdt, dev)
-    cs = _rows("c_kv", c_kv, n, d.d_kv, tdt, dev)
-    ks = _rows("k_pe", k_pe, n, d.d_rope, tdt, dev)
+    num_pages, page, cp, kp = _cache(d, c_cache, kpe_cache, tdt, at)
+    cs = _rows("c_kv", c_kv, n, d.d_kv, tdt, at)
+    ks = _rows("k_pe", k_pe, n, d.d_rope, tdt, at)
     rows, i32 = (n,), torch.int32
-    _launch(dev, stream, lib().mla_paged_append, "mla_paged_append", d, dt, n, num_pages, page, c_kv.data_ptr(), cs,
-            k_pe.data_ptr(), ks, _need("rms_w", rms_w, (d.d_kv,), tdt, dev), _need("slots", slots, rows, i32, dev),
-            _need("positions", positions, rows, i32, dev), cp, kp)
+    _launch(at, stream, lib().mla_paged_append, "mla_paged_append", d, dt, n, num_pages, page, c_kv.data_ptr(), cs,
+            k_pe.data_ptr(), ks, _need("rms_w", rms_w, (d.d_kv,), tdt, at), _need("slots", slots, rows, i32, at),
+            _need("positions", positions, rows, i32, at), cp, kp)
     return c_cache, kpe_cache
 
 
@@ -698,17 +699,17 @@ def paged_decode(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens
     """Latent decode of one query per request over the paged cache; ``kv_lens`` and
     ``block_table`` (int32) stay on the device.  Returns (out, lse)."""
     dev = _device(q_nope)
-    dt, tdt = _dt(q_nope), q_nope.dtype
+    dt, tdt, at = _dt(q_nope), q_nope.dtype, q_nope.get_device()
     if q_nope.dim() != 3 or not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("q_nope must be [B, n_heads, d_nope] and block_table [B, max_pages]")
     B, H, i32 = q_nope.shape[0], d.n_heads, torch.int32
     max_pages = block_table.shape[1]
-    num_pages, page, cp, kp = _cache(d, c_cache, kpe_cache, tdt, dev)
+    num_pages, page, cp, kp = _cache(d, c_cache, kpe_cache, tdt, at)
     if not isinstance(w_kv_b, torch.Tensor):
         raise TypeError("w_kv_b: expected a torch.Tensor, got %s" % type(w_kv_b).__name__)
     _expect("w_kv_b", w_kv_b, H * (d.d_nope + d.d_v) * d.d_kv, tdt, dev)
-    ptrs = (_need("q_nope", q_nope, (B, H, d.d_nope), tdt, dev), _need("q_pe", q_pe, (B, H, d.d_rope), tdt, dev), cp, kp,
-            _need("block_table", block_table, (B, max_pages), i32, dev), _need("kv_lens", kv_lens, (B,), i32, dev),
+    ptrs = (_need("q_nope", q_nope, (B, H, d.d_nope), tdt, at), _need("q_pe", q_pe, (B, H, d.d_rope), tdt, at), cp, kp,
+            _need("block_table", block_table, (B, max_pages), i32, at), _need("kv_lens", kv_lens, (B,), i32, at),
             w_kv_b.data_ptr())
     if out is None:
         out = torch.empty(B, H, d.d_v, dtype=tdt, device=dev)
@@ -718,7 +719,7 @@ def paged_decode(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens
         workspace = paged_decode_workspace(d, c_cache, block_table)
     else:
         _workspace(0, dev, workspace)
-    _launch(dev, stream, lib().mla_paged_decode, "mla_paged_decode", d, dt, B, num_pages, page, max_pages, *ptrs,
-            _need("out", out, (B, H, d.d_v), tdt, dev), _need("lse", lse, (B, H), torch.float32, dev), _ptr(workspace),
+    _launch(at, stream, lib().mla_paged_decode, "mla_paged_decode", d, dt, B, num_pages, page, max_pages, *ptrs,
+            _need("out", out, (B, H, d.d_v), tdt, at), _need("lse", lse, (B, H), torch.float32, at), _ptr(workspace),
             workspace.numel() * workspace.element_size())
     return out, lse

@@ -351,6 +351,36 @@ def test_decode_agrees_with_the_dense_decode():
     assert float((o1.float() - o2.float()).norm() / o1.float().norm()) < 1e-2
 
 
+def test_refusals_on_the_device():
+    d, t = decode_case(TINY, 4, F32, [5, 9], 4)
+    dev = [x.cuda() for x in t]
+    for i, bad, kind, match in ((0, dev[0][:1], ValueError, "q_pe: .* elements|q_pe: shape"), (1, dev[1].double(), TypeError, "q_pe: dtype"),
+                                (2, dev[2][:, :3], ValueError, "c_cache: tensors must be contiguous"), (3, dev[3][:-1], ValueError, "kpe_cache"),
+                                (4, dev[4].long(), TypeError, "block_table: dtype"), (5, dev[5][:1], ValueError, "kv_lens"),
+                                (6, dev[6][:-1], ValueError, "w_kv_b"), (5, t[5], ValueError, "kv_lens: on cpu"),
+                                (1, dev[1].view(2, 16, 4), ValueError, "q_pe: shape")):
+        args = list(dev)
+        args[i] = bad
+        with pytest.raises(kind, match=match):
+            mla.paged_decode(d, *args)
+    with pytest.raises(mla.MlaError, match="WORKSPACE"):
+        mla.paged_decode(d, *dev, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(mla.MlaError, match="ALIAS"):
+        mla.paged_decode(d, *dev, out=dev[0].view(-1)[:2 * 4 * 32].view(2, 4, 32))
+    i = i32([1, 2])
+    with pytest.raises(TypeError, match="past_lens"):
+        mla.paged_tables(None, i, i, dev[4], page_size=4, n_tokens=2)
+    with pytest.raises(ValueError, match="n_tokens or slots"):
+        mla.paged_tables(i, i, i, dev[4], page_size=4)
+    with pytest.raises(mla.MlaError, match="SHAPE"):
+        mla.paged_tables(i, i, i, dev[4], page_size=0, n_tokens=2)
+    rows = torch.zeros(2, 80, device="cuda")
+    with pytest.raises(ValueError, match="adjacent"):
+        mla.paged_append(d, rows[:, :64], torch.zeros(16, 2, device="cuda").t(), rows[0, :64], i, i, dev[2], dev[3])
+    with pytest.raises(ValueError, match="slots"):
+        mla.paged_append(d, rows[:, :64], rows[:, 64:], rows[0, :64].contiguous(), i[:1], i, dev[2], dev[3])
+
+
 # --------------------------------------------------------------- the three in a row ----
 @pytest.mark.parametrize("dims,heads,dtype,page", [(DS, 16, BF16, 16), (TINY, 4, F32, 5)])
 def test_serving_steps_captured(dims, heads, dtype, page):

@@ -149,9 +149,8 @@ def test_wrappers_refuse_host_tensors():
 
 
 def test_row_pitch_check():
-    cpu = torch.device("cpu")
     x = torch.zeros(6, 30)
-    f = lambda t, n=6, width=20: mla._rows("x", t, n, width, torch.float32, cpu)   # noqa: E731
+    f = lambda t, n=6, width=20, at=-1: mla._rows("x", t, n, width, torch.float32, at)   # noqa: E731 (-1: the host)
     assert f(x[:, :20]) == 30 and f(x[:, 10:]) == 30 and f(torch.zeros(6, 20)) == 20
     assert f(x[::2, :20], n=3) == 60
     assert f(x[:1, :20], n=1) == 20                         # one row has no pitch
@@ -162,23 +161,19 @@ def test_row_pitch_check():
         f(x[:, :20].double())
     with pytest.raises(ValueError, match="shape"):
         f(x)
+    with pytest.raises(ValueError, match="CUDA device 0"):
+        f(x[:, :20], at=0)
     with pytest.raises(TypeError, match="expected a torch.Tensor"):
         f(None)
 
 
 def test_tensor_check():
-    cpu = torch.device("cpu")
     x = torch.zeros(4, 6)
-    assert mla._need("x", x, (4, 6), torch.float32, cpu) == x.data_ptr()
-    with pytest.raises(ValueError, match="x: shape"):
-        mla._need("x", x, (6, 4), torch.float32, cpu)
-    with pytest.raises(ValueError, match="x: 24 elements, expected 20"):
-        mla._need("x", x, (4, 5), torch.float32, cpu)
-    with pytest.raises(ValueError, match="contiguous"):
-        mla._need("x", torch.zeros(6, 4).t(), (4, 6), torch.float32, cpu)
-    with pytest.raises(TypeError, match="dtype"):
-        mla._need("x", x.double(), (4, 6), torch.float32, cpu)
-    with pytest.raises(ValueError, match="on cpu"):
-        mla._need("x", x, (4, 6), torch.float32, torch.device("cuda", 0))
-    with pytest.raises(TypeError, match="expected a torch.Tensor"):
-        mla._need("x", None, (4, 6), torch.float32, cpu)
+    assert mla._need("x", x, (4, 6), torch.float32, -1) == x.data_ptr()   # (-1: the host)
+    for t, shape, kind, match in (
+            (x, (6, 4), ValueError, "x: on cpu"), (x, (4, 5), ValueError, "x: on cpu"),
+            (torch.zeros(6, 4).t(), (4, 6), ValueError, "x: on cpu"), (x.double(), (4, 6), ValueError, "x: on cpu"),
+            (None, (4, 6), TypeError, "expected a torch.Tensor"), (3, (4, 6), TypeError, "expected a torch.Tensor"),
+            (np.zeros((4, 6), np.float32), (4, 6), TypeError, "expected a torch.Tensor")):
+        with pytest.raises(kind, match=match):
+            mla._need("x", t, shape, torch.float32, 0)
