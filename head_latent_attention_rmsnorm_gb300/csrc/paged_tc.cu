@@ -204,55 +204,77 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
 }
 
 // -------------------------------------------------------------------------- join ----
-// out[b, h, :] = W_V(h) sum_c w_c o_c: a block holds W_V(h) in shared memory and walks groups of 32
-// requests (one block per SM, so that the weights cross the L2 once per block).  Latency is what it
-// spends, so each phase has its loads in flight at once: W_V(h) lands while the rest runs (the
-// attention's last tiles brought it into L2); a warp per request forms the parts' weights; the
-// merge runs over eight groups of 128 threads (a thread per four latent dims), which share out the
-// requests, or, for up to four requests, their parts; the product (bf16 hi + lo of o against W_V,
-// m16n8k16) runs over eight warps of 16 value dims for each quarter of the 512 dims.  A step's
-// 16 summed dims are permuted alike in A and B (lane t of a row owns dims 64 i + 16 t .. + 15, four
-// dims a step), so both come by 16-byte loads.
-constexpr int JB = 32, JNT = 1024, JPITCH = DK * 2 + 16, JMAXC = 80;
-constexpr int JO = DV * JPITCH;                // W_V
-constexpr int JW = JO + 2 * JB * JPITCH;       // o as bf16 hi + lo; before it the groups' sums (7 x 4 x 512 fp32),
-                                               // after it the quarters' products [3][request][132]
-constexpr int JSMEM = JW + 2 * JB * JMAXC * 4; // the parts' weights for either half of the dims
-static_assert(2 * JB * JPITCH >= 7 * 4 * DK * 4 && 2 * JB * JPITCH >= 3 * JB * 132 * 4, "the join's exchanges");
+// out[b, h, :] = W_V(h) sum_c w_c o_c: a block holds W_V(h) in shared memory (by TMA, from the L2 into
+// which the attention's last tiles brought it) and walks groups of 32 requests.  Latency is what it
+// spends, so each phase has its loads in flight at once: a warp per request forms the parts'
+// weights; the merge runs over 16 groups of 64 threads (a thread per eight latent dims), which share
+// out the requests, or, for one or two requests, their parts; the product is tcgen05 (M = 128 value
+// dims, N = 32 requests, o as bf16 hi + lo, so that it is as exact as fp32 o): 64 MMAs of 32
+// columns, where mma.sync took 7500 cycles a group.
+constexpr int JB = 32, JNT = 1024, JMAXC = 80;
+constexpr int JO = DV * DK * 2;                // W_V: eight boxes of 64 dims x 128 rows
+constexpr int JBLK = JB * 128;                 // o: 64 dims x 32 requests
+constexpr int JW = JO + 2 * 8 * JBLK;          // o hi, o lo; before them the groups' sums [16][2][512]
+constexpr int JV = JW + 2 * JB * JMAXC * 4;    // the parts' weights for either half of the dims; then out [request][132]
+struct JoinVars {
+    uint64_t bar_w, bar_d;
+    int sc[JB][2];            // first part, number of parts
+    float sl[JB], sd[2][JB];  // log-sum-exp without the q_lo term; the warps' shares of q_lo . o
+    uint32_t tslot;
+    int abort;
+};
+constexpr int JSMEM = JV + sizeof(JoinVars);
+static_assert(2 * 8 * JBLK >= 16 * 2 * DK * 4 && 2 * JB * JMAXC >= JB * 132, "the join's exchanges");
 static_assert(PAGED_TC_WORKERS <= JMAXC && JMAXC <= 96, "parts of an item");
 
-__global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_constant__ PagedDecode p, const bf16 *qlo, int per_head) {
-    extern __shared__ __align__(16) uint8_t sm[];
-    __shared__ int sc[JB][2];            // first part, number of parts
-    __shared__ float sl[JB], sd[4][JB];  // log-sum-exp without the q_lo term; the warps' shares of q_lo . o
-    __shared__ uint64_t bar;
-    __shared__ int abort;
+__global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_constant__ CUtensorMap mW,
+                                                               const __grid_constant__ PagedDecode p, const bf16 *qlo,
+                                                               int per_head) {
+    extern __shared__ __align__(1024) uint8_t sm[];
+    if (smem_u32(sm) & 1023) {   // no room to align by hand; the same answer in every block
+        if (threadIdx.x == 0) atomicOr(&g_paged_tc_err, 2u);
+        return;
+    }
+    JoinVars &v0 = *(JoinVars *)(sm + JSMEM - sizeof(JoinVars));   // (static shared memory would push sm off its alignment)
+    auto &sc = v0.sc;
+    auto &sl = v0.sl;
+    auto &sd = v0.sd;
     uint8_t *so = sm + JO;
     float (*sw)[JB][JMAXC] = (float (*)[JB][JMAXC])(sm + JW);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x / per_head, rt = h / p.row_tile, r = h % p.row_tile;
-    const long pitch = (long)p.row_tile * (DK / 4);
+    const long pitch = (long)p.row_tile * (DK / 8);
     bool ok = true;
     if (tid == 0) {
-        mbar_init(&bar, 1);
-        abort = 0;
+        mbar_init(&v0.bar_w, 1);
+        mbar_init(&v0.bar_d, 1);
+        v0.abort = 0;
         fence_mbar_init();
-        mbar_arrive_expect_tx(&bar, DV * DK * 2);
-    }
-    __syncthreads();
-    if (tid < DV) bulk_load(sm + tid * JPITCH, (const bf16 *)p.w + ((long)h * (DN + DV) + DN + tid) * DK, DK * 2, &bar);
-    pdl_wait();
+        mbar_arrive_expect_tx(&v0.bar_w, JO);
 #pragma unroll 1
-    for (int b0 = (int)(blockIdx.x % per_head) * JB; b0 < p.B; b0 += per_head * JB) {
+        for (int i = 0; i < 8; ++i) tma_load_2d(sm + i * 16384, &mW, &v0.bar_w, 64 * i, h * (DN + DV) + DN);
+    }
+    if (warp == 1) {
+        tmem_alloc(&v0.tslot, 32);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = v0.tslot;
+    pdl_wait();
+    uint32_t ph = 0;
+#pragma unroll 1
+    for (int b0 = (int)(blockIdx.x % per_head) * JB; b0 < p.B; b0 += per_head * JB, ph ^= 1) {
         const int nb = min(JB, p.B - b0);
-        const int d4 = tid & 127, q8 = tid >> 7;
-        const bool few = nb <= 4;                                // the groups share out parts, not requests
-        const int j0 = few ? 0 : q8, dj = few ? 1 : 8, c0 = few ? q8 : 0, dc = few ? 8 : 1;
-        uint2 ql[4];
+        const int d8 = tid & 63, q16 = tid >> 6;
+        const bool few = nb <= 2;                                // the groups share out parts, not requests
+        const int j0 = few ? 0 : q16, dj = few ? 1 : 16, c0 = few ? q16 : 0, dc = few ? 16 : 1;
+        uint4 ql[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             const int j = j0 + dj * i;
-            ql[i] = j < nb ? __ldcg((const uint2 *)(qlo + ((long)(b0 + j) * p.H + h) * DK) + d4) : make_uint2(0, 0);
+            ql[i] = j < nb ? __ldcg((const uint4 *)(qlo + ((long)(b0 + j) * p.H + h) * DK) + d8) : make_uint4(0, 0, 0, 0);
         }
         {   // a warp per request: the weights of its parts (up to 96)
             int s0 = 0, n = 0;
@@ -295,116 +317,121 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
             }
         }
         __syncthreads();
-        float4 o[4];
+        float o[2][8] = {};
         {
-            const uint2 *src[4];
-            int n[4], most = 0;
+            const uint4 *src[2];
+            int n[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 const int j = j0 + dj * i;
-                src[i] = (const uint2 *)(p.po + ((long)sc[j][0] * p.row_tile + r) * DK) + d4;
+                src[i] = (const uint4 *)(p.po + ((long)sc[j][0] * p.row_tile + r) * DK) + d8;
                 n[i] = sc[j][1];
-                most = max(most, n[i]);
-                o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
+            const float *wt = sw[d8 >> 5][j0];
+            const int most = max(n[0], n[1]);
 #pragma unroll 1
-            for (int c = c0; c < most; c += 2 * dc) {
-                uint2 v[4][2];
+            for (int c = c0; c < most; c += 3 * dc) {
+                uint4 v[2][3];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < 3; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 2; ++i)
                         if (c + u * dc < n[i]) v[i][u] = __ldcg(src[i] + (c + u * dc) * pitch);
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < 3; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 2; ++i)
                         if (c + u * dc < n[i]) {
-                            const float x = sw[d4 >> 6][j0 + dj * i][c + u * dc];
-                            const float2 f0 = __half22float2(*(const __half2 *)&v[i][u].x), f1 = __half22float2(*(const __half2 *)&v[i][u].y);
-                            o[i].x = fmaf(x, f0.x, o[i].x);
-                            o[i].y = fmaf(x, f0.y, o[i].y);
-                            o[i].z = fmaf(x, f1.x, o[i].z);
-                            o[i].w = fmaf(x, f1.y, o[i].w);
+                            const float x = wt[dj * i * JMAXC + c + u * dc];
+                            const uint32_t w[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 f = __half22float2(*(const __half2 *)&w[e]);
+                                o[i][2 * e] = fmaf(x, f.x, o[i][2 * e]);
+                                o[i][2 * e + 1] = fmaf(x, f.y, o[i][2 * e + 1]);
+                            }
                         }
             }
         }
         if (few) {   // the groups' sums meet in the first
-            float4 *x = (float4 *)so;
-            if (q8 > 0)
+            float4 *x = (float4 *)so + d8 * 2;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[((q8 - 1) * 4 + i) * 128 + d4] = o[i];
+            for (int i = 0; i < 2; ++i) {
+                x[(q16 * 2 + i) * 128] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                x[(q16 * 2 + i) * 128 + 1] = make_float4(o[i][4], o[i][5], o[i][6], o[i][7]);
+            }
             __syncthreads();
-            if (q8 == 0)
-#pragma unroll 1
-                for (int k = 0; k < 7; ++k)
+            float sum = 0.f;   // a thread per request and dim
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 v = x[(k * 4 + i) * 128 + d4];
-                        o[i].x += v.x;
-                        o[i].y += v.y;
-                        o[i].z += v.z;
-                        o[i].w += v.w;
-                    }
+            for (int k = 0; k < 16; ++k) sum += ((float *)so)[(k * 2) * DK + tid];
+            __syncthreads();
+            ((float *)so)[tid] = sum;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[i][e] = q16 == 0 ? ((float *)so)[i * DK + d8 * 8 + e] : 0.f;
             __syncthreads();
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = few ? 4 * q8 + i : j0 + dj * i;   // (few: the other groups bring rows of zeros)
-            if (few && q8 > 0) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            uint32_t h0, l0, h1, l1;
-            split2(o[i].x, o[i].y, h0, l0);
-            split2(o[i].z, o[i].w, h1, l1);
-            *(uint2 *)(so + j * JPITCH + d4 * 8) = make_uint2(h0, h1);
-            *(uint2 *)(so + (JB + j) * JPITCH + d4 * 8) = make_uint2(l0, l1);
-            // the log-sum-exp's q_lo term: this warp's 128 dims
-            float dot = o[i].x * __uint_as_float(ql[i].x << 16) + o[i].y * __uint_as_float(ql[i].x & 0xffff0000u);
-            dot += o[i].z * __uint_as_float(ql[i].y << 16) + o[i].w * __uint_as_float(ql[i].y & 0xffff0000u);
+        for (int i = 0; i < 2; ++i) {
+            const int j = few ? 2 * q16 + i : j0 + dj * i;   // (few: the other groups bring rows of zeros)
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split2(o[i][2 * e], o[i][2 * e + 1], hi[e], lo[e]);
+            uint4 *x = (uint4 *)(so + (d8 >> 3) * JBLK + j * 128 + (((d8 ^ j) & 7) << 4));   // 128-byte swizzle
+            x[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            x[8 * JBLK / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            // the log-sum-exp's q_lo term: this warp's 256 dims
+            const uint32_t q[4] = {ql[i].x, ql[i].y, ql[i].z, ql[i].w};
+            float dot = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                dot += o[i][2 * e] * __uint_as_float(q[e] << 16) + o[i][2 * e + 1] * __uint_as_float(q[e] & 0xffff0000u);
             dot = warp_sum(dot);
-            if (lane == 0) sd[warp & 3][j] = dot;
+            if (lane == 0) sd[warp & 1][j] = dot;
         }
-        ok = ok && mbar_wait(&bar, 0, (volatile int *)&abort, &g_paged_tc_err);   // W_V is here
+        fence_proxy_async_smem();
+        tc_fence_before();
         __syncthreads();
-        if (tid < nb)
-            p.lse[(long)(b0 + tid) * p.H + h] = sl[tid] + p.scale * ((sd[0][tid] + sd[1][tid]) + (sd[2][tid] + sd[3][tid]));
-        float d[4][4] = {};
-        const int kq = warp >> 3, v0 = (warp & 7) * 16 + g;
-        const uint8_t *wa = sm + v0 * JPITCH + (128 * kq + 16 * t) * 2, *ob = so + g * JPITCH + (128 * kq + 16 * t) * 2;
+        if (tid < nb) p.lse[(long)(b0 + tid) * p.H + h] = sl[tid] + p.scale * (sd[0][tid] + sd[1][tid]);
+        if (warp == 0) {
+            ok = __all_sync(FULL, ok && mbar_wait(&v0.bar_w, 0, (volatile int *)&v0.abort, &g_paged_tc_err));   // W_V is here
+            tc_fence_after();
+            if (ok && elect_one()) {
+                const uint64_t a = sdesc_kmajor(sm), b = sdesc_kmajor(so);
+                constexpr uint32_t idesc = idesc_f16(128, JB, false);
 #pragma unroll 1
-        for (int i = 0; i < 4 && ok; ++i) {   // 16-byte pieces of the lane's dims: two of either 64
-            const int at = (i >> 1) * 128 + (i & 1) * 16;
-            const uint4 x = *(const uint4 *)(wa + at), y = *(const uint4 *)(wa + 8 * JPITCH + at);
-            const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
+                for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                if (8 * n >= nb) break;
-                const uint4 bh = *(const uint4 *)(ob + 8 * n * JPITCH + at), bl = *(const uint4 *)(ob + (JB + 8 * n) * JPITCH + at);
-                mma_16816(d[n], a0, bh.x, bh.y);
-                mma_16816(d[n], a0, bl.x, bl.y);
-                mma_16816(d[n], a1, bh.z, bh.w);
-                mma_16816(d[n], a1, bl.z, bl.w);
+                    for (int q = 0; q < 4; ++q) {
+                        const uint64_t ai = a + (uint64_t)(i * (16384 >> 4) + 2 * q), bi = b + (uint64_t)(i * (JBLK >> 4) + 2 * q);
+                        mma_ss(tmem, ai, bi, idesc, (i | q) != 0);
+                        mma_ss(tmem, ai, bi + (8 * JBLK >> 4), idesc, 1);
+                    }
+                mma_commit(&v0.bar_d);
             }
+            __syncwarp();
         }
-        // d[n][..]: value dims v0, v0 + 8, requests 8 n + 2t, + 1; the quarters meet where o was
-        __syncthreads();
-        float *ss = (float *)so + (2 * t) * 132 + v0;   // [quarter][request][128 dims + pad]
-        if (kq > 0)
+        float *ss = (float *)(sm + JW);   // out [request][128 dims + pad], where the weights were
+        if (warp < 4) {
+            ok = __all_sync(FULL, ok && mbar_wait(&v0.bar_d, ph, (volatile int *)&v0.abort, &g_paged_tc_err));
+            tc_fence_after();
+            uint32_t v[32];
+            tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16), v);
+            tmem_ld_wait();
+            tc_fence_before();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) ss[((kq - 1) * JB + 8 * (e >> 2) + (e & 1)) * 132 + 8 * (e >> 1 & 1)] = d[e >> 2][e & 3];
+            for (int j = 0; j < JB; ++j) ss[j * 132 + tid] = __uint_as_float(v[j]);
+        }
         __syncthreads();
-        if (kq == 0)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float *x = ss + (8 * (e >> 2) + (e & 1)) * 132 + 8 * (e >> 1 & 1);
-                x[0] += d[e >> 2][e & 3] + (x[JB * 132] + x[2 * JB * 132]);
-            }
-        __syncthreads();
-        if (warp < nb && ok) {
-            const float4 v = *(const float4 *)((float *)so + warp * 132 + lane * 4);
+        if (warp < nb) {   // (an abandoned wait leaves rubbish here, and the error word)
+            const float4 v = *(const float4 *)(ss + warp * 132 + lane * 4);
             *(uint2 *)((bf16 *)p.out + ((long)(b0 + warp) * p.H + h) * DV + lane * 4) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
         }
         __syncthreads();
     }
+    if (warp == 1) tmem_dealloc(tmem, 32);
 }
 
 // --------------------------------------------------------------------- attention ----
@@ -1202,6 +1229,12 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     if ((e = cudaFuncSetAttribute(paged_absorb_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM)) != cudaSuccess)
         return e;
     if ((e = cudaFuncSetAttribute(paged_join_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, JSMEM)) != cudaSuccess) return e;
+    CUtensorMap mW;
+    {
+        const ull d[2] = {DK, (ull)p.H * (DN + DV)}, s[1] = {DK * 2};
+        const unsigned b[2] = {64, DV};
+        if ((e = make_tma_map(&mW, p.w, 2, d, s, b)) != cudaSuccess) return e;
+    }
     const int per_head = std::max(1, std::min((p.B + JB - 1) / JB, 2 * p.workers / p.H));   // one wave of join blocks
     auto attn = p.H <= 64 ? (unit == 64   ? paged_attn_tc_kernel<64, true>
                              : unit == 32 ? paged_attn_tc_kernel<32, true>
@@ -1225,7 +1258,7 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     {
         ProfScope ps("paged_join", st);
-        e = launch_after(paged_join_tc_kernel, (unsigned)(p.H * per_head), JNT, JSMEM, st, p, (const bf16 *)ab.qlo, per_head);
+        e = launch_after(paged_join_tc_kernel, (unsigned)(p.H * per_head), JNT, JSMEM, st, mW, p, (const bf16 *)ab.qlo, per_head);
     }
     return e;
 }
