@@ -1145,6 +1145,9 @@ mla_status paged_decode_shape(const mla_dims *d, mla_dtype dt, int B, int page_s
         p->min_tiles = 1;
     }
     p->row_tiles = (p->H + p->row_tile - 1) / p->row_tile;
+    // a worker counts its tiles in 32 bits
+    if ((long)B * p->row_tiles * (((long)max_pages * page_size + p->tile - 1) / p->tile) > (long)INT_MAX * p->workers)
+        return MLA_ERR_SHAPE;
     return MLA_OK;
 }
 

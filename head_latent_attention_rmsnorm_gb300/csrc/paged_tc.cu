@@ -132,7 +132,7 @@ __device__ void rotate_queries(const Absorb &a, int i, int lane) {
 }
 
 __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_constant__ Absorb a) {
-    extern __shared__ __align__(16) uint8_t sm[];
+    extern __shared__ __align__(1024) uint8_t sm[];
     const PagedDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();

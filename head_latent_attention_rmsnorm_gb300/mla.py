@@ -565,8 +565,9 @@ def lse_combine(part_out, part_lse, *, out_dtype=torch.float32, out=None, lse=No
 
 
 # ------------------------------------------------------------------- paged cache ----
-# A serving step makes these three calls for every layer, and a small step's kernels last a few
+# A serving step makes these calls for every layer, and a small step's kernels last a few
 # microseconds: the checks are one expression per tensor, and only a failed one finds out why.
+# The library launches on the current device: a call on another one's tensors makes that current.
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
@@ -581,18 +582,6 @@ def _need(name: str, t, shape: tuple, dtype: torch.dtype, index: int) -> int:
         raise TypeError("%s: expected a torch.Tensor, got %s" % (name, type(t).__name__))
     _expect(name, t, math.prod(shape), dtype, torch.device("cuda", index))
     raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), shape))
-
-
-def _launch(index: int, stream, fn, where: str, *args) -> None:
-    """The call with the tensors' device current (the library launches on the current device; the
-    default stream is that device's current one)."""
-    if index == _current_device():
-        st = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
-    else:
-        with torch.cuda.device(index):
-            st = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
-    if st != 0:
-        raise MlaError(st, where)
 
 
 class PagedTables(NamedTuple):
@@ -631,12 +620,20 @@ def paged_tables(past_lens, new_lens, free_pages, block_table, *, page_size, n_t
     if counts is None:
         counts = torch.empty(2, dtype=i32, device=dev)
     rows, at = (B,), block_table.get_device()
-    _launch(at, stream, lib().mla_paged_tables, "mla_paged_tables", B, page_size, max_pages, n_free, n_tokens,
-            _need("past_lens", past_lens, rows, i32, at), _need("new_lens", new_lens, rows, i32, at),
-            _need("free_pages", free_pages, (n_free,), i32, at),
-            _need("block_table", block_table, (B, max_pages), i32, at), _need("kv_lens", kv_lens, rows, i32, at),
-            _need("cu_tokens", cu_tokens, (B + 1,), i32, at), _need("slots", slots, (n_tokens,), i32, at),
-            _need("positions", positions, (n_tokens,), i32, at), _need("counts", counts, (2,), i32, at))
+    if at != _current_device():
+        with torch.cuda.device(at):
+            return paged_tables(past_lens, new_lens, free_pages, block_table, page_size=page_size, n_tokens=n_tokens,
+                                kv_lens=kv_lens, cu_tokens=cu_tokens, slots=slots, positions=positions, counts=counts,
+                                stream=stream)
+    st = lib().mla_paged_tables(
+        B, page_size, max_pages, n_free, n_tokens, _need("past_lens", past_lens, rows, i32, at),
+        _need("new_lens", new_lens, rows, i32, at), _need("free_pages", free_pages, (n_free,), i32, at),
+        _need("block_table", block_table, (B, max_pages), i32, at), _need("kv_lens", kv_lens, rows, i32, at),
+        _need("cu_tokens", cu_tokens, (B + 1,), i32, at), _need("slots", slots, (n_tokens,), i32, at),
+        _need("positions", positions, (n_tokens,), i32, at), _need("counts", counts, (2,), i32, at),
+        _raw_stream(at) if stream is None else _stream(stream))
+    if st != 0:
+        raise MlaError(st, "mla_paged_tables")
     return PagedTables(kv_lens, cu_tokens, slots, positions, counts)
 
 
@@ -680,9 +677,15 @@ def paged_append(d: Dims, c_kv, k_pe, rms_w, slots, positions, c_cache, kpe_cach
     cs = _rows("c_kv", c_kv, n, d.d_kv, tdt, at)
     ks = _rows("k_pe", k_pe, n, d.d_rope, tdt, at)
     rows, i32 = (n,), torch.int32
-    _launch(at, stream, lib().mla_paged_append, "mla_paged_append", d, dt, n, num_pages, page, c_kv.data_ptr(), cs,
-            k_pe.data_ptr(), ks, _need("rms_w", rms_w, (d.d_kv,), tdt, at), _need("slots", slots, rows, i32, at),
-            _need("positions", positions, rows, i32, at), cp, kp)
+    if at != _current_device():
+        with torch.cuda.device(at):
+            return paged_append(d, c_kv, k_pe, rms_w, slots, positions, c_cache, kpe_cache, stream=stream)
+    st = lib().mla_paged_append(
+        d, dt, n, num_pages, page, c_kv.data_ptr(), cs, k_pe.data_ptr(), ks, _need("rms_w", rms_w, (d.d_kv,), tdt, at),
+        _need("slots", slots, rows, i32, at), _need("positions", positions, rows, i32, at), cp, kp,
+        _raw_stream(at) if stream is None else _stream(stream))
+    if st != 0:
+        raise MlaError(st, "mla_paged_append")
     return c_cache, kpe_cache
 
 
@@ -705,6 +708,10 @@ def paged_decode(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens
     B, H, i32 = q_nope.shape[0], d.n_heads, torch.int32
     max_pages = block_table.shape[1]
     num_pages, page, cp, kp = _cache(d, c_cache, kpe_cache, tdt, at)
+    if at != _current_device():
+        with torch.cuda.device(at):
+            return paged_decode(d, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, w_kv_b, out=out, lse=lse,
+                                workspace=workspace, stream=stream)
     if not isinstance(w_kv_b, torch.Tensor):
         raise TypeError("w_kv_b: expected a torch.Tensor, got %s" % type(w_kv_b).__name__)
     _expect("w_kv_b", w_kv_b, H * (d.d_nope + d.d_v) * d.d_kv, tdt, dev)
@@ -719,7 +726,10 @@ def paged_decode(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens
         workspace = paged_decode_workspace(d, c_cache, block_table)
     else:
         _workspace(0, dev, workspace)
-    _launch(at, stream, lib().mla_paged_decode, "mla_paged_decode", d, dt, B, num_pages, page, max_pages, *ptrs,
-            _need("out", out, (B, H, d.d_v), tdt, at), _need("lse", lse, (B, H), torch.float32, at), _ptr(workspace),
-            workspace.numel() * workspace.element_size())
+    st = lib().mla_paged_decode(
+        d, dt, B, num_pages, page, max_pages, *ptrs, _need("out", out, (B, H, d.d_v), tdt, at),
+        _need("lse", lse, (B, H), torch.float32, at), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _raw_stream(at) if stream is None else _stream(stream))
+    if st != 0:
+        raise MlaError(st, "mla_paged_decode")
     return out, lse

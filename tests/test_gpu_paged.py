@@ -272,7 +272,7 @@ def test_decode_junk_behind_the_end(junk, heads, dtype):
     check(*decode_case(DS, heads, dtype, [1, 37, 90, 81], 64, junk=junk))
 
 
-@pytest.mark.parametrize("heads,dtype", [(16, BF16), (16, F32)])
+@pytest.mark.parametrize("heads,dtype", [(16, BF16), (40, BF16), (128, BF16), (16, F32)])
 def test_decode_nan_key_is_seen(heads, dtype):
     """A NaN in a key that is attended to reaches its request's results, and no other's."""
     d, t = decode_case(DS, heads, dtype, [40, 40], 8)
@@ -320,6 +320,69 @@ def test_decode_same_bits_and_untouched_inputs():
             assert torch.equal(a, b)
     for a, b in zip(keep, dev):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dims,heads,dtype,page", [(DS, 128, BF16, 64), (DS, 130, BF16, 16), (DS, 5, BF16, 8), (DS, 7, F32, 3),
+                                                   (ODD, 17, BF16, 4)])
+def test_decode_writes_its_outputs_only(dims, heads, dtype, page):
+    """Outputs and a workspace of exactly the queried size, inside buffers whose other bytes stay."""
+    lens = [150, 0, 1, 333, 64, 65, 7]
+    d, t = decode_case(dims, heads, dtype, lens, page)
+    dev = [x.cuda() for x in t]
+    want = mla.paged_decode(d, *dev)
+    n = mla.paged_decode_workspace(d, dev[2], dev[4]).numel()
+    room = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+
+    def inside(shape, ty):
+        x = torch.full((math.prod(shape) + 512,), 7.0, dtype=ty, device="cuda")
+        return x, x[256:256 + math.prod(shape)].view(shape)
+
+    ob, out = inside((len(lens), heads, d.d_v), dtype)
+    lb, lse = inside((len(lens), heads), F32)
+    mla.paged_decode(d, *dev, out=out, lse=lse, workspace=room[4096:4096 + n])
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert bool((room[:4096] == 0xA5).all()) and bool((room[4096 + n:] == 0xA5).all())
+    for x in (ob, lb):
+        assert bool((x[:256] == 7).all()) and bool((x[-256:] == 7).all())
+
+
+def test_far_pages():
+    """Slots whose element and byte offsets pass 2^31 and 2^32: written and attended to at a large
+    cache's end, the pages at its start holding others' tokens."""
+    d = mla.dims(16, **DS)
+    pages, page = 140000, 64                       # 4.6e9 latent elements
+    c = torch.empty(pages, page, 512, dtype=BF16, device="cuda")
+    k = torch.empty(pages, page, 64, dtype=BF16, device="cuda")
+    ids = [pages - 1, 3, pages - 70, 70000, pages - 2]
+    c[[3, 70000]], k[[3, 70000]] = 0, 0
+    g = ref.generator(31)
+    n = 4 * page + 9
+    x = torch.randn(n, 576, generator=g).to(BF16)
+    w_norm = torch.ones(512, dtype=BF16)
+    table = torch.tensor([ids], dtype=torch.int32)
+    slots = [ids[p // page] * page + p % page for p in range(n)]
+    mla.paged_append(d, x.cuda()[:, :512], x.cuda()[:, 512:], w_norm.cuda(), i32(slots), i32(list(range(n))), c, k)
+    q, r, w = ref.queries(g, d, BF16, 1)
+    lens = torch.tensor([n], dtype=torch.int32)
+    out, lse = mla.paged_decode(d, q.cuda(), r.cuda(), c, k, table.cuda(), lens.cuda(), w.cuda())
+    cc, kk = c[ids].cpu(), k[ids].cpu()
+    y = ref.rmsnorm(x[:, :512], w_norm, d.rms_eps)
+    assert float((cc.view(-1, 512)[:n].double() - y).abs().max()) <= 2.0 ** -8 * float(y.abs().max()) * 1.01
+    ref.check_decode(BF16, out, lse, ref.decode(d, q, r, cc, kk, torch.arange(5, dtype=torch.int32)[None], lens, w))
+    del c, k
+    # the CUDA-core kernels, fp32
+    d = mla.dims(2, **TINY)
+    pages, page = 40_000_000 // 5, 5               # 2.6e9 latent elements
+    c = torch.empty(pages, page, 64, device="cuda")
+    k = torch.empty(pages, page, 16, device="cuda")
+    ids = [pages - 1, 1, pages - 5]
+    x = torch.randn(13, 80, generator=g)
+    slots = [ids[p // page] * page + p % page for p in range(13)]
+    mla.paged_append(d, x.cuda()[:, :64], x.cuda()[:, 64:], torch.ones(64, device="cuda"), i32(slots), i32(list(range(13))), c, k)
+    q, r, w = ref.queries(g, d, F32, 1)
+    lens = torch.tensor([13], dtype=torch.int32)
+    out, lse = mla.paged_decode(d, q.cuda(), r.cuda(), c, k, i32([ids]), lens.cuda(), w.cuda())
+    ref.check_decode(F32, out, lse, ref.decode(d, q, r, c[ids].cpu(), k[ids].cpu(), torch.arange(3, dtype=torch.int32)[None], lens, w))
 
 
 def test_decode_batch_of_none():
