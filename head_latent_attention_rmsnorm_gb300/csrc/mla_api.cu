@@ -1161,8 +1161,8 @@ size_t paged_decode_ws(PagedDecode *p, void *base) {
         p->first = (int *)c.take((size_t)p->workers * 2 * sizeof(int));
         p->spans = (int2 *)c.take((size_t)p->B * p->row_tiles * sizeof(int2));
     }
-    p->qabs = c.take(rows * p->Dk * 4);
-    p->qpe = c.take(rows * p->Dr * 4);
+    p->qabs = c.take(rows * p->Dk * (p->tc ? 6 : 4));   // (three bf16 parts, or fp32)
+    p->qpe = c.take(rows * p->Dr * (p->tc ? 6 : 4));
     if (p->tc) {
         p->po = (__half *)c.take(slots * p->row_tile * p->Dk * 2);
         p->pscale = (float *)c.take(slots * p->row_tile * 2 * 4);

@@ -11,29 +11,45 @@
 //
 // Attention.  One work item = 128 heads (fewer rows are zero-filled) of one request; its fp32
 // accumulator, 128 x 512, is a whole SM's tensor memory, so an item runs on two SMs:
-//   rank 0 (scores): q_hi in TMEM; 80-key tiles of the cache (latent + key band) through a
-//     two-deep TMA ring that fills and drains in three groups of 64-dim blocks; S = Q K^T, two
-//     S buffers; online softmax by eight warps (two threads per head); P in bf16 to rank 1 by bulk
-//     copies into its two P slots;
-//   rank 1 (accumulator): O in TMEM; streams the same tiles' latent (L2 hits: an idle warp
-//     prefetches rank 0's next tiles) and issues O += P C.
-// The persistent walk matters: equal shares of tiles per cluster (a request may be cut anywhere,
-// parts meet in the join) leave no wave tail, and the next request's queries and first score tiles
-// run under the previous one's drain and epilogue.
+//   rank 0 (scores): the queries in TMEM; 64-key tiles of the cache (latent + key band) through a
+//     two-deep TMA ring that fills and drains in three groups of 64-dim blocks, a producer warp for
+//     each; S = Q K^T, two S buffers; online softmax by eight warps (two threads per head); P in
+//     bf16 to rank 1 by bulk copies into its two P slots;
+//   rank 1 (accumulator): O in TMEM; streams the same tiles' latent in halves of 256 dims (L2 hits:
+//     an idle warp prefetches rank 0's next tiles) and issues O += P C.
+// The walk is persistent: equal shares of whole tiles per cluster (a request may be cut between any
+// two tiles, parts meet in the join) leave no wave tail.  Between parts the next request's query boxes
+// land in the key stages, in flight at once, while the softmax and rank 1 finish.
 //
-// Pages.  A tile is ten groups of eight rows; TMA boxes of 8 or 16 rows never cross a page.  The
-// map's 4-D view {64 dims, 8 rows, 8 blocks, row groups} lands each 8 x 64 block as one 1024-byte
-// swizzle atom with constant strides between atoms, which one matrix descriptor per 64 dims covers.
-// Groups behind the request's end and pages with a bad id load out of bounds (zeros); rows behind
-// the end inside a group are set to zero in shared memory before P C reads them (whatever they
-// held, 0 * NaN included), and their scores are masked.
+// What bounds it.  64 ragged requests of up to 32768 keys, 128 heads: the attention 275-285 us, 0.96 us
+// per tile and pair of SMs, 5.3-5.5 TB/s; 16 heads 5.8-5.9 TB/s; without its MMAs the kernel moves 6.6
+// TB/s (the copy peak is 6.8).  Per tile the shared memory of rank 0 takes 74 KB of boxes, gives the
+// score MMAs 80 KB (N = 64 reads 2 KB per 16 cycles of tensor work, the port's whole width) and
+// turns P over, about 1500 of the tile's 1840 cycles; rank 1's 64 KB in, 96 KB to the MMAs (P once per
+// 256 dims) and P in, about 1400.  Sixteen more score MMAs a tile (256 cycles) cost 0.14 us a tile.
 //
-// Precision.  The score product takes q_hi; the band's lo half has MMAs of its own, and the missing
-// latent term shifts a part's log-sum-exp by scale q_lo . o to first order, which the epilogue
-// adds (the second order is half the variance of scale q_lo . c_j, ~1e-6 at unit scale).  q_lo
-// keeps q to 2^-17.  P is bf16 (relative 2^-8 on the weights of an average; the sums take the
+// Pages.  A unit is the largest power of two of rows, up to a tile, that divides the page (8, 16, 32
+// or 64): a TMA box per unit and group never crosses a page.  The map's 4-D view {64 dims, 8 rows, 8
+// blocks, row groups} lands each 8 x 64 block as one 1024-byte swizzle atom with constant strides
+// between atoms, which one matrix descriptor per 64 dims covers.  Units behind the request's end and
+// pages with a bad id load out of bounds (zeros).  Rank 1 takes a request's last tile by groups of
+// eight rows, with zeros behind the end's group, and sets the rows behind the end in that group to
+// zero in shared memory before P C reads them (whatever they held, 0 * NaN included); rank 0's scores
+// of them are masked.
+//
+// Precision.  P is bf16 (relative 2^-9 on average, on the weights of an average; the sums take the
 // unrounded ones); up to 64 heads, what that rounding leaves goes through the idle rows 64 on, at no
-// cost in MMAs.  Partials are fp16 with a power of two per half row.
+// cost in MMAs.  q and the rotated band are bf16 pairs, hi + lo to 2^-17.  The scores take q_hi and
+// both halves of the band.  q_lo's latent part shifts a part's log-sum-exp by scale q_lo . o to first
+// order, which the join adds (the second order is half the variance of scale q_lo . c_j, ~1e-6 at unit
+// scale), and its weights by a relative 2^-9, like P's own rounding.  Where both count, it is taken in
+// part: above 64 heads and up to 4096 keys (EX_LATENT) q_lo of 128 of the 512 dims has MMAs, for
+// which tensor memory has the room.  Measured as the output's error over that of an fp32
+// evaluation rounded to bf16, 128 heads: 2000 keys 1.51 -> 1.43, 100 keys 1.54 -> 1.48; 12000 keys
+// without it 1.45, since an average over more keys rounds better (16 heads: 1.26-1.43 throughout).  Up
+// to 64 keys (EX_BAND) the log-sum-exp is small and bf16 pairs show in it: the band's third part has
+// MMAs and the join adds the latent's (1 to 3 keys: 1.5e-6 -> 8e-7 of its value).  Partials are fp16
+// with a power of two per half row.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -81,6 +97,21 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     hi = pack_bf16(x, y);
     lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
 }
+// the same, and what lo leaves
+__device__ __forceinline__ void split3(float x, float y, uint32_t &hi, uint32_t &lo, uint32_t &rest) {
+    hi = pack_bf16(x, y);
+    x -= __uint_as_float(hi << 16);
+    y -= __uint_as_float(hi & 0xffff0000u);
+    split2(x, y, lo, rest);
+}
+
+// What a request's scores and log-sum-exp take of the queries besides q_hi and the band's hi and lo
+// (the header's part on precision).
+enum Extra { EX_NONE, EX_LATENT, EX_BAND };
+constexpr int SHORT_KEYS = 64, MIDDLE_KEYS = 4096;
+__device__ __forceinline__ Extra extra_of(bool paired, int keys) {
+    return keys <= SHORT_KEYS ? EX_BAND : (!paired && keys <= MIDDLE_KEYS ? EX_LATENT : EX_NONE);
+}
 
 // ------------------------------------------------------------------------ absorb ----
 // q[b, h, :] = W_K(h)^T q_nope[b, h, :]: streams 16 KB x heads x 8 of weights for B x 128 x 512
@@ -88,13 +119,15 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
 // products run on mma.sync (M = latent dims, N = requests: eight per step, no padding to 128
 // rows).  Block (head, 128 latent dims, group of up to 64 requests): the weight block and the group's
 // queries by cp.async, all in flight at once; the weights then stay in registers as A fragments.
+// 128 heads, events around it alone: one request 10 us, 64 requests 20 us (17 MB of weights, 2.5 us at the copy
+// peak; 19 MB of queries out).
 constexpr int AB_DIMS = 128, AB_PITCH = 256 + 16, AB_GROUP = 64;
 constexpr int AB_OUT = 40;              // halves per request of a warp's staging (32 dims + pad)
-constexpr int AB_SMEM = DN * AB_PITCH + AB_GROUP * AB_PITCH + 4 * 2 * 8 * AB_OUT * 2;
+constexpr int AB_SMEM = DN * AB_PITCH + AB_GROUP * AB_PITCH + 4 * 3 * 8 * AB_OUT * 2 + AB_GROUP * 4;
 
 struct Absorb {
     PagedDecode p;
-    bf16 *qhi, *qlo, *rhi, *rlo;   // [B][H][512], [B][H][64]
+    bf16 *qhi, *qlo, *qrest, *rhi, *rlo, *rrest;   // [B][H][512], [B][H][64]; the rests of short requests only
     int groups, group;             // groups of `group` requests
     int rot_blocks;                // blocks 1 .. rot_blocks rotate the queries; block 0 divides the batch
     Turns64 turns;
@@ -105,7 +138,8 @@ __device__ void rotate_queries(const Absorb &a, int i, int lane) {
     const PagedDecode &p = a.p;
     const int per = (p.H + 31) / 32, b = i / per, h0 = i % per * 32;
     if (b >= p.B) return;
-    const float2 cs = turn_cs(a.turns.v[lane], keys_of(p, b) - 1);
+    const int keys = keys_of(p, b);
+    const float2 cs = turn_cs(a.turns.v[lane], keys - 1);
     const int h1 = min(h0 + 32, p.H);
 #pragma unroll 1
     for (int h = h0; h < h1; h += 8) {
@@ -121,12 +155,16 @@ __device__ void rotate_queries(const Absorb &a, int i, int lane) {
             if (h + j >= h1) break;
             const long o = ((long)b * p.H + h + j) * DR + lane;
             const float f0 = __uint_as_float((uint32_t)x0[j] << 16), f1 = __uint_as_float((uint32_t)x1[j] << 16);
-            uint32_t hi, lo;
-            split2(f0 * cs.x - f1 * cs.y, f1 * cs.x + f0 * cs.y, hi, lo);
+            uint32_t hi, lo, rest;
+            split3(f0 * cs.x - f1 * cs.y, f1 * cs.x + f0 * cs.y, hi, lo, rest);
             ((uint16_t *)a.rhi)[o] = (uint16_t)hi;
             ((uint16_t *)a.rhi)[o + 32] = (uint16_t)(hi >> 16);
             ((uint16_t *)a.rlo)[o] = (uint16_t)lo;
             ((uint16_t *)a.rlo)[o + 32] = (uint16_t)(lo >> 16);
+            if (keys <= SHORT_KEYS) {
+                ((uint16_t *)a.rrest)[o] = (uint16_t)rest;
+                ((uint16_t *)a.rrest)[o + 32] = (uint16_t)(rest >> 16);
+            }
         }
     }
 }
@@ -156,6 +194,8 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
 #pragma unroll 4
     for (int i = tid; i < DN * (AB_DIMS / 8); i += 128)
         cp16(sw + (i >> 4) * AB_PITCH + (i & 15) * 16, w + (long)(i >> 4) * DK + (i & 15) * 8);
+    int *keys = (int *)(sm + AB_SMEM) - AB_GROUP;
+    if (tid < nb) keys[tid] = keys_of(p, b0 + tid);
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     uint32_t A[2][8][4];
@@ -166,7 +206,8 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
         for (int s = 0; s < 8; ++s)   // matrices: (dims 0-7, k 0-7), (dims 8-15, k 0-7), the same of k 8-15
             ldsm4_t(A[m][s], smem_u32(sw + (16 * s + (mi >> 1) * 8 + r) * AB_PITCH + (warp * 32 + m * 16 + (mi & 1) * 8) * 2));
     const int g = lane >> 2, t = lane & 3;
-    uint16_t *sh = (uint16_t *)(sq + AB_GROUP * AB_PITCH) + warp * 2 * 8 * AB_OUT, *sl = sh + 8 * AB_OUT;
+    uint16_t *sh = (uint16_t *)(sq + AB_GROUP * AB_PITCH) + warp * 3 * 8 * AB_OUT, *sl = sh + 8 * AB_OUT,
+             *sr = sl + 8 * AB_OUT;
 #pragma unroll 1
     for (int b = 0; b < nb; b += 8) {   // (rows behind the group's last request are not read back)
         float d[2][4] = {};
@@ -185,19 +226,22 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                uint32_t hi, lo;
-                split2(d[m][2 * e], d[m][2 * e + 1], hi, lo);
+                uint32_t hi, lo, rest;
+                split3(d[m][2 * e], d[m][2 * e + 1], hi, lo, rest);
                 const int dim = 16 * m + 8 * e + g;
                 sh[(2 * t) * AB_OUT + dim] = (uint16_t)hi;
                 sh[(2 * t + 1) * AB_OUT + dim] = (uint16_t)(hi >> 16);
                 sl[(2 * t) * AB_OUT + dim] = (uint16_t)lo;
                 sl[(2 * t + 1) * AB_OUT + dim] = (uint16_t)(lo >> 16);
+                sr[(2 * t) * AB_OUT + dim] = (uint16_t)rest;
+                sr[(2 * t + 1) * AB_OUT + dim] = (uint16_t)(rest >> 16);
             }
         __syncwarp();
         if (b + g < nb) {   // 8 requests x 64 bytes: a 16-byte piece per lane
             const long o = ((long)(b0 + b + g) * p.H + h) * DK + dc * AB_DIMS + warp * 32 + t * 8;
             *(uint4 *)(a.qhi + o) = *(const uint4 *)(sh + g * AB_OUT + t * 8);
             *(uint4 *)(a.qlo + o) = *(const uint4 *)(sl + g * AB_OUT + t * 8);
+            if (keys[b + g] <= SHORT_KEYS) *(uint4 *)(a.qrest + o) = *(const uint4 *)(sr + g * AB_OUT + t * 8);
         }
         __syncwarp();
     }
@@ -210,7 +254,8 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
 // weights; the merge runs over 16 groups of 64 threads (a thread per eight latent dims), which share
 // out the requests, or, for one or two requests, their parts; the product is tcgen05 (M = 128 value
 // dims, N = 32 requests, o as bf16 hi + lo, so that it is as exact as fp32 o): 64 MMAs of 32
-// columns, where mma.sync took 7500 cycles a group.
+// columns, where mma.sync took 7500 cycles a group.  128 heads, events around it alone: one request
+// 14 us, 64 requests 27 us (33 with mma.sync).
 constexpr int JB = 32, JNT = 1024, JMAXC = 80;
 constexpr int JO = DV * DK * 2;                // W_V: eight boxes of 64 dims x 128 rows
 constexpr int JBLK = JB * 128;                 // o: 64 dims x 32 requests
@@ -218,7 +263,7 @@ constexpr int JW = JO + 2 * 8 * JBLK;          // o hi, o lo; before them the gr
 constexpr int JV = JW + 2 * JB * JMAXC * 4;    // the parts' weights for either half of the dims; then out [request][132]
 struct JoinVars {
     uint64_t bar_w, bar_d;
-    int sc[JB][2];            // first part, number of parts
+    int sc[JB][3];            // first part, number of parts, Extra
     float sl[JB], sd[2][JB];  // log-sum-exp without the q_lo term; the warps' shares of q_lo . o
     uint32_t tslot;
     int abort;
@@ -229,7 +274,7 @@ static_assert(PAGED_TC_WORKERS <= JMAXC && JMAXC <= 96, "parts of an item");
 
 __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_constant__ CUtensorMap mW,
                                                                const __grid_constant__ PagedDecode p, const bf16 *qlo,
-                                                               int per_head) {
+                                                               const bf16 *qrest, int per_head) {
     extern __shared__ __align__(1024) uint8_t sm[];
     if (smem_u32(sm) & 1023) {   // no room to align by hand; the same answer in every block
         if (threadIdx.x == 0) atomicOr(&g_paged_tc_err, 2u);
@@ -277,8 +322,9 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
             ql[i] = j < nb ? __ldcg((const uint4 *)(qlo + ((long)(b0 + j) * p.H + h) * DK) + d8) : make_uint4(0, 0, 0, 0);
         }
         {   // a warp per request: the weights of its parts (up to 96)
-            int s0 = 0, n = 0;
+            int s0 = 0, n = 0, ex = EX_NONE;
             if (warp < nb) {
+                ex = extra_of(p.H <= 64, keys_of(p, b0 + warp));
                 const int2 sp = __ldcg(p.spans + (long)(b0 + warp) * p.row_tiles + rt);
                 s0 = sp.x;
                 n = sp.y;
@@ -313,6 +359,7 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
             if (lane == 0) {
                 sc[warp][0] = s0;
                 sc[warp][1] = n;
+                sc[warp][2] = ex;
                 sl[warp] = s == 0.f ? -INFINITY : m + logf(s);
             }
         }
@@ -388,6 +435,14 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 dot += o[i][2 * e] * __uint_as_float(q[e] << 16) + o[i][2 * e + 1] * __uint_as_float(q[e] & 0xffff0000u);
+            if (sc[j][2] == EX_LATENT && d8 < 16) dot = 0.f;   // the scores have it
+            if (sc[j][2] == EX_BAND && j < nb) {
+                const uint4 x = __ldcg((const uint4 *)(qrest + ((long)(b0 + j) * p.H + h) * DK) + d8);
+                const uint32_t z[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    dot += o[i][2 * e] * __uint_as_float(z[e] << 16) + o[i][2 * e + 1] * __uint_as_float(z[e] & 0xffff0000u);
+            }
             dot = warp_sum(dot);
             if (lane == 0) sd[warp & 1][j] = dot;
         }
@@ -440,10 +495,9 @@ constexpr int NGRP = NK / 8;            // row groups of a tile
 constexpr int KST = 2, KGRP = 3;        // rank 0: tile stages, block groups of a stage
 constexpr int VSL = 4;                  // rank 1: slots of half a tile (256 latent dims)
 constexpr int NPB = 2;                  // P slots of rank 1 = staging slots of rank 0
-#ifndef PFD
-#define PFD 4
-#endif
-constexpr int PF = PFD;                 // tiles prefetched into L2 ahead of rank 1's loads
+// tiles prefetched into L2 ahead of rank 1's loads (76 requests of 32000 keys: 1 tile 526 us, 3 and 4
+// 520, 6 527, 10 656)
+constexpr int PF = 4;
 constexpr uint32_t ATOM = 1024;
 // rank 0 stage: groups of 64-dim blocks {0-2}, {3-5}, {6-7}, each [row group][block][8 rows], then the
 // key band [row group][8 rows]
@@ -454,8 +508,8 @@ constexpr uint32_t VHALF = NGRP * 4 * ATOM;   // [row group][block][8 rows]
 constexpr uint32_t P_BYTES = 16384;
 constexpr uint32_t X_ALPHA = 0, X_INVL = 512, X_LSE = 1024, X_FLAG = 1536, X_BYTES = X_FLAG + 16;
 constexpr uint32_t XOFF = P_BYTES, XSLOT = 18432, EXT_STRIDE = 1664;
-// rank 0: key stages (between parts: query boxes 0-8), query box 9, P staging, extras, row maxima [tile parity][half][row], row sums
-constexpr uint32_t OFF_Q = KST * KSTAGE, OFF_STG = OFF_Q + 16384, OFF_EXT = OFF_STG + NPB * P_BYTES;
+// rank 0: key stages (between parts: query boxes 0-8), two more query boxes, P staging, extras, row maxima [tile parity][half][row], row sums
+constexpr uint32_t OFF_Q = KST * KSTAGE, OFF_STG = OFF_Q + 2 * 16384, OFF_EXT = OFF_STG + NPB * P_BYTES;
 constexpr uint32_t OFF_RED = OFF_EXT + NPB * EXT_STRIDE, OFF_SUM = OFF_RED + 2 * 2 * ROWS * 4;
 // rank 1: latent slots, P slots, 1/l of each row for the epilogue's other warps [part parity][row], the
 // epilogue's transposes (4 KB a warp)
@@ -463,12 +517,12 @@ constexpr uint32_t OFF_PB = VSL * VHALF, OFF_INV = OFF_PB + NPB * XSLOT, OFF_OUT
 constexpr uint32_t END0 = OFF_SUM + 2 * ROWS * 4, END1 = OFF_OUT + 8 * 4096;
 constexpr uint32_t OFF_BAR = END0 > END1 ? END0 : END1;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 512;
-constexpr uint32_t T_S = 0, T_Q = 2 * NK;   // rank 0's TMEM columns: S buffers; 32 per 64 query dims (10 blocks)
+constexpr uint32_t T_S = 0, T_Q = 2 * NK;   // rank 0's TMEM columns: S buffers; 32 per 64 query dims (hi 0-7, band hi and lo, EX_LATENT's lo 0-1 or EX_BAND's rest)
 constexpr float RESCALE_LOG2 = 8.0f;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 static_assert(KSTAGE % 1024 == 0 && OFF_STG % 1024 == 0 && OFF_PB % 1024 == 0 && XSLOT % 1024 == 0, "swizzle atoms");
 static_assert(XOFF + X_BYTES <= XSLOT && X_BYTES <= EXT_STRIDE && OFF_EXT % 16 == 0, "P transfer layout");
-static_assert(T_Q + 320 <= 512, "TMEM budget of rank 0");
+static_assert(T_Q + 12 * 32 <= 512, "TMEM budget of rank 0");
 static_assert(5 * 16384 >= KSTAGE && 9 * 16384 <= KST * KSTAGE, "query boxes in the key stages");
 // Barriers, by index; the same places in both CTAs.
 enum : int {
@@ -501,11 +555,12 @@ __device__ __forceinline__ uint32_t arrivals(int i) {
 struct Maps {
     CUtensorMap k3, k2, v, r;   // boxes of a unit's rows: blocks 0-2 / 3-5, blocks 6-7, four blocks, key band
     CUtensorMap v8;             // eight rows, four blocks
-    CUtensorMap qh, rh, rl;     // queries [B][H][512], [B][H][64] twice
+    CUtensorMap qh, ql, rh, rl, rr; // queries [B][H][512] and [B][H][64]: hi, lo, rest
 };
 struct Attn {
     PagedDecode p;
     int q_rows;                 // rows of the query boxes
+    const bf16 *qlo;
     Divisor by_page;
     float scale_log2;
     uint32_t idesc_s, idesc_pv;
@@ -614,7 +669,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
-    if (warp == 2 && lane < 8) tma_prefetch_desc((const CUtensorMap *)&m + lane);
+    if (warp == 2 && lane < 10) tma_prefetch_desc((const CUtensorMap *)&m + lane);
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // both CTAs' barriers exist before any cross-CTA arrival
@@ -682,6 +737,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             bool ok = true;
             for (; more && ok; next(), ++seg) {
                 ok = wait_all(&bars[B_QREADY], seg & 1, ctl);
+                const Extra ex = extra_of(paired, w.keys);
 #pragma unroll 1
                 for (int i = 0; i < w.nt && ok; ++i, ++n) {
                     if ((n & 1) != s) continue;
@@ -693,15 +749,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                         if (!ok) break;
                         tc_fence_after();
                         if (elect_one()) {
-                            // blocks of 64 dims: latent 0-7 (q_hi), then the key band twice (hi, lo)
+                            // blocks of 64 dims: latent 0-7 (q_hi; the first two also with q_lo), then the key band
+                            // twice (hi, lo) or three times
                             uint64_t d = sdesc_sw128(base + g * KG1, 16, (g < 2 ? 3 : 2) * ATOM);
-                            const int j1 = g < 2 ? 3 * g + 3 : 10;
+                            const int j1 = g < 2 ? 3 * g + 3 : (ex == EX_BAND ? 11 : 10);
 #pragma unroll 1
                             for (int j = 3 * g; j < j1; ++j) {
                                 if (j >= 8) d = sdesc_sw128(base + KG3, 16, ATOM);
 #pragma unroll
                                 for (int q = 0; q < 4; ++q)
                                     mma_ts(dt, tmem + T_Q + j * 32 + q * 8, d + 2 * q, a.idesc_s, (j | q) != 0);
+                                if (ex == EX_LATENT && j < 2) {
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) mma_ts(dt, tmem + T_Q + (10 + j) * 32 + q * 8, d + 2 * q, a.idesc_s, 1);
+                                }
                                 d += ATOM >> 4;
                             }
                             mma_commit(&bars[B_GEMPTY + s * KGRP + g]);
@@ -851,18 +912,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             }
         } else if (warp == 18) {
             // ------------------------------- the parts' query boxes: 64 dims x 128 heads each, hi of the latent
-            // (0-7), hi and lo of the band (8, 9), all in flight at once in the key stages, which the
-            // last part's MMAs have left
+            // (0-7), hi and lo of the band (8, 9), Extra's (10); all in flight at once in the key stages, which
+            // the last part's MMAs have left, and the two boxes behind them
             int seg = 0;
             bool go = lane == 0;
             for (; more && go; next(), ++seg) {
+                const Extra ex = extra_of(paired, w.keys);
+                const int boxes = ex == EX_NONE ? 10 : 11;
                 go = wait_for(&bars[B_QFREE], (seg & 1) ^ 1, ctl);   // (passes at first)
                 if (!go) break;
-                mbar_arrive_expect_tx(&bars[B_QFULL], 10 * 128 * a.q_rows);
+                mbar_arrive_expect_tx(&bars[B_QFULL], boxes * 128 * a.q_rows);
 #pragma unroll 1
-                for (int j = 0; j < 10; ++j)
-                    tma_load_3d(smem + (j < 9 ? j * 16384 : OFF_Q), j < 8 ? &m.qh : (j == 8 ? &m.rh : &m.rl), &bars[B_QFULL],
-                                j < 8 ? 64 * j : 0, w.rt * ROWS, w.b);
+                for (int j = 0; j < boxes; ++j) {
+                    const CUtensorMap *map = j < 8 ? &m.qh : (j == 8 ? &m.rh : (j == 9 ? &m.rl : (ex == EX_BAND ? &m.rr : &m.ql)));
+                    tma_load_3d(smem + (j < 9 ? j * 16384 : OFF_Q + (j - 9) * 16384), map, &bars[B_QFULL], j < 8 ? 64 * j : 0,
+                                w.rt * ROWS, w.b);
+                }
             }
         } else {
             // ------------------------------- queries into TMEM (warps 14-17, a thread per head)
@@ -872,11 +937,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             bool ok = true;
             for (; more && ok; next(), ++seg) {
                 const bool act = w.rt * ROWS + quad * 32 < p.H;
+                const Extra ex = extra_of(paired, w.keys);
+                const int boxes = ex == EX_NONE ? 10 : 11;
+                // q_lo of dims 64-127 has no box: each thread's 128 bytes come straight from memory, under
+                // the boxes' flight
+                uint4 x[8];
+                if (ex == EX_LATENT && act) {
+                    const bf16 *src = a.qlo + ((long)w.b * p.H + min(w.rt * ROWS + row, p.H - 1)) * DK + 64;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = __ldcg((const uint4 *)src + e);
+                }
                 ok = wait_all(&bars[B_QFULL], seg & 1, ctl);
                 tc_fence_after();   // (the boxes landed behind the commit of the last part's MMAs)
+                if (ex == EX_LATENT && act && ok) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        v[4 * e] = x[e].x;
+                        v[4 * e + 1] = x[e].y;
+                        v[4 * e + 2] = x[e].z;
+                        v[4 * e + 3] = x[e].w;
+                    }
+                    tmem_st32(dst + 11 * 32, v);
+                }
 #pragma unroll 1
-                for (int j = 0; j < 10 && ok; ++j) {
-                    const uint8_t *box = smem + (j < 9 ? j * 16384 : OFF_Q) + row * 128;
+                for (int j = 0; j < boxes && ok; ++j) {
+                    const uint8_t *box = smem + (j < 9 ? j * 16384 : OFF_Q + (j - 9) * 16384) + row * 128;
                     uint32_t v[32];
                     if (act) {
 #pragma unroll
@@ -1187,8 +1273,10 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     ab.p = p;
     ab.qhi = (bf16 *)p.qabs;
     ab.qlo = ab.qhi + heads * DK;
+    ab.qrest = ab.qlo + heads * DK;
     ab.rhi = (bf16 *)p.qpe;
     ab.rlo = ab.rhi + heads * DR;
+    ab.rrest = ab.rlo + heads * DR;
     // at least two blocks per SM, where the batch has that many groups of eight
     const int want = (2 * 152 + 4 * p.H - 1) / (4 * p.H), most = (p.B + 7) / 8;
     ab.groups = std::max((p.B + AB_GROUP - 1) / AB_GROUP, std::min(want, most));
@@ -1201,6 +1289,7 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     int unit = NK;   // rows that always share a page: the largest power of two up to a tile that divides one
     while (p.page % unit) unit /= 2;
     at.q_rows = std::min(ROWS, (p.H + 31) / 32 * 32);
+    at.qlo = ab.qlo;
     Maps m{};
     {
         const ull d[4] = {64, 8, 8, rows / 8}, s[3] = {1024, 128, 8192}, dr[2] = {64, rows}, sr[1] = {128};
@@ -1217,9 +1306,11 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
         const unsigned bq[3] = {64, (unsigned)at.q_rows, 1};
         const ull d[3] = {DK, (ull)p.H, (ull)p.B}, s[2] = {DK * 2, (ull)p.H * DK * 2};
         if ((e = make_tma_map(&m.qh, ab.qhi, 3, d, s, bq)) != cudaSuccess) return e;
+        if ((e = make_tma_map(&m.ql, ab.qlo, 3, d, s, bq)) != cudaSuccess) return e;
         const ull dr[3] = {DR, (ull)p.H, (ull)p.B}, sr[2] = {DR * 2, (ull)p.H * DR * 2};
         if ((e = make_tma_map(&m.rh, ab.rhi, 3, dr, sr, bq)) != cudaSuccess) return e;
         if ((e = make_tma_map(&m.rl, ab.rlo, 3, dr, sr, bq)) != cudaSuccess) return e;
+        if ((e = make_tma_map(&m.rr, ab.rrest, 3, dr, sr, bq)) != cudaSuccess) return e;
     }
     at.p = p;
     at.by_page = divisor(p.page);
@@ -1258,7 +1349,8 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     {
         ProfScope ps("paged_join", st);
-        e = launch_after(paged_join_tc_kernel, (unsigned)(p.H * per_head), JNT, JSMEM, st, mW, p, (const bf16 *)ab.qlo, per_head);
+        e = launch_after(paged_join_tc_kernel, (unsigned)(p.H * per_head), JNT, JSMEM, st, mW, p, (const bf16 *)ab.qlo,
+                         (const bf16 *)ab.qrest, per_head);
     }
     return e;
 }
