@@ -7,6 +7,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "mla_internal.h"
 #include "paged.h"
 
@@ -188,6 +190,22 @@ __device__ void plan_block(const PagedDecode &p, int *sm = nullptr, int room = 0
     __syncthreads();
     if (near) plan_parts<NT>(p, sm, carry * p.row_tiles);
     else plan_parts<NT>(p, p.tile_off, carry * p.row_tiles);
+}
+
+// Started early, behind the kernel in front of it (programmatic dependent launch).
+template <typename... Par, typename... Arg>
+cudaError_t launch_after(void (*kern)(Par...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, Arg &&...arg) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Arg>(arg)...);
 }
 
 }  // namespace paged

@@ -8,11 +8,14 @@
 #include <algorithm>
 
 #include "paged_common.cuh"
+#include "tc_common.cuh"
 
 namespace mla {
 namespace {
 
 using namespace paged;
+using tc::pdl_launch_dependents;
+using tc::pdl_wait;
 
 constexpr int NT = 256;         // threads
 constexpr int HT = 16;          // heads per work item
@@ -33,6 +36,7 @@ __global__ void __launch_bounds__(NT) paged_absorb_simt_kernel(const __grid_cons
     extern __shared__ float sm[];   // q [BT][Dn], sums [8 warps][BT][DC]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int groups = (p.B + BT - 1) / BT, chunks = (p.Dk + DC - 1) / DC;
+    pdl_launch_dependents();
     if (blockIdx.x == 0) {
         plan_block<NT>(p);
         return;
@@ -102,16 +106,30 @@ __host__ __device__ inline Lay layout(int Dq) {
     l.k = HT * l.dqp;
     l.s = l.k + KT * l.dqp;
     l.flag = l.s + 8 * HT * KT;
-    l.total = l.flag + KT + 3 * HT;
+    l.total = l.flag + 2 * KT + 3 * HT;
     return l;
 }
 
-__device__ __forceinline__ float4 load4(const float *p) { return __ldg((const float4 *)p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 x = __ldg((const uint2 *)p);
-    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
-                       __uint_as_float(x.y & 0xffff0000u));
-}
+template <typename T>
+struct Four;   // four elements as they are loaded
+template <>
+struct Four<float> {
+    float4 x;
+    __device__ __forceinline__ void load(const float *p) { x = __ldg((const float4 *)p); }
+    __device__ __forceinline__ void zero() { x = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ float4 f() const { return x; }
+};
+template <>
+struct Four<__nv_bfloat16> {
+    uint2 x;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { x = __ldg((const uint2 *)p); }
+    __device__ __forceinline__ void zero() { x = make_uint2(0, 0); }
+    __device__ __forceinline__ float4 f() const {
+        return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                           __uint_as_float(x.y & 0xffff0000u));
+    }
+};
+constexpr int KR = KT / (NT / 32), KC = DQ_MAX / 4 / 32;   // rows of a tile per warp, groups of four per lane
 
 template <typename T>
 __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_constant__ PagedDecode p) {
@@ -119,9 +137,11 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
     const int Dq = p.Dk + p.Dr;
     const Lay L = layout(Dq);
     float *sQ = sm + L.q, *sK = sm + L.k, *sS = sm + L.s;
-    int *sRow = (int *)(sm + L.flag);                   // the keys' cache rows, -1 = no key
-    float *sM = sm + L.flag + KT, *sL = sM + HT, *sA = sL + HT;   // running maximum, sum, rescale
+    int *sRow = (int *)(sm + L.flag);                   // the keys' cache rows, -1 = no key; by parity of the tile
+    float *sM = sm + L.flag + 2 * KT, *sL = sM + HT, *sA = sL + HT;   // running maximum, sum, rescale
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_launch_dependents();
+    pdl_wait();
     const long total = p.tile_off[p.B] * p.row_tiles;
     const long q = share_of(p, total);
     long t = blockIdx.x * q;
@@ -135,15 +155,67 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
         const long k0 = (t - first * p.row_tiles) % per;        // first tile of the item here
         const long k1 = min(per, k0 + tend - t);
         const int keys = keys_of(p, b), h0 = rt * HT, nh = min(HT, p.H - h0);
-        __syncthreads();
-        for (int i = tid; i < HT * L.dqp; i += NT) {
-            const int h = i / L.dqp, d = i % L.dqp;
-            float v = 0.f;
-            if (h < nh && d < Dq) {
-                const long row = (long)b * p.H + h0 + h;
-                v = d < p.Dk ? ((const float *)p.qabs)[row * p.Dk + d] : ((const float *)p.qpe)[row * p.Dr + d - p.Dk];
+        // the rows of tile kt's keys
+        auto look_up = [&](long kt) {
+            if (tid < KT) {
+                int row = -1;
+                const long key = kt * KT + tid;
+                if (key < keys) {
+                    const int id = p.table[(long)b * p.max_pages + (int)key / p.page];
+                    if (id >= 0 && id < p.num_pages) row = id * p.page + (int)key % p.page;
+                }
+                sRow[(kt & 1) * KT + tid] = row;
             }
-            sQ[i] = v;
+        };
+        // tile kt into registers: rows of whole groups of four, a lane per group, a warp's rows and groups
+        // all in flight
+        const int ck = p.Dk / 4, c4 = ck + p.Dr / 4;
+        Four<T> v[KR][KC];
+        auto fetch = [&](long kt) {
+#pragma unroll
+            for (int k = 0; k < KR; ++k) {
+                const int row = sRow[(kt & 1) * KT + warp + 8 * k];
+#pragma unroll
+                for (int c = 0; c < KC; ++c) {
+                    const int i = lane + 32 * c;
+                    v[k][c].zero();
+                    if (row >= 0 && i < c4)
+                        v[k][c].load(i < ck ? (const T *)p.c_cache + (long)row * p.Dk + 4 * i
+                                            : (const T *)p.kpe_cache + (long)row * p.Dr + 4 * (i - ck));
+                }
+            }
+        };
+        __syncthreads();   // the previous item has been read
+        look_up(k0);
+        __syncthreads();
+        if (four) fetch(k0);
+        if (four) {
+            constexpr int QN = (HT * DQ_MAX / 4 + NT - 1) / NT;   // ten groups a thread, in flight at once
+            float4 x[QN];
+#pragma unroll
+            for (int k = 0; k < QN; ++k) {
+                const int i = tid + k * NT, h = i / c4, d = i % c4;
+                const long row = (long)b * p.H + h0 + h;
+                x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (h < nh)
+                    x[k] = __ldcg((const float4 *)(d < ck ? (const float *)p.qabs + row * p.Dk + 4 * d
+                                                          : (const float *)p.qpe + row * p.Dr + 4 * (d - ck)));
+            }
+#pragma unroll
+            for (int k = 0; k < QN; ++k) {
+                const int i = tid + k * NT, h = i / c4, d = i % c4;
+                if (h < HT) *(float4 *)(sQ + h * L.dqp + 4 * d) = x[k];
+            }
+        } else {
+            for (int i = tid; i < HT * L.dqp; i += NT) {
+                const int h = i / L.dqp, d = i % L.dqp;
+                float v = 0.f;
+                if (h < nh && d < Dq) {
+                    const long row = (long)b * p.H + h0 + h;
+                    v = d < p.Dk ? ((const float *)p.qabs)[row * p.Dk + d] : ((const float *)p.qpe)[row * p.Dr + d - p.Dk];
+                }
+                sQ[i] = v;
+            }
         }
         if (tid < HT) {
             sM[tid] = -INFINITY;
@@ -153,41 +225,17 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
 #pragma unroll
         for (int h = 0; h < HT; ++h) o[h][0] = o[h][1] = 0.f;
         for (long kt = k0; kt < k1; ++kt) {
-            const int key0 = (int)kt * KT;
+            const int *rows = sRow + (kt & 1) * KT;
             __syncthreads();   // the previous tile has been read
-            if (tid < KT) {
-                int row = -1;
-                const int key = key0 + tid;
-                if (key < keys) {
-                    const int id = p.table[(long)b * p.max_pages + key / p.page];
-                    if (id >= 0 && id < p.num_pages) row = id * p.page + key % p.page;
-                }
-                sRow[tid] = row;
-            }
-            __syncthreads();
-            if (four) {   // rows of whole groups of four: a lane per group, a warp's four rows in flight
-                const int ck = p.Dk / 4, cr = p.Dr / 4;
-                for (int i0 = lane; i0 < ck + cr; i0 += 64) {
-                    float4 v[KT / 8][2];
+            if (four) {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
+                for (int k = 0; k < KR; ++k)
 #pragma unroll
-                        for (int k = 0; k < KT / 8; ++k) {
-                            const int row = sRow[warp + 8 * k], i = i0 + 32 * q;
-                            v[k][q] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (row >= 0 && i < ck + cr)
-                                v[k][q] = i < ck ? load4((const T *)p.c_cache + (long)row * p.Dk + 4 * i)
-                                                 : load4((const T *)p.kpe_cache + (long)row * p.Dr + 4 * (i - ck));
-                        }
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int k = 0; k < KT / 8; ++k)
-                            if (i0 + 32 * q < ck + cr) *(float4 *)(sK + (warp + 8 * k) * L.dqp + 4 * (i0 + 32 * q)) = v[k][q];
-                }
+                    for (int c = 0; c < KC; ++c)
+                        if (lane + 32 * c < c4) *(float4 *)(sK + (warp + 8 * k) * L.dqp + 4 * (lane + 32 * c)) = v[k][c].f();
             } else {
                 for (int k = warp; k < KT; k += NT / 32) {   // a warp per key row; absent keys as zeros
-                    const int row = sRow[k];
+                    const int row = rows[k];
                     const T *c = (const T *)p.c_cache + (long)row * p.Dk, *r = (const T *)p.kpe_cache + (long)row * p.Dr;
                     for (int d = lane; d < L.dqp; d += 32) {
                         float v = 0.f;
@@ -196,7 +244,9 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
                     }
                 }
             }
+            if (kt + 1 < k1) look_up(kt + 1);
             __syncthreads();
+            if (four && kt + 1 < k1) fetch(kt + 1);   // under this tile's products
             {
                 const int hg = lane >> 3, kg = lane & 7;   // heads 4 hg .., keys kg, kg + 8, ..
                 float acc[4][4] = {};
@@ -226,7 +276,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
                 float s = 0.f;
 #pragma unroll
                 for (int w = 0; w < NT / 32; ++w) s += sS[(w * HT + h) * KT + lane];
-                s = sRow[lane] >= 0 ? s * p.scale : -INFINITY;
+                s = rows[lane] >= 0 ? s * p.scale : -INFINITY;
                 float m = s;
 #pragma unroll
                 for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
@@ -278,8 +328,9 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
 }
 
 // -------------------------------------------------------------------------- join ----
-// Block (head, VC value dims, group of BT requests): the parts' weights, their merge (a thread per
-// latent dim and two requests), then a warp per four rows of W_V.
+// Block (head, VC value dims, group of BT requests): four rows of W_V per warp into registers, before
+// the attention ends; the parts' weights; their merge (a thread per four latent dims of a request, eight
+// parts in flight); the product.
 constexpr int JP = 160;   // parts of an item at most (the workers)
 
 template <typename T>
@@ -295,6 +346,15 @@ __global__ void __launch_bounds__(NT) paged_join_simt_kernel(const __grid_consta
     u /= chunks;
     const int h = u / groups, b0 = (u % groups) * BT, nb = min(BT, p.B - b0);
     const int rt = h / p.row_tile, r = h % p.row_tile;
+    constexpr int WN = DK_MAX / 32;
+    const int v0 = ch * VC + warp * 4;
+    const T *w = (const T *)p.w + ((long)h * (p.Dn + p.Dv) + p.Dn + v0) * p.Dk + lane;
+    T wr[4][WN];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < WN; ++i) wr[k][i] = v0 + k < p.Dv && lane + 32 * i < p.Dk ? w[(long)k * p.Dk + 32 * i] : from_f<T>(0.f);
+    pdl_wait();
     if (warp < BT) {
         const int b = b0 + warp;
         long s0 = 0;
@@ -327,27 +387,54 @@ __global__ void __launch_bounds__(NT) paged_join_simt_kernel(const __grid_consta
         }
     }
     __syncthreads();
-    for (int i = tid; i < BT * p.Dk; i += NT) {
-        const int j = i / p.Dk, d = i % p.Dk;
-        const float *po = p.po32 + (ss[j] * p.row_tile + r) * p.Dk + d;
-        const long pitch = (long)p.row_tile * p.Dk;
-        float o = 0.f;
+    const long pitch = (long)p.row_tile * p.Dk;
+    if (p.Dk % 4 == 0) {
+        const int d4 = p.Dk / 4;
+        for (int i = tid; i < BT * d4; i += NT) {
+            const int j = i / d4, n = sn[j];
+            const float *po = p.po32 + (ss[j] * p.row_tile + r) * p.Dk + i % d4 * 4;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int c = 0; c < n; c += 8) {
+                float4 x[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (c + u < n) x[u] = __ldcg((const float4 *)(po + (c + u) * pitch));
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (c + u < n) {
+                        const float f = sw[j][c + u];
+                        o.x = fmaf(f, x[u].x, o.x);
+                        o.y = fmaf(f, x[u].y, o.y);
+                        o.z = fmaf(f, x[u].z, o.z);
+                        o.w = fmaf(f, x[u].w, o.w);
+                    }
+            }
+            *(float4 *)(sm + 4 * i) = o;
+        }
+    } else {
+        for (int i = tid; i < BT * p.Dk; i += NT) {
+            const int j = i / p.Dk, d = i % p.Dk;
+            const float *po = p.po32 + (ss[j] * p.row_tile + r) * p.Dk + d;
+            float o = 0.f;
 #pragma unroll 4
-        for (int c = 0; c < sn[j]; ++c) o = fmaf(sw[j][c], po[c * pitch], o);
-        sm[i] = o;
+            for (int c = 0; c < sn[j]; ++c) o = fmaf(sw[j][c], po[c * pitch], o);
+            sm[i] = o;
+        }
     }
     __syncthreads();
-    const int v0 = ch * VC + warp * 4;
-    const T *w = (const T *)p.w + ((long)h * (p.Dn + p.Dv) + p.Dn + v0) * p.Dk;
     float acc[4][BT] = {};
-#pragma unroll 4
-    for (int d = lane; d < p.Dk; d += 32)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float x = v0 + k < p.Dv ? to_f<T>(w[(long)k * p.Dk + d]) : 0.f;
+    for (int i = 0; i < WN; ++i) {
+        const int d = lane + 32 * i;
+        if (d < p.Dk)
 #pragma unroll
-            for (int j = 0; j < BT; ++j) acc[k][j] = fmaf(x, sm[j * p.Dk + d], acc[k][j]);
-        }
+            for (int j = 0; j < BT; ++j) {
+                const float x = sm[j * p.Dk + d];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[k][j] = fmaf(to_f<T>(wr[k][i]), x, acc[k][j]);
+            }
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -376,14 +463,14 @@ cudaError_t decode_simt(const PagedDecode &p, cudaStream_t st) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     {
         ProfScope ps("paged_attn", st);
-        paged_attn_simt_kernel<T><<<p.workers, NT, s2, st>>>(p);
+        e = launch_after(paged_attn_simt_kernel<T>, (unsigned)p.workers, NT, s2, st, p);
     }
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
     {
         ProfScope ps("paged_join", st);
-        paged_join_simt_kernel<T><<<jblocks, NT, s3, st>>>(p);
+        e = launch_after(paged_join_simt_kernel<T>, jblocks, NT, s3, st, p);
     }
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace

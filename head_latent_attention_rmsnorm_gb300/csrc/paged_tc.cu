@@ -1244,21 +1244,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <typename... Par, typename... Arg>
-cudaError_t launch_after(void (*kern)(Par...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, Arg &&...arg) {
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, std::forward<Arg>(arg)...);
-}
-
 }  // namespace
 
 bool paged_tc_supported(int Dk, int Dn, int Dr, int Dv, int page) {
