@@ -4,7 +4,11 @@
 // Three launches: absorb (q_abs = W_K^T q_nope, the query's rotation, the division of the batch
 // among the workers), attention (each worker walks its key tiles with the running maximum and sum
 // of the softmax and writes one normalised partial per request it met), join (the partials'
-// log-sum-exp merge and out = W_V o).
+// log-sum-exp merge and out = W_V o), the latter two launched early.  16 heads of 512 + 64 dims, fp32: 4
+// ragged requests of up to 1000 keys 23.5 us (one tile per worker: three launches' latency; 46 before the
+// loads of queries, tiles, parts and W_V went out together), 16 requests of 3000 keys 101 us: 8 us a
+// tile, in which shared-memory reads take about twice the time of the 557 thousand multiply-adds.  512
+// threads take 8.8 us a tile (registers for the next tile's loads run out), the same otherwise.
 #include <algorithm>
 
 #include "paged_common.cuh"
@@ -95,17 +99,26 @@ __global__ void __launch_bounds__(NT) paged_absorb_simt_kernel(const __grid_cons
 // --------------------------------------------------------------------- attention ----
 // Scores: 16 heads x 32 keys of a tile; the 640 query dims are cut among the 8 warps in chunks of
 // four, each lane holding 4 heads x 4 keys, and the warps' sums meet in shared memory (eight
-// 16-byte shared loads feed 64 FMAs).  Values: a thread owns two latent dims of every head.
+// 16-byte shared loads feed 64 FMAs).  Values: a thread owns two latent dims of every head, for one of up to
+// four groups of the tile's keys, whose sums meet at the item's end (16 requests of 3000 keys at 64 + 16
+// dims, bf16: 48 us with one group, 41 with four).
 struct Lay {   // shared memory, in floats
     int dqp, q, k, s, flag, total;
+    int per, groups;   // threads and number of the groups
 };
-__host__ __device__ inline Lay layout(int Dq) {
+__host__ __device__ inline Lay layout(int Dk, int Dr) {
     Lay l;
+    const int Dq = Dk + Dr;
+    l.per = 64;
+    while (2 * l.per < Dk) l.per *= 2;
+    l.groups = NT / l.per;
     l.dqp = (Dq + 3) / 4 * 4 + 4;   // row pitch: rows four banks apart
     l.q = 0;
     l.k = HT * l.dqp;
     l.s = l.k + KT * l.dqp;
-    l.flag = l.s + 8 * HT * KT;
+    l.flag = l.s + NT / 32 * HT * KT;
+    const int meet = NT * HT * 2;   // the groups' sums, over the rest
+    if (l.flag < meet) l.flag = meet;
     l.total = l.flag + 2 * KT + 3 * HT;
     return l;
 }
@@ -135,7 +148,7 @@ template <typename T>
 __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_constant__ PagedDecode p) {
     extern __shared__ float sm[];
     const int Dq = p.Dk + p.Dr;
-    const Lay L = layout(Dq);
+    const Lay L = layout(p.Dk, p.Dr);
     float *sQ = sm + L.q, *sK = sm + L.k, *sS = sm + L.s;
     int *sRow = (int *)(sm + L.flag);                   // the keys' cache rows, -1 = no key; by parity of the tile
     float *sM = sm + L.flag + 2 * KT, *sL = sM + HT, *sA = sL + HT;   // running maximum, sum, rescale
@@ -146,7 +159,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
     const long q = share_of(p, total);
     long t = blockIdx.x * q;
     const long tend = min(t + q, total);
-    const int chunks = (Dq + 3) / 4;
+    const int chunks = (Dq + 3) / 4, grp = tid / L.per, d = tid % L.per * 2;   // group, first latent dim
     const bool four = p.Dk % 4 == 0 && p.Dr % 4 == 0;
     while (t < tend) {
         const int b = request_of(p, p.tile_off, t);
@@ -250,6 +263,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
             {
                 const int hg = lane >> 3, kg = lane & 7;   // heads 4 hg .., keys kg, kg + 8, ..
                 float acc[4][4] = {};
+#pragma unroll 2
                 for (int c = warp; c < chunks; c += NT / 32) {
                     float4 q[4], k[4];
 #pragma unroll
@@ -298,11 +312,12 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
                 o[h][0] *= sA[h];
                 o[h][1] *= sA[h];
             }
-            if (2 * tid < p.Dk) {
-                for (int k = 0; k < KT; k += 4) {
+            if (d < p.Dk) {
+                const int n = KT / L.groups;
+                for (int k = grp * n; k < (grp + 1) * n; k += 4) {
                     float2 v[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = *(const float2 *)(sK + (k + j) * L.dqp + 2 * tid);
+                    for (int j = 0; j < 4; ++j) v[j] = *(const float2 *)(sK + (k + j) * L.dqp + d);
 #pragma unroll
                     for (int h = 0; h < HT; ++h) {
                         const float4 w = *(const float4 *)(sS + h * KT + k);
@@ -313,13 +328,30 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
             }
         }
         const long slot = (long)blockIdx.x + (long)b * p.row_tiles + rt;
-#pragma unroll
-        for (int h = 0; h < HT; ++h) {
+        float *po = p.po32 + slot * HT * p.Dk + d;
+        auto store = [&](int h, float x, float y) {
             const float inv = sL[h] == 0.f ? 0.f : 1.f / sL[h];
-            float *po = p.po32 + (slot * HT + h) * p.Dk + 2 * tid;
-            if (h < nh && 2 * tid < p.Dk) {
-                po[0] = o[h][0] * inv;
-                if (2 * tid + 1 < p.Dk) po[1] = o[h][1] * inv;
+            po[(long)h * p.Dk] = x * inv;
+            if (d + 1 < p.Dk) po[(long)h * p.Dk + 1] = y * inv;
+        };
+        if (L.groups == 1) {
+#pragma unroll
+            for (int h = 0; h < HT; ++h)
+                if (h < nh && d < p.Dk) store(h, o[h][0], o[h][1]);
+        } else {
+            __syncthreads();   // the last tile has been read
+            float2 *meet = (float2 *)sm + tid % L.per;
+#pragma unroll
+            for (int h = 0; h < HT; ++h) meet[(grp * HT + h) * L.per] = make_float2(o[h][0], o[h][1]);
+            __syncthreads();
+            for (int h = grp; h < nh && d < p.Dk; h += L.groups) {   // the groups share out the heads
+                float2 x = make_float2(0.f, 0.f);
+                for (int g = 0; g < L.groups; ++g) {
+                    const float2 y = meet[(g * HT + h) * L.per];
+                    x.x += y.x;
+                    x.y += y.y;
+                }
+                store(h, x.x, x.y);
             }
         }
         if (tid < nh) p.pl[slot * HT + tid] = sL[tid] == 0.f ? -INFINITY : sM[tid] + logf(sL[tid]);
@@ -450,7 +482,7 @@ cudaError_t decode_simt(const PagedDecode &p, cudaStream_t st) {
     std::copy_n(paged_turns(p.base, p.Dr), p.Dr / 2, turns.v);
     const unsigned units = (unsigned)((p.B + BT - 1) / BT) * (unsigned)p.H;
     const unsigned blocks = units * (unsigned)((p.Dk + DC - 1) / DC), jblocks = units * (unsigned)((p.Dv + VC - 1) / VC);
-    const size_t s1 = ((size_t)BT * p.Dn + (size_t)NT / 32 * BT * DC) * 4, s2 = (size_t)layout(p.Dk + p.Dr).total * 4, s3 = (size_t)BT * p.Dk * 4;
+    const size_t s1 = ((size_t)BT * p.Dn + (size_t)NT / 32 * BT * DC) * 4, s2 = (size_t)layout(p.Dk, p.Dr).total * 4, s3 = (size_t)BT * p.Dk * 4;
     cudaError_t e;
     if ((e = cudaFuncSetAttribute(paged_absorb_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1)) != cudaSuccess)
         return e;
