@@ -606,19 +606,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             for (int t = 0; t < nt && ok && g == 0; ++t) {
                 const int pb = t % NPB;
                 ok = __all_sync(FULL, mbar_wait_cluster(&p_full[pb], (t / NPB) & 1, abort, err));
+                // slot pb's previous use is over (its transfer waited for that): taken note of on every
+                // tile, so that the parity test below is at most one phase behind
+                ok = ok && (t < NPB || mbar_wait(&p_empty[pb], ((t / NPB) - 1) & 1, abort, err));
+                ok = __all_sync(FULL, ok);
                 if (!ok) break;
                 if (warp == 2 && lane == 0 && t + NPB < nt)   // arm the slot for tile t + NPB
                     mbar_arrive_expect_tx(&p_full[pb], P_BYTES + X_BYTES);
                 const uint8_t *xs = smem + OFF_PB + pb * XSLOT + XOFF;
                 const uint32_t *fl = (const uint32_t *)(xs + X_FLAG);
                 if ((fl[0] | fl[1] | fl[2] | fl[3]) != 0u) {   // the same answer in every thread
-                    // O must hold tile t - 1's product before it is rescaled.  Slot q's
-                    // previous phase is waited for first, so the parity test is never
-                    // two phases behind.
+                    // O must hold tile t - 1's product before it is rescaled
                     const int q = (t - 1) % NPB, k = (t - 1) / NPB;
-                    bool gw = k == 0 || mbar_wait(&p_empty[q], (k - 1) & 1, abort, err);
-                    gw = gw && mbar_wait(&p_empty[q], k & 1, abort, err);
-                    ok = __all_sync(FULL, gw);
+                    ok = __all_sync(FULL, mbar_wait(&p_empty[q], k & 1, abort, err));
                     if (!ok) break;
                     tc_fence_after();
                     const float a = ((const float *)(xs + X_ALPHA))[row];
