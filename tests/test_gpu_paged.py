@@ -295,6 +295,20 @@ def test_decode_growing_maximum(heads, dtype):
     check(d, t)
 
 
+@pytest.mark.parametrize("dims,heads,dtype,page", [(DS, 128, BF16, 16), (DS, 16, BF16, 64), (DS, 72, BF16, 8), (DS, 16, F32, 16),
+                                                   (TINY, 4, F32, 7)])
+@pytest.mark.parametrize("rise", [6.0, -6.0])
+def test_decode_rescaled_maximum(dims, heads, dtype, page, rise):
+    """Scores of tens, rising (the accumulator rescaled at most tiles, by more than 2^8) or falling."""
+    d, t = decode_case(dims, heads, dtype, [900, 333, 4500 if dims is DS else 70], page)
+    q, r, c, k, table, lens, w = t
+    for b, n in enumerate(lens.tolist()):
+        for p in range(n):
+            row = int(table[b, p // page]) * page + p % page
+            c.view(-1, d.d_kv)[row] *= 0.25 + abs(rise) * (p if rise > 0 else n - p) / n
+    check(d, t)
+
+
 def test_decode_shared_pages():
     """Requests whose first pages are the same ones (a shared prompt)."""
     d, t = decode_case(DS, 16, BF16, [200, 200, 200], 32)
