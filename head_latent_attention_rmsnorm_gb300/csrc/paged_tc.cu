@@ -473,8 +473,7 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
             ok = __all_sync(FULL, ok && mbar_wait(&v0.bar_d, ph, (volatile int *)&v0.abort, &g_paged_tc_err));
             tc_fence_after();
             uint32_t v[32];
-            tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16), v);
-            tmem_ld_wait();
+            tmem_ld32_wait(tmem + ((uint32_t)(warp * 32) << 16), v);
             tc_fence_before();
 #pragma unroll
             for (int j = 0; j < JB; ++j) ss[j * 132 + tid] = __uint_as_float(v[j]);
@@ -811,8 +810,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     tc_fence_after();
                     uint32_t sa[HK];
                     if (act) {
-                        tmem_ld32(sbase + s * NK, sa);
-                        tmem_ld_wait();
+                        tmem_ld32_wait(sbase + s * NK, sa);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -1129,8 +1127,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
                                 for (int cc = 0; cc < 16; ++cc) {
                                     uint32_t o[32];
-                                    tmem_ld32(lb + cc * 32, o);
-                                    tmem_ld_wait();
+                                    tmem_ld32_wait(lb + cc * 32, o);
 #pragma unroll
                                     for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
                                     tmem_st32(lb + cc * 32, o);
@@ -1164,8 +1161,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
                     for (int cc = 0; cc < 8; ++cc) {
                         uint32_t o[32];
-                        tmem_ld32(lb + 256 * g + 32 * cc, o);
-                        tmem_ld_wait();
+                        tmem_ld32_wait(lb + 256 * g + 32 * cc, o);
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             *(uint4 *)(buf + ((e ^ (lane & 7)) << 4)) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
@@ -1180,8 +1176,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
                     for (int cc = 0; cc < 8; ++cc) {
                         uint32_t o[32];
-                        tmem_ld32(lb + 256 * g + 32 * cc, o);
-                        tmem_ld_wait();
+                        tmem_ld32_wait(lb + 256 * g + 32 * cc, o);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) big = fmaxf(big, fabsf(__uint_as_float(o[e])));
                     }
@@ -1197,8 +1192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             uint32_t o[32];
-                            tmem_ld32(lb + 256 * g + 64 * cc + 32 * k, o);
-                            tmem_ld_wait();
+                            tmem_ld32_wait(lb + 256 * g + 64 * cc + 32 * k, o);
                             if (paired) {
                                 const uint8_t *lo = smem + OFF_OUT + (4 * g + quad) * 4096 + lane * 128;
                                 named_bar_sync(5 + 2 * quad + g, 64);
