@@ -22,11 +22,13 @@
 // land in the key stages, in flight at once, while the softmax and rank 1 finish.
 //
 // What bounds it.  64 ragged requests of up to 32768 keys, 128 heads: the attention 275-285 us, 0.96 us
-// per tile and pair of SMs, 5.3-5.5 TB/s; 16 heads 5.8-5.9 TB/s; without its MMAs the kernel moves 6.6
-// TB/s (the copy peak is 6.8).  Per tile the shared memory of rank 0 takes 74 KB of boxes, gives the
-// score MMAs 80 KB (N = 64 reads 2 KB per 16 cycles of tensor work, the port's whole width) and
-// turns P over, about 1500 of the tile's 1840 cycles; rank 1's 64 KB in, 96 KB to the MMAs (P once per
-// 256 dims) and P in, about 1400.  Sixteen more score MMAs a tile (256 cycles) cost 0.14 us a tile.
+// per tile and pair of SMs, 5.3-5.6 TB/s; 16 heads 5.8 TB/s; without its MMAs the kernel moves 6.6 TB/s
+// (the copy peak is 6.8).  No unit is full: of a tile's 1800 cycles rank 0's tensor pipe needs 1280
+// (40 MMAs of N = 64 with A in TMEM, 32 cycles each) and rank 1's 1024, DRAM runs at 71 %, L2 at 66 %,
+// shared memory below 50 %.  The MMAs' issue is part of the chain: one issuing warp takes 1.22 us a tile,
+// two 0.96.  Measured no faster: a ring of seven 24 KB slots instead of six, sixteen softmax warps of 16
+// keys, fully unrolled MMAs (all 0.95-0.98), 128-key steps with N = 128 (1.03), P written to rank 1 by the
+// softmax threads themselves (1.15), warp-uniform issue (1.05).
 //
 // Pages.  A unit is the largest power of two of rows, up to a tile, that divides the page (8, 16, 32
 // or 64): a TMA box per unit and group never crosses a page.  The map's 4-D view {64 dims, 8 rows, 8
@@ -603,10 +605,10 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Bounded waits.  A kernel of this file lasts milliseconds (every byte that the GPU holds, read once);
-// KERNEL_NS after its start a wait records the timeout and gives up, as does every other wait of the
-// CTA.
-constexpr uint64_t KERNEL_NS = 4000000000ull;
+// Bounded waits.  A tile takes about a microsecond; KERNEL_NS after the kernel's start and TILE_NS more
+// for each tile of its share (requests may share pages, so there is no bound on those) a wait records
+// the timeout and gives up, as does every other wait of the CTA.
+constexpr uint64_t KERNEL_NS = 4000000000ull, TILE_NS = 20000ull;
 struct Ctl {
     unsigned long long deadline;
     int abort;
@@ -680,6 +682,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     // this cluster's parts: a list from the division of the batch
     const PagedPart *part = p.parts + __ldcg(p.first + (blockIdx.x >> 1));
     const int n_all = __ldcg(p.first + p.workers + (blockIdx.x >> 1));   // tiles
+    if (tid == 0 && n_all > 0) ((volatile Ctl *)ctl)->deadline += TILE_NS * n_all;
     PagedPart w{};
     bool more = n_all > 0;
     auto load = [&]() {
