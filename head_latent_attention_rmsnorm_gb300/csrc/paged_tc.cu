@@ -26,9 +26,9 @@
 // (the copy peak is 6.8).  No unit is full: of a tile's 1800 cycles rank 0's tensor pipe needs 1280
 // (40 MMAs of N = 64 with A in TMEM, 32 cycles each) and rank 1's 1024, DRAM runs at 71 %, L2 at 66 %,
 // shared memory below 50 %.  The MMAs' issue is part of the chain: one issuing warp takes 1.22 us a tile,
-// two 0.96.  Measured no faster: a ring of seven 24 KB slots instead of six, sixteen softmax warps of 16
-// keys, fully unrolled MMAs (all 0.95-0.98), 128-key steps with N = 128 (1.03), P written to rank 1 by the
-// softmax threads themselves (1.15), warp-uniform issue (1.05).
+// two 0.96.  Measured no faster: a ring of seven 24 KB slots instead of six, a third P slot, sixteen
+// softmax warps of 16 keys, fully unrolled MMAs, and these together (all 0.94-0.98), 128-key steps with
+// N = 128 (1.03), P written to rank 1 by the softmax threads themselves (1.15), warp-uniform issue (1.05).
 //
 // Pages.  A unit is the largest power of two of rows, up to a tile, that divides the page (8, 16, 32
 // or 64): a TMA box per unit and group never crosses a page.  The map's 4-D view {64 dims, 8 rows, 8
