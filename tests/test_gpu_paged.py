@@ -417,6 +417,36 @@ def test_decode_on_another_stream():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("dims,heads,dtype,page", [(DS, 16, BF16, 16), (DS, 128, BF16, 64), (TINY, 4, F32, 5)])
+def test_decode_same_page_twice(dims, heads, dtype, page):
+    """A request whose table names one page several times: its keys count as often."""
+    d, t = decode_case(dims, heads, dtype, [5 * page, 3 * page + 2, 9], page)
+    t[4][0, 1:4] = t[4][0, 0]
+    t[4][1, 2] = t[4][0, 0]
+    check(d, t)
+
+
+@pytest.mark.parametrize("dims,heads,dtype,page", [(DS, 128, BF16, 64), (DS, 16, F32, 16)])
+def test_decodes_on_two_streams_at_once(dims, heads, dtype, page):
+    """Calls that run side by side, a workspace each, have the bits of calls alone."""
+    cases = [decode_case(dims, heads, dtype, lens, page, seed=k) for k, lens in enumerate(([1500, 3, 800, 64], [70] * 90))]
+    dev = [(d, [x.cuda() for x in t]) for d, t in cases]
+    want = [mla.paged_decode(d, *x) for d, x in dev]
+    ws = [mla.paged_decode_workspace(d, x[2], x[4]) for d, x in dev]
+    streams = [torch.cuda.Stream() for _ in dev]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(12):
+        for k, (d, x) in enumerate(dev):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(mla.paged_decode(d, *x, workspace=ws[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for o, l in got[k]:
+            assert torch.equal(o, want[k][0]) and torch.equal(l, want[k][1])
+    assert mla.mla_check_device_error(None) == 0
+
+
 def test_decode_agrees_with_the_dense_decode():
     """One length for all: the paged decode and the dense split-KV decode of the same cache."""
     d, t = decode_case(DS, 128, BF16, [640, 640], 64)
