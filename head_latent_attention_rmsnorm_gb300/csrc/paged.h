@@ -19,9 +19,9 @@ cudaError_t launch_paged_append(int ty, int T, long n_slots, int Dk, int Dr, flo
                                 const int *positions, void *c_cache, void *kpe_cache, cudaStream_t st);
 
 // One decode call.  A work item is (request b, row tile of `row_tile` heads); its keys are cut
-// into tiles of `tile` keys, all items' tiles are numbered through, and worker c of W takes tiles
-// [c T / W, (c + 1) T / W).  The part of item i that worker c computes goes to partial slot
-// c + i: unique, because going along the tiles every cut raises c or i.
+// into tiles of `tile` keys, all items' T tiles are numbered through, and worker c of W takes tiles
+// [c q, (c + 1) q) with q = max(min_tiles, ceil(T / W)).  The part of item i that worker c computes goes
+// to partial slot c + i: unique, because going along the tiles every cut raises c or i.
 struct alignas(16) PagedPart {   // what a worker computes of one item
     int b, rt, k0, nt;           // request, row tile, first key tile, key tiles
     int keys, next;              // the request's length; distance to the worker's next part, 0 for none
