@@ -285,7 +285,7 @@ def test_decode_nan_key_is_seen(heads, dtype):
 
 @pytest.mark.parametrize("heads,dtype", [(16, BF16), (128, BF16), (16, F32)])
 def test_decode_growing_maximum(heads, dtype):
-    """Keys whose scores rise by far more than the rescale threshold along the request."""
+    """Keys that grow along the request: the maximum rises all the way, by less than a rescale."""
     d, t = decode_case(DS, heads, dtype, [900, 333], 16, qscale=0.25)
     q, r, c, k, table, lens, w = t
     for b, n in enumerate(lens.tolist()):
