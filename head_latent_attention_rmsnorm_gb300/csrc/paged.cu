@@ -4,10 +4,12 @@
 #include <algorithm>
 
 #include "paged_common.cuh"
+#include "tc_common.cuh"
 
 namespace mla {
 
 using namespace paged;
+using tc::pdl_wait;
 
 const unsigned long long *paged_turns(float base, int Dr) {
     static thread_local unsigned long long v[MAX_HALF];
@@ -81,6 +83,7 @@ __global__ void __launch_bounds__(1024) paged_tables_kernel(const __grid_constan
     __shared__ long warp_tot[32];
     int *cu = sm, *off = cu + a.B + 1, *past = off + a.B + 1;
     const int tid = threadIdx.x, cap = a.max_pages * a.page;
+    pdl_wait();
     long tok = 0, pages = 0;
     for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
         const int b = b0 + tid;
@@ -190,6 +193,7 @@ __device__ __forceinline__ void rotate_row(const Append &a, const TU &turns, lon
 template <typename T>
 __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ Append a, const __grid_constant__ Turns turns) {
     const int lane = threadIdx.x & 31;
+    pdl_wait();
     const long t = ((long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     if (t >= a.T) return;
     const long slot = a.slots[t];
@@ -213,6 +217,7 @@ template <typename T, int NC, typename TU>
 __global__ void __launch_bounds__(256) paged_append_vec_kernel(const __grid_constant__ Append a, const __grid_constant__ TU turns) {
     constexpr int E = 16 / (int)sizeof(T);
     const int lane = threadIdx.x & 31, pieces = a.Dk / E;
+    pdl_wait();
     const long t = ((long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     if (t >= a.T) return;
     const long slot = a.slots[t];
@@ -253,21 +258,20 @@ __global__ void __launch_bounds__(256) paged_append_vec_kernel(const __grid_cons
 }
 
 template <typename T, int NC>
-void append_vec(const Append &a, const unsigned long long *v, cudaStream_t st) {
+cudaError_t append_vec(const Append &a, const unsigned long long *v, cudaStream_t st) {
     const unsigned blocks = (unsigned)(((long)a.T + 7) / 8);
     if (a.Dr <= 64) {
         Turns64 turns{};
         std::copy(v, v + a.Dr / 2, turns.v);
-        paged_append_vec_kernel<T, NC><<<blocks, 256, 0, st>>>(a, turns);
-    } else {
-        Turns turns{};
-        std::copy(v, v + a.Dr / 2, turns.v);
-        paged_append_vec_kernel<T, NC><<<blocks, 256, 0, st>>>(a, turns);
+        return launch_after(paged_append_vec_kernel<T, NC, Turns64>, blocks, 256, 0, st, a, turns);
     }
+    Turns turns{};
+    std::copy(v, v + a.Dr / 2, turns.v);
+    return launch_after(paged_append_vec_kernel<T, NC, Turns>, blocks, 256, 0, st, a, turns);
 }
 
 template <typename T>
-void append(const Append &a, const unsigned long long *v, cudaStream_t st) {
+cudaError_t append(const Append &a, const unsigned long long *v, cudaStream_t st) {
     constexpr int E = 16 / (int)sizeof(T);
     const int pieces = a.Dk % E == 0 && a.c_stride % E == 0 ? a.Dk / E : 0;
     if (pieces > 0 && pieces <= 32) return append_vec<T, 1>(a, v, st);
@@ -275,7 +279,7 @@ void append(const Append &a, const unsigned long long *v, cudaStream_t st) {
     if (pieces > 0 && pieces <= 128) return append_vec<T, 4>(a, v, st);
     Turns turns{};
     std::copy(v, v + a.Dr / 2, turns.v);
-    paged_append_kernel<T><<<(unsigned)(((long)a.T + 7) / 8), 256, 0, st>>>(a, turns);
+    return launch_after(paged_append_kernel<T>, (unsigned)(((long)a.T + 7) / 8), 256, 0, st, a, turns);
 }
 
 }  // namespace
@@ -298,8 +302,7 @@ cudaError_t launch_paged_tables(int B, int page, int max_pages, int n_free, int 
         if (e != cudaSuccess) return e;
     }
     ProfScope ps("paged_tables", st);
-    kern<<<blocks, threads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_after(kern, (unsigned)blocks, (unsigned)threads, (size_t)smem, st, a);
 }
 
 cudaError_t launch_paged_append(int ty, int T, long n_slots, int Dk, int Dr, float base, float eps, const void *c,
@@ -308,9 +311,7 @@ cudaError_t launch_paged_append(int ty, int T, long n_slots, int Dk, int Dr, flo
     Append a{T, Dk, Dr, n_slots, c_stride, k_stride, eps, c, k, w, slots, positions, c_cache, kpe_cache};
     const unsigned long long *v = paged_turns(base, Dr);
     ProfScope ps("paged_append", st);
-    if (ty == TY_F32) append<float>(a, v, st);
-    else append<__nv_bfloat16>(a, v, st);
-    return cudaGetLastError();
+    return ty == TY_F32 ? append<float>(a, v, st) : append<__nv_bfloat16>(a, v, st);
 }
 
 }  // namespace mla

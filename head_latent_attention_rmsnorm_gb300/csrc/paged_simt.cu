@@ -4,7 +4,7 @@
 // Three launches: absorb (q_abs = W_K^T q_nope, the query's rotation, the division of the batch
 // among the workers), attention (each worker walks its key tiles with the running maximum and sum
 // of the softmax and writes one normalised partial per request it met), join (the partials'
-// log-sum-exp merge and out = W_V o), the latter two launched early.  16 heads of 512 + 64 dims, fp32: 4
+// log-sum-exp merge and out = W_V o), each launched early.  16 heads of 512 + 64 dims, fp32: 4
 // ragged requests of up to 1000 keys 23.5 us (one tile per worker: three launches' latency; 46 before the
 // loads of queries, tiles, parts and W_V went out together), 16 requests of 3000 keys 101 us: 8 us a
 // tile, in which shared-memory reads take about twice the time of the 557 thousand multiply-adds.  512
@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(NT) paged_absorb_simt_kernel(const __grid_cons
     extern __shared__ float sm[];   // q [BT][Dn], sums [8 warps][BT][DC]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int groups = (p.B + BT - 1) / BT, chunks = (p.Dk + DC - 1) / DC;
+    pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x == 0) {
         plan_block<NT>(p);
@@ -490,9 +491,9 @@ cudaError_t decode_simt(const PagedDecode &p, cudaStream_t st) {
         return e;
     {
         ProfScope ps("paged_absorb", st);
-        paged_absorb_simt_kernel<T><<<blocks + 1, NT, s1, st>>>(p, turns);
+        e = launch_after(paged_absorb_simt_kernel<T>, blocks + 1, NT, s1, st, p, turns);
     }
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
     {
         ProfScope ps("paged_attn", st);
         e = launch_after(paged_attn_simt_kernel<T>, (unsigned)p.workers, NT, s2, st, p);

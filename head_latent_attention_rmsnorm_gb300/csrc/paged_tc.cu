@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
     extern __shared__ __align__(1024) uint8_t sm[];
     const PagedDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x == 0) {
         plan_block<128>(p, (int *)sm, AB_SMEM / 4);
@@ -1321,9 +1322,9 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
         return e;
     {
         ProfScope ps("paged_absorb", st);
-        paged_absorb_tc_kernel<<<(unsigned)(p.H * 4 * ab.groups + 1 + ab.rot_blocks), 128, AB_SMEM, st>>>(ab);
+        e = launch_after(paged_absorb_tc_kernel, (unsigned)(p.H * 4 * ab.groups + 1 + ab.rot_blocks), 128, AB_SMEM, st, ab);
     }
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
     {
         ProfScope ps("paged_attn", st);
         e = launch_after(attn, 2 * p.workers, NTHREADS, SMEM_BYTES, st, m, at);
