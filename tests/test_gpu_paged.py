@@ -417,6 +417,30 @@ def test_decode_on_another_stream():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("dims,heads,dtype,page", [(DS, 128, BF16, 64), (DS, 16, F32, 16), (TINY, 4, F32, 7)])
+def test_inputs_written_by_the_kernel_in_front(dims, heads, dtype, page):
+    """Every input rewritten in place right before the call, call after call, has the bits of a call that
+    finds them settled."""
+    cases = [decode_case(dims, heads, dtype, lens, page, seed=k)[1] for k, lens in enumerate(([700, 30, 1], [64, 700, 9], [5, 8, 700]))]
+    d = decode_case(dims, heads, dtype, [1], page)[0]
+    cases = [[x.cuda() for x in t] for t in cases]
+    rows = max(t[2].shape[0] for t in cases)
+    want = [mla.paged_decode(d, *t) for t in cases]
+    live = [torch.zeros(*([rows] if i in (2, 3) else [x.shape[0]]), *x.shape[1:], dtype=x.dtype, device="cuda")
+            for i, x in enumerate(cases[0])]
+    ws = mla.paged_decode_workspace(d, live[2], live[4])
+    got = []
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for t in cases:
+            for x, y in zip(live, t):
+                x[:y.shape[0]].copy_(y)
+            got.append(mla.paged_decode(d, *live, workspace=ws))
+    torch.cuda.synchronize()
+    for k, (o, l) in enumerate(got):
+        assert torch.equal(o, want[k % 3][0]) and torch.equal(l, want[k % 3][1]), k
+
+
 @pytest.mark.parametrize("dims,heads,dtype,page", [(DS, 16, BF16, 16), (DS, 128, BF16, 64), (TINY, 4, F32, 5)])
 def test_decode_same_page_twice(dims, heads, dtype, page):
     """A request whose table names one page several times: its keys count as often."""
