@@ -614,3 +614,50 @@ def test_two_captured_decodes_with_a_workspace_each():
     torch.cuda.synchronize()
     for (o, l), (wo, wl) in zip(outs, (wa, wb)):
         assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+@pytest.mark.parametrize("dims,heads,dtype,page", [(DS, 128, BF16, 64), (TINY, 4, F32, 7)])
+def test_captured_behind_a_join_of_streams(dims, heads, dtype, page):
+    """Captured calls whose inputs come from two streams that meet right in front of them: the first kernel of
+    each call depends on both."""
+    d, t = decode_case(dims, heads, dtype, [300, 70, 1], page)
+    dev = [x.cuda() for x in t]
+    q, r, c, k, table, lens, w = dev
+    src_q, src_c = q.clone(), c.clone()
+    lens_src, past = lens.clone(), torch.zeros_like(lens)
+    free = torch.arange(64, dtype=torch.int32, device="cuda")
+    tab2 = torch.full((3, table.shape[1] + 1), -1, dtype=torch.int32, device="cuda")
+    ws = mla.paged_decode_workspace(d, c, table)
+    n = int(lens.sum())
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            c.copy_(src_c)
+            past.copy_(lens_src * 0)
+        q.copy_(src_q)
+        here.wait_stream(side)
+        tables = mla.paged_tables(past, lens_src, free, tab2, page_size=page, n_tokens=n)
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            r2 = r * 1
+        here.wait_stream(side)
+        return tables, mla.paged_decode(d, q, r2, c, k, table, lens, w, workspace=ws)
+
+    want = [x.clone() for x in step()[1]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tables, (out, lse) = step()
+    for scale in (1.0, 0.5, 1.0):
+        src_q.copy_(t[0].cuda() * scale)
+        q.zero_(), c.zero_(), out.fill_(5), lse.fill_(5), tables.kv_lens.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(tables.kv_lens, lens)
+        if scale == 1.0:
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        else:
+            got = mla.paged_decode(d, src_q, r, c, k, table, lens, w)
+            assert torch.equal(out, got[0]) and torch.equal(lse, got[1])
