@@ -121,11 +121,13 @@ __device__ __forceinline__ Extra extra_of(bool paired, int keys) {
 // products run on mma.sync (M = latent dims, N = requests: eight per step, no padding to 128
 // rows).  Block (head, 128 latent dims, group of up to 64 requests): the weight block and the group's
 // queries by cp.async, all in flight at once; the weights then stay in registers as A fragments.
-// 128 heads, events around it alone: one request 10 us, 64 requests 20 us (17 MB of weights, 2.5 us at the copy
+// 128 heads, events around it alone: one request 10 us, 64 requests 17 us (20 with three
+// blocks an SM, whose 512 blocks took a second wave; 17 MB of weights, 2.5 us at the copy
 // peak; 19 MB of queries out).
 constexpr int AB_DIMS = 128, AB_PITCH = 256 + 16, AB_GROUP = 64;
 constexpr int AB_OUT = 40;              // halves per request of a warp's staging (32 dims + pad)
-constexpr int AB_SMEM = DN * AB_PITCH + AB_GROUP * AB_PITCH + 4 * 3 * 8 * AB_OUT * 2 + AB_GROUP * 4;
+constexpr int AB_SMEM = DN * AB_PITCH + AB_GROUP * AB_PITCH + AB_GROUP * 4;   // four blocks an SM
+static_assert(4 * 3 * 8 * AB_OUT * 2 <= DN * AB_PITCH, "the staging lies where the weights were");
 
 struct Absorb {
     PagedDecode p;
@@ -208,8 +210,9 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
 #pragma unroll
         for (int s = 0; s < 8; ++s)   // matrices: (dims 0-7, k 0-7), (dims 8-15, k 0-7), the same of k 8-15
             ldsm4_t(A[m][s], smem_u32(sw + (16 * s + (mi >> 1) * 8 + r) * AB_PITCH + (warp * 32 + m * 16 + (mi & 1) * 8) * 2));
+    __syncthreads();   // all have their weights: the room is the staging's
     const int g = lane >> 2, t = lane & 3;
-    uint16_t *sh = (uint16_t *)(sq + AB_GROUP * AB_PITCH) + warp * 3 * 8 * AB_OUT, *sl = sh + 8 * AB_OUT,
+    uint16_t *sh = (uint16_t *)sw + warp * 3 * 8 * AB_OUT, *sl = sh + 8 * AB_OUT,
              *sr = sl + 8 * AB_OUT;
 #pragma unroll 1
     for (int b = 0; b < nb; b += 8) {   // (rows behind the group's last request are not read back)
