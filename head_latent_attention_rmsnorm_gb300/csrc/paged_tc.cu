@@ -45,12 +45,14 @@
 // both halves of the band.  q_lo's latent part shifts a part's log-sum-exp by scale q_lo . o to first
 // order, which the join adds (the second order is half the variance of scale q_lo . c_j, ~1e-6 at unit
 // scale), and its weights by a relative 2^-9, like P's own rounding.  Where both count, it is taken in
-// part: above 64 heads and up to 4096 keys (EX_LATENT) q_lo of 128 of the 512 dims has MMAs, for
-// which tensor memory has the room.  Measured as the output's error over that of an fp32
-// evaluation rounded to bf16, 128 heads: 2000 keys 1.51 -> 1.43, 100 keys 1.54 -> 1.48; 12000 keys
-// without it 1.45, since an average over more keys rounds better (16 heads: 1.26-1.43 throughout).  Up
-// to 64 keys (EX_BAND) the log-sum-exp is small and bf16 pairs show in it: the band's third part has
-// MMAs and the join adds the latent's (1 to 3 keys: 1.5e-6 -> 8e-7 of its value).  Partials are fp16
+// part above 64 heads: q_lo of 256 of the 512 dims has MMAs up to 1024 keys (EX_WIDE), of 128 dims up to 4096
+// (EX_LATENT), for which tensor memory has the room; the other half of EX_WIDE's is read in shared memory.
+// Measured as the output's error over that of an fp32 evaluation rounded to bf16, 128 heads, 60 random
+// cases: up to 1.54 without, 1.49 with (at 4500 keys; an average over more keys rounds better; 8 to 64
+// heads: up to 1.41 without).  Up to 8192 keys it would be 1.47, but tiles of 7 % more MMAs hold up their
+// cluster's equal share: 64 ragged requests 294 -> 315 us.  Up to 64 keys (EX_BAND) the log-sum-exp is small
+// and bf16 pairs show in it: the band's third part has MMAs, above 64 heads q_lo of 192 dims too, and the
+// join adds the latent's third part (1 to 3 keys: 1.5e-6 -> 8e-7 of its value).  Partials are fp16
 // with a power of two per half row.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -109,10 +111,16 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t &hi, uint32_t 
 
 // What a request's scores and log-sum-exp take of the queries besides q_hi and the band's hi and lo
 // (the header's part on precision).
-enum Extra { EX_NONE, EX_LATENT, EX_BAND };
-constexpr int SHORT_KEYS = 64, MIDDLE_KEYS = 4096;
+enum Extra { EX_NONE, EX_LATENT, EX_WIDE, EX_BAND };
+constexpr int SHORT_KEYS = 64, WIDE_KEYS = 1024, MIDDLE_KEYS = 4096;
 __device__ __forceinline__ Extra extra_of(bool paired, int keys) {
-    return keys <= SHORT_KEYS ? EX_BAND : (!paired && keys <= MIDDLE_KEYS ? EX_LATENT : EX_NONE);
+    if (keys <= SHORT_KEYS) return EX_BAND;
+    return paired || keys > MIDDLE_KEYS ? EX_NONE : (keys > WIDE_KEYS ? EX_LATENT : EX_WIDE);
+}
+// The blocks of 64 latent dims, as bits, whose q_lo the scores take.
+__device__ __forceinline__ unsigned lo_blocks(bool paired, Extra ex) {
+    if (ex == EX_NONE || (ex == EX_BAND && paired)) return 0;
+    return ex == EX_LATENT ? 0x3 : (ex == EX_WIDE ? 0xf : 0xe);
 }
 
 // ------------------------------------------------------------------------ absorb ----
@@ -441,7 +449,7 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 dot += o[i][2 * e] * __uint_as_float(q[e] << 16) + o[i][2 * e + 1] * __uint_as_float(q[e] & 0xffff0000u);
-            if (sc[j][2] == EX_LATENT && d8 < 16) dot = 0.f;   // the scores have it
+            if ((lo_blocks(p.H <= 64, (Extra)sc[j][2]) >> (d8 >> 3)) & 1) dot = 0.f;   // the scores have it
             if (sc[j][2] == EX_BAND && j < nb) {
                 const uint4 x = __ldcg((const uint4 *)(qrest + ((long)(b0 + j) * p.H + h) * DK) + d8);
                 const uint32_t z[4] = {x.x, x.y, x.z, x.w};
@@ -522,7 +530,7 @@ constexpr uint32_t OFF_PB = VSL * VHALF, OFF_INV = OFF_PB + NPB * XSLOT, OFF_OUT
 constexpr uint32_t END0 = OFF_SUM + 2 * ROWS * 4, END1 = OFF_OUT + 8 * 4096;
 constexpr uint32_t OFF_BAR = END0 > END1 ? END0 : END1;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 512;
-constexpr uint32_t T_S = 0, T_Q = 2 * NK;   // rank 0's TMEM columns: S buffers; 32 per 64 query dims (hi 0-7, band hi and lo, EX_LATENT's lo 0-1 or EX_BAND's rest)
+constexpr uint32_t T_S = 0, T_Q = 2 * NK;   // rank 0's TMEM columns: S buffers; 32 per 64 query dims (hi 0-7, band hi and lo, lo 0-1 or EX_BAND's rest)
 constexpr float RESCALE_LOG2 = 8.0f;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 static_assert(KSTAGE % 1024 == 0 && OFF_STG % 1024 == 0 && OFF_PB % 1024 == 0 && XSLOT % 1024 == 0, "swizzle atoms");
@@ -548,11 +556,12 @@ enum : int {
     B_VEMPTY = B_VFULL + VSL,
     B_OFINAL = B_VEMPTY + VSL,   // rank 1: the part's O complete / read
     B_EPIDONE = B_OFINAL + 1,
-    B_COUNT = B_EPIDONE + 1
+    B_QNEXT = B_EPIDONE + 1,     // rank 0: the two boxes behind the key stages are in TMEM
+    B_COUNT = B_QNEXT + 1
 };
 __device__ __forceinline__ uint32_t arrivals(int i) {
     if (i >= B_SFREE && i < B_STGFREE) return 8;   // one per softmax warp
-    if ((i >= B_KFREE && i <= B_QREADY) || (i >= B_PCREADY && i < B_VFULL)) return 4;
+    if ((i >= B_KFREE && i <= B_QREADY) || (i >= B_PCREADY && i < B_VFULL) || i == B_QNEXT) return 4;
     if (i == B_QFREE) return 2;
     return i == B_EPIDONE ? 8 : 1;
 }
@@ -744,6 +753,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             for (; more && ok; next(), ++seg) {
                 ok = wait_all(&bars[B_QREADY], seg & 1, ctl);
                 const Extra ex = extra_of(paired, w.keys);
+                const unsigned lo = lo_blocks(paired, ex);
 #pragma unroll 1
                 for (int i = 0; i < w.nt && ok; ++i, ++n) {
                     if ((n & 1) != s) continue;
@@ -755,8 +765,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                         if (!ok) break;
                         tc_fence_after();
                         if (elect_one()) {
-                            // blocks of 64 dims: latent 0-7 (q_hi; the first two also with q_lo), then the key band
-                            // twice (hi, lo) or three times
+                            // blocks of 64 dims: latent 0-7 (q_hi), then the key band twice (hi, lo) or three times
                             uint64_t d = sdesc_sw128(base + g * KG1, 16, (g < 2 ? 3 : 2) * ATOM);
                             const int j1 = g < 2 ? 3 * g + 3 : (ex == EX_BAND ? 11 : 10);
 #pragma unroll 1
@@ -765,12 +774,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                                 for (int q = 0; q < 4; ++q)
                                     mma_ts(dt, tmem + T_Q + j * 32 + q * 8, d + 2 * q, a.idesc_s, (j | q) != 0);
-                                if (ex == EX_LATENT && j < 2) {
-#pragma unroll
-                                    for (int q = 0; q < 4; ++q) mma_ts(dt, tmem + T_Q + (10 + j) * 32 + q * 8, d + 2 * q, a.idesc_s, 1);
-                                }
                                 d += ATOM >> 4;
                             }
+                            if (lo)   // q_lo's blocks of this group: 0, 1 in TMEM, 2, 3 in the boxes behind the key stages
+#pragma unroll 1
+                                for (int j = 3 * g; j < min(3 * g + 3, 4); ++j) {
+                                    if (!((lo >> j) & 1)) continue;
+                                    const uint64_t kd = sdesc_sw128(base + g * KG1 + (j - 3 * g) * ATOM, 16, 3 * ATOM),
+                                                   ql = sdesc_kmajor(smem + OFF_Q + (j & 1) * 16384);
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) {
+                                        if (j < 2) mma_ts(dt, tmem + T_Q + (10 + j) * 32 + q * 8, kd + 2 * q, a.idesc_s, 1);
+                                        else mma_ss(dt, ql + 2 * q, kd + 2 * q, a.idesc_s, 1);
+                                    }
+                                }
                             mma_commit(&bars[B_GEMPTY + s * KGRP + g]);
                             if (g == KGRP - 1) mma_commit(&bars[B_SFULL + s]);
                         }
@@ -920,6 +937,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             // (0-7), hi and lo of the band (8, 9), Extra's (10); all in flight at once in the key stages, which
             // the last part's MMAs have left, and the two boxes behind them
             int seg = 0;
+            uint32_t wide = 0;   // parity of the moves waited for below
             bool go = lane == 0;
             for (; more && go; next(), ++seg) {
                 const Extra ex = extra_of(paired, w.keys);
@@ -933,28 +951,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     tma_load_3d(smem + (j < 9 ? j * 16384 : OFF_Q + (j - 9) * 16384), map, &bars[B_QFULL], j < 8 ? 64 * j : 0,
                                 w.rt * ROWS, w.b);
                 }
+                if (!(lo_blocks(paired, ex) & 0xc)) continue;
+                // lo of dims 128-255 for the MMAs to read in shared memory, once the two boxes there have moved
+                go = wait_for(&bars[B_QNEXT], wide, ctl);
+                if (!go) break;
+                wide ^= 1;
+                mbar_arrive_expect_tx(&bars[B_QFULL], 2 * 128 * a.q_rows);
+#pragma unroll 1
+                for (int j = 0; j < 2; ++j) tma_load_3d(smem + OFF_Q + j * 16384, &m.ql, &bars[B_QFULL], 64 * (j + 2), w.rt * ROWS, w.b);
             }
         } else {
             // ------------------------------- queries into TMEM (warps 14-17, a thread per head)
             const int quad = warp & 3, row = quad * 32 + lane;
             const uint32_t dst = tmem + ((uint32_t)(quad * 32) << 16) + T_Q;
-            int seg = 0;
+            uint32_t ph = 0;
             bool ok = true;
-            for (; more && ok; next(), ++seg) {
+            for (; more && ok; next()) {
                 const bool act = w.rt * ROWS + quad * 32 < p.H;
                 const Extra ex = extra_of(paired, w.keys);
                 const int boxes = ex == EX_NONE ? 10 : 11;
                 // q_lo of dims 64-127 has no box: each thread's 128 bytes come straight from memory, under
                 // the boxes' flight
                 uint4 x[8];
-                if (ex == EX_LATENT && act) {
+                const unsigned lo = lo_blocks(paired, ex);
+                if ((lo & 2) && act) {
                     const bf16 *src = a.qlo + ((long)w.b * p.H + min(w.rt * ROWS + row, p.H - 1)) * DK + 64;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = __ldcg((const uint4 *)src + e);
                 }
-                ok = wait_all(&bars[B_QFULL], seg & 1, ctl);
+                ok = wait_all(&bars[B_QFULL], ph, ctl);
+                ph ^= 1;
                 tc_fence_after();   // (the boxes landed behind the commit of the last part's MMAs)
-                if (ex == EX_LATENT && act && ok) {
+                if ((lo & 2) && act && ok) {
                     uint32_t v[32];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -984,6 +1012,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bars[B_KFREE + (j == 8)]);
                     }
+                }
+                if ((lo & 0xc) && ok) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[B_QNEXT]);
+                    ok = wait_all(&bars[B_QFULL], ph, ctl);
+                    ph ^= 1;
                 }
                 tmem_st_wait();
                 tc_fence_before();
