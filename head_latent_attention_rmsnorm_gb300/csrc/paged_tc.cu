@@ -546,7 +546,7 @@ enum : int {
     B_STAGED = B_SFREE + 2,      // rank 0 [slot]: P staged / its copy has read it
     B_STGFREE = B_STAGED + 2,
     B_QFULL = B_STGFREE + 2,     // rank 0: the part's query boxes landed
-    B_KFREE = B_QFULL + 1,       // rank 0 [stage]: the boxes there are in TMEM
+    B_KFREE = B_QFULL + 1,       // rank 0 [stage]: the boxes there are in TMEM (parts that use the stage)
     B_QREADY = B_KFREE + 2,      // rank 0: the part's queries in TMEM / no longer read by MMAs
     B_QFREE = B_QREADY + 1,
     B_PEMPTY = B_QFREE + 1,      // both [slot]: P consumed (one multicast commit completes it in both)
@@ -722,9 +722,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             // a lane per unit of the tile's rows; the whole warp waits.  A group's refill costs the time
             // from its last MMA to the issue of its boxes, hence a warp for each.
             const int g = warp == 0 ? 0 : warp - 11;
-            int n = 0, seg = 0;
+            int n = 0;
+            uint32_t moved = 0;   // per stage, the parity of the next move of queries out of it
             bool go = true;
-            for (; more && go; next(), ++seg) {
+            for (; more && go; next()) {
                 Rows<UNIT> rows{-1, -1, -64};
 #pragma unroll 1
                 for (int i = 0; i < w.nt; ++i, ++n) {
@@ -732,9 +733,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     uint8_t *dst = smem + s * KSTAGE + g * KG1 + lane * NRG * (g < 2 ? 3 : 2) * ATOM;
                     uint64_t *full = &bars[B_GFULL + s * KGRP + g];
                     const int row = rows.tile(a, w, i, lane), rg = row >= 0 ? row >> 3 : none;
-                    // a part's first tiles go where its queries were, the others behind the MMAs of two tiles ago
-                    go = wait_all(i < KST ? &bars[B_KFREE + s] : &bars[B_GEMPTY + s * KGRP + g],
-                                  i < KST ? seg & 1 : ((n >> 1) & 1) ^ 1, ctl);
+                    // behind the MMAs of two tiles ago (a fresh barrier passes), a part's first tiles also behind
+                    // the move of its queries, which lay in their stages
+                    go = wait_all(&bars[B_GEMPTY + s * KGRP + g], ((n >> 1) & 1) ^ 1, ctl);
+                    if (go && i < KST) {
+                        go = wait_all(&bars[B_KFREE + s], (moved >> s) & 1, ctl);
+                        moved ^= 1u << s;
+                    }
                     if (!go) break;
                     if (lane == 0) mbar_arrive_expect_tx(full, NGRP * 3 * ATOM);
                     if (lane < UNITS) {
@@ -965,8 +970,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             const int quad = warp & 3, row = quad * 32 + lane;
             const uint32_t dst = tmem + ((uint32_t)(quad * 32) << 16) + T_Q;
             uint32_t ph = 0;
+            int n = 0;
             bool ok = true;
-            for (; more && ok; next()) {
+            for (; more && ok; n += w.nt, next()) {
                 const bool act = w.rt * ROWS + quad * 32 < p.H;
                 const Extra ex = extra_of(paired, w.keys);
                 const int boxes = ex == EX_NONE ? 10 : 11;
@@ -1008,7 +1014,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                         }
                         tmem_st32(dst + j * 32, v);
                     }
-                    if (j == 4 || j == 8) {   // boxes 0-4 cover the first stage
+                    // Boxes 0-4 cover the first stage, 4-8 the second.  Only a stage that the part uses gets its
+                    // phase: the producers wait for each, and none can still be open when the next part's test of
+                    // its parity would pass on the phase before.
+                    if ((j == 4 || j == 8) && (w.nt >= KST || (n & 1) == (j == 8))) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bars[B_KFREE + (j == 8)]);
                     }
