@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
         fence_proxy_async_smem();
         tc_fence_before();
         __syncthreads();
-        if (tid < nb) p.lse[(long)(b0 + tid) * p.H + h] = sl[tid] + p.scale * (sd[0][tid] + sd[1][tid]);
+        // (no keys: -inf stays, whatever the queries of a padded request hold; 0 * NaN is not added)
+        if (tid < nb) p.lse[(long)(b0 + tid) * p.H + h] = sl[tid] == -INFINITY ? sl[tid] : sl[tid] + p.scale * (sd[0][tid] + sd[1][tid]);
         if (warp == 0) {
             ok = __all_sync(FULL, ok && mbar_wait(&v0.bar_w, 0, (volatile int *)&v0.abort, &g_paged_tc_err));   // W_V is here
             tc_fence_after();
