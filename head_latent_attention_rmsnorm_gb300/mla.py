@@ -10,7 +10,10 @@ Two layers, argument marshalling only:
   ``paged_decode``:
   the same calls taking torch tensors; they allocate any output or workspace the
   caller did not pass (through torch's allocator, so the CUDA caching allocator sees
-  every byte) and raise :class:`MlaError` on a non-OK status.
+  every byte) and raise :class:`MlaError` on a non-OK status.  ``stream`` (a
+  ``torch.cuda.Stream`` or a ``cudaStream_t`` as an integer; default: torch's current
+  stream) is the stream they launch on and allocate for, as ``with torch.cuda.stream(stream):``
+  around the call would.
 
 Every step of the computation runs in the library's CUDA kernels.  If the library
 is missing this module raises on first use; there is no fallback.
@@ -18,6 +21,7 @@ is missing this module raises on first use; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import NamedTuple
@@ -360,10 +364,39 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+def _stream() -> int:
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _on_stream(stream, fn, *args, **kw):
+    """``fn(*args, **kw)`` with ``stream`` as the current one.  What the call allocates then belongs to
+    the stream that its kernels run on: a workspace dropped on return is not handed to other work
+    while they use it, and an output's memory holds nothing that other work still reads.  Outputs
+    are recorded for the caller's stream too, which may read them until they are dropped."""
+    like = next((a for a in (*args, *kw.values()) if isinstance(a, torch.Tensor) and a.is_cuda), None)
+    if like is None:
+        return fn(*args, **kw)   # refuses its tensors
+    caller = torch.cuda.current_stream(like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        handle = 0 if handle == 1 else handle   # (cudaStreamLegacy: the default stream by another handle)
+        stream = caller if handle == caller.cuda_stream else torch.cuda.ExternalStream(handle, device=like.device)
+    if stream.device != like.device:
+        raise ValueError("stream: on %s, the call's tensors are on %s" % (stream.device, like.device))
+    with torch.cuda.stream(stream):
+        result = fn(*args, **kw)
+    if stream != caller:
+        for t in result.values() if isinstance(result, dict) else result if isinstance(result, tuple) else (result,):
+            t.record_stream(caller)
+    return result
+
+
+def _takes_stream(fn):
+    """A wrapper whose ``stream`` is made current before it runs."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        return fn(*args, **kw) if stream is None else _on_stream(stream, fn, *args, **kw)
+    return call
 
 
 def _check(status: int, where: str) -> None:
@@ -379,6 +412,7 @@ def _workspace(nbytes: int, device, workspace):
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
 
 
+@_takes_stream
 def latent_attn_fwd(d: Dims, q_nope, q_pe, c_kv, k_pe, w_kv_b, rms_w, *, q_offset=0, causal=True,
                     head_begin=0, head_shard=0, out=None, lse=None, workspace=None, stream=None,
                     absorbed=False):
@@ -395,7 +429,7 @@ def latent_attn_fwd(d: Dims, q_nope, q_pe, c_kv, k_pe, w_kv_b, rms_w, *, q_offse
     fn = mla_absorbed_attn_fwd if absorbed else mla_latent_attn_fwd
     st = fn(ctypes.byref(d), dt, B, s_q, s_kv, q_offset, int(causal), head_begin, hc, head_shard,
             _ptr(q_nope), _ptr(q_pe), _ptr(c_kv), _ptr(k_pe), _ptr(w_kv_b), _ptr(rms_w), _ptr(out),
-            _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+            _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream())
     _check(st, fn.__name__)
     return out, lse
 
@@ -404,6 +438,7 @@ def absorbed_attn_fwd(d: Dims, *args, **kw):
     return latent_attn_fwd(d, *args, absorbed=True, **kw)
 
 
+@_takes_stream
 def latent_attn_fused_fwd(d: Dims, q_nope, q_pe, c_kv, k_pe, w_kv_b, rms_w, *, q_offset=0, causal=True,
                           head_begin=0, out=None, lse=None, workspace=None, stream=None):
     """Explicit MLA prefill with the K/V up-projection inside the attention kernel (no
@@ -418,11 +453,12 @@ def latent_attn_fused_fwd(d: Dims, q_nope, q_pe, c_kv, k_pe, w_kv_b, rms_w, *, q
     ws = _workspace(nbytes, q_nope.device, workspace)
     st = mla_latent_attn_fused_fwd(ctypes.byref(d), dt, B, s_q, s_kv, q_offset, int(causal), head_begin, hc,
                                    _ptr(q_nope), _ptr(q_pe), _ptr(c_kv), _ptr(k_pe), _ptr(w_kv_b), _ptr(rms_w),
-                                   _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+                                   _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream())
     _check(st, "mla_latent_attn_fused_fwd")
     return out, lse
 
 
+@_takes_stream
 def latent_attn_bwd(d: Dims, q_nope, q_pe, c_kv, k_pe, w_kv_b, rms_w, out, lse, dout, *, q_offset=0, causal=True,
                     head_begin=0, head_shard=0, grads=None, workspace=None, stream=None):
     """Backward of :func:`latent_attn_fwd` for an upstream gradient ``dout`` of its output.
@@ -450,7 +486,7 @@ def latent_attn_bwd(d: Dims, q_nope, q_pe, c_kv, k_pe, w_kv_b, rms_w, out, lse, 
                              _ptr(q_nope), _ptr(q_pe), _ptr(c_kv), _ptr(k_pe), _ptr(w_kv_b), _ptr(rms_w), _ptr(out),
                              _ptr(lse), _ptr(dout), _ptr(g["q_nope"]), _ptr(g["q_pe"]), _ptr(g["c_kv"]),
                              _ptr(g["k_pe"]), _ptr(g["w_kv_b"]), _ptr(g["rms_w"]), _ptr(ws),
-                             ws.numel() * ws.element_size(), _stream(stream))
+                             ws.numel() * ws.element_size(), _stream())
     _check(st, "mla_latent_attn_bwd")
     return g
 
@@ -459,6 +495,7 @@ def set_fused_cluster(size: int) -> None:
     lib().mla_set_fused_cluster(size)
 
 
+@_takes_stream
 def decode_splitkv(d: Dims, q_nope, q_pe, c_cache, kpe_cache, w_kv_b, *, n_splits=1, out=None, lse=None,
                    part_out=None, part_lse=None, workspace=None, stream=None):
     """Split-KV latent decode.  Returns (out, lse)."""
@@ -477,11 +514,12 @@ def decode_splitkv(d: Dims, q_nope, q_pe, c_cache, kpe_cache, w_kv_b, *, n_split
     ws = _workspace(nbytes, q_nope.device, workspace)
     st = mla_decode_splitkv(ctypes.byref(d), dt, B, L, n_splits, _ptr(q_nope), _ptr(q_pe), _ptr(c_cache),
                             _ptr(kpe_cache), _ptr(w_kv_b), _ptr(out), _ptr(lse), _ptr(part_out),
-                            _ptr(part_lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+                            _ptr(part_lse), _ptr(ws), ws.numel() * ws.element_size(), _stream())
     _check(st, "mla_decode_splitkv")
     return out, lse
 
 
+@_takes_stream
 def tpla_decode(d: Dims, q_nope, q_pe, c_cache, kpe_cache, w_kv_b, *, n_shards=2, n_splits=1, out=None,
                 shard_lse=None, workspace=None, stream=None):
     """TPLA decode over ``n_shards`` latent shards (``c_cache`` normalised per shard, as
@@ -497,11 +535,12 @@ def tpla_decode(d: Dims, q_nope, q_pe, c_cache, kpe_cache, w_kv_b, *, n_shards=2
     ws = _workspace(nbytes, q_nope.device, workspace)
     st = mla_tpla_decode(ctypes.byref(d), dt, B, L, n_splits, n_shards, _ptr(q_nope), _ptr(q_pe), _ptr(c_cache),
                          _ptr(kpe_cache), _ptr(w_kv_b), _ptr(out), _ptr(shard_lse), _ptr(ws),
-                         ws.numel() * ws.element_size(), _stream(stream))
+                         ws.numel() * ws.element_size(), _stream())
     _check(st, "mla_tpla_decode")
     return out, shard_lse
 
 
+@_takes_stream
 def rmsnorm(x, w, *, n_shards=1, eps=1e-6, out=None, stream=None):
     """RMSNorm over the last dim of ``x``, cut into ``n_shards`` shards normalised on
     their own.  Returns ``out``."""
@@ -514,11 +553,12 @@ def rmsnorm(x, w, *, n_shards=1, eps=1e-6, out=None, stream=None):
     if out is None:
         out = torch.empty_like(x)
     st = mla_rmsnorm(_dt(x), x.numel() // d if d else 0, d, n_shards, float(eps), _ptr(x), _ptr(w), _ptr(out),
-                     _stream(stream))
+                     _stream())
     _check(st, "mla_rmsnorm")
     return out
 
 
+@_takes_stream
 def rmsnorm_bwd(x, w, dy, *, n_shards=1, eps=1e-6, dx=None, dw=None, workspace=None, stream=None):
     """Backward of :func:`rmsnorm`.  Returns (dx like x, dw fp32 [d])."""
     dev = _device(x)
@@ -537,11 +577,12 @@ def rmsnorm_bwd(x, w, dy, *, n_shards=1, eps=1e-6, dx=None, dw=None, workspace=N
         dw = torch.empty(d, dtype=torch.float32, device=x.device)
     ws = _workspace(mla_rmsnorm_bwd_workspace(dt, rows, d, n_shards), x.device, workspace)
     st = mla_rmsnorm_bwd(dt, rows, d, n_shards, float(eps), _ptr(x), _ptr(w), _ptr(dy), _ptr(dx), _ptr(dw),
-                         _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+                         _ptr(ws), ws.numel() * ws.element_size(), _stream())
     _check(st, "mla_rmsnorm_bwd")
     return dx, dw
 
 
+@_takes_stream
 def lse_combine(part_out, part_lse, *, out_dtype=torch.float32, out=None, lse=None, stream=None):
     """Merge fp32 split partials [n, rows, D] / [n, rows].  Returns (out, lse)."""
     dev = _device(part_out)
@@ -559,7 +600,7 @@ def lse_combine(part_out, part_lse, *, out_dtype=torch.float32, out=None, lse=No
     if lse is None:
         lse = torch.empty(rows, dtype=torch.float32, device=part_out.device)
     st = mla_lse_combine(_dt(out), n, rows, D, _ptr(part_out), _ptr(part_lse), _ptr(out), _ptr(lse),
-                         _stream(stream))
+                         _stream())
     _check(st, "mla_lse_combine")
     return out, lse
 
@@ -597,6 +638,10 @@ def paged_tables(past_lens, new_lens, free_pages, block_table, *, page_size, n_t
     """One step's block tables and slot map (all int32) from the requests' lengths; the new
     pages are entered into ``block_table`` [B, max_pages] in place.  ``n_tokens``: rows of the
     step's token arrays (default: those of ``slots``), at least the sum of ``new_lens``."""
+    if stream is not None:
+        return _on_stream(stream, paged_tables, past_lens, new_lens, free_pages, block_table, page_size=page_size,
+                          n_tokens=n_tokens, kv_lens=kv_lens, cu_tokens=cu_tokens, slots=slots, positions=positions,
+                          counts=counts)
     dev = _device(block_table)
     if block_table.dim() != 2 or block_table.shape[1] < 1:
         raise ValueError("block_table must be [B, max_pages]")
@@ -623,15 +668,14 @@ def paged_tables(past_lens, new_lens, free_pages, block_table, *, page_size, n_t
     if at != _current_device():
         with torch.cuda.device(at):
             return paged_tables(past_lens, new_lens, free_pages, block_table, page_size=page_size, n_tokens=n_tokens,
-                                kv_lens=kv_lens, cu_tokens=cu_tokens, slots=slots, positions=positions, counts=counts,
-                                stream=stream)
+                                kv_lens=kv_lens, cu_tokens=cu_tokens, slots=slots, positions=positions, counts=counts)
     st = lib().mla_paged_tables(
         B, page_size, max_pages, n_free, n_tokens, _need("past_lens", past_lens, rows, i32, at),
         _need("new_lens", new_lens, rows, i32, at), _need("free_pages", free_pages, (n_free,), i32, at),
         _need("block_table", block_table, (B, max_pages), i32, at), _need("kv_lens", kv_lens, rows, i32, at),
         _need("cu_tokens", cu_tokens, (B + 1,), i32, at), _need("slots", slots, (n_tokens,), i32, at),
         _need("positions", positions, (n_tokens,), i32, at), _need("counts", counts, (2,), i32, at),
-        _raw_stream(at) if stream is None else _stream(stream))
+        _raw_stream(at))
     if st != 0:
         raise MlaError(st, "mla_paged_tables")
     return PagedTables(kv_lens, cu_tokens, slots, positions, counts)
@@ -668,6 +712,8 @@ def paged_append(d: Dims, c_kv, k_pe, rms_w, slots, positions, c_cache, kpe_cach
     """Write the tokens' normalised latent and rotated key band into their slots of the paged
     cache, in place.  ``c_kv`` [n, d_kv] and ``k_pe`` [n, d_rope] may be column ranges of wider
     rows.  Returns (c_cache, kpe_cache)."""
+    if stream is not None:
+        return _on_stream(stream, paged_append, d, c_kv, k_pe, rms_w, slots, positions, c_cache, kpe_cache)
     _device(c_kv)
     dt, tdt, at = _dt(c_kv), c_kv.dtype, c_kv.get_device()
     if c_kv.dim() != 2:
@@ -679,11 +725,11 @@ def paged_append(d: Dims, c_kv, k_pe, rms_w, slots, positions, c_cache, kpe_cach
     rows, i32 = (n,), torch.int32
     if at != _current_device():
         with torch.cuda.device(at):
-            return paged_append(d, c_kv, k_pe, rms_w, slots, positions, c_cache, kpe_cache, stream=stream)
+            return paged_append(d, c_kv, k_pe, rms_w, slots, positions, c_cache, kpe_cache)
     st = lib().mla_paged_append(
         d, dt, n, num_pages, page, c_kv.data_ptr(), cs, k_pe.data_ptr(), ks, _need("rms_w", rms_w, (d.d_kv,), tdt, at),
         _need("slots", slots, rows, i32, at), _need("positions", positions, rows, i32, at), cp, kp,
-        _raw_stream(at) if stream is None else _stream(stream))
+        _raw_stream(at))
     if st != 0:
         raise MlaError(st, "mla_paged_append")
     return c_cache, kpe_cache
@@ -701,6 +747,9 @@ def paged_decode(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens
                  workspace=None, stream=None):
     """Latent decode of one query per request over the paged cache; ``kv_lens`` and
     ``block_table`` (int32) stay on the device.  Returns (out, lse)."""
+    if stream is not None:
+        return _on_stream(stream, paged_decode, d, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, w_kv_b,
+                          out=out, lse=lse, workspace=workspace)
     dev = _device(q_nope)
     dt, tdt, at = _dt(q_nope), q_nope.dtype, q_nope.get_device()
     if q_nope.dim() != 3 or not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
@@ -711,7 +760,7 @@ def paged_decode(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens
     if at != _current_device():
         with torch.cuda.device(at):
             return paged_decode(d, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, w_kv_b, out=out, lse=lse,
-                                workspace=workspace, stream=stream)
+                                workspace=workspace)
     if not isinstance(w_kv_b, torch.Tensor):
         raise TypeError("w_kv_b: expected a torch.Tensor, got %s" % type(w_kv_b).__name__)
     _expect("w_kv_b", w_kv_b, H * (d.d_nope + d.d_v) * d.d_kv, tdt, dev)
@@ -729,7 +778,7 @@ def paged_decode(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens
     st = lib().mla_paged_decode(
         d, dt, B, num_pages, page, max_pages, *ptrs, _need("out", out, (B, H, d.d_v), tdt, at),
         _need("lse", lse, (B, H), torch.float32, at), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _raw_stream(at) if stream is None else _stream(stream))
+        _raw_stream(at))
     if st != 0:
         raise MlaError(st, "mla_paged_decode")
     return out, lse
