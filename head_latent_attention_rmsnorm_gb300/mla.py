@@ -609,7 +609,9 @@ def lse_combine(part_out, part_lse, *, out_dtype=torch.float32, out=None, lse=No
 # A serving step makes these calls for every layer, and a small step's kernels last a few
 # microseconds: the checks are one expression per tensor, and only a failed one finds out why.
 # The library launches on the current device: a call on another one's tensors makes that current.
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# Torch's own short ways to the current stream's handle and the current device, where a build has them.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
 
 
 def _need(name: str, t, shape: tuple, dtype: torch.dtype, index: int) -> int:
