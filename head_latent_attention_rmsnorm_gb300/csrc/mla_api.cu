@@ -6,7 +6,9 @@
 //  * tensor cores (tcgen05 + TMA, tc_*.cu) for bf16 calls at the dimensions they
 //    were written for; their intermediates (normalised latent, rotated RoPE bands,
 //    K_nope, V^T, q_abs, o_lat) are stored as fp16, whose 11-bit significand keeps
-//    every score within ~3e-4 of exact;
+//    every score within ~3e-4 of exact (the decodes read a bf16 cache and hold q_abs and the
+//    band as bf16 pairs instead, of which the latent scores take one or both: tc_decode.cu,
+//    paged_tc.cu);
 //  * CUDA cores (simt.cu) for fp32 calls and any other shape; their intermediates
 //    are fp32.
 #include <limits.h>

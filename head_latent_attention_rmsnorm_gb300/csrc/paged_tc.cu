@@ -39,21 +39,28 @@
 // zero in shared memory before P C reads them (whatever they held, 0 * NaN included); rank 0's scores
 // of them are masked.
 //
-// Precision.  P is bf16 (relative 2^-9 on average, on the weights of an average; the sums take the
-// unrounded ones); up to 64 heads, what that rounding leaves goes through the idle rows 64 on, at no
-// cost in MMAs.  q and the rotated band are bf16 pairs, hi + lo to 2^-17.  The scores take q_hi and
-// both halves of the band.  q_lo's latent part shifts a part's log-sum-exp by scale q_lo . o to first
-// order, which the join adds (the second order is half the variance of scale q_lo . c_j, ~1e-6 at unit
-// scale), and its weights by a relative 2^-9, like P's own rounding.  Where both count, it is taken in
-// part above 64 heads: q_lo of 256 of the 512 dims has MMAs up to 1024 keys (EX_WIDE), of 128 dims up to 4096
-// (EX_LATENT), for which tensor memory has the room; the other half of EX_WIDE's is read in shared memory.
-// Measured as the output's error over that of an fp32 evaluation rounded to bf16, 128 heads, 60 random
-// cases: up to 1.54 without, 1.49 with (at 4500 keys; an average over more keys rounds better; 8 to 64
-// heads: up to 1.41 without).  Up to 8192 keys it would be 1.47, but tiles of 7 % more MMAs hold up their
-// cluster's equal share: 64 ragged requests 294 -> 315 us.  Up to 64 keys (EX_BAND) the log-sum-exp is small
-// and bf16 pairs show in it: the band's third part has MMAs, above 64 heads q_lo of 192 dims too, and the
-// join adds the latent's third part (1 to 3 keys: 1.5e-6 -> 8e-7 of its value).  Partials are fp16
-// with a power of two per half row.
+// Precision.  q and the rotated band are bf16 pairs, hi + lo to 2^-17; P is bf16 (a relative 2^-9 on average,
+// on the weights of an average; the sums take the unrounded ones); partials are fp16 with a power of two per
+// half row.  Errors below: the output's over that of an fp32 evaluation rounded to bf16.
+//   Up to 64 heads the MMAs' idle rows, 64 on, carry the low halves of both: of q and the band in the scores,
+// which the softmax adds to the head's, and of P in the values.  Error 1.00-1.01 at every length and size of
+// the scores.
+//   Above 64 heads the scores take q_hi and both halves of the band.  What they leave of q_lo shifts a part's
+// log-sum-exp by scale q_lo . o to first order, which the join adds, and errs in the weights by scale q_lo . c_j,
+// a relative 2^-9 times the scores' deviation, and in the log-sum-exp by half the square of that: both grow
+// with the scores.  q_lo of 256 of the 512 dims has MMAs up to 1024 keys (EX_WIDE), of 128 dims up to 4096
+// (EX_LATENT): tensor memory has room for that many, the other half of EX_WIDE's is read in shared memory.
+// Measured, 128 heads, scores of standard deviation 1 / 2 / 4 / 8 (log-sum-exp: largest error relative to it):
+//    200 keys  1.43 / 1.50 / 1.63 / 1.82   6e-7 / 2e-6 / 3e-6 / 6e-6
+//   1000 keys  1.39 / 1.58 / 1.74 / 2.09   3e-7 / 1e-6 / 3e-6 / 7e-6
+//   3000 keys  1.41 / 1.66 / 1.99 / 2.54   3e-7 / 1e-6 / 4e-6 / 6e-6
+//   8192 keys  1.46 / 1.78 / 2.15 / 2.66   3e-7 / 1e-6 / 3e-6 / 7e-6
+// The limits: 128 dims up to 8192 keys too would be 1.47 for 1.49 at unit scale (60 random cases), but tiles of
+// 7 % more MMAs hold up their cluster's equal share (64 ragged requests 294 -> 315 us); all 512 dims need eight more
+// blocks of tensor memory than there are, and 64 more MMAs on a tile's 40.
+//   Up to 64 keys (EX_BAND) the log-sum-exp is small and bf16 pairs show in it: the band's third part has
+// MMAs, above 64 heads q_lo of 192 dims too, and the join adds the latent's third part (1 to 3 keys:
+// 1.5e-6 -> 8e-7 of its value).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -117,10 +124,9 @@ __device__ __forceinline__ Extra extra_of(bool paired, int keys) {
     if (keys <= SHORT_KEYS) return EX_BAND;
     return paired || keys > MIDDLE_KEYS ? EX_NONE : (keys > WIDE_KEYS ? EX_LATENT : EX_WIDE);
 }
-// The blocks of 64 latent dims, as bits, whose q_lo the scores take.
-__device__ __forceinline__ unsigned lo_blocks(bool paired, Extra ex) {
-    if (ex == EX_NONE || (ex == EX_BAND && paired)) return 0;
-    return ex == EX_LATENT ? 0x3 : (ex == EX_WIDE ? 0xf : 0xe);
+// The blocks of 64 latent dims, as bits, whose q_lo has MMAs of its own above 64 heads (up to 64 all have idle rows).
+__device__ __forceinline__ unsigned lo_blocks(Extra ex) {
+    return ex == EX_NONE ? 0 : (ex == EX_LATENT ? 0x3 : (ex == EX_WIDE ? 0xf : 0xe));
 }
 
 // ------------------------------------------------------------------------ absorb ----
@@ -303,6 +309,7 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x / per_head, rt = h / p.row_tile, r = h % p.row_tile;
     const long pitch = (long)p.row_tile * (DK / 8);
+    const bool paired = p.H <= 64;
     bool ok = true;
     if (tid == 0) {
         mbar_init(&v0.bar_w, 1);
@@ -333,12 +340,12 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int j = j0 + dj * i;
-            ql[i] = j < nb ? __ldcg((const uint4 *)(qlo + ((long)(b0 + j) * p.H + h) * DK) + d8) : make_uint4(0, 0, 0, 0);
+            ql[i] = j < nb && !paired ? __ldcg((const uint4 *)(qlo + ((long)(b0 + j) * p.H + h) * DK) + d8) : make_uint4(0, 0, 0, 0);
         }
         {   // a warp per request: the weights of its parts (up to 96)
             int s0 = 0, n = 0, ex = EX_NONE;
             if (warp < nb) {
-                ex = extra_of(p.H <= 64, keys_of(p, b0 + warp));
+                ex = extra_of(paired, keys_of(p, b0 + warp));
                 const int2 sp = __ldcg(p.spans + (long)(b0 + warp) * p.row_tiles + rt);
                 s0 = sp.x;
                 n = sp.y;
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 dot += o[i][2 * e] * __uint_as_float(q[e] << 16) + o[i][2 * e + 1] * __uint_as_float(q[e] & 0xffff0000u);
-            if ((lo_blocks(p.H <= 64, (Extra)sc[j][2]) >> (d8 >> 3)) & 1) dot = 0.f;   // the scores have it
+            if ((lo_blocks((Extra)sc[j][2]) >> (d8 >> 3)) & 1) dot = 0.f;   // the scores have it
             if (sc[j][2] == EX_BAND && j < nb) {
                 const uint4 x = __ldcg((const uint4 *)(qrest + ((long)(b0 + j) * p.H + h) * DK) + d8);
                 const uint32_t z[4] = {x.x, x.y, x.z, x.w};
@@ -531,7 +538,8 @@ constexpr uint32_t OFF_PB = VSL * VHALF, OFF_INV = OFF_PB + NPB * XSLOT, OFF_OUT
 constexpr uint32_t END0 = OFF_SUM + 2 * ROWS * 4, END1 = OFF_OUT + 8 * 4096;
 constexpr uint32_t OFF_BAR = END0 > END1 ? END0 : END1;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 512;
-constexpr uint32_t T_S = 0, T_Q = 2 * NK;   // rank 0's TMEM columns: S buffers; 32 per 64 query dims (hi 0-7, band hi and lo, lo 0-1 or EX_BAND's rest)
+constexpr uint32_t T_S = 0, T_Q = 2 * NK;   // rank 0's TMEM columns: S buffers; 32 per 64 query dims (hi 0-7, band hi and lo, lo 0-1 or
+                                             // EX_BAND's rest; paired: hi over lo 0-7, band hi over lo, EX_BAND's rest)
 constexpr float RESCALE_LOG2 = 8.0f;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 static_assert(KSTAGE % 1024 == 0 && OFF_STG % 1024 == 0 && OFF_PB % 1024 == 0 && XSLOT % 1024 == 0, "swizzle atoms");
@@ -650,7 +658,8 @@ __device__ void settle() {   // after an abandoned wait: loads in flight land be
     }
 }
 
-// PAIRED (up to 64 heads): the rows behind the heads, 64 on, carry P's low halves.
+// PAIRED (up to 64 heads): the rows behind the heads, 64 on, carry the queries' low halves in the scores and P's
+// in the values.
 template <int UNIT, bool PAIRED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     paged_attn_tc_kernel(const __grid_constant__ Maps m, const __grid_constant__ Attn a) {
@@ -759,7 +768,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             for (; more && ok; next(), ++seg) {
                 ok = wait_all(&bars[B_QREADY], seg & 1, ctl);
                 const Extra ex = extra_of(paired, w.keys);
-                const unsigned lo = lo_blocks(paired, ex);
+                const unsigned lo = paired ? 0 : lo_blocks(ex);
+                const int blocks = 9 + !paired + (ex == EX_BAND);
 #pragma unroll 1
                 for (int i = 0; i < w.nt && ok; ++i, ++n) {
                     if ((n & 1) != s) continue;
@@ -771,9 +781,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                         if (!ok) break;
                         tc_fence_after();
                         if (elect_one()) {
-                            // blocks of 64 dims: latent 0-7 (q_hi), then the key band twice (hi, lo) or three times
+                            // blocks of 64 dims: latent 0-7 (q_hi), then the key band twice (hi, lo) or three times;
+                            // paired, q_lo and the band's lo are rows of the same MMAs
                             uint64_t d = sdesc_sw128(base + g * KG1, 16, (g < 2 ? 3 : 2) * ATOM);
-                            const int j1 = g < 2 ? 3 * g + 3 : (ex == EX_BAND ? 11 : 10);
+                            const int j1 = g < 2 ? 3 * g + 3 : blocks;
 #pragma unroll 1
                             for (int j = 3 * g; j < j1; ++j) {
                                 if (j >= 8) d = sdesc_sw128(base + KG3, 16, ATOM);
@@ -817,8 +828,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             int n = 0;
             bool ok = true;
             for (; more; next()) {
-                // a warp whose 32 rows are all behind the last head only keeps the barriers
-                const bool act = w.rt * ROWS + quad * 32 < p.H;
+                // a warp whose 32 rows are all behind the last head only keeps the barriers, or, paired, brings
+                // the scores of q_lo to the warp 64 rows in front
+                const bool act = w.rt * ROWS + quad * 32 < p.H, low = paired && quad >= 2 && (quad - 2) * 32 < p.H;
                 // whether every page of the part has an id inside the cache
                 bool sound = true;
                 {
@@ -839,9 +851,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     ok = __all_sync(FULL, ok && wait_for(&bars[B_SFULL + s], ph, ctl));
                     tc_fence_after();
                     uint32_t sa[HK];
-                    if (act) {
-                        tmem_ld32_wait(sbase + s * NK, sa);
-                    }
+                    if (act || low) tmem_ld32_wait(sbase + s * NK, sa);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars[B_SFREE + s]);
@@ -849,6 +859,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     // staging slot s: its copy of tile n - 2 has read it (a fresh barrier passes)
                     ok = __all_sync(FULL, ok && wait_for(&bars[B_STGFREE + s], ph ^ 1, ctl));
                     bool rescaled = false;
+                    uint8_t *stg = smem + OFF_STG + s * P_BYTES + (paired ? row & 63 : row) * 128;   // (row + 64: the same swizzle)
+                    if (paired && (act || low)) {
+                        // q_lo's scores pass through the pieces of the staging slot that the head's thread
+                        // fills with P next
+                        auto piece = [&](int q) { return (float4 *)(stg + (((h * (HK / 8) + (q & 3)) ^ (row & 7)) << 4)) + (q >> 2) * (64 * 128 / 16); };
+                        if (low) {
+#pragma unroll
+                            for (int q = 0; q < HK / 4; ++q)
+                                *piece(q) = make_float4(__uint_as_float(sa[4 * q]), __uint_as_float(sa[4 * q + 1]),
+                                                        __uint_as_float(sa[4 * q + 2]), __uint_as_float(sa[4 * q + 3]));
+                        }
+                        named_bar_sync(5 + 2 * (quad & 1) + h, 64);
+                        if (act) {
+#pragma unroll
+                            for (int q = 0; q < HK / 4; ++q) {
+                                const float4 x = *piece(q);
+                                sa[4 * q] = __float_as_uint(__uint_as_float(sa[4 * q]) + x.x);
+                                sa[4 * q + 1] = __float_as_uint(__uint_as_float(sa[4 * q + 1]) + x.y);
+                                sa[4 * q + 2] = __float_as_uint(__uint_as_float(sa[4 * q + 2]) + x.z);
+                                sa[4 * q + 3] = __float_as_uint(__uint_as_float(sa[4 * q + 3]) + x.w);
+                            }
+                        }
+                    }
                     if (act) {
                         const int key0 = (w.k0 + i) * NK + h * HK;
                         if (groups != (1u << NGRP) - 1 || key0 + HK > w.keys) {
@@ -881,7 +914,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                         rescaled = __any_sync(FULL, need && i > 0);
                         const float m_eff = top == -INFINITY ? 0.f : top;
                         float ra[4] = {0.f, 0.f, 0.f, 0.f};
-                        uint8_t *stg = smem + OFF_STG + s * P_BYTES + row * 128;   // (row + 64: the same swizzle)
 #pragma unroll
                         for (int q = 0; q < HK / 8; ++q) {
                             uint32_t pk[4], lo[4];
@@ -941,7 +973,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         } else if (warp == 18) {
             // ------------------------------- the parts' query boxes: 64 dims x 128 heads each, hi of the latent
             // (0-7), hi and lo of the band (8, 9), Extra's (10); all in flight at once in the key stages, which
-            // the last part's MMAs have left, and the two boxes behind them
+            // the last part's MMAs have left, and the two boxes behind them.  Paired: lo in the rows 64 on of hi's
+            // boxes (0-8), the band's rest (9)
             int seg = 0;
             uint32_t wide = 0;   // parity of the moves waited for below
             bool go = lane == 0;
@@ -950,6 +983,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 const int boxes = ex == EX_NONE ? 10 : 11;
                 go = wait_for(&bars[B_QFREE], (seg & 1) ^ 1, ctl);   // (passes at first)
                 if (!go) break;
+                if (paired) {
+                    mbar_arrive_expect_tx(&bars[B_QFULL], (18 + (ex == EX_BAND)) * 128 * a.q_rows);
+#pragma unroll 1
+                    for (int j = 0; j < 9; ++j) {
+                        tma_load_3d(smem + j * 16384, j < 8 ? &m.qh : &m.rh, &bars[B_QFULL], j < 8 ? 64 * j : 0, 0, w.b);
+                        tma_load_3d(smem + j * 16384 + 64 * 128, j < 8 ? &m.ql : &m.rl, &bars[B_QFULL], j < 8 ? 64 * j : 0, 0, w.b);
+                    }
+                    if (ex == EX_BAND) tma_load_3d(smem + OFF_Q, &m.rr, &bars[B_QFULL], 0, 0, w.b);
+                    continue;
+                }
                 mbar_arrive_expect_tx(&bars[B_QFULL], boxes * 128 * a.q_rows);
 #pragma unroll 1
                 for (int j = 0; j < boxes; ++j) {
@@ -957,7 +1000,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     tma_load_3d(smem + (j < 9 ? j * 16384 : OFF_Q + (j - 9) * 16384), map, &bars[B_QFULL], j < 8 ? 64 * j : 0,
                                 w.rt * ROWS, w.b);
                 }
-                if (!(lo_blocks(paired, ex) & 0xc)) continue;
+                if (!(lo_blocks(ex) & 0xc)) continue;
                 // lo of dims 128-255 for the MMAs to read in shared memory, once the two boxes there have moved
                 go = wait_for(&bars[B_QNEXT], wide, ctl);
                 if (!go) break;
@@ -974,13 +1017,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             int n = 0;
             bool ok = true;
             for (; more && ok; n += w.nt, next()) {
-                const bool act = w.rt * ROWS + quad * 32 < p.H;
+                const bool act = w.rt * ROWS + (paired ? quad & 1 : quad) * 32 < p.H;
                 const Extra ex = extra_of(paired, w.keys);
-                const int boxes = ex == EX_NONE ? 10 : 11;
+                const int boxes = paired ? 9 + (ex == EX_BAND) : ex == EX_NONE ? 10 : 11;
                 // q_lo of dims 64-127 has no box: each thread's 128 bytes come straight from memory, under
                 // the boxes' flight
                 uint4 x[8];
-                const unsigned lo = lo_blocks(paired, ex);
+                const unsigned lo = paired ? 0 : lo_blocks(ex);
                 if ((lo & 2) && act) {
                     const bf16 *src = a.qlo + ((long)w.b * p.H + min(w.rt * ROWS + row, p.H - 1)) * DK + 64;
 #pragma unroll
@@ -1012,6 +1055,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                             v[4 * e + 1] = x.y;
                             v[4 * e + 2] = x.z;
                             v[4 * e + 3] = x.w;
+                        }
+                        if (paired && quad >= 2 && j == 9) {   // the band's rest has rows of the heads only
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = 0;
                         }
                         tmem_st32(dst + j * 32, v);
                     }

@@ -33,7 +33,7 @@
  *    input or each other (MLA_ERR_ALIAS).
  *  - On any error status nothing has been launched, except MLA_ERR_CUDA, which
  *    reports a failed launch or failed CUDA runtime call.
- *  - Precision of the bf16 tensor-core kernels: their score operands (normalised
+ *  - Precision of the bf16 tensor-core kernels (mla_paged_decode's stands there): their score operands (normalised
  *    latent, rotated RoPE bands, K_nope, q_abs) and P are fp16, so every such value
  *    must lie inside fp16's range (|x| < 65504), and a log-sum-exp carries an absolute
  *    error of up to about 2^-11 of the largest |lse| of the call (measured 5.7e-4 at
@@ -311,9 +311,13 @@ mla_status mla_paged_append(const mla_dims *dims, mla_dtype dtype, int n_tokens,
  * Key tiles of the whole batch are divided evenly among the GPU's SMs whatever the
  * lengths are, and the parts of a request merged by the log-sum-exp rescale; results do not depend on
  * timing (the same bits for the same call).  bf16 with d_kv 512, d_nope = d_v = 128, d_rope 64 and pages of
- * a multiple of eight tokens runs on the tensor cores: against an fp32 evaluation of the same inputs, rounded to
- * bf16, the output's error is 1.0 to 1.5 times as large at unit scale, and the log-sum-exp off by ~1e-6; every other
- * case runs in fp32 arithmetic on the CUDA cores.  d_kv <= 512, d_kv + d_rope <= 640, d_nope <= 1024
+ * a multiple of eight tokens runs on the tensor cores, every other case in fp32 arithmetic on the CUDA cores.
+ * Precision of the tensor-core form, the output's error over that of an fp32 evaluation of the same inputs rounded
+ * to bf16, and the log-sum-exp's relative to its value: up to 64 heads 1.0 and < 4e-6 whatever the scores' size;
+ * above 64 heads they grow with the scores' standard deviation, because the softmax weights meet a bf16 rounding
+ * of the absorbed query: up to 1.5 and 6e-7 at a deviation of 1, 1.8 and 2e-6 at 2, 2.2 and 4e-6 at 4, 2.7 and 7e-6
+ * at 8 (200 to 8192 keys; shorter requests are the more exact ones).  mla_set_path_override(1) selects
+ * the fp32 kernels.  d_kv <= 512, d_kv + d_rope <= 640, d_nope <= 1024
  * (MLA_ERR_UNSUPPORTED otherwise).  The workspace belongs to one call at a time: calls that may overlap
  * (other streams, graphs replayed side by side) each need their own.
  */
