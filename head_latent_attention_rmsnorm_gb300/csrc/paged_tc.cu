@@ -13,7 +13,7 @@
 // accumulator, 128 x 512, is a whole SM's tensor memory, so an item runs on two SMs:
 //   rank 0 (scores): the queries in TMEM; 64-key tiles of the cache (latent + key band) through a
 //     two-deep TMA ring that fills and drains in three groups of 64-dim blocks, a producer warp for
-//     each; S = Q K^T, two S buffers; online softmax by eight warps (two threads per head); P in
+//     each; S = Q K^T, two S buffers; online softmax by eight warps (two threads per head, four up to 64 heads); P in
 //     bf16 to rank 1 by bulk copies into its two P slots;
 //   rank 1 (accumulator): O in TMEM; streams the same tiles' latent in halves of 256 dims (L2 hits:
 //     an idle warp prefetches rank 0's next tiles) and issues O += P C.
@@ -817,20 +817,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             }
         } else if (warp >= 2 && warp < 10) {
             // ---------------------------------------------------------- softmax warps
-            // two threads per head: warps 2-5 take keys 0-31 of a tile, warps 6-9 keys 32-63.  An
-            // abandoned wait clears `ok`; the walk goes on without waiting, so that both warps of a row
-            // reach every barrier.
+            // two threads per head: warps 2-5 take keys 0-31 of a tile, warps 6-9 keys 32-63.  Paired, the
+            // row 64 behind a head's has q_lo's scores: its two threads exchange halves with the head's and
+            // each of the four takes 16 keys (with the head's two alone 76 requests of 16384 keys, 16
+            // heads, took 279 us a call, with four 250).  An abandoned wait clears `ok`; the walk goes on without waiting, so
+            // that all warps of a row reach every barrier.
+            constexpr int HK = NK / 2, PER = paired ? 4 : 2, KN = NK / PER;   // scores here, threads of a head, keys of each
+            constexpr int RED = ROWS * 2 / PER;
             const int quad = warp & 3, row = quad * 32 + lane, h = (warp - 2) >> 2;
-            const uint32_t sbase = tmem + ((uint32_t)(quad * 32) << 16) + T_S + h * (NK / 2);
+            const int head = paired ? row & 63 : row, lo_row = paired ? quad >> 1 : 0, me = h + 2 * lo_row;
+            const uint32_t sbase = tmem + ((uint32_t)(quad * 32) << 16) + T_S + h * HK;
             const float c = a.scale_log2;
-            float *red = (float *)(smem + OFF_RED) + row, *sums = (float *)(smem + OFF_SUM) + row;
-            constexpr int HK = NK / 2;
+            float *red = (float *)(smem + OFF_RED) + head, *sums = (float *)(smem + OFF_SUM) + head;
             int n = 0;
             bool ok = true;
             for (; more; next()) {
-                // a warp whose 32 rows are all behind the last head only keeps the barriers, or, paired, brings
-                // the scores of q_lo to the warp 64 rows in front
-                const bool act = w.rt * ROWS + quad * 32 < p.H, low = paired && quad >= 2 && (quad - 2) * 32 < p.H;
+                // a warp without a head only keeps the barriers
+                const bool act = w.rt * ROWS + (paired ? quad & 1 : quad) * 32 < p.H;
                 // whether every page of the part has an id inside the cache
                 bool sound = true;
                 {
@@ -840,7 +843,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     for (int col = c0 + lane; col <= c1; col += 32) sound = sound && (unsigned)__ldg(ids + col) < (unsigned)p.num_pages;
                     sound = __all_sync(FULL, sound);
                 }
-                float top = -INFINITY, l = 0.f;   // running maximum (scaled, log2 units), this half's sum
+                float top = -INFINITY, l = 0.f;   // running maximum (scaled, log2 units), this thread's sum
 #pragma unroll 1
                 for (int i = 0; i < w.nt; ++i, ++n) {
                     const int s = n & 1;
@@ -850,8 +853,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     if (!sound) groups = __ballot_sync(FULL, lane < NGRP && row_of(a, w, (w.k0 + i) * NK + lane * 8) >= 0);
                     ok = __all_sync(FULL, ok && wait_for(&bars[B_SFULL + s], ph, ctl));
                     tc_fence_after();
-                    uint32_t sa[HK];
-                    if (act || low) tmem_ld32_wait(sbase + s * NK, sa);
+                    uint32_t sa[HK];   // paired: the 16 keys that this thread takes, then those it hands on
+                    if (act) {
+                        if (paired) tmem_ld16x2_wait(sbase + s * NK + lo_row * KN, sbase + s * NK + (lo_row ^ 1) * KN, sa);
+                        else tmem_ld32_wait(sbase + s * NK, sa);
+                    }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars[B_SFREE + s]);
@@ -859,52 +865,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     // staging slot s: its copy of tile n - 2 has read it (a fresh barrier passes)
                     ok = __all_sync(FULL, ok && wait_for(&bars[B_STGFREE + s], ph ^ 1, ctl));
                     bool rescaled = false;
-                    uint8_t *stg = smem + OFF_STG + s * P_BYTES + (paired ? row & 63 : row) * 128;   // (row + 64: the same swizzle)
-                    if (paired && (act || low)) {
-                        // q_lo's scores pass through the pieces of the staging slot that the head's thread
-                        // fills with P next
-                        auto piece = [&](int q) { return (float4 *)(stg + (((h * (HK / 8) + (q & 3)) ^ (row & 7)) << 4)) + (q >> 2) * (64 * 128 / 16); };
-                        if (low) {
+                    if (act) {
+                        uint8_t *stg = smem + OFF_STG + s * P_BYTES + head * 128;   // (row + 64: the same swizzle)
+                        // 16-byte piece q of this thread's keys of P, or of thread `of`'s
+                        auto piece = [&](int q, int of) {
+                            return (uint4 *)(stg + ((((of & 1) * (HK / 8) + (of >> 1) * (KN / 8) + q) ^ (row & 7)) << 4));
+                        };
+                        if (paired) {
+                            // through the pieces of the staging slot that the receiving thread fills with P next
+                            constexpr int LO = 64 * 128 / 16;
 #pragma unroll
-                            for (int q = 0; q < HK / 4; ++q)
-                                *piece(q) = make_float4(__uint_as_float(sa[4 * q]), __uint_as_float(sa[4 * q + 1]),
-                                                        __uint_as_float(sa[4 * q + 2]), __uint_as_float(sa[4 * q + 3]));
-                        }
-                        named_bar_sync(5 + 2 * (quad & 1) + h, 64);
-                        if (act) {
+                            for (int q = 0; q < KN / 4; ++q) {
+                                const uint32_t *x = sa + KN + 4 * q;
+                                piece(q & 1, me ^ 2)[(q >> 1) * LO] = make_uint4(x[0], x[1], x[2], x[3]);
+                            }
+                            named_bar_sync(5 + 2 * (quad & 1) + h, 64);
 #pragma unroll
-                            for (int q = 0; q < HK / 4; ++q) {
-                                const float4 x = *piece(q);
-                                sa[4 * q] = __float_as_uint(__uint_as_float(sa[4 * q]) + x.x);
-                                sa[4 * q + 1] = __float_as_uint(__uint_as_float(sa[4 * q + 1]) + x.y);
-                                sa[4 * q + 2] = __float_as_uint(__uint_as_float(sa[4 * q + 2]) + x.z);
-                                sa[4 * q + 3] = __float_as_uint(__uint_as_float(sa[4 * q + 3]) + x.w);
+                            for (int q = 0; q < KN / 4; ++q) {
+                                const uint4 x = piece(q & 1, me)[(q >> 1) * LO];
+                                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) sa[4 * q + e] = __float_as_uint(__uint_as_float(sa[4 * q + e]) + __uint_as_float(y[e]));
                             }
                         }
-                    }
-                    if (act) {
-                        const int key0 = (w.k0 + i) * NK + h * HK;
-                        if (groups != (1u << NGRP) - 1 || key0 + HK > w.keys) {
+                        const int key0 = (w.k0 + i) * NK + h * HK + lo_row * KN;
+                        if (groups != (1u << NGRP) - 1 || key0 + KN > w.keys) {
                             const int end = w.keys - key0;
-                            groups >>= 4 * h;
+                            groups >>= 4 * h + 2 * lo_row;
 #pragma unroll
-                            for (int e = 0; e < HK; ++e)
+                            for (int e = 0; e < KN; ++e)
                                 if (e >= end || !((groups >> (e >> 3)) & 1)) sa[e] = 0xff800000u;   // -inf
                         }
                         float mx[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(sa[e]), __uint_as_float(sa[e + 4]));
 #pragma unroll
-                        for (int e = 8; e < HK; e += 8)
+                        for (int e = 8; e < KN; e += 8)
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
                                 mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(sa[e + q]), __uint_as_float(sa[e + q + 4])));
                         float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                        red[(s * 2 + h) * ROWS] = mt;
-                        named_bar_sync(1 + quad, 64);   // the two warps of these 32 heads
-                        mt = fmaxf(mt, red[(s * 2 + (h ^ 1)) * ROWS]) * c;
-                        // O is rescaled only when the maximum grows by more than 2^8 (both threads of a
-                        // row decide alike from the same numbers)
+                        red[(s * PER + me) * RED] = mt;
+                        named_bar_sync(1 + (paired ? quad & 1 : quad), 32 * PER);   // the warps of these 32 heads
+#pragma unroll
+                        for (int k = 1; k < PER; ++k) mt = fmaxf(mt, red[(s * PER + (me ^ k)) * RED]);
+                        mt *= c;
+                        // O is rescaled only when the maximum grows by more than 2^8 (all threads of a
+                        // head decide alike from the same numbers)
                         const bool need = mt > top + RESCALE_LOG2;
                         float alpha = 1.f;
                         if (need) {
@@ -915,7 +922,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                         const float m_eff = top == -INFINITY ? 0.f : top;
                         float ra[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int q = 0; q < HK / 8; ++q) {
+                        for (int q = 0; q < KN / 8; ++q) {
                             uint32_t pk[4], lo[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
@@ -925,21 +932,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                                 pk[e] = pack_bf16(p0, p1);
                                 if (paired) lo[e] = pack_bf16(p0 - __uint_as_float(pk[e] << 16), p1 - __uint_as_float(pk[e] & 0xffff0000u));
                             }
-                            uint4 *at = (uint4 *)(stg + (((h * (HK / 8) + q) ^ (row & 7)) << 4));
+                            uint4 *at = piece(q, me);
                             at[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                             if (paired) at[64 * 128 / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         }
                         l = l * alpha + ((ra[0] + ra[1]) + (ra[2] + ra[3]));
-                        if (i == w.nt - 1) {   // the row's sum, with the partner's half
-                            sums[h * ROWS] = l;
-                            named_bar_sync(1 + quad, 64);
-                            const float lt = l + sums[(h ^ 1) * ROWS];
-                            if (h == 0) {
+                        if (i == w.nt - 1) {   // the row's sum, with the other threads'
+                            sums[me * RED] = l;
+                            named_bar_sync(1 + (paired ? quad & 1 : quad), 32 * PER);
+                            float lt = l;
+#pragma unroll
+                            for (int k = 1; k < PER; ++k) lt += sums[(me ^ k) * RED];
+                            if (me == 0) {
                                 ((float *)(ext + X_INVL))[row] = lt == 0.f ? 0.f : 1.f / lt;
                                 ((float *)(ext + X_LSE))[row] = lt == 0.f ? -INFINITY : m_eff + log2f(lt);
                             }
                         }
-                        if (h == 0) {
+                        if (me == 0) {
                             ((float *)(ext + X_ALPHA))[row] = alpha;
                             if (paired) ((float *)(ext + X_ALPHA))[row + 64] = alpha;
                         }
