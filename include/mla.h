@@ -260,9 +260,13 @@ mla_status mla_lse_combine(mla_dtype out_dtype, int n_splits, int rows, int D,
  * lies in slot block_table[b][p / page_size] * page_size + p % page_size, where row b of
  * block_table [B, max_pages] (int32) holds the ids of its pages.  A step of a server is
  * mla_paged_tables (which pages and slots the new tokens take), mla_paged_append (their
- * rows written) and mla_paged_decode (one query per request attends); all three take the lengths
- * from device memory, so the calls may be captured once and replayed as requests grow.  Their int32
- * arrays need 4-byte alignment only (a slice of a list of free pages may start anywhere).
+ * rows written) and mla_paged_decode (one query per request attends); all three take lengths, tables
+ * and page ids from device memory, so the calls may be captured once and replayed as requests grow.  What
+ * a capture fixes is the addresses and n_free, n_tokens, B and max_pages: mla_paged_tables takes pages from
+ * the front of free_pages at every replay and does not move that front, so before the next replay the
+ * list is moved up by counts[0] (on the device, as part of the capture, if the host is not to wait), and past_lens
+ * is set to kv_lens.  Their int32 arrays need 4-byte alignment only (a slice of a list of free pages may
+ * start anywhere).
  *
  * mla_paged_tables: one step's tables from the requests' lengths.  past_lens [B]: tokens that a
  * request holds already; new_lens [B]: tokens it gains; free_pages [n_free]: ids of free pages,
