@@ -52,7 +52,8 @@ struct PagedDecode {
 cudaError_t paged_decode_simt(const PagedDecode &p, cudaStream_t st);
 
 // The tensor-core form (bf16): these dimensions and page size, any number of heads.
-constexpr int PAGED_TC_WORKERS = 76, PAGED_TC_TILE = 64;   // pairs of SMs, keys per tile
+// pairs of SMs of a GB300, keys per tile (no worker waits for another: with fewer SMs free they take turns)
+constexpr int PAGED_TC_WORKERS = 76, PAGED_TC_TILE = 64;
 bool paged_tc_supported(int Dk, int Dn, int Dr, int Dv, int page);
 cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st);
 cudaError_t paged_tc_read_and_clear_error(unsigned *flags, cudaStream_t st);

@@ -52,8 +52,8 @@ __device__ __forceinline__ float2 turn_cs(unsigned long long turns, int pos) {
     return make_float2(c, s);
 }
 
-// x / d for 0 <= x < 2^31 by a multiplication (round-up multiplier; the sum cannot overflow, as the high
-// product is at most x).
+// x / d for 0 <= x < 2^31 by a multiplication (round-up multiplier, Granlund and Montgomery 1994; the sum cannot
+// overflow, as the high product is at most x).
 struct Divisor {
     uint32_t mul, shift;
 };

@@ -22,7 +22,7 @@
 // land in the key stages, in flight at once, while the softmax and rank 1 finish.
 //
 // What bounds it.  64 ragged requests of up to 32768 keys, 128 heads: the attention 275-285 us, 0.96 us
-// per tile and pair of SMs, 5.3-5.6 TB/s; 16 heads 5.8 TB/s; without its MMAs the kernel moves 6.6 TB/s
+// per tile and pair of SMs, 5.3-5.6 TB/s; 16 heads 6.0-6.2 TB/s; without its MMAs the kernel moves 6.6 TB/s
 // (the copy peak is 6.8).  No unit is full: of a tile's 1800 cycles rank 0's tensor pipe needs 1280
 // (40 MMAs of N = 64 with A in TMEM, 32 cycles each) and rank 1's 1024, DRAM runs at 71 %, L2 at 66 %,
 // shared memory below 50 %.  The MMAs' issue is part of the chain: one issuing warp takes 1.22 us a tile,
@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
 // out the requests, or, for one or two requests, their parts; the product is tcgen05 (M = 128 value
 // dims, N = 32 requests, o as bf16 hi + lo, so that it is as exact as fp32 o): 64 MMAs of 32
 // columns, where mma.sync took 7500 cycles a group.  128 heads, events around it alone: one request
-// 14 us, 64 requests 27 us (33 with mma.sync).
+// 14-16 us, 64 requests 26-28 us (33 with mma.sync); barriers and loads from memory share the stalls, and at 64
+// registers 46 bytes spill.
 constexpr int JB = 32, JNT = 1024, JMAXC = 80;
 constexpr int JO = DV * DK * 2;                // W_V: eight boxes of 64 dims x 128 rows
 constexpr int JBLK = JB * 128;                 // o: 64 dims x 32 requests
