@@ -371,8 +371,8 @@ def _stream() -> int:
 def _on_stream(stream, fn, *args, **kw):
     """``fn(*args, **kw)`` with ``stream`` as the current one.  What the call allocates then belongs to
     the stream that its kernels run on: a workspace dropped on return is not handed to other work
-    while they use it, and an output's memory holds nothing that other work still reads.  Outputs
-    are recorded for the caller's stream too, which may read them until they are dropped."""
+    while they use it, and an output's memory holds nothing that other work still reads.  Outputs that
+    the call allocates are recorded for the caller's stream too, which may read them until they are dropped."""
     like = next((a for a in (*args, *kw.values()) if isinstance(a, torch.Tensor) and a.is_cuda), None)
     if like is None:
         return fn(*args, **kw)   # refuses its tensors
@@ -383,11 +383,13 @@ def _on_stream(stream, fn, *args, **kw):
         stream = caller if handle == caller.cuda_stream else torch.cuda.ExternalStream(handle, device=like.device)
     if stream.device != like.device:
         raise ValueError("stream: on %s, the call's tensors are on %s" % (stream.device, like.device))
+    given = {id(t) for a in (*args, *kw.values()) for t in (a.values() if isinstance(a, dict) else (a,))}
     with torch.cuda.stream(stream):
         result = fn(*args, **kw)
     if stream != caller:
         for t in result.values() if isinstance(result, dict) else result if isinstance(result, tuple) else (result,):
-            t.record_stream(caller)
+            if id(t) not in given:
+                t.record_stream(caller)
     return result
 
 
