@@ -1122,7 +1122,7 @@ mla_status paged_decode_shape(const mla_dims *d, mla_dtype dt, int B, int page_s
     if (B < 0 || page_size < 1 || max_pages < 1 || (long)max_pages * page_size > 1 << 30 ||
         ((long)B + 3) * d->n_heads > INT_MAX / 4 || ((long)B + 3) / 4 * d->n_heads * (((long)d->d_v + 31) / 32) > INT_MAX)
         return MLA_ERR_SHAPE;
-    p->B = B;
+    p->B = p->T = B;
     p->H = d->n_heads;
     p->Dk = d->d_kv;
     p->Dn = d->d_nope;
@@ -1157,10 +1157,8 @@ mla_status paged_decode_shape(const mla_dims *d, mla_dtype dt, int B, int page_s
     return MLA_OK;
 }
 
-size_t paged_decode_ws(PagedDecode *p, void *base) {
-    Carve c;
-    c.base = (char *)base;
-    const size_t rows = (size_t)p->B * p->H, slots = (size_t)p->workers + (size_t)p->B * p->row_tiles;
+void paged_decode_carve(PagedDecode *p, Carve &c) {
+    const size_t rows = (size_t)p->T * p->H, slots = (size_t)p->workers + (size_t)p->B * p->row_tiles;
     p->tile_off = (long *)c.take(((size_t)p->B + 1) * sizeof(long));
     if (p->tc) {
         p->parts = (PagedPart *)c.take(slots * sizeof(PagedPart));
@@ -1176,6 +1174,41 @@ size_t paged_decode_ws(PagedDecode *p, void *base) {
         p->po32 = (float *)c.take(slots * p->row_tile * p->Dk * 4);
     }
     p->pl = (float *)c.take(slots * p->row_tile * 4);
+}
+
+size_t paged_decode_ws(PagedDecode *p, void *base) {
+    Carve c;
+    c.base = (char *)base;
+    paged_decode_carve(p, c);
+    return align_up(c.off, 256);
+}
+
+// A step's tokens in the absorbed form, a round of them at a time.
+struct PagedRound {
+    int *lens, *limits;   // keys of each group, of each token
+    int2 *of;
+    int4 *groups;
+};
+mla_status paged_step_shape(const mla_dims *d, mla_dtype dt, int B, int n_tokens, int page_size, int max_pages,
+                            PagedDecode *p) {
+    if (d && d->n_heads > 0 && (n_tokens < 0 || ((long)n_tokens + 3) * d->n_heads > INT_MAX / 4)) return MLA_ERR_SHAPE;
+    mla_status st = paged_decode_shape(d, dt, std::min(n_tokens, PAGED_ROUND), page_size, max_pages, p);
+    if (st != MLA_OK) return st;
+    if (B < 0) return MLA_ERR_SHAPE;
+    if (p->tc) p->row_tile = p->H <= 64 ? 64 : 128;   // few heads: several tokens of a request share an item
+    p->row_tiles = (p->H + p->row_tile - 1) / p->row_tile;
+    return MLA_OK;
+}
+
+size_t paged_step_ws(PagedDecode *p, PagedRound *r, void *base) {
+    Carve c;
+    c.base = (char *)base;
+    paged_decode_carve(p, c);
+    const size_t T = p->T;
+    r->lens = (int *)c.take(T * sizeof(int));
+    r->limits = (int *)c.take(T * sizeof(int));
+    r->of = (int2 *)c.take(T * sizeof(int2));
+    r->groups = (int4 *)c.take(T * sizeof(int4));
     return align_up(c.off, 256);
 }
 }  // namespace
@@ -1223,6 +1256,71 @@ mla_status mla_paged_decode(const mla_dims *dims, mla_dtype dtype, int B, int nu
     p.lse = lse;
     g_last_path = p.tc ? 2 : 1;
     return cuda_status(p.tc ? paged_decode_tc(p, (cudaStream_t)cuda_stream) : paged_decode_simt(p, (cudaStream_t)cuda_stream));
+}
+
+size_t mla_paged_prefill_workspace(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int page_size, int max_pages) {
+    PagedDecode p{};
+    PagedRound r{};
+    if (paged_step_shape(dims, dtype, B, n_tokens, page_size, max_pages, &p) != MLA_OK || B == 0 || n_tokens == 0) return 0;
+    return paged_step_ws(&p, &r, nullptr);
+}
+
+mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int num_pages, int page_size,
+                             int max_pages, const void *q_nope, const void *q_pe, const void *c_cache,
+                             const void *kpe_cache, const int *block_table, const int *kv_lens, const int *cu_tokens,
+                             const int *positions, const void *w_kv_b, void *out, float *lse, void *workspace,
+                             size_t workspace_bytes, void *cuda_stream) {
+    PagedDecode p{};
+    PagedRound r{};
+    mla_status st = paged_step_shape(dims, dtype, B, n_tokens, page_size, max_pages, &p);
+    if (st != MLA_OK) return st;
+    if (num_pages < 1 || (long)num_pages * page_size > INT_MAX) return MLA_ERR_SHAPE;
+    if (B == 0 || n_tokens == 0) return MLA_OK;
+    const void *ptrs[] = {q_nope, q_pe, c_cache, kpe_cache, w_kv_b, out, lse, workspace};
+    for (const void *q : ptrs)
+        if (!q) return MLA_ERR_NULL;
+    const int *idx[] = {block_table, kv_lens, cu_tokens, positions};
+    for (const int *q : idx)
+        if (!q) return MLA_ERR_NULL;
+    for (const void *q : ptrs)
+        if (!aligned16(q)) return MLA_ERR_ALIGN;
+    for (const int *q : idx)
+        if (!aligned4(q)) return MLA_ERR_ALIGN;
+    const size_t need = paged_step_ws(&p, &r, workspace);
+    if (workspace_bytes < need) return MLA_ERR_WORKSPACE;
+    const size_t es = ty_size(p.ty), rows = (size_t)n_tokens * p.H, keys = (size_t)num_pages * page_size, e = sizeof(int);
+    Range in[] = {rng(q_nope, rows * p.Dn * es), rng(q_pe, rows * p.Dr * es), rng(c_cache, keys * p.Dk * es),
+                  rng(kpe_cache, keys * p.Dr * es), rng(block_table, (size_t)B * max_pages * e), rng(kv_lens, B * e),
+                  rng(cu_tokens, ((size_t)B + 1) * e), rng(positions, n_tokens * e),
+                  rng(w_kv_b, (size_t)p.H * (p.Dn + p.Dv) * p.Dk * es)};
+    Range outs[] = {rng(out, rows * p.Dv * es), rng(lse, rows * 4), rng(workspace, need)};
+    st = check_alias(in, 9, outs, 3);
+    if (st != MLA_OK) return st;
+    p.num_pages = num_pages;
+    p.c_cache = c_cache;
+    p.kpe_cache = kpe_cache;
+    p.w = w_kv_b;
+    p.table = block_table;
+    p.lens = r.lens;
+    p.of = r.of;
+    p.limits = r.limits;
+    p.groups = r.groups;
+    const PagedStep step{B, n_tokens, cu_tokens, positions, kv_lens};
+    g_last_path = p.tc ? 2 : 1;
+    for (int s0 = 0; s0 < n_tokens; s0 += PAGED_ROUND) {
+        PagedDecode q = p;
+        const size_t at = (size_t)s0 * p.H;
+        q.T = q.B = std::min(n_tokens - s0, PAGED_ROUND);
+        q.q_nope = (const char *)q_nope + at * p.Dn * es;
+        q.q_pe = (const char *)q_pe + at * p.Dr * es;
+        q.pos = positions + s0;
+        q.out = (char *)out + at * p.Dv * es;
+        q.lse = lse + at;
+        cudaStream_t cs = (cudaStream_t)cuda_stream;
+        MLA_TRY(launch_paged_plan(q, step, s0, r.lens, r.of, r.limits, r.groups, cs));
+        MLA_TRY(p.tc ? paged_decode_tc(q, cs) : paged_decode_simt(q, cs));
+    }
+    return MLA_OK;
 }
 
 const char *mla_status_string(mla_status s) {

@@ -1,4 +1,4 @@
-// paged.h -- host interface of the paged-cache kernels (paged.cu, paged_simt.cu).
+// paged.h -- host interface of the paged-cache kernels (paged*.cu).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -18,28 +18,40 @@ cudaError_t launch_paged_append(int ty, int T, long n_slots, int Dk, int Dr, flo
                                 long c_stride, const void *k, long k_stride, const void *w, const int *slots,
                                 const int *positions, void *c_cache, void *kpe_cache, cudaStream_t st);
 
-// One decode call.  A work item is (request b, row tile of `row_tile` heads); its keys are cut
+// One absorbed-form call: decode (one query per request), or the tokens of a step.  A query row is a head of a
+// token, rows T H.  Rows of one request that lie together form a group: a decode's request with its H
+// rows, or a few tokens of one request, as many as fit `row_tile` rows (of more heads one).  A work item is
+// (group b, row tile of `row_tile` rows); its keys are cut
 // into tiles of `tile` keys, all items' T tiles are numbered through, and worker c of W takes tiles
 // [c q, (c + 1) q) with q = max(min_tiles, ceil(T / W)).  The part of item i that worker c computes goes
 // to partial slot c + i: unique, because going along the tiles every cut raises c or i.
 struct alignas(16) PagedPart {   // what a worker computes of one item
-    int b, rt, k0, nt;           // request, row tile, first key tile, key tiles
-    int keys, next;              // the request's length; distance to the worker's next part, 0 for none
-    int pad[2];
+    int row, q, k0, nt;          // row of the block table, first query row, first key tile, key tiles
+    int keys, next;              // the group's length; distance to the worker's next part, 0 for none
+    int rows, pad;               // query rows of the item
 };
 struct PagedDecode {
-    int B, H, Dk, Dn, Dr, Dv;
+    int B, H, Dk, Dn, Dr, Dv;        // groups (decode: requests), ..
+    int T;                           // tokens (decode: B)
     int num_pages, page, max_pages;
     int ty;
     bool tc;                         // the tensor-core form
     float scale, base;
     const void *q_nope, *q_pe, *c_cache, *kpe_cache, *w;
-    const int *table, *lens;
+    const int *table, *lens;         // lens [B]: the groups' keys
+    // The tokens of a step (null for decode): each one's position, group (-1: not computed here, its output
+    // stays) and first row in the group, and the keys that it sees; each group's row of the table, first query
+    // row and number of rows.  done: tokens that are nonzero there have no group (null: none).
+    const int *pos;
+    const int2 *of;
+    const int *limits;
+    const int4 *groups;
+    const int *done;
     void *out;
     float *lse;
-    int row_tile, row_tiles, tile;   // heads per item, items per request, keys per tile
+    int row_tile, row_tiles, tile;   // rows per item, items per group, keys per tile
     int workers, min_tiles;          // most workers, fewest tiles that make one worker more
-    long *tile_off;                  // [B + 1] first tile of request b, for one row tile
+    long *tile_off;                  // [B + 1] first tile of group b, for one row tile
     PagedPart *parts;                // [slots], the tensor-core form's
     int *first;                      // [2][workers]: a worker's first part, its number of tiles
     int2 *spans;                     // [B row_tiles]: an item's first part, its number of parts
@@ -49,7 +61,22 @@ struct PagedDecode {
     float *po32, *pl, *pscale;
     __half *po;
 };
+// The launches of a call: absorb, attention, join.  Of a step's tokens behind launch_paged_plan.
 cudaError_t paged_decode_simt(const PagedDecode &p, cudaStream_t st);
+
+// A step: request b's tokens are rows cu[b] .. cu[b + 1] - 1 of n_tokens, each at its position; the request
+// holds lens[b] tokens, its new ones among them.
+struct PagedStep {
+    int B, n_tokens;
+    const int *cu, *positions, *lens;
+};
+// Tokens of one round of the absorbed form: a step of more takes several (the partials are 128 KB a token at 128
+// heads).
+constexpr int PAGED_ROUND = 2048;
+// The plan of tokens s0 .. s0 + p.T - 1: their groups, and the division of the groups' tiles (p.lens, p.of,
+// p.limits, p.groups are written; p.B = p.T).
+cudaError_t launch_paged_plan(const PagedDecode &p, const PagedStep &s, int s0, int *lens, int2 *of, int *limits, int4 *groups,
+                              cudaStream_t st);
 
 // The tensor-core form (bf16): these dimensions and page size, any number of heads.
 // pairs of SMs of a GB300, keys per tile (no worker waits for another: with fewer SMs free they take turns)

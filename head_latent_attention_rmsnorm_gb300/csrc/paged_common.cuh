@@ -76,17 +76,17 @@ __device__ __forceinline__ long share_of(const PagedDecode &p, long T) {
     return q > p.min_tiles ? q : p.min_tiles;
 }
 
-// A request's keys: its length cut to what its table row can hold.
+// A group's keys (decode: a request's): its length cut to what a table row can hold.
 __device__ __forceinline__ int keys_of(const PagedDecode &p, int b) {
     const int cap = p.max_pages * p.page;   // checked to fit by the caller
     return min(max(p.lens[b], 0), cap);
 }
 
-// The request whose tiles (for all its row tiles) hold tile t < T; `off`: the prefix sums.
+// The group whose tiles (for all its row tiles) hold tile t < T; `off`: the prefix sums.
 template <typename I>
 __device__ __forceinline__ int request_of(const PagedDecode &p, const I *off, long t) {
     int lo = 0, hi = p.B - 1;
-    while (lo < hi) {   // the last b whose first tile is <= t: empty requests before it share that tile
+    while (lo < hi) {   // the last b whose first tile is <= t: empty groups before it share that tile
         const int mid = (lo + hi + 1) >> 1;
         if ((long)off[mid] * p.row_tiles <= t) lo = mid;
         else hi = mid - 1;
@@ -130,9 +130,11 @@ __device__ void plan_parts(const PagedDecode &p, const I *off, long total) {
         }
         const long i0 = o * p.row_tiles + rt * per, i1 = i0 + per, end = min((c + 1) * q, total), t1 = min(end, i1);
         const int item = b * p.row_tiles + rt;
+        const int4 g = p.groups ? p.groups[b] : make_int4(b, b * p.H, p.H, 0);
         PagedPart x{};
-        x.b = b;
-        x.rt = rt;
+        x.row = g.x;
+        x.q = g.y + rt * p.row_tile;
+        x.rows = min(g.z - rt * p.row_tile, p.row_tile);
         x.k0 = (int)(t0 - i0);
         x.nt = (int)(t1 - t0);
         x.keys = keys_of(p, b);
@@ -149,7 +151,7 @@ __device__ void plan_parts(const PagedDecode &p, const I *off, long total) {
     }
 }
 
-// The tile prefix sums of all requests and the workers' parts, by one block of NT threads; `room`
+// The tile prefix sums of all groups and the workers' parts, by one block of NT threads; `room`
 // ints of shared memory keep the sums at hand where they fit.
 template <int NT>
 __device__ void plan_block(const PagedDecode &p, int *sm = nullptr, int room = 0) {

@@ -39,27 +39,30 @@ __global__ void __launch_bounds__(NT) paged_absorb_simt_kernel(const __grid_cons
                                                                const __grid_constant__ Turns turns) {
     extern __shared__ float sm[];   // q [BT][Dn], sums [8 warps][BT][DC]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int groups = (p.B + BT - 1) / BT, chunks = (p.Dk + DC - 1) / DC;
-    pdl_wait();
+    const int groups = (p.T + BT - 1) / BT, chunks = (p.Dk + DC - 1) / DC;
+    // a step's plan is the launch in front and runs beside this one, as in the tensor-core form
+    const bool step = p.pos != nullptr;
+    if (!step) pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x == 0) {
-        plan_block<NT>(p);
+        if (!step) plan_block<NT>(p);
+        else pdl_wait();
         return;
     }
     int u = blockIdx.x - 1;
     const int ch = u % chunks;
     u /= chunks;
-    const int h = u / groups, b0 = (u % groups) * BT, nb = min(BT, p.B - b0), d0 = ch * DC;
+    const int h = u / groups, b0 = (u % groups) * BT, nb = min(BT, p.T - b0), d0 = ch * DC;
     for (int i = tid; i < BT * p.Dn; i += NT) {
         const int j = i / p.Dn, n = i % p.Dn;
         sm[i] = j < nb ? to_f<T>(((const T *)p.q_nope)[((long)(b0 + j) * p.H + h) * p.Dn + n]) : 0.f;
     }
-    if (ch == 0) {   // the query sits at its request's last key
+    if (ch == 0) {   // a decode's query sits at its request's last key
         const int half = p.Dr / 2;
         for (int i = tid; i < nb * half; i += NT) {
             const int j = i / half, t = i % half;
             const long row = (long)(b0 + j) * p.H + h;
-            const float2 cs = turn_cs(turns.v[t], keys_of(p, b0 + j) - 1);
+            const float2 cs = turn_cs(turns.v[t], step ? p.pos[b0 + j] : keys_of(p, b0 + j) - 1);
             const T *x = (const T *)p.q_pe + row * p.Dr;
             const float x0 = to_f<T>(x[t]), x1 = to_f<T>(x[t + half]);
             float *y = (float *)p.qpe + row * p.Dr;
@@ -95,6 +98,7 @@ __global__ void __launch_bounds__(NT) paged_absorb_simt_kernel(const __grid_cons
         for (int k = 0; k < NT / 32; ++k) x += sum[(k * BT + j) * DC + d];
         if (j < nb && d0 + d < p.Dk) ((float *)p.qabs)[((long)(b0 + j) * p.H + h) * p.Dk + d0 + d] = x;
     }
+    if (step) pdl_wait();
 }
 
 // --------------------------------------------------------------------- attention ----
@@ -120,7 +124,7 @@ __host__ __device__ inline Lay layout(int Dk, int Dr) {
     l.flag = l.s + NT / 32 * HT * KT;
     const int meet = NT * HT * 2;   // the groups' sums, over the rest
     if (l.flag < meet) l.flag = meet;
-    l.total = l.flag + 2 * KT + 3 * HT;
+    l.total = l.flag + 2 * KT + 4 * HT;
     return l;
 }
 
@@ -153,6 +157,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
     float *sQ = sm + L.q, *sK = sm + L.k, *sS = sm + L.s;
     int *sRow = (int *)(sm + L.flag);                   // the keys' cache rows, -1 = no key; by parity of the tile
     float *sM = sm + L.flag + 2 * KT, *sL = sM + HT, *sA = sL + HT;   // running maximum, sum, rescale
+    int *sLim = (int *)(sA + HT);                       // the rows' keys
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
     pdl_wait();
@@ -168,14 +173,16 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
         const int rt = (int)((t - first * p.row_tiles) / per);
         const long k0 = (t - first * p.row_tiles) % per;        // first tile of the item here
         const long k1 = min(per, k0 + tend - t);
-        const int keys = keys_of(p, b), h0 = rt * HT, nh = min(HT, p.H - h0);
+        const int keys = keys_of(p, b);
+        const int4 g = p.groups ? p.groups[b] : make_int4(b, b * p.H, p.H, 0);
+        const int q0 = g.y + rt * HT, nh = min(HT, g.z - rt * HT);   // first query row, query rows
         // the rows of tile kt's keys
         auto look_up = [&](long kt) {
             if (tid < KT) {
                 int row = -1;
                 const long key = kt * KT + tid;
                 if (key < keys) {
-                    const int id = p.table[(long)b * p.max_pages + (int)key / p.page];
+                    const int id = p.table[(long)g.x * p.max_pages + (int)key / p.page];
                     if (id >= 0 && id < p.num_pages) row = id * p.page + (int)key % p.page;
                 }
                 sRow[(kt & 1) * KT + tid] = row;
@@ -209,7 +216,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
 #pragma unroll
             for (int k = 0; k < QN; ++k) {
                 const int i = tid + k * NT, h = i / c4, d = i % c4;
-                const long row = (long)b * p.H + h0 + h;
+                const long row = (long)q0 + h;
                 x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (h < nh)
                     x[k] = __ldcg((const float4 *)(d < ck ? (const float *)p.qabs + row * p.Dk + 4 * d
@@ -225,7 +232,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
                 const int h = i / L.dqp, d = i % L.dqp;
                 float v = 0.f;
                 if (h < nh && d < Dq) {
-                    const long row = (long)b * p.H + h0 + h;
+                    const long row = (long)q0 + h;
                     v = d < p.Dk ? ((const float *)p.qabs)[row * p.Dk + d] : ((const float *)p.qpe)[row * p.Dr + d - p.Dk];
                 }
                 sQ[i] = v;
@@ -234,6 +241,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
         if (tid < HT) {
             sM[tid] = -INFINITY;
             sL[tid] = 0.f;
+            sLim[tid] = p.limits && tid < nh ? p.limits[(q0 + tid) / p.H] : keys;
         }
         float o[HT][2];
 #pragma unroll
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_simt_kernel(const __grid_con
                 float s = 0.f;
 #pragma unroll
                 for (int w = 0; w < NT / 32; ++w) s += sS[(w * HT + h) * KT + lane];
-                s = rows[lane] >= 0 ? s * p.scale : -INFINITY;
+                s = rows[lane] >= 0 && kt * KT + lane < sLim[h] ? s * p.scale : -INFINITY;
                 float m = s;
 #pragma unroll
                 for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
@@ -371,14 +379,13 @@ __global__ void __launch_bounds__(NT) paged_join_simt_kernel(const __grid_consta
     extern __shared__ float sm[];   // o [BT][Dk]
     __shared__ float sw[BT][JP];
     __shared__ long ss[BT];
-    __shared__ int sn[BT];
+    __shared__ int sn[BT], sr[BT];   // parts (-1: a token that is not computed here), row in the item
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int groups = (p.B + BT - 1) / BT, chunks = (p.Dv + VC - 1) / VC;
+    const int groups = (p.T + BT - 1) / BT, chunks = (p.Dv + VC - 1) / VC;
     int u = blockIdx.x;
     const int ch = u % chunks;
     u /= chunks;
-    const int h = u / groups, b0 = (u % groups) * BT, nb = min(BT, p.B - b0);
-    const int rt = h / p.row_tile, r = h % p.row_tile;
+    const int h = u / groups, b0 = (u % groups) * BT, nb = min(BT, p.T - b0);
     constexpr int WN = DK_MAX / 32;
     const int v0 = ch * VC + warp * 4;
     const T *w = (const T *)p.w + ((long)h * (p.Dn + p.Dv) + p.Dn + v0) * p.Dk + lane;
@@ -391,14 +398,17 @@ __global__ void __launch_bounds__(NT) paged_join_simt_kernel(const __grid_consta
     if (warp < BT) {
         const int b = b0 + warp;
         long s0 = 0;
-        int n = 0;
-        if (warp < nb) {
+        int n = 0, r = 0;
+        const int2 of = warp >= nb ? make_int2(-1, 0) : p.of ? p.of[b0 + warp] : make_int2(b0 + warp, 0);
+        if (of.x >= 0) {
+            const int g = of.x, rt = (of.y + h) / p.row_tile;
+            r = (of.y + h) % p.row_tile;
             const long total = p.tile_off[p.B] * p.row_tiles;
-            const long per = p.tile_off[b + 1] - p.tile_off[b], first = p.tile_off[b] * p.row_tiles + rt * per;
+            const long per = p.tile_off[g + 1] - p.tile_off[g], first = p.tile_off[g] * p.row_tiles + rt * per;
             if (per > 0) {
                 const long q = share_of(p, total), c0 = first / q;
                 n = (int)((first + per - 1) / q - c0) + 1;
-                s0 = c0 + (long)b * p.row_tiles + rt;
+                s0 = c0 + (long)g * p.row_tiles + rt;
             }
         }
         const float *pl = p.pl + s0 * p.row_tile + r;
@@ -415,8 +425,9 @@ __global__ void __launch_bounds__(NT) paged_join_simt_kernel(const __grid_consta
         for (int c = lane; c < n; c += 32) sw[warp][c] *= inv;
         if (lane == 0) {
             ss[warp] = s0;
-            sn[warp] = n;
-            if (ch == 0 && warp < nb) p.lse[(long)b * p.H + h] = sum == 0.f ? -INFINITY : m + logf(sum);
+            sn[warp] = of.x >= 0 ? n : -1;
+            sr[warp] = r;
+            if (ch == 0 && of.x >= 0) p.lse[(long)b * p.H + h] = sum == 0.f ? -INFINITY : m + logf(sum);
         }
     }
     __syncthreads();
@@ -425,7 +436,7 @@ __global__ void __launch_bounds__(NT) paged_join_simt_kernel(const __grid_consta
         const int d4 = p.Dk / 4;
         for (int i = tid; i < BT * d4; i += NT) {
             const int j = i / d4, n = sn[j];
-            const float *po = p.po32 + (ss[j] * p.row_tile + r) * p.Dk + i % d4 * 4;
+            const float *po = p.po32 + (ss[j] * p.row_tile + sr[j]) * p.Dk + i % d4 * 4;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
             for (int c = 0; c < n; c += 8) {
@@ -448,7 +459,7 @@ __global__ void __launch_bounds__(NT) paged_join_simt_kernel(const __grid_consta
     } else {
         for (int i = tid; i < BT * p.Dk; i += NT) {
             const int j = i / p.Dk, d = i % p.Dk;
-            const float *po = p.po32 + (ss[j] * p.row_tile + r) * p.Dk + d;
+            const float *po = p.po32 + (ss[j] * p.row_tile + sr[j]) * p.Dk + d;
             float o = 0.f;
 #pragma unroll 4
             for (int c = 0; c < sn[j]; ++c) o = fmaf(sw[j][c], po[c * pitch], o);
@@ -473,7 +484,7 @@ __global__ void __launch_bounds__(NT) paged_join_simt_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < BT; ++j) {
             const float x = warp_sum(acc[k][j]);
-            if (lane == 0 && j < nb && v0 + k < p.Dv) ((T *)p.out)[((long)(b0 + j) * p.H + h) * p.Dv + v0 + k] = from_f<T>(x);
+            if (lane == 0 && sn[j] >= 0 && v0 + k < p.Dv) ((T *)p.out)[((long)(b0 + j) * p.H + h) * p.Dv + v0 + k] = from_f<T>(x);
         }
 }
 
@@ -481,7 +492,7 @@ template <typename T>
 cudaError_t decode_simt(const PagedDecode &p, cudaStream_t st) {
     Turns turns{};
     std::copy_n(paged_turns(p.base, p.Dr), p.Dr / 2, turns.v);
-    const unsigned units = (unsigned)((p.B + BT - 1) / BT) * (unsigned)p.H;
+    const unsigned units = (unsigned)((p.T + BT - 1) / BT) * (unsigned)p.H;
     const unsigned blocks = units * (unsigned)((p.Dk + DC - 1) / DC), jblocks = units * (unsigned)((p.Dv + VC - 1) / VC);
     const size_t s1 = ((size_t)BT * p.Dn + (size_t)NT / 32 * BT * DC) * 4, s2 = (size_t)layout(p.Dk, p.Dr).total * 4, s3 = (size_t)BT * p.Dk * 4;
     cudaError_t e;

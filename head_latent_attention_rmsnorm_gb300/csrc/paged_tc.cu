@@ -151,13 +151,13 @@ struct Absorb {
     Turns64 turns;
 };
 
-// The queries' rotation: a warp per request and 32 heads, a lane per pair of dims, the angle formed once.
+// The queries' rotation: a warp per token and 32 heads, a lane per pair of dims, the angle formed once.
 __device__ void rotate_queries(const Absorb &a, int i, int lane) {
     const PagedDecode &p = a.p;
     const int per = (p.H + 31) / 32, b = i / per, h0 = i % per * 32;
-    if (b >= p.B) return;
-    const int keys = keys_of(p, b);
-    const float2 cs = turn_cs(a.turns.v[lane], keys - 1);
+    if (b >= p.T || (p.done && p.done[b])) return;
+    const int keys = p.pos ? 0 : keys_of(p, b);   // (a step's tokens may be few keys' whatever their position)
+    const float2 cs = turn_cs(a.turns.v[lane], p.pos ? p.pos[b] : keys - 1);
     const int h1 = min(h0 + 32, p.H);
 #pragma unroll 1
     for (int h = h0; h < h1; h += 8) {
@@ -191,14 +191,19 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
     extern __shared__ __align__(1024) uint8_t sm[];
     const PagedDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    pdl_wait();
+    // A step's plan is the launch in front and runs beside this one (it began behind the end of all before it,
+    // and nothing here reads what it writes): the wait for it is at each block's end, for the launch behind.
+    const bool step = p.pos != nullptr;
+    if (!step) pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x == 0) {
-        plan_block<128>(p, (int *)sm, AB_SMEM / 4);
+        if (!step) plan_block<128>(p, (int *)sm, AB_SMEM / 4);
+        else pdl_wait();
         return;
     }
     if ((int)blockIdx.x <= a.rot_blocks) {
         rotate_queries(a, ((int)blockIdx.x - 1) * 4 + warp, lane);
+        if (step) pdl_wait();
         return;
     }
     uint8_t *sw = sm, *sq = sm + DN * AB_PITCH;
@@ -206,7 +211,11 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
     const int dc = u & 3;
     u >>= 2;
     const int grp = u % a.groups, h = u / a.groups;
-    const int b0 = grp * a.group, nb = min(a.group, p.B - b0);
+    const int b0 = grp * a.group, nb = min(a.group, p.T - b0);
+    if (p.done && __syncthreads_and(tid >= nb || p.done[b0 + tid])) {
+        pdl_wait();
+        return;
+    }
     const bf16 *w = (const bf16 *)p.w + (long)h * (DN + DV) * DK + dc * AB_DIMS;
     for (int i = tid; i < nb * 16; i += 128)
         cp16(sq + (i >> 4) * AB_PITCH + (i & 15) * 16, (const bf16 *)p.q_nope + ((long)(b0 + (i >> 4)) * p.H + h) * DN + (i & 15) * 8);
@@ -214,7 +223,7 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
     for (int i = tid; i < DN * (AB_DIMS / 8); i += 128)
         cp16(sw + (i >> 4) * AB_PITCH + (i & 15) * 16, w + (long)(i >> 4) * DK + (i & 15) * 8);
     int *keys = (int *)(sm + AB_SMEM) - AB_GROUP;
-    if (tid < nb) keys[tid] = keys_of(p, b0 + tid);
+    if (tid < nb) keys[tid] = step ? 0 : keys_of(p, b0 + tid);
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     uint32_t A[2][8][4];
@@ -265,6 +274,7 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
         }
         __syncwarp();
     }
+    if (step) pdl_wait();
 }
 
 // -------------------------------------------------------------------------- join ----
@@ -284,7 +294,7 @@ constexpr int JW = JO + 2 * 8 * JBLK;          // o hi, o lo; before them the gr
 constexpr int JV = JW + 2 * JB * JMAXC * 4;    // the parts' weights for either half of the dims; then out [request][132]
 struct JoinVars {
     uint64_t bar_w, bar_d;
-    int sc[JB][3];            // first part, number of parts, Extra
+    int sc[JB][4];            // first part, number of parts (-1: a token that is not computed here), Extra, row in the item
     float sl[JB], sd[2][JB];  // log-sum-exp without the q_lo term; the warps' shares of q_lo . o
     uint32_t tslot;
     int abort;
@@ -308,9 +318,9 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
     uint8_t *so = sm + JO;
     float (*sw)[JB][JMAXC] = (float (*)[JB][JMAXC])(sm + JW);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x / per_head, rt = h / p.row_tile, r = h % p.row_tile;
+    const int h = blockIdx.x / per_head;
     const long pitch = (long)p.row_tile * (DK / 8);
-    const bool paired = p.H <= 64;
+    const bool paired = p.row_tile <= 64;
     bool ok = true;
     if (tid == 0) {
         mbar_init(&v0.bar_w, 1);
@@ -332,8 +342,9 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
     pdl_wait();
     uint32_t ph = 0;
 #pragma unroll 1
-    for (int b0 = (int)(blockIdx.x % per_head) * JB; b0 < p.B; b0 += per_head * JB, ph ^= 1) {
-        const int nb = min(JB, p.B - b0);
+    for (int b0 = (int)(blockIdx.x % per_head) * JB; b0 < p.T; b0 += per_head * JB) {
+        const int nb = min(JB, p.T - b0);
+        if (p.of && __syncthreads_and(tid >= nb || __ldcg(&p.of[b0 + tid].x) < 0)) continue;
         const int d8 = tid & 63, q16 = tid >> 6;
         const bool few = nb <= 2;                                // the groups share out parts, not requests
         const int j0 = few ? 0 : q16, dj = few ? 1 : 16, c0 = few ? q16 : 0, dc = few ? 16 : 1;
@@ -344,12 +355,19 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
             ql[i] = j < nb && !paired ? __ldcg((const uint4 *)(qlo + ((long)(b0 + j) * p.H + h) * DK) + d8) : make_uint4(0, 0, 0, 0);
         }
         {   // a warp per request: the weights of its parts (up to 96)
-            int s0 = 0, n = 0, ex = EX_NONE;
+            int s0 = 0, n = 0, ex = EX_NONE, r = 0;
+            bool here = true;
             if (warp < nb) {
-                ex = extra_of(paired, keys_of(p, b0 + warp));
-                const int2 sp = __ldcg(p.spans + (long)(b0 + warp) * p.row_tiles + rt);
-                s0 = sp.x;
-                n = sp.y;
+                const int2 of = p.of ? __ldcg(p.of + b0 + warp) : make_int2(b0 + warp, 0);
+                here = of.x >= 0;
+                if (here) {
+                    ex = extra_of(paired, keys_of(p, of.x));
+                    const int rt = (of.y + h) / p.row_tile;
+                    r = (of.y + h) % p.row_tile;
+                    const int2 sp = __ldcg(p.spans + (long)of.x * p.row_tiles + rt);
+                    s0 = sp.x;
+                    n = sp.y;
+                }
             }
             const long at = (long)s0 * p.row_tile + r;
             float x[3], m = -INFINITY, s = 0.f;
@@ -380,8 +398,9 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
                 }
             if (lane == 0) {
                 sc[warp][0] = s0;
-                sc[warp][1] = n;
+                sc[warp][1] = here ? n : -1;
                 sc[warp][2] = ex;
+                sc[warp][3] = r;
                 sl[warp] = s == 0.f ? -INFINITY : m + logf(s);
             }
         }
@@ -393,7 +412,7 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int j = j0 + dj * i;
-                src[i] = (const uint4 *)(p.po + ((long)sc[j][0] * p.row_tile + r) * DK) + d8;
+                src[i] = (const uint4 *)(p.po + ((long)sc[j][0] * p.row_tile + sc[j][3]) * DK) + d8;
                 n[i] = sc[j][1];
             }
             const float *wt = sw[d8 >> 5][j0];
@@ -472,7 +491,7 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
         tc_fence_before();
         __syncthreads();
         // (no keys: -inf stays, whatever the queries of a padded request hold; 0 * NaN is not added)
-        if (tid < nb) p.lse[(long)(b0 + tid) * p.H + h] = sl[tid] == -INFINITY ? sl[tid] : sl[tid] + p.scale * (sd[0][tid] + sd[1][tid]);
+        if (tid < nb && sc[tid][1] >= 0) p.lse[(long)(b0 + tid) * p.H + h] = sl[tid] == -INFINITY ? sl[tid] : sl[tid] + p.scale * (sd[0][tid] + sd[1][tid]);
         if (warp == 0) {
             ok = __all_sync(FULL, ok && mbar_wait(&v0.bar_w, 0, (volatile int *)&v0.abort, &g_paged_tc_err));   // W_V is here
             tc_fence_after();
@@ -502,11 +521,12 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
             for (int j = 0; j < JB; ++j) ss[j * 132 + tid] = __uint_as_float(v[j]);
         }
         __syncthreads();
-        if (warp < nb) {   // (an abandoned wait leaves rubbish here, and the error word)
+        if (warp < nb && sc[warp][1] >= 0) {   // (an abandoned wait leaves rubbish here, and the error word)
             const float4 v = *(const float4 *)(ss + warp * 132 + lane * 4);
             *(uint2 *)((bf16 *)p.out + ((long)(b0 + warp) * p.H + h) * DV + lane * 4) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
         }
         __syncthreads();
+        ph ^= 1;
     }
     if (warp == 1) tmem_dealloc(tmem, 32);
 }
@@ -579,7 +599,7 @@ __device__ __forceinline__ uint32_t arrivals(int i) {
 struct Maps {
     CUtensorMap k3, k2, v, r;   // boxes of a unit's rows: blocks 0-2 / 3-5, blocks 6-7, four blocks, key band
     CUtensorMap v8;             // eight rows, four blocks
-    CUtensorMap qh, ql, rh, rl, rr; // queries [B][H][512] and [B][H][64]: hi, lo, rest
+    CUtensorMap qh, ql, rh, rl, rr; // query rows of 512 and of 64 dims: hi, lo, rest (a box may reach into another group's)
 };
 struct Attn {
     PagedDecode p;
@@ -599,7 +619,7 @@ struct Attn {
 __device__ __forceinline__ int row_of(const Attn &a, const PagedPart &w, int key) {
     if (key >= w.keys) return -1;
     const int col = quotient(a.by_page, key);
-    const int id = __ldg(a.p.table + (long)w.b * a.p.max_pages + col);
+    const int id = __ldg(a.p.table + (long)w.row * a.p.max_pages + col);
     return (unsigned)id < (unsigned)a.p.num_pages ? id * a.p.page + (key - col * a.p.page) : -1;
 }
 
@@ -659,7 +679,7 @@ __device__ void settle() {   // after an abandoned wait: loads in flight land be
     }
 }
 
-// PAIRED (up to 64 heads): the rows behind the heads, 64 on, carry the queries' low halves in the scores and P's
+// PAIRED (items of up to 64 rows): the rows behind the heads, 64 on, carry the queries' low halves in the scores and P's
 // in the values.
 template <int UNIT, bool PAIRED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
@@ -711,12 +731,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     bool more = n_all > 0;
     auto load = [&]() {
         const int4 x = __ldcg((const int4 *)part), y = __ldcg((const int4 *)part + 1);
-        w.b = x.x;
-        w.rt = x.y;
+        w.row = x.x;
+        w.q = x.y;
         w.k0 = x.z;
         w.nt = x.w;
         w.keys = y.x;
         w.next = y.y;
+        w.rows = y.z;
     };
     if (more) load();
     auto next = [&]() {
@@ -833,13 +854,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             int n = 0;
             bool ok = true;
             for (; more; next()) {
-                // a warp without a head only keeps the barriers
-                const bool act = w.rt * ROWS + (paired ? quad & 1 : quad) * 32 < p.H;
+                // a warp without a row only keeps the barriers
+                const bool act = (paired ? quad & 1 : quad) * 32 < w.rows;
+                // keys that this row sees: a step's token not all of its group's
+                const int lim = p.limits && head < w.rows ? __ldcg(p.limits + (w.q + head) / p.H) : w.keys;
                 // whether every page of the part has an id inside the cache
                 bool sound = true;
                 {
                     const int c0 = quotient(a.by_page, w.k0 * NK), c1 = quotient(a.by_page, min(w.keys, (w.k0 + w.nt) * NK) - 1);
-                    const int *ids = p.table + (long)w.b * p.max_pages;
+                    const int *ids = p.table + (long)w.row * p.max_pages;
 #pragma unroll 2
                     for (int col = c0 + lane; col <= c1; col += 32) sound = sound && (unsigned)__ldg(ids + col) < (unsigned)p.num_pages;
                     sound = __all_sync(FULL, sound);
@@ -890,8 +913,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                             }
                         }
                         const int key0 = (w.k0 + i) * NK + h * HK + lo_row * KN;
-                        if (groups != (1u << NGRP) - 1 || key0 + KN > w.keys) {
-                            const int end = w.keys - key0;
+                        if (groups != (1u << NGRP) - 1 || key0 + KN > lim) {
+                            const int end = lim - key0;
                             groups >>= 4 * h + 2 * lo_row;
 #pragma unroll
                             for (int e = 0; e < KN; ++e)
@@ -997,18 +1020,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     mbar_arrive_expect_tx(&bars[B_QFULL], (18 + (ex == EX_BAND)) * 128 * a.q_rows);
 #pragma unroll 1
                     for (int j = 0; j < 9; ++j) {
-                        tma_load_3d(smem + j * 16384, j < 8 ? &m.qh : &m.rh, &bars[B_QFULL], j < 8 ? 64 * j : 0, 0, w.b);
-                        tma_load_3d(smem + j * 16384 + 64 * 128, j < 8 ? &m.ql : &m.rl, &bars[B_QFULL], j < 8 ? 64 * j : 0, 0, w.b);
+                        tma_load_3d(smem + j * 16384, j < 8 ? &m.qh : &m.rh, &bars[B_QFULL], j < 8 ? 64 * j : 0, w.q, 0);
+                        tma_load_3d(smem + j * 16384 + 64 * 128, j < 8 ? &m.ql : &m.rl, &bars[B_QFULL], j < 8 ? 64 * j : 0, w.q, 0);
                     }
-                    if (ex == EX_BAND) tma_load_3d(smem + OFF_Q, &m.rr, &bars[B_QFULL], 0, 0, w.b);
+                    if (ex == EX_BAND) tma_load_3d(smem + OFF_Q, &m.rr, &bars[B_QFULL], 0, w.q, 0);
                     continue;
                 }
                 mbar_arrive_expect_tx(&bars[B_QFULL], boxes * 128 * a.q_rows);
 #pragma unroll 1
                 for (int j = 0; j < boxes; ++j) {
                     const CUtensorMap *map = j < 8 ? &m.qh : (j == 8 ? &m.rh : (j == 9 ? &m.rl : (ex == EX_BAND ? &m.rr : &m.ql)));
-                    tma_load_3d(smem + (j < 9 ? j * 16384 : OFF_Q + (j - 9) * 16384), map, &bars[B_QFULL], j < 8 ? 64 * j : 0,
-                                w.rt * ROWS, w.b);
+                    tma_load_3d(smem + (j < 9 ? j * 16384 : OFF_Q + (j - 9) * 16384), map, &bars[B_QFULL], j < 8 ? 64 * j : 0, w.q,
+                                0);
                 }
                 if (!(lo_blocks(ex) & 0xc)) continue;
                 // lo of dims 128-255 for the MMAs to read in shared memory, once the two boxes there have moved
@@ -1017,7 +1040,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 wide ^= 1;
                 mbar_arrive_expect_tx(&bars[B_QFULL], 2 * 128 * a.q_rows);
 #pragma unroll 1
-                for (int j = 0; j < 2; ++j) tma_load_3d(smem + OFF_Q + j * 16384, &m.ql, &bars[B_QFULL], 64 * (j + 2), w.rt * ROWS, w.b);
+                for (int j = 0; j < 2; ++j) tma_load_3d(smem + OFF_Q + j * 16384, &m.ql, &bars[B_QFULL], 64 * (j + 2), w.q, 0);
             }
         } else {
             // ------------------------------- queries into TMEM (warps 14-17, a thread per head)
@@ -1027,7 +1050,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             int n = 0;
             bool ok = true;
             for (; more && ok; n += w.nt, next()) {
-                const bool act = w.rt * ROWS + (paired ? quad & 1 : quad) * 32 < p.H;
+                const bool act = (paired ? quad & 1 : quad) * 32 < w.rows;
                 const Extra ex = extra_of(paired, w.keys);
                 const int boxes = paired ? 9 + (ex == EX_BAND) : ex == EX_NONE ? 10 : 11;
                 // q_lo of dims 64-127 has no box: each thread's 128 bytes come straight from memory, under
@@ -1035,7 +1058,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 uint4 x[8];
                 const unsigned lo = paired ? 0 : lo_blocks(ex);
                 if ((lo & 2) && act) {
-                    const bf16 *src = a.qlo + ((long)w.b * p.H + min(w.rt * ROWS + row, p.H - 1)) * DK + 64;
+                    const bf16 *src = a.qlo + (w.q + (long)min(row, w.rows - 1)) * DK + 64;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = __ldcg((const uint4 *)src + e);
                 }
@@ -1208,8 +1231,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             int n = 0, seg = 0;
             bool ok = true;   // as in the softmax warps: every barrier is reached
             for (; more; next(), ++seg) {
-                const bool act = w.rt * ROWS + quad * 32 < p.H;
-                const bool acc = act || (paired && quad >= 2 && (quad - 2) * 32 < p.H);   // rows that O is kept for
+                const bool act = quad * 32 < w.rows;
+                const bool acc = act || (paired && quad >= 2 && (quad - 2) * 32 < w.rows);   // rows that O is kept for
                 const long slot = part - p.parts;
                 if (g == 0) {
                     float lse2 = -INFINITY, inv_l = 0.f;
@@ -1252,7 +1275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                         if (lane == 0) mbar_arrive(&bars[B_PCREADY + s]);
                     }
                     invs[(seg & 1) * ROWS] = inv_l;
-                    if (ok && act && w.rt * ROWS + row < p.H) p.pl[slot * p.row_tile + row] = lse2 * 0.69314718055994531f;
+                    if (ok && act && row < w.rows) p.pl[slot * p.row_tile + row] = lse2 * 0.69314718055994531f;
                 }
                 // ---- epilogue: the part's normalised output, 256 latent dims per warp: 64 columns of 32
                 // heads at a time, turned in shared memory so that a store writes whole 128-byte lines.
@@ -1278,7 +1301,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     }
                 }
                 if (act) {   // (an abandoned wait leaves rubbish here, and the error word)
-                    const int live = min(32, p.H - (w.rt * ROWS + quad * 32));
+                    const int live = min(32, w.rows - quad * 32);
                     // the row's largest value here sets its power of two
                     float big = 0.f;
 #pragma unroll 1
@@ -1355,7 +1378,7 @@ bool paged_tc_supported(int Dk, int Dn, int Dr, int Dv, int page) {
 cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     using ull = unsigned long long;
     cudaError_t e;
-    const ull rows = (ull)p.num_pages * p.page, heads = (ull)p.B * p.H;
+    const ull rows = (ull)p.num_pages * p.page, heads = (ull)p.T * p.H;
     Absorb ab{};
     ab.p = p;
     ab.qhi = (bf16 *)p.qabs;
@@ -1365,17 +1388,17 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     ab.rlo = ab.rhi + heads * DR;
     ab.rrest = ab.rlo + heads * DR;
     // at least two blocks per SM, where the batch has that many groups of eight
-    const int want = (2 * 152 + 4 * p.H - 1) / (4 * p.H), most = (p.B + 7) / 8;
-    ab.groups = std::max((p.B + AB_GROUP - 1) / AB_GROUP, std::min(want, most));
-    ab.group = ((p.B + ab.groups - 1) / ab.groups + 7) / 8 * 8;
-    ab.groups = (p.B + ab.group - 1) / ab.group;
-    ab.rot_blocks = (int)(((long)p.B * ((p.H + 31) / 32) + 3) / 4);
+    const int want = (2 * 152 + 4 * p.H - 1) / (4 * p.H), most = (p.T + 7) / 8;
+    ab.groups = std::max((p.T + AB_GROUP - 1) / AB_GROUP, std::min(want, most));
+    ab.group = ((p.T + ab.groups - 1) / ab.groups + 7) / 8 * 8;
+    ab.groups = (p.T + ab.group - 1) / ab.group;
+    ab.rot_blocks = (int)(((long)p.T * ((p.H + 31) / 32) + 3) / 4);
     std::copy_n(paged_turns(p.base, DR), DR / 2, ab.turns.v);
 
     Attn at{};
     int unit = NK;   // rows that always share a page: the largest power of two up to a tile that divides one
     while (p.page % unit) unit /= 2;
-    at.q_rows = std::min(ROWS, (p.H + 31) / 32 * 32);
+    at.q_rows = std::min(ROWS, (p.row_tile + 31) / 32 * 32);
     at.qlo = ab.qlo;
     Maps m{};
     {
@@ -1391,10 +1414,10 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     }
     {
         const unsigned bq[3] = {64, (unsigned)at.q_rows, 1};
-        const ull d[3] = {DK, (ull)p.H, (ull)p.B}, s[2] = {DK * 2, (ull)p.H * DK * 2};
+        const ull d[3] = {DK, heads, 1}, s[2] = {DK * 2, heads * DK * 2};
         if ((e = make_tma_map(&m.qh, ab.qhi, 3, d, s, bq)) != cudaSuccess) return e;
         if ((e = make_tma_map(&m.ql, ab.qlo, 3, d, s, bq)) != cudaSuccess) return e;
-        const ull dr[3] = {DR, (ull)p.H, (ull)p.B}, sr[2] = {DR * 2, (ull)p.H * DR * 2};
+        const ull dr[3] = {DR, heads, 1}, sr[2] = {DR * 2, heads * DR * 2};
         if ((e = make_tma_map(&m.rh, ab.rhi, 3, dr, sr, bq)) != cudaSuccess) return e;
         if ((e = make_tma_map(&m.rl, ab.rlo, 3, dr, sr, bq)) != cudaSuccess) return e;
         if ((e = make_tma_map(&m.rr, ab.rrest, 3, dr, sr, bq)) != cudaSuccess) return e;
@@ -1413,8 +1436,8 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
         const unsigned b[2] = {64, DV};
         if ((e = make_tma_map(&mW, p.w, 2, d, s, b)) != cudaSuccess) return e;
     }
-    const int per_head = std::max(1, std::min((p.B + JB - 1) / JB, 2 * p.workers / p.H));   // one wave of join blocks
-    auto attn = p.H <= 64 ? (unit == 64   ? paged_attn_tc_kernel<64, true>
+    const int per_head = std::max(1, std::min((p.T + JB - 1) / JB, 2 * p.workers / p.H));   // one wave of join blocks
+    auto attn = p.row_tile <= 64 ? (unit == 64   ? paged_attn_tc_kernel<64, true>
                              : unit == 32 ? paged_attn_tc_kernel<32, true>
                              : unit == 16 ? paged_attn_tc_kernel<16, true>
                                           : paged_attn_tc_kernel<8, true>)

@@ -7,7 +7,7 @@ Two layers, argument marshalling only:
   own names, taking integers for pointers and sizes.
 * ``latent_attn_fwd``, ``absorbed_attn_fwd``, ``decode_splitkv``, ``lse_combine``,
   ``tpla_decode``, ``rmsnorm``, ``rmsnorm_bwd``, ``paged_tables``, ``paged_append``,
-  ``paged_decode``:
+  ``paged_decode``, ``paged_prefill``:
   the same calls taking torch tensors; they allocate any output or workspace the
   caller did not pass (through torch's allocator, so the CUDA caching allocator sees
   every byte) and raise :class:`MlaError` on a non-OK status.  ``stream`` (a
@@ -114,6 +114,10 @@ def lib() -> ctypes.CDLL:
         L.mla_paged_decode.restype = _i
         L.mla_paged_decode_workspace.argtypes = [D, _i, _i, _i, _i]
         L.mla_paged_decode_workspace.restype = _sz
+        L.mla_paged_prefill.argtypes = [D, _i, _i, _i, _i, _i, _i] + [_vp] * 12 + [_sz, _vp]
+        L.mla_paged_prefill.restype = _i
+        L.mla_paged_prefill_workspace.argtypes = [D, _i, _i, _i, _i, _i]
+        L.mla_paged_prefill_workspace.restype = _sz
         L.mla_status_string.argtypes = [_i]
         L.mla_status_string.restype = ctypes.c_char_p
         L.mla_check_device_error.argtypes = [_vp]
@@ -225,6 +229,14 @@ def mla_paged_decode_workspace(*args) -> int:
     return lib().mla_paged_decode_workspace(*args)
 
 
+def mla_paged_prefill(*args) -> int:
+    return lib().mla_paged_prefill(*args)
+
+
+def mla_paged_prefill_workspace(*args) -> int:
+    return lib().mla_paged_prefill_workspace(*args)
+
+
 def mla_status_string(status: int) -> str:
     return lib().mla_status_string(status).decode()
 
@@ -249,7 +261,7 @@ KERNELS = ("prep", "latent_prep", "rope_table", "rope_rows", "convert", "gemm_si
            "tc_gemm", "tc_attn", "tc_latent_attn", "tc_decode_attn", "transpose", "rmsnorm", "rmsnorm_bwd", "tpla_expand",
            "tpla_combine", "wait_probe", "tc_fused_attn", "bwd_rowdot", "attn_bwd_simt", "bwd_rows",
            "bwd_prep", "tc_bwd_dkv", "tc_bwd_dq", "paged_tables", "paged_append", "paged_absorb", "paged_attn",
-           "paged_join")
+           "paged_join", "paged_plan")
 
 
 def launch_count() -> int:
@@ -785,4 +797,65 @@ def paged_decode(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens
         _raw_stream(at))
     if st != 0:
         raise MlaError(st, "mla_paged_decode")
+    return out, lse
+
+
+def paged_prefill_workspace(d: Dims, n_tokens: int, c_cache, block_table) -> torch.Tensor:
+    """A workspace for :func:`paged_prefill` calls of ``n_tokens`` rows with this cache and table, one call
+    at a time."""
+    n = lib().mla_paged_prefill_workspace(ctypes.byref(d), _dt(c_cache), block_table.shape[0], n_tokens,
+                                          c_cache.shape[1], block_table.shape[1])
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=c_cache.device)
+
+
+def _step_args(d, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, cu_tokens, positions, w_kv_b):
+    """Checks of a step's inputs: (device, dtype code, torch dtype, index, B, n_tokens, num_pages, page, max_pages,
+    addresses in the order of the arguments)."""
+    dev = _device(q_nope)
+    dt, tdt, at = _dt(q_nope), q_nope.dtype, q_nope.get_device()
+    if q_nope.dim() != 3 or not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("q_nope must be [n_tokens, n_heads, d_nope] and block_table [B, max_pages]")
+    n, H, i32 = q_nope.shape[0], d.n_heads, torch.int32
+    B, max_pages = block_table.shape
+    num_pages, page, cp, kp = _cache(d, c_cache, kpe_cache, tdt, at)
+    if not isinstance(w_kv_b, torch.Tensor):
+        raise TypeError("w_kv_b: expected a torch.Tensor, got %s" % type(w_kv_b).__name__)
+    _expect("w_kv_b", w_kv_b, H * (d.d_nope + d.d_v) * d.d_kv, tdt, dev)
+    ptrs = (_need("q_nope", q_nope, (n, H, d.d_nope), tdt, at), _need("q_pe", q_pe, (n, H, d.d_rope), tdt, at), cp, kp,
+            _need("block_table", block_table, (B, max_pages), i32, at), _need("kv_lens", kv_lens, (B,), i32, at),
+            _need("cu_tokens", cu_tokens, (B + 1,), i32, at), _need("positions", positions, (n,), i32, at),
+            w_kv_b.data_ptr())
+    return dev, dt, tdt, at, B, n, num_pages, page, max_pages, ptrs
+
+
+def paged_prefill(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, cu_tokens, positions, w_kv_b, *,
+                  out=None, lse=None, workspace=None, stream=None):
+    """Latent attention of a step's new tokens over the paged cache, any number of them a request: rows
+    ``cu_tokens[b]`` .. ``cu_tokens[b + 1] - 1`` of ``q_nope`` [n_tokens, n_heads, d_nope] and ``q_pe`` are request
+    b's, each at its position, as :func:`paged_tables` gives them.  Returns (out [n_tokens, n_heads, d_v],
+    lse [n_tokens, n_heads]); rows of no request are left as they were (zeros where this call allocates)."""
+    if stream is not None:
+        return _on_stream(stream, paged_prefill, d, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, cu_tokens,
+                          positions, w_kv_b, out=out, lse=lse, workspace=workspace)
+    dev, dt, tdt, at, B, n, num_pages, page, max_pages, ptrs = _step_args(
+        d, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, cu_tokens, positions, w_kv_b)
+    if at != _current_device():
+        with torch.cuda.device(at):
+            return paged_prefill(d, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, cu_tokens, positions,
+                                 w_kv_b, out=out, lse=lse, workspace=workspace)
+    H = d.n_heads
+    if out is None:
+        out = torch.zeros(n, H, d.d_v, dtype=tdt, device=dev)
+    if lse is None:
+        lse = torch.zeros(n, H, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = paged_prefill_workspace(d, n, c_cache, block_table)
+    else:
+        _workspace(0, dev, workspace)
+    st = lib().mla_paged_prefill(
+        d, dt, B, n, num_pages, page, max_pages, *ptrs, _need("out", out, (n, H, d.d_v), tdt, at),
+        _need("lse", lse, (n, H), torch.float32, at), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _raw_stream(at))
+    if st != 0:
+        raise MlaError(st, "mla_paged_prefill")
     return out, lse

@@ -331,6 +331,28 @@ mla_status mla_paged_decode(const mla_dims *dims, mla_dtype dtype, int B, int nu
                             void *workspace, size_t workspace_bytes, void *cuda_stream);
 size_t mla_paged_decode_workspace(const mla_dims *dims, mla_dtype dtype, int B, int page_size, int max_pages);
 
+/*
+ * Attention of a step's new tokens over the paged cache, any number of them a request (a prompt's
+ * chunk, speculated tokens, one): mla_paged_decode with a position per query.  Rows cu_tokens[b] ..
+ * cu_tokens[b + 1] - 1 of the token arrays are request b's; cu_tokens does not decrease.  Token t at positions[t]
+ * sees the keys j <= positions[t], j < kv_lens[b] of its request's pages, so its own row is written first
+ * (mla_paged_append).  cu_tokens, positions and kv_lens are what mla_paged_tables gives; positions need not be in order.
+ *   q_nope [n_tokens, H, d_nope]   q_pe [n_tokens, H, d_rope] (not rotated)   block_table [B, max_pages]
+ *   kv_lens [B]   cu_tokens [B + 1]   positions [n_tokens]   w_kv_b as above
+ *   out [n_tokens, H, d_v]   lse (fp32) [n_tokens, H]
+ * A token that sees no key (a negative position, no pages) gives out 0 and lse -inf.  Rows of no request (in front of
+ * cu_tokens[0], from cu_tokens[B] on) are left as they were.  Lengths, slots behind them and bad page ids are
+ * treated as in mla_paged_decode, as are types, dimensions, precision (a token has the kernel of its request's
+ * length), determinism and the workspace.  A NaN in the cached row of a token of the step may show in its request's
+ * other tokens of the step.
+ */
+mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int num_pages, int page_size,
+                             int max_pages, const void *q_nope, const void *q_pe, const void *c_cache,
+                             const void *kpe_cache, const int *block_table, const int *kv_lens, const int *cu_tokens,
+                             const int *positions, const void *w_kv_b, void *out, float *lse, void *workspace,
+                             size_t workspace_bytes, void *cuda_stream);
+size_t mla_paged_prefill_workspace(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int page_size, int max_pages);
+
 /* Workspace bytes the matching call needs (0 on invalid arguments). */
 size_t mla_latent_attn_workspace(const mla_dims *dims, mla_dtype dtype, int B, int s_q, int s_kv,
                                  int q_offset, int causal, int head_count, int head_shard);
@@ -429,7 +451,7 @@ mla_status mla_decode_splitkv_noalloc(const mla_dims *dims, mla_dtype dtype, int
  *   "tc_latent_attn", "tc_decode_attn", "transpose", "rmsnorm", "rmsnorm_bwd", "tpla_expand",
  *   "tpla_combine", "wait_probe", "tc_fused_attn", "bwd_rowdot",
  *   "attn_bwd_simt", "bwd_rows", "bwd_prep", "tc_bwd_dkv", "tc_bwd_dq",
- *   "paged_tables", "paged_append", "paged_absorb", "paged_attn", "paged_join".
+ *   "paged_tables", "paged_append", "paged_absorb", "paged_attn", "paged_join", "paged_plan".
  * mla_profile_reset: forgets recorded events, keeps recording on/off as it was.
  * Launches from several host threads are recorded safely; call enable, reset and the
  * queries between computations, not while another thread's calls are in flight.

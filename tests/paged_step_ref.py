@@ -1,0 +1,88 @@
+"""Several tokens a request over the paged cache, in 64 bits, token by token, on the host: what the tests of
+paged prefill, page weights and eviction compare the kernels with."""
+import math
+
+import torch
+
+import paged_ref as ref
+
+
+def step(g, d, dtype, lens, page, *, extra_rows=0, junk=math.nan, scale=1.0, lead=0):
+    """A step's inputs for requests of (past, new) lengths, on the host; `lead` rows in front belong to no request."""
+    kv = [p + n for p, n in lens]
+    c, k, table = ref.cache(g, d, dtype, kv, page, junk=junk, scale=scale)
+    cu = [lead]
+    for _, n in lens:
+        cu.append(cu[-1] + n)
+    n_tokens = cu[-1] + extra_rows
+    positions = torch.full((n_tokens,), 7, dtype=torch.int32)
+    for b, (p, n) in enumerate(lens):
+        positions[cu[b]:cu[b + 1]] = torch.arange(p, p + n, dtype=torch.int32)
+    q, r, w = ref.queries(g, d, dtype, n_tokens)
+    i32 = dict(dtype=torch.int32)
+    return dict(q_nope=q, q_pe=r, c_cache=c, kpe_cache=k, block_table=table, kv_lens=torch.tensor(kv, **i32),
+                cu_tokens=torch.tensor(cu, **i32), positions=positions, w_kv_b=w)
+
+
+NAMES = ("q_nope", "q_pe", "c_cache", "kpe_cache", "block_table", "kv_lens", "cu_tokens", "positions", "w_kv_b")
+
+
+def on_gpu(s):
+    return [s[n].cuda() for n in NAMES]
+
+
+def owners(s):
+    """Each token row's request, -1 for none."""
+    cu, n = s["cu_tokens"].tolist(), s["positions"].numel()
+    got = [-1] * n
+    for b in range(len(cu) - 1):
+        for t in range(max(cu[b], 0), min(cu[b + 1], n)):
+            got[t] = b
+    return got
+
+
+def prefill(d, s):
+    """(out, lse, mass, sq) of every token row as ref.decode's, rows of no request with lse NaN."""
+    H, dn, dv, dk = d.n_heads, d.d_nope, d.d_v, d.d_kv
+    num_pages, page = s["c_cache"].shape[:2]
+    scale = d.softmax_scale if d.softmax_scale > 0 else 1.0 / math.sqrt(dn + d.d_rope)
+    w = s["w_kv_b"].double().view(H, dn + dv, dk)
+    table = s["block_table"]
+    n_tokens = s["positions"].numel()
+    out = torch.zeros(n_tokens, H, dv, dtype=torch.float64)
+    lse = torch.full((n_tokens, H), math.nan, dtype=torch.float64)
+    mass, sq = torch.zeros(n_tokens, H, dtype=torch.float64), torch.zeros(n_tokens, H, dtype=torch.float64)
+    c, kr = s["c_cache"].reshape(-1, dk), s["kpe_cache"].reshape(-1, d.d_rope)
+    for t, b in enumerate(owners(s)):
+        if b < 0:
+            continue
+        pos = int(s["positions"][t])
+        n = min(max(int(s["kv_lens"][b]), 0), table.shape[1] * page, pos + 1)
+        ids = table[b, :-(-n // page)].tolist() if n > 0 else []
+        rows = [i * page + o for j, i in enumerate(ids) if 0 <= i < num_pages for o in range(min(page, n - j * page))]
+        if not rows:
+            lse[t] = -math.inf
+            continue
+        q = torch.einsum("hn,hnk->hk", s["q_nope"][t].double(), w[:, :dn])
+        full_q = torch.cat([q, ref.rope(s["q_pe"][t], torch.full((H,), pos), d.rope_base)], 1)
+        full_k = torch.cat([c[rows].double(), kr[rows].double()], 1)
+        x = full_q @ full_k.T * scale
+        m = x.amax(1, keepdim=True)
+        p = torch.exp(x - m)
+        lse[t] = torch.log(p.sum(1)) + m[:, 0]
+        out[t] = torch.einsum("hk,hvk->hv", p @ c[rows].double() / p.sum(1, keepdim=True), w[:, dn:])
+        aq = torch.cat([torch.einsum("hn,hnk->hk", s["q_nope"][t].double().abs(), w[:, :dn].abs()) / math.sqrt(dn),
+                        full_q[:, dk:].abs()], 1)
+        mass[t] = torch.maximum((aq @ full_k.abs().T).amax(1), (full_q.abs() @ full_k.abs().T).amax(1)) * scale
+        sq[t] = (full_q.square() @ full_k.square().T).amax(1) * scale * scale
+    return out, lse, mass, sq
+
+
+def check_prefill(dtype, out, lse, want, before=None):
+    """Every computed row by ref.check_decode; rows of no request hold what they held (`before`: (out, lse))."""
+    ro, rl, mass, sq = want
+    mine = ~torch.isnan(rl[:, 0])
+    if before is not None:
+        assert torch.equal(out.cpu()[~mine], before[0].cpu()[~mine])
+        assert torch.equal(lse.cpu()[~mine], before[1].cpu()[~mine])
+    ref.check_decode(dtype, out.cpu()[mine], lse.cpu()[mine], (ro[mine], rl[mine], mass[mine], sq[mine]))
