@@ -1157,14 +1157,17 @@ mla_status paged_decode_shape(const mla_dims *d, mla_dtype dt, int B, int page_s
     return MLA_OK;
 }
 
+void paged_plan_carve(PagedDecode *p, size_t slots, Carve &c) {
+    p->tile_off = (long *)c.take(((size_t)p->B + 1) * sizeof(long));
+    if (!p->tc) return;
+    p->parts = (PagedPart *)c.take(slots * sizeof(PagedPart));
+    p->first = (int *)c.take((size_t)p->workers * 2 * sizeof(int));
+    p->spans = (int2 *)c.take((size_t)p->B * p->row_tiles * sizeof(int2));
+}
+
 void paged_decode_carve(PagedDecode *p, Carve &c) {
     const size_t rows = (size_t)p->T * p->H, slots = (size_t)p->workers + (size_t)p->B * p->row_tiles;
-    p->tile_off = (long *)c.take(((size_t)p->B + 1) * sizeof(long));
-    if (p->tc) {
-        p->parts = (PagedPart *)c.take(slots * sizeof(PagedPart));
-        p->first = (int *)c.take((size_t)p->workers * 2 * sizeof(int));
-        p->spans = (int2 *)c.take((size_t)p->B * p->row_tiles * sizeof(int2));
-    }
+    paged_plan_carve(p, slots, c);
     p->qabs = c.take(rows * p->Dk * (p->tc ? 6 : 4));   // (three bf16 parts, or fp32)
     p->qpe = c.take(rows * p->Dr * (p->tc ? 6 : 4));
     if (p->tc) {
@@ -1183,7 +1186,7 @@ size_t paged_decode_ws(PagedDecode *p, void *base) {
     return align_up(c.off, 256);
 }
 
-// A step's tokens in the absorbed form, a round of them at a time.
+// A step's tokens, a round of them at a time.
 struct PagedRound {
     int *lens, *limits;   // keys of each group, of each token
     int2 *of;
@@ -1200,15 +1203,45 @@ mla_status paged_step_shape(const mla_dims *d, mla_dtype dt, int B, int n_tokens
     return MLA_OK;
 }
 
-size_t paged_step_ws(PagedDecode *p, PagedRound *r, void *base) {
-    Carve c;
-    c.base = (char *)base;
-    paged_decode_carve(p, c);
-    const size_t T = p->T;
+void paged_round_carve(const PagedDecode &p, PagedRound *r, Carve &c) {
+    const size_t T = p.T;
     r->lens = (int *)c.take(T * sizeof(int));
     r->limits = (int *)c.take(T * sizeof(int));
     r->of = (int2 *)c.take(T * sizeof(int2));
     r->groups = (int4 *)c.take(T * sizeof(int4));
+}
+
+size_t paged_step_ws(PagedDecode *p, PagedRound *r, void *base) {
+    Carve c;
+    c.base = (char *)base;
+    paged_decode_carve(p, c);
+    paged_round_carve(*p, r, c);
+    return align_up(c.off, 256);
+}
+
+mla_status paged_weights_shape(const mla_dims *d, mla_dtype dt, int B, int n_tokens, int page_size, int max_pages,
+                               PagedDecode *p) {
+    mla_status st = paged_step_shape(d, dt, B, n_tokens, page_size, max_pages, p);
+    if (st != MLA_OK) return st;
+    if (p->tc) {
+        p->row_tile = PAGED_W_ROWS;
+        p->tile = PAGED_W_TILE;
+        p->min_tiles = 1;
+    }
+    p->row_tiles = (p->H + p->row_tile - 1) / p->row_tile;
+    p->scores_only = true;
+    return MLA_OK;
+}
+
+size_t paged_weights_ws(PagedDecode *p, PagedRound *r, int B, unsigned long long **acc, void *base) {
+    Carve c;
+    c.base = (char *)base;
+    const size_t rows = (size_t)p->T * p->H, slots = (size_t)p->workers + (size_t)p->T * p->row_tiles;
+    paged_plan_carve(p, slots, c);
+    p->qabs = c.take(rows * p->Dk * 4);   // (two bf16 parts, or fp32)
+    p->qpe = c.take(rows * p->Dr * 4);
+    paged_round_carve(*p, r, c);
+    *acc = (unsigned long long *)c.take((size_t)B * p->max_pages * 8);
     return align_up(c.off, 256);
 }
 }  // namespace
@@ -1321,6 +1354,116 @@ mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n
         MLA_TRY(p.tc ? paged_decode_tc(q, cs) : paged_decode_simt(q, cs));
     }
     return MLA_OK;
+}
+
+size_t mla_paged_weights_workspace(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int page_size, int max_pages) {
+    PagedDecode p{};
+    PagedRound r{};
+    unsigned long long *acc;
+    if (paged_weights_shape(dims, dtype, B, n_tokens, page_size, max_pages, &p) != MLA_OK || B == 0) return 0;
+    return paged_weights_ws(&p, &r, B, &acc, nullptr);
+}
+
+mla_status mla_paged_weights(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int num_pages, int page_size,
+                             int max_pages, const void *q_nope, const void *q_pe, const float *lse, const void *c_cache,
+                             const void *kpe_cache, const int *block_table, const int *kv_lens, const int *cu_tokens,
+                             const int *positions, const void *w_kv_b, const float *prior, float *page_weights,
+                             void *workspace, size_t workspace_bytes, void *cuda_stream) {
+    PagedDecode p{};
+    PagedRound r{};
+    mla_status st = paged_weights_shape(dims, dtype, B, n_tokens, page_size, max_pages, &p);
+    if (st != MLA_OK) return st;
+    if (num_pages < 1 || (long)num_pages * page_size > INT_MAX) return MLA_ERR_SHAPE;
+    if (B == 0) return MLA_OK;
+    const void *ptrs[] = {c_cache, kpe_cache, w_kv_b, workspace}, *tok[] = {q_nope, q_pe, lse, positions};
+    for (const void *q : ptrs)
+        if (!q) return MLA_ERR_NULL;
+    for (const void *q : tok)
+        if (n_tokens && !q) return MLA_ERR_NULL;
+    if (!block_table || !kv_lens || !cu_tokens || !page_weights) return MLA_ERR_NULL;
+    for (const void *q : ptrs)
+        if (!aligned16(q)) return MLA_ERR_ALIGN;
+    if (!aligned16(q_nope) || !aligned16(q_pe)) return MLA_ERR_ALIGN;
+    const void *words[] = {lse, block_table, kv_lens, cu_tokens, positions, prior, page_weights};
+    for (const void *q : words)
+        if (!aligned4(q)) return MLA_ERR_ALIGN;
+    unsigned long long *acc;
+    const size_t need = paged_weights_ws(&p, &r, B, &acc, workspace);
+    if (workspace_bytes < need) return MLA_ERR_WORKSPACE;
+    const size_t es = ty_size(p.ty), rows = (size_t)n_tokens * p.H, keys = (size_t)num_pages * page_size, e = sizeof(int);
+    const size_t pages = (size_t)B * max_pages;
+    Range in[] = {rng(q_nope, rows * p.Dn * es), rng(q_pe, rows * p.Dr * es), rng(lse, rows * 4), rng(c_cache, keys * p.Dk * es),
+                  rng(kpe_cache, keys * p.Dr * es), rng(block_table, pages * e), rng(kv_lens, B * e),
+                  rng(cu_tokens, ((size_t)B + 1) * e), rng(positions, n_tokens * e),
+                  rng(w_kv_b, (size_t)p.H * (p.Dn + p.Dv) * p.Dk * es), rng(prior, prior == page_weights ? 0 : pages * 4)};
+    Range outs[] = {rng(page_weights, pages * 4), rng(workspace, need)};
+    st = check_alias(in, 11, outs, 2);
+    if (st != MLA_OK) return st;
+    p.num_pages = num_pages;
+    p.c_cache = c_cache;
+    p.kpe_cache = kpe_cache;
+    p.w = w_kv_b;
+    p.table = block_table;
+    p.lens = r.lens;
+    p.of = r.of;
+    p.limits = r.limits;
+    p.groups = r.groups;
+    // a page's sum is at most 2 n_tokens H page
+    int bits = 61;
+    for (double most = 2.0 * std::max(n_tokens, 1) * p.H * page_size; most > 1.0; most /= 2.0) --bits;
+    const PagedStep step{B, n_tokens, cu_tokens, positions, kv_lens};
+    cudaStream_t cs = (cudaStream_t)cuda_stream;
+    g_last_path = p.tc ? 2 : 1;
+    int s0 = 0;
+    do {   // (without tokens: the plan's zeros)
+        PagedDecode q = p;
+        const size_t at = (size_t)s0 * p.H;
+        q.T = q.B = std::min(n_tokens - s0, PAGED_ROUND);
+        q.q_nope = (const char *)q_nope + at * p.Dn * es;
+        q.q_pe = (const char *)q_pe + at * p.Dr * es;
+        q.pos = positions + s0;
+        MLA_TRY(launch_paged_plan(q, step, s0, r.lens, r.of, r.limits, r.groups, cs, acc, s0 == 0 ? (long)pages : 0));
+        if (n_tokens) {
+            MLA_TRY(p.tc ? paged_absorb_tc(q, cs) : paged_absorb_simt(q, cs));
+            MLA_TRY(launch_paged_weights(q, lse + at, acc, bits, cs));
+        }
+        s0 += PAGED_ROUND;
+    } while (s0 < n_tokens);
+    return cuda_status(launch_paged_weights_out((long)pages, acc, bits, prior, page_weights, cs));
+}
+
+size_t mla_paged_evict_workspace(int B) { return B < 1 ? 0 : (size_t)B * 12 + 512; }
+
+mla_status mla_paged_evict(int B, int page_size, int max_pages, int n_room, int keep_pages, int first_pages, int last_pages,
+                           const int *kv_lens, const int *block_table, const float *page_weights, int *table_out,
+                           float *weights_out, int *freed_pages, int *counts, void *workspace, size_t workspace_bytes,
+                           void *cuda_stream) {
+    if (B < 0 || B > PAGED_MAX_BATCH || page_size < 1 || max_pages < 1 || n_room < 0 || keep_pages < 0 || first_pages < 0 ||
+        last_pages < 1 || (long)max_pages * page_size > 1 << 30 || (long)B * max_pages > INT_MAX)
+        return MLA_ERR_SHAPE;
+    if (!counts || (n_room && !freed_pages) ||
+        (B && (!kv_lens || !block_table || !page_weights || !table_out || !weights_out || !workspace)))
+        return MLA_ERR_NULL;
+    const void *words[] = {kv_lens, block_table, page_weights, table_out, weights_out, freed_pages, counts};
+    for (const void *q : words)
+        if (!aligned4(q)) return MLA_ERR_ALIGN;
+    if (!aligned16(workspace)) return MLA_ERR_ALIGN;
+    if (workspace_bytes < mla_paged_evict_workspace(B)) return MLA_ERR_WORKSPACE;
+    const size_t e = 4, pages = (size_t)B * max_pages;
+    Range in[] = {rng(kv_lens, B * e), rng(block_table, table_out == block_table ? 0 : pages * e),
+                  rng(page_weights, weights_out == page_weights ? 0 : pages * e)};
+    Range outs[] = {rng(table_out, pages * e), rng(weights_out, pages * e), rng(freed_pages, n_room * e), rng(counts, 2 * e),
+                    rng(workspace, mla_paged_evict_workspace(B))};
+    mla_status st = check_alias(in, 3, outs, 5);
+    if (st != MLA_OK) return st;
+    Carve c;
+    c.base = (char *)workspace;
+    uint2 *pick = (uint2 *)c.take(B * sizeof(uint2));
+    int *gone = (int *)c.take(B * sizeof(int));
+    g_last_path = 1;
+    return cuda_status(launch_paged_evict(B, page_size, max_pages, n_room, keep_pages, first_pages, last_pages, kv_lens,
+                                          block_table, page_weights, table_out, weights_out, freed_pages, counts, gone, pick,
+                                          (cudaStream_t)cuda_stream));
 }
 
 const char *mla_status_string(mla_status s) {

@@ -13,6 +13,11 @@ cudaError_t launch_paged_tables(int B, int page, int max_pages, int n_free, int 
                                 const int *fresh, const int *free_pages, int *table, int *kv_lens, int *cu, int *slots,
                                 int *positions, int *counts, cudaStream_t st);
 
+// gone [B], pick [B]: scratch.
+cudaError_t launch_paged_evict(int B, int page, int max_pages, int room, int keep, int first, int last, const int *lens,
+                               const int *table, const float *weights, int *table_out, float *weights_out, int *freed,
+                               int *counts, int *gone, uint2 *pick, cudaStream_t st);
+
 // c rows at c + t * c_stride elements, k rows at k + t * k_stride.
 cudaError_t launch_paged_append(int ty, int T, long n_slots, int Dk, int Dr, float base, float eps, const void *c,
                                 long c_stride, const void *k, long k_stride, const void *w, const int *slots,
@@ -47,6 +52,7 @@ struct PagedDecode {
     const int *limits;
     const int4 *groups;
     const int *done;
+    bool scores_only;                // the absorb leaves the third parts of the queries out
     void *out;
     float *lse;
     int row_tile, row_tiles, tile;   // rows per item, items per group, keys per tile
@@ -63,6 +69,7 @@ struct PagedDecode {
 };
 // The launches of a call: absorb, attention, join.  Of a step's tokens behind launch_paged_plan.
 cudaError_t paged_decode_simt(const PagedDecode &p, cudaStream_t st);
+cudaError_t paged_absorb_simt(const PagedDecode &p, cudaStream_t st);
 
 // A step: request b's tokens are rows cu[b] .. cu[b + 1] - 1 of n_tokens, each at its position; the request
 // holds lens[b] tokens, its new ones among them.
@@ -74,15 +81,25 @@ struct PagedStep {
 // heads).
 constexpr int PAGED_ROUND = 2048;
 // The plan of tokens s0 .. s0 + p.T - 1: their groups, and the division of the groups' tiles (p.lens, p.of,
-// p.limits, p.groups are written; p.B = p.T).
+// p.limits, p.groups are written; p.B = p.T); n_zero words at `zero` are set to zero.
 cudaError_t launch_paged_plan(const PagedDecode &p, const PagedStep &s, int s0, int *lens, int2 *of, int *limits, int4 *groups,
-                              cudaStream_t st);
+                              cudaStream_t st, unsigned long long *zero = nullptr, long n_zero = 0);
+
+// The weights that the tokens of p gave the pages of their requests, added to acc [requests][max_pages] as integers of
+// 2^-bits, behind the plan and the absorb (scores_only): tensor cores with items of 128 rows and tiles of 256 keys, CUDA
+// cores with 16 and 32.  lse [T H].
+constexpr int PAGED_W_ROWS = 128, PAGED_W_TILE = 256;
+cudaError_t launch_paged_weights(const PagedDecode &p, const float *lse, unsigned long long *acc, int bits, cudaStream_t st);
+// out [n] = acc 2^-bits + prior (null: 0)
+cudaError_t launch_paged_weights_out(long n, const unsigned long long *acc, int bits, const float *prior, float *out, cudaStream_t st);
+cudaError_t paged_weights_read_and_clear_error(unsigned *flags, cudaStream_t st);
 
 // The tensor-core form (bf16): these dimensions and page size, any number of heads.
 // pairs of SMs of a GB300, keys per tile (no worker waits for another: with fewer SMs free they take turns)
 constexpr int PAGED_TC_WORKERS = 76, PAGED_TC_TILE = 64;
 bool paged_tc_supported(int Dk, int Dn, int Dr, int Dv, int page);
 cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st);
+cudaError_t paged_absorb_tc(const PagedDecode &p, cudaStream_t st);
 cudaError_t paged_tc_read_and_clear_error(unsigned *flags, cudaStream_t st);
 
 }  // namespace mla

@@ -489,22 +489,25 @@ __global__ void __launch_bounds__(NT) paged_join_simt_kernel(const __grid_consta
 }
 
 template <typename T>
-cudaError_t decode_simt(const PagedDecode &p, cudaStream_t st) {
+cudaError_t absorb_simt(const PagedDecode &p, cudaStream_t st) {
     Turns turns{};
     std::copy_n(paged_turns(p.base, p.Dr), p.Dr / 2, turns.v);
-    const unsigned units = (unsigned)((p.T + BT - 1) / BT) * (unsigned)p.H;
-    const unsigned blocks = units * (unsigned)((p.Dk + DC - 1) / DC), jblocks = units * (unsigned)((p.Dv + VC - 1) / VC);
-    const size_t s1 = ((size_t)BT * p.Dn + (size_t)NT / 32 * BT * DC) * 4, s2 = (size_t)layout(p.Dk, p.Dr).total * 4, s3 = (size_t)BT * p.Dk * 4;
+    const unsigned blocks = (unsigned)((p.T + BT - 1) / BT) * (unsigned)p.H * (unsigned)((p.Dk + DC - 1) / DC);
+    const size_t sm = ((size_t)BT * p.Dn + (size_t)NT / 32 * BT * DC) * 4;
+    const cudaError_t e = cudaFuncSetAttribute(paged_absorb_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    if (e != cudaSuccess) return e;
+    ProfScope ps("paged_absorb", st);
+    return launch_after(paged_absorb_simt_kernel<T>, blocks + 1, NT, sm, st, p, turns);
+}
+
+template <typename T>
+cudaError_t decode_simt(const PagedDecode &p, cudaStream_t st) {
+    const unsigned jblocks = (unsigned)((p.T + BT - 1) / BT) * (unsigned)p.H * (unsigned)((p.Dv + VC - 1) / VC);
+    const size_t s2 = (size_t)layout(p.Dk, p.Dr).total * 4, s3 = (size_t)BT * p.Dk * 4;
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(paged_absorb_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1)) != cudaSuccess)
-        return e;
     if ((e = cudaFuncSetAttribute(paged_attn_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2)) != cudaSuccess)
         return e;
-    {
-        ProfScope ps("paged_absorb", st);
-        e = launch_after(paged_absorb_simt_kernel<T>, blocks + 1, NT, s1, st, p, turns);
-    }
-    if (e != cudaSuccess) return e;
+    if ((e = absorb_simt<T>(p, st)) != cudaSuccess) return e;
     {
         ProfScope ps("paged_attn", st);
         e = launch_after(paged_attn_simt_kernel<T>, (unsigned)p.workers, NT, s2, st, p);
@@ -518,6 +521,10 @@ cudaError_t decode_simt(const PagedDecode &p, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t paged_absorb_simt(const PagedDecode &p, cudaStream_t st) {
+    return p.ty == TY_F32 ? absorb_simt<float>(p, st) : absorb_simt<__nv_bfloat16>(p, st);
+}
 
 cudaError_t paged_decode_simt(const PagedDecode &p, cudaStream_t st) {
     return p.ty == TY_F32 ? decode_simt<float>(p, st) : decode_simt<__nv_bfloat16>(p, st);

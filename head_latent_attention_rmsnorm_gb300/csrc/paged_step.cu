@@ -14,7 +14,7 @@ using tc::pdl_wait;
 namespace {
 
 // -------------------------------------------------------------------------- plan ----
-// One block, two tokens a thread: a token's request by binary search of the prefix sums, the keys that
+// Block 0, two tokens a thread: a token's request by binary search of the prefix sums, the keys that
 // it sees; groups begin where a request's tokens do, where one is not computed here, and after every
 // `most` tokens; then the groups' tile sums and the workers' parts as for decode.
 constexpr int PNT = 1024, CU_NEAR = 4096;
@@ -26,6 +26,8 @@ struct Plan {
     int *lens, *limits;
     int2 *of;
     int4 *groups;
+    unsigned long long *zero;
+    long n_zero;
 };
 
 __global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__ Plan a) {
@@ -36,6 +38,10 @@ __global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__
     int *lim = sm, *req = lim + PAGED_ROUND, *sums = req + PAGED_ROUND, *near = sums + PAGED_ROUND + 1;
     pdl_wait();
     pdl_launch_dependents();   // the absorb beside this; what follows it waits for both
+    if (blockIdx.x > 0) {
+        for (long i = (long)(blockIdx.x - 1) * PNT + tid; i < a.n_zero; i += (long)(gridDim.x - 1) * PNT) a.zero[i] = 0;
+        return;
+    }
     const bool here = a.s.B < CU_NEAR;
     if (here) {
         for (int i = tid; i <= a.s.B; i += PNT) near[i] = a.s.cu[i];
@@ -115,11 +121,11 @@ __global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__
 }  // namespace
 
 cudaError_t launch_paged_plan(const PagedDecode &p, const PagedStep &s, int s0, int *lens, int2 *of, int *limits, int4 *groups,
-                              cudaStream_t st) {
-    Plan a{p, s, s0, std::max(1, p.row_tile / p.H), lens, limits, of, groups};
+                              cudaStream_t st, unsigned long long *zero, long n_zero) {
+    Plan a{p, s, s0, std::max(1, p.row_tile / p.H), lens, limits, of, groups, zero, n_zero};
     const size_t sm = (3 * PAGED_ROUND + 1 + (s.B < CU_NEAR ? s.B + 1 : 0)) * sizeof(int);
     ProfScope ps("paged_plan", st);
-    return launch_after(paged_plan_kernel, 1, PNT, sm, st, a);
+    return launch_after(paged_plan_kernel, 1 + (unsigned)std::min((n_zero + PNT - 1) / PNT, 150l), PNT, sm, st, a);
 }
 
 }  // namespace mla

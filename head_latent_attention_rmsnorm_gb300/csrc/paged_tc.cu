@@ -156,7 +156,8 @@ __device__ void rotate_queries(const Absorb &a, int i, int lane) {
     const PagedDecode &p = a.p;
     const int per = (p.H + 31) / 32, b = i / per, h0 = i % per * 32;
     if (b >= p.T || (p.done && p.done[b])) return;
-    const int keys = p.pos ? 0 : keys_of(p, b);   // (a step's tokens may be few keys' whatever their position)
+    // (a step's tokens may see few keys whatever their position)
+    const int keys = p.scores_only ? 2147483647 : p.pos ? 0 : keys_of(p, b);
     const float2 cs = turn_cs(a.turns.v[lane], p.pos ? p.pos[b] : keys - 1);
     const int h1 = min(h0 + 32, p.H);
 #pragma unroll 1
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
     for (int i = tid; i < DN * (AB_DIMS / 8); i += 128)
         cp16(sw + (i >> 4) * AB_PITCH + (i & 15) * 16, w + (long)(i >> 4) * DK + (i & 15) * 8);
     int *keys = (int *)(sm + AB_SMEM) - AB_GROUP;
-    if (tid < nb) keys[tid] = step ? 0 : keys_of(p, b0 + tid);
+    if (tid < nb) keys[tid] = p.scores_only ? 2147483647 : step ? 0 : keys_of(p, b0 + tid);
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     uint32_t A[2][8][4];
@@ -1375,10 +1376,9 @@ bool paged_tc_supported(int Dk, int Dn, int Dr, int Dv, int page) {
     return Dk == DK && Dn == DN && Dr == DR && Dv == DV && page % 8 == 0;
 }
 
-cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
-    using ull = unsigned long long;
-    cudaError_t e;
-    const ull rows = (ull)p.num_pages * p.page, heads = (ull)p.T * p.H;
+namespace {
+Absorb absorb_of(const PagedDecode &p) {
+    const size_t heads = (size_t)p.T * p.H;
     Absorb ab{};
     ab.p = p;
     ab.qhi = (bf16 *)p.qabs;
@@ -1394,7 +1394,23 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     ab.groups = (p.T + ab.group - 1) / ab.group;
     ab.rot_blocks = (int)(((long)p.T * ((p.H + 31) / 32) + 3) / 4);
     std::copy_n(paged_turns(p.base, DR), DR / 2, ab.turns.v);
+    return ab;
+}
+}  // namespace
 
+cudaError_t paged_absorb_tc(const PagedDecode &p, cudaStream_t st) {
+    const Absorb ab = absorb_of(p);
+    const cudaError_t e = cudaFuncSetAttribute(paged_absorb_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM);
+    if (e != cudaSuccess) return e;
+    ProfScope ps("paged_absorb", st);
+    return launch_after(paged_absorb_tc_kernel, (unsigned)(p.H * 4 * ab.groups + 1 + ab.rot_blocks), 128, AB_SMEM, st, ab);
+}
+
+cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
+    using ull = unsigned long long;
+    cudaError_t e;
+    const ull rows = (ull)p.num_pages * p.page, heads = (ull)p.T * p.H;
+    const Absorb ab = absorb_of(p);
     Attn at{};
     int unit = NK;   // rows that always share a page: the largest power of two up to a tile that divides one
     while (p.page % unit) unit /= 2;
@@ -1427,8 +1443,6 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     at.scale_log2 = p.scale * 1.4426950408889634f;
     at.idesc_s = idesc_f16(128, NK, false);
     at.idesc_pv = idesc_f16(128, 256, false, true);
-    if ((e = cudaFuncSetAttribute(paged_absorb_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM)) != cudaSuccess)
-        return e;
     if ((e = cudaFuncSetAttribute(paged_join_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, JSMEM)) != cudaSuccess) return e;
     CUtensorMap mW;
     {
@@ -1447,11 +1461,7 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
                                           : paged_attn_tc_kernel<8, false>);
     if ((e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess)
         return e;
-    {
-        ProfScope ps("paged_absorb", st);
-        e = launch_after(paged_absorb_tc_kernel, (unsigned)(p.H * 4 * ab.groups + 1 + ab.rot_blocks), 128, AB_SMEM, st, ab);
-    }
-    if (e != cudaSuccess) return e;
+    if ((e = paged_absorb_tc(p, st)) != cudaSuccess) return e;
     {
         ProfScope ps("paged_attn", st);
         e = launch_after(attn, 2 * p.workers, NTHREADS, SMEM_BYTES, st, m, at);

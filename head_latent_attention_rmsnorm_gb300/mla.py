@@ -7,7 +7,7 @@ Two layers, argument marshalling only:
   own names, taking integers for pointers and sizes.
 * ``latent_attn_fwd``, ``absorbed_attn_fwd``, ``decode_splitkv``, ``lse_combine``,
   ``tpla_decode``, ``rmsnorm``, ``rmsnorm_bwd``, ``paged_tables``, ``paged_append``,
-  ``paged_decode``, ``paged_prefill``:
+  ``paged_decode``, ``paged_prefill``, ``paged_weights``, ``paged_evict``:
   the same calls taking torch tensors; they allocate any output or workspace the
   caller did not pass (through torch's allocator, so the CUDA caching allocator sees
   every byte) and raise :class:`MlaError` on a non-OK status.  ``stream`` (a
@@ -118,6 +118,14 @@ def lib() -> ctypes.CDLL:
         L.mla_paged_prefill.restype = _i
         L.mla_paged_prefill_workspace.argtypes = [D, _i, _i, _i, _i, _i]
         L.mla_paged_prefill_workspace.restype = _sz
+        L.mla_paged_weights.argtypes = [D, _i, _i, _i, _i, _i, _i] + [_vp] * 13 + [_sz, _vp]
+        L.mla_paged_weights.restype = _i
+        L.mla_paged_weights_workspace.argtypes = [D, _i, _i, _i, _i, _i]
+        L.mla_paged_weights_workspace.restype = _sz
+        L.mla_paged_evict.argtypes = [_i] * 7 + [_vp] * 8 + [_sz, _vp]
+        L.mla_paged_evict.restype = _i
+        L.mla_paged_evict_workspace.argtypes = [_i]
+        L.mla_paged_evict_workspace.restype = _sz
         L.mla_status_string.argtypes = [_i]
         L.mla_status_string.restype = ctypes.c_char_p
         L.mla_check_device_error.argtypes = [_vp]
@@ -237,6 +245,22 @@ def mla_paged_prefill_workspace(*args) -> int:
     return lib().mla_paged_prefill_workspace(*args)
 
 
+def mla_paged_weights(*args) -> int:
+    return lib().mla_paged_weights(*args)
+
+
+def mla_paged_weights_workspace(*args) -> int:
+    return lib().mla_paged_weights_workspace(*args)
+
+
+def mla_paged_evict(*args) -> int:
+    return lib().mla_paged_evict(*args)
+
+
+def mla_paged_evict_workspace(*args) -> int:
+    return lib().mla_paged_evict_workspace(*args)
+
+
 def mla_status_string(status: int) -> str:
     return lib().mla_status_string(status).decode()
 
@@ -261,7 +285,7 @@ KERNELS = ("prep", "latent_prep", "rope_table", "rope_rows", "convert", "gemm_si
            "tc_gemm", "tc_attn", "tc_latent_attn", "tc_decode_attn", "transpose", "rmsnorm", "rmsnorm_bwd", "tpla_expand",
            "tpla_combine", "wait_probe", "tc_fused_attn", "bwd_rowdot", "attn_bwd_simt", "bwd_rows",
            "bwd_prep", "tc_bwd_dkv", "tc_bwd_dq", "paged_tables", "paged_append", "paged_absorb", "paged_attn",
-           "paged_join", "paged_plan")
+           "paged_join", "paged_plan", "paged_weights", "paged_weights_out", "paged_evict")
 
 
 def launch_count() -> int:
@@ -859,3 +883,88 @@ def paged_prefill(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_len
     if st != 0:
         raise MlaError(st, "mla_paged_prefill")
     return out, lse
+
+
+def paged_weights_workspace(d: Dims, n_tokens: int, c_cache, block_table) -> torch.Tensor:
+    """A workspace for :func:`paged_weights` calls of ``n_tokens`` rows with this cache and table, one call
+    at a time."""
+    n = lib().mla_paged_weights_workspace(ctypes.byref(d), _dt(c_cache), block_table.shape[0], n_tokens,
+                                          c_cache.shape[1], block_table.shape[1])
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=c_cache.device)
+
+
+def paged_weights(d: Dims, q_nope, q_pe, lse, c_cache, kpe_cache, block_table, kv_lens, cu_tokens, positions, w_kv_b, *,
+                  prior=None, out=None, workspace=None, stream=None):
+    """The attention weight that the step's tokens gave each page of their requests, summed over tokens and
+    heads, on top of ``prior`` [B, max_pages] (fp32); ``lse`` as :func:`paged_prefill` (or :func:`paged_decode`)
+    returned it.  ``out`` may be ``prior``.  Returns ``out`` [B, max_pages]."""
+    if stream is not None:
+        return _on_stream(stream, paged_weights, d, q_nope, q_pe, lse, c_cache, kpe_cache, block_table, kv_lens, cu_tokens,
+                          positions, w_kv_b, prior=prior, out=out, workspace=workspace)
+    dev, dt, _, at, B, n, num_pages, page, max_pages, ptrs = _step_args(
+        d, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, cu_tokens, positions, w_kv_b)
+    if at != _current_device():
+        with torch.cuda.device(at):
+            return paged_weights(d, q_nope, q_pe, lse, c_cache, kpe_cache, block_table, kv_lens, cu_tokens, positions,
+                                 w_kv_b, prior=prior, out=out, workspace=workspace)
+    f32, shape = torch.float32, (B, max_pages)
+    if out is None:
+        out = torch.empty(shape, dtype=f32, device=dev)
+    if workspace is None:
+        workspace = paged_weights_workspace(d, n, c_cache, block_table)
+    else:
+        _workspace(0, dev, workspace)
+    st = lib().mla_paged_weights(
+        d, dt, B, n, num_pages, page, max_pages, *ptrs[:2], _need("lse", lse, (n, d.n_heads), f32, at), *ptrs[2:],
+        None if prior is None else _need("prior", prior, shape, f32, at), _need("out", out, shape, f32, at),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _raw_stream(at))
+    if st != 0:
+        raise MlaError(st, "mla_paged_weights")
+    return out
+
+
+class PagedEvicted(NamedTuple):
+    freed: torch.Tensor    # ids of the evicted pages, counts[0] of them
+    counts: torch.Tensor   # [2] pages evicted, pages that were to be
+
+
+def paged_evict(kv_lens, block_table, page_weights, *, page_size, keep_pages, first_pages=0, last_pages=1, table_out=None,
+                weights_out=None, freed=None, counts=None, workspace=None, stream=None) -> PagedEvicted:
+    """Evict the pages of least ``page_weights`` [B, max_pages] (fp32) from the requests that hold more than
+    ``keep_pages``, never their ``first_pages`` first and ``last_pages`` last ones: -1 in ``table_out`` and 0 in
+    ``weights_out`` (default: ``block_table`` and ``page_weights`` themselves), the ids in ``freed``."""
+    if stream is not None:
+        return _on_stream(stream, paged_evict, kv_lens, block_table, page_weights, page_size=page_size, keep_pages=keep_pages,
+                          first_pages=first_pages, last_pages=last_pages, table_out=table_out, weights_out=weights_out,
+                          freed=freed, counts=counts, workspace=workspace)
+    dev = _device(block_table)
+    if block_table.dim() != 2 or block_table.shape[1] < 1:
+        raise ValueError("block_table must be [B, max_pages]")
+    shape, at, i32, f32 = tuple(block_table.shape), block_table.get_device(), torch.int32, torch.float32
+    if at != _current_device():
+        with torch.cuda.device(at):
+            return paged_evict(kv_lens, block_table, page_weights, page_size=page_size, keep_pages=keep_pages,
+                               first_pages=first_pages, last_pages=last_pages, table_out=table_out, weights_out=weights_out,
+                               freed=freed, counts=counts, workspace=workspace)
+    B, max_pages = shape
+    if freed is None:
+        freed = torch.empty(B * max_pages, dtype=i32, device=dev)
+    elif not isinstance(freed, torch.Tensor):
+        raise TypeError("freed: expected a torch.Tensor, got %s" % type(freed).__name__)
+    if counts is None:
+        counts = torch.empty(2, dtype=i32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(lib().mla_paged_evict_workspace(B), dtype=torch.uint8, device=dev)
+    else:
+        _workspace(0, dev, workspace)
+    room = freed.numel()
+    st = lib().mla_paged_evict(
+        B, page_size, max_pages, room, keep_pages, first_pages, last_pages, _need("kv_lens", kv_lens, (B,), i32, at),
+        _need("block_table", block_table, shape, i32, at), _need("page_weights", page_weights, shape, f32, at),
+        _need("table_out", block_table if table_out is None else table_out, shape, i32, at),
+        _need("weights_out", page_weights if weights_out is None else weights_out, shape, f32, at),
+        _need("freed", freed, (room,), i32, at), _need("counts", counts, (2,), i32, at), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _raw_stream(at))
+    if st != 0:
+        raise MlaError(st, "mla_paged_evict")
+    return PagedEvicted(freed, counts)

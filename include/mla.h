@@ -353,6 +353,48 @@ mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n
                              size_t workspace_bytes, void *cuda_stream);
 size_t mla_paged_prefill_workspace(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int page_size, int max_pages);
 
+/*
+ * The attention weight that a step's tokens gave each page of their requests:
+ *   page_weights[b][c] = prior[b][c] + sum over b's tokens t, all heads h and the keys j of the page in column c
+ *                        that t sees of exp(s_tjh - lse[t][h])
+ * for every column of block_table; scores, rows and what a token sees as in mla_paged_prefill, whose lse (or, for
+ * one token a request, mla_paged_decode's: cu_tokens 0, 1, .., B and positions kv_lens - 1) is the input.  Which tokens
+ * count is the caller's choice: all of a step, or a prompt's last ones.  Pages that a token does not see, or whose
+ * id is bad, gain nothing, nor does anything from a token whose lse is -inf.
+ *   lse (fp32) [n_tokens, H]   prior, page_weights (fp32) [B, max_pages]; prior NULL: zeros; may be page_weights itself
+ * A weight is cut to [0, 2] (1 to rounding, where lse belongs to the scores) and NaN counts as 0.  The sums
+ * are 64-bit integers, of which one is 2^-k, k such that 2 n_tokens H page_size weights fit 61 bits: the same bits for
+ * the same call.  Types, dimensions (W_K's rows of w_kv_b are read) and the workspace as in mla_paged_prefill;
+ * on the tensor cores the queries are bf16 pairs, exact to 2^-17.
+ */
+mla_status mla_paged_weights(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int num_pages, int page_size,
+                             int max_pages, const void *q_nope, const void *q_pe, const float *lse, const void *c_cache,
+                             const void *kpe_cache, const int *block_table, const int *kv_lens, const int *cu_tokens,
+                             const int *positions, const void *w_kv_b, const float *prior, float *page_weights,
+                             void *workspace, size_t workspace_bytes, void *cuda_stream);
+size_t mla_paged_weights_workspace(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int page_size, int max_pages);
+
+/*
+ * Eviction to a budget.  A request of kv_lens[b] tokens holds the pages with an id >= 0 among its first
+ * n = ceil(kv_lens[b] / page_size) columns.  Where it holds more than keep_pages, those of least page_weights go: as
+ * many as it holds too many, among the columns first_pages .. n - last_pages - 1; of equal weights the lowest
+ * column, NaN last.  last_pages >= 1, so that the page being filled stays.
+ *   table_out   [B, max_pages]   block_table with -1 for the evicted pages (may be block_table itself): the attention
+ *                                calls give such positions no weight, mla_paged_tables enters no page there, and
+ *                                the request's positions stay what they are
+ *   weights_out [B, max_pages]   page_weights with 0 for them (may be page_weights itself)
+ *   freed_pages [n_room]         their ids, in the order of the requests and columns, to be put behind the list of free
+ *                                pages; entries behind counts[0] are left
+ *   counts      [2]              pages evicted, pages that were to be; a page behind the list's n_room-th is not evicted
+ * A page that several requests name is listed once for each.  Lengths as in mla_paged_decode; 0 <= B <= 16384,
+ * B max_pages < 2^31.  The workspace belongs to one call at a time.
+ */
+mla_status mla_paged_evict(int B, int page_size, int max_pages, int n_room, int keep_pages, int first_pages, int last_pages,
+                           const int *kv_lens, const int *block_table, const float *page_weights, int *table_out,
+                           float *weights_out, int *freed_pages, int *counts, void *workspace, size_t workspace_bytes,
+                           void *cuda_stream);
+size_t mla_paged_evict_workspace(int B);
+
 /* Workspace bytes the matching call needs (0 on invalid arguments). */
 size_t mla_latent_attn_workspace(const mla_dims *dims, mla_dtype dtype, int B, int s_q, int s_kv,
                                  int q_offset, int causal, int head_count, int head_shard);
@@ -451,7 +493,8 @@ mla_status mla_decode_splitkv_noalloc(const mla_dims *dims, mla_dtype dtype, int
  *   "tc_latent_attn", "tc_decode_attn", "transpose", "rmsnorm", "rmsnorm_bwd", "tpla_expand",
  *   "tpla_combine", "wait_probe", "tc_fused_attn", "bwd_rowdot",
  *   "attn_bwd_simt", "bwd_rows", "bwd_prep", "tc_bwd_dkv", "tc_bwd_dq",
- *   "paged_tables", "paged_append", "paged_absorb", "paged_attn", "paged_join", "paged_plan".
+ *   "paged_tables", "paged_append", "paged_absorb", "paged_attn", "paged_join", "paged_plan",
+ *   "paged_weights", "paged_weights_out", "paged_evict".
  * mla_profile_reset: forgets recorded events, keeps recording on/off as it was.
  * Launches from several host threads are recorded safely; call enable, reset and the
  * queries between computations, not while another thread's calls are in flight.
