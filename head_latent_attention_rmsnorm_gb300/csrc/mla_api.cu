@@ -1211,11 +1211,41 @@ void paged_round_carve(const PagedDecode &p, PagedRound *r, Carve &c) {
     r->groups = (int4 *)c.take(T * sizeof(int4));
 }
 
-size_t paged_step_ws(PagedDecode *p, PagedRound *r, void *base) {
+// The buffers of the explicit form: none where the call cannot use it.
+struct PagedExplicit {
+    PagedChunk c;
+    int hs;   // heads of a shard, 0: none of it
+};
+void paged_explicit_carve(const PagedDecode &p, int B, int n_tokens, int key_rows, int head_shard, PagedExplicit *x, Carve &c) {
+    *x = PagedExplicit{};
+    key_rows = key_rows / 256 * 256;
+    if (!p.tc || n_tokens < CHUNK_MIN || key_rows == 0) return;
+    x->hs = head_shard == 0 ? p.H : std::min(head_shard, p.H);
+    const size_t R = key_rows, T = n_tokens;
+    x->c.key_rows = key_rows;
+    x->c.max_tiles = chunk_tiles(n_tokens);
+    x->c.ctl = (int *)c.take(2 * sizeof(int));
+    x->c.key0 = (int *)c.take(B * sizeof(int));
+    x->c.holes = (int *)c.take(B * sizeof(int));
+    x->c.block_of = (int *)c.take(R / 128 * sizeof(int));
+    x->c.limits = (int *)c.take(T * sizeof(int));
+    x->c.done = (int *)c.take(T * sizeof(int));
+    x->c.raw = (StepTile *)c.take((size_t)x->c.max_tiles * sizeof(StepTile));
+    x->c.tiles = (StepTile *)c.take((size_t)x->c.max_tiles * sizeof(StepTile));
+    x->c.held = (uint32_t *)c.take(R / 32 * sizeof(uint32_t));
+    x->c.chat = c.take(R * p.Dk * 2);
+    x->c.kpe = c.take(R * p.Dr * 2);
+    x->c.qpe = c.take(T * p.H * p.Dr * 2);
+    x->c.kws = c.take(R * x->hs * p.Dn * 2);
+    x->c.vws = c.take(R * x->hs * p.Dv * 2);
+}
+
+size_t paged_prefill_ws(PagedDecode *p, PagedRound *r, PagedExplicit *x, int B, int n_tokens, int key_rows, int head_shard, void *base) {
     Carve c;
     c.base = (char *)base;
     paged_decode_carve(p, c);
     paged_round_carve(*p, r, c);
+    paged_explicit_carve(*p, B, n_tokens, key_rows, head_shard, x, c);
     return align_up(c.off, 256);
 }
 
@@ -1291,23 +1321,28 @@ mla_status mla_paged_decode(const mla_dims *dims, mla_dtype dtype, int B, int nu
     return cuda_status(p.tc ? paged_decode_tc(p, (cudaStream_t)cuda_stream) : paged_decode_simt(p, (cudaStream_t)cuda_stream));
 }
 
-size_t mla_paged_prefill_workspace(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int page_size, int max_pages) {
+size_t mla_paged_prefill_workspace(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int page_size, int max_pages,
+                                   int key_rows, int head_shard) {
     PagedDecode p{};
     PagedRound r{};
-    if (paged_step_shape(dims, dtype, B, n_tokens, page_size, max_pages, &p) != MLA_OK || B == 0 || n_tokens == 0) return 0;
-    return paged_step_ws(&p, &r, nullptr);
+    PagedExplicit x{};
+    if (paged_step_shape(dims, dtype, B, n_tokens, page_size, max_pages, &p) != MLA_OK || B == 0 || n_tokens == 0 ||
+        key_rows < 0 || head_shard < 0)
+        return 0;
+    return paged_prefill_ws(&p, &r, &x, B, n_tokens, key_rows, head_shard, nullptr);
 }
 
 mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int num_pages, int page_size,
-                             int max_pages, const void *q_nope, const void *q_pe, const void *c_cache,
-                             const void *kpe_cache, const int *block_table, const int *kv_lens, const int *cu_tokens,
-                             const int *positions, const void *w_kv_b, void *out, float *lse, void *workspace,
-                             size_t workspace_bytes, void *cuda_stream) {
+                             int max_pages, int key_rows, int head_shard, const void *q_nope, const void *q_pe,
+                             const void *c_cache, const void *kpe_cache, const int *block_table, const int *kv_lens,
+                             const int *cu_tokens, const int *positions, const void *w_kv_b, void *out, float *lse,
+                             void *workspace, size_t workspace_bytes, void *cuda_stream) {
     PagedDecode p{};
     PagedRound r{};
+    PagedExplicit x{};
     mla_status st = paged_step_shape(dims, dtype, B, n_tokens, page_size, max_pages, &p);
     if (st != MLA_OK) return st;
-    if (num_pages < 1 || (long)num_pages * page_size > INT_MAX) return MLA_ERR_SHAPE;
+    if (num_pages < 1 || (long)num_pages * page_size > INT_MAX || key_rows < 0 || head_shard < 0) return MLA_ERR_SHAPE;
     if (B == 0 || n_tokens == 0) return MLA_OK;
     const void *ptrs[] = {q_nope, q_pe, c_cache, kpe_cache, w_kv_b, out, lse, workspace};
     for (const void *q : ptrs)
@@ -1319,7 +1354,7 @@ mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n
         if (!aligned16(q)) return MLA_ERR_ALIGN;
     for (const int *q : idx)
         if (!aligned4(q)) return MLA_ERR_ALIGN;
-    const size_t need = paged_step_ws(&p, &r, workspace);
+    const size_t need = paged_prefill_ws(&p, &r, &x, B, n_tokens, key_rows, head_shard, workspace);
     if (workspace_bytes < need) return MLA_ERR_WORKSPACE;
     const size_t es = ty_size(p.ty), rows = (size_t)n_tokens * p.H, keys = (size_t)num_pages * page_size, e = sizeof(int);
     Range in[] = {rng(q_nope, rows * p.Dn * es), rng(q_pe, rows * p.Dr * es), rng(c_cache, keys * p.Dk * es),
@@ -1340,6 +1375,14 @@ mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n
     p.groups = r.groups;
     const PagedStep step{B, n_tokens, cu_tokens, positions, kv_lens};
     g_last_path = p.tc ? 2 : 1;
+    if (x.hs) {
+        PagedDecode q = p;
+        q.q_pe = q_pe;
+        MLA_TRY(launch_paged_chunk(q, step, x.c, (cudaStream_t)cuda_stream));
+        const TcStep t{n_tokens, p.H, x.hs, x.c.key_rows, p.scale, q_nope, x.c.qpe, x.c.chat, x.c.kpe, w_kv_b, x.c.kws, x.c.vws,
+                       out, lse, x.c.ctl, x.c.tiles, x.c.limits, x.c.done, x.c.held, x.c.holes};
+        MLA_TRY(tc_step_prefill(t, (cudaStream_t)cuda_stream));
+    }
     for (int s0 = 0; s0 < n_tokens; s0 += PAGED_ROUND) {
         PagedDecode q = p;
         const size_t at = (size_t)s0 * p.H;
@@ -1347,6 +1390,7 @@ mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n
         q.q_nope = (const char *)q_nope + at * p.Dn * es;
         q.q_pe = (const char *)q_pe + at * p.Dr * es;
         q.pos = positions + s0;
+        q.done = x.hs ? x.c.done + s0 : nullptr;
         q.out = (char *)out + at * p.Dv * es;
         q.lse = lse + at;
         cudaStream_t cs = (cudaStream_t)cuda_stream;

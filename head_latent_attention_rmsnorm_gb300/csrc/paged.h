@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "tc.h"
+
 namespace mla {
 
 constexpr int PAGED_MAX_BATCH = 16384;   // requests of one mla_paged_tables call (its prefix sums stay in shared memory)
@@ -84,6 +86,24 @@ constexpr int PAGED_ROUND = 2048;
 // p.limits, p.groups are written; p.B = p.T); n_zero words at `zero` are set to zero.
 cudaError_t launch_paged_plan(const PagedDecode &p, const PagedStep &s, int s0, int *lens, int2 *of, int *limits, int4 *groups,
                               cudaStream_t st, unsigned long long *zero = nullptr, long n_zero = 0);
+
+// The explicit form of the requests with many tokens (tensor cores): CHUNK_MIN tokens and more that see more than CHUNK_FEW
+// keys.  Tiles of 128 tokens: at most n_tokens / 128 and one more a request.
+constexpr int CHUNK_MIN = 160, CHUNK_FEW = 512, CHUNK_SORT = 2048;
+struct PagedChunk {
+    int key_rows;                // rows of the key buffers, a multiple of 256
+    int max_tiles;
+    int *ctl;                    // [2]: rows in use, tiles
+    int *key0, *holes;           // [B]: a request's first key row (-1: absorbed); nonzero: some page is missing
+    int *block_of;               // [key_rows / 128]: the request of each 128 rows
+    int *limits, *done;          // [n_tokens]: keys seen; nonzero: explicit
+    StepTile *raw, *tiles;
+    uint32_t *held;              // a bit per key row
+    void *chat, *kpe, *qpe, *kws, *vws;
+};
+inline int chunk_tiles(int n_tokens) { return n_tokens / 128 + n_tokens / CHUNK_MIN + 1; }
+// The plan and the gathered rows; p.q_pe of the whole step.
+cudaError_t launch_paged_chunk(const PagedDecode &p, const PagedStep &s, const PagedChunk &c, cudaStream_t st);
 
 // The weights that the tokens of p gave the pages of their requests, added to acc [requests][max_pages] as integers of
 // 2^-bits, behind the plan and the absorb (scores_only): tensor cores with items of 128 rows and tiles of 256 keys, CUDA

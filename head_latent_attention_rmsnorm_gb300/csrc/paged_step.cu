@@ -1,5 +1,8 @@
-// paged_step.cu -- a serving step's tokens over the paged latent cache: which tokens share a work item, and
-// the division of the items among the workers.
+// paged_step.cu -- a serving step's tokens over the paged latent cache: which tokens share a work item, the
+// division of the items among the workers; which requests' tokens go in the explicit form, and their keys'
+// rows gathered from the pages.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 
 #include "paged_common.cuh"
@@ -118,7 +121,233 @@ __global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__
     else plan_block<PNT>(p);
 }
 
+// The sum of the values of the threads in front, and of all, by a block of PNT threads.
+__device__ long block_before(long n, long *warp_tot, long &all) {
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    long x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();   // the previous call's totals have been read
+    if (lane == 31) warp_tot[wp] = x;
+    __syncthreads();
+    long before = x - n;
+    all = 0;
+#pragma unroll
+    for (int i = 0; i < PNT / 32; ++i) {
+        if (i < wp) before += warp_tot[i];
+        all += warp_tot[i];
+    }
+    return before;
+}
+
+// ----------------------------------------------------------------- explicit plan ----
+// Which form is cheaper.  A (token, key, head) costs 2 (512 + 64 + 512) = 2176 operations absorbed and 2 (192 + 128) =
+// 640 explicit, which has 2 * 256 * 512 on top for a key and head, once for all of the request's tokens: equal at 171
+// tokens, whatever the keys and heads.  A request goes explicit from CHUNK_MIN tokens on, where its keys' rows,
+// rounded up to whole tiles, fit in what the requests in front of it left of the buffers.  Its tokens
+// that see up to CHUNK_FEW keys stay absorbed: the explicit form rounds K_nope and P to fp16, an error of about
+// 2e-4 / sqrt(0.4 keys) in a log-sum-exp, which at few keys is more than the rest of the call's.
+// One block: prefix sums over the requests, then a warp per 128 tokens, then the tiles in falling order of their keys.
+struct Chunk {
+    PagedStep s;
+    PagedChunk c;
+    int cap, key_rows;
+};
+
+__global__ void __launch_bounds__(PNT) paged_chunk_kernel(const __grid_constant__ Chunk a) {
+    __shared__ long warp_tot[PNT / 32];
+    __shared__ int weight[CHUNK_SORT];
+    const int tid = threadIdx.x, lane = tid & 31, N = a.s.n_tokens;
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int i = tid; i < N; i += PNT) a.c.done[i] = 0;
+    long rows = 0, tiles = 0, used = 0;
+    for (int b0 = 0; b0 < a.s.B; b0 += PNT) {
+        const int b = b0 + tid;
+        int t0 = 0, n = 0, keys = 0;
+        if (b < a.s.B) {
+            t0 = min(max(a.s.cu[b], 0), N);
+            n = min(max(a.s.cu[b + 1], 0), N) - t0;
+            keys = min(max(a.s.lens[b], 0), a.cap);
+        }
+        const bool may = min(n, keys - CHUNK_FEW) >= CHUNK_MIN;
+        const long need = may ? (keys + 127l) / 128 * 128 : 0;
+        long all;
+        const long r0 = rows + block_before(need, warp_tot, all);
+        rows += all;
+        const bool fits = may && r0 + need <= a.key_rows;
+        const int mine = fits ? (n + 127) / 128 : 0;
+        const long e0 = tiles + block_before(mine, warp_tot, all);
+        tiles += all;
+        block_before(fits ? need : 0, warp_tot, all);   // (those that fit are the first of those that may)
+        used += all;
+        if (b < a.s.B) {
+            a.c.key0[b] = fits ? (int)r0 : -1;
+            a.c.holes[b] = 0;
+            if (fits) {
+                for (int e = 0; e < mine && e0 + e < a.c.max_tiles; ++e) {   // (more only where cu decreases)
+                    StepTile x{};
+                    x.token = t0 + 128 * e;
+                    x.rows = min(128, n - 128 * e);
+                    x.key = (int)r0;
+                    x.request = b;
+                    a.c.raw[e0 + e] = x;
+                }
+                for (int i = 0; i < (int)(need / 128); ++i) a.c.block_of[r0 / 128 + i] = b;
+            }
+        }
+    }
+    __syncthreads();
+    const int n = (int)min(tiles, (long)a.c.max_tiles);
+    const bool sorted = n <= CHUNK_SORT;
+    for (int e = tid >> 5; e < n; e += PNT / 32) {
+        const StepTile x = a.c.raw[e];
+        const int keys = min(max(a.s.lens[x.request], 0), a.cap);
+        int most = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = lane + 32 * i, t = x.token + r;
+            if (r >= x.rows) continue;
+            const int pos = a.s.positions[t], sees = pos < 0 ? 0 : min(keys, pos == 2147483647 ? pos : pos + 1);
+            a.c.limits[t] = sees;
+            if (sees > CHUNK_FEW) {
+                a.c.done[t] = 1;
+                most = max(most, sees);
+            }
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) {
+            a.c.raw[e].tiles = (most + 127) / 128;
+            if (sorted) weight[e] = (most + 127) / 128;
+        }
+    }
+    __syncthreads();
+    // the tiles that have keys here, the heaviest first (a step of more than CHUNK_SORT tiles as they come)
+    long out = 0;
+    for (int base = 0; base < n; base += PNT) {
+        const int e = base + tid;
+        StepTile x{};
+        if (e < n) x = a.c.raw[e];
+        long all, at = out + block_before(x.tiles > 0, warp_tot, all);
+        out += all;
+        if (x.tiles == 0) continue;
+        if (sorted) {
+            at = 0;
+            for (int i = 0; i < n; ++i) at += weight[i] > x.tiles || (weight[i] == x.tiles && i < e);
+        }
+        a.c.tiles[at] = x;
+    }
+    if (tid == 0) {
+        a.c.ctl[0] = (int)used;
+        a.c.ctl[1] = (int)out;
+    }
+}
+
+// ------------------------------------------------------------------------ gather ----
+// A warp per 32 key rows of the explicit requests: the keys' latent rows as they are, their bands in fp16, zeros and no bit
+// where there is no key (behind the length, a missing page); and a warp per token and 32 heads: the rotated
+// band in fp16.
+struct Gather {
+    PagedDecode p;
+    PagedStep s;
+    PagedChunk c;
+    Divisor by_page;
+    Turns64 turns;
+};
+__device__ __forceinline__ uint32_t half_pair(uint32_t bf) {   // two bf16 as two fp16
+    const __half2 h = __floats2half2_rn(__uint_as_float(bf << 16), __uint_as_float(bf & 0xffff0000u));
+    return *(const uint32_t *)&h;
+}
+
+__global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant__ Gather a) {
+    const PagedDecode &p = a.p;
+    const int lane = threadIdx.x & 31, warps = gridDim.x * 8;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int R = __ldcg(a.c.ctl) / 32, per = (p.H + 31) / 32;
+    if (R == 0) return;
+    const long total = R + (long)a.s.n_tokens * per;
+#pragma unroll 1
+    for (long u = blockIdx.x * 8 + (threadIdx.x >> 5); u < total; u += warps) {
+        if (u < R) {
+            const int r0 = (int)u * 32, b = a.c.block_of[r0 / 128];
+            const int keys = min(max(a.s.lens[b], 0), p.max_pages * p.page), key = r0 - a.c.key0[b] + lane;
+            int row = -1;
+            if (key < keys) {
+                const int col = quotient(a.by_page, key), id = p.table[(long)b * p.max_pages + col];
+                if ((unsigned)id < (unsigned)p.num_pages) row = id * p.page + (key - col * p.page);
+            }
+            const unsigned held = __ballot_sync(0xffffffffu, row >= 0);
+            if (lane == 0) {
+                a.c.held[u] = held;
+                if (held != (keys - key >= 32 ? 0xffffffffu : keys > key ? (1u << (keys - key)) - 1 : 0u)) a.c.holes[b] = 1;
+            }
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+            for (int r = 0; r < 32; r += 8) {
+                uint4 x[8][2], y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int from = __shfl_sync(0xffffffffu, row, r + e);
+                    const uint4 *c = (const uint4 *)p.c_cache + (long)from * 64, *k = (const uint4 *)p.kpe_cache + (long)from * 8;
+                    x[e][0] = from >= 0 ? __ldcg(c + lane) : zero;
+                    x[e][1] = from >= 0 ? __ldcg(c + lane + 32) : zero;
+                    y[e] = from >= 0 && lane < 8 ? __ldcg(k + lane) : zero;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    uint4 *c = (uint4 *)a.c.chat + (long)(r0 + r + e) * 64;
+                    c[lane] = x[e][0];
+                    c[lane + 32] = x[e][1];
+                    if (lane < 8)
+                        ((uint4 *)a.c.kpe)[(long)(r0 + r + e) * 8 + lane] =
+                            make_uint4(half_pair(y[e].x), half_pair(y[e].y), half_pair(y[e].z), half_pair(y[e].w));
+                }
+            }
+        } else {
+            const long i = u - R;
+            const int t = (int)(i / per), h0 = (int)(i % per) * 32, h1 = min(h0 + 32, p.H);
+            if (!a.c.done[t]) continue;
+            const float2 cs = turn_cs(a.turns.v[lane], a.s.positions[t]);
+#pragma unroll 1
+            for (int h = h0; h < h1; h += 8) {
+                uint16_t x0[8], x1[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint16_t *x = (const uint16_t *)p.q_pe + ((long)t * p.H + min(h + j, h1 - 1)) * 64 + lane;
+                    x0[j] = x[0];
+                    x1[j] = x[32];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (h + j >= h1) break;
+                    const float f0 = __uint_as_float((uint32_t)x0[j] << 16), f1 = __uint_as_float((uint32_t)x1[j] << 16);
+                    __half *y = (__half *)a.c.qpe + ((long)t * p.H + h + j) * 64 + lane;
+                    y[0] = __float2half_rn(f0 * cs.x - f1 * cs.y);
+                    y[32] = __float2half_rn(f1 * cs.x + f0 * cs.y);
+                }
+            }
+        }
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_paged_chunk(const PagedDecode &p, const PagedStep &s, const PagedChunk &c, cudaStream_t st) {
+    cudaError_t e;
+    {
+        const Chunk a{s, c, p.max_pages * p.page, c.key_rows};
+        ProfScope ps("paged_chunk", st);
+        if ((e = launch_after(paged_chunk_kernel, 1, PNT, 0, st, a)) != cudaSuccess) return e;
+    }
+    Gather g{p, s, c, divisor(p.page), {}};
+    std::copy_n(paged_turns(p.base, p.Dr), 32, g.turns.v);
+    ProfScope ps("paged_gather", st);
+    return launch_after(paged_gather_kernel, 152 * 4, 256, 0, st, g);
+}
 
 cudaError_t launch_paged_plan(const PagedDecode &p, const PagedStep &s, int s0, int *lens, int2 *of, int *limits, int4 *groups,
                               cudaStream_t st, unsigned long long *zero, long n_zero) {

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stdint.h>
 
 namespace mla {
 
@@ -31,6 +32,27 @@ bool tc_decode_supported(int Dk, int Dn, int Dr, int Dv, int H);
 cudaError_t tc_explicit_prefill(const TcPrefill &p, const void *q_nope, const void *w_kv_b, void *out,
                                 float *lse, const void *chat, const void *kpe, const void *qpe, void *kws,
                                 void *vws, const void *w16, cudaStream_t st);
+// The explicit form of a paged step's tokens (d 512 / 128 / 64 / 128, bf16): the reconstruction and the attention
+// of one head shard after the other.
+struct alignas(16) StepTile {
+    int token, rows, key, tiles;   // first token, tokens (up to 128), first key row, key tiles of 128
+    int request, pad[3];
+};
+struct TcStep {
+    int T, H, hs, key_rows;        // tokens, heads, heads of a shard, rows of the key buffers (a multiple of 256)
+    float scale;
+    const void *q_nope, *qpe;      // [T][H][128] bf16; [T][H][64] fp16, rotated
+    const void *chat, *kpe, *w;    // [key_rows][512] bf16, [key_rows][64] fp16, W_kv_b
+    void *kws, *vws;               // [key_rows][hs 128], [hs 128][key_rows] fp16
+    void *out;                     // [T][H][128]
+    float *lse;                    // [T][H]
+    const int *ctl;                // key rows in use, number of tiles
+    const StepTile *tiles;
+    const int *limits, *done;      // [T]: keys seen; nonzero: computed here
+    const uint32_t *held;          // a bit per key row
+    const int *holes;              // [requests]
+};
+cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st);
 // Explicit prefill with the K_nope / V^T reconstruction inside the attention kernel
 // (tc_fused.cu): no K/V workspace; `cluster` (4 or 8) query tiles of a head share every
 // rebuilt key tile.  Inputs as tc_explicit_prefill (w16 holds all head_count heads).

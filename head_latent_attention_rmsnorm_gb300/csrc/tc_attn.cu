@@ -83,12 +83,30 @@ struct AttnK {
     int nh, nb, n_qt, units;       // heads of this launch, batch, query tiles, work units
 };
 
+// The units of a paged step (STEP): 128 tokens of one request, whose keys are rebuilt rows `keys` .. of K_nope and
+// V^T; each row has its own limit, pages may be missing.
+struct StepK {
+    const StepTile *tiles;    // heaviest first
+    const int *n_tiles;
+    const int *limits, *done; // [tokens]: keys seen; nonzero: this kernel's
+    const uint32_t *held;     // a bit per key row: there is such a key
+    const int *holes;         // [requests]: nonzero: some page is missing
+    long lse_i;               // log-sum-exps of a token
+};
+
 // One work unit = (128-query tile, head, batch).  Units are numbered heaviest first
 // under the causal mask: (head, batch) fastest, query tiles from the latest down.
 struct Work {
     int hl, b, q0, nt;
+    int k0, rows, request;   // STEP: first key row, query rows, request
 };
-__device__ __forceinline__ Work work_of(const AttnK &p, int u) {
+template <bool STEP>
+__device__ __forceinline__ Work work_of(const AttnK &p, const StepK &s, int u) {
+    if (STEP) {
+        const int4 *e = (const int4 *)(s.tiles + u / p.nh);
+        const int4 x = __ldcg(e), y = __ldcg(e + 1);
+        return Work{u % p.nh, 0, x.x, x.w, x.z, x.y, y.x};
+    }
     const int nhb = p.nh * p.nb;
     const int hb = u % nhb;
     Work w;
@@ -97,6 +115,7 @@ __device__ __forceinline__ Work work_of(const AttnK &p, int u) {
     w.q0 = (p.n_qt - 1 - u / nhb) * BQ;
     const int kv_end = p.causal ? min(p.kv_need, p.q_offset + w.q0 + BQ) : p.kv_need;
     w.nt = (kv_end + BKV - 1) / BKV;
+    w.k0 = 0;
     return w;
 }
 // Unit of round k for CTA c of G: rounds alternate direction over the heaviest-first
@@ -109,10 +128,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+template <bool STEP>
 __global__ void __launch_bounds__(32 * (NSM + 4), 1)
     tc_attn_kernel(const __grid_constant__ CUtensorMap mQn, const __grid_constant__ CUtensorMap mQr,
                    const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mKr,
-                   const __grid_constant__ CUtensorMap mV, AttnK p) {
+                   const __grid_constant__ CUtensorMap mV, AttnK p, StepK sp) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sQs = smem;
@@ -171,6 +191,9 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
     // The prologue overlaps the reconstruction GEMM (programmatic launch).  Every role
     // waits for it (pdl_wait) before touching K_nope, V^T, the rotated k_pe or the RoPE
     // table; the softmax warps first read their first unit's q rows, which are inputs.
+    // A step's units and limits come from the launches in front: there every warp waits.
+    if (STEP) pdl_wait();
+    const int units = STEP ? __ldcg(sp.n_tiles) * p.nh : p.units;
 
     // Every role walks the same units in the same order and counts key tiles T across
     // units, so ring slots and barrier parities continue from one unit to the next.
@@ -184,10 +207,10 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             tma_prefetch_desc(&mKr);
             bool ok = true;
             int T = 0, n = 0;
-            for (int k = 0; k * G < p.units && ok; ++k) {
+            for (int k = 0; k * G < units && ok; ++k) {
                 const int u = unit_at(k, c, G);
-                if (u >= p.units) continue;
-                const Work w = work_of(p, u);
+                if (u >= units) continue;
+                const Work w = work_of<STEP>(p, sp, u);
                 // this unit's Q into the staging buffer, once the softmax warps have moved
                 // the previous unit's Q into TMEM (this runs a couple of key tiles ahead of
                 // them, so the load has that long to land)
@@ -205,9 +228,9 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                     }
                     uint8_t *kd = sK + ks * K_BYTES;
                     mbar_arrive_expect_tx(&k_full[ks], K_BYTES);
-                    tma_load_3d(kd, &mK, &k_full[ks], w.hl * 128, j * BKV, w.b);
-                    tma_load_3d(kd + BOX, &mK, &k_full[ks], w.hl * 128 + 64, j * BKV, w.b);
-                    tma_load_3d(kd + 2 * BOX, &mKr, &k_full[ks], 0, j * BKV, w.b);
+                    tma_load_3d(kd, &mK, &k_full[ks], w.hl * 128, w.k0 + j * BKV, w.b);
+                    tma_load_3d(kd + BOX, &mK, &k_full[ks], w.hl * 128 + 64, w.k0 + j * BKV, w.b);
+                    tma_load_3d(kd + 2 * BOX, &mKr, &k_full[ks], 0, w.k0 + j * BKV, w.b);
                 }
             }
         }
@@ -218,10 +241,10 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             tma_prefetch_desc(&mV);
             bool ok = true;
             int T = 0;
-            for (int k = 0; k * G < p.units && ok; ++k) {
+            for (int k = 0; k * G < units && ok; ++k) {
                 const int u = unit_at(k, c, G);
-                if (u >= p.units) continue;
-                const Work w = work_of(p, u);
+                if (u >= units) continue;
+                const Work w = work_of<STEP>(p, sp, u);
                 for (int j = 0; j < w.nt; ++j, ++T) {
                     const int vs = T % VST;
                     if (T >= VST && !mbar_wait(&v_empty[vs], ((T / VST) - 1) & 1, abort, &g_tc_attn_err)) {
@@ -230,8 +253,8 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                     }
                     uint8_t *vd = sV + vs * V_SLOT;
                     mbar_arrive_expect_tx(&v_full[vs], V_BYTES);
-                    tma_load_3d(vd, &mV, &v_full[vs], j * BKV, w.hl * 128, w.b);
-                    tma_load_3d(vd + VBOX, &mV, &v_full[vs], j * BKV + 64, w.hl * 128, w.b);
+                    tma_load_3d(vd, &mV, &v_full[vs], w.k0 + j * BKV, w.hl * 128, w.b);
+                    tma_load_3d(vd + VBOX, &mV, &v_full[vs], w.k0 + j * BKV + 64, w.hl * 128, w.b);
                 }
             }
         }
@@ -243,10 +266,10 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             pdl_wait();
             bool ok = true;
             int T = 0, n = 0;   // key tiles, units so far
-            for (int k = 0; k * G < p.units && ok; ++k) {
+            for (int k = 0; k * G < units && ok; ++k) {
                 const int u = unit_at(k, c, G);
-                if (u >= p.units) continue;
-                const Work w = work_of(p, u);
+                if (u >= units) continue;
+                const Work w = work_of<STEP>(p, sp, u);
                 // this unit's Q is in TMEM
                 if (!__all_sync(0xffffffffu, mbar_wait(q_ready, n & 1, abort, &g_tc_attn_err))) break;
                 ++n;
@@ -285,10 +308,10 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             pdl_wait();
             bool ok = true;
             int T = 0, n = 0;
-            for (int k = 0; k * G < p.units && ok; ++k) {
+            for (int k = 0; k * G < units && ok; ++k) {
                 const int u = unit_at(k, c, G);
-                if (u >= p.units) continue;
-                const Work w = work_of(p, u);
+                if (u >= units) continue;
+                const Work w = work_of<STEP>(p, sp, u);
                 // the epilogue of the previous unit has read O before P.V_0 overwrites it
                 if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(o_free, (n - 1) & 1, abort, &g_tc_attn_err))) break;
                 ++n;
@@ -335,8 +358,8 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
         int T = 0, n = 0;
         // this CTA's units in order: round k, skipping rounds past the end
         auto next_unit = [&](int k) -> int {
-            for (; k * G < p.units; ++k)
-                if (unit_at(k, c, G) < p.units) return k;
+            for (; k * G < units; ++k)
+                if (unit_at(k, c, G) < units) return k;
             return k;
         };
         // ---- a unit's Q from the staging buffer into TMEM (the previous unit's score MMAs
@@ -382,12 +405,18 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             if (lane == 0) mbar_arrive(q_ready);
         };
         int k = next_unit(0);
-        if (k * G < p.units) load_q(0);
-        for (; k * G < p.units;) {
+        if (k * G < units) load_q(0);
+        for (; k * G < units;) {
             const int u = unit_at(k, c, G);
-            const Work w = work_of(p, u);
+            const Work w = work_of<STEP>(p, sp, u);
             const int hq = p.head_off + w.hl, b = w.b, q0 = w.q0, nt = w.nt;
             const int pos = p.q_offset + q0 + row;
+            int sees = 0, all_see = 0, holes = 0;   // STEP: keys that the row, that every row of the warp sees
+            if (STEP) {
+                sees = row < w.rows ? __ldcg(sp.limits + q0 + row) : 2147483647;
+                all_see = __reduce_min_sync(0xffffffffu, sees);
+                holes = __ldcg(sp.holes + w.request);
+            }
             float m = -INFINITY;
             for (int j = 0; j < nt; ++j, ++T) {
                 const int sb = T & 1;
@@ -411,7 +440,19 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                 // test); the masking is a pass of its own so that the maximum and the
                 // exponentials stay straight runs
                 const int j0 = j * BKV;
-                if ((j0 + BKV > p.kv_need) || (p.causal && j0 + BKV - 1 > p.q_offset + q0)) {
+                if (STEP) {
+                    if (j0 + BKV > all_see || holes) {
+                        const int lim = sees - j0;
+#pragma unroll
+                        for (int cc = 0; cc < 128; ++cc) x[cc] = cc < lim ? x[cc] : -INFINITY;
+                        if (holes) {
+                            const uint4 h = __ldcg((const uint4 *)(sp.held + (w.k0 + j0) / 32));
+                            const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+                            for (int cc = 0; cc < 128; ++cc) x[cc] = hw[cc >> 5] >> (cc & 31) & 1 ? x[cc] : -INFINITY;
+                        }
+                    }
+                } else if ((j0 + BKV > p.kv_need) || (p.causal && j0 + BKV - 1 > p.q_offset + q0)) {
                     // the row sees keys j0 .. j0 + lim - 1 of this tile
                     const int lim = min(p.kv_need, p.causal ? pos + 1 : p.kv_need) - j0;
 #pragma unroll
@@ -469,7 +510,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                 if (lane == 0) mbar_arrive(&p_full[sb]);
             }
             const int k_next = next_unit(k + 1);
-            if (k_next * G < p.units) load_q(n + 1);
+            if (k_next * G < units) load_q(n + 1);
             // ---- epilogue: the row sum is O's column 128; the row's 128 outputs in bf16
             if (nt > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(o_final, n & 1, abort, &g_tc_attn_err));
             tc_fence_after();
@@ -492,7 +533,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free);   // the next unit's P.V_0 may overwrite O
-            if (ok && qi < p.s_q) {
+            if (ok && (STEP ? row < w.rows && __ldcg(sp.done + qi) : qi < p.s_q)) {
                 // the row's 256 bytes in 32-byte stores (16-byte ones when the rows are not
                 // 32-byte aligned)
                 uint32_t *dst = (uint32_t *)(p.out + b * p.out_b + (long)qi * p.out_i + (long)hq * p.out_h);
@@ -511,7 +552,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                             ((uint4 *)(dst + 16 * q))[v] = make_uint4(wv[4 * v], wv[4 * v + 1], wv[4 * v + 2], wv[4 * v + 3]);
                     }
                 }
-                p.lse[b * p.lse_b + (long)hq * p.lse_h + qi] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                p.lse[STEP ? qi * sp.lse_i + hq : b * p.lse_b + (long)hq * p.lse_h + qi] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
             }
             ++n;
             k = k_next;
@@ -592,7 +633,7 @@ cudaError_t tc_explicit_prefill(const TcPrefill &p, const void *q_nope, const vo
         unsigned box[3] = {64, 128, 1};
         if ((e = make_tma_map(&mV, vws, 3, d, s, box)) != cudaSuccess) return e;
     }
-    e = cudaFuncSetAttribute(tc_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    e = cudaFuncSetAttribute(tc_attn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
     if (e != cudaSuccess) return e;
     int dev = 0, n_sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -638,9 +679,72 @@ cudaError_t tc_explicit_prefill(const TcPrefill &p, const void *q_nope, const vo
             attr[0].val.programmaticStreamSerializationAllowed = 1;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            e = cudaLaunchKernelEx(&cfg, tc_attn_kernel, mQn, mQr, mK, mKr, mV, a);
+            e = cudaLaunchKernelEx(&cfg, tc_attn_kernel<false>, mQn, mQr, mK, mKr, mV, a, StepK{});
         }
         if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+// A paged step's tokens in the explicit form.  The maps are the prefill's with one batch, the key rows of all requests
+// behind one another; how many there are, and the units, is known on the device only, so the grids are fixed.
+cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st) {
+    using ull = unsigned long long;
+    const ull R = p.key_rows, H = p.H, T = p.T, hs = p.hs;
+    cudaError_t e;
+    CUtensorMap mQn, mQr, mK, mKr, mV;
+    {
+        const ull d[4] = {128, H, T, 1}, s[3] = {256, H * 256, T * H * 256}, dr[4] = {64, H, T, 1}, sr[3] = {128, H * 128, T * H * 128};
+        const unsigned box[4] = {64, 1, 128, 1};
+        if ((e = make_tma_map(&mQn, p.q_nope, 4, d, s, box)) != cudaSuccess) return e;
+        if ((e = make_tma_map(&mQr, p.qpe, 4, dr, sr, box)) != cudaSuccess) return e;
+    }
+    {
+        const ull dr[3] = {64, R, 1}, sr[2] = {128, R * 128}, dk[3] = {hs * 128, R, 1}, sk[2] = {hs * 256, R * hs * 256};
+        const ull dv[3] = {R, hs * 128, 1}, sv[2] = {R * 2, R * hs * 256};
+        const unsigned box[3] = {64, 128, 1};
+        if ((e = make_tma_map(&mKr, p.kpe, 3, dr, sr, box)) != cudaSuccess) return e;
+        if ((e = make_tma_map(&mK, p.kws, 3, dk, sk, box)) != cudaSuccess) return e;
+        if ((e = make_tma_map(&mV, p.vws, 3, dv, sv, box)) != cudaSuccess) return e;
+    }
+    if ((e = cudaFuncSetAttribute(tc_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess) return e;
+    int dev = 0, n_sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&n_sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    AttnK a{};
+    a.scale_log2 = p.scale * 1.4426950408889634f;
+    a.out = (__nv_bfloat16 *)p.out;
+    a.out_i = p.H * 128L;
+    a.out_h = 128;
+    a.out_v8 = ((uintptr_t)p.out % 32) == 0;
+    a.lse = p.lse;
+    a.idesc_s = idesc_f16(128, 128, true);
+    a.idesc_pv = idesc_f16(128, 144, true);
+    a.nb = 1;
+    const StepK sp{p.tiles, p.ctl + 1, p.limits, p.done, p.held, p.holes, p.H};
+    for (int h0 = 0; h0 < p.H; h0 += p.hs) {
+        const int nh = std::min(p.hs, p.H - h0);
+        // bf16 rows and weights as they are: their products are exact in the fp32 accumulator
+        TmaOperand latent{p.chat, 512, (long)R, 1, 1024, (long)R * 1024, (int)R, 0, 1};
+        const char *w = (const char *)p.w + (long)h0 * 256 * 1024;
+        TmaOperand wk{w, 512, 128, nh, 1024, 256 * 1024, 128, 0, 0}, wv{w + 128 * 1024, 512, 128, nh, 1024, 256 * 1024, 128, 0, 0};
+        const GemmProblem kv[2] = {{latent, wk, (int)R, nh * 128, 512, 1, p.kws, (long)hs * 128, 1, 0, 0},
+                                   {wv, latent, nh * 128, (int)R, 512, 1, p.vws, (long)R, 1, 0, 0}};
+        if ((e = tc_gemm_group(kv, 2, false, st, p.ctl)) != cudaSuccess) return e;
+        a.head_off = h0;
+        a.nh = nh;
+        ProfScope ps("tc_attn", st);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(n_sms);
+        cfg.blockDim = dim3(32 * (NSM + 4));
+        cfg.dynamicSmemBytes = SMEM_BYTES;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // overlap the GEMM's tail
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if ((e = cudaLaunchKernelEx(&cfg, tc_attn_kernel<true>, mQn, mQr, mK, mKr, mV, a, sp)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

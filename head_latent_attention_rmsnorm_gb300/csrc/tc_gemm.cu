@@ -273,21 +273,29 @@ constexpr int PST = 5;   // stages of the pair kernel's ring
 constexpr uint32_t PA_BYTES = 128 * BK * 2, PB_BYTES = 128 * BK * 2;
 constexpr uint32_t PC_BYTES = 4 * 4 * 4096;   // four epilogue warps x a 32-row x 256-column 16-bit tile slice
 
-__device__ __forceinline__ Tile pair_tile_of(const GemmK &p, int t) {
+// The tiles to walk: all, or, where the rows of problem 0 and the columns of problem 1 are known on the device
+// only, those of that many.
+struct Walk {
+    int total, tiles0, tiles_n1;
+};
+__device__ __forceinline__ Tile pair_tile_of(const GemmK &p, const Walk &k, int t) {
     Tile r;
-    r.prob = t < p.pr[0].tiles ? 0 : 1;
+    r.prob = t < k.tiles0 ? 0 : 1;
     const GemmP &q = p.pr[r.prob];
-    int u = r.prob ? t - p.pr[0].tiles : t;
-    r.n0 = (u % q.tiles_n) * 256;
-    u /= q.tiles_n;
+    int u = r.prob ? t - k.tiles0 : t;
+    const int tiles_n = r.prob ? k.tiles_n1 : q.tiles_n;
+    r.n0 = (u % tiles_n) * 256;
+    u /= tiles_n;
     r.m0 = (u % q.tiles_m) * 256;
     r.batch = u / q.tiles_m;
     return r;
 }
 
+template <bool DYN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     tc_gemm_pair_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUtensorMap tb0,
-                        const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUtensorMap tb1, GemmK p) {
+                        const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUtensorMap tb1, GemmK p,
+                        const int *rows) {
     using namespace tc;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -327,6 +335,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     const uint32_t tmem = *tslot;
     pdl_launch_dependents();
     pdl_wait();
+    Walk k{p.total, p.pr[0].tiles, p.pr[1].tiles_n};
+    if (DYN) {   // (problems of one batch)
+        const int n = (__ldcg(rows) + 255) / 256;
+        k.tiles0 = n * p.pr[0].tiles_n;
+        k.tiles_n1 = n;
+        k.total = k.tiles0 + n * p.pr[1].tiles_m;
+    }
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer (both CTAs)
@@ -340,8 +355,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             const uint32_t full0 = map_peer(smem_u32(full), 0);   // the leader's barriers
             int it = 0;
             bool ok = true;
-            for (int t = pair; t < p.total && ok; t += pairs) {
-                const Tile w = pair_tile_of(p, t);
+            for (int t = pair; t < k.total && ok; t += pairs) {
+                const Tile w = pair_tile_of(p, k, t);
                 const GemmP &q = p.pr[w.prob];
                 const CUtensorMap *ma = w.prob ? &ta1 : &ta0, *mb = w.prob ? &tb1 : &tb0;
                 const int ar = w.m0 + 128 * (int)rank;
@@ -367,8 +382,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         {
             int it = 0, lt = 0;
             bool ok = true;
-            for (int t = pair; t < p.total && ok; t += pairs, ++lt) {
-                const Tile w = pair_tile_of(p, t);
+            for (int t = pair; t < k.total && ok; t += pairs, ++lt) {
+                const Tile w = pair_tile_of(p, k, t);
                 const int a = lt & 1;
                 // both CTAs' epilogues have drained what tile lt-2 left in accumulator a
                 if (lt >= 2 &&
@@ -387,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                     const uint64_t db = sdesc_kmajor(sB + s * PB_BYTES);
                     if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < BK / 16; ++k) mma_ss_pair(d, da + 2 * k, db + 2 * k, p.idesc, (kb | k) != 0);
+                        for (int e = 0; e < BK / 16; ++e) mma_ss_pair(d, da + 2 * e, db + 2 * e, p.idesc, (kb | e) != 0);
                         mma_commit_pair(&empty[s], 3);
                     }
                     __syncwarp();
@@ -402,8 +417,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         const uint32_t acc_empty0 = map_peer(smem_u32(acc_empty), 0);
         int lt = 0;
         bool ok = true;
-        for (int t = pair; t < p.total; t += pairs, ++lt) {
-            const Tile w = pair_tile_of(p, t);
+        for (int t = pair; t < k.total; t += pairs, ++lt) {
+            const Tile w = pair_tile_of(p, k, t);
             const GemmP &q = p.pr[w.prob];
             const int a = lt & 1;
             ok = __all_sync(0xffffffffu, ok && mbar_wait(&acc_full[a], (lt >> 1) & 1, abort, &g_tc_gemm_err));
@@ -537,9 +552,10 @@ int num_sms() {
     return n;
 }
 
-cudaError_t launch_gemm_pair(const CUtensorMap *maps, const GemmK &p, cudaStream_t st) {
+cudaError_t launch_gemm_pair(const CUtensorMap *maps, const GemmK &p, const int *rows, cudaStream_t st) {
     const size_t sm = PST * (PA_BYTES + PB_BYTES) + PC_BYTES + 1024 + 256;
-    cudaError_t e = cudaFuncSetAttribute(tc_gemm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    auto kern = rows ? tc_gemm_pair_kernel<true> : tc_gemm_pair_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     if (e != cudaSuccess) return e;
     const int grid = 2 * std::min(p.total, num_sms() / 2);
     cudaLaunchConfig_t cfg = {};
@@ -552,7 +568,7 @@ cudaError_t launch_gemm_pair(const CUtensorMap *maps, const GemmK &p, cudaStream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tc_gemm_pair_kernel, maps[0], maps[1], maps[2], maps[3], p);
+    return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p, rows);
 }
 
 template <int BN>
@@ -577,7 +593,7 @@ cudaError_t launch_gemm(const CUtensorMap *maps, const GemmK &p, cudaStream_t st
 
 }  // namespace
 
-cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaStream_t st) {
+cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaStream_t st, const int *rows) {
     if (n_probs < 1 || n_probs > 2) return cudaErrorInvalidValue;
     int maxN = 0;
     for (int i = 0; i < n_probs; ++i) {
@@ -596,6 +612,7 @@ cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaS
         if (probs[i].B.rows_per_z % 128 != 0) pair = false;
     }
     if (BN == 256 && !pair) BN = 128;
+    if (rows && (!pair || n_probs != 2 || probs[0].batch != 1 || probs[1].batch != 1)) return cudaErrorInvalidValue;
     const int TM = pair ? 256 : BM, TN = BN;
     CUtensorMap maps[4];
     GemmK p{};
@@ -643,7 +660,7 @@ cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaS
     switch (BN) {
         case 256:
             p.idesc = tc::idesc_f16(256, 256, f16);   // cta_group::2: M = 256 across the pair
-            return launch_gemm_pair(maps, p, st);
+            return launch_gemm_pair(maps, p, rows, st);
         case 128:
             p.idesc = tc::idesc_f16(BM, 128, f16, false, p.a_mn != 0);
             return launch_gemm<128>(maps, p, st);

@@ -48,7 +48,9 @@ cudaError_t tc_gemm(const TmaOperand &A, const TmaOperand &B, int M, int N, int 
                     bool accumulate = false);
 // One persistent launch over the tiles of one or two problems (same K, same operand
 // type): the explicit path's K_nope and V^T products share one launch.
-cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaStream_t st);
+// `rows` (device memory, null: all): so many rows of problem 0 and columns of problem 1 only; two problems of one batch on
+// SM pairs (N >= 256).
+cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaStream_t st, const int *rows = nullptr);
 
 cudaError_t tc_gemm_read_and_clear_error(unsigned *flags, cudaStream_t st);
 cudaError_t tc_attn_read_and_clear_error(unsigned *flags, cudaStream_t st);

@@ -114,9 +114,9 @@ def lib() -> ctypes.CDLL:
         L.mla_paged_decode.restype = _i
         L.mla_paged_decode_workspace.argtypes = [D, _i, _i, _i, _i]
         L.mla_paged_decode_workspace.restype = _sz
-        L.mla_paged_prefill.argtypes = [D, _i, _i, _i, _i, _i, _i] + [_vp] * 12 + [_sz, _vp]
+        L.mla_paged_prefill.argtypes = [D, _i, _i, _i, _i, _i, _i, _i, _i] + [_vp] * 12 + [_sz, _vp]
         L.mla_paged_prefill.restype = _i
-        L.mla_paged_prefill_workspace.argtypes = [D, _i, _i, _i, _i, _i]
+        L.mla_paged_prefill_workspace.argtypes = [D, _i, _i, _i, _i, _i, _i, _i]
         L.mla_paged_prefill_workspace.restype = _sz
         L.mla_paged_weights.argtypes = [D, _i, _i, _i, _i, _i, _i] + [_vp] * 13 + [_sz, _vp]
         L.mla_paged_weights.restype = _i
@@ -285,7 +285,8 @@ KERNELS = ("prep", "latent_prep", "rope_table", "rope_rows", "convert", "gemm_si
            "tc_gemm", "tc_attn", "tc_latent_attn", "tc_decode_attn", "transpose", "rmsnorm", "rmsnorm_bwd", "tpla_expand",
            "tpla_combine", "wait_probe", "tc_fused_attn", "bwd_rowdot", "attn_bwd_simt", "bwd_rows",
            "bwd_prep", "tc_bwd_dkv", "tc_bwd_dq", "paged_tables", "paged_append", "paged_absorb", "paged_attn",
-           "paged_join", "paged_plan", "paged_weights", "paged_weights_out", "paged_evict")
+           "paged_join", "paged_plan", "paged_weights", "paged_weights_out", "paged_evict",
+           "paged_chunk", "paged_gather")
 
 
 def launch_count() -> int:
@@ -824,11 +825,25 @@ def paged_decode(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens
     return out, lse
 
 
-def paged_prefill_workspace(d: Dims, n_tokens: int, c_cache, block_table) -> torch.Tensor:
-    """A workspace for :func:`paged_prefill` calls of ``n_tokens`` rows with this cache and table, one call
-    at a time."""
+PREFILL_KEY_ROWS = 65536   # key rows that paged_prefill takes for its explicit form by itself, at most
+PREFILL_HEAD_SHARD = 16
+
+
+def _prefill_room(n_tokens, block_table, page, key_rows, head_shard):
+    """The explicit form's (key_rows, head_shard): by default room for every row of the table, up to
+    PREFILL_KEY_ROWS, in shards of PREFILL_HEAD_SHARD heads."""
+    if key_rows is None:
+        rows = -(-block_table.shape[1] * page // 128) * 128 * min(block_table.shape[0], n_tokens)
+        key_rows = min(-(-rows // 256) * 256, PREFILL_KEY_ROWS)
+    return key_rows, PREFILL_HEAD_SHARD if head_shard is None else head_shard
+
+
+def paged_prefill_workspace(d: Dims, n_tokens: int, c_cache, block_table, *, key_rows=None, head_shard=None) -> torch.Tensor:
+    """A workspace for :func:`paged_prefill` calls of ``n_tokens`` rows with this cache and table (and the same
+    ``key_rows`` and ``head_shard``), one call at a time."""
+    room = _prefill_room(n_tokens, block_table, c_cache.shape[1], key_rows, head_shard)
     n = lib().mla_paged_prefill_workspace(ctypes.byref(d), _dt(c_cache), block_table.shape[0], n_tokens,
-                                          c_cache.shape[1], block_table.shape[1])
+                                          c_cache.shape[1], block_table.shape[1], *room)
     return torch.empty(max(n, 1), dtype=torch.uint8, device=c_cache.device)
 
 
@@ -853,31 +868,33 @@ def _step_args(d, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, cu_tok
 
 
 def paged_prefill(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, cu_tokens, positions, w_kv_b, *,
-                  out=None, lse=None, workspace=None, stream=None):
+                  key_rows=None, head_shard=None, out=None, lse=None, workspace=None, stream=None):
     """Latent attention of a step's new tokens over the paged cache, any number of them a request: rows
     ``cu_tokens[b]`` .. ``cu_tokens[b + 1] - 1`` of ``q_nope`` [n_tokens, n_heads, d_nope] and ``q_pe`` are request
-    b's, each at its position, as :func:`paged_tables` gives them.  Returns (out [n_tokens, n_heads, d_v],
+    b's, each at its position, as :func:`paged_tables` gives them.  ``key_rows`` and ``head_shard`` are the room for
+    the form that serves long chunks (0 rows: without it).  Returns (out [n_tokens, n_heads, d_v],
     lse [n_tokens, n_heads]); rows of no request are left as they were (zeros where this call allocates)."""
     if stream is not None:
         return _on_stream(stream, paged_prefill, d, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, cu_tokens,
-                          positions, w_kv_b, out=out, lse=lse, workspace=workspace)
+                          positions, w_kv_b, key_rows=key_rows, head_shard=head_shard, out=out, lse=lse, workspace=workspace)
     dev, dt, tdt, at, B, n, num_pages, page, max_pages, ptrs = _step_args(
         d, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, cu_tokens, positions, w_kv_b)
     if at != _current_device():
         with torch.cuda.device(at):
             return paged_prefill(d, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, cu_tokens, positions,
-                                 w_kv_b, out=out, lse=lse, workspace=workspace)
+                                 w_kv_b, key_rows=key_rows, head_shard=head_shard, out=out, lse=lse, workspace=workspace)
     H = d.n_heads
+    key_rows, head_shard = _prefill_room(n, block_table, page, key_rows, head_shard)
     if out is None:
         out = torch.zeros(n, H, d.d_v, dtype=tdt, device=dev)
     if lse is None:
         lse = torch.zeros(n, H, dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = paged_prefill_workspace(d, n, c_cache, block_table)
+        workspace = paged_prefill_workspace(d, n, c_cache, block_table, key_rows=key_rows, head_shard=head_shard)
     else:
         _workspace(0, dev, workspace)
     st = lib().mla_paged_prefill(
-        d, dt, B, n, num_pages, page, max_pages, *ptrs, _need("out", out, (n, H, d.d_v), tdt, at),
+        d, dt, B, n, num_pages, page, max_pages, key_rows, head_shard, *ptrs, _need("out", out, (n, H, d.d_v), tdt, at),
         _need("lse", lse, (n, H), torch.float32, at), _ptr(workspace), workspace.numel() * workspace.element_size(),
         _raw_stream(at))
     if st != 0:

@@ -340,6 +340,13 @@ size_t mla_paged_decode_workspace(const mla_dims *dims, mla_dtype dtype, int B, 
  *   q_nope [n_tokens, H, d_nope]   q_pe [n_tokens, H, d_rope] (not rotated)   block_table [B, max_pages]
  *   kv_lens [B]   cu_tokens [B + 1]   positions [n_tokens]   w_kv_b as above
  *   out [n_tokens, H, d_v]   lse (fp32) [n_tokens, H]
+ * The tensor-core kernels take one of two forms for a request.  Absorbed, as decode: needs nothing but the call's
+ * own rounds, and is the cheaper one up to about 170 tokens a request.  Explicit, as mla_latent_attn_fwd: K_nope and V
+ * are rebuilt from the request's pages, head_shard heads at a time (0: all), into the workspace; it takes the requests of
+ * many new tokens whose keys, rounded up to 128 each, fit in key_rows rows (in the order of the requests; 0:
+ * none do), except for tokens that see few keys.  Both are exact to rounding, so key_rows (rounded down to a multiple
+ * of 256) and head_shard are a matter of memory, 1280 + 512 head_shard bytes a row, and of time.  The choice is
+ * made on the device from the lengths there.
  * A token that sees no key (a negative position, no pages) gives out 0 and lse -inf.  Rows of no request (in front of
  * cu_tokens[0], from cu_tokens[B] on) are left as they were.  Lengths, slots behind them and bad page ids are
  * treated as in mla_paged_decode, as are types, dimensions, precision (a token has the kernel of its request's
@@ -347,11 +354,12 @@ size_t mla_paged_decode_workspace(const mla_dims *dims, mla_dtype dtype, int B, 
  * other tokens of the step.
  */
 mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int num_pages, int page_size,
-                             int max_pages, const void *q_nope, const void *q_pe, const void *c_cache,
-                             const void *kpe_cache, const int *block_table, const int *kv_lens, const int *cu_tokens,
-                             const int *positions, const void *w_kv_b, void *out, float *lse, void *workspace,
-                             size_t workspace_bytes, void *cuda_stream);
-size_t mla_paged_prefill_workspace(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int page_size, int max_pages);
+                             int max_pages, int key_rows, int head_shard, const void *q_nope, const void *q_pe,
+                             const void *c_cache, const void *kpe_cache, const int *block_table, const int *kv_lens,
+                             const int *cu_tokens, const int *positions, const void *w_kv_b, void *out, float *lse,
+                             void *workspace, size_t workspace_bytes, void *cuda_stream);
+size_t mla_paged_prefill_workspace(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int page_size, int max_pages,
+                                   int key_rows, int head_shard);
 
 /*
  * The attention weight that a step's tokens gave each page of their requests:
@@ -494,7 +502,7 @@ mla_status mla_decode_splitkv_noalloc(const mla_dims *dims, mla_dtype dtype, int
  *   "tpla_combine", "wait_probe", "tc_fused_attn", "bwd_rowdot",
  *   "attn_bwd_simt", "bwd_rows", "bwd_prep", "tc_bwd_dkv", "tc_bwd_dq",
  *   "paged_tables", "paged_append", "paged_absorb", "paged_attn", "paged_join", "paged_plan",
- *   "paged_weights", "paged_weights_out", "paged_evict".
+ *   "paged_weights", "paged_weights_out", "paged_evict", "paged_chunk", "paged_gather".
  * mla_profile_reset: forgets recorded events, keeps recording on/off as it was.
  * Launches from several host threads are recorded safely; call enable, reset and the
  * queries between computations, not while another thread's calls are in flight.

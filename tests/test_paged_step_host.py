@@ -59,8 +59,8 @@ def test_reference_eviction_by_hand():
 # ------------------------------------------------------------------------ C ABI ----
 def prefill_args(**over):
     d = mla.dims(**{**V3, **over.pop("dims_over", {})})
-    a = dict(dims=ctypes.byref(d), dtype=mla.MLA_BF16, B=4, n=9, pages=1000, page=64, max_pages=100, q=fake(1), r=fake(2),
-             c=fake(3), k=fake(4), table=fake(5), lens=fake(6), cu=fake(11), pos=fake(12), w=fake(7), out=fake(8), lse=fake(9),
+    a = dict(dims=ctypes.byref(d), dtype=mla.MLA_BF16, B=4, n=9, pages=1000, page=64, max_pages=100, rows=4096, shard=16,
+             q=fake(1), r=fake(2), c=fake(3), k=fake(4), table=fake(5), lens=fake(6), cu=fake(11), pos=fake(12), w=fake(7), out=fake(8), lse=fake(9),
              ws=fake(10), ws_bytes=1 << 31, stream=None)
     a.update(over)
     return list(a.values()), d
@@ -81,6 +81,7 @@ COMMON = [
 @pytest.mark.parametrize("over,status", COMMON + [
     (dict(out=None), -1), (dict(out=fake(8) + 8), -4), (dict(lse=fake(9) + 4), -4), (dict(out=fake(1)), -9),
     (dict(lse=fake(11)), -9), (dict(lse=fake(8) + 256), -9), (dict(n=0, q=None), 0),
+    (dict(rows=-1), -2), (dict(shard=-1), -2),
 ])
 def test_prefill_rejects(over, status):
     args, _d = prefill_args(**dict(over))
@@ -127,15 +128,20 @@ def test_evict_rejects(over, status):
 
 def test_workspace_queries():
     d = mla.dims(**V3)
-    for query, call, args in ((mla.mla_paged_prefill_workspace, mla.mla_paged_prefill, prefill_args),
-                              (mla.mla_paged_weights_workspace, mla.mla_paged_weights, weights_args)):
-        f = lambda *a: query(ctypes.byref(d), *a)   # noqa: E731
+    for query, call, args, room in ((mla.mla_paged_prefill_workspace, mla.mla_paged_prefill, prefill_args, (4096, 16)),
+                                    (mla.mla_paged_weights_workspace, mla.mla_paged_weights, weights_args, ())):
+        f = lambda *a: query(ctypes.byref(d), *a, *room)   # noqa: E731
         few, many = f(mla.MLA_BF16, 4, 9, 64, 100), f(mla.MLA_BF16, 4, 900, 64, 100)
         assert 0 < few < many
         assert f(mla.MLA_BF16, 0, 9, 64, 100) == 0 and f(9, 4, 9, 64, 100) == 0 and f(mla.MLA_BF16, 4, 9, 0, 100) == 0
         assert f(mla.MLA_BF16, 4, -1, 64, 100) == 0
         a, _ = args(n=900, ws_bytes=many - 1)
         assert call(*a) == -5
+    f = lambda *a: mla.mla_paged_prefill_workspace(ctypes.byref(d), mla.MLA_BF16, 4, *a)   # noqa: E731
+    none = f(900, 64, 100, 0, 16)
+    assert none == f(900, 64, 100, 255, 16) < f(900, 64, 100, 4096, 16) < f(900, 64, 100, 4096, 0) == f(900, 64, 100, 4097, 999)
+    assert f(900, 64, 100, -1, 16) == 0 == f(900, 64, 100, 4096, -1)
+    assert f(900, 60, 100, 4096, 16) == f(900, 60, 100, 0, 16)   # pages that the tensor cores do not take
     assert mla.mla_paged_evict_workspace(0) == 0 < mla.mla_paged_evict_workspace(3) < mla.mla_paged_evict_workspace(9000)
 
 
