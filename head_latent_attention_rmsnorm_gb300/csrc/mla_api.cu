@@ -1224,18 +1224,19 @@ void paged_explicit_carve(const PagedDecode &p, int B, int n_tokens, int key_row
     const size_t R = key_rows, T = n_tokens;
     x->c.key_rows = key_rows;
     x->c.max_tiles = chunk_tiles(n_tokens);
-    x->c.ctl = (int *)c.take(2 * sizeof(int));
+    x->c.ctl = (int *)c.take(3 * sizeof(int));
     x->c.key0 = (int *)c.take(B * sizeof(int));
     x->c.holes = (int *)c.take(B * sizeof(int));
     x->c.block_of = (int *)c.take(R / 128 * sizeof(int));
     x->c.limits = (int *)c.take(T * sizeof(int));
     x->c.done = (int *)c.take(T * sizeof(int));
+    x->c.list = (int *)c.take(T * sizeof(int));
     x->c.raw = (StepTile *)c.take((size_t)x->c.max_tiles * sizeof(StepTile));
     x->c.tiles = (StepTile *)c.take((size_t)x->c.max_tiles * sizeof(StepTile));
     x->c.held = (uint32_t *)c.take(R / 32 * sizeof(uint32_t));
     x->c.chat = c.take(R * p.Dk * 2);
     x->c.kpe = c.take(R * p.Dr * 2);
-    x->c.qpe = c.take(T * p.H * p.Dr * 2);
+    x->c.qpe = c.take(T * p.H * p.Dr * 4);
     x->c.kws = c.take(R * x->hs * p.Dn * 2);
     x->c.vws = c.take(R * x->hs * p.Dv * 2);
 }
@@ -1385,12 +1386,17 @@ mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n
     }
     for (int s0 = 0; s0 < n_tokens; s0 += PAGED_ROUND) {
         PagedDecode q = p;
-        const size_t at = (size_t)s0 * p.H;
+        // (the list's tokens are the step's; without one the round's)
+        const size_t at = x.hs ? 0 : (size_t)s0 * p.H;
         q.T = q.B = std::min(n_tokens - s0, PAGED_ROUND);
         q.q_nope = (const char *)q_nope + at * p.Dn * es;
         q.q_pe = (const char *)q_pe + at * p.Dr * es;
-        q.pos = positions + s0;
-        q.done = x.hs ? x.c.done + s0 : nullptr;
+        q.pos = positions + (x.hs ? 0 : s0);
+        if (x.hs) {
+            q.list = x.c.list + s0;
+            q.n_list = x.c.ctl + 2;
+            q.list_at = s0;
+        }
         q.out = (char *)out + at * p.Dv * es;
         q.lse = lse + at;
         cudaStream_t cs = (cudaStream_t)cuda_stream;

@@ -48,12 +48,16 @@ struct PagedDecode {
     const int *table, *lens;         // lens [B]: the groups' keys
     // The tokens of a step (null for decode): each one's position, group (-1: not computed here, its output
     // stays) and first row in the group, and the keys that it sees; each group's row of the table, first query
-    // row and number of rows.  done: tokens that are nonzero there have no group (null: none).
+    // row and number of rows.
     const int *pos;
     const int2 *of;
     const int *limits;
     const int4 *groups;
-    const int *done;
+    // list: the step's tokens that are computed here, T of them from there on at most, *n_list - list_at in fact; then a
+    // token in all of the above is its place in the list, but for pos, q_nope, q_pe, out and lse, which are the step's
+    // (null: the tokens themselves, T of them).
+    const int *list, *n_list;
+    int list_at;
     bool scores_only;                // the absorb leaves the third parts of the queries out
     void *out;
     float *lse;
@@ -93,10 +97,10 @@ constexpr int CHUNK_MIN = 160, CHUNK_FEW = 512, CHUNK_SORT = 2048;
 struct PagedChunk {
     int key_rows;                // rows of the key buffers, a multiple of 256
     int max_tiles;
-    int *ctl;                    // [2]: rows in use, tiles
+    int *ctl;                    // [3]: rows in use, tiles, tokens of the list
     int *key0, *holes;           // [B]: a request's first key row (-1: absorbed); nonzero: some page is missing
     int *block_of;               // [key_rows / 128]: the request of each 128 rows
-    int *limits, *done;          // [n_tokens]: keys seen; nonzero: explicit
+    int *limits, *done, *list;   // [n_tokens]: keys seen; nonzero: explicit; the requests' other tokens
     StepTile *raw, *tiles;
     uint32_t *held;              // a bit per key row
     void *chat, *kpe, *qpe, *kws, *vws;

@@ -82,6 +82,12 @@ __device__ __forceinline__ int keys_of(const PagedDecode &p, int b) {
     return min(max(p.lens[b], 0), cap);
 }
 
+// The tokens of the call, and token i's row in the step.
+__device__ __forceinline__ int tokens_of(const PagedDecode &p) {
+    return p.list ? min(max(__ldcg(p.n_list) - p.list_at, 0), p.T) : p.T;
+}
+__device__ __forceinline__ int token_of(const PagedDecode &p, int i) { return p.list ? __ldcg(p.list + i) : i; }
+
 // The group whose tiles (for all its row tiles) hold tile t < T; `off`: the prefix sums.
 template <typename I>
 __device__ __forceinline__ int request_of(const PagedDecode &p, const I *off, long t) {

@@ -38,11 +38,16 @@ __global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__
     __shared__ int warp_tot[PNT / 32];
     const PagedDecode &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
-    int *lim = sm, *req = lim + PAGED_ROUND, *sums = req + PAGED_ROUND, *near = sums + PAGED_ROUND + 1;
+    int *lim = sm, *req = lim + PAGED_ROUND, *sums = req + PAGED_ROUND, *tok = sums + PAGED_ROUND + 1, *near = tok + PAGED_ROUND;
     pdl_wait();
     pdl_launch_dependents();   // the absorb beside this; what follows it waits for both
     if (blockIdx.x > 0) {
         for (long i = (long)(blockIdx.x - 1) * PNT + tid; i < a.n_zero; i += (long)(gridDim.x - 1) * PNT) a.zero[i] = 0;
+        return;
+    }
+    const int T = tokens_of(p);
+    if (p.list && T == 0) {   // (the join has no token to look anything up for)
+        for (int i = tid; i < 2 * p.workers; i += PNT) p.first[i] = 0;
         return;
     }
     const bool here = a.s.B < CU_NEAR;
@@ -52,16 +57,17 @@ __global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__
     }
     const int *cu = here ? near : a.s.cu;
     const int cap = p.max_pages * p.page;
-    for (int i = tid; i < p.T; i += PNT) {
-        const int t = a.s0 + i;
+    for (int i = tid; i < T; i += PNT) {
+        const int t = p.list ? __ldcg(p.list + i) : a.s0 + i;
         int lo = 0, hi = a.s.B;   // the first request whose tokens end behind t
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (cu[mid + 1] > t) hi = mid;
             else lo = mid + 1;
         }
-        const bool in = lo < a.s.B && cu[lo] <= t && !(p.done && p.done[i]);
+        const bool in = lo < a.s.B && cu[lo] <= t;
         req[i] = in ? lo : -1;
+        tok[i] = t;
         int n = 0;
         if (in) {
             const int pos = a.s.positions[t], keys = min(max(a.s.lens[lo], 0), cap);
@@ -72,13 +78,20 @@ __global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__
     __syncthreads();
     // which tokens begin a group
     const int i0 = 2 * tid;
-    int first[2];
+    int first[2], place[2];   // place: among the request's tokens of this round
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int i = i0 + e;
-        first[e] = 0;
-        if (i < p.T && req[i] >= 0)
-            first[e] = i == 0 || req[i - 1] != req[i] || (a.s0 + i - max(cu[req[i]], a.s0)) % a.most == 0;
+        first[e] = place[e] = 0;
+        if (i >= T || req[i] < 0) continue;
+        int lo = 0, hi = i;   // the request's first token here
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (tok[mid] >= cu[req[i]]) hi = mid;
+            else lo = mid + 1;
+        }
+        place[e] = i - lo;
+        first[e] = i == 0 || req[i - 1] != req[i] || place[e] % a.most == 0;
     }
     int x = first[0] + first[1];
     const int own = x;
@@ -98,13 +111,13 @@ __global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int i = i0 + e;
-        if (i >= p.T) continue;
+        if (i >= T) continue;
         if (req[i] < 0) a.of[i] = make_int2(-1, 0);
         if (!first[e]) continue;
         // the group's tokens: up to the next beginning
-        const int b = req[i], in_request = a.s0 + i - max(cu[b], a.s0);
+        const int b = req[i];
         int n = 0, most = 0;
-        for (int k = i; k < p.T && req[k] == b && (k == i || (in_request + k - i) % a.most); ++k, ++n) {
+        for (int k = i; k < T && req[k] == b && (k == i || (place[e] + k - i) % a.most); ++k, ++n) {
             a.of[k] = make_int2(g, n * p.H);
             most = max(most, lim[k]);
         }
@@ -240,16 +253,33 @@ __global__ void __launch_bounds__(PNT) paged_chunk_kernel(const __grid_constant_
         }
         a.c.tiles[at] = x;
     }
+    // the requests' other tokens, eight neighbours a thread
+    long listed = 0;
+    const int first = min(max(a.s.cu[0], 0), N), last = min(max(a.s.cu[a.s.B], 0), N);
+    for (int base = first; base < last; base += 8 * PNT) {
+        const int t0 = base + 8 * tid;
+        int mine = 0;   // (mask)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (t0 + i < last && !a.c.done[t0 + i]) mine |= 1 << i;
+        long all;
+        int *at = a.c.list + listed + block_before(__popc(mine), warp_tot, all);
+        listed += all;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (mine >> i & 1) *at++ = t0 + i;
+    }
     if (tid == 0) {
         a.c.ctl[0] = (int)used;
         a.c.ctl[1] = (int)out;
+        a.c.ctl[2] = (int)listed;
     }
 }
 
 // ------------------------------------------------------------------------ gather ----
 // A warp per 32 key rows of the explicit requests: the keys' latent rows as they are, their bands in fp16, zeros and no bit
 // where there is no key (behind the length, a missing page); and a warp per token and 32 heads: the rotated
-// band in fp16.
+// band in fp16, as a rounding and its rest.
 struct Gather {
     PagedDecode p;
     PagedStep s;
@@ -325,9 +355,13 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant
                 for (int j = 0; j < 8; ++j) {
                     if (h + j >= h1) break;
                     const float f0 = __uint_as_float((uint32_t)x0[j] << 16), f1 = __uint_as_float((uint32_t)x1[j] << 16);
-                    __half *y = (__half *)a.c.qpe + ((long)t * p.H + h + j) * 64 + lane;
-                    y[0] = __float2half_rn(f0 * cs.x - f1 * cs.y);
-                    y[32] = __float2half_rn(f1 * cs.x + f0 * cs.y);
+                    __half *y = (__half *)a.c.qpe + ((long)t * p.H + h + j) * 128 + lane;
+                    const float r0 = f0 * cs.x - f1 * cs.y, r1 = f1 * cs.x + f0 * cs.y;
+                    const __half h0r = __float2half_rn(r0), h1r = __float2half_rn(r1);
+                    y[0] = h0r;
+                    y[32] = h1r;
+                    y[64] = __float2half_rn(r0 - __half2float(h0r));
+                    y[96] = __float2half_rn(r1 - __half2float(h1r));
                 }
             }
         }
@@ -352,7 +386,11 @@ cudaError_t launch_paged_chunk(const PagedDecode &p, const PagedStep &s, const P
 cudaError_t launch_paged_plan(const PagedDecode &p, const PagedStep &s, int s0, int *lens, int2 *of, int *limits, int4 *groups,
                               cudaStream_t st, unsigned long long *zero, long n_zero) {
     Plan a{p, s, s0, std::max(1, p.row_tile / p.H), lens, limits, of, groups, zero, n_zero};
-    const size_t sm = (3 * PAGED_ROUND + 1 + (s.B < CU_NEAR ? s.B + 1 : 0)) * sizeof(int);
+    const size_t sm = (4 * PAGED_ROUND + 1 + (s.B < CU_NEAR ? s.B + 1 : 0)) * sizeof(int);
+    if (sm > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+        if (e != cudaSuccess) return e;
+    }
     ProfScope ps("paged_plan", st);
     return launch_after(paged_plan_kernel, 1 + (unsigned)std::min((n_zero + PNT - 1) / PNT, 150l), PNT, sm, st, a);
 }

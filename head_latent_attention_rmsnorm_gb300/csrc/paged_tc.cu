@@ -147,6 +147,7 @@ struct Absorb {
     PagedDecode p;
     bf16 *qhi, *qlo, *qrest, *rhi, *rlo, *rrest;   // [B][H][512], [B][H][64]; the rests of short requests only
     int groups, group;             // groups of `group` requests
+    int blocks;                    // blocks that share them out, of each head and 128 dims: the groups, but for a list
     int rot_blocks;                // blocks 1 .. rot_blocks rotate the queries; block 0 divides the batch
     Turns64 turns;
 };
@@ -155,17 +156,18 @@ struct Absorb {
 __device__ void rotate_queries(const Absorb &a, int i, int lane) {
     const PagedDecode &p = a.p;
     const int per = (p.H + 31) / 32, b = i / per, h0 = i % per * 32;
-    if (b >= p.T || (p.done && p.done[b])) return;
+    if (b >= tokens_of(p)) return;
+    const int t = token_of(p, b);
     // (a step's tokens may see few keys whatever their position)
     const int keys = p.scores_only ? 2147483647 : p.pos ? 0 : keys_of(p, b);
-    const float2 cs = turn_cs(a.turns.v[lane], p.pos ? p.pos[b] : keys - 1);
+    const float2 cs = turn_cs(a.turns.v[lane], p.pos ? p.pos[t] : keys - 1);
     const int h1 = min(h0 + 32, p.H);
 #pragma unroll 1
     for (int h = h0; h < h1; h += 8) {
         uint16_t x0[8], x1[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint16_t *x = (const uint16_t *)p.q_pe + ((long)b * p.H + min(h + j, h1 - 1)) * DR + lane;
+            const uint16_t *x = (const uint16_t *)p.q_pe + ((long)t * p.H + min(h + j, h1 - 1)) * DR + lane;
             x0[j] = x[0];
             x1[j] = x[32];
         }
@@ -207,24 +209,29 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
         if (step) pdl_wait();
         return;
     }
-    uint8_t *sw = sm, *sq = sm + DN * AB_PITCH;
+    uint8_t *sq = sm + DN * AB_PITCH;
+    const int T = tokens_of(p);
     int u = (int)blockIdx.x - 1 - a.rot_blocks;
     const int dc = u & 3;
     u >>= 2;
-    const int grp = u % a.groups, h = u / a.groups;
-    const int b0 = grp * a.group, nb = min(a.group, p.T - b0);
-    if (p.done && __syncthreads_and(tid >= nb || p.done[b0 + tid])) {
+    const int h = u / a.blocks;
+    int b0 = u % a.blocks * a.group;
+    if (b0 >= T) {
         pdl_wait();
         return;
     }
     const bf16 *w = (const bf16 *)p.w + (long)h * (DN + DV) * DK + dc * AB_DIMS;
-    for (int i = tid; i < nb * 16; i += 128)
-        cp16(sq + (i >> 4) * AB_PITCH + (i & 15) * 16, (const bf16 *)p.q_nope + ((long)(b0 + (i >> 4)) * p.H + h) * DN + (i & 15) * 8);
+    int *keys = (int *)(sm + AB_SMEM) - AB_GROUP;
+    auto load = [&](int nb) {
+        for (int i = tid; i < nb * 16; i += 128)
+            cp16(sq + (i >> 4) * AB_PITCH + (i & 15) * 16,
+                 (const bf16 *)p.q_nope + ((long)token_of(p, b0 + (i >> 4)) * p.H + h) * DN + (i & 15) * 8);
+        if (tid < nb) keys[tid] = p.scores_only ? 2147483647 : step ? 0 : keys_of(p, b0 + tid);
+    };
+    load(min(a.group, T - b0));
 #pragma unroll 4
     for (int i = tid; i < DN * (AB_DIMS / 8); i += 128)
-        cp16(sw + (i >> 4) * AB_PITCH + (i & 15) * 16, w + (long)(i >> 4) * DK + (i & 15) * 8);
-    int *keys = (int *)(sm + AB_SMEM) - AB_GROUP;
-    if (tid < nb) keys[tid] = p.scores_only ? 2147483647 : step ? 0 : keys_of(p, b0 + tid);
+        cp16(sm + (i >> 4) * AB_PITCH + (i & 15) * 16, w + (long)(i >> 4) * DK + (i & 15) * 8);
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     uint32_t A[2][8][4];
@@ -233,47 +240,57 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
     for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int s = 0; s < 8; ++s)   // matrices: (dims 0-7, k 0-7), (dims 8-15, k 0-7), the same of k 8-15
-            ldsm4_t(A[m][s], smem_u32(sw + (16 * s + (mi >> 1) * 8 + r) * AB_PITCH + (warp * 32 + m * 16 + (mi & 1) * 8) * 2));
+            ldsm4_t(A[m][s], smem_u32(sm + (16 * s + (mi >> 1) * 8 + r) * AB_PITCH + (warp * 32 + m * 16 + (mi & 1) * 8) * 2));
     __syncthreads();   // all have their weights: the room is the staging's
     const int g = lane >> 2, t = lane & 3;
-    uint16_t *sh = (uint16_t *)sw + warp * 3 * 8 * AB_OUT, *sl = sh + 8 * AB_OUT,
+    uint16_t *sh = (uint16_t *)sm + warp * 3 * 8 * AB_OUT, *sl = sh + 8 * AB_OUT,
              *sr = sl + 8 * AB_OUT;
 #pragma unroll 1
-    for (int b = 0; b < nb; b += 8) {   // (rows behind the group's last request are not read back)
-        float d[2][4] = {};
+    for (;;) {
+        const int nb = min(a.group, T - b0);
+#pragma unroll 1
+        for (int b = 0; b < nb; b += 8) {   // (rows behind the group's last request are not read back)
+            float d[2][4] = {};
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {   // 32 of the summed dims
-            uint32_t q[4];
-            ldsm4(q, smem_u32(sq + (b + r) * AB_PITCH + (32 * s + mi * 8) * 2));
+            for (int s = 0; s < 4; ++s) {   // 32 of the summed dims
+                uint32_t q[4];
+                ldsm4(q, smem_u32(sq + (b + r) * AB_PITCH + (32 * s + mi * 8) * 2));
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                mma_16816(d[m], A[m][2 * s], q[0], q[1]);
-                mma_16816(d[m], A[m][2 * s + 1], q[2], q[3]);
+                for (int m = 0; m < 2; ++m) {
+                    mma_16816(d[m], A[m][2 * s], q[0], q[1]);
+                    mma_16816(d[m], A[m][2 * s + 1], q[2], q[3]);
+                }
             }
-        }
-        // d[m][..]: dim 16 m + g (+ 8), requests 2t, 2t + 1
+            // d[m][..]: dim 16 m + g (+ 8), requests 2t, 2t + 1
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                uint32_t hi, lo, rest;
-                split3(d[m][2 * e], d[m][2 * e + 1], hi, lo, rest);
-                const int dim = 16 * m + 8 * e + g;
-                sh[(2 * t) * AB_OUT + dim] = (uint16_t)hi;
-                sh[(2 * t + 1) * AB_OUT + dim] = (uint16_t)(hi >> 16);
-                sl[(2 * t) * AB_OUT + dim] = (uint16_t)lo;
-                sl[(2 * t + 1) * AB_OUT + dim] = (uint16_t)(lo >> 16);
-                sr[(2 * t) * AB_OUT + dim] = (uint16_t)rest;
-                sr[(2 * t + 1) * AB_OUT + dim] = (uint16_t)(rest >> 16);
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t hi, lo, rest;
+                    split3(d[m][2 * e], d[m][2 * e + 1], hi, lo, rest);
+                    const int dim = 16 * m + 8 * e + g;
+                    sh[(2 * t) * AB_OUT + dim] = (uint16_t)hi;
+                    sh[(2 * t + 1) * AB_OUT + dim] = (uint16_t)(hi >> 16);
+                    sl[(2 * t) * AB_OUT + dim] = (uint16_t)lo;
+                    sl[(2 * t + 1) * AB_OUT + dim] = (uint16_t)(lo >> 16);
+                    sr[(2 * t) * AB_OUT + dim] = (uint16_t)rest;
+                    sr[(2 * t + 1) * AB_OUT + dim] = (uint16_t)(rest >> 16);
+                }
+            __syncwarp();
+            if (b + g < nb) {   // 8 requests x 64 bytes: a 16-byte piece per lane
+                const long o = ((long)(b0 + b + g) * p.H + h) * DK + dc * AB_DIMS + warp * 32 + t * 8;
+                *(uint4 *)(a.qhi + o) = *(const uint4 *)(sh + g * AB_OUT + t * 8);
+                *(uint4 *)(a.qlo + o) = *(const uint4 *)(sl + g * AB_OUT + t * 8);
+                if (keys[b + g] <= SHORT_KEYS) *(uint4 *)(a.qrest + o) = *(const uint4 *)(sr + g * AB_OUT + t * 8);
             }
-        __syncwarp();
-        if (b + g < nb) {   // 8 requests x 64 bytes: a 16-byte piece per lane
-            const long o = ((long)(b0 + b + g) * p.H + h) * DK + dc * AB_DIMS + warp * 32 + t * 8;
-            *(uint4 *)(a.qhi + o) = *(const uint4 *)(sh + g * AB_OUT + t * 8);
-            *(uint4 *)(a.qlo + o) = *(const uint4 *)(sl + g * AB_OUT + t * 8);
-            if (keys[b + g] <= SHORT_KEYS) *(uint4 *)(a.qrest + o) = *(const uint4 *)(sr + g * AB_OUT + t * 8);
+            __syncwarp();
         }
-        __syncwarp();
+        b0 += a.blocks * a.group;
+        if (b0 >= T) break;
+        __syncthreads();   // the group has been read
+        load(min(a.group, T - b0));
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
     }
     if (step) pdl_wait();
 }
@@ -296,6 +313,7 @@ constexpr int JV = JW + 2 * JB * JMAXC * 4;    // the parts' weights for either 
 struct JoinVars {
     uint64_t bar_w, bar_d;
     int sc[JB][4];            // first part, number of parts (-1: a token that is not computed here), Extra, row in the item
+    int tok[JB];              // the tokens' rows in the step
     float sl[JB], sd[2][JB];  // log-sum-exp without the q_lo term; the warps' shares of q_lo . o
     uint32_t tslot;
     int abort;
@@ -342,9 +360,10 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
     const uint32_t tmem = v0.tslot;
     pdl_wait();
     uint32_t ph = 0;
+    const int T = tokens_of(p);
 #pragma unroll 1
-    for (int b0 = (int)(blockIdx.x % per_head) * JB; b0 < p.T; b0 += per_head * JB) {
-        const int nb = min(JB, p.T - b0);
+    for (int b0 = (int)(blockIdx.x % per_head) * JB; b0 < T; b0 += per_head * JB) {
+        const int nb = min(JB, T - b0);
         if (p.of && __syncthreads_and(tid >= nb || __ldcg(&p.of[b0 + tid].x) < 0)) continue;
         const int d8 = tid & 63, q16 = tid >> 6;
         const bool few = nb <= 2;                                // the groups share out parts, not requests
@@ -402,6 +421,7 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
                 sc[warp][1] = here ? n : -1;
                 sc[warp][2] = ex;
                 sc[warp][3] = r;
+                v0.tok[warp] = warp < nb ? token_of(p, b0 + warp) : 0;
                 sl[warp] = s == 0.f ? -INFINITY : m + logf(s);
             }
         }
@@ -492,7 +512,7 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
         tc_fence_before();
         __syncthreads();
         // (no keys: -inf stays, whatever the queries of a padded request hold; 0 * NaN is not added)
-        if (tid < nb && sc[tid][1] >= 0) p.lse[(long)(b0 + tid) * p.H + h] = sl[tid] == -INFINITY ? sl[tid] : sl[tid] + p.scale * (sd[0][tid] + sd[1][tid]);
+        if (tid < nb && sc[tid][1] >= 0) p.lse[(long)v0.tok[tid] * p.H + h] = sl[tid] == -INFINITY ? sl[tid] : sl[tid] + p.scale * (sd[0][tid] + sd[1][tid]);
         if (warp == 0) {
             ok = __all_sync(FULL, ok && mbar_wait(&v0.bar_w, 0, (volatile int *)&v0.abort, &g_paged_tc_err));   // W_V is here
             tc_fence_after();
@@ -524,7 +544,7 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
         __syncthreads();
         if (warp < nb && sc[warp][1] >= 0) {   // (an abandoned wait leaves rubbish here, and the error word)
             const float4 v = *(const float4 *)(ss + warp * 132 + lane * 4);
-            *(uint2 *)((bf16 *)p.out + ((long)(b0 + warp) * p.H + h) * DV + lane * 4) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+            *(uint2 *)((bf16 *)p.out + ((long)v0.tok[warp] * p.H + h) * DV + lane * 4) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
         }
         __syncthreads();
         ph ^= 1;
@@ -1392,6 +1412,8 @@ Absorb absorb_of(const PagedDecode &p) {
     ab.groups = std::max((p.T + AB_GROUP - 1) / AB_GROUP, std::min(want, most));
     ab.group = ((p.T + ab.groups - 1) / ab.groups + 7) / 8 * 8;
     ab.groups = (p.T + ab.group - 1) / ab.group;
+    // (of a list's tokens there may be few: blocks that find none are 25 us of launches at 2048 tokens, 128 heads)
+    ab.blocks = p.list ? std::min(ab.groups, std::max(1, 2048 / (4 * p.H))) : ab.groups;
     ab.rot_blocks = (int)(((long)p.T * ((p.H + 31) / 32) + 3) / 4);
     std::copy_n(paged_turns(p.base, DR), DR / 2, ab.turns.v);
     return ab;
@@ -1403,7 +1425,7 @@ cudaError_t paged_absorb_tc(const PagedDecode &p, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(paged_absorb_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM);
     if (e != cudaSuccess) return e;
     ProfScope ps("paged_absorb", st);
-    return launch_after(paged_absorb_tc_kernel, (unsigned)(p.H * 4 * ab.groups + 1 + ab.rot_blocks), 128, AB_SMEM, st, ab);
+    return launch_after(paged_absorb_tc_kernel, (unsigned)(p.H * 4 * ab.blocks + 1 + ab.rot_blocks), 128, AB_SMEM, st, ab);
 }
 
 cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {

@@ -14,9 +14,16 @@
 // shares of all items' tiles of 256 keys, cta_group::2 MMAs: S = K Q^T with the keys as the 256 rows
 // (128 in each SM), and Q's bf16 high halves as the columns that CTA 0 holds, its low halves those of CTA 1:
 // N = 2 x rows.  So a key is loaded by one SM only, the scores are exact to the queries' 2^-17, and a
-// key's weights of all rows lie in one thread's TMEM lane: their sum needs no exchange.  Per CTA: a warp that
-// loads the keys' 64-dim blocks (16 KB a stage), one that loads the queries, four that take the exponentials, one that
-// brings the next tiles into the L2; CTA 0's second warp issues the MMAs.
+// key's weights of all rows lie in one thread's TMEM lane: their sum needs no exchange.  Per CTA: three warps that
+// load the keys' 64-dim blocks (16 KB a stage) in turns, one that loads the queries, four that take the exponentials; CTA
+// 0's second warp issues the MMAs.
+//
+// What bounds it.  64 ragged requests of up to 32768 keys, 128 heads: 218 us, 6.2 TB/s, 0.92 of a copy's rate; 8 requests'
+// last 32 tokens over 8192 keys, 16 heads: 48 us, 3.4 us a tile, in which the tensor pipes are busy 2.2 (their operands,
+// from L2, come in stages of which five are in flight).  What it took: no L2 prefetch (asking for tiles one to five
+// ahead, by bulk copies or line by line, cost 0.1-0.17 ms of the first case), three loading warps (one issues
+// the boxes of 16-row pages too slowly: 76 us for the second case, 55 with three), five stages (238 us with four).
+// Eight warps for the exponentials gained 2 us of the second case and cost 7 of the first.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -52,10 +59,10 @@ __device__ __forceinline__ void add_fixed(unsigned long long *at, float x, float
 // ------------------------------------------------------------------- tensor cores ----
 constexpr int DK = 512, DR = 64;
 constexpr int ROWS = 128, KT = 128;                // query rows of an item, keys of a CTA's half of a tile
-constexpr int BLOCKS = (DK + DR) / 64, STAGES = 4;
+constexpr int BLOCKS = (DK + DR) / 64, STAGES = 5;
 constexpr uint32_t BLK = 128 * 128;                // 128 rows of 64 dims
-constexpr int NTHREADS = 256;
-constexpr int PF = 2;                              // tiles asked for ahead of the loads
+// warps: 0, 7, 8 load keys, 1 issues, 2-5 weigh, 6 loads queries
+constexpr int LOADERS = 3, NTHREADS = 32 * (6 + LOADERS);
 constexpr uint32_t OFF_K = BLOCKS * BLK, OFF_ROW = OFF_K + STAGES * BLK, OFF_BAR = OFF_ROW + 2 * ROWS * 8 + 64;
 constexpr uint32_t W_SMEM = OFF_BAR + 256;
 static_assert(W_SMEM <= 232448, "shared memory budget");
@@ -110,7 +117,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     int *least = row_lim + 2 * ROWS;               // [part parity][warp]: the least of them
     uint64_t *bars = (uint64_t *)(smem + OFF_BAR);
     uint32_t *tslot = (uint32_t *)(bars + B_COUNT);
-    volatile int *abort = (volatile int *)(tslot + 1), *prog = abort + 1;   // prog: tiles whose loads have begun
+    volatile int *abort = (volatile int *)(tslot + 1);
     const PagedDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
@@ -118,7 +125,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     if (tid == 0) {
         for (int i = 0; i < B_COUNT; ++i) mbar_init(&bars[i], i >= B_SFREE ? 8 : 1);
         *abort = 0;
-        *prog = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -155,21 +161,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     auto wait = [&](int i, uint32_t parity) { return mbar_wait(&bars[i], parity, abort, &g_paged_weights_err); };
     auto wait_pair = [&](int i, uint32_t parity) { return mbar_wait_cluster(&bars[i], parity, abort, &g_paged_weights_err); };
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ the keys' blocks, a lane per unit
+    if (warp == 0 || warp >= 7) {
+        // ------------------------------------------------------------ the keys' blocks in turns, a lane per unit
         const uint32_t full0 = map_peer(smem_u32(&bars[B_FULL]), 0);
         const int none = p.num_pages * p.page;   // a row outside the cache: zeros
-        int it = 0, n = 0;
+        const int me = warp == 0 ? 0 : warp - 6;
+        int it = 0;
         bool go = true;
         for (; more && go; next()) {
             const int key0 = (int)rank * KT + lane * UNIT;   // of the lane's unit in a tile
             int ahead = lane < UNITS ? row_of(a, w, w.k0 * 2 * KT + key0) : -1;
-            for (int i = 0; i < w.nt && go; ++i, ++n) {
+            for (int i = 0; i < w.nt && go; ++i) {
                 const int row = ahead >= 0 ? ahead : none;
                 if (i + 1 < w.nt && lane < UNITS) ahead = row_of(a, w, (w.k0 + i + 1) * 2 * KT + key0);
-                *prog = n + 1;
 #pragma unroll 1
                 for (int j = 0; j < BLOCKS; ++j, ++it) {
+                    if (it % LOADERS != me) continue;
                     const int s = it % STAGES;
                     go = __all_sync(FULL, wait_pair(B_EMPTY + s, ((it / STAGES) & 1) ^ 1));   // (passes at first)
                     if (!go) break;
@@ -301,27 +308,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                 for (int o = SHARE / 2; o > 0; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
                 if (ok && held && lane % SHARE == 0 && x > 0.f) add_fixed(a.acc + (long)w.row * p.max_pages + col, x, a.one);
-            }
-        }
-    } else if (warp == 7) {
-        // ------------------------------------------------------------ L2 prefetch of the tiles loaded next
-        int n = 0;
-        bool go = true;
-        for (; more && go; next()) {
-#pragma unroll 1
-            for (int i = 0; i < w.nt && go; ++i, ++n) {
-                const int r = lane < UNITS ? row_of(a, w, ((w.k0 + i) * 2 + (int)rank) * KT + lane * UNIT) : -1;
-                const uint64_t t0 = global_ns();
-                for (uint32_t k = 1; *prog < n - PF && go; ++k) {
-                    __nanosleep(128);
-                    if ((k & 1023) == 0 && (*abort || global_ns() - t0 > WAIT_NS)) go = false;
-                }
-                go = __all_sync(FULL, go);
-                if (go && r >= 0) {
-                    l2_prefetch((const bf16 *)p.c_cache + (long)r * DK, UNIT * DK * 2);
-                    l2_prefetch((const bf16 *)p.kpe_cache + (long)r * DR, UNIT * DR * 2);
-                }
-                __syncwarp();
             }
         }
     }

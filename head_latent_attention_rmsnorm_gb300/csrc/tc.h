@@ -41,7 +41,7 @@ struct alignas(16) StepTile {
 struct TcStep {
     int T, H, hs, key_rows;        // tokens, heads, heads of a shard, rows of the key buffers (a multiple of 256)
     float scale;
-    const void *q_nope, *qpe;      // [T][H][128] bf16; [T][H][64] fp16, rotated
+    const void *q_nope, *qpe;      // [T][H][128] bf16; [T][H][2][64] fp16: rotated q_pe, what its rounding leaves
     const void *chat, *kpe, *w;    // [key_rows][512] bf16, [key_rows][64] fp16, W_kv_b
     void *kws, *vws;               // [key_rows][hs 128], [hs 128][key_rows] fp16
     void *out;                     // [T][H][128]

@@ -58,16 +58,27 @@ constexpr uint32_t V_BYTES = 2 * BOX;          // V^T: 128 dv rows x 2 key halve
 // runs with N = 144, so O column 128 accumulates the row sum of P exactly as the MMA used
 // it, and the softmax needs no sum of its own.
 constexpr uint32_t ONES = 16 * 128;
-constexpr uint32_t VBOX = BOX + ONES;          // one key half of a V slot
-constexpr uint32_t V_SLOT = 2 * VBOX;
 constexpr int KST = 2, VST = 2;
-constexpr uint32_t QS_BYTES = 3 * BOX;         // staged Q of the next unit: q_nope lo, hi (bf16), rotated q_pe (fp16)
 constexpr int NSM = 4;                        // softmax warps: one thread per query row
-// Q staging, K/V rings, 1 KB alignment slack, 256 B of barriers
-constexpr uint32_t SMEM_BYTES = QS_BYTES + KST * K_BYTES + VST * V_SLOT + 1024 + 256;
-// TMEM columns: S buffers 0-127 and 128-255, O 256-399 (dv 0-127, row sum 128, zeros),
-// Q (192 fp16 = 96 columns) 400-495
-constexpr uint32_t T_O = 256, T_L = T_O + 128, T_Q = 400;
+constexpr uint32_t T_O = 256, T_L = T_O + 128;
+// STEP (a paged step's tokens): the row sums are the softmax's, in fp32 and of the unrounded weights: the column of ones
+// gathers 16 weights at a time in an accumulator that cuts off, 3e-5 of the sum at 16384 keys; and the rotated
+// q_pe has its fp16 rest too (four more score MMAs of 12): its rounding is the same for all keys, and shifted a
+// log-sum-exp by 1.5e-5 whatever their number.  Together the log-sum-exp's error there falls from 2.9e-6 to 2e-7 of it.
+template <bool STEP>
+struct Lay {
+    static constexpr uint32_t VBOX = STEP ? BOX : BOX + ONES;   // one key half of a V slot
+    static constexpr uint32_t V_SLOT = 2 * VBOX;
+    // staged Q of the next unit: q_nope lo, hi (bf16), rotated q_pe (fp16; STEP: and its rest)
+    static constexpr int Q_BOXES = STEP ? 4 : 3;
+    static constexpr uint32_t QS_BYTES = Q_BOXES * BOX;
+    // Q staging, K/V rings, 1 KB alignment slack, 256 B of barriers
+    static constexpr uint32_t SMEM_BYTES = QS_BYTES + KST * K_BYTES + VST * V_SLOT + 1024 + 256;
+    // TMEM columns: S buffers 0-127 and 128-255, O 256-399 (dv 0-127, row sum 128, zeros), Q (192 fp16 = 96 columns)
+    // 400-495; STEP: O 256-383, Q 384-511
+    static constexpr uint32_t T_Q = STEP ? 384 : 400;
+    static_assert(SMEM_BYTES <= 232448 && T_Q + 32 * Q_BOXES <= 512, "budgets");
+};
 constexpr float RESCALE_LOG2 = 8.0f;
 
 struct AttnK {
@@ -87,12 +98,14 @@ struct AttnK {
 // V^T; each row has its own limit, pages may be missing.
 struct StepK {
     const StepTile *tiles;    // heaviest first
-    const int *n_tiles;
+    const int *ctl;           // key rows in use, number of tiles
     const int *limits, *done; // [tokens]: keys seen; nonzero: this kernel's
     const uint32_t *held;     // a bit per key row: there is such a key
     const int *holes;         // [requests]: nonzero: some page is missing
     long lse_i;               // log-sum-exps of a token
 };
+
+constexpr int L2_KEYS = (112 << 20) / 512;   // (key, head) pairs whose K_nope and V^T stay in L2 (of 129 MB)
 
 // One work unit = (128-query tile, head, batch).  Units are numbered heaviest first
 // under the causal mask: (head, batch) fastest, query tiles from the latest down.
@@ -101,11 +114,15 @@ struct Work {
     int k0, rows, request;   // STEP: first key row, query rows, request
 };
 template <bool STEP>
-__device__ __forceinline__ Work work_of(const AttnK &p, const StepK &s, int u) {
+__device__ __forceinline__ Work work_of(const AttnK &p, const StepK &s, int n_tiles, bool heaviest, int u) {
     if (STEP) {
-        const int4 *e = (const int4 *)(s.tiles + u / p.nh);
+        // the heaviest tiles first, where L2 holds all heads' K_nope and V^T; else a head's tiles behind one another, so
+        // that it holds those of the ten or so heads in work (three prompts of up to 4096 tokens, 16 heads, 103 MB: 102 us
+        // against 127; 2048 tokens over 16384 keys, 64 heads a shard: 2.07 ms against 2.17)
+        const int div = heaviest ? p.nh : n_tiles, a = u / div, b = u - a * div;
+        const int4 *e = (const int4 *)(s.tiles + (heaviest ? a : b));
         const int4 x = __ldcg(e), y = __ldcg(e + 1);
-        return Work{u % p.nh, 0, x.x, x.w, x.z, x.y, y.x};
+        return Work{heaviest ? b : a, 0, x.x, x.w, x.z, x.y, y.x};
     }
     const int nhb = p.nh * p.nb;
     const int hb = u % nhb;
@@ -134,6 +151,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                    const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mKr,
                    const __grid_constant__ CUtensorMap mV, AttnK p, StepK sp) {
     extern __shared__ uint8_t smem_raw[];
+    constexpr uint32_t VBOX = Lay<STEP>::VBOX, V_SLOT = Lay<STEP>::V_SLOT, QS_BYTES = Lay<STEP>::QS_BYTES, T_Q = Lay<STEP>::T_Q;
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sQs = smem;
     uint8_t *sK = sQs + QS_BYTES;
@@ -178,7 +196,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
     }
     // the constant rows after every V^T box: row 0 ones (fp16 1.0), rows 1-15 zeros (a
     // row that is constant is unchanged by the 128-byte swizzle)
-    for (int i = tid; i < VST * 2 * (int)(ONES / 16); i += blockDim.x) {
+    for (int i = tid; !STEP && i < VST * 2 * (int)(ONES / 16); i += blockDim.x) {
         const int box = i / (ONES / 16), off = i % (ONES / 16);   // 16-byte chunk of the block
         const uint32_t v = off < 8 ? 0x3c003c00u : 0u;             // first 128-byte row: ones
         *(uint4 *)(sV + (box >> 1) * V_SLOT + (box & 1) * VBOX + BOX + off * 16) = make_uint4(v, v, v, v);
@@ -193,7 +211,8 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
     // table; the softmax warps first read their first unit's q rows, which are inputs.
     // A step's units and limits come from the launches in front: there every warp waits.
     if (STEP) pdl_wait();
-    const int units = STEP ? __ldcg(sp.n_tiles) * p.nh : p.units;
+    const int n_tiles = STEP ? __ldcg(sp.ctl + 1) : 0, units = STEP ? n_tiles * p.nh : p.units;
+    const bool heaviest = STEP && (long)__ldcg(sp.ctl) * p.nh <= L2_KEYS;
 
     // Every role walks the same units in the same order and counts key tiles T across
     // units, so ring slots and barrier parities continue from one unit to the next.
@@ -210,7 +229,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             for (int k = 0; k * G < units && ok; ++k) {
                 const int u = unit_at(k, c, G);
                 if (u >= units) continue;
-                const Work w = work_of<STEP>(p, sp, u);
+                const Work w = work_of<STEP>(p, sp, n_tiles, heaviest, u);
                 // this unit's Q into the staging buffer, once the softmax warps have moved
                 // the previous unit's Q into TMEM (this runs a couple of key tiles ahead of
                 // them, so the load has that long to land)
@@ -220,6 +239,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                 tma_load_4d(sQs, &mQn, qs_full, 0, p.head_off + w.hl, w.q0, w.b);
                 tma_load_4d(sQs + BOX, &mQn, qs_full, 64, p.head_off + w.hl, w.q0, w.b);
                 tma_load_4d(sQs + 2 * BOX, &mQr, qs_full, 0, p.head_off + w.hl, w.q0, w.b);
+                if (STEP) tma_load_4d(sQs + 3 * BOX, &mQr, qs_full, 64, p.head_off + w.hl, w.q0, w.b);
                 for (int j = 0; j < w.nt; ++j, ++T) {
                     const int ks = T % KST;
                     if (T >= KST && !mbar_wait(&k_empty[ks], ((T / KST) - 1) & 1, abort, &g_tc_attn_err)) {
@@ -244,7 +264,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             for (int k = 0; k * G < units && ok; ++k) {
                 const int u = unit_at(k, c, G);
                 if (u >= units) continue;
-                const Work w = work_of<STEP>(p, sp, u);
+                const Work w = work_of<STEP>(p, sp, n_tiles, heaviest, u);
                 for (int j = 0; j < w.nt; ++j, ++T) {
                     const int vs = T % VST;
                     if (T >= VST && !mbar_wait(&v_empty[vs], ((T / VST) - 1) & 1, abort, &g_tc_attn_err)) {
@@ -269,7 +289,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             for (int k = 0; k * G < units && ok; ++k) {
                 const int u = unit_at(k, c, G);
                 if (u >= units) continue;
-                const Work w = work_of<STEP>(p, sp, u);
+                const Work w = work_of<STEP>(p, sp, n_tiles, heaviest, u);
                 // this unit's Q is in TMEM
                 if (!__all_sync(0xffffffffu, mbar_wait(q_ready, n & 1, abort, &g_tc_attn_err))) break;
                 ++n;
@@ -288,8 +308,8 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                     const uint8_t *kd = sK + ks * K_BYTES;
                     if (elect_one()) {
 #pragma unroll
-                        for (int kb = 0; kb < 3; ++kb) {
-                            const uint64_t db = sdesc_kmajor(kd + kb * BOX);
+                        for (int kb = 0; kb < Lay<STEP>::Q_BOXES; ++kb) {
+                            const uint64_t db = sdesc_kmajor(kd + (kb < 3 ? kb : 2) * BOX);
 #pragma unroll
                             for (int k4 = 0; k4 < 4; ++k4)
                                 mma_ts(s_tm, tmem + T_Q + (kb * 4 + k4) * 8, db + 2 * k4, p.idesc_s, (kb | k4) != 0);
@@ -311,7 +331,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             for (int k = 0; k * G < units && ok; ++k) {
                 const int u = unit_at(k, c, G);
                 if (u >= units) continue;
-                const Work w = work_of<STEP>(p, sp, u);
+                const Work w = work_of<STEP>(p, sp, n_tiles, heaviest, u);
                 // the epilogue of the previous unit has read O before P.V_0 overwrites it
                 if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(o_free, (n - 1) & 1, abort, &g_tc_attn_err))) break;
                 ++n;
@@ -387,8 +407,9 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                 tmem_st16(lane_base + T_Q + 32 * h, qn[0]);
                 tmem_st16(lane_base + T_Q + 32 * h + 16, qn[1]);
             }
-            {
-                const uint8_t *prow = sQs + 2 * BOX + row * 128;
+#pragma unroll
+            for (int h = 2; h < Lay<STEP>::Q_BOXES; ++h) {
+                const uint8_t *prow = sQs + h * BOX + row * 128;
                 uint32_t pe[2][16];
 #pragma unroll
                 for (int cc = 0; cc < 8; ++cc) {
@@ -396,8 +417,8 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                     pe[cc >> 2][4 * (cc & 3)] = v.x, pe[cc >> 2][4 * (cc & 3) + 1] = v.y;
                     pe[cc >> 2][4 * (cc & 3) + 2] = v.z, pe[cc >> 2][4 * (cc & 3) + 3] = v.w;
                 }
-                tmem_st16(lane_base + T_Q + 64, pe[0]);
-                tmem_st16(lane_base + T_Q + 80, pe[1]);
+                tmem_st16(lane_base + T_Q + 32 * h, pe[0]);
+                tmem_st16(lane_base + T_Q + 32 * h + 16, pe[1]);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -408,7 +429,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
         if (k * G < units) load_q(0);
         for (; k * G < units;) {
             const int u = unit_at(k, c, G);
-            const Work w = work_of<STEP>(p, sp, u);
+            const Work w = work_of<STEP>(p, sp, n_tiles, heaviest, u);
             const int hq = p.head_off + w.hl, b = w.b, q0 = w.q0, nt = w.nt;
             const int pos = p.q_offset + q0 + row;
             int sees = 0, all_see = 0, holes = 0;   // STEP: keys that the row, that every row of the warp sees
@@ -418,6 +439,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                 holes = __ldcg(sp.holes + w.request);
             }
             float m = -INFINITY;
+            float sum = 0.f;   // STEP: the row sum
             for (int j = 0; j < nt; ++j, ++T) {
                 const int sb = T & 1;
                 ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[sb], (T >> 1) & 1, abort, &g_tc_attn_err));
@@ -486,28 +508,39 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
                             tmem_st32(lane_base + T_O + 32 * q, o);
                         }
-                        const uint32_t lv = tmem_ld1(lane_base + T_L);   // the row sum, rescaled with the row
-                        tmem_ld_wait();
-                        tmem_st1(lane_base + T_L, __float_as_uint(__uint_as_float(lv) * alpha));
+                        if (!STEP) {
+                            const uint32_t lv = tmem_ld1(lane_base + T_L);   // the row sum, rescaled with the row
+                            tmem_ld_wait();
+                            tmem_st1(lane_base + T_L, __float_as_uint(__uint_as_float(lv) * alpha));
+                        }
                         tmem_st_wait();
                     }
+                    sum *= alpha;
                     m = m_use;
                 }
                 const float nm = (m == -INFINITY) ? 0.f : -m;
                 // P over the S columns it came from, 32 keys (16 columns) at a time
+                float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        pk[i] = pack_f16(ex2(fmaf(x[32 * q + 2 * i], p.scale_log2, nm)),
-                                         ex2(fmaf(x[32 * q + 2 * i + 1], p.scale_log2, nm)));
+                    for (int i = 0; i < 16; ++i) {
+                        const float p0 = ex2(fmaf(x[32 * q + 2 * i], p.scale_log2, nm)),
+                                    p1 = ex2(fmaf(x[32 * q + 2 * i + 1], p.scale_log2, nm));
+                        pk[i] = pack_f16(p0, p1);
+                        if (STEP) {
+                            add[2 * (i & 1)] += p0;
+                            add[2 * (i & 1) + 1] += p1;
+                        }
+                    }
                     if (ok) tmem_st16(lane_base + sb * 128 + 16 * q, pk);
                 }
                 if (ok) tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[sb]);
+                sum += (add[0] + add[1]) + (add[2] + add[3]);
             }
             const int k_next = next_unit(k + 1);
             if (k_next * G < units) load_q(n + 1);
@@ -522,7 +555,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                 for (int q = 0; q < 4; ++q) tmem_ld32(lane_base + T_O + 32 * q, o[q]);
                 const uint32_t lv = tmem_ld1(lane_base + T_L);
                 tmem_ld_wait();
-                l = __uint_as_float(lv);
+                l = STEP ? sum : __uint_as_float(lv);
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -633,6 +666,7 @@ cudaError_t tc_explicit_prefill(const TcPrefill &p, const void *q_nope, const vo
         unsigned box[3] = {64, 128, 1};
         if ((e = make_tma_map(&mV, vws, 3, d, s, box)) != cudaSuccess) return e;
     }
+    constexpr uint32_t SMEM_BYTES = Lay<false>::SMEM_BYTES;
     e = cudaFuncSetAttribute(tc_attn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
     if (e != cudaSuccess) return e;
     int dev = 0, n_sms = 0;
@@ -694,10 +728,10 @@ cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st) {
     cudaError_t e;
     CUtensorMap mQn, mQr, mK, mKr, mV;
     {
-        const ull d[4] = {128, H, T, 1}, s[3] = {256, H * 256, T * H * 256}, dr[4] = {64, H, T, 1}, sr[3] = {128, H * 128, T * H * 128};
+        const ull d[4] = {128, H, T, 1}, s[3] = {256, H * 256, T * H * 256}, dr[4] = {128, H, T, 1};
         const unsigned box[4] = {64, 1, 128, 1};
         if ((e = make_tma_map(&mQn, p.q_nope, 4, d, s, box)) != cudaSuccess) return e;
-        if ((e = make_tma_map(&mQr, p.qpe, 4, dr, sr, box)) != cudaSuccess) return e;
+        if ((e = make_tma_map(&mQr, p.qpe, 4, dr, s, box)) != cudaSuccess) return e;
     }
     {
         const ull dr[3] = {64, R, 1}, sr[2] = {128, R * 128}, dk[3] = {hs * 128, R, 1}, sk[2] = {hs * 256, R * hs * 256};
@@ -707,6 +741,7 @@ cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st) {
         if ((e = make_tma_map(&mK, p.kws, 3, dk, sk, box)) != cudaSuccess) return e;
         if ((e = make_tma_map(&mV, p.vws, 3, dv, sv, box)) != cudaSuccess) return e;
     }
+    constexpr uint32_t SMEM_BYTES = Lay<true>::SMEM_BYTES;
     if ((e = cudaFuncSetAttribute(tc_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess) return e;
     int dev = 0, n_sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -719,9 +754,9 @@ cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st) {
     a.out_v8 = ((uintptr_t)p.out % 32) == 0;
     a.lse = p.lse;
     a.idesc_s = idesc_f16(128, 128, true);
-    a.idesc_pv = idesc_f16(128, 144, true);
+    a.idesc_pv = idesc_f16(128, 128, true);
     a.nb = 1;
-    const StepK sp{p.tiles, p.ctl + 1, p.limits, p.done, p.held, p.holes, p.H};
+    const StepK sp{p.tiles, p.ctl, p.limits, p.done, p.held, p.holes, p.H};
     for (int h0 = 0; h0 < p.H; h0 += p.hs) {
         const int nh = std::min(p.hs, p.H - h0);
         // bf16 rows and weights as they are: their products are exact in the fp32 accumulator

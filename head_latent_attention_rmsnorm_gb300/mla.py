@@ -826,7 +826,7 @@ def paged_decode(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens
 
 
 PREFILL_KEY_ROWS = 65536   # key rows that paged_prefill takes for its explicit form by itself, at most
-PREFILL_HEAD_SHARD = 16
+PREFILL_HEAD_SHARD = 64
 
 
 def _prefill_room(n_tokens, block_table, page, key_rows, head_shard):
