@@ -1224,6 +1224,8 @@ void paged_explicit_carve(const PagedDecode &p, int B, int n_tokens, int key_row
     const size_t R = key_rows, T = n_tokens;
     x->c.key_rows = key_rows;
     x->c.max_tiles = chunk_tiles(n_tokens);
+    x->c.max_rests = chunk_rests(n_tokens, key_rows);
+    x->c.rest_of = (int *)c.take(R / 128 * sizeof(int));
     x->c.ctl = (int *)c.take(3 * sizeof(int));
     x->c.key0 = (int *)c.take(B * sizeof(int));
     x->c.holes = (int *)c.take(B * sizeof(int));
@@ -1239,6 +1241,7 @@ void paged_explicit_carve(const PagedDecode &p, int B, int n_tokens, int key_row
     x->c.qpe = c.take(T * p.H * p.Dr * 4);
     x->c.kws = c.take(R * x->hs * p.Dn * 2);
     x->c.vws = c.take(R * x->hs * p.Dv * 2);
+    x->c.rest = c.take((size_t)x->c.max_rests * 128 * x->hs * p.Dn * 2);
 }
 
 size_t paged_prefill_ws(PagedDecode *p, PagedRound *r, PagedExplicit *x, int B, int n_tokens, int key_rows, int head_shard, void *base) {
@@ -1381,7 +1384,7 @@ mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n
         q.q_pe = q_pe;
         MLA_TRY(launch_paged_chunk(q, step, x.c, (cudaStream_t)cuda_stream));
         const TcStep t{n_tokens, p.H, x.hs, x.c.key_rows, p.scale, q_nope, x.c.qpe, x.c.chat, x.c.kpe, w_kv_b, x.c.kws, x.c.vws,
-                       out, lse, x.c.ctl, x.c.tiles, x.c.limits, x.c.done, x.c.held, x.c.holes};
+                       x.c.rest, x.c.max_rests * 128, x.c.rest_of, out, lse, x.c.ctl, x.c.tiles, x.c.limits, x.c.done, x.c.held, x.c.holes};
         MLA_TRY(tc_step_prefill(t, (cudaStream_t)cuda_stream));
     }
     for (int s0 = 0; s0 < n_tokens; s0 += PAGED_ROUND) {

@@ -91,12 +91,14 @@ constexpr int PAGED_ROUND = 2048;
 cudaError_t launch_paged_plan(const PagedDecode &p, const PagedStep &s, int s0, int *lens, int2 *of, int *limits, int4 *groups,
                               cudaStream_t st, unsigned long long *zero = nullptr, long n_zero = 0);
 
-// The explicit form of the requests with many tokens (tensor cores): CHUNK_MIN tokens and more that see more than CHUNK_FEW
-// keys.  Tiles of 128 tokens: at most n_tokens / 128 and one more a request.
-constexpr int CHUNK_MIN = 160, CHUNK_FEW = 512, CHUNK_SORT = 2048;
+// The explicit form of the requests with many tokens (tensor cores), CHUNK_MIN and more.  Tiles of 128 tokens: at most
+// n_tokens / 128 and one more a request.  CHUNK_RESTS: tiles of 128 keys that have the rest of K_nope.
+constexpr int CHUNK_MIN = 160, CHUNK_RESTS = 4, CHUNK_SORT = 2048;
 struct PagedChunk {
     int key_rows;                // rows of the key buffers, a multiple of 256
-    int max_tiles;
+    int max_tiles, max_rests;    // tiles of 128 tokens; tiles of 128 keys with a rest
+    int *rest_of;                // [key_rows / 128]
+    void *rest;
     int *ctl;                    // [3]: rows in use, tiles, tokens of the list
     int *key0, *holes;           // [B]: a request's first key row (-1: absorbed); nonzero: some page is missing
     int *block_of;               // [key_rows / 128]: the request of each 128 rows
@@ -105,6 +107,10 @@ struct PagedChunk {
     uint32_t *held;              // a bit per key row
     void *chat, *kpe, *qpe, *kws, *vws;
 };
+inline int chunk_rests(int n_tokens, int key_rows) {
+    const int a = key_rows / 128, b = n_tokens / CHUNK_MIN;
+    return b < a / CHUNK_RESTS ? b * CHUNK_RESTS : a;
+}
 inline int chunk_tiles(int n_tokens) { return n_tokens / 128 + n_tokens / CHUNK_MIN + 1; }
 // The plan and the gathered rows; p.q_pe of the whole step.
 cudaError_t launch_paged_chunk(const PagedDecode &p, const PagedStep &s, const PagedChunk &c, cudaStream_t st);

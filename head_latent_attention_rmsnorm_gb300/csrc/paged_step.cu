@@ -160,9 +160,7 @@ __device__ long block_before(long n, long *warp_tot, long &all) {
 // Which form is cheaper.  A (token, key, head) costs 2 (512 + 64 + 512) = 2176 operations absorbed and 2 (192 + 128) =
 // 640 explicit, which has 2 * 256 * 512 on top for a key and head, once for all of the request's tokens: equal at 171
 // tokens, whatever the keys and heads.  A request goes explicit from CHUNK_MIN tokens on, where its keys' rows,
-// rounded up to whole tiles, fit in what the requests in front of it left of the buffers.  Its tokens
-// that see up to CHUNK_FEW keys stay absorbed: the explicit form rounds K_nope and P to fp16, an error of about
-// 2e-4 / sqrt(0.4 keys) in a log-sum-exp, which at few keys is more than the rest of the call's.
+// rounded up to whole tiles, fit in what the requests in front of it left of the buffers.
 // One block: prefix sums over the requests, then a warp per 128 tokens, then the tiles in falling order of their keys.
 struct Chunk {
     PagedStep s;
@@ -177,7 +175,7 @@ __global__ void __launch_bounds__(PNT) paged_chunk_kernel(const __grid_constant_
     pdl_wait();
     pdl_launch_dependents();
     for (int i = tid; i < N; i += PNT) a.c.done[i] = 0;
-    long rows = 0, tiles = 0, used = 0;
+    long rows = 0, tiles = 0, used = 0, rests = 0;
     for (int b0 = 0; b0 < a.s.B; b0 += PNT) {
         const int b = b0 + tid;
         int t0 = 0, n = 0, keys = 0;
@@ -186,7 +184,7 @@ __global__ void __launch_bounds__(PNT) paged_chunk_kernel(const __grid_constant_
             n = min(max(a.s.cu[b + 1], 0), N) - t0;
             keys = min(max(a.s.lens[b], 0), a.cap);
         }
-        const bool may = min(n, keys - CHUNK_FEW) >= CHUNK_MIN;
+        const bool may = min(n, keys) >= CHUNK_MIN;
         const long need = may ? (keys + 127l) / 128 * 128 : 0;
         long all;
         const long r0 = rows + block_before(need, warp_tot, all);
@@ -197,6 +195,10 @@ __global__ void __launch_bounds__(PNT) paged_chunk_kernel(const __grid_constant_
         tiles += all;
         block_before(fits ? need : 0, warp_tot, all);   // (those that fit are the first of those that may)
         used += all;
+        int rest = fits ? (int)min(need / 128, (long)CHUNK_RESTS) : 0;
+        const long p0 = rests + block_before(rest, warp_tot, all);
+        rests += all;
+        if (p0 + rest > a.c.max_rests) rest = 0;   // (only where cu decreases)
         if (b < a.s.B) {
             a.c.key0[b] = fits ? (int)r0 : -1;
             a.c.holes[b] = 0;
@@ -207,9 +209,14 @@ __global__ void __launch_bounds__(PNT) paged_chunk_kernel(const __grid_constant_
                     x.rows = min(128, n - 128 * e);
                     x.key = (int)r0;
                     x.request = b;
+                    x.rest = (int)p0 * 128;
+                    x.rests = rest;
                     a.c.raw[e0 + e] = x;
                 }
-                for (int i = 0; i < (int)(need / 128); ++i) a.c.block_of[r0 / 128 + i] = b;
+                for (int i = 0; i < (int)(need / 128); ++i) {
+                    a.c.block_of[r0 / 128 + i] = b;
+                    a.c.rest_of[r0 / 128 + i] = i < rest ? (int)p0 + i : -1;
+                }
             }
         }
     }
@@ -226,7 +233,7 @@ __global__ void __launch_bounds__(PNT) paged_chunk_kernel(const __grid_constant_
             if (r >= x.rows) continue;
             const int pos = a.s.positions[t], sees = pos < 0 ? 0 : min(keys, pos == 2147483647 ? pos : pos + 1);
             a.c.limits[t] = sees;
-            if (sees > CHUNK_FEW) {
+            if (sees > 0) {
                 a.c.done[t] = 1;
                 most = max(most, sees);
             }

@@ -36,7 +36,7 @@ cudaError_t tc_explicit_prefill(const TcPrefill &p, const void *q_nope, const vo
 // of one head shard after the other.
 struct alignas(16) StepTile {
     int token, rows, key, tiles;   // first token, tokens (up to 128), first key row, key tiles of 128
-    int request, pad[3];
+    int request, rest, rests, pad; // first row of K_nope's rest, key tiles that have one
 };
 struct TcStep {
     int T, H, hs, key_rows;        // tokens, heads, heads of a shard, rows of the key buffers (a multiple of 256)
@@ -44,6 +44,9 @@ struct TcStep {
     const void *q_nope, *qpe;      // [T][H][128] bf16; [T][H][2][64] fp16: rotated q_pe, what its rounding leaves
     const void *chat, *kpe, *w;    // [key_rows][512] bf16, [key_rows][64] fp16, W_kv_b
     void *kws, *vws;               // [key_rows][hs 128], [hs 128][key_rows] fp16
+    void *rest;                    // [rest_rows][hs 128] fp16: what K_nope's rounding leaves
+    int rest_rows;
+    const int *rest_of;            // [key_rows / 128]: 128 rows' place there, -1: none
     void *out;                     // [T][H][128]
     float *lse;                    // [T][H]
     const int *ctl;                // key rows in use, number of tiles

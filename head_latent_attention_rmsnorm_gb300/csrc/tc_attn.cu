@@ -65,6 +65,8 @@ constexpr uint32_t T_O = 256, T_L = T_O + 128;
 // gathers 16 weights at a time in an accumulator that cuts off, 3e-5 of the sum at 16384 keys; and the rotated
 // q_pe has its fp16 rest too (four more score MMAs of 12): its rounding is the same for all keys, and shifted a
 // log-sum-exp by 1.5e-5 whatever their number.  Together the log-sum-exp's error there falls from 2.9e-6 to 2e-7 of it.
+// K_nope's rounding errs by 1.6e-4 in each score, 1.6e-4 / sqrt(0.4 keys) in a row's log-sum-exp: little but for rows of
+// few keys, so the request's first 512 keys have K_nope's rest in the scores too (eight MMAs more for those tiles).
 template <bool STEP>
 struct Lay {
     static constexpr uint32_t VBOX = STEP ? BOX : BOX + ONES;   // one key half of a V slot
@@ -112,6 +114,7 @@ constexpr int L2_KEYS = (112 << 20) / 512;   // (key, head) pairs whose K_nope a
 struct Work {
     int hl, b, q0, nt;
     int k0, rows, request;   // STEP: first key row, query rows, request
+    int r0, nr;              // STEP: first row of K_nope's rest, key tiles that have one
 };
 template <bool STEP>
 __device__ __forceinline__ Work work_of(const AttnK &p, const StepK &s, int n_tiles, bool heaviest, int u) {
@@ -122,7 +125,7 @@ __device__ __forceinline__ Work work_of(const AttnK &p, const StepK &s, int n_ti
         const int div = heaviest ? p.nh : n_tiles, a = u / div, b = u - a * div;
         const int4 *e = (const int4 *)(s.tiles + (heaviest ? a : b));
         const int4 x = __ldcg(e), y = __ldcg(e + 1);
-        return Work{heaviest ? b : a, 0, x.x, x.w, x.z, x.y, y.x};
+        return Work{heaviest ? b : a, 0, x.x, x.w, x.z, x.y, y.x, y.y, min(y.z, x.w)};
     }
     const int nhb = p.nh * p.nb;
     const int hb = u % nhb;
@@ -132,7 +135,7 @@ __device__ __forceinline__ Work work_of(const AttnK &p, const StepK &s, int n_ti
     w.q0 = (p.n_qt - 1 - u / nhb) * BQ;
     const int kv_end = p.causal ? min(p.kv_need, p.q_offset + w.q0 + BQ) : p.kv_need;
     w.nt = (kv_end + BKV - 1) / BKV;
-    w.k0 = 0;
+    w.k0 = w.nr = 0;
     return w;
 }
 // Unit of round k for CTA c of G: rounds alternate direction over the heaviest-first
@@ -149,7 +152,7 @@ template <bool STEP>
 __global__ void __launch_bounds__(32 * (NSM + 4), 1)
     tc_attn_kernel(const __grid_constant__ CUtensorMap mQn, const __grid_constant__ CUtensorMap mQr,
                    const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mKr,
-                   const __grid_constant__ CUtensorMap mV, AttnK p, StepK sp) {
+                   const __grid_constant__ CUtensorMap mV, AttnK p, const __grid_constant__ CUtensorMap mR, StepK sp) {
     extern __shared__ uint8_t smem_raw[];
     constexpr uint32_t VBOX = Lay<STEP>::VBOX, V_SLOT = Lay<STEP>::V_SLOT, QS_BYTES = Lay<STEP>::QS_BYTES, T_Q = Lay<STEP>::T_Q;
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             tma_prefetch_desc(&mK);
             tma_prefetch_desc(&mKr);
             bool ok = true;
-            int T = 0, n = 0;
+            int T = 0, n = 0;   // ring entries, units so far
             for (int k = 0; k * G < units && ok; ++k) {
                 const int u = unit_at(k, c, G);
                 if (u >= units) continue;
@@ -251,6 +254,16 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                     tma_load_3d(kd, &mK, &k_full[ks], w.hl * 128, w.k0 + j * BKV, w.b);
                     tma_load_3d(kd + BOX, &mK, &k_full[ks], w.hl * 128 + 64, w.k0 + j * BKV, w.b);
                     tma_load_3d(kd + 2 * BOX, &mKr, &k_full[ks], 0, w.k0 + j * BKV, w.b);
+                    if (STEP && j < w.nr) {   // the tile's rest of K_nope, an entry of its own
+                        const int rs = ++T % KST;
+                        if (T >= KST && !mbar_wait(&k_empty[rs], ((T / KST) - 1) & 1, abort, &g_tc_attn_err)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&k_full[rs], 2 * BOX);
+                        tma_load_3d(sK + rs * K_BYTES, &mR, &k_full[rs], w.hl * 128, w.r0 + j * BKV, 0);
+                        tma_load_3d(sK + rs * K_BYTES + BOX, &mR, &k_full[rs], w.hl * 128 + 64, w.r0 + j * BKV, 0);
+                    }
                 }
             }
         }
@@ -285,7 +298,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
         {
             pdl_wait();
             bool ok = true;
-            int T = 0, n = 0;   // key tiles, units so far
+            int T = 0, n = 0, R = 0;   // key tiles, units, entries of rests so far
             for (int k = 0; k * G < units && ok; ++k) {
                 const int u = unit_at(k, c, G);
                 if (u >= units) continue;
@@ -294,8 +307,8 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                 if (!__all_sync(0xffffffffu, mbar_wait(q_ready, n & 1, abort, &g_tc_attn_err))) break;
                 ++n;
                 for (int j = 0; j < w.nt; ++j, ++T) {
-                    const int ks = T % KST;
-                    bool go = __all_sync(0xffffffffu, mbar_wait(&k_full[ks], (T / KST) & 1, abort, &g_tc_attn_err));
+                    const int E = STEP ? T + R : T, ks = E % KST;
+                    bool go = __all_sync(0xffffffffu, mbar_wait(&k_full[ks], (E / KST) & 1, abort, &g_tc_attn_err));
                     // S buffer T & 1 last held P_{T-2}: P.V_{T-2} must have read it
                     if (go && T >= 2)
                         go = __all_sync(0xffffffffu, mbar_wait(&pv_done[T & 1], ((T - 2) >> 1) & 1, abort, &g_tc_attn_err));
@@ -314,10 +327,31 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                             for (int k4 = 0; k4 < 4; ++k4)
                                 mma_ts(s_tm, tmem + T_Q + (kb * 4 + k4) * 8, db + 2 * k4, p.idesc_s, (kb | k4) != 0);
                         }
-                        mma_commit(&s_full[T & 1]);
+                        if (!STEP || j >= w.nr) mma_commit(&s_full[T & 1]);
                         mma_commit(&k_empty[ks]);
                     }
                     __syncwarp();
+                    if (STEP && j < w.nr) {
+                        const int rs = (E + 1) % KST;
+                        ++R;
+                        if (!__all_sync(0xffffffffu, mbar_wait(&k_full[rs], ((E + 1) / KST) & 1, abort, &g_tc_attn_err))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kb = 0; kb < 2; ++kb) {
+                                const uint64_t db = sdesc_kmajor(sK + rs * K_BYTES + kb * BOX);
+#pragma unroll
+                                for (int k4 = 0; k4 < 4; ++k4)
+                                    mma_ts(s_tm, tmem + T_Q + (kb * 4 + k4) * 8, db + 2 * k4, p.idesc_s, 1);
+                            }
+                            mma_commit(&s_full[T & 1]);
+                            mma_commit(&k_empty[rs]);
+                        }
+                        __syncwarp();
+                    }
                 }
             }
         }
@@ -713,7 +747,7 @@ cudaError_t tc_explicit_prefill(const TcPrefill &p, const void *q_nope, const vo
             attr[0].val.programmaticStreamSerializationAllowed = 1;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            e = cudaLaunchKernelEx(&cfg, tc_attn_kernel<false>, mQn, mQr, mK, mKr, mV, a, StepK{});
+            e = cudaLaunchKernelEx(&cfg, tc_attn_kernel<false>, mQn, mQr, mK, mKr, mV, a, mK, StepK{});
         }
         if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
     }
@@ -726,7 +760,7 @@ cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st) {
     using ull = unsigned long long;
     const ull R = p.key_rows, H = p.H, T = p.T, hs = p.hs;
     cudaError_t e;
-    CUtensorMap mQn, mQr, mK, mKr, mV;
+    CUtensorMap mQn, mQr, mK, mKr, mV, mR;
     {
         const ull d[4] = {128, H, T, 1}, s[3] = {256, H * 256, T * H * 256}, dr[4] = {128, H, T, 1};
         const unsigned box[4] = {64, 1, 128, 1};
@@ -739,6 +773,8 @@ cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st) {
         const unsigned box[3] = {64, 128, 1};
         if ((e = make_tma_map(&mKr, p.kpe, 3, dr, sr, box)) != cudaSuccess) return e;
         if ((e = make_tma_map(&mK, p.kws, 3, dk, sk, box)) != cudaSuccess) return e;
+        const ull nr = p.rest_rows, drest[3] = {hs * 128, nr, 1}, srest[2] = {hs * 256, nr * hs * 256};
+        if ((e = make_tma_map(&mR, p.rest, 3, drest, srest, box)) != cudaSuccess) return e;
         if ((e = make_tma_map(&mV, p.vws, 3, dv, sv, box)) != cudaSuccess) return e;
     }
     constexpr uint32_t SMEM_BYTES = Lay<true>::SMEM_BYTES;
@@ -765,7 +801,8 @@ cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st) {
         TmaOperand wk{w, 512, 128, nh, 1024, 256 * 1024, 128, 0, 0}, wv{w + 128 * 1024, 512, 128, nh, 1024, 256 * 1024, 128, 0, 0};
         const GemmProblem kv[2] = {{latent, wk, (int)R, nh * 128, 512, 1, p.kws, (long)hs * 128, 1, 0, 0},
                                    {wv, latent, nh * 128, (int)R, 512, 1, p.vws, (long)R, 1, 0, 0}};
-        if ((e = tc_gemm_group(kv, 2, false, st, p.ctl)) != cudaSuccess) return e;
+        const GemmStep gs{p.ctl, p.rest_of, p.rest};
+        if ((e = tc_gemm_group(kv, 2, false, st, &gs)) != cudaSuccess) return e;
         a.head_off = h0;
         a.nh = nh;
         ProfScope ps("tc_attn", st);
@@ -779,7 +816,7 @@ cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st) {
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if ((e = cudaLaunchKernelEx(&cfg, tc_attn_kernel<true>, mQn, mQr, mK, mKr, mV, a, sp)) != cudaSuccess) return e;
+        if ((e = cudaLaunchKernelEx(&cfg, tc_attn_kernel<true>, mQn, mQr, mK, mKr, mV, a, mR, sp)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

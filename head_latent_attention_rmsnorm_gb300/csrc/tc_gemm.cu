@@ -295,7 +295,7 @@ template <bool DYN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     tc_gemm_pair_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUtensorMap tb0,
                         const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUtensorMap tb1, GemmK p,
-                        const int *rows) {
+                        GemmStep step) {
     using namespace tc;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -336,8 +336,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     pdl_launch_dependents();
     pdl_wait();
     Walk k{p.total, p.pr[0].tiles, p.pr[1].tiles_n};
+    int used = 0;
     if (DYN) {   // (problems of one batch)
-        const int n = (__ldcg(rows) + 255) / 256;
+        used = __ldcg(step.rows);
+        const int n = (used + 255) / 256;
         k.tiles0 = n * p.pr[0].tiles_n;
         k.tiles_n1 = n;
         k.total = k.tiles0 + n * p.pr[1].tiles_m;
@@ -430,61 +432,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 // rows per instruction and stored in whole 128-byte rows.  (TMA tile stores
                 // from here queued in the TMA unit behind the producer's operand loads, and
                 // releasing the accumulator after the stores waited for them to land.)
-                char *const C = (char *)q.C;
+                char *C = (char *)q.C;
                 const long cbase = q.c_batch * w.batch, c_m = q.c_m;
-                const int row0 = w.m0 + 128 * (int)rank + quad * 32, M = q.M, N = q.N;
+                int row0 = w.m0 + 128 * (int)rank + quad * 32, M = q.M;
+                const int N = q.N;
+                const int rest = DYN && w.prob == 0 && row0 < used ? __ldcg(step.rest_of + row0 / 128) : -1;
                 const bool f16out = q.out_kind == 0;
                 const uint32_t sbuf0 = smem_u32(sC + (warp - 2) * 16384);
                 const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16) + a * 256;
-                __syncwarp();   // every lane has read the previous tile's buffers
-                uint32_t r[2][64];
-                if (ok) {
-                    tmem_ld32(tq, *reinterpret_cast<uint32_t(*)[32]>(&r[0][0]));
-                    tmem_ld32(tq + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[0][32]));
-                    tmem_ld_wait();
-                }
-#pragma unroll
-                for (int cc = 0; cc < 4; ++cc) {
-                    if (ok && cc < 3) {   // the next chunk's columns load while this one is packed
-                        tmem_ld32(tq + (cc + 1) * 64, *reinterpret_cast<uint32_t(*)[32]>(&r[(cc + 1) & 1][0]));
-                        tmem_ld32(tq + (cc + 1) * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[(cc + 1) & 1][32]));
-                    }
-                    uint32_t o[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float x0 = __uint_as_float(r[cc & 1][2 * i]), x1 = __uint_as_float(r[cc & 1][2 * i + 1]);
-                        o[i] = f16out ? pack_f16(x0, x1) : pack_bf16(x0, x1);
-                    }
-                    const uint32_t buf = sbuf0 + cc * 4096;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        st_shared_v4(buf + lane * 128 + ((j ^ (lane & 7)) << 4), o[4 * j], o[4 * j + 1], o[4 * j + 2],
-                                     o[4 * j + 3]);
-                    if (ok && cc < 3) tmem_ld_wait();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_peer(acc_empty0 + a * 8);
-                // 32-byte piece j of a 128-byte row per lane: eight rows per store instruction
-                const int j = lane & 3;
 #pragma unroll 1
-                for (int cc = 0; cc < 4 && ok; ++cc) {
-                    const int n = w.n0 + cc * 64;
-                    if (n >= N) break;
-                    const uint32_t buf = sbuf0 + cc * 4096;
-                    uint32_t v[4][8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int rr = 8 * i + (lane >> 2);
-                        const uint4 a0 = ld_shared_v4(buf + rr * 128 + (((2 * j) ^ (rr & 7)) << 4));
-                        const uint4 a1 = ld_shared_v4(buf + rr * 128 + (((2 * j + 1) ^ (rr & 7)) << 4));
-                        v[i][0] = a0.x, v[i][1] = a0.y, v[i][2] = a0.z, v[i][3] = a0.w;
-                        v[i][4] = a1.x, v[i][5] = a1.y, v[i][6] = a1.z, v[i][7] = a1.w;
+                for (int pass = 0; pass < (DYN ? 1 + (rest >= 0) : 1); ++pass) {   // (the second one: the rest)
+                    if (DYN && pass) {
+                        C = (char *)step.rest;
+                        row0 = rest * 128 + quad * 32;
+                        M = row0 + 32;
                     }
-                    char *dst = C + (cbase + (long)(row0 + (lane >> 2)) * c_m + n) * 2 + j * 32;
+                    __syncwarp();   // every lane has read the previous tile's buffers
+                    uint32_t r[2][64];
+                    if (ok) {
+                        tmem_ld32(tq, *reinterpret_cast<uint32_t(*)[32]>(&r[0][0]));
+                        tmem_ld32(tq + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[0][32]));
+                        tmem_ld_wait();
+                    }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (row0 + 8 * i + (lane >> 2) < M) st_global_v8(dst + (long)(8 * i) * c_m * 2, v[i]);
+                    for (int cc = 0; cc < 4; ++cc) {
+                        if (ok && cc < 3) {   // the next chunk's columns load while this one is packed
+                            tmem_ld32(tq + (cc + 1) * 64, *reinterpret_cast<uint32_t(*)[32]>(&r[(cc + 1) & 1][0]));
+                            tmem_ld32(tq + (cc + 1) * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[(cc + 1) & 1][32]));
+                        }
+                        uint32_t o[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float x0 = __uint_as_float(r[cc & 1][2 * i]), x1 = __uint_as_float(r[cc & 1][2 * i + 1]);
+                            o[i] = f16out ? pack_f16(x0, x1) : pack_bf16(x0, x1);
+                            if (DYN && pass) {
+                                const float2 f = __half22float2(*(const __half2 *)&o[i]);
+                                o[i] = pack_f16(x0 - f.x, x1 - f.y);
+                            }
+                        }
+                        const uint32_t buf = sbuf0 + cc * 4096;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            st_shared_v4(buf + lane * 128 + ((j ^ (lane & 7)) << 4), o[4 * j], o[4 * j + 1], o[4 * j + 2],
+                                         o[4 * j + 3]);
+                        if (ok && cc < 3) tmem_ld_wait();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0 && (!DYN || pass || rest < 0)) mbar_arrive_peer(acc_empty0 + a * 8);
+                    // 32-byte piece j of a 128-byte row per lane: eight rows per store instruction
+                    const int j = lane & 3;
+#pragma unroll 1
+                    for (int cc = 0; cc < 4 && ok; ++cc) {
+                        const int n = w.n0 + cc * 64;
+                        if (n >= N) break;
+                        const uint32_t buf = sbuf0 + cc * 4096;
+                        uint32_t v[4][8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int rr = 8 * i + (lane >> 2);
+                            const uint4 a0 = ld_shared_v4(buf + rr * 128 + (((2 * j) ^ (rr & 7)) << 4));
+                            const uint4 a1 = ld_shared_v4(buf + rr * 128 + (((2 * j + 1) ^ (rr & 7)) << 4));
+                            v[i][0] = a0.x, v[i][1] = a0.y, v[i][2] = a0.z, v[i][3] = a0.w;
+                            v[i][4] = a1.x, v[i][5] = a1.y, v[i][6] = a1.z, v[i][7] = a1.w;
+                        }
+                        char *dst = C + (cbase + (long)(row0 + (lane >> 2)) * c_m + n) * 2 + j * 32;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (row0 + 8 * i + (lane >> 2) < M) st_global_v8(dst + (long)(8 * i) * c_m * 2, v[i]);
+                    }
                 }
                 continue;
             }
@@ -552,9 +568,9 @@ int num_sms() {
     return n;
 }
 
-cudaError_t launch_gemm_pair(const CUtensorMap *maps, const GemmK &p, const int *rows, cudaStream_t st) {
+cudaError_t launch_gemm_pair(const CUtensorMap *maps, const GemmK &p, const GemmStep *step, cudaStream_t st) {
     const size_t sm = PST * (PA_BYTES + PB_BYTES) + PC_BYTES + 1024 + 256;
-    auto kern = rows ? tc_gemm_pair_kernel<true> : tc_gemm_pair_kernel<false>;
+    auto kern = step ? tc_gemm_pair_kernel<true> : tc_gemm_pair_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     if (e != cudaSuccess) return e;
     const int grid = 2 * std::min(p.total, num_sms() / 2);
@@ -568,7 +584,7 @@ cudaError_t launch_gemm_pair(const CUtensorMap *maps, const GemmK &p, const int 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p, rows);
+    return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p, step ? *step : GemmStep{});
 }
 
 template <int BN>
@@ -593,7 +609,7 @@ cudaError_t launch_gemm(const CUtensorMap *maps, const GemmK &p, cudaStream_t st
 
 }  // namespace
 
-cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaStream_t st, const int *rows) {
+cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaStream_t st, const GemmStep *step) {
     if (n_probs < 1 || n_probs > 2) return cudaErrorInvalidValue;
     int maxN = 0;
     for (int i = 0; i < n_probs; ++i) {
@@ -612,7 +628,7 @@ cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaS
         if (probs[i].B.rows_per_z % 128 != 0) pair = false;
     }
     if (BN == 256 && !pair) BN = 128;
-    if (rows && (!pair || n_probs != 2 || probs[0].batch != 1 || probs[1].batch != 1)) return cudaErrorInvalidValue;
+    if (step && (!pair || n_probs != 2 || probs[0].batch != 1 || probs[1].batch != 1)) return cudaErrorInvalidValue;
     const int TM = pair ? 256 : BM, TN = BN;
     CUtensorMap maps[4];
     GemmK p{};
@@ -660,7 +676,8 @@ cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaS
     switch (BN) {
         case 256:
             p.idesc = tc::idesc_f16(256, 256, f16);   // cta_group::2: M = 256 across the pair
-            return launch_gemm_pair(maps, p, rows, st);
+            if (step && !p.pr[0].c_stage) return cudaErrorInvalidValue;
+            return launch_gemm_pair(maps, p, step, st);
         case 128:
             p.idesc = tc::idesc_f16(BM, 128, f16, false, p.a_mn != 0);
             return launch_gemm<128>(maps, p, st);

@@ -48,9 +48,14 @@ cudaError_t tc_gemm(const TmaOperand &A, const TmaOperand &B, int M, int N, int 
                     bool accumulate = false);
 // One persistent launch over the tiles of one or two problems (same K, same operand
 // type): the explicit path's K_nope and V^T products share one launch.
-// `rows` (device memory, null: all): so many rows of problem 0 and columns of problem 1 only; two problems of one batch on
-// SM pairs (N >= 256).
-cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaStream_t st, const int *rows = nullptr);
+// With `step` (two problems of one batch on SM pairs, N >= 256): *rows (device memory) rows of problem 0 and columns of
+// problem 1 only; and what the rounding to fp16 leaves of the 128 rows i of problem 0, for those with rest_of[i] >= 0, to
+// rows 128 rest_of[i] .. of `rest` (fp16, row pitch c_m).
+struct GemmStep {
+    const int *rows, *rest_of;
+    void *rest;
+};
+cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaStream_t st, const GemmStep *step = nullptr);
 
 cudaError_t tc_gemm_read_and_clear_error(unsigned *flags, cudaStream_t st);
 cudaError_t tc_attn_read_and_clear_error(unsigned *flags, cudaStream_t st);
