@@ -1485,7 +1485,9 @@ mla_status mla_paged_weights(const mla_dims *dims, mla_dtype dtype, int B, int n
     return cuda_status(launch_paged_weights_out((long)pages, acc, bits, prior, page_weights, cs));
 }
 
-size_t mla_paged_evict_workspace(int B) { return B < 1 ? 0 : (size_t)B * 12 + 512; }
+size_t mla_paged_evict_workspace(int B, int max_pages) {
+    return B < 1 || max_pages < 1 ? 0 : align_up((size_t)B * 4, 256) + align_up((size_t)B * paged_evict_segments(max_pages) * 16, 256);
+}
 
 mla_status mla_paged_evict(int B, int page_size, int max_pages, int n_room, int keep_pages, int first_pages, int last_pages,
                            const int *kv_lens, const int *block_table, const float *page_weights, int *table_out,
@@ -1501,18 +1503,18 @@ mla_status mla_paged_evict(int B, int page_size, int max_pages, int n_room, int 
     for (const void *q : words)
         if (!aligned4(q)) return MLA_ERR_ALIGN;
     if (!aligned16(workspace)) return MLA_ERR_ALIGN;
-    if (workspace_bytes < mla_paged_evict_workspace(B)) return MLA_ERR_WORKSPACE;
+    if (workspace_bytes < mla_paged_evict_workspace(B, max_pages)) return MLA_ERR_WORKSPACE;
     const size_t e = 4, pages = (size_t)B * max_pages;
     Range in[] = {rng(kv_lens, B * e), rng(block_table, table_out == block_table ? 0 : pages * e),
                   rng(page_weights, weights_out == page_weights ? 0 : pages * e)};
     Range outs[] = {rng(table_out, pages * e), rng(weights_out, pages * e), rng(freed_pages, n_room * e), rng(counts, 2 * e),
-                    rng(workspace, mla_paged_evict_workspace(B))};
+                    rng(workspace, mla_paged_evict_workspace(B, max_pages))};
     mla_status st = check_alias(in, 3, outs, 5);
     if (st != MLA_OK) return st;
     Carve c;
     c.base = (char *)workspace;
-    uint2 *pick = (uint2 *)c.take(B * sizeof(uint2));
     int *gone = (int *)c.take(B * sizeof(int));
+    uint4 *pick = (uint4 *)c.take((size_t)B * paged_evict_segments(max_pages) * sizeof(uint4));
     g_last_path = 1;
     return cuda_status(launch_paged_evict(B, page_size, max_pages, n_room, keep_pages, first_pages, last_pages, kv_lens,
                                           block_table, page_weights, table_out, weights_out, freed_pages, counts, gone, pick,

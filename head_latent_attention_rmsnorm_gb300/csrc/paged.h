@@ -15,10 +15,11 @@ cudaError_t launch_paged_tables(int B, int page, int max_pages, int n_free, int 
                                 const int *fresh, const int *free_pages, int *table, int *kv_lens, int *cu, int *slots,
                                 int *positions, int *counts, cudaStream_t st);
 
-// gone [B], pick [B]: scratch.
+// gone [B], pick [B][segments]: scratch.
+int paged_evict_segments(int max_pages);
 cudaError_t launch_paged_evict(int B, int page, int max_pages, int room, int keep, int first, int last, const int *lens,
                                const int *table, const float *weights, int *table_out, float *weights_out, int *freed,
-                               int *counts, int *gone, uint2 *pick, cudaStream_t st);
+                               int *counts, int *gone, uint4 *pick, cudaStream_t st);
 
 // c rows at c + t * c_stride elements, k rows at k + t * k_stride.
 cudaError_t launch_paged_append(int ty, int T, long n_slots, int Dk, int Dr, float base, float eps, const void *c,
@@ -83,9 +84,9 @@ struct PagedStep {
     int B, n_tokens;
     const int *cu, *positions, *lens;
 };
-// Tokens of one round of the absorbed form: a step of more takes several (the partials are 128 KB a token at 128
-// heads).
-constexpr int PAGED_ROUND = 2048;
+// Tokens of one round of the absorbed form: a step of more takes several (queries and partials are 570 KB a token at 128
+// heads; a round costs four launches, of which a step whose tokens all go explicit has nothing).
+constexpr int PAGED_ROUND = 4096;
 // The plan of tokens s0 .. s0 + p.T - 1: their groups, and the division of the groups' tiles (p.lens, p.of,
 // p.limits, p.groups are written; p.B = p.T); n_zero words at `zero` are set to zero.
 cudaError_t launch_paged_plan(const PagedDecode &p, const PagedStep &s, int s0, int *lens, int2 *of, int *limits, int4 *groups,

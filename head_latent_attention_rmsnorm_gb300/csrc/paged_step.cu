@@ -17,7 +17,7 @@ using tc::pdl_wait;
 namespace {
 
 // -------------------------------------------------------------------------- plan ----
-// Block 0, two tokens a thread: a token's request by binary search of the prefix sums, the keys that
+// Block 0, four tokens a thread: a token's request by binary search of the prefix sums, the keys that
 // it sees; groups begin where a request's tokens do, where one is not computed here, and after every
 // `most` tokens; then the groups' tile sums and the workers' parts as for decode.
 constexpr int PNT = 1024, CU_NEAR = 4096;
@@ -77,10 +77,11 @@ __global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__
     }
     __syncthreads();
     // which tokens begin a group
-    const int i0 = 2 * tid;
-    int first[2], place[2];   // place: among the request's tokens of this round
+    constexpr int PER = PAGED_ROUND / PNT;
+    const int i0 = PER * tid;
+    int first[PER], place[PER];   // place: among the request's tokens of this round
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < PER; ++e) {
         const int i = i0 + e;
         first[e] = place[e] = 0;
         if (i >= T || req[i] < 0) continue;
@@ -93,8 +94,10 @@ __global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__
         place[e] = i - lo;
         first[e] = i == 0 || req[i - 1] != req[i] || place[e] % a.most == 0;
     }
-    int x = first[0] + first[1];
-    const int own = x;
+    int own = 0;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) own += first[e];
+    int x = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -109,7 +112,7 @@ __global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__
         all += warp_tot[i];
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < PER; ++e) {
         const int i = i0 + e;
         if (i >= T) continue;
         if (req[i] < 0) a.of[i] = make_int2(-1, 0);

@@ -341,6 +341,10 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
     const long pitch = (long)p.row_tile * (DK / 8);
     const bool paired = p.row_tile <= 64;
     bool ok = true;
+    if (p.list && tokens_of(p) == 0) {   // (the list's length is of a launch long ended)
+        pdl_wait();
+        return;
+    }
     if (tid == 0) {
         mbar_init(&v0.bar_w, 1);
         mbar_init(&v0.bar_d, 1);
@@ -719,6 +723,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     const PagedDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
+    if (p.list && tokens_of(p) == 0) {   // (the list's length is of a launch long ended)
+        pdl_wait();
+        return;
+    }
 
     if (warp == 0) {
         for (int i = lane; i < B_COUNT; i += 32) mbar_init(&bars[i], arrivals(i));

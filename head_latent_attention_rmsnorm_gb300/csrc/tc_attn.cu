@@ -153,6 +153,10 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
     tc_attn_kernel(const __grid_constant__ CUtensorMap mQn, const __grid_constant__ CUtensorMap mQr,
                    const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mKr,
                    const __grid_constant__ CUtensorMap mV, AttnK p, const __grid_constant__ CUtensorMap mR, StepK sp) {
+    if (STEP && __ldcg(sp.ctl + 1) == 0) {   // (of a launch that ended before the one in front began its work)
+        pdl_wait();
+        return;
+    }
     extern __shared__ uint8_t smem_raw[];
     constexpr uint32_t VBOX = Lay<STEP>::VBOX, V_SLOT = Lay<STEP>::V_SLOT, QS_BYTES = Lay<STEP>::QS_BYTES, T_Q = Lay<STEP>::T_Q;
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);

@@ -124,7 +124,7 @@ def lib() -> ctypes.CDLL:
         L.mla_paged_weights_workspace.restype = _sz
         L.mla_paged_evict.argtypes = [_i] * 7 + [_vp] * 8 + [_sz, _vp]
         L.mla_paged_evict.restype = _i
-        L.mla_paged_evict_workspace.argtypes = [_i]
+        L.mla_paged_evict_workspace.argtypes = [_i, _i]
         L.mla_paged_evict_workspace.restype = _sz
         L.mla_status_string.argtypes = [_i]
         L.mla_status_string.restype = ctypes.c_char_p
@@ -971,7 +971,7 @@ def paged_evict(kv_lens, block_table, page_weights, *, page_size, keep_pages, fi
     if counts is None:
         counts = torch.empty(2, dtype=i32, device=dev)
     if workspace is None:
-        workspace = torch.empty(lib().mla_paged_evict_workspace(B), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(lib().mla_paged_evict_workspace(B, max_pages), dtype=torch.uint8, device=dev)
     else:
         _workspace(0, dev, workspace)
     room = freed.numel()

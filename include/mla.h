@@ -401,7 +401,7 @@ mla_status mla_paged_evict(int B, int page_size, int max_pages, int n_room, int 
                            const int *kv_lens, const int *block_table, const float *page_weights, int *table_out,
                            float *weights_out, int *freed_pages, int *counts, void *workspace, size_t workspace_bytes,
                            void *cuda_stream);
-size_t mla_paged_evict_workspace(int B);
+size_t mla_paged_evict_workspace(int B, int max_pages);
 
 /* Workspace bytes the matching call needs (0 on invalid arguments). */
 size_t mla_latent_attn_workspace(const mla_dims *dims, mla_dtype dtype, int B, int s_q, int s_kv,

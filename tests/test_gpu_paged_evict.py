@@ -35,7 +35,8 @@ def same(a, b):
 @pytest.mark.parametrize("kinds", ["plain", "ties", "odd ties"])
 @pytest.mark.parametrize("B,cols,page,keep,first,last", [
     (1, 1, 16, 0, 0, 1), (1, 40, 8, 10, 0, 1), (7, 33, 64, 12, 2, 3), (5, 130, 7, 0, 0, 1), (3, 700, 16, 333, 1, 40),
-    (2, 5000, 16, 1000, 4, 64), (300, 20, 32, 7, 1, 2), (4, 20, 32, 100, 0, 1), (4, 20, 32, 3, 30, 1), (4, 20, 32, 3, 0, 30),
+    (2, 5000, 16, 1000, 4, 64), (300, 20, 32, 7, 1, 2), (3, 8192, 1, 4000, 0, 1),
+    (2, 8200, 4, 4001, 3, 9), (2, 30001, 2, 7000, 100, 17), (1, 66000, 3, 20000, 5, 64), (2, 70001, 1, 70000, 0, 1), (1, 140000, 1, 500, 0, 1), (4, 20, 32, 100, 0, 1), (4, 20, 32, 3, 30, 1), (4, 20, 32, 3, 0, 30),
 ])
 def test_against_a_plain_eviction(kinds, B, cols, page, keep, first, last):
     rng = random.Random(B * cols + keep)

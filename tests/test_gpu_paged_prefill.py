@@ -102,14 +102,15 @@ def test_one_token_a_request_is_decode(heads, dtype, page):
     assert float((lse - l2).abs().max()) <= 1e-5 and float((out.float() - o2.float()).abs().max()) <= 0.05
 
 
-@pytest.mark.parametrize("heads,dims,dtype", [(2, TINY, F32), (16, V3, BF), (128, V3, BF)])
-def test_more_tokens_than_a_round(heads, dims, dtype):
-    """4300 tokens: three rounds of the absorbed form; sampled rows against 64 bits, all rows finite."""
+@pytest.mark.parametrize("heads,dims,dtype,key_rows", [(2, TINY, F32, None), (16, V3, BF, None), (16, V3, BF, 0),
+                                                       (128, V3, BF, None), (128, V3, BF, 0)])
+def test_more_tokens_than_a_round(heads, dims, dtype, key_rows):
+    """4300 tokens: two rounds of the absorbed form; sampled rows against 64 bits, all rows finite."""
     d = mla.dims(heads, **dims)
     lens = [(5, 1), (0, 2100), (30, 60), (100, 2139)]
     s = sref.step(ref.generator(9), d, dtype, lens, 64, extra_rows=2)
     n = s["positions"].numel()
-    out, lse = call(d, s)
+    out, lse = call(d, s, key_rows=key_rows)
     assert bool(torch.isfinite(lse[:-2]).all()) and bool((lse[-2:] == 0).all()) and bool((out[-2:] == 0).all())
     rows = [0, 1, 2, 700, 2047, 2048, 2049, 2100, 2101, 2130, 2160, 2161, 2162, 4095, 4096, 4097, n - 3]
     want = sref.prefill(d, dict(s, **sample(s, rows)))

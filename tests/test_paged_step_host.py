@@ -142,7 +142,8 @@ def test_workspace_queries():
     assert none == f(900, 64, 100, 255, 16) < f(900, 64, 100, 4096, 16) < f(900, 64, 100, 4096, 0) == f(900, 64, 100, 4097, 999)
     assert f(900, 64, 100, -1, 16) == 0 == f(900, 64, 100, 4096, -1)
     assert f(900, 60, 100, 4096, 16) == f(900, 60, 100, 0, 16)   # pages that the tensor cores do not take
-    assert mla.mla_paged_evict_workspace(0) == 0 < mla.mla_paged_evict_workspace(3) < mla.mla_paged_evict_workspace(9000)
+    f = mla.mla_paged_evict_workspace
+    assert f(0, 9) == 0 == f(3, 0) < f(3, 9) < f(9000, 9) < f(9000, 70000)
 
 
 # ---------------------------------------------------------------------- binding ----
