@@ -102,7 +102,7 @@ __device__ __forceinline__ int request_of(const PagedDecode &p, const I *off, lo
 
 // The parts begin where a worker's share begins and where an item does (one may be both): a thread per
 // beginning finds its part's worker, item and end.
-template <int NT, typename I>
+template <int NT, bool STEP, typename I>
 __device__ void plan_parts(const PagedDecode &p, const I *off, long total) {
     const long q = share_of(p, total);
     const long items = (long)p.B * p.row_tiles;
@@ -136,7 +136,7 @@ __device__ void plan_parts(const PagedDecode &p, const I *off, long total) {
         }
         const long i0 = o * p.row_tiles + rt * per, i1 = i0 + per, end = min((c + 1) * q, total), t1 = min(end, i1);
         const int item = b * p.row_tiles + rt;
-        const int4 g = p.groups ? p.groups[b] : make_int4(b, b * p.H, p.H, 0);
+        const int4 g = STEP ? p.groups[b] : make_int4(b, b * p.H, p.H, 0);
         PagedPart x{};
         x.row = g.x;
         x.q = g.y + rt * p.row_tile;
@@ -159,7 +159,7 @@ __device__ void plan_parts(const PagedDecode &p, const I *off, long total) {
 
 // The tile prefix sums of all groups and the workers' parts, by one block of NT threads; `room`
 // ints of shared memory keep the sums at hand where they fit.
-template <int NT>
+template <int NT, bool STEP>
 __device__ void plan_block(const PagedDecode &p, int *sm = nullptr, int room = 0) {
     __shared__ long warp_tot[NT / 32];
     const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
@@ -196,8 +196,8 @@ __device__ void plan_block(const PagedDecode &p, int *sm = nullptr, int room = 0
     }
     if (!p.parts) return;
     __syncthreads();
-    if (near) plan_parts<NT>(p, sm, carry * p.row_tiles);
-    else plan_parts<NT>(p, p.tile_off, carry * p.row_tiles);
+    if (near) plan_parts<NT, STEP>(p, sm, carry * p.row_tiles);
+    else plan_parts<NT, STEP>(p, p.tile_off, carry * p.row_tiles);
 }
 
 // Started early, behind the kernel in front of it (programmatic dependent launch): the kernel waits for that one's

@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(NT) paged_absorb_simt_kernel(const __grid_cons
     if (!step) pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x == 0) {
-        if (!step) plan_block<NT>(p);
+        if (!step) plan_block<NT, false>(p);
         else pdl_wait();
         return;
     }

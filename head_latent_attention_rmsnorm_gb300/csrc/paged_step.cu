@@ -17,10 +17,11 @@ using tc::pdl_wait;
 namespace {
 
 // -------------------------------------------------------------------------- plan ----
-// Block 0, four tokens a thread: a token's request by binary search of the prefix sums, the keys that
+// Block 0 of NT threads, PER tokens each: a token's request by binary search of the prefix sums, the keys that
 // it sees; groups begin where a request's tokens do, where one is not computed here, and after every
 // `most` tokens; then the groups' tile sums and the workers' parts as for decode.
 constexpr int PNT = 1024, CU_NEAR = 4096;
+constexpr int FEW = 128, SOME = 512;   // tokens up to which a block of as many threads is enough (fewer warps to bring together)
 
 struct Plan {
     PagedDecode p;
@@ -33,31 +34,33 @@ struct Plan {
     long n_zero;
 };
 
-__global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__ Plan a) {
+template <int NT, int PER>
+__global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ Plan a) {
     extern __shared__ int sm[];
-    __shared__ int warp_tot[PNT / 32];
+    __shared__ int warp_tot[NT / 32];
+    constexpr int MOST = NT * PER;
     const PagedDecode &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
-    int *lim = sm, *req = lim + PAGED_ROUND, *sums = req + PAGED_ROUND, *tok = sums + PAGED_ROUND + 1, *near = tok + PAGED_ROUND;
+    int *lim = sm, *req = lim + MOST, *sums = req + MOST, *tok = sums + MOST + 1, *near = tok + MOST;
     pdl_wait();
     pdl_launch_dependents();   // the absorb beside this; what follows it waits for both
     if (blockIdx.x > 0) {
-        for (long i = (long)(blockIdx.x - 1) * PNT + tid; i < a.n_zero; i += (long)(gridDim.x - 1) * PNT) a.zero[i] = 0;
+        for (long i = (long)(blockIdx.x - 1) * NT + tid; i < a.n_zero; i += (long)(gridDim.x - 1) * NT) a.zero[i] = 0;
         return;
     }
     const int T = tokens_of(p);
     if (p.list && T == 0) {   // (the join has no token to look anything up for)
-        for (int i = tid; i < 2 * p.workers; i += PNT) p.first[i] = 0;
+        for (int i = tid; i < 2 * p.workers; i += NT) p.first[i] = 0;
         return;
     }
     const bool here = a.s.B < CU_NEAR;
     if (here) {
-        for (int i = tid; i <= a.s.B; i += PNT) near[i] = a.s.cu[i];
+        for (int i = tid; i <= a.s.B; i += NT) near[i] = a.s.cu[i];
         __syncthreads();
     }
     const int *cu = here ? near : a.s.cu;
     const int cap = p.max_pages * p.page;
-    for (int i = tid; i < T; i += PNT) {
+    for (int i = tid; i < T; i += NT) {
         const int t = p.list ? __ldcg(p.list + i) : a.s0 + i;
         int lo = 0, hi = a.s.B;   // the first request whose tokens end behind t
         while (lo < hi) {
@@ -77,7 +80,6 @@ __global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__
     }
     __syncthreads();
     // which tokens begin a group
-    constexpr int PER = PAGED_ROUND / PNT;
     const int i0 = PER * tid;
     int first[PER], place[PER];   // place: among the request's tokens of this round
 #pragma unroll
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__
     __syncthreads();
     int g = x - own, all = 0;
 #pragma unroll
-    for (int i = 0; i < PNT / 32; ++i) {
+    for (int i = 0; i < NT / 32; ++i) {
         if (i < wp) g += warp_tot[i];
         all += warp_tot[i];
     }
@@ -128,16 +130,17 @@ __global__ void __launch_bounds__(PNT) paged_plan_kernel(const __grid_constant__
         a.lens[g] = most;
         ++g;
     }
-    for (int i = all + tid; i < p.B; i += PNT) {
+    for (int i = all + tid; i < p.B; i += NT) {
         a.lens[i] = 0;
         a.groups[i] = make_int4(0, 0, 0, 0);
     }
     __syncthreads();
-    if (p.parts) plan_block<PNT>(p, sums, PAGED_ROUND + 1);
-    else plan_block<PNT>(p);
+    if (p.parts) plan_block<NT, true>(p, sums, MOST + 1);
+    else plan_block<NT, true>(p);
 }
 
-// The sum of the values of the threads in front, and of all, by a block of PNT threads.
+// The sum of the values of the threads in front, and of all, by a block of NT threads.
+template <int NT>
 __device__ long block_before(long n, long *warp_tot, long &all) {
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     long x = n;
@@ -152,7 +155,7 @@ __device__ long block_before(long n, long *warp_tot, long &all) {
     long before = x - n;
     all = 0;
 #pragma unroll
-    for (int i = 0; i < PNT / 32; ++i) {
+    for (int i = 0; i < NT / 32; ++i) {
         if (i < wp) before += warp_tot[i];
         all += warp_tot[i];
     }
@@ -171,15 +174,16 @@ struct Chunk {
     int cap, key_rows;
 };
 
-__global__ void __launch_bounds__(PNT) paged_chunk_kernel(const __grid_constant__ Chunk a) {
-    __shared__ long warp_tot[PNT / 32];
+template <int NT>
+__global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__ Chunk a) {
+    __shared__ long warp_tot[NT / 32];
     __shared__ int weight[CHUNK_SORT];
     const int tid = threadIdx.x, lane = tid & 31, N = a.s.n_tokens;
     pdl_wait();
     pdl_launch_dependents();
-    for (int i = tid; i < N; i += PNT) a.c.done[i] = 0;
+    for (int i = tid; i < N; i += NT) a.c.done[i] = 0;
     long rows = 0, tiles = 0, used = 0, rests = 0;
-    for (int b0 = 0; b0 < a.s.B; b0 += PNT) {
+    for (int b0 = 0; b0 < a.s.B; b0 += NT) {
         const int b = b0 + tid;
         int t0 = 0, n = 0, keys = 0;
         if (b < a.s.B) {
@@ -190,16 +194,16 @@ __global__ void __launch_bounds__(PNT) paged_chunk_kernel(const __grid_constant_
         const bool may = min(n, keys) >= CHUNK_MIN;
         const long need = may ? (keys + 127l) / 128 * 128 : 0;
         long all;
-        const long r0 = rows + block_before(need, warp_tot, all);
+        const long r0 = rows + block_before<NT>(need, warp_tot, all);
         rows += all;
         const bool fits = may && r0 + need <= a.key_rows;
         const int mine = fits ? (n + 127) / 128 : 0;
-        const long e0 = tiles + block_before(mine, warp_tot, all);
+        const long e0 = tiles + block_before<NT>(mine, warp_tot, all);
         tiles += all;
-        block_before(fits ? need : 0, warp_tot, all);   // (those that fit are the first of those that may)
+        block_before<NT>(fits ? need : 0, warp_tot, all);   // (those that fit are the first of those that may)
         used += all;
         int rest = fits ? (int)min(need / 128, (long)CHUNK_RESTS) : 0;
-        const long p0 = rests + block_before(rest, warp_tot, all);
+        const long p0 = rests + block_before<NT>(rest, warp_tot, all);
         rests += all;
         if (p0 + rest > a.c.max_rests) rest = 0;   // (only where cu decreases)
         if (b < a.s.B) {
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(PNT) paged_chunk_kernel(const __grid_constant_
     __syncthreads();
     const int n = (int)min(tiles, (long)a.c.max_tiles);
     const bool sorted = n <= CHUNK_SORT;
-    for (int e = tid >> 5; e < n; e += PNT / 32) {
+    for (int e = tid >> 5; e < n; e += NT / 32) {
         const StepTile x = a.c.raw[e];
         const int keys = min(max(a.s.lens[x.request], 0), a.cap);
         int most = 0;
@@ -250,11 +254,11 @@ __global__ void __launch_bounds__(PNT) paged_chunk_kernel(const __grid_constant_
     __syncthreads();
     // the tiles that have keys here, the heaviest first (a step of more than CHUNK_SORT tiles as they come)
     long out = 0;
-    for (int base = 0; base < n; base += PNT) {
+    for (int base = 0; base < n; base += NT) {
         const int e = base + tid;
         StepTile x{};
         if (e < n) x = a.c.raw[e];
-        long all, at = out + block_before(x.tiles > 0, warp_tot, all);
+        long all, at = out + block_before<NT>(x.tiles > 0, warp_tot, all);
         out += all;
         if (x.tiles == 0) continue;
         if (sorted) {
@@ -266,14 +270,14 @@ __global__ void __launch_bounds__(PNT) paged_chunk_kernel(const __grid_constant_
     // the requests' other tokens, eight neighbours a thread
     long listed = 0;
     const int first = min(max(a.s.cu[0], 0), N), last = min(max(a.s.cu[a.s.B], 0), N);
-    for (int base = first; base < last; base += 8 * PNT) {
+    for (int base = first; base < last; base += 8 * NT) {
         const int t0 = base + 8 * tid;
         int mine = 0;   // (mask)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (t0 + i < last && !a.c.done[t0 + i]) mine |= 1 << i;
         long all;
-        int *at = a.c.list + listed + block_before(__popc(mine), warp_tot, all);
+        int *at = a.c.list + listed + block_before<NT>(__popc(mine), warp_tot, all);
         listed += all;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -385,7 +389,9 @@ cudaError_t launch_paged_chunk(const PagedDecode &p, const PagedStep &s, const P
     {
         const Chunk a{s, c, p.max_pages * p.page, c.key_rows};
         ProfScope ps("paged_chunk", st);
-        if ((e = launch_after(paged_chunk_kernel, 1, PNT, 0, st, a)) != cudaSuccess) return e;
+        const bool few = s.n_tokens <= 2048 && s.B <= 256;   // few warps come together sooner
+        auto kern = few ? paged_chunk_kernel<256> : paged_chunk_kernel<PNT>;
+        if ((e = launch_after(kern, 1, few ? 256 : PNT, 0, st, a)) != cudaSuccess) return e;
     }
     Gather g{p, s, c, divisor(p.page), {}};
     std::copy_n(paged_turns(p.base, p.Dr), 32, g.turns.v);
@@ -396,13 +402,15 @@ cudaError_t launch_paged_chunk(const PagedDecode &p, const PagedStep &s, const P
 cudaError_t launch_paged_plan(const PagedDecode &p, const PagedStep &s, int s0, int *lens, int2 *of, int *limits, int4 *groups,
                               cudaStream_t st, unsigned long long *zero, long n_zero) {
     Plan a{p, s, s0, std::max(1, p.row_tile / p.H), lens, limits, of, groups, zero, n_zero};
-    const size_t sm = (4 * PAGED_ROUND + 1 + (s.B < CU_NEAR ? s.B + 1 : 0)) * sizeof(int);
+    const unsigned nt = p.T <= FEW ? FEW : p.T <= SOME ? SOME : PNT;
+    auto kern = nt == FEW ? paged_plan_kernel<FEW, 1> : nt == SOME ? paged_plan_kernel<SOME, 1> : paged_plan_kernel<PNT, PAGED_ROUND / PNT>;
+    const size_t sm = (4 * (nt < PNT ? (int)nt : PAGED_ROUND) + 1 + (s.B < CU_NEAR ? s.B + 1 : 0)) * sizeof(int);
     if (sm > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
         if (e != cudaSuccess) return e;
     }
     ProfScope ps("paged_plan", st);
-    return launch_after(paged_plan_kernel, 1 + (unsigned)std::min((n_zero + PNT - 1) / PNT, 150l), PNT, sm, st, a);
+    return launch_after(kern, 1 + (unsigned)std::min((n_zero + nt - 1) / nt, 150l), nt, sm, st, a);
 }
 
 }  // namespace mla

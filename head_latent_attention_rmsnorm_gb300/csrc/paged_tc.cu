@@ -153,14 +153,15 @@ struct Absorb {
 };
 
 // The queries' rotation: a warp per token and 32 heads, a lane per pair of dims, the angle formed once.
+template <bool STEP>
 __device__ void rotate_queries(const Absorb &a, int i, int lane) {
     const PagedDecode &p = a.p;
     const int per = (p.H + 31) / 32, b = i / per, h0 = i % per * 32;
-    if (b >= tokens_of(p)) return;
-    const int t = token_of(p, b);
+    if (b >= (STEP ? tokens_of(p) : p.B)) return;
+    const int t = STEP ? token_of(p, b) : b;
     // (a step's tokens may see few keys whatever their position)
-    const int keys = p.scores_only ? 2147483647 : p.pos ? 0 : keys_of(p, b);
-    const float2 cs = turn_cs(a.turns.v[lane], p.pos ? p.pos[t] : keys - 1);
+    const int keys = !STEP ? keys_of(p, b) : p.scores_only ? 2147483647 : 0;
+    const float2 cs = turn_cs(a.turns.v[lane], STEP ? p.pos[t] : keys - 1);
     const int h1 = min(h0 + 32, p.H);
 #pragma unroll 1
     for (int h = h0; h < h1; h += 8) {
@@ -190,33 +191,33 @@ __device__ void rotate_queries(const Absorb &a, int i, int lane) {
     }
 }
 
+template <bool STEP>
 __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_constant__ Absorb a) {
     extern __shared__ __align__(1024) uint8_t sm[];
     const PagedDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // A step's plan is the launch in front and runs beside this one (it began behind the end of all before it,
     // and nothing here reads what it writes): the wait for it is at each block's end, for the launch behind.
-    const bool step = p.pos != nullptr;
-    if (!step) pdl_wait();
+    if (!STEP) pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x == 0) {
-        if (!step) plan_block<128>(p, (int *)sm, AB_SMEM / 4);
+        if (!STEP) plan_block<128, false>(p, (int *)sm, AB_SMEM / 4);
         else pdl_wait();
         return;
     }
     if ((int)blockIdx.x <= a.rot_blocks) {
-        rotate_queries(a, ((int)blockIdx.x - 1) * 4 + warp, lane);
-        if (step) pdl_wait();
+        rotate_queries<STEP>(a, ((int)blockIdx.x - 1) * 4 + warp, lane);
+        if (STEP) pdl_wait();
         return;
     }
     uint8_t *sq = sm + DN * AB_PITCH;
-    const int T = tokens_of(p);
+    const int T = STEP ? tokens_of(p) : p.B;
     int u = (int)blockIdx.x - 1 - a.rot_blocks;
     const int dc = u & 3;
     u >>= 2;
     const int h = u / a.blocks;
     int b0 = u % a.blocks * a.group;
-    if (b0 >= T) {
+    if (STEP && b0 >= T) {
         pdl_wait();
         return;
     }
@@ -225,13 +226,16 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
     auto load = [&](int nb) {
         for (int i = tid; i < nb * 16; i += 128)
             cp16(sq + (i >> 4) * AB_PITCH + (i & 15) * 16,
-                 (const bf16 *)p.q_nope + ((long)token_of(p, b0 + (i >> 4)) * p.H + h) * DN + (i & 15) * 8);
-        if (tid < nb) keys[tid] = p.scores_only ? 2147483647 : step ? 0 : keys_of(p, b0 + tid);
+                 (const bf16 *)p.q_nope + ((long)(STEP ? token_of(p, b0 + (i >> 4)) : b0 + (i >> 4)) * p.H + h) * DN + (i & 15) * 8);
+    };
+    auto set_keys = [&](int nb) {
+        if (tid < nb) keys[tid] = !STEP ? keys_of(p, b0 + tid) : p.scores_only ? 2147483647 : 0;
     };
     load(min(a.group, T - b0));
 #pragma unroll 4
     for (int i = tid; i < DN * (AB_DIMS / 8); i += 128)
         cp16(sm + (i >> 4) * AB_PITCH + (i & 15) * 16, w + (long)(i >> 4) * DK + (i & 15) * 8);
+    set_keys(min(a.group, T - b0));   // (behind the copies: it waits for its own load)
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     uint32_t A[2][8][4];
@@ -286,13 +290,14 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
             __syncwarp();
         }
         b0 += a.blocks * a.group;
-        if (b0 >= T) break;
+        if (!STEP || b0 >= T) break;
         __syncthreads();   // the group has been read
         load(min(a.group, T - b0));
+        set_keys(min(a.group, T - b0));
         asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
         __syncthreads();
     }
-    if (step) pdl_wait();
+    if (STEP) pdl_wait();
 }
 
 // -------------------------------------------------------------------------- join ----
@@ -322,6 +327,7 @@ constexpr int JSMEM = JV + sizeof(JoinVars);
 static_assert(2 * 8 * JBLK >= 16 * 2 * DK * 4 && 2 * JB * JMAXC >= JB * 132, "the join's exchanges");
 static_assert(PAGED_TC_WORKERS <= JMAXC && JMAXC <= 96, "parts of an item");
 
+template <bool STEP>
 __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_constant__ CUtensorMap mW,
                                                                const __grid_constant__ PagedDecode p, const bf16 *qlo,
                                                                const bf16 *qrest, int per_head) {
@@ -337,11 +343,11 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
     uint8_t *so = sm + JO;
     float (*sw)[JB][JMAXC] = (float (*)[JB][JMAXC])(sm + JW);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x / per_head;
+    const int h = blockIdx.x / per_head, rt0 = h / p.row_tile, r0 = h % p.row_tile;   // (decode's; a step's vary by token)
     const long pitch = (long)p.row_tile * (DK / 8);
     const bool paired = p.row_tile <= 64;
     bool ok = true;
-    if (p.list && tokens_of(p) == 0) {   // (the list's length is of a launch long ended)
+    if (STEP && p.list && tokens_of(p) == 0) {   // (the list's length is of a launch long ended)
         pdl_wait();
         return;
     }
@@ -364,11 +370,14 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
     const uint32_t tmem = v0.tslot;
     pdl_wait();
     uint32_t ph = 0;
-    const int T = tokens_of(p);
+    const int T = STEP ? tokens_of(p) : p.B;
 #pragma unroll 1
-    for (int b0 = (int)(blockIdx.x % per_head) * JB; b0 < T; b0 += per_head * JB) {
+    for (int b0 = (int)(blockIdx.x % per_head) * JB; b0 < T; b0 += per_head * JB, ph ^= 1) {
         const int nb = min(JB, T - b0);
-        if (p.of && __syncthreads_and(tid >= nb || __ldcg(&p.of[b0 + tid].x) < 0)) continue;
+        if (STEP && __syncthreads_and(tid >= nb || __ldcg(&p.of[b0 + tid].x) < 0)) {
+            ph ^= 1;   // (no phase of this turn's)
+            continue;
+        }
         const int d8 = tid & 63, q16 = tid >> 6;
         const bool few = nb <= 2;                                // the groups share out parts, not requests
         const int j0 = few ? 0 : q16, dj = few ? 1 : 16, c0 = few ? q16 : 0, dc = few ? 16 : 1;
@@ -379,15 +388,15 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
             ql[i] = j < nb && !paired ? __ldcg((const uint4 *)(qlo + ((long)(b0 + j) * p.H + h) * DK) + d8) : make_uint4(0, 0, 0, 0);
         }
         {   // a warp per request: the weights of its parts (up to 96)
-            int s0 = 0, n = 0, ex = EX_NONE, r = 0;
+            int s0 = 0, n = 0, ex = EX_NONE, r = r0;
             bool here = true;
             if (warp < nb) {
-                const int2 of = p.of ? __ldcg(p.of + b0 + warp) : make_int2(b0 + warp, 0);
-                here = of.x >= 0;
+                const int2 of = STEP ? __ldcg(p.of + b0 + warp) : make_int2(b0 + warp, 0);
+                here = !STEP || of.x >= 0;
                 if (here) {
                     ex = extra_of(paired, keys_of(p, of.x));
-                    const int rt = (of.y + h) / p.row_tile;
-                    r = (of.y + h) % p.row_tile;
+                    const int rt = STEP ? (of.y + h) / p.row_tile : rt0;
+                    if (STEP) r = (of.y + h) % p.row_tile;
                     const int2 sp = __ldcg(p.spans + (long)of.x * p.row_tiles + rt);
                     s0 = sp.x;
                     n = sp.y;
@@ -424,8 +433,10 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
                 sc[warp][0] = s0;
                 sc[warp][1] = here ? n : -1;
                 sc[warp][2] = ex;
-                sc[warp][3] = r;
-                v0.tok[warp] = warp < nb ? token_of(p, b0 + warp) : 0;
+                if (STEP) {
+                    sc[warp][3] = r;
+                    v0.tok[warp] = warp < nb ? token_of(p, b0 + warp) : 0;
+                }
                 sl[warp] = s == 0.f ? -INFINITY : m + logf(s);
             }
         }
@@ -437,7 +448,7 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int j = j0 + dj * i;
-                src[i] = (const uint4 *)(p.po + ((long)sc[j][0] * p.row_tile + sc[j][3]) * DK) + d8;
+                src[i] = (const uint4 *)(p.po + ((long)sc[j][0] * p.row_tile + (STEP ? sc[j][3] : r0)) * DK) + d8;
                 n[i] = sc[j][1];
             }
             const float *wt = sw[d8 >> 5][j0];
@@ -516,7 +527,7 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
         tc_fence_before();
         __syncthreads();
         // (no keys: -inf stays, whatever the queries of a padded request hold; 0 * NaN is not added)
-        if (tid < nb && sc[tid][1] >= 0) p.lse[(long)v0.tok[tid] * p.H + h] = sl[tid] == -INFINITY ? sl[tid] : sl[tid] + p.scale * (sd[0][tid] + sd[1][tid]);
+        if (tid < nb && (!STEP || sc[tid][1] >= 0)) p.lse[(long)(STEP ? v0.tok[tid] : b0 + tid) * p.H + h] = sl[tid] == -INFINITY ? sl[tid] : sl[tid] + p.scale * (sd[0][tid] + sd[1][tid]);
         if (warp == 0) {
             ok = __all_sync(FULL, ok && mbar_wait(&v0.bar_w, 0, (volatile int *)&v0.abort, &g_paged_tc_err));   // W_V is here
             tc_fence_after();
@@ -546,12 +557,11 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
             for (int j = 0; j < JB; ++j) ss[j * 132 + tid] = __uint_as_float(v[j]);
         }
         __syncthreads();
-        if (warp < nb && sc[warp][1] >= 0) {   // (an abandoned wait leaves rubbish here, and the error word)
+        if (warp < nb && (!STEP || sc[warp][1] >= 0)) {   // (an abandoned wait leaves rubbish here, and the error word)
             const float4 v = *(const float4 *)(ss + warp * 132 + lane * 4);
-            *(uint2 *)((bf16 *)p.out + ((long)v0.tok[warp] * p.H + h) * DV + lane * 4) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+            *(uint2 *)((bf16 *)p.out + ((long)(STEP ? v0.tok[warp] : b0 + warp) * p.H + h) * DV + lane * 4) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
         }
         __syncthreads();
-        ph ^= 1;
     }
     if (warp == 1) tmem_dealloc(tmem, 32);
 }
@@ -705,8 +715,8 @@ __device__ void settle() {   // after an abandoned wait: loads in flight land be
 }
 
 // PAIRED (items of up to 64 rows): the rows behind the heads, 64 on, carry the queries' low halves in the scores and P's
-// in the values.
-template <int UNIT, bool PAIRED>
+// in the values.  STEP: the tokens of a step, whose rows see each its own number of the group's keys.
+template <int UNIT, bool PAIRED, bool STEP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     paged_attn_tc_kernel(const __grid_constant__ Maps m, const __grid_constant__ Attn a) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -723,7 +733,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     const PagedDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
-    if (p.list && tokens_of(p) == 0) {   // (the list's length is of a launch long ended)
+    if (STEP && p.list && tokens_of(p) == 0) {   // (the list's length is of a launch long ended)
         pdl_wait();
         return;
     }
@@ -886,7 +896,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 // a warp without a row only keeps the barriers
                 const bool act = (paired ? quad & 1 : quad) * 32 < w.rows;
                 // keys that this row sees: a step's token not all of its group's
-                const int lim = p.limits && head < w.rows ? __ldcg(p.limits + (w.q + head) / p.H) : w.keys;
+                const int lim = STEP && head < w.rows ? __ldcg(p.limits + (w.q + head) / p.H) : w.keys;
                 // whether every page of the part has an id inside the cache
                 bool sound = true;
                 {
@@ -1430,11 +1440,26 @@ Absorb absorb_of(const PagedDecode &p) {
 
 cudaError_t paged_absorb_tc(const PagedDecode &p, cudaStream_t st) {
     const Absorb ab = absorb_of(p);
-    const cudaError_t e = cudaFuncSetAttribute(paged_absorb_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM);
+    auto kern = p.groups ? paged_absorb_tc_kernel<true> : paged_absorb_tc_kernel<false>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM);
     if (e != cudaSuccess) return e;
     ProfScope ps("paged_absorb", st);
-    return launch_after(paged_absorb_tc_kernel, (unsigned)(p.H * 4 * ab.blocks + 1 + ab.rot_blocks), 128, AB_SMEM, st, ab);
+    return launch_after(kern, (unsigned)(p.H * 4 * ab.blocks + 1 + ab.rot_blocks), 128, AB_SMEM, st, ab);
 }
+
+namespace {
+template <bool STEP>
+auto attn_kernel(int unit, bool paired) {
+    return paired ? (unit == 64   ? paged_attn_tc_kernel<64, true, STEP>
+                     : unit == 32 ? paged_attn_tc_kernel<32, true, STEP>
+                     : unit == 16 ? paged_attn_tc_kernel<16, true, STEP>
+                                  : paged_attn_tc_kernel<8, true, STEP>)
+                  : (unit == 64   ? paged_attn_tc_kernel<64, false, STEP>
+                     : unit == 32 ? paged_attn_tc_kernel<32, false, STEP>
+                     : unit == 16 ? paged_attn_tc_kernel<16, false, STEP>
+                                  : paged_attn_tc_kernel<8, false, STEP>);
+}
+}  // namespace
 
 cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     using ull = unsigned long long;
@@ -1473,7 +1498,8 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     at.scale_log2 = p.scale * 1.4426950408889634f;
     at.idesc_s = idesc_f16(128, NK, false);
     at.idesc_pv = idesc_f16(128, 256, false, true);
-    if ((e = cudaFuncSetAttribute(paged_join_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, JSMEM)) != cudaSuccess) return e;
+    auto join = p.groups ? paged_join_tc_kernel<true> : paged_join_tc_kernel<false>;
+    if ((e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, JSMEM)) != cudaSuccess) return e;
     CUtensorMap mW;
     {
         const ull d[2] = {DK, (ull)p.H * (DN + DV)}, s[1] = {DK * 2};
@@ -1481,14 +1507,7 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
         if ((e = make_tma_map(&mW, p.w, 2, d, s, b)) != cudaSuccess) return e;
     }
     const int per_head = std::max(1, std::min((p.T + JB - 1) / JB, 2 * p.workers / p.H));   // one wave of join blocks
-    auto attn = p.row_tile <= 64 ? (unit == 64   ? paged_attn_tc_kernel<64, true>
-                             : unit == 32 ? paged_attn_tc_kernel<32, true>
-                             : unit == 16 ? paged_attn_tc_kernel<16, true>
-                                          : paged_attn_tc_kernel<8, true>)
-                          : (unit == 64   ? paged_attn_tc_kernel<64, false>
-                             : unit == 32 ? paged_attn_tc_kernel<32, false>
-                             : unit == 16 ? paged_attn_tc_kernel<16, false>
-                                          : paged_attn_tc_kernel<8, false>);
+    auto attn = p.groups ? attn_kernel<true>(unit, p.row_tile <= 64) : attn_kernel<false>(unit, p.row_tile <= 64);
     if ((e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess)
         return e;
     if ((e = paged_absorb_tc(p, st)) != cudaSuccess) return e;
@@ -1499,7 +1518,7 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     {
         ProfScope ps("paged_join", st);
-        e = launch_after(paged_join_tc_kernel, (unsigned)(p.H * per_head), JNT, JSMEM, st, mW, p, (const bf16 *)ab.qlo,
+        e = launch_after(join, (unsigned)(p.H * per_head), JNT, JSMEM, st, mW, p, (const bf16 *)ab.qlo,
                          (const bf16 *)ab.qrest, per_head);
     }
     return e;

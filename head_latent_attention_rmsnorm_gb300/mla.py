@@ -945,6 +945,11 @@ class PagedEvicted(NamedTuple):
     counts: torch.Tensor   # [2] pages evicted, pages that were to be
 
 
+@functools.lru_cache(maxsize=256)
+def _evict_workspace_bytes(B: int, max_pages: int) -> int:
+    return lib().mla_paged_evict_workspace(B, max_pages)
+
+
 def paged_evict(kv_lens, block_table, page_weights, *, page_size, keep_pages, first_pages=0, last_pages=1, table_out=None,
                 weights_out=None, freed=None, counts=None, workspace=None, stream=None) -> PagedEvicted:
     """Evict the pages of least ``page_weights`` [B, max_pages] (fp32) from the requests that hold more than
@@ -971,7 +976,7 @@ def paged_evict(kv_lens, block_table, page_weights, *, page_size, keep_pages, fi
     if counts is None:
         counts = torch.empty(2, dtype=i32, device=dev)
     if workspace is None:
-        workspace = torch.empty(lib().mla_paged_evict_workspace(B, max_pages), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(_evict_workspace_bytes(B, max_pages), dtype=torch.uint8, device=dev)
     else:
         _workspace(0, dev, workspace)
     room = freed.numel()
