@@ -94,7 +94,7 @@ cudaError_t launch_paged_plan(const PagedDecode &p, const PagedStep &s, int s0, 
 
 // The explicit form of the requests with many tokens (tensor cores), CHUNK_MIN and more.  Tiles of 128 tokens: at most
 // n_tokens / 128 and one more a request.  CHUNK_RESTS: tiles of 128 keys that have the rest of K_nope.
-constexpr int CHUNK_MIN = 160, CHUNK_RESTS = 4, CHUNK_SORT = 2048;
+constexpr int CHUNK_MIN = 64, CHUNK_RESTS = 4, CHUNK_SORT = 2048;
 struct PagedChunk {
     int key_rows;                // rows of the key buffers, a multiple of 256
     int max_tiles, max_rests;    // tiles of 128 tokens; tiles of 128 keys with a rest

@@ -165,8 +165,12 @@ __device__ long block_before(long n, long *warp_tot, long &all) {
 // ----------------------------------------------------------------- explicit plan ----
 // Which form is cheaper.  A (token, key, head) costs 2 (512 + 64 + 512) = 2176 operations absorbed and 2 (192 + 128) =
 // 640 explicit, which has 2 * 256 * 512 on top for a key and head, once for all of the request's tokens: equal at 171
-// tokens, whatever the keys and heads.  A request goes explicit from CHUNK_MIN tokens on, where its keys' rows,
-// rounded up to whole tiles, fit in what the requests in front of it left of the buffers.
+// tokens, whatever the keys and heads.  Besides, an absorbed token costs as much as some 2500 keys of its own (its
+// queries, a part's beginning and end, its share of the join), so a request goes explicit from 192 keys / (keys + 2560)
+// tokens on, at least CHUNK_MIN, where its keys' rows, rounded up to whole tiles, fit in what the requests in front of it
+// left of the buffers.  Measured, explicit / absorbed, us: 128 heads, one request of 8192 keys, 128 tokens 383 / 272, 192
+// 389 / 408; four of 2048, 64 tokens 377 / 273, 96 380 / 403; 16 heads, four of 8192, 96 tokens 216 / 207, 128 217 / 253;
+// 16 of 2048, 64 tokens 217 / 203, 96 220 / 302; 16 of 200, 64 tokens 78 / 109.
 // One block: prefix sums over the requests, then a warp per 128 tokens, then the tiles in falling order of their keys.
 struct Chunk {
     PagedStep s;
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
             n = min(max(a.s.cu[b + 1], 0), N) - t0;
             keys = min(max(a.s.lens[b], 0), a.cap);
         }
-        const bool may = min(n, keys) >= CHUNK_MIN;
+        const bool may = min(n, keys) >= CHUNK_MIN && n * (keys + 2560l) >= keys * 192l;
         const long need = may ? (keys + 127l) / 128 * 128 : 0;
         long all;
         const long r0 = rows + block_before<NT>(need, warp_tot, all);

@@ -341,10 +341,10 @@ size_t mla_paged_decode_workspace(const mla_dims *dims, mla_dtype dtype, int B, 
  *   kv_lens [B]   cu_tokens [B + 1]   positions [n_tokens]   w_kv_b as above
  *   out [n_tokens, H, d_v]   lse (fp32) [n_tokens, H]
  * The tensor-core kernels take one of two forms for a request.  Absorbed, as decode: needs nothing but the call's
- * own rounds, and is the cheaper one up to about 170 tokens a request.  Explicit, as mla_latent_attn_fwd: K_nope and V
+ * own rounds, and is the cheaper one up to 64 to 180 tokens a request, by its length.  Explicit, as mla_latent_attn_fwd: K_nope and V
  * are rebuilt from the request's pages, head_shard heads at a time (0: all), into the workspace; it takes the requests of
  * many new tokens whose keys, rounded up to 128 each, fit in key_rows rows (in the order of the requests; 0:
- * none do), except for tokens that see few keys.  Both are exact to rounding, so key_rows (rounded down to a multiple
+ * none do, and a call of 64 tokens or more that holds no such request is some 10 us shorter).  Both are exact to rounding, so key_rows (rounded down to a multiple
  * of 256) and head_shard are a matter of memory, 1280 + 512 head_shard bytes a row, and of time.  The choice is
  * made on the device from the lengths there.
  * A token that sees no key (a negative position, no pages) gives out 0 and lse -inf.  Rows of no request (in front of

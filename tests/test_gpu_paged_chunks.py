@@ -52,11 +52,13 @@ def spread(cu, b, n):
 
 CASES = [   # heads, page, (past, new) of each request, requests that go explicit
     (16, 16, [(0, 700)], [0]),
-    (16, 64, [(900, 161), (3, 2), (0, 1300), (0, 0), (2000, 159)], [0, 2]),
+    (16, 64, [(900, 161), (3, 2), (0, 1300), (0, 0), (8000, 65)], [0, 2]),
     (128, 64, [(600, 200), (50, 1), (1024, 128)], [0]),
     (20, 48, [(511, 333), (512, 333)], [0, 1]),
     (1, 8, [(1000, 300), (0, 673)], [0, 1]),
     (3, 128, [(0, 5), (5, 800)], [1]),
+    (16, 16, [(0, 64), (0, 63), (100, 65)], [0, 2]),
+    (16, 64, [(2048, 300)] * 3 + [(130, 70), (40000, 200)], [0, 1, 2, 3, 4]),
 ]
 
 
