@@ -58,29 +58,16 @@ constexpr uint32_t V_BYTES = 2 * BOX;          // V^T: 128 dv rows x 2 key halve
 // runs with N = 144, so O column 128 accumulates the row sum of P exactly as the MMA used
 // it, and the softmax needs no sum of its own.
 constexpr uint32_t ONES = 16 * 128;
+constexpr uint32_t VBOX = BOX + ONES;          // one key half of a V slot
+constexpr uint32_t V_SLOT = 2 * VBOX;
 constexpr int KST = 2, VST = 2;
+constexpr uint32_t QS_BYTES = 3 * BOX;         // staged Q of the next unit: q_nope lo, hi (bf16), rotated q_pe (fp16)
 constexpr int NSM = 4;                        // softmax warps: one thread per query row
-constexpr uint32_t T_O = 256, T_L = T_O + 128;
-// STEP (a paged step's tokens): the row sums are the softmax's, in fp32 and of the unrounded weights: the column of ones
-// gathers 16 weights at a time in an accumulator that cuts off, 3e-5 of the sum at 16384 keys; and the rotated
-// q_pe has its fp16 rest too (four more score MMAs of 12): its rounding is the same for all keys, and shifted a
-// log-sum-exp by 1.5e-5 whatever their number.  Together the log-sum-exp's error there falls from 2.9e-6 to 2e-7 of it.
-// K_nope's rounding errs by 1.6e-4 in each score, 1.6e-4 / sqrt(0.4 keys) in a row's log-sum-exp: little but for rows of
-// few keys, so the request's first 512 keys have K_nope's rest in the scores too (eight MMAs more for those tiles).
-template <bool STEP>
-struct Lay {
-    static constexpr uint32_t VBOX = STEP ? BOX : BOX + ONES;   // one key half of a V slot
-    static constexpr uint32_t V_SLOT = 2 * VBOX;
-    // staged Q of the next unit: q_nope lo, hi (bf16), rotated q_pe (fp16; STEP: and its rest)
-    static constexpr int Q_BOXES = STEP ? 4 : 3;
-    static constexpr uint32_t QS_BYTES = Q_BOXES * BOX;
-    // Q staging, K/V rings, 1 KB alignment slack, 256 B of barriers
-    static constexpr uint32_t SMEM_BYTES = QS_BYTES + KST * K_BYTES + VST * V_SLOT + 1024 + 256;
-    // TMEM columns: S buffers 0-127 and 128-255, O 256-399 (dv 0-127, row sum 128, zeros), Q (192 fp16 = 96 columns)
-    // 400-495; STEP: O 256-383, Q 384-511
-    static constexpr uint32_t T_Q = STEP ? 384 : 400;
-    static_assert(SMEM_BYTES <= 232448 && T_Q + 32 * Q_BOXES <= 512, "budgets");
-};
+// Q staging, K/V rings, 1 KB alignment slack, 256 B of barriers
+constexpr uint32_t SMEM_BYTES = QS_BYTES + KST * K_BYTES + VST * V_SLOT + 1024 + 256;
+// TMEM columns: S buffers 0-127 and 128-255, O 256-399 (dv 0-127, row sum 128, zeros),
+// Q (192 fp16 = 96 columns) 400-495
+constexpr uint32_t T_O = 256, T_L = T_O + 128, T_Q = 400;
 constexpr float RESCALE_LOG2 = 8.0f;
 
 struct AttnK {
@@ -96,37 +83,12 @@ struct AttnK {
     int nh, nb, n_qt, units;       // heads of this launch, batch, query tiles, work units
 };
 
-// The units of a paged step (STEP): 128 tokens of one request, whose keys are rebuilt rows `keys` .. of K_nope and
-// V^T; each row has its own limit, pages may be missing.
-struct StepK {
-    const StepTile *tiles;    // heaviest first
-    const int *ctl;           // key rows in use, number of tiles
-    const int *limits, *done; // [tokens]: keys seen; nonzero: this kernel's
-    const uint32_t *held;     // a bit per key row: there is such a key
-    const int *holes;         // [requests]: nonzero: some page is missing
-    long lse_i;               // log-sum-exps of a token
-};
-
-constexpr int L2_KEYS = (112 << 20) / 512;   // (key, head) pairs whose K_nope and V^T stay in L2 (of 129 MB)
-
 // One work unit = (128-query tile, head, batch).  Units are numbered heaviest first
 // under the causal mask: (head, batch) fastest, query tiles from the latest down.
 struct Work {
     int hl, b, q0, nt;
-    int k0, rows, request;   // STEP: first key row, query rows, request
-    int r0, nr;              // STEP: first row of K_nope's rest, key tiles that have one
 };
-template <bool STEP>
-__device__ __forceinline__ Work work_of(const AttnK &p, const StepK &s, int n_tiles, bool heaviest, int u) {
-    if (STEP) {
-        // the heaviest tiles first, where L2 holds all heads' K_nope and V^T; else a head's tiles behind one another, so
-        // that it holds those of the ten or so heads in work (three prompts of up to 4096 tokens, 16 heads, 103 MB: 102 us
-        // against 127; 2048 tokens over 16384 keys, 64 heads a shard: 2.07 ms against 2.17)
-        const int div = heaviest ? p.nh : n_tiles, a = u / div, b = u - a * div;
-        const int4 *e = (const int4 *)(s.tiles + (heaviest ? a : b));
-        const int4 x = __ldcg(e), y = __ldcg(e + 1);
-        return Work{heaviest ? b : a, 0, x.x, x.w, x.z, x.y, y.x, y.y, min(y.z, x.w)};
-    }
+__device__ __forceinline__ Work work_of(const AttnK &p, int u) {
     const int nhb = p.nh * p.nb;
     const int hb = u % nhb;
     Work w;
@@ -135,7 +97,6 @@ __device__ __forceinline__ Work work_of(const AttnK &p, const StepK &s, int n_ti
     w.q0 = (p.n_qt - 1 - u / nhb) * BQ;
     const int kv_end = p.causal ? min(p.kv_need, p.q_offset + w.q0 + BQ) : p.kv_need;
     w.nt = (kv_end + BKV - 1) / BKV;
-    w.k0 = w.nr = 0;
     return w;
 }
 // Unit of round k for CTA c of G: rounds alternate direction over the heaviest-first
@@ -148,17 +109,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-template <bool STEP>
 __global__ void __launch_bounds__(32 * (NSM + 4), 1)
     tc_attn_kernel(const __grid_constant__ CUtensorMap mQn, const __grid_constant__ CUtensorMap mQr,
                    const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mKr,
-                   const __grid_constant__ CUtensorMap mV, AttnK p, const __grid_constant__ CUtensorMap mR, StepK sp) {
-    if (STEP && __ldcg(sp.ctl + 1) == 0) {   // (of a launch that ended before the one in front began its work)
-        pdl_wait();
-        return;
-    }
+                   const __grid_constant__ CUtensorMap mV, AttnK p) {
     extern __shared__ uint8_t smem_raw[];
-    constexpr uint32_t VBOX = Lay<STEP>::VBOX, V_SLOT = Lay<STEP>::V_SLOT, QS_BYTES = Lay<STEP>::QS_BYTES, T_Q = Lay<STEP>::T_Q;
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sQs = smem;
     uint8_t *sK = sQs + QS_BYTES;
@@ -203,7 +158,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
     }
     // the constant rows after every V^T box: row 0 ones (fp16 1.0), rows 1-15 zeros (a
     // row that is constant is unchanged by the 128-byte swizzle)
-    for (int i = tid; !STEP && i < VST * 2 * (int)(ONES / 16); i += blockDim.x) {
+    for (int i = tid; i < VST * 2 * (int)(ONES / 16); i += blockDim.x) {
         const int box = i / (ONES / 16), off = i % (ONES / 16);   // 16-byte chunk of the block
         const uint32_t v = off < 8 ? 0x3c003c00u : 0u;             // first 128-byte row: ones
         *(uint4 *)(sV + (box >> 1) * V_SLOT + (box & 1) * VBOX + BOX + off * 16) = make_uint4(v, v, v, v);
@@ -216,10 +171,6 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
     // The prologue overlaps the reconstruction GEMM (programmatic launch).  Every role
     // waits for it (pdl_wait) before touching K_nope, V^T, the rotated k_pe or the RoPE
     // table; the softmax warps first read their first unit's q rows, which are inputs.
-    // A step's units and limits come from the launches in front: there every warp waits.
-    if (STEP) pdl_wait();
-    const int n_tiles = STEP ? __ldcg(sp.ctl + 1) : 0, units = STEP ? n_tiles * p.nh : p.units;
-    const bool heaviest = STEP && (long)__ldcg(sp.ctl) * p.nh <= L2_KEYS;
 
     // Every role walks the same units in the same order and counts key tiles T across
     // units, so ring slots and barrier parities continue from one unit to the next.
@@ -232,11 +183,11 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             tma_prefetch_desc(&mK);
             tma_prefetch_desc(&mKr);
             bool ok = true;
-            int T = 0, n = 0;   // ring entries, units so far
-            for (int k = 0; k * G < units && ok; ++k) {
+            int T = 0, n = 0;
+            for (int k = 0; k * G < p.units && ok; ++k) {
                 const int u = unit_at(k, c, G);
-                if (u >= units) continue;
-                const Work w = work_of<STEP>(p, sp, n_tiles, heaviest, u);
+                if (u >= p.units) continue;
+                const Work w = work_of(p, u);
                 // this unit's Q into the staging buffer, once the softmax warps have moved
                 // the previous unit's Q into TMEM (this runs a couple of key tiles ahead of
                 // them, so the load has that long to land)
@@ -246,7 +197,6 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                 tma_load_4d(sQs, &mQn, qs_full, 0, p.head_off + w.hl, w.q0, w.b);
                 tma_load_4d(sQs + BOX, &mQn, qs_full, 64, p.head_off + w.hl, w.q0, w.b);
                 tma_load_4d(sQs + 2 * BOX, &mQr, qs_full, 0, p.head_off + w.hl, w.q0, w.b);
-                if (STEP) tma_load_4d(sQs + 3 * BOX, &mQr, qs_full, 64, p.head_off + w.hl, w.q0, w.b);
                 for (int j = 0; j < w.nt; ++j, ++T) {
                     const int ks = T % KST;
                     if (T >= KST && !mbar_wait(&k_empty[ks], ((T / KST) - 1) & 1, abort, &g_tc_attn_err)) {
@@ -255,19 +205,9 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                     }
                     uint8_t *kd = sK + ks * K_BYTES;
                     mbar_arrive_expect_tx(&k_full[ks], K_BYTES);
-                    tma_load_3d(kd, &mK, &k_full[ks], w.hl * 128, w.k0 + j * BKV, w.b);
-                    tma_load_3d(kd + BOX, &mK, &k_full[ks], w.hl * 128 + 64, w.k0 + j * BKV, w.b);
-                    tma_load_3d(kd + 2 * BOX, &mKr, &k_full[ks], 0, w.k0 + j * BKV, w.b);
-                    if (STEP && j < w.nr) {   // the tile's rest of K_nope, an entry of its own
-                        const int rs = ++T % KST;
-                        if (T >= KST && !mbar_wait(&k_empty[rs], ((T / KST) - 1) & 1, abort, &g_tc_attn_err)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_arrive_expect_tx(&k_full[rs], 2 * BOX);
-                        tma_load_3d(sK + rs * K_BYTES, &mR, &k_full[rs], w.hl * 128, w.r0 + j * BKV, 0);
-                        tma_load_3d(sK + rs * K_BYTES + BOX, &mR, &k_full[rs], w.hl * 128 + 64, w.r0 + j * BKV, 0);
-                    }
+                    tma_load_3d(kd, &mK, &k_full[ks], w.hl * 128, j * BKV, w.b);
+                    tma_load_3d(kd + BOX, &mK, &k_full[ks], w.hl * 128 + 64, j * BKV, w.b);
+                    tma_load_3d(kd + 2 * BOX, &mKr, &k_full[ks], 0, j * BKV, w.b);
                 }
             }
         }
@@ -278,10 +218,10 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             tma_prefetch_desc(&mV);
             bool ok = true;
             int T = 0;
-            for (int k = 0; k * G < units && ok; ++k) {
+            for (int k = 0; k * G < p.units && ok; ++k) {
                 const int u = unit_at(k, c, G);
-                if (u >= units) continue;
-                const Work w = work_of<STEP>(p, sp, n_tiles, heaviest, u);
+                if (u >= p.units) continue;
+                const Work w = work_of(p, u);
                 for (int j = 0; j < w.nt; ++j, ++T) {
                     const int vs = T % VST;
                     if (T >= VST && !mbar_wait(&v_empty[vs], ((T / VST) - 1) & 1, abort, &g_tc_attn_err)) {
@@ -290,8 +230,8 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                     }
                     uint8_t *vd = sV + vs * V_SLOT;
                     mbar_arrive_expect_tx(&v_full[vs], V_BYTES);
-                    tma_load_3d(vd, &mV, &v_full[vs], w.k0 + j * BKV, w.hl * 128, w.b);
-                    tma_load_3d(vd + VBOX, &mV, &v_full[vs], w.k0 + j * BKV + 64, w.hl * 128, w.b);
+                    tma_load_3d(vd, &mV, &v_full[vs], j * BKV, w.hl * 128, w.b);
+                    tma_load_3d(vd + VBOX, &mV, &v_full[vs], j * BKV + 64, w.hl * 128, w.b);
                 }
             }
         }
@@ -302,17 +242,17 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
         {
             pdl_wait();
             bool ok = true;
-            int T = 0, n = 0, R = 0;   // key tiles, units, entries of rests so far
-            for (int k = 0; k * G < units && ok; ++k) {
+            int T = 0, n = 0;   // key tiles, units so far
+            for (int k = 0; k * G < p.units && ok; ++k) {
                 const int u = unit_at(k, c, G);
-                if (u >= units) continue;
-                const Work w = work_of<STEP>(p, sp, n_tiles, heaviest, u);
+                if (u >= p.units) continue;
+                const Work w = work_of(p, u);
                 // this unit's Q is in TMEM
                 if (!__all_sync(0xffffffffu, mbar_wait(q_ready, n & 1, abort, &g_tc_attn_err))) break;
                 ++n;
                 for (int j = 0; j < w.nt; ++j, ++T) {
-                    const int E = STEP ? T + R : T, ks = E % KST;
-                    bool go = __all_sync(0xffffffffu, mbar_wait(&k_full[ks], (E / KST) & 1, abort, &g_tc_attn_err));
+                    const int ks = T % KST;
+                    bool go = __all_sync(0xffffffffu, mbar_wait(&k_full[ks], (T / KST) & 1, abort, &g_tc_attn_err));
                     // S buffer T & 1 last held P_{T-2}: P.V_{T-2} must have read it
                     if (go && T >= 2)
                         go = __all_sync(0xffffffffu, mbar_wait(&pv_done[T & 1], ((T - 2) >> 1) & 1, abort, &g_tc_attn_err));
@@ -325,37 +265,16 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                     const uint8_t *kd = sK + ks * K_BYTES;
                     if (elect_one()) {
 #pragma unroll
-                        for (int kb = 0; kb < Lay<STEP>::Q_BOXES; ++kb) {
-                            const uint64_t db = sdesc_kmajor(kd + (kb < 3 ? kb : 2) * BOX);
+                        for (int kb = 0; kb < 3; ++kb) {
+                            const uint64_t db = sdesc_kmajor(kd + kb * BOX);
 #pragma unroll
                             for (int k4 = 0; k4 < 4; ++k4)
                                 mma_ts(s_tm, tmem + T_Q + (kb * 4 + k4) * 8, db + 2 * k4, p.idesc_s, (kb | k4) != 0);
                         }
-                        if (!STEP || j >= w.nr) mma_commit(&s_full[T & 1]);
+                        mma_commit(&s_full[T & 1]);
                         mma_commit(&k_empty[ks]);
                     }
                     __syncwarp();
-                    if (STEP && j < w.nr) {
-                        const int rs = (E + 1) % KST;
-                        ++R;
-                        if (!__all_sync(0xffffffffu, mbar_wait(&k_full[rs], ((E + 1) / KST) & 1, abort, &g_tc_attn_err))) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int kb = 0; kb < 2; ++kb) {
-                                const uint64_t db = sdesc_kmajor(sK + rs * K_BYTES + kb * BOX);
-#pragma unroll
-                                for (int k4 = 0; k4 < 4; ++k4)
-                                    mma_ts(s_tm, tmem + T_Q + (kb * 4 + k4) * 8, db + 2 * k4, p.idesc_s, 1);
-                            }
-                            mma_commit(&s_full[T & 1]);
-                            mma_commit(&k_empty[rs]);
-                        }
-                        __syncwarp();
-                    }
                 }
             }
         }
@@ -366,10 +285,10 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             pdl_wait();
             bool ok = true;
             int T = 0, n = 0;
-            for (int k = 0; k * G < units && ok; ++k) {
+            for (int k = 0; k * G < p.units && ok; ++k) {
                 const int u = unit_at(k, c, G);
-                if (u >= units) continue;
-                const Work w = work_of<STEP>(p, sp, n_tiles, heaviest, u);
+                if (u >= p.units) continue;
+                const Work w = work_of(p, u);
                 // the epilogue of the previous unit has read O before P.V_0 overwrites it
                 if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(o_free, (n - 1) & 1, abort, &g_tc_attn_err))) break;
                 ++n;
@@ -416,8 +335,8 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
         int T = 0, n = 0;
         // this CTA's units in order: round k, skipping rounds past the end
         auto next_unit = [&](int k) -> int {
-            for (; k * G < units; ++k)
-                if (unit_at(k, c, G) < units) return k;
+            for (; k * G < p.units; ++k)
+                if (unit_at(k, c, G) < p.units) return k;
             return k;
         };
         // ---- a unit's Q from the staging buffer into TMEM (the previous unit's score MMAs
@@ -445,9 +364,8 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                 tmem_st16(lane_base + T_Q + 32 * h, qn[0]);
                 tmem_st16(lane_base + T_Q + 32 * h + 16, qn[1]);
             }
-#pragma unroll
-            for (int h = 2; h < Lay<STEP>::Q_BOXES; ++h) {
-                const uint8_t *prow = sQs + h * BOX + row * 128;
+            {
+                const uint8_t *prow = sQs + 2 * BOX + row * 128;
                 uint32_t pe[2][16];
 #pragma unroll
                 for (int cc = 0; cc < 8; ++cc) {
@@ -455,8 +373,8 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                     pe[cc >> 2][4 * (cc & 3)] = v.x, pe[cc >> 2][4 * (cc & 3) + 1] = v.y;
                     pe[cc >> 2][4 * (cc & 3) + 2] = v.z, pe[cc >> 2][4 * (cc & 3) + 3] = v.w;
                 }
-                tmem_st16(lane_base + T_Q + 32 * h, pe[0]);
-                tmem_st16(lane_base + T_Q + 32 * h + 16, pe[1]);
+                tmem_st16(lane_base + T_Q + 64, pe[0]);
+                tmem_st16(lane_base + T_Q + 80, pe[1]);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -464,20 +382,13 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             if (lane == 0) mbar_arrive(q_ready);
         };
         int k = next_unit(0);
-        if (k * G < units) load_q(0);
-        for (; k * G < units;) {
+        if (k * G < p.units) load_q(0);
+        for (; k * G < p.units;) {
             const int u = unit_at(k, c, G);
-            const Work w = work_of<STEP>(p, sp, n_tiles, heaviest, u);
+            const Work w = work_of(p, u);
             const int hq = p.head_off + w.hl, b = w.b, q0 = w.q0, nt = w.nt;
             const int pos = p.q_offset + q0 + row;
-            int sees = 0, all_see = 0, holes = 0;   // STEP: keys that the row, that every row of the warp sees
-            if (STEP) {
-                sees = row < w.rows ? __ldcg(sp.limits + q0 + row) : 2147483647;
-                all_see = __reduce_min_sync(0xffffffffu, sees);
-                holes = __ldcg(sp.holes + w.request);
-            }
             float m = -INFINITY;
-            float sum = 0.f;   // STEP: the row sum
             for (int j = 0; j < nt; ++j, ++T) {
                 const int sb = T & 1;
                 ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[sb], (T >> 1) & 1, abort, &g_tc_attn_err));
@@ -500,19 +411,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                 // test); the masking is a pass of its own so that the maximum and the
                 // exponentials stay straight runs
                 const int j0 = j * BKV;
-                if (STEP) {
-                    if (j0 + BKV > all_see || holes) {
-                        const int lim = sees - j0;
-#pragma unroll
-                        for (int cc = 0; cc < 128; ++cc) x[cc] = cc < lim ? x[cc] : -INFINITY;
-                        if (holes) {
-                            const uint4 h = __ldcg((const uint4 *)(sp.held + (w.k0 + j0) / 32));
-                            const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-                            for (int cc = 0; cc < 128; ++cc) x[cc] = hw[cc >> 5] >> (cc & 31) & 1 ? x[cc] : -INFINITY;
-                        }
-                    }
-                } else if ((j0 + BKV > p.kv_need) || (p.causal && j0 + BKV - 1 > p.q_offset + q0)) {
+                if ((j0 + BKV > p.kv_need) || (p.causal && j0 + BKV - 1 > p.q_offset + q0)) {
                     // the row sees keys j0 .. j0 + lim - 1 of this tile
                     const int lim = min(p.kv_need, p.causal ? pos + 1 : p.kv_need) - j0;
 #pragma unroll
@@ -546,42 +445,31 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
                             tmem_st32(lane_base + T_O + 32 * q, o);
                         }
-                        if (!STEP) {
-                            const uint32_t lv = tmem_ld1(lane_base + T_L);   // the row sum, rescaled with the row
-                            tmem_ld_wait();
-                            tmem_st1(lane_base + T_L, __float_as_uint(__uint_as_float(lv) * alpha));
-                        }
+                        const uint32_t lv = tmem_ld1(lane_base + T_L);   // the row sum, rescaled with the row
+                        tmem_ld_wait();
+                        tmem_st1(lane_base + T_L, __float_as_uint(__uint_as_float(lv) * alpha));
                         tmem_st_wait();
                     }
-                    sum *= alpha;
                     m = m_use;
                 }
                 const float nm = (m == -INFINITY) ? 0.f : -m;
                 // P over the S columns it came from, 32 keys (16 columns) at a time
-                float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float p0 = ex2(fmaf(x[32 * q + 2 * i], p.scale_log2, nm)),
-                                    p1 = ex2(fmaf(x[32 * q + 2 * i + 1], p.scale_log2, nm));
-                        pk[i] = pack_f16(p0, p1);
-                        if (STEP) {
-                            add[2 * (i & 1)] += p0;
-                            add[2 * (i & 1) + 1] += p1;
-                        }
-                    }
+                    for (int i = 0; i < 16; ++i)
+                        pk[i] = pack_f16(ex2(fmaf(x[32 * q + 2 * i], p.scale_log2, nm)),
+                                         ex2(fmaf(x[32 * q + 2 * i + 1], p.scale_log2, nm)));
                     if (ok) tmem_st16(lane_base + sb * 128 + 16 * q, pk);
                 }
                 if (ok) tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[sb]);
-                sum += (add[0] + add[1]) + (add[2] + add[3]);
             }
             const int k_next = next_unit(k + 1);
-            if (k_next * G < units) load_q(n + 1);
+            if (k_next * G < p.units) load_q(n + 1);
             // ---- epilogue: the row sum is O's column 128; the row's 128 outputs in bf16
             if (nt > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(o_final, n & 1, abort, &g_tc_attn_err));
             tc_fence_after();
@@ -593,7 +481,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                 for (int q = 0; q < 4; ++q) tmem_ld32(lane_base + T_O + 32 * q, o[q]);
                 const uint32_t lv = tmem_ld1(lane_base + T_L);
                 tmem_ld_wait();
-                l = STEP ? sum : __uint_as_float(lv);
+                l = __uint_as_float(lv);
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -604,7 +492,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free);   // the next unit's P.V_0 may overwrite O
-            if (ok && (STEP ? row < w.rows && __ldcg(sp.done + qi) : qi < p.s_q)) {
+            if (ok && qi < p.s_q) {
                 // the row's 256 bytes in 32-byte stores (16-byte ones when the rows are not
                 // 32-byte aligned)
                 uint32_t *dst = (uint32_t *)(p.out + b * p.out_b + (long)qi * p.out_i + (long)hq * p.out_h);
@@ -623,7 +511,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
                             ((uint4 *)(dst + 16 * q))[v] = make_uint4(wv[4 * v], wv[4 * v + 1], wv[4 * v + 2], wv[4 * v + 3]);
                     }
                 }
-                p.lse[STEP ? qi * sp.lse_i + hq : b * p.lse_b + (long)hq * p.lse_h + qi] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                p.lse[b * p.lse_b + (long)hq * p.lse_h + qi] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
             }
             ++n;
             k = k_next;
@@ -704,8 +592,7 @@ cudaError_t tc_explicit_prefill(const TcPrefill &p, const void *q_nope, const vo
         unsigned box[3] = {64, 128, 1};
         if ((e = make_tma_map(&mV, vws, 3, d, s, box)) != cudaSuccess) return e;
     }
-    constexpr uint32_t SMEM_BYTES = Lay<false>::SMEM_BYTES;
-    e = cudaFuncSetAttribute(tc_attn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    e = cudaFuncSetAttribute(tc_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
     if (e != cudaSuccess) return e;
     int dev = 0, n_sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -751,76 +638,9 @@ cudaError_t tc_explicit_prefill(const TcPrefill &p, const void *q_nope, const vo
             attr[0].val.programmaticStreamSerializationAllowed = 1;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            e = cudaLaunchKernelEx(&cfg, tc_attn_kernel<false>, mQn, mQr, mK, mKr, mV, a, mK, StepK{});
+            e = cudaLaunchKernelEx(&cfg, tc_attn_kernel, mQn, mQr, mK, mKr, mV, a);
         }
         if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    return cudaSuccess;
-}
-
-// A paged step's tokens in the explicit form.  The maps are the prefill's with one batch, the key rows of all requests
-// behind one another; how many there are, and the units, is known on the device only, so the grids are fixed.
-cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st) {
-    using ull = unsigned long long;
-    const ull R = p.key_rows, H = p.H, T = p.T, hs = p.hs;
-    cudaError_t e;
-    CUtensorMap mQn, mQr, mK, mKr, mV, mR;
-    {
-        const ull d[4] = {128, H, T, 1}, s[3] = {256, H * 256, T * H * 256}, dr[4] = {128, H, T, 1};
-        const unsigned box[4] = {64, 1, 128, 1};
-        if ((e = make_tma_map(&mQn, p.q_nope, 4, d, s, box)) != cudaSuccess) return e;
-        if ((e = make_tma_map(&mQr, p.qpe, 4, dr, s, box)) != cudaSuccess) return e;
-    }
-    {
-        const ull dr[3] = {64, R, 1}, sr[2] = {128, R * 128}, dk[3] = {hs * 128, R, 1}, sk[2] = {hs * 256, R * hs * 256};
-        const ull dv[3] = {R, hs * 128, 1}, sv[2] = {R * 2, R * hs * 256};
-        const unsigned box[3] = {64, 128, 1};
-        if ((e = make_tma_map(&mKr, p.kpe, 3, dr, sr, box)) != cudaSuccess) return e;
-        if ((e = make_tma_map(&mK, p.kws, 3, dk, sk, box)) != cudaSuccess) return e;
-        const ull nr = p.rest_rows, drest[3] = {hs * 128, nr, 1}, srest[2] = {hs * 256, nr * hs * 256};
-        if ((e = make_tma_map(&mR, p.rest, 3, drest, srest, box)) != cudaSuccess) return e;
-        if ((e = make_tma_map(&mV, p.vws, 3, dv, sv, box)) != cudaSuccess) return e;
-    }
-    constexpr uint32_t SMEM_BYTES = Lay<true>::SMEM_BYTES;
-    if ((e = cudaFuncSetAttribute(tc_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess) return e;
-    int dev = 0, n_sms = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&n_sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    AttnK a{};
-    a.scale_log2 = p.scale * 1.4426950408889634f;
-    a.out = (__nv_bfloat16 *)p.out;
-    a.out_i = p.H * 128L;
-    a.out_h = 128;
-    a.out_v8 = ((uintptr_t)p.out % 32) == 0;
-    a.lse = p.lse;
-    a.idesc_s = idesc_f16(128, 128, true);
-    a.idesc_pv = idesc_f16(128, 128, true);
-    a.nb = 1;
-    const StepK sp{p.tiles, p.ctl, p.limits, p.done, p.held, p.holes, p.H};
-    for (int h0 = 0; h0 < p.H; h0 += p.hs) {
-        const int nh = std::min(p.hs, p.H - h0);
-        // bf16 rows and weights as they are: their products are exact in the fp32 accumulator
-        TmaOperand latent{p.chat, 512, (long)R, 1, 1024, (long)R * 1024, (int)R, 0, 1};
-        const char *w = (const char *)p.w + (long)h0 * 256 * 1024;
-        TmaOperand wk{w, 512, 128, nh, 1024, 256 * 1024, 128, 0, 0}, wv{w + 128 * 1024, 512, 128, nh, 1024, 256 * 1024, 128, 0, 0};
-        const GemmProblem kv[2] = {{latent, wk, (int)R, nh * 128, 512, 1, p.kws, (long)hs * 128, 1, 0, 0},
-                                   {wv, latent, nh * 128, (int)R, 512, 1, p.vws, (long)R, 1, 0, 0}};
-        const GemmStep gs{p.ctl, p.rest_of, p.rest};
-        if ((e = tc_gemm_group(kv, 2, false, st, &gs)) != cudaSuccess) return e;
-        a.head_off = h0;
-        a.nh = nh;
-        ProfScope ps("tc_attn", st);
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(n_sms);
-        cfg.blockDim = dim3(32 * (NSM + 4));
-        cfg.dynamicSmemBytes = SMEM_BYTES;
-        cfg.stream = st;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // overlap the GEMM's tail
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if ((e = cudaLaunchKernelEx(&cfg, tc_attn_kernel<true>, mQn, mQr, mK, mKr, mV, a, mR, sp)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

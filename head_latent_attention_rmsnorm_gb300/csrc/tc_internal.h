@@ -59,6 +59,7 @@ cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaS
 
 cudaError_t tc_gemm_read_and_clear_error(unsigned *flags, cudaStream_t st);
 cudaError_t tc_attn_read_and_clear_error(unsigned *flags, cudaStream_t st);
+cudaError_t tc_step_read_and_clear_error(unsigned *flags, cudaStream_t st);
 cudaError_t tc_latent_read_and_clear_error(unsigned *flags, cudaStream_t st);
 cudaError_t tc_decode_read_and_clear_error(unsigned *flags, cudaStream_t st);
 cudaError_t tc_fused_read_and_clear_error(unsigned *flags, cudaStream_t st);

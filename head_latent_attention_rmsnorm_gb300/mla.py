@@ -286,7 +286,7 @@ KERNELS = ("prep", "latent_prep", "rope_table", "rope_rows", "convert", "gemm_si
            "tpla_combine", "wait_probe", "tc_fused_attn", "bwd_rowdot", "attn_bwd_simt", "bwd_rows",
            "bwd_prep", "tc_bwd_dkv", "tc_bwd_dq", "paged_tables", "paged_append", "paged_absorb", "paged_attn",
            "paged_join", "paged_plan", "paged_weights", "paged_weights_out", "paged_evict",
-           "paged_chunk", "paged_gather")
+           "paged_chunk", "paged_gather", "tc_step_attn")
 
 
 def launch_count() -> int:

@@ -502,7 +502,7 @@ mla_status mla_decode_splitkv_noalloc(const mla_dims *dims, mla_dtype dtype, int
  *   "tpla_combine", "wait_probe", "tc_fused_attn", "bwd_rowdot",
  *   "attn_bwd_simt", "bwd_rows", "bwd_prep", "tc_bwd_dkv", "tc_bwd_dq",
  *   "paged_tables", "paged_append", "paged_absorb", "paged_attn", "paged_join", "paged_plan",
- *   "paged_weights", "paged_weights_out", "paged_evict", "paged_chunk", "paged_gather".
+ *   "paged_weights", "paged_weights_out", "paged_evict", "paged_chunk", "paged_gather", "tc_step_attn".
  * mla_profile_reset: forgets recorded events, keeps recording on/off as it was.
  * Launches from several host threads are recorded safely; call enable, reset and the
  * queries between computations, not while another thread's calls are in flight.

@@ -72,7 +72,7 @@ def test_against_64_bits(heads, page, lens, explicit, head_shard):
     out = torch.full((n, heads, 128), 5.0, dtype=BF).cuda()
     lse = torch.full((n, heads), 6.0).cuda()
     _, names = kernels(lambda: mla.paged_prefill(d, *a, out=out, lse=lse, head_shard=head_shard))
-    assert {"paged_chunk", "tc_gemm", "tc_attn"} <= names
+    assert {"paged_chunk", "tc_gemm", "tc_step_attn"} <= names
     for t in (0, 1, n - 3, n - 2, n - 1):
         assert bool((out[t] == 5).all()) and bool((lse[t] == 6).all())
     cu = s["cu_tokens"].tolist()
@@ -105,7 +105,7 @@ def test_missing_pages_and_odd_positions(heads):
     s["kv_lens"][1] = 1000
     a = sref.on_gpu(s)
     (out, lse), names = kernels(lambda: mla.paged_prefill(d, *a))
-    assert "tc_attn" in names
+    assert "tc_step_attn" in names
     check_rows(d, s, out, lse, [0, 4, 5, 6, 7, 20, 128, 299, 300, 399, 400, 469, 470, 471])
 
 
