@@ -1226,7 +1226,8 @@ void paged_explicit_carve(const PagedDecode &p, int B, int n_tokens, int key_row
     x->c.max_tiles = chunk_tiles(n_tokens);
     x->c.max_rests = chunk_rests(n_tokens, key_rows);
     x->c.rest_of = (int *)c.take(R / 128 * sizeof(int));
-    x->c.ctl = (int *)c.take(3 * sizeof(int));
+    x->c.ctl = (int *)c.take(4 * sizeof(int));
+    x->c.heads = x->hs;
     x->c.key0 = (int *)c.take(B * sizeof(int));
     x->c.holes = (int *)c.take(B * sizeof(int));
     x->c.block_of = (int *)c.take(R / 128 * sizeof(int));

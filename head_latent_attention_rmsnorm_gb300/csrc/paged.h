@@ -100,7 +100,8 @@ struct PagedChunk {
     int max_tiles, max_rests;    // tiles of 128 tokens; tiles of 128 keys with a rest
     int *rest_of;                // [key_rows / 128]
     void *rest;
-    int *ctl;                    // [3]: rows in use, tiles, tokens of the list
+    int heads;                   // of a shard
+    int *ctl;                    // [4]: rows in use, tiles, tokens of the list, whether the tiles are in falling order
     int *key0, *holes;           // [B]: a request's first key row (-1: absorbed); nonzero: some page is missing
     int *block_of;               // [key_rows / 128]: the request of each 128 rows
     int *limits, *done, *list;   // [n_tokens]: keys seen; nonzero: explicit; the requests' other tokens

@@ -171,21 +171,26 @@ __device__ long block_before(long n, long *warp_tot, long &all) {
 // left of the buffers.  Measured, explicit / absorbed, us: 128 heads, one request of 8192 keys, 128 tokens 383 / 272, 192
 // 389 / 408; four of 2048, 64 tokens 377 / 273, 96 380 / 403; 16 heads, four of 8192, 96 tokens 216 / 207, 128 217 / 253;
 // 16 of 2048, 64 tokens 217 / 203, 96 220 / 302; 16 of 200, 64 tokens 78 / 109.
-// One block: prefix sums over the requests, then a warp per 128 tokens, then the tiles in falling order of their keys.
+// One block: prefix sums over the requests, then a warp per 128 tokens, then the order of the tiles: in falling order of
+// their keys where L2 holds all K_nope and V^T of a shard's heads, which then take turns; else request by request, the
+// longest first, so that the tiles of one head and request, which read the same rows, run together.
 struct Chunk {
     PagedStep s;
     PagedChunk c;
-    int cap, key_rows;
+    int cap, key_rows, heads;   // heads of a shard
 };
+constexpr int L2_KEYS = (112 << 20) / 512;   // (key, head) pairs whose K_nope and V^T stay in L2 (of 129 MB)
 
 template <int NT>
 __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__ Chunk a) {
     __shared__ long warp_tot[NT / 32];
-    __shared__ int weight[CHUNK_SORT];
+    __shared__ int2 order[CHUNK_SORT];   // a tile's key tiles, its request
+    __shared__ int explicit_tokens;
     const int tid = threadIdx.x, lane = tid & 31, N = a.s.n_tokens;
     pdl_wait();
     pdl_launch_dependents();
     for (int i = tid; i < N; i += NT) a.c.done[i] = 0;
+    if (tid == 0) explicit_tokens = 0;
     long rows = 0, tiles = 0, used = 0, rests = 0;
     for (int b0 = 0; b0 < a.s.B; b0 += NT) {
         const int b = b0 + tid;
@@ -234,29 +239,50 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
     __syncthreads();
     const int n = (int)min(tiles, (long)a.c.max_tiles);
     const bool sorted = n <= CHUNK_SORT;
-    for (int e = tid >> 5; e < n; e += NT / 32) {
-        const StepTile x = a.c.raw[e];
-        const int keys = min(max(a.s.lens[x.request], 0), a.cap);
-        int most = 0;
+    constexpr int AT_ONCE = 3;   // tiles of a warp whose loads are in flight together
+    for (int e0 = tid >> 5; e0 < n; e0 += AT_ONCE * (NT / 32)) {
+        StepTile x[AT_ONCE];
+        int keys[AT_ONCE], pos[AT_ONCE][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = lane + 32 * i, t = x.token + r;
-            if (r >= x.rows) continue;
-            const int pos = a.s.positions[t], sees = pos < 0 ? 0 : min(keys, pos == 2147483647 ? pos : pos + 1);
-            a.c.limits[t] = sees;
-            if (sees > 0) {
-                a.c.done[t] = 1;
-                most = max(most, sees);
-            }
+        for (int k = 0; k < AT_ONCE; ++k) {
+            x[k].rows = x[k].token = x[k].request = 0;
+            if (e0 + k * (NT / 32) < n) x[k] = a.c.raw[e0 + k * (NT / 32)];
         }
-        most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0) {
-            a.c.raw[e].tiles = (most + 127) / 128;
-            if (sorted) weight[e] = (most + 127) / 128;
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            keys[k] = a.s.lens[x[k].request];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pos[k][i] = lane + 32 * i < x[k].rows ? a.s.positions[x[k].token + lane + 32 * i] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            const int e = e0 + k * (NT / 32);
+            if (e >= n) break;
+            int most = 0, mine = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = lane + 32 * i, t = x[k].token + r, p = pos[k][i];
+                if (r >= x[k].rows) continue;
+                const int sees = p < 0 ? 0 : min(min(max(keys[k], 0), a.cap), p == 2147483647 ? p : p + 1);
+                a.c.limits[t] = sees;
+                if (sees > 0) {
+                    a.c.done[t] = 1;
+                    ++mine;
+                    most = max(most, sees);
+                }
+            }
+            most = __reduce_max_sync(0xffffffffu, most);
+            mine = __reduce_add_sync(0xffffffffu, mine);
+            if (lane == 0) {
+                a.c.raw[e].tiles = (most + 127) / 128;
+                atomicAdd(&explicit_tokens, mine);
+                if (sorted) order[e] = make_int2((most + 127) / 128, x[k].request);
+            }
         }
     }
     __syncthreads();
-    // the tiles that have keys here, the heaviest first (a step of more than CHUNK_SORT tiles as they come)
+    // the tiles that have keys here in their order (a step of more than CHUNK_SORT tiles: as they come, heads in turns)
+    const bool heaviest = !sorted || used * a.heads <= L2_KEYS;
     long out = 0;
     for (int base = 0; base < n; base += NT) {
         const int e = base + tid;
@@ -265,16 +291,37 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
         long all, at = out + block_before<NT>(x.tiles > 0, warp_tot, all);
         out += all;
         if (x.tiles == 0) continue;
-        if (sorted) {
+        if (sorted && heaviest) {
             at = 0;
-            for (int i = 0; i < n; ++i) at += weight[i] > x.tiles || (weight[i] == x.tiles && i < e);
+            for (int i = 0; i < n; ++i) at += order[i].x > x.tiles || (order[i].x == x.tiles && i < e);
+        } else if (sorted) {   // by the request's longest tile, then as they come: a request's tiles are neighbours in raw
+            int lo = e, hi = e + 1, most = x.tiles, count = 0, before = 0;
+            while (lo > 0 && order[lo - 1].y == x.request) --lo;
+            while (hi < n && order[hi].y == x.request) ++hi;
+            for (int i = lo; i < hi; ++i) {
+                most = max(most, order[i].x);
+                count += order[i].x > 0;
+                before += i < e && order[i].x > 0;
+            }
+            at = 0;   // tiles of the requests in front
+            for (int i = 0; i < n;) {
+                int j = i, m = 0, c = 0;
+                for (; j < n && order[j].y == order[i].y; ++j) {
+                    m = max(m, order[j].x);
+                    c += order[j].x > 0;
+                }
+                if (m > most || (m == most && i < lo)) at += c;
+                i = j;
+            }
+            x.place = (int)at << 16 | count;
+            at += before;
         }
         a.c.tiles[at] = x;
     }
     // the requests' other tokens, eight neighbours a thread
     long listed = 0;
     const int first = min(max(a.s.cu[0], 0), N), last = min(max(a.s.cu[a.s.B], 0), N);
-    for (int base = first; base < last; base += 8 * NT) {
+    for (int base = explicit_tokens == last - first ? last : first; base < last; base += 8 * NT) {
         const int t0 = base + 8 * tid;
         int mine = 0;   // (mask)
 #pragma unroll
@@ -291,6 +338,7 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
         a.c.ctl[0] = (int)used;
         a.c.ctl[1] = (int)out;
         a.c.ctl[2] = (int)listed;
+        a.c.ctl[3] = heaviest;
     }
 }
 
@@ -391,7 +439,7 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant
 cudaError_t launch_paged_chunk(const PagedDecode &p, const PagedStep &s, const PagedChunk &c, cudaStream_t st) {
     cudaError_t e;
     {
-        const Chunk a{s, c, p.max_pages * p.page, c.key_rows};
+        const Chunk a{s, c, p.max_pages * p.page, c.key_rows, c.heads};
         ProfScope ps("paged_chunk", st);
         const bool few = s.n_tokens <= 2048 && s.B <= 256;   // few warps come together sooner
         auto kern = few ? paged_chunk_kernel<256> : paged_chunk_kernel<PNT>;

@@ -36,7 +36,8 @@ cudaError_t tc_explicit_prefill(const TcPrefill &p, const void *q_nope, const vo
 // of one head shard after the other.
 struct alignas(16) StepTile {
     int token, rows, key, tiles;   // first token, tokens (up to 128), first key row, key tiles of 128
-    int request, rest, rests, pad; // first row of K_nope's rest, key tiles that have one
+    int request, rest, rests;      // first row of K_nope's rest, key tiles that have one
+    int place;                     // tiles request by request: the request's first in the list << 16 | their number
 };
 struct TcStep {
     int T, H, hs, key_rows;        // tokens, heads, heads of a shard, rows of the key buffers (a multiple of 256)
@@ -49,7 +50,7 @@ struct TcStep {
     const int *rest_of;            // [key_rows / 128]: 128 rows' place there, -1: none
     void *out;                     // [T][H][128]
     float *lse;                    // [T][H]
-    const int *ctl;                // key rows in use, number of tiles
+    const int *ctl;                // key rows in use, number of tiles, -, nonzero: tiles in falling order
     const StepTile *tiles;
     const int *limits, *done;      // [T]: keys seen; nonzero: computed here
     const uint32_t *held;          // a bit per key row

@@ -62,11 +62,10 @@ constexpr int NTHREADS = 384;
 // 63488 of 384 x 168 = 64512
 constexpr int REGS_ISSUE = 80, REGS_SOFTMAX = 208;
 static_assert(128 * (REGS_ISSUE + 2 * REGS_SOFTMAX) <= NTHREADS * 168, "the split draws on the launch's registers");
-constexpr int L2_KEYS = (112 << 20) / 512;   // (key, head) pairs whose K_nope and V^T stay in L2 (of 129 MB)
 
 struct StepK {
-    const StepTile *tiles;    // heaviest first
-    const int *ctl;           // key rows in use, number of tiles
+    const StepTile *tiles;
+    const int *ctl;           // as TcStep's
     const int *limits, *done; // [tokens]: keys seen; nonzero: computed here
     const uint32_t *held;     // a bit per key row: there is such a key
     const int *holes;         // [requests]: nonzero: some page is missing
@@ -83,14 +82,20 @@ struct Work {
     int hl, q0, rows, nt;     // head, first token, tokens, key tiles
     int k0, request, r0, nr;  // first key row, request, first row of K_nope's rest, key tiles that have one
 };
-__device__ __forceinline__ Work work_of(const StepK &s, int n_tiles, bool heaviest, int u) {
-    // the heaviest tiles first, where L2 holds all heads' K_nope and V^T; else a head's tiles behind one another, so
-    // that it holds those of the ten or so heads in work (three prompts of up to 4096 tokens, 16 heads, 103 MB: 102 us
-    // against 127; 2048 tokens over 16384 keys, 64 heads a shard: 2.07 ms against 2.17)
-    const int div = heaviest ? s.nh : n_tiles, a = u / div, b = u - a * div;
-    const int4 *e = (const int4 *)(s.tiles + (heaviest ? a : b));
+__device__ __forceinline__ Work work_of(const StepK &s, bool heaviest, int u) {
+    // The heaviest tiles first, heads in turns, where L2 holds all heads' K_nope and V^T; else a request's tiles of one
+    // head behind one another, so that L2 holds those of the ten or so heads in work (three prompts of up to 4096
+    // tokens, 16 heads, 103 MB: 102 us against 127; 2048 tokens over 16384 keys, 64 heads a shard: 2.07 ms against 2.17).
+    // A request of tiles f .. f + c - 1 then has units f nh .. (f + c) nh - 1, so unit u / nh is one of its tiles.
+    int i = u / s.nh, h = u - i * s.nh;
+    const int4 *e = (const int4 *)(s.tiles + i);
+    if (!heaviest) {
+        const int place = __ldcg(&e[1].w), f = place >> 16, c = place & 0xffff, v = u - f * s.nh;
+        h = v / c;
+        e = (const int4 *)(s.tiles + f + (v - h * c));
+    }
     const int4 x = __ldcg(e), y = __ldcg(e + 1);
-    return Work{heaviest ? b : a, x.x, x.y, x.w, x.z, y.x, y.y, min(y.z, x.w)};
+    return Work{h, x.x, x.y, x.w, x.z, y.x, y.y, min(y.z, x.w)};
 }
 // Unit of round k for CTA c of G: rounds alternate direction, so that every CTA gets a mix of heavy and light ones.
 __device__ __forceinline__ int unit_at(int k, int c, int G) { return (k & 1) ? (k + 1) * G - 1 - c : k * G + c; }
@@ -159,8 +164,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tslot;
     pdl_wait();   // units, limits, rows: all from the launches in front
-    const int n_tiles = __ldcg(p.ctl + 1), units = n_tiles * p.nh;
-    const bool heaviest = (long)__ldcg(p.ctl) * p.nh <= L2_KEYS;
+    const int units = __ldcg(p.ctl + 1) * p.nh;
+    const bool heaviest = __ldcg(p.ctl + 3) != 0;
     // Every role walks the same units in the same order and counts key tiles T across units, so ring slots and barrier
     // parities continue from one unit to the next.  This CTA's next unit from round k on, -1 behind the last:
     auto next_unit = [&](int &k) {
@@ -182,7 +187,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 bool ok = true;
                 int E = 0, n = 0, k = 0;   // ring entries, units so far
                 for (int u; ok && (u = next_unit(k)) >= 0; ++k) {
-                    const Work w = work_of(p, n_tiles, heaviest, u);
+                    const Work w = work_of(p, heaviest, u);
                     const int h = p.head_off + w.hl;
                     // once the softmax warps have moved the last unit's Q into TMEM
                     if (n > 0 && !wait(B_QREADY, (n - 1) & 1)) break;
@@ -214,7 +219,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 bool ok = true;
                 int T = 0, k = 0;
                 for (int u; ok && (u = next_unit(k)) >= 0; ++k) {
-                    const Work w = work_of(p, n_tiles, heaviest, u);
+                    const Work w = work_of(p, heaviest, u);
                     for (int j = 0; j < w.nt; ++j, ++T) {
                         const int s = T % VST;
                         ok = wait(B_VEMPTY + s, ((T / VST) & 1) ^ 1);   // (passes at first)
@@ -231,7 +236,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             bool ok = true;
             int T = 0, E = 0, n = 0, k = 0;
             for (int u; ok && (u = next_unit(k)) >= 0; ++k) {
-                const Work w = work_of(p, n_tiles, heaviest, u);
+                const Work w = work_of(p, heaviest, u);
                 ok = wait_all(B_QREADY, n & 1);   // this unit's Q is in TMEM
                 ++n;
                 for (int j = 0; j < w.nt && ok; ++j, ++T) {
@@ -282,7 +287,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             bool ok = true;
             int T = 0, n = 0, k = 0;
             for (int u; ok && (u = next_unit(k)) >= 0; ++k) {
-                const Work w = work_of(p, n_tiles, heaviest, u);
+                const Work w = work_of(p, heaviest, u);
                 ok = wait_all(B_OFREE, (n & 1) ^ 1);   // the last unit's O has been read (passes at first)
                 ++n;
                 for (int j = 0; j < w.nt && ok; ++j, ++T) {
@@ -347,7 +352,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         int T = 0, n = 0, k = 0, u = next_unit(k);
         if (u >= 0) load_q(0);
         while (u >= 0) {
-            const Work w = work_of(p, n_tiles, heaviest, u);
+            const Work w = work_of(p, heaviest, u);
             ++k;
             const int u_next = next_unit(k);
             // keys that the row, that every row of the warp sees (rows behind the tile's tokens: no matter what)
