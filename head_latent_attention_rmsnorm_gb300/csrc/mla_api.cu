@@ -1197,7 +1197,7 @@ mla_status paged_step_shape(const mla_dims *d, mla_dtype dt, int B, int n_tokens
     if (d && d->n_heads > 0 && (n_tokens < 0 || ((long)n_tokens + 3) * d->n_heads > INT_MAX / 4)) return MLA_ERR_SHAPE;
     mla_status st = paged_decode_shape(d, dt, std::min(n_tokens, PAGED_ROUND), page_size, max_pages, p);
     if (st != MLA_OK) return st;
-    if (B < 0) return MLA_ERR_SHAPE;
+    if (B < 0 || B > 1 << 24) return MLA_ERR_SHAPE;
     if (p->tc) p->row_tile = p->H <= 64 ? 64 : 128;   // few heads: several tokens of a request share an item
     p->row_tiles = (p->H + p->row_tile - 1) / p->row_tile;
     return MLA_OK;

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(1024) paged_evict_pick_kernel(const __grid_con
                 if (ids[c] >= 0) f(ordered(w[c]));
         }
     };
-    for (int i = tid; i < 512; i += nt) bins[0][i] = 0;   // (both)
+    for (int i = tid; i < 512; i += nt) bins[i >> 8][i & 255] = 0;
     const int2 sums = block_sums(held, n_may, sm);
     held = sums.x;
     n_may = sums.y;

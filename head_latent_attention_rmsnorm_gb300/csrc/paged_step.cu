@@ -18,8 +18,8 @@ namespace {
 
 // -------------------------------------------------------------------------- plan ----
 // Block 0 of NT threads, PER tokens each: a token's request by binary search of the prefix sums, the keys that
-// it sees; groups begin where a request's tokens do, where one is not computed here, and after every
-// `most` tokens; then the groups' tile sums and the workers' parts as for decode.
+// it sees; groups begin where a request's tokens do and after every `most` tokens; then the groups' tile sums and the
+// workers' parts as for decode.  The other blocks set `zero` to zero.
 constexpr int PNT = 1024, CU_NEAR = 4096;
 constexpr int FEW = 128, SOME = 512;   // tokens up to which a block of as many threads is enough (fewer warps to bring together)
 

@@ -8,6 +8,8 @@
 //   absorb     q and the rotated q_pe, each as a bf16 pair hi + lo; the division of the batch;
 //   attention  persistent clusters of two CTAs walk equal shares of all requests' key tiles;
 //   join       the partials' log-sum-exp merge and the product with W_V.
+// The same three compute the tokens of a step (STEP; paged_step.cu divides those): a request is then a group of tokens
+// that share an item, each row with its own number of keys.
 //
 // Attention.  One work item = 128 heads (fewer rows are zero-filled) of one request; its fp32
 // accumulator, 128 x 512, is a whole SM's tensor memory, so an item runs on two SMs:
@@ -134,7 +136,8 @@ __device__ __forceinline__ unsigned lo_blocks(Extra ex) {
 // multiply-adds a head, so it is bound by the weights' bytes until B is in the hundreds; the
 // products run on mma.sync (M = latent dims, N = requests: eight per step, no padding to 128
 // rows).  Block (head, 128 latent dims, group of up to 64 requests): the weight block and the group's
-// queries by cp.async, all in flight at once; the weights then stay in registers as A fragments.
+// queries by cp.async, all in flight at once; the weights then stay in registers as A fragments.  (Of the tokens of a
+// step that are listed, which may be few of those that the grid is for, a block takes several groups in turn.)
 // 128 heads, events around it alone: one request 10 us, 64 requests 17 us (20 with three
 // blocks an SM, whose 512 blocks took a second wave; 17 MB of weights, 2.5 us at the copy
 // peak; 19 MB of queries out).

@@ -67,7 +67,7 @@ def prefill_args(**over):
 
 
 COMMON = [
-    (dict(dims=None), -1), (dict(dtype=2), -3), (dict(B=-1), -2), (dict(n=-1), -2), (dict(pages=0), -2), (dict(page=0), -2),
+    (dict(dims=None), -1), (dict(dtype=2), -3), (dict(B=-1), -2), (dict(B=(1 << 24) + 1), -2), (dict(n=-1), -2), (dict(pages=0), -2), (dict(page=0), -2),
     (dict(max_pages=0), -2), (dict(pages=1 << 26), -2), (dict(max_pages=1 << 26), -2), (dict(n=1 << 25), -2),
     (dict(q=None), -1), (dict(table=None), -1), (dict(lens=None), -1), (dict(cu=None), -1), (dict(pos=None), -1),
     (dict(lse=None), -1), (dict(ws=None), -1), (dict(w=None), -1),
