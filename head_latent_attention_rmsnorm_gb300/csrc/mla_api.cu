@@ -1211,6 +1211,11 @@ void paged_round_carve(const PagedDecode &p, PagedRound *r, Carve &c) {
     r->groups = (int4 *)c.take(T * sizeof(int4));
 }
 
+PagedPlan paged_plan_of(const PagedDecode &p, const PagedStep &s, int s0, const PagedRound &r, unsigned long long *zero,
+                        long n_zero) {
+    return PagedPlan{s, s0, std::max(1, p.row_tile / p.H), r.lens, r.limits, r.of, r.groups, zero, n_zero};
+}
+
 // The buffers of the explicit form: none where the call cannot use it.
 struct PagedExplicit {
     PagedChunk c;
@@ -1323,7 +1328,7 @@ mla_status mla_paged_decode(const mla_dims *dims, mla_dtype dtype, int B, int nu
     p.out = out;
     p.lse = lse;
     g_last_path = p.tc ? 2 : 1;
-    return cuda_status(p.tc ? paged_decode_tc(p, (cudaStream_t)cuda_stream) : paged_decode_simt(p, (cudaStream_t)cuda_stream));
+    return cuda_status(p.tc ? paged_decode_tc(p, nullptr, (cudaStream_t)cuda_stream) : paged_decode_simt(p, nullptr, (cudaStream_t)cuda_stream));
 }
 
 size_t mla_paged_prefill_workspace(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int page_size, int max_pages,
@@ -1404,8 +1409,11 @@ mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n
         q.out = (char *)out + at * p.Dv * es;
         q.lse = lse + at;
         cudaStream_t cs = (cudaStream_t)cuda_stream;
-        MLA_TRY(launch_paged_plan(q, step, s0, r.lens, r.of, r.limits, r.groups, cs));
-        MLA_TRY(p.tc ? paged_decode_tc(q, cs) : paged_decode_simt(q, cs));
+        const PagedPlan plan = paged_plan_of(q, step, s0, r, nullptr, 0);
+        const bool in_absorb = plan_in_absorb(q, plan);
+        if (!in_absorb) MLA_TRY(launch_paged_plan(q, plan, cs));
+        const PagedPlan *here = in_absorb ? &plan : nullptr;
+        MLA_TRY(p.tc ? paged_decode_tc(q, here, cs) : paged_decode_simt(q, here, cs));
     }
     return MLA_OK;
 }
@@ -1476,9 +1484,12 @@ mla_status mla_paged_weights(const mla_dims *dims, mla_dtype dtype, int B, int n
         q.q_nope = (const char *)q_nope + at * p.Dn * es;
         q.q_pe = (const char *)q_pe + at * p.Dr * es;
         q.pos = positions + s0;
-        MLA_TRY(launch_paged_plan(q, step, s0, r.lens, r.of, r.limits, r.groups, cs, acc, s0 == 0 ? (long)pages : 0));
+        const PagedPlan plan = paged_plan_of(q, step, s0, r, acc, s0 == 0 ? (long)pages : 0);
+        const bool in_absorb = n_tokens > 0 && plan_in_absorb(q, plan);
+        if (!in_absorb) MLA_TRY(launch_paged_plan(q, plan, cs));
         if (n_tokens) {
-            MLA_TRY(p.tc ? paged_absorb_tc(q, cs) : paged_absorb_simt(q, cs));
+            const PagedPlan *here = in_absorb ? &plan : nullptr;
+            MLA_TRY(p.tc ? paged_absorb_tc(q, here, cs) : paged_absorb_simt(q, here, cs));
             MLA_TRY(launch_paged_weights(q, lse + at, acc, bits, cs));
         }
         s0 += PAGED_ROUND;

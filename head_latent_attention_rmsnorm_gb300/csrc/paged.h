@@ -74,10 +74,6 @@ struct PagedDecode {
     float *po32, *pl, *pscale;
     __half *po;
 };
-// The launches of a call: absorb, attention, join.  Of a step's tokens behind launch_paged_plan.
-cudaError_t paged_decode_simt(const PagedDecode &p, cudaStream_t st);
-cudaError_t paged_absorb_simt(const PagedDecode &p, cudaStream_t st);
-
 // A step: request b's tokens are rows cu[b] .. cu[b + 1] - 1 of n_tokens, each at its position; the request
 // holds lens[b] tokens, its new ones among them.
 struct PagedStep {
@@ -87,10 +83,27 @@ struct PagedStep {
 // Tokens of one round of the absorbed form: a step of more takes several (queries and partials are 570 KB a token at 128
 // heads; a round costs four launches, of which a step whose tokens all go explicit has nothing).
 constexpr int PAGED_ROUND = 4096;
-// The plan of tokens s0 .. s0 + p.T - 1: their groups, and the division of the groups' tiles (p.lens, p.of,
-// p.limits, p.groups are written; p.B = p.T); n_zero words at `zero` are set to zero.
-cudaError_t launch_paged_plan(const PagedDecode &p, const PagedStep &s, int s0, int *lens, int2 *of, int *limits, int4 *groups,
-                              cudaStream_t st, unsigned long long *zero = nullptr, long n_zero = 0);
+// The plan of tokens s0 .. s0 + p.T - 1: their groups of `most` at most, and the division of the groups' tiles (what is
+// written are p's lens, of, limits and groups; p.B = p.T); n_zero words at `zero` are set to zero.
+struct PagedPlan {
+    PagedStep s;
+    int s0, most;
+    int *lens, *limits;
+    int2 *of;
+    int4 *groups;
+    unsigned long long *zero;
+    long n_zero;
+};
+cudaError_t launch_paged_plan(const PagedDecode &p, const PagedPlan &s, cudaStream_t st);
+// Few tokens, not of a list: the absorb's first block divides them, as decode's does, which saves a launch.
+inline bool plan_in_absorb(const PagedDecode &p, const PagedPlan &s) {
+    return p.T <= 128 && !p.list && s.s.B <= 1024 && s.n_zero <= 4096;
+}
+
+// The launches of a call: absorb, attention, join.  `plan` of a step's tokens: theirs, for the absorb to make (null: made
+// by launch_paged_plan in front, or decode's).
+cudaError_t paged_decode_simt(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st);
+cudaError_t paged_absorb_simt(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st);
 
 // The explicit form of the requests with many tokens (tensor cores), CHUNK_MIN and more.  Tiles of 128 tokens: at most
 // n_tokens / 128 and one more a request.  CHUNK_RESTS: tiles of 128 keys that have the rest of K_nope.
@@ -130,8 +143,8 @@ cudaError_t paged_weights_read_and_clear_error(unsigned *flags, cudaStream_t st)
 // pairs of SMs of a GB300, keys per tile (no worker waits for another: with fewer SMs free they take turns)
 constexpr int PAGED_TC_WORKERS = 76, PAGED_TC_TILE = 64;
 bool paged_tc_supported(int Dk, int Dn, int Dr, int Dv, int page);
-cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st);
-cudaError_t paged_absorb_tc(const PagedDecode &p, cudaStream_t st);
+cudaError_t paged_decode_tc(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st);
+cudaError_t paged_absorb_tc(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st);
 cudaError_t paged_tc_read_and_clear_error(unsigned *flags, cudaStream_t st);
 
 }  // namespace mla

@@ -200,6 +200,105 @@ __device__ void plan_block(const PagedDecode &p, int *sm = nullptr, int room = 0
     else plan_parts<NT, STEP>(p, p.tile_off, carry * p.row_tiles);
 }
 
+// ------------------------------------------------------------------ plan of a step ----
+// A block of NT threads, PER tokens each: a token's request by binary search of the prefix sums, the keys that it
+// sees; groups begin where a request's tokens do and after every `most` tokens; then the groups' tile sums and
+// the workers' parts as for decode.  `sm`: plan_ints(NT PER, B) ints.
+constexpr int CU_NEAR = 4096;   // requests whose prefix sums are kept at hand
+inline size_t plan_ints(int most, int B) { return 4 * (size_t)most + 1 + (B < CU_NEAR ? B + 1 : 0); }
+
+template <int NT, int PER>
+__device__ void plan_tokens(const PagedDecode &p, const PagedPlan &a, int T, int *sm) {
+    __shared__ int warp_tot[NT / 32];
+    constexpr int MOST = NT * PER;
+    const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
+    int *lim = sm, *req = lim + MOST, *sums = req + MOST, *tok = sums + MOST + 1, *near = tok + MOST;
+    const bool here = a.s.B < CU_NEAR;
+    if (here) {
+        for (int i = tid; i <= a.s.B; i += NT) near[i] = a.s.cu[i];
+        __syncthreads();
+    }
+    const int *cu = here ? near : a.s.cu;
+    const int cap = p.max_pages * p.page;
+    for (int i = tid; i < T; i += NT) {
+        const int t = p.list ? __ldcg(p.list + i) : a.s0 + i;
+        int lo = 0, hi = a.s.B;   // the first request whose tokens end behind t
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (cu[mid + 1] > t) hi = mid;
+            else lo = mid + 1;
+        }
+        const bool in = lo < a.s.B && cu[lo] <= t;
+        req[i] = in ? lo : -1;
+        tok[i] = t;
+        int n = 0;
+        if (in) {
+            const int pos = a.s.positions[t], keys = min(max(a.s.lens[lo], 0), cap);
+            n = pos < 0 ? 0 : min(keys, pos == 2147483647 ? pos : pos + 1);
+        }
+        lim[i] = a.limits[i] = n;
+    }
+    __syncthreads();
+    // which tokens begin a group
+    const int i0 = PER * tid;
+    int first[PER], place[PER];   // place: among the request's tokens of this round
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        const int i = i0 + e;
+        first[e] = place[e] = 0;
+        if (i >= T || req[i] < 0) continue;
+        int lo = 0, hi = i;   // the request's first token here
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (tok[mid] >= cu[req[i]]) hi = mid;
+            else lo = mid + 1;
+        }
+        place[e] = i - lo;
+        first[e] = i == 0 || req[i - 1] != req[i] || place[e] % a.most == 0;
+    }
+    int own = 0;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) own += first[e];
+    int x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_tot[wp] = x;
+    __syncthreads();
+    int g = x - own, all = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) {
+        if (i < wp) g += warp_tot[i];
+        all += warp_tot[i];
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        const int i = i0 + e;
+        if (i >= T) continue;
+        if (req[i] < 0) a.of[i] = make_int2(-1, 0);
+        if (!first[e]) continue;
+        // the group's tokens: up to the next beginning
+        const int b = req[i];
+        int n = 0, most = 0;
+        for (int k = i; k < T && req[k] == b && (k == i || (place[e] + k - i) % a.most); ++k, ++n) {
+            a.of[k] = make_int2(g, n * p.H);
+            most = max(most, lim[k]);
+        }
+        a.groups[g] = make_int4(b, i * p.H, n * p.H, 0);
+        a.lens[g] = most;
+        ++g;
+    }
+    for (int i = all + tid; i < p.B; i += NT) {
+        a.lens[i] = 0;
+        a.groups[i] = make_int4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    if (p.parts) plan_block<NT, true>(p, sums, MOST + 1);
+    else plan_block<NT, true>(p);
+}
+
 // Started early, behind the kernel in front of it (programmatic dependent launch): the kernel waits for that one's
 // end before it touches memory (pdl_wait).  Against plain launches a call that the GPU bounds took 2.7 us
 // less back to back (one request of 4096 keys, 128 heads: 32.8 -> 30.0 us), a small kernel in a graph 0.2-0.6.

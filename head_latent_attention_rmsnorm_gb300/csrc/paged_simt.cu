@@ -36,17 +36,24 @@ constexpr int VC = 32;          // value dims of a join block
 // flight at once.  One block more forms the tile prefix sums.
 template <typename T>
 __global__ void __launch_bounds__(NT) paged_absorb_simt_kernel(const __grid_constant__ PagedDecode p,
-                                                               const __grid_constant__ Turns turns) {
+                                                               const __grid_constant__ Turns turns,
+                                                               const __grid_constant__ PagedPlan plan) {
     extern __shared__ float sm[];   // q [BT][Dn], sums [8 warps][BT][DC]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int groups = (p.T + BT - 1) / BT, chunks = (p.Dk + DC - 1) / DC;
-    // a step's plan is the launch in front and runs beside this one, as in the tensor-core form
-    const bool step = p.pos != nullptr;
-    if (!step) pdl_wait();
+    // a step's plan, but for few tokens, is the launch in front and runs beside this one, as in the tensor-core form
+    const bool step = p.pos != nullptr, behind = step && !plan.s.cu;
+    if (!behind) pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x == 0) {
-        if (!step) plan_block<NT, false>(p);
-        else pdl_wait();
+        if (behind) {
+            pdl_wait();
+        } else if (step) {
+            for (int i = tid; i < plan.n_zero; i += NT) plan.zero[i] = 0;
+            plan_tokens<NT, 1>(p, plan, p.T, (int *)sm);
+        } else {
+            plan_block<NT, false>(p);
+        }
         return;
     }
     int u = blockIdx.x - 1;
@@ -98,7 +105,7 @@ __global__ void __launch_bounds__(NT) paged_absorb_simt_kernel(const __grid_cons
         for (int k = 0; k < NT / 32; ++k) x += sum[(k * BT + j) * DC + d];
         if (j < nb && d0 + d < p.Dk) ((float *)p.qabs)[((long)(b0 + j) * p.H + h) * p.Dk + d0 + d] = x;
     }
-    if (step) pdl_wait();
+    if (behind) pdl_wait();
 }
 
 // --------------------------------------------------------------------- attention ----
@@ -489,25 +496,26 @@ __global__ void __launch_bounds__(NT) paged_join_simt_kernel(const __grid_consta
 }
 
 template <typename T>
-cudaError_t absorb_simt(const PagedDecode &p, cudaStream_t st) {
+cudaError_t absorb_simt(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st) {
     Turns turns{};
     std::copy_n(paged_turns(p.base, p.Dr), p.Dr / 2, turns.v);
     const unsigned blocks = (unsigned)((p.T + BT - 1) / BT) * (unsigned)p.H * (unsigned)((p.Dk + DC - 1) / DC);
-    const size_t sm = ((size_t)BT * p.Dn + (size_t)NT / 32 * BT * DC) * 4;
+    size_t sm = ((size_t)BT * p.Dn + (size_t)NT / 32 * BT * DC) * 4;
+    if (plan) sm = std::max(sm, plan_ints(NT, plan->s.B) * sizeof(int));
     const cudaError_t e = cudaFuncSetAttribute(paged_absorb_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     if (e != cudaSuccess) return e;
     ProfScope ps("paged_absorb", st);
-    return launch_after(paged_absorb_simt_kernel<T>, blocks + 1, NT, sm, st, p, turns);
+    return launch_after(paged_absorb_simt_kernel<T>, blocks + 1, NT, sm, st, p, turns, plan ? *plan : PagedPlan{});
 }
 
 template <typename T>
-cudaError_t decode_simt(const PagedDecode &p, cudaStream_t st) {
+cudaError_t decode_simt(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st) {
     const unsigned jblocks = (unsigned)((p.T + BT - 1) / BT) * (unsigned)p.H * (unsigned)((p.Dv + VC - 1) / VC);
     const size_t s2 = (size_t)layout(p.Dk, p.Dr).total * 4, s3 = (size_t)BT * p.Dk * 4;
     cudaError_t e;
     if ((e = cudaFuncSetAttribute(paged_attn_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2)) != cudaSuccess)
         return e;
-    if ((e = absorb_simt<T>(p, st)) != cudaSuccess) return e;
+    if ((e = absorb_simt<T>(p, plan, st)) != cudaSuccess) return e;
     {
         ProfScope ps("paged_attn", st);
         e = launch_after(paged_attn_simt_kernel<T>, (unsigned)p.workers, NT, s2, st, p);
@@ -522,12 +530,12 @@ cudaError_t decode_simt(const PagedDecode &p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t paged_absorb_simt(const PagedDecode &p, cudaStream_t st) {
-    return p.ty == TY_F32 ? absorb_simt<float>(p, st) : absorb_simt<__nv_bfloat16>(p, st);
+cudaError_t paged_absorb_simt(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st) {
+    return p.ty == TY_F32 ? absorb_simt<float>(p, plan, st) : absorb_simt<__nv_bfloat16>(p, plan, st);
 }
 
-cudaError_t paged_decode_simt(const PagedDecode &p, cudaStream_t st) {
-    return p.ty == TY_F32 ? decode_simt<float>(p, st) : decode_simt<__nv_bfloat16>(p, st);
+cudaError_t paged_decode_simt(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st) {
+    return p.ty == TY_F32 ? decode_simt<float>(p, plan, st) : decode_simt<__nv_bfloat16>(p, plan, st);
 }
 
 }  // namespace mla

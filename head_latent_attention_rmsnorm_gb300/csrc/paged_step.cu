@@ -17,35 +17,24 @@ using tc::pdl_wait;
 namespace {
 
 // -------------------------------------------------------------------------- plan ----
-// Block 0 of NT threads, PER tokens each: a token's request by binary search of the prefix sums, the keys that
-// it sees; groups begin where a request's tokens do and after every `most` tokens; then the groups' tile sums and the
-// workers' parts as for decode.  The other blocks set `zero` to zero.
-constexpr int PNT = 1024, CU_NEAR = 4096;
-constexpr int FEW = 128, SOME = 512;   // tokens up to which a block of as many threads is enough (fewer warps to bring together)
+// Block 0 divides (plan_tokens); the others set `zero` to zero.
+constexpr int PNT = 1024;
+constexpr int SOME = 512;   // tokens up to which a block of as many threads is enough (fewer warps to bring together)
 
 struct Plan {
     PagedDecode p;
-    PagedStep s;
-    int s0, most;   // first token of the round; tokens of a group at most
-    int *lens, *limits;
-    int2 *of;
-    int4 *groups;
-    unsigned long long *zero;
-    long n_zero;
+    PagedPlan s;
 };
 
 template <int NT, int PER>
 __global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ Plan a) {
     extern __shared__ int sm[];
-    __shared__ int warp_tot[NT / 32];
-    constexpr int MOST = NT * PER;
     const PagedDecode &p = a.p;
-    const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
-    int *lim = sm, *req = lim + MOST, *sums = req + MOST, *tok = sums + MOST + 1, *near = tok + MOST;
+    const int tid = threadIdx.x;
     pdl_wait();
     pdl_launch_dependents();   // the absorb beside this; what follows it waits for both
     if (blockIdx.x > 0) {
-        for (long i = (long)(blockIdx.x - 1) * NT + tid; i < a.n_zero; i += (long)(gridDim.x - 1) * NT) a.zero[i] = 0;
+        for (long i = (long)(blockIdx.x - 1) * NT + tid; i < a.s.n_zero; i += (long)(gridDim.x - 1) * NT) a.s.zero[i] = 0;
         return;
     }
     const int T = tokens_of(p);
@@ -53,90 +42,7 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ 
         for (int i = tid; i < 2 * p.workers; i += NT) p.first[i] = 0;
         return;
     }
-    const bool here = a.s.B < CU_NEAR;
-    if (here) {
-        for (int i = tid; i <= a.s.B; i += NT) near[i] = a.s.cu[i];
-        __syncthreads();
-    }
-    const int *cu = here ? near : a.s.cu;
-    const int cap = p.max_pages * p.page;
-    for (int i = tid; i < T; i += NT) {
-        const int t = p.list ? __ldcg(p.list + i) : a.s0 + i;
-        int lo = 0, hi = a.s.B;   // the first request whose tokens end behind t
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (cu[mid + 1] > t) hi = mid;
-            else lo = mid + 1;
-        }
-        const bool in = lo < a.s.B && cu[lo] <= t;
-        req[i] = in ? lo : -1;
-        tok[i] = t;
-        int n = 0;
-        if (in) {
-            const int pos = a.s.positions[t], keys = min(max(a.s.lens[lo], 0), cap);
-            n = pos < 0 ? 0 : min(keys, pos == 2147483647 ? pos : pos + 1);
-        }
-        lim[i] = a.limits[i] = n;
-    }
-    __syncthreads();
-    // which tokens begin a group
-    const int i0 = PER * tid;
-    int first[PER], place[PER];   // place: among the request's tokens of this round
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-        const int i = i0 + e;
-        first[e] = place[e] = 0;
-        if (i >= T || req[i] < 0) continue;
-        int lo = 0, hi = i;   // the request's first token here
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (tok[mid] >= cu[req[i]]) hi = mid;
-            else lo = mid + 1;
-        }
-        place[e] = i - lo;
-        first[e] = i == 0 || req[i - 1] != req[i] || place[e] % a.most == 0;
-    }
-    int own = 0;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) own += first[e];
-    int x = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_tot[wp] = x;
-    __syncthreads();
-    int g = x - own, all = 0;
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) {
-        if (i < wp) g += warp_tot[i];
-        all += warp_tot[i];
-    }
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-        const int i = i0 + e;
-        if (i >= T) continue;
-        if (req[i] < 0) a.of[i] = make_int2(-1, 0);
-        if (!first[e]) continue;
-        // the group's tokens: up to the next beginning
-        const int b = req[i];
-        int n = 0, most = 0;
-        for (int k = i; k < T && req[k] == b && (k == i || (place[e] + k - i) % a.most); ++k, ++n) {
-            a.of[k] = make_int2(g, n * p.H);
-            most = max(most, lim[k]);
-        }
-        a.groups[g] = make_int4(b, i * p.H, n * p.H, 0);
-        a.lens[g] = most;
-        ++g;
-    }
-    for (int i = all + tid; i < p.B; i += NT) {
-        a.lens[i] = 0;
-        a.groups[i] = make_int4(0, 0, 0, 0);
-    }
-    __syncthreads();
-    if (p.parts) plan_block<NT, true>(p, sums, MOST + 1);
-    else plan_block<NT, true>(p);
+    plan_tokens<NT, PER>(p, a.s, T, sm);
 }
 
 // The sum of the values of the threads in front, and of all, by a block of NT threads.
@@ -451,18 +357,17 @@ cudaError_t launch_paged_chunk(const PagedDecode &p, const PagedStep &s, const P
     return launch_after(paged_gather_kernel, 152 * 4, 256, 0, st, g);
 }
 
-cudaError_t launch_paged_plan(const PagedDecode &p, const PagedStep &s, int s0, int *lens, int2 *of, int *limits, int4 *groups,
-                              cudaStream_t st, unsigned long long *zero, long n_zero) {
-    Plan a{p, s, s0, std::max(1, p.row_tile / p.H), lens, limits, of, groups, zero, n_zero};
-    const unsigned nt = p.T <= FEW ? FEW : p.T <= SOME ? SOME : PNT;
-    auto kern = nt == FEW ? paged_plan_kernel<FEW, 1> : nt == SOME ? paged_plan_kernel<SOME, 1> : paged_plan_kernel<PNT, PAGED_ROUND / PNT>;
-    const size_t sm = (4 * (nt < PNT ? (int)nt : PAGED_ROUND) + 1 + (s.B < CU_NEAR ? s.B + 1 : 0)) * sizeof(int);
+cudaError_t launch_paged_plan(const PagedDecode &p, const PagedPlan &s, cudaStream_t st) {
+    const Plan a{p, s};
+    const unsigned nt = p.T <= SOME ? SOME : PNT;
+    auto kern = nt == SOME ? paged_plan_kernel<SOME, 1> : paged_plan_kernel<PNT, PAGED_ROUND / PNT>;
+    const size_t sm = plan_ints(nt == SOME ? SOME : PAGED_ROUND, s.s.B) * sizeof(int);
     if (sm > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
         if (e != cudaSuccess) return e;
     }
     ProfScope ps("paged_plan", st);
-    return launch_after(kern, 1 + (unsigned)std::min((n_zero + nt - 1) / nt, 150l), nt, sm, st, a);
+    return launch_after(kern, 1 + (unsigned)std::min((s.n_zero + nt - 1) / nt, 150l), nt, sm, st, a);
 }
 
 }  // namespace mla

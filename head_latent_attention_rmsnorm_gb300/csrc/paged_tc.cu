@@ -195,22 +195,29 @@ __device__ void rotate_queries(const Absorb &a, int i, int lane) {
 }
 
 template <bool STEP>
-__global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_constant__ Absorb a) {
+__global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_constant__ Absorb a, const __grid_constant__ PagedPlan plan) {
     extern __shared__ __align__(1024) uint8_t sm[];
     const PagedDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // A step's plan is the launch in front and runs beside this one (it began behind the end of all before it,
-    // and nothing here reads what it writes): the wait for it is at each block's end, for the launch behind.
-    if (!STEP) pdl_wait();
+    // A step's plan, but for few tokens, is the launch in front and runs beside this one (it began behind the end of all
+    // before it, and nothing here reads what it writes): the wait for it is at each block's end, for the launch behind.
+    const bool behind = STEP && !plan.s.cu;
+    if (!behind) pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x == 0) {
-        if (!STEP) plan_block<128, false>(p, (int *)sm, AB_SMEM / 4);
-        else pdl_wait();
+        if (behind) {
+            pdl_wait();
+        } else if (STEP) {
+            for (int i = tid; i < plan.n_zero; i += 128) plan.zero[i] = 0;
+            plan_tokens<128, 1>(p, plan, p.T, (int *)sm);
+        } else {
+            plan_block<128, false>(p, (int *)sm, AB_SMEM / 4);
+        }
         return;
     }
     if ((int)blockIdx.x <= a.rot_blocks) {
         rotate_queries<STEP>(a, ((int)blockIdx.x - 1) * 4 + warp, lane);
-        if (STEP) pdl_wait();
+        if (behind) pdl_wait();
         return;
     }
     uint8_t *sq = sm + DN * AB_PITCH;
@@ -300,7 +307,7 @@ __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_const
         asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
         __syncthreads();
     }
-    if (STEP) pdl_wait();
+    if (behind) pdl_wait();
 }
 
 // -------------------------------------------------------------------------- join ----
@@ -1441,13 +1448,14 @@ Absorb absorb_of(const PagedDecode &p) {
 }
 }  // namespace
 
-cudaError_t paged_absorb_tc(const PagedDecode &p, cudaStream_t st) {
+cudaError_t paged_absorb_tc(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st) {
+    static_assert((4 * 128 + 1 + 1025) * 4 <= AB_SMEM, "the plan's room");
     const Absorb ab = absorb_of(p);
     auto kern = p.groups ? paged_absorb_tc_kernel<true> : paged_absorb_tc_kernel<false>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM);
     if (e != cudaSuccess) return e;
     ProfScope ps("paged_absorb", st);
-    return launch_after(kern, (unsigned)(p.H * 4 * ab.blocks + 1 + ab.rot_blocks), 128, AB_SMEM, st, ab);
+    return launch_after(kern, (unsigned)(p.H * 4 * ab.blocks + 1 + ab.rot_blocks), 128, AB_SMEM, st, ab, plan ? *plan : PagedPlan{});
 }
 
 namespace {
@@ -1464,7 +1472,7 @@ auto attn_kernel(int unit, bool paired) {
 }
 }  // namespace
 
-cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
+cudaError_t paged_decode_tc(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st) {
     using ull = unsigned long long;
     cudaError_t e;
     const ull rows = (ull)p.num_pages * p.page, heads = (ull)p.T * p.H;
@@ -1513,7 +1521,7 @@ cudaError_t paged_decode_tc(const PagedDecode &p, cudaStream_t st) {
     auto attn = p.groups ? attn_kernel<true>(unit, p.row_tile <= 64) : attn_kernel<false>(unit, p.row_tile <= 64);
     if ((e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess)
         return e;
-    if ((e = paged_absorb_tc(p, st)) != cudaSuccess) return e;
+    if ((e = paged_absorb_tc(p, plan, st)) != cudaSuccess) return e;
     {
         ProfScope ps("paged_attn", st);
         e = launch_after(attn, 2 * p.workers, NTHREADS, SMEM_BYTES, st, m, at);

@@ -519,6 +519,14 @@ cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st) {
         if ((e = make_tma_map(&mV, p.vws, 3, dv, sv, box)) != cudaSuccess) return e;
     }
     if ((e = cudaFuncSetAttribute(tc_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S_BYTES)) != cudaSuccess) return e;
+    // the register split waits for ever where the launch has fewer to draw on: another compiler's choice is refused
+    static int regs = 0;
+    if (regs == 0) {
+        cudaFuncAttributes at;
+        if ((e = cudaFuncGetAttributes(&at, tc_step_kernel)) != cudaSuccess) return e;
+        regs = at.numRegs;
+    }
+    if (NTHREADS * regs < 128 * (REGS_ISSUE + 2 * REGS_SOFTMAX)) return cudaErrorInvalidConfiguration;
     int dev = 0, n_sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&n_sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
