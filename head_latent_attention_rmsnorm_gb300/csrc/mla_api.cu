@@ -1251,12 +1251,12 @@ void paged_explicit_carve(const PagedDecode &p, int B, int n_tokens, int key_row
 }
 
 size_t paged_prefill_ws(PagedDecode *p, PagedRound *r, PagedExplicit *x, int B, int n_tokens, int key_rows, int head_shard, void *base) {
-    Carve c;
-    c.base = (char *)base;
+    Carve c;   // from a 32-byte boundary of the workspace on, which may begin at a 16-byte one: its rows are written 32 bytes at a time
+    c.base = base ? (char *)align_up((size_t)base, 32) : nullptr;
     paged_decode_carve(p, c);
     paged_round_carve(*p, r, c);
     paged_explicit_carve(*p, B, n_tokens, key_rows, head_shard, x, c);
-    return align_up(c.off, 256);
+    return align_up(c.off, 256) + 32;
 }
 
 mla_status paged_weights_shape(const mla_dims *d, mla_dtype dt, int B, int n_tokens, int page_size, int max_pages,

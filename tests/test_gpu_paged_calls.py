@@ -69,6 +69,18 @@ def test_allocates_for_the_launch_stream(name, kind):
     assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("off", [16, 32, 48])
+@pytest.mark.parametrize("name", list(CALLS))
+def test_workspace_at_any_16_bytes(name, off):
+    call = CALLS[name]()
+    want = [x.clone() for x in flat(call())]
+    room = torch.empty((512 << 20) + off, dtype=torch.uint8, device="cuda")
+    assert room.data_ptr() % 32 == 0
+    got = flat(call(workspace=room[off:]))
+    torch.cuda.synchronize()
+    assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_evict_on_a_stream():
     call = evict()
     want = [x.clone() for x in call()]
