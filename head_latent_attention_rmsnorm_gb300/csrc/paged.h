@@ -146,5 +146,6 @@ bool paged_tc_supported(int Dk, int Dn, int Dr, int Dv, int page);
 cudaError_t paged_decode_tc(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st);
 cudaError_t paged_absorb_tc(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st);
 cudaError_t paged_tc_read_and_clear_error(unsigned *flags, cudaStream_t st);
+cudaError_t paged_many_read_and_clear_error(unsigned *flags, cudaStream_t st);
 
 }  // namespace mla

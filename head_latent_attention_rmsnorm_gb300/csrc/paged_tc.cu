@@ -68,8 +68,7 @@
 
 #include <algorithm>
 
-#include "paged_common.cuh"
-#include "tc_common.cuh"
+#include "paged_tc.cuh"
 #include "tc_internal.h"
 
 namespace mla {
@@ -80,10 +79,8 @@ namespace {
 
 using namespace tc;
 using namespace paged;
-using bf16 = __nv_bfloat16;
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int DK = 512, DN = 128, DR = 64, DV = 128;
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -102,34 +99,6 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
 }
-__device__ __forceinline__ void cp16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-// x as hi + lo in bf16 (hi its rounding, lo the rounding of the rest)
-__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
-    hi = pack_bf16(x, y);
-    lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
-}
-// the same, and what lo leaves
-__device__ __forceinline__ void split3(float x, float y, uint32_t &hi, uint32_t &lo, uint32_t &rest) {
-    hi = pack_bf16(x, y);
-    x -= __uint_as_float(hi << 16);
-    y -= __uint_as_float(hi & 0xffff0000u);
-    split2(x, y, lo, rest);
-}
-
-// What a request's scores and log-sum-exp take of the queries besides q_hi and the band's hi and lo
-// (the header's part on precision).
-enum Extra { EX_NONE, EX_LATENT, EX_WIDE, EX_BAND };
-constexpr int SHORT_KEYS = 64, WIDE_KEYS = 1024, MIDDLE_KEYS = 4096;
-__device__ __forceinline__ Extra extra_of(bool paired, int keys) {
-    if (keys <= SHORT_KEYS) return EX_BAND;
-    return paired || keys > MIDDLE_KEYS ? EX_NONE : (keys > WIDE_KEYS ? EX_LATENT : EX_WIDE);
-}
-// The blocks of 64 latent dims, as bits, whose q_lo has MMAs of its own above 64 heads (up to 64 all have idle rows).
-__device__ __forceinline__ unsigned lo_blocks(Extra ex) {
-    return ex == EX_NONE ? 0 : (ex == EX_LATENT ? 0x3 : (ex == EX_WIDE ? 0xf : 0xe));
-}
 
 // ------------------------------------------------------------------------ absorb ----
 // q[b, h, :] = W_K(h)^T q_nope[b, h, :]: streams 16 KB x heads x 8 of weights for B x 128 x 512
@@ -145,54 +114,6 @@ constexpr int AB_DIMS = 128, AB_PITCH = 256 + 16, AB_GROUP = 64;
 constexpr int AB_OUT = 40;              // halves per request of a warp's staging (32 dims + pad)
 constexpr int AB_SMEM = DN * AB_PITCH + AB_GROUP * AB_PITCH + AB_GROUP * 4;   // four blocks an SM
 static_assert(4 * 3 * 8 * AB_OUT * 2 <= DN * AB_PITCH, "the staging lies where the weights were");
-
-struct Absorb {
-    PagedDecode p;
-    bf16 *qhi, *qlo, *qrest, *rhi, *rlo, *rrest;   // [B][H][512], [B][H][64]; the rests of short requests only
-    int groups, group;             // groups of `group` requests
-    int blocks;                    // blocks that share them out, of each head and 128 dims: the groups, but for a list
-    int rot_blocks;                // blocks 1 .. rot_blocks rotate the queries; block 0 divides the batch
-    Turns64 turns;
-};
-
-// The queries' rotation: a warp per token and 32 heads, a lane per pair of dims, the angle formed once.
-template <bool STEP>
-__device__ void rotate_queries(const Absorb &a, int i, int lane) {
-    const PagedDecode &p = a.p;
-    const int per = (p.H + 31) / 32, b = i / per, h0 = i % per * 32;
-    if (b >= (STEP ? tokens_of(p) : p.B)) return;
-    const int t = STEP ? token_of(p, b) : b;
-    // (a step's tokens may see few keys whatever their position)
-    const int keys = !STEP ? keys_of(p, b) : p.scores_only ? 2147483647 : 0;
-    const float2 cs = turn_cs(a.turns.v[lane], STEP ? p.pos[t] : keys - 1);
-    const int h1 = min(h0 + 32, p.H);
-#pragma unroll 1
-    for (int h = h0; h < h1; h += 8) {
-        uint16_t x0[8], x1[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint16_t *x = (const uint16_t *)p.q_pe + ((long)t * p.H + min(h + j, h1 - 1)) * DR + lane;
-            x0[j] = x[0];
-            x1[j] = x[32];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (h + j >= h1) break;
-            const long o = ((long)b * p.H + h + j) * DR + lane;
-            const float f0 = __uint_as_float((uint32_t)x0[j] << 16), f1 = __uint_as_float((uint32_t)x1[j] << 16);
-            uint32_t hi, lo, rest;
-            split3(f0 * cs.x - f1 * cs.y, f1 * cs.x + f0 * cs.y, hi, lo, rest);
-            ((uint16_t *)a.rhi)[o] = (uint16_t)hi;
-            ((uint16_t *)a.rhi)[o + 32] = (uint16_t)(hi >> 16);
-            ((uint16_t *)a.rlo)[o] = (uint16_t)lo;
-            ((uint16_t *)a.rlo)[o + 32] = (uint16_t)(lo >> 16);
-            if (keys <= SHORT_KEYS) {
-                ((uint16_t *)a.rrest)[o] = (uint16_t)rest;
-                ((uint16_t *)a.rrest)[o + 32] = (uint16_t)(rest >> 16);
-            }
-        }
-    }
-}
 
 template <bool STEP>
 __global__ void __launch_bounds__(128) paged_absorb_tc_kernel(const __grid_constant__ Absorb a, const __grid_constant__ PagedPlan plan) {
@@ -1446,11 +1367,19 @@ Absorb absorb_of(const PagedDecode &p) {
     std::copy_n(paged_turns(p.base, DR), DR / 2, ab.turns.v);
     return ab;
 }
+// Many tokens of a step (their plan is a launch of its own then): tiles of 128, a block an SM.  The absorb's from as many
+// (head, tile) as half the SMs on: 20 heads, 512 tokens 17.5 us against 23.9 (80 of them), 32 heads, 144 tokens 15.3 against
+// 12.4 to 14.2 (64).  The join's where the other's blocks would take three turns of 32 tokens: 32 heads of 1000 keys, 320
+// tokens 18 us against 34, 144 tokens (two turns) 17 against 23, but with 8000 keys, whose tokens come in four parts and
+// more, 30 against 17 (two turns) and 31 against 27 (three).
+bool absorbs_many(const PagedDecode &p) { return (long)p.H * ((p.T + 127) / 128) >= PAGED_TC_WORKERS; }
+bool joins_many(const PagedDecode &p, int per_head) { return (p.T + JB - 1) / JB > 2 * per_head; }
 }  // namespace
 
 cudaError_t paged_absorb_tc(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st) {
     static_assert((4 * 128 + 1 + 1025) * 4 <= AB_SMEM, "the plan's room");
     const Absorb ab = absorb_of(p);
+    if (p.groups && !plan && absorbs_many(p)) return paged_absorb_many(ab, st);
     auto kern = p.groups ? paged_absorb_tc_kernel<true> : paged_absorb_tc_kernel<false>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM);
     if (e != cudaSuccess) return e;
@@ -1527,6 +1456,7 @@ cudaError_t paged_decode_tc(const PagedDecode &p, const PagedPlan *plan, cudaStr
         e = launch_after(attn, 2 * p.workers, NTHREADS, SMEM_BYTES, st, m, at);
     }
     if (e != cudaSuccess) return e;
+    if (p.groups && !plan && joins_many(p, per_head)) return paged_join_many(p, ab.qlo, ab.qrest, st);
     {
         ProfScope ps("paged_join", st);
         e = launch_after(join, (unsigned)(p.H * per_head), JNT, JSMEM, st, mW, p, (const bf16 *)ab.qlo,

@@ -629,6 +629,7 @@ cudaError_t tc_read_and_clear_error(unsigned int *flags, cudaStream_t st) {
     if (e == cudaSuccess) e = tc_bwd_read_and_clear_error(flags, st);
     if (e == cudaSuccess) e = simt_read_and_clear_error(flags, st);
     if (e == cudaSuccess) e = paged_tc_read_and_clear_error(flags, st);
+    if (e == cudaSuccess) e = paged_many_read_and_clear_error(flags, st);
     if (e == cudaSuccess) e = paged_weights_read_and_clear_error(flags, st);
     if (e == cudaSuccess) e = tc_step_read_and_clear_error(flags, st);
     return e;
