@@ -69,14 +69,14 @@ __device__ long block_before(long n, long *warp_tot, long &all) {
 }
 
 // ----------------------------------------------------------------- explicit plan ----
-// Which form is cheaper.  A (token, key, head) costs 2 (512 + 64 + 512) = 2176 operations absorbed and 2 (192 + 128) =
-// 640 explicit, which has 2 * 256 * 512 on top for a key and head, once for all of the request's tokens: equal at 171
-// tokens, whatever the keys and heads.  Besides, an absorbed token costs as much as some 2500 keys of its own (its
-// queries, a part's beginning and end, its share of the join), so a request goes explicit from 192 keys / (keys + 2560)
-// tokens on, at least CHUNK_MIN, where its keys' rows, rounded up to whole tiles, fit in what the requests in front of it
-// left of the buffers.  Measured, explicit / absorbed, us: 128 heads, one request of 8192 keys, 128 tokens 383 / 272, 192
-// 389 / 408; four of 2048, 64 tokens 377 / 273, 96 380 / 403; 16 heads, four of 8192, 96 tokens 216 / 207, 128 217 / 253;
-// 16 of 2048, 64 tokens 217 / 203, 96 220 / 302; 16 of 200, 64 tokens 78 / 109.
+// Which form is cheaper.  Absorbed, a token costs its share of an item, r query rows of up to 128 (or 64, which take as
+// long): 0.17 ns a key of its own and as much as 12 r keys more for its queries, a part's beginning and end and its share of
+// the join.  Explicit, a request costs the rebuild of its keys, 0.3 ns a key and head, once for all of its tokens, and a
+// tenth of the absorbed form's time for a token.  So a request goes explicit from 11 r keys / (6 keys + 72 r) tokens on, at
+// least CHUNK_MIN, where its keys' rows, rounded up to whole tiles, fit in what the requests in front of it left of the
+// buffers.  Measured, explicit / absorbed, us: 128 heads, one request of 8192 keys, 192 tokens 384 / 357, 224 385 / 411;
+// four of 2048, 96 tokens 373 / 304, 128 375 / 382; 64 heads, eight of 2048, 64 tokens 359 / 289, 96 363 / 424; 16 heads, four
+// of 8192, 96 tokens 216 / 209, 128 215 / 250; 16 of 2048, 80 tokens 215 / 214, 96 215 / 243; 16 of 200, 64 tokens 77 / 78.
 // One block: prefix sums over the requests, then a warp per 128 tokens, then the order of the tiles: in falling order of
 // their keys where L2 holds all K_nope and V^T of a shard's heads, which then take turns; else request by request, the
 // longest first, so that the tiles of one head and request, which read the same rows, run together.
@@ -84,6 +84,7 @@ struct Chunk {
     PagedStep s;
     PagedChunk c;
     int cap, key_rows, heads;   // heads of a shard
+    int rows;                   // of an item of the absorbed form
 };
 constexpr int L2_KEYS = (112 << 20) / 512;   // (key, head) pairs whose K_nope and V^T stay in L2 (of 129 MB)
 
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
             n = min(max(a.s.cu[b + 1], 0), N) - t0;
             keys = min(max(a.s.lens[b], 0), a.cap);
         }
-        const bool may = min(n, keys) >= CHUNK_MIN && n * (keys + 2560l) >= keys * 192l;
+        const bool may = min(n, keys) >= CHUNK_MIN && 6l * n * (keys + 12l * a.rows) >= 11l * a.rows * keys;
         const long need = may ? (keys + 127l) / 128 * 128 : 0;
         long all;
         const long r0 = rows + block_before<NT>(need, warp_tot, all);
@@ -345,7 +346,8 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant
 cudaError_t launch_paged_chunk(const PagedDecode &p, const PagedStep &s, const PagedChunk &c, cudaStream_t st) {
     cudaError_t e;
     {
-        const Chunk a{s, c, p.max_pages * p.page, c.key_rows, c.heads};
+        const int rows = p.row_tiles > 1 ? p.H / p.row_tiles : p.row_tile / p.H * p.H;
+        const Chunk a{s, c, p.max_pages * p.page, c.key_rows, c.heads, rows};
         ProfScope ps("paged_chunk", st);
         const bool few = s.n_tokens <= 2048 && s.B <= 256;   // few warps come together sooner
         auto kern = few ? paged_chunk_kernel<256> : paged_chunk_kernel<PNT>;
