@@ -1224,7 +1224,7 @@ struct PagedExplicit {
 void paged_explicit_carve(const PagedDecode &p, int B, int n_tokens, int key_rows, int head_shard, PagedExplicit *x, Carve &c) {
     *x = PagedExplicit{};
     key_rows = key_rows / 256 * 256;
-    if (!p.tc || n_tokens < CHUNK_MIN || key_rows == 0) return;
+    if (!p.tc || n_tokens < CHUNK_CALL || key_rows == 0) return;
     x->hs = head_shard == 0 ? p.H : std::min(head_shard, p.H);
     const size_t R = key_rows, T = n_tokens;
     x->c.key_rows = key_rows;

@@ -105,9 +105,10 @@ inline bool plan_in_absorb(const PagedDecode &p, const PagedPlan &s) {
 cudaError_t paged_decode_simt(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st);
 cudaError_t paged_absorb_simt(const PagedDecode &p, const PagedPlan *plan, cudaStream_t st);
 
-// The explicit form of the requests with many tokens (tensor cores), CHUNK_MIN and more.  Tiles of 128 tokens: at most
-// n_tokens / 128 and one more a request.  CHUNK_RESTS: tiles of 128 keys that have the rest of K_nope.
-constexpr int CHUNK_MIN = 64, CHUNK_RESTS = 4, CHUNK_SORT = 2048;
+// The explicit form of the requests with many tokens (tensor cores), CHUNK_MIN and more, in calls of CHUNK_CALL tokens and
+// more (its launches, with nothing to do, are 10 to 16 us).  Tiles of 128 tokens: at most n_tokens / 128 and one more a
+// request.  Tiles of 128 keys that have the rest of K_nope: CHUNK_RESTS a request, and one for CHUNK_REST_TOKENS tokens.
+constexpr int CHUNK_CALL = 64, CHUNK_MIN = 32, CHUNK_RESTS = 4, CHUNK_REST_TOKENS = 16, CHUNK_SORT = 2048;
 struct PagedChunk {
     int key_rows;                // rows of the key buffers, a multiple of 256
     int max_tiles, max_rests;    // tiles of 128 tokens; tiles of 128 keys with a rest
@@ -123,8 +124,8 @@ struct PagedChunk {
     void *chat, *kpe, *qpe, *kws, *vws;
 };
 inline int chunk_rests(int n_tokens, int key_rows) {
-    const int a = key_rows / 128, b = n_tokens / CHUNK_MIN;
-    return b < a / CHUNK_RESTS ? b * CHUNK_RESTS : a;
+    const int a = key_rows / 128, b = n_tokens / CHUNK_REST_TOKENS;
+    return b < a ? b : a;
 }
 inline int chunk_tiles(int n_tokens) { return n_tokens / 128 + n_tokens / CHUNK_MIN + 1; }
 // The plan and the gathered rows; p.q_pe of the whole step.

@@ -71,12 +71,13 @@ __device__ long block_before(long n, long *warp_tot, long &all) {
 // ----------------------------------------------------------------- explicit plan ----
 // Which form is cheaper.  Absorbed, a token costs its share of an item, r query rows of up to 128 (or 64, which take as
 // long): 0.17 ns a key of its own and as much as 12 r keys more for its queries, a part's beginning and end and its share of
-// the join.  Explicit, a request costs the rebuild of its keys, 0.3 ns a key and head, once for all of its tokens, and a
-// tenth of the absorbed form's time for a token.  So a request goes explicit from 11 r keys / (6 keys + 72 r) tokens on, at
-// least CHUNK_MIN, where its keys' rows, rounded up to whole tiles, fit in what the requests in front of it left of the
+// the join.  Explicit, a request costs the rebuild of its keys, rounded up to whole tiles, 0.3 ns a key and head, once for
+// all of its tokens, and a tenth of the absorbed form's time for a token.  So a request goes explicit from 11 r (tiled keys
+// + 64) / (6 keys + 72 r) tokens on, at least CHUNK_MIN, where its rows fit in what the requests in front of it left of the
 // buffers.  Measured, explicit / absorbed, us: 128 heads, one request of 8192 keys, 192 tokens 384 / 357, 224 385 / 411;
-// four of 2048, 96 tokens 373 / 304, 128 375 / 382; 64 heads, eight of 2048, 64 tokens 359 / 289, 96 363 / 424; 16 heads, four
-// of 8192, 96 tokens 216 / 209, 128 215 / 250; 16 of 2048, 80 tokens 215 / 214, 96 215 / 243; 16 of 200, 64 tokens 77 / 78.
+// four of 2048, 96 tokens 373 / 304, 128 375 / 382; 16 of 200, 40 tokens 273 / 226, 56 276 / 292; 16 of none, 32 tokens
+// 175 / 217; 64 heads, eight of 2048, 64 tokens 359 / 289, 96 363 / 424; 16 heads, four of 8192, 96 tokens 216 / 209, 128
+// 215 / 250; 16 of 2048, 80 tokens 215 / 214, 96 215 / 243; 48 of 200, 40 tokens 125 / 125, 56 131 / 161.
 // One block: prefix sums over the requests, then a warp per 128 tokens, then the order of the tiles: in falling order of
 // their keys where L2 holds all K_nope and V^T of a shard's heads, which then take turns; else request by request, the
 // longest first, so that the tiles of one head and request, which read the same rows, run together.
@@ -107,8 +108,9 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
             n = min(max(a.s.cu[b + 1], 0), N) - t0;
             keys = min(max(a.s.lens[b], 0), a.cap);
         }
-        const bool may = min(n, keys) >= CHUNK_MIN && 6l * n * (keys + 12l * a.rows) >= 11l * a.rows * keys;
-        const long need = may ? (keys + 127l) / 128 * 128 : 0;
+        const long tiled = (keys + 127l) / 128 * 128;
+        const bool may = min(n, keys) >= CHUNK_MIN && 6l * n * (keys + 12l * a.rows) >= 11l * a.rows * (tiled + 64);
+        const long need = may ? tiled : 0;
         long all;
         const long r0 = rows + block_before<NT>(need, warp_tot, all);
         rows += all;
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
         tiles += all;
         block_before<NT>(fits ? need : 0, warp_tot, all);   // (those that fit are the first of those that may)
         used += all;
-        int rest = fits ? (int)min(need / 128, (long)CHUNK_RESTS) : 0;
+        int rest = fits ? (int)min(need / 128, (long)min(n / CHUNK_REST_TOKENS, CHUNK_RESTS)) : 0;
         const long p0 = rests + block_before<NT>(rest, warp_tot, all);
         rests += all;
         if (p0 + rest > a.c.max_rests) rest = 0;   // (only where cu decreases)

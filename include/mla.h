@@ -341,7 +341,7 @@ size_t mla_paged_decode_workspace(const mla_dims *dims, mla_dtype dtype, int B, 
  *   kv_lens [B]   cu_tokens [B + 1]   positions [n_tokens]   w_kv_b as above
  *   out [n_tokens, H, d_v]   lse (fp32) [n_tokens, H]     0 <= B <= 2^24
  * The tensor-core kernels take one of two forms for a request.  Absorbed, as decode: needs no room for keys, and is the
- * cheaper one up to 64 to 180 tokens a request, by its length.  Explicit, as mla_latent_attn_fwd: K_nope and V are
+ * cheaper one up to 30 to 200 tokens a request, by its length.  Explicit, as mla_latent_attn_fwd: K_nope and V are
  * rebuilt from the request's pages, head_shard heads at a time (0: all), in the workspace; it takes the requests of many
  * new tokens whose keys, rounded up to 128 each, fit in key_rows rows, in the order of the requests (0: none do, and a
  * call of 64 tokens or more without such requests is some 10 us shorter).  Both compute the same function, so key_rows

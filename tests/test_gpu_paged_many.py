@@ -111,3 +111,18 @@ def test_the_same_bits_twice_in_a_graph_and_two_at_once():
     assert mla.mla_check_device_error(None) == 0
     for x in others + [(out, lse)]:
         assert torch.equal(x[0], first[0]) and torch.equal(x[1], first[1])
+
+
+@pytest.mark.parametrize("heads,lens", [(16, [(0, 40), (0, 33), (5, 47), (0, 32), (100, 48), (0, 31), (0, 63), (330, 60)]),
+                                        (64, [(0, 32), (0, 0), (90, 47), (200, 63)]), (20, [(1, 34), (64, 50), (127, 33)]),
+                                        (128, [(0, 45), (83, 45), (150, 63)])])
+def test_short_requests_that_go_explicit(heads, lens):
+    """32 tokens and more over few keys: tiles of 128 rows that are mostly empty, rests of fewer key tiles than there are."""
+    d = mla.dims(heads, **V3)
+    s = sref.step(ref.generator(heads), d, BF, lens, 16, extra_rows=2, lead=1)
+    n = s["positions"].numel()
+    out = torch.randn(n, heads, 128, generator=ref.generator(4)).to(BF).cuda()
+    lse = torch.randn(n, heads, generator=ref.generator(5)).cuda()
+    before = out.clone(), lse.clone()
+    call(d, s, out=out, lse=lse)
+    sref.check_prefill(BF, out, lse, sref.prefill(d, s), before)
