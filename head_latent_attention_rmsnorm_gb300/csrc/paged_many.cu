@@ -407,8 +407,6 @@ constexpr int AM_SMEM = AM_STG + 8 * 4096 + (int)sizeof(AbsorbCtl);
 static_assert(AM_SMEM <= 232448, "shared memory budget");
 
 __global__ void __launch_bounds__(AM_NT, 1) paged_absorb_many_kernel(const __grid_constant__ CUtensorMap mW,
-                                                                     const __grid_constant__ CUtensorMap mhi,
-                                                                     const __grid_constant__ CUtensorMap mlo,
                                                                      const __grid_constant__ Absorb a) {
     extern __shared__ __align__(1024) uint8_t sm[];
     const PagedDecode &p = a.p;
@@ -580,16 +578,12 @@ cudaError_t paged_absorb_many(const paged::Absorb &ab, cudaStream_t st) {
     const PagedDecode &p = ab.p;
     cudaError_t e;
     if ((e = cudaFuncSetAttribute(paged_absorb_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AM_SMEM)) != cudaSuccess) return e;
-    CUtensorMap mW, mhi, mlo;
+    CUtensorMap mW;
     const ull dw[2] = {DK, (ull)p.H * (DN + DV)}, sw[1] = {DK * 2};
     const unsigned bw[2] = {64, DN};
     if ((e = make_tma_map(&mW, p.w, 2, dw, sw, bw)) != cudaSuccess) return e;
-    const ull d[3] = {DK, (ull)p.H, (ull)p.T}, s[2] = {DK * 2, (ull)p.H * DK * 2};
-    const unsigned b[3] = {64, 1, 32};
-    if ((e = make_tma_map(&mhi, ab.qhi, 3, d, s, b)) != cudaSuccess) return e;
-    if ((e = make_tma_map(&mlo, ab.qlo, 3, d, s, b)) != cudaSuccess) return e;
     ProfScope ps("paged_absorb", st);
-    return launch_after(paged_absorb_many_kernel, 2 * PAGED_TC_WORKERS, AM_NT, AM_SMEM, st, mW, mhi, mlo, ab);
+    return launch_after(paged_absorb_many_kernel, 2 * PAGED_TC_WORKERS, AM_NT, AM_SMEM, st, mW, ab);
 }
 
 cudaError_t paged_join_many(const PagedDecode &p, const __nv_bfloat16 *qlo, const __nv_bfloat16 *qrest, cudaStream_t st) {
