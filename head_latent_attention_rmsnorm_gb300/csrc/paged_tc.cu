@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
     const long pitch = (long)p.row_tile * (DK / 8);
     const bool paired = p.row_tile <= 64;
     bool ok = true;
-    if (STEP && p.list && tokens_of(p) == 0) {   // (the list's length is of a launch long ended)
+    if (STEP && (int)(blockIdx.x % per_head) * JB >= tokens_of(p)) {   // (a list's length is of a launch long ended)
         pdl_wait();
         return;
     }
@@ -494,6 +494,8 @@ __global__ void __launch_bounds__(JNT, 1) paged_join_tc_kernel(const __grid_cons
         }
         __syncthreads();
     }
+    // W_V lands before the block leaves, also where all of its tokens are of no request and no turn has waited for it
+    if (STEP && warp == 0) mbar_wait(&v0.bar_w, 0, (volatile int *)&v0.abort, &g_paged_tc_err);
     if (warp == 1) tmem_dealloc(tmem, 32);
 }
 
