@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(JM_NT, 1) paged_join_many_kernel(const __grid_
                         for (int i = 0; i < 8; ++i) tma_load_2d(sm + i * BOX, &mW, &ct.w_full, 64 * i, h * (DN + DV) + DN);
                     }
                     __syncwarp();
+                    pdl_wait();   // (here and in the other roles: no wait runs out while the attention still works)
                     ok = __all_sync(FULL, wait(&ct.w_full, wp, &ct.abort));
                     wp ^= 1;
                     head = h;
@@ -354,6 +355,7 @@ __global__ void __launch_bounds__(JM_NT, 1) paged_join_many_kernel(const __grid_
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OUT));
+        pdl_wait();
         const int quarter = warp & 3, r = quarter * 32 + lane;   // the tensor memory's lanes that the warp reads
 #pragma unroll 1
         for (int u = my.from, k = 0; u < my.to; ++u, ++k) {
