@@ -387,6 +387,7 @@ __global__ void __launch_bounds__(JM_NT, 1) paged_join_many_kernel(const __grid_
     }
     tc_fence_before();
     __syncthreads();
+    if (*(volatile int *)&ct.abort) settle();
     if (warp == 20) tmem_dealloc(tmem, 256);
 }
 
@@ -570,6 +571,7 @@ __global__ void __launch_bounds__(AM_NT, 1) paged_absorb_many_kernel(const __gri
     }
     tc_fence_before();
     __syncthreads();
+    if (*(volatile int *)&ct.abort) settle();
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 

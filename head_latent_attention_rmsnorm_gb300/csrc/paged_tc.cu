@@ -641,12 +641,6 @@ __device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, Ctl *c)
     return __all_sync(FULL, wait_for(bar, parity, c));
 }
 
-__device__ void settle() {   // after an abandoned wait: loads in flight land before the CTA leaves
-    const uint64_t t0 = global_ns();
-    while (global_ns() - t0 < 100000ull) {
-    }
-}
-
 // PAIRED (items of up to 64 rows): the rows behind the heads, 64 on, carry the queries' low halves in the scores and P's
 // in the values.  STEP: the tokens of a step, whose rows see each its own number of the group's keys.
 template <int UNIT, bool PAIRED, bool STEP>

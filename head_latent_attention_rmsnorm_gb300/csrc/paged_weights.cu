@@ -312,11 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
     }
     __syncwarp();
-    if (tid == 0 && *abort) {   // after an abandoned wait: loads in flight land before the CTA leaves
-        const uint64_t t0 = global_ns();
-        while (global_ns() - t0 < 100000ull) {
-        }
-    }
+    if (tid == 0 && *abort) settle();
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // the leader's MMAs read this CTA's shared memory until here

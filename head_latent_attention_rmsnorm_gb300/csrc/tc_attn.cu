@@ -519,6 +519,7 @@ __global__ void __launch_bounds__(32 * (NSM + 4), 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (*abort) settle();
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 

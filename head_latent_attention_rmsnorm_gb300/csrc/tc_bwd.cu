@@ -44,12 +44,6 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ void settle() {   // let copies into this CTA land before it leaves after an abort
-    const uint64_t t0 = global_ns();
-    while (global_ns() - t0 < 100000ull) {
-    }
-}
-
 // ------------------------------------------------------------------------ prep ----
 // Row (b, i, h): q_nope and dO widened to fp16 copies, D = dO . out.  Warp per row,
 // 128-wide rows, 8-byte pieces.

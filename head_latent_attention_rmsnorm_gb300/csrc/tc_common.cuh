@@ -104,6 +104,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     return mbar_wait_limit(bar, parity, abort, err, WAIT_NS);
 }
 
+// After an abandoned wait: what was asked of the TMA and the tensor core lands before the CTA gives up its shared
+// memory (bounded: 100 microseconds).
+__device__ __forceinline__ void settle() {
+    const uint64_t t0 = global_ns();
+    while (global_ns() - t0 < 100000ull) {
+    }
+}
+
 // ----------------------------------------------------------------------- TMA ----
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)m) : "memory");

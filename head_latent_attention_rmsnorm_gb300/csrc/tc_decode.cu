@@ -159,14 +159,6 @@ __device__ __forceinline__ Unit unit_of(const DecK &p, int u) {
     return w;
 }
 
-// After an abandoned wait: give TMA loads that were already issued time to land
-// before the CTA's shared memory is released (bounded: 100 microseconds).
-__device__ void settle() {
-    const uint64_t t0 = global_ns();
-    while (global_ns() - t0 < 100000ull) {
-    }
-}
-
 // SHD: the TPLA two-shard units (a template parameter so that the plain decode's issue
 // loops carry no shard branches).
 template <bool SHD>

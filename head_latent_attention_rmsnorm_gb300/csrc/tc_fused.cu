@@ -107,12 +107,6 @@ __device__ __forceinline__ int tiles_of(const FusedK &p, int q0) {
     return (kv_end + BKV - 1) / BKV;
 }
 
-__device__ void settle() {   // let copies into this CTA land before it leaves after an abort
-    const uint64_t t0 = global_ns();
-    while (global_ns() - t0 < 100000ull) {
-    }
-}
-
 template <int CL>
 __global__ void __launch_bounds__(32 * NWARPS, 1)
     tc_fused_kernel(const __grid_constant__ CUtensorMap mQn, const __grid_constant__ CUtensorMap mQr,

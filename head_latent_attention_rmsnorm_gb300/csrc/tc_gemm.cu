@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(256, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (*abort) settle();
     if (warp == 1) tmem_dealloc(tmem, 2 * ACC_COLS);
 }
 
@@ -553,6 +554,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (*abort) settle();
     cluster_sync();   // the leader's MMAs read this CTA's shared memory until here
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }

@@ -400,6 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (*abort) settle();
     cluster_sync();   // the peer may still be arriving on this CTA's barriers until here
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
