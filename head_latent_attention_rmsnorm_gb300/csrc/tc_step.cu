@@ -451,11 +451,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // ---- the groups' sums meet; a group stores half of the row's outputs
             named_bar_sync(b_meet, 64);   // (the last tile's group has set its maximum)
             const float top = row_max[(T - 1) & 1][row];
-            sum = m == -INFINITY ? 0.f : sum * ex2(m - top);
+            if (m != -INFINITY) sum *= ex2(m - top);   // (else 0, or NaN where a score is NaN)
             row_sum[g][row] = sum;
             named_bar_sync(b_meet, 64);   // (and the last unit's sums were read before the first of the two)
             const float s2 = row_sum[g ^ 1][row], l = g ? s2 + sum : sum + s2;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             ok = __all_sync(FULL, ok && wait(B_OFINAL, n & 1));
             tc_fence_after();
             uint32_t o[2][32];
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                             ((uint4 *)(dst + 16 * q))[v] = make_uint4(wv[4 * v], wv[4 * v + 1], wv[4 * v + 2], wv[4 * v + 3]);
                     }
                 }
-                if (g == 0) p.lse[t * p.H + h] = l > 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                if (g == 0) p.lse[t * p.H + h] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
             }
             ++n;
             u = u_next;
