@@ -94,12 +94,14 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
     __shared__ long warp_tot[NT / 32];
     __shared__ int2 order[CHUNK_SORT];   // a tile's key tiles, its request
     __shared__ int explicit_tokens;
+    __shared__ int room[NT];             // a request's need of rows, then its place
+    __shared__ long taken;
     const int tid = threadIdx.x, lane = tid & 31, N = a.s.n_tokens;
     pdl_wait();
     pdl_launch_dependents();
     for (int i = tid; i < N; i += NT) a.c.done[i] = 0;
     if (tid == 0) explicit_tokens = 0;
-    long rows = 0, tiles = 0, used = 0, rests = 0;
+    long rows = 0, tiles = 0, rests = 0;
     for (int b0 = 0; b0 < a.s.B; b0 += NT) {
         const int b = b0 + tid;
         int t0 = 0, n = 0, keys = 0;
@@ -111,15 +113,36 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
         const long tiled = (keys + 127l) / 128 * 128;
         const bool may = min(n, keys) >= CHUNK_MIN && 6l * n * (keys + 12l * a.rows) >= 11l * a.rows * (tiled + 64);
         const long need = may ? tiled : 0;
-        long all;
-        const long r0 = rows + block_before<NT>(need, warp_tot, all);
-        rows += all;
-        const bool fits = may && r0 + need <= a.key_rows;
+        long all, r0 = rows + block_before<NT>(need, warp_tot, all);
+        bool fits = may;
+        if (rows + all <= a.key_rows) {
+            rows += all;
+        } else {   // not all of them: in their order, each that fits in what is left
+            room[tid] = (int)need;
+            __syncthreads();
+            if (tid < 32) {
+                long at = rows;
+                for (int i = lane; i < NT; i += 32) {
+                    const int x = room[i];
+                    int place = -1;
+                    for (unsigned some = __ballot_sync(0xffffffffu, x > 0); some; some &= some - 1) {
+                        const int l = __ffs(some) - 1, y = __shfl_sync(0xffffffffu, x, l);
+                        if (at + y > a.key_rows) continue;
+                        if (l == lane) place = (int)at;
+                        at += y;
+                    }
+                    room[i] = place;
+                }
+                if (lane == 0) taken = at;
+            }
+            __syncthreads();
+            r0 = room[tid];
+            fits = may && r0 >= 0;
+            rows = taken;
+        }
         const int mine = fits ? (n + 127) / 128 : 0;
         const long e0 = tiles + block_before<NT>(mine, warp_tot, all);
         tiles += all;
-        block_before<NT>(fits ? need : 0, warp_tot, all);   // (those that fit are the first of those that may)
-        used += all;
         int rest = fits ? (int)min(need / 128, (long)min(n / CHUNK_REST_TOKENS, CHUNK_RESTS)) : 0;
         const long p0 = rests + block_before<NT>(rest, warp_tot, all);
         rests += all;
@@ -191,7 +214,7 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
     }
     __syncthreads();
     // the tiles that have keys here in their order (a step of more than CHUNK_SORT tiles: as they come, heads in turns)
-    const bool heaviest = !sorted || used * a.heads <= L2_KEYS;
+    const bool heaviest = !sorted || rows * a.heads <= L2_KEYS;
     long out = 0;
     for (int base = 0; base < n; base += NT) {
         const int e = base + tid;
@@ -244,7 +267,7 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
             if (mine >> i & 1) *at++ = t0 + i;
     }
     if (tid == 0) {
-        a.c.ctl[0] = (int)used;
+        a.c.ctl[0] = (int)rows;
         a.c.ctl[1] = (int)out;
         a.c.ctl[2] = (int)listed;
         a.c.ctl[3] = heaviest;

@@ -343,8 +343,8 @@ size_t mla_paged_decode_workspace(const mla_dims *dims, mla_dtype dtype, int B, 
  * The tensor-core kernels take one of two forms for a request.  Absorbed, as decode: needs no room for keys, and is the
  * cheaper one up to 30 to 200 tokens a request, by its length.  Explicit, as mla_latent_attn_fwd: K_nope and V are
  * rebuilt from the request's pages, head_shard heads at a time (0: all), in the workspace; it takes the requests of many
- * new tokens whose keys, rounded up to 128 each, fit in key_rows rows, in the order of the requests (0: none do, and a
- * call of 64 tokens or more without such requests is some 10 us shorter).  Both compute the same function, so key_rows
+ * new tokens, in their order, each whose keys, rounded up to 128, fit in what those in front of it left of key_rows rows (0:
+ * none do, and a call of 64 tokens or more without such requests is some 10 us shorter).  Both compute the same function, so key_rows
  * (rounded down to a multiple of 256) and head_shard are a matter of memory, 1280 + 512 head_shard bytes a row, of
  * time and of rounding.  The choice is made on the device from the lengths there.  Precision: absorbed as mla_paged_decode.  Explicit, the output's error over
  * that of an fp32 evaluation rounded to bf16 is 1.0 to 1.1; the log-sum-exp's, relative to its value and as a root mean
