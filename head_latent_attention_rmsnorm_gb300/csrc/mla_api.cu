@@ -1331,6 +1331,13 @@ mla_status mla_paged_decode(const mla_dims *dims, mla_dtype dtype, int B, int nu
     return cuda_status(p.tc ? paged_decode_tc(p, nullptr, (cudaStream_t)cuda_stream) : paged_decode_simt(p, nullptr, (cudaStream_t)cuda_stream));
 }
 
+int mla_paged_prefill_key_rows(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int page_size, int max_pages) {
+    PagedDecode p{};
+    if (paged_step_shape(dims, dtype, B, n_tokens, page_size, max_pages, &p) != MLA_OK || !p.tc || n_tokens < CHUNK_CALL) return 0;
+    const long rows = chunk_most_rows(B, n_tokens, (long)max_pages * page_size, chunk_item_rows(p));
+    return (int)std::min((rows + 255) / 256 * 256, (long)INT_MAX / 256 * 256);
+}
+
 size_t mla_paged_prefill_workspace(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int page_size, int max_pages,
                                    int key_rows, int head_shard) {
     PagedDecode p{};

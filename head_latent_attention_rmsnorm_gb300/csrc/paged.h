@@ -128,6 +128,14 @@ inline int chunk_rests(int n_tokens, int key_rows) {
     return b < a ? b : a;
 }
 inline int chunk_tiles(int n_tokens) { return n_tokens / 128 + n_tokens / CHUNK_MIN + 1; }
+// Whether n tokens of a request of `keys` keys, `tiled` rounded up to whole tiles, go explicit: the cheaper form (its reasons
+// and measurements are at paged_chunk_kernel).  rows: query rows of an item of the absorbed form.
+__host__ __device__ inline bool chunk_pays(long n, long keys, long tiled, long rows) {
+    return n >= CHUNK_MIN && keys >= CHUNK_MIN && 6 * n * (keys + 12 * rows) >= 11 * rows * (tiled + 64);
+}
+inline int chunk_item_rows(const PagedDecode &p) { return p.row_tiles > 1 ? p.H / p.row_tiles : p.row_tile / p.H * p.H; }
+// A bound of the key rows that the requests of a step can take together; cap: keys of a row of the table.
+long chunk_most_rows(int B, int n_tokens, long cap, int rows);
 // The plan and the gathered rows; p.q_pe of the whole step.
 cudaError_t launch_paged_chunk(const PagedDecode &p, const PagedStep &s, const PagedChunk &c, cudaStream_t st);
 

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
             keys = min(max(a.s.lens[b], 0), a.cap);
         }
         const long tiled = (keys + 127l) / 128 * 128;
-        const bool may = min(n, keys) >= CHUNK_MIN && 6l * n * (keys + 12l * a.rows) >= 11l * a.rows * (tiled + 64);
+        const bool may = chunk_pays(n, keys, tiled, a.rows);
         const long need = may ? tiled : 0;
         long all, r0 = rows + block_before<NT>(need, warp_tot, all);
         bool fits = may;
@@ -368,11 +368,33 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant
 
 }  // namespace
 
+// n tokens of one request take at most f(n) rows: whole tiles t <= L, L a row of the table, with
+// t (11 rows - 6 n) <= rows (72 n - 704).  Up to L that is a convex function, below 0 at 0, so while no request can have a
+// whole row of the table, all tokens in one request take the most; else no token brings more rows than the largest f(n) / n.
+long chunk_most_rows(int B, int n_tokens, long cap, int rows) {
+    const long L = (cap + 127) / 128 * 128, r = rows;
+    auto most = [&](long n) {
+        if (n < CHUNK_MIN) return 0l;
+        const long num = r * (72 * n - 704), den = 11 * r - 6 * n;
+        return den <= 0 ? L : std::min(L, num / den / 128 * 128);
+    };
+    const long requests = std::min((long)B, (long)n_tokens / CHUNK_MIN);
+    long whole = CHUNK_MIN;   // tokens that may have a whole row of the table
+    while (most(whole) < L) ++whole;
+    if (n_tokens < whole) return requests > 0 ? most(n_tokens) : 0;
+    long top = 0, by = 1;   // the largest f(n) / n
+    for (long n = CHUNK_MIN; n <= whole; ++n)
+        if (most(n) * by > top * n) {
+            top = most(n);
+            by = n;
+        }
+    return std::min(requests * L, (n_tokens * top + by - 1) / by);
+}
+
 cudaError_t launch_paged_chunk(const PagedDecode &p, const PagedStep &s, const PagedChunk &c, cudaStream_t st) {
     cudaError_t e;
     {
-        const int rows = p.row_tiles > 1 ? p.H / p.row_tiles : p.row_tile / p.H * p.H;
-        const Chunk a{s, c, p.max_pages * p.page, c.key_rows, c.heads, rows};
+        const Chunk a{s, c, p.max_pages * p.page, c.key_rows, c.heads, chunk_item_rows(p)};
         ProfScope ps("paged_chunk", st);
         const bool few = s.n_tokens <= 2048 && s.B <= 256;   // few warps come together sooner
         auto kern = few ? paged_chunk_kernel<256> : paged_chunk_kernel<PNT>;

@@ -118,6 +118,8 @@ def lib() -> ctypes.CDLL:
         L.mla_paged_prefill.restype = _i
         L.mla_paged_prefill_workspace.argtypes = [D, _i, _i, _i, _i, _i, _i, _i]
         L.mla_paged_prefill_workspace.restype = _sz
+        L.mla_paged_prefill_key_rows.argtypes = [D, _i, _i, _i, _i, _i]
+        L.mla_paged_prefill_key_rows.restype = _i
         L.mla_paged_weights.argtypes = [D, _i, _i, _i, _i, _i, _i] + [_vp] * 13 + [_sz, _vp]
         L.mla_paged_weights.restype = _i
         L.mla_paged_weights_workspace.argtypes = [D, _i, _i, _i, _i, _i]
@@ -243,6 +245,10 @@ def mla_paged_prefill(*args) -> int:
 
 def mla_paged_prefill_workspace(*args) -> int:
     return lib().mla_paged_prefill_workspace(*args)
+
+
+def mla_paged_prefill_key_rows(*args) -> int:
+    return lib().mla_paged_prefill_key_rows(*args)
 
 
 def mla_paged_weights(*args) -> int:
@@ -832,21 +838,21 @@ PREFILL_HEAD_SHARD = 64
 PREFILL_ALL_HEADS = 5120 * 128
 
 
-def _prefill_room(n_heads, n_tokens, block_table, page, key_rows, head_shard):
-    """The explicit form's (key_rows, head_shard): by default room for every row of the table, up to
+def _prefill_room(d, dt, n_tokens, table_shape, page, key_rows, head_shard):
+    """The explicit form's (key_rows, head_shard): by default room for all that so many tokens can use of it, up to
     PREFILL_KEY_ROWS, all heads at once or in shards of PREFILL_HEAD_SHARD."""
     if key_rows is None:
-        rows = -(-block_table.shape[1] * page // 128) * 128 * min(block_table.shape[0], n_tokens)
-        key_rows = min(-(-rows // 256) * 256, PREFILL_KEY_ROWS)
+        rows = lib().mla_paged_prefill_key_rows(ctypes.byref(d), dt, table_shape[0], n_tokens, page, table_shape[1])
+        key_rows = min(rows, PREFILL_KEY_ROWS)
     if head_shard is None:
-        head_shard = 0 if key_rows * n_heads <= PREFILL_ALL_HEADS else PREFILL_HEAD_SHARD
+        head_shard = 0 if key_rows * d.n_heads <= PREFILL_ALL_HEADS else PREFILL_HEAD_SHARD
     return key_rows, head_shard
 
 
 def paged_prefill_workspace(d: Dims, n_tokens: int, c_cache, block_table, *, key_rows=None, head_shard=None) -> torch.Tensor:
     """A workspace for :func:`paged_prefill` calls of ``n_tokens`` rows with this cache and table (and the same
     ``key_rows`` and ``head_shard``), one call at a time."""
-    room = _prefill_room(d.n_heads, n_tokens, block_table, c_cache.shape[1], key_rows, head_shard)
+    room = _prefill_room(d, _dt(c_cache), n_tokens, block_table.shape, c_cache.shape[1], key_rows, head_shard)
     n = lib().mla_paged_prefill_workspace(ctypes.byref(d), _dt(c_cache), block_table.shape[0], n_tokens,
                                           c_cache.shape[1], block_table.shape[1], *room)
     return torch.empty(max(n, 1), dtype=torch.uint8, device=c_cache.device)
@@ -889,7 +895,7 @@ def paged_prefill(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_len
             return paged_prefill(d, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, cu_tokens, positions,
                                  w_kv_b, key_rows=key_rows, head_shard=head_shard, out=out, lse=lse, workspace=workspace)
     H = d.n_heads
-    key_rows, head_shard = _prefill_room(H, n, block_table, page, key_rows, head_shard)
+    key_rows, head_shard = _prefill_room(d, dt, n, (B, max_pages), page, key_rows, head_shard)
     if out is None:
         out = torch.zeros(n, H, d.d_v, dtype=tdt, device=dev)
     if lse is None:

@@ -343,10 +343,11 @@ size_t mla_paged_decode_workspace(const mla_dims *dims, mla_dtype dtype, int B, 
  * The tensor-core kernels take one of two forms for a request.  Absorbed, as decode: needs no room for keys, and is the
  * cheaper one up to 30 to 200 tokens a request, by its length.  Explicit, as mla_latent_attn_fwd: K_nope and V are
  * rebuilt from the request's pages, head_shard heads at a time (0: all), in the workspace; it takes the requests of many
- * new tokens, in their order, each whose keys, rounded up to 128, fit in what those in front of it left of key_rows rows (0:
- * none do, and a call of 64 tokens or more without such requests is some 10 us shorter).  Both compute the same function, so key_rows
- * (rounded down to a multiple of 256) and head_shard are a matter of memory, 1280 + 512 head_shard bytes a row, of
- * time and of rounding.  The choice is made on the device from the lengths there.  Precision: absorbed as mla_paged_decode.  Explicit, the output's error over
+ * new tokens, in their order, each whose keys, rounded up to 128, fit in what those in front of it left of key_rows rows
+ * (0: none do, and a call of 64 tokens or more without such requests is some 10 us shorter).  Both compute the same
+ * function, so key_rows (rounded down to a multiple of 256) and head_shard are a matter of memory, 1280 + 512 head_shard
+ * bytes a row (256 head_shard more for the first 512 of a request), of time and of rounding.  The choice is made on the
+ * device from the lengths there.  Precision: absorbed as mla_paged_decode.  Explicit, the output's error over
  * that of an fp32 evaluation rounded to bf16 is 1.0 to 1.1; the log-sum-exp's, relative to its value and as a root mean
  * square, 2e-7 to 7e-7 at scores of standard deviation 1, 4e-6 at 2, 2e-5 at 4 and 4e-5 at 8 (a request's first 512 keys
  * alone: 9e-7 at most); and its operands are fp16: q_nope, the cached band and the rebuilt K_nope and V must lie inside
@@ -363,6 +364,8 @@ mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n
                              void *workspace, size_t workspace_bytes, void *cuda_stream);
 size_t mla_paged_prefill_workspace(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int page_size, int max_pages,
                                    int key_rows, int head_shard);
+/* The key_rows of which no step of these sizes can use more, whatever its lengths are (0: its requests all go absorbed). */
+int mla_paged_prefill_key_rows(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int page_size, int max_pages);
 
 /*
  * The attention weight that a step's tokens gave each page of their requests:
