@@ -1235,6 +1235,8 @@ void paged_explicit_carve(const PagedDecode &p, int B, int n_tokens, int key_row
     x->c.heads = x->hs;
     x->c.key0 = (int *)c.take(B * sizeof(int));
     x->c.holes = (int *)c.take(B * sizeof(int));
+    x->c.w_max = (unsigned *)c.take(p.H * sizeof(unsigned));
+    x->c.c_max = (unsigned *)c.take(B * sizeof(unsigned));
     x->c.block_of = (int *)c.take(R / 128 * sizeof(int));
     x->c.limits = (int *)c.take(T * sizeof(int));
     x->c.done = (int *)c.take(T * sizeof(int));
@@ -1397,7 +1399,8 @@ mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n
         q.q_pe = q_pe;
         MLA_TRY(launch_paged_chunk(q, step, x.c, (cudaStream_t)cuda_stream));
         const TcStep t{n_tokens, p.H, x.hs, x.c.key_rows, p.scale, q_nope, x.c.qpe, x.c.chat, x.c.kpe, w_kv_b, x.c.kws, x.c.vws,
-                       x.c.rest, x.c.max_rests * 128, x.c.rest_of, out, lse, x.c.ctl, x.c.tiles, x.c.limits, x.c.done, x.c.held, x.c.holes};
+                       x.c.rest, x.c.max_rests * 128, x.c.rest_of, out, lse, x.c.ctl, x.c.tiles, x.c.limits, x.c.done, x.c.held, x.c.holes, x.c.block_of,
+                       x.c.w_max, x.c.c_max};
         MLA_TRY(tc_step_prefill(t, (cudaStream_t)cuda_stream));
     }
     for (int s0 = 0; s0 < n_tokens; s0 += PAGED_ROUND) {

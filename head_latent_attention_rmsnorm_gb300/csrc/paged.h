@@ -117,6 +117,7 @@ struct PagedChunk {
     int heads;                   // of a shard
     int *ctl;                    // [4]: rows in use, tiles, tokens of the list, whether the tiles are in falling order
     int *key0, *holes;           // [B]: a request's first key row (-1: absorbed); nonzero: some page is missing
+    unsigned *w_max, *c_max;     // [H], [B]: as TcStep's
     int *block_of;               // [key_rows / 128]: the request of each 128 rows
     int *limits, *done, *list;   // [n_tokens]: keys seen; nonzero: explicit; the requests' other tokens
     StepTile *raw, *tiles;

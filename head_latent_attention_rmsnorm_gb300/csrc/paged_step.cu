@@ -85,6 +85,7 @@ struct Chunk {
     PagedStep s;
     PagedChunk c;
     int cap, key_rows, heads;   // heads of a shard
+    int all_heads;
     int rows;                   // of an item of the absorbed form
 };
 constexpr int L2_KEYS = (112 << 20) / 512;   // (key, head) pairs whose K_nope and V^T stay in L2 (of 129 MB)
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
     pdl_wait();
     pdl_launch_dependents();
     for (int i = tid; i < N; i += NT) a.c.done[i] = 0;
+    for (int i = tid; i < a.all_heads; i += NT) a.c.w_max[i] = 0;
     if (tid == 0) explicit_tokens = 0;
     long rows = 0, tiles = 0, rests = 0;
     for (int b0 = 0; b0 < a.s.B; b0 += NT) {
@@ -150,6 +152,7 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
         if (b < a.s.B) {
             a.c.key0[b] = fits ? (int)r0 : -1;
             a.c.holes[b] = 0;
+            a.c.c_max[b] = 0;
             if (fits) {
                 for (int e = 0; e < mine && e0 + e < a.c.max_tiles; ++e) {   // (more only where cu decreases)
                     StepTile x{};
@@ -276,8 +279,10 @@ __global__ void __launch_bounds__(NT) paged_chunk_kernel(const __grid_constant__
 
 // ------------------------------------------------------------------------ gather ----
 // A warp per 32 key rows of the explicit requests: the keys' latent rows as they are, their bands in fp16, zeros and no bit
-// where there is no key (behind the length, a missing page); and a warp per token and 32 heads: the rotated
-// band in fp16, as a rounding and its rest.
+// where there is no key (behind the length, a missing page); a warp per token and 32 heads: the rotated
+// band in fp16, as a rounding and its rest; and a warp per eight rows of W_V.  The largest |c| of a request and the largest
+// sum |W_V row| of a head bound V, which is held in fp16 times a power of two of theirs (value_shift): bf16 models whose
+// values are small or large lose nothing by the form.  Numbers that are not finite do not count: they show in V as they are.
 struct Gather {
     PagedDecode p;
     PagedStep s;
@@ -285,6 +290,44 @@ struct Gather {
     Divisor by_page;
     Turns64 turns;
 };
+// Pairs of bf16: |x|, with FINITE 0 for what is not finite; the larger ones of pairs; the sum of a pair
+template <bool FINITE>
+__device__ __forceinline__ uint32_t magnitudes(uint32_t x) {
+    x &= 0x7fff7fffu;
+    return FINITE ? x & ~__vcmpgeu2(x, 0x7f807f80u) : x;
+}
+template <bool FINITE>
+__device__ __forceinline__ uint32_t largest(const uint4 (&x)[8][2]) {
+    uint32_t m[4] = {};
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const uint4 &v = x[e >> 1][e & 1];
+        m[0] = __vmaxu2(m[0], magnitudes<FINITE>(v.x));
+        m[1] = __vmaxu2(m[1], magnitudes<FINITE>(v.y));
+        m[2] = __vmaxu2(m[2], magnitudes<FINITE>(v.z));
+        m[3] = __vmaxu2(m[3], magnitudes<FINITE>(v.w));
+    }
+    return __vmaxu2(__vmaxu2(m[0], m[1]), __vmaxu2(m[2], m[3]));
+}
+// The largest sum of magnitudes of the warp's eight rows of 512; NaN where one of them is NaN
+template <bool FINITE>
+__device__ __forceinline__ float largest_sum(const uint4 (&x)[8][2]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        const uint32_t w[8] = {x[r][0].x, x[r][0].y, x[r][0].z, x[r][0].w, x[r][1].x, x[r][1].y, x[r][1].z, x[r][1].w};
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t m = magnitudes<FINITE>(w[e]);
+            sum[0] += __uint_as_float(m << 16);
+            sum[1] += __uint_as_float(m & 0xffff0000u);
+        }
+        const float all = warp_sum(sum[0] + sum[1]);
+        top = max(top, __float_as_uint(all));   // (as integers: NaN the largest)
+    }
+    return __uint_as_float(top);
+}
 __device__ __forceinline__ uint32_t half_pair(uint32_t bf) {   // two bf16 as two fp16
     const __half2 h = __floats2half2_rn(__uint_as_float(bf << 16), __uint_as_float(bf & 0xffff0000u));
     return *(const uint32_t *)&h;
@@ -297,7 +340,7 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant
     pdl_launch_dependents();
     const int R = __ldcg(a.c.ctl) / 32, per = (p.H + 31) / 32;
     if (R == 0) return;
-    const long total = R + (long)a.s.n_tokens * per;
+    const long heads = R + (long)a.s.n_tokens * per, total = heads + p.H * 16l;
 #pragma unroll 1
     for (long u = blockIdx.x * 8 + (threadIdx.x >> 5); u < total; u += warps) {
         if (u < R) {
@@ -314,6 +357,7 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant
                 if (held != (keys - key >= 32 ? 0xffffffffu : keys > key ? (1u << (keys - key)) - 1 : 0u)) a.c.holes[b] = 1;
             }
             const uint4 zero = make_uint4(0, 0, 0, 0);
+            uint32_t most = 0;
 #pragma unroll 1
             for (int r = 0; r < 32; r += 8) {
                 uint4 x[8][2], y[8];
@@ -325,6 +369,9 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant
                     x[e][1] = from >= 0 ? __ldcg(c + lane + 32) : zero;
                     y[e] = from >= 0 && lane < 8 ? __ldcg(k + lane) : zero;
                 }
+                uint32_t here = largest<false>(x);
+                if (__vcmpgeu2(here, 0x7f807f80u)) here = largest<true>(x);   // (seldom)
+                most = __vmaxu2(most, here);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     uint4 *c = (uint4 *)a.c.chat + (long)(r0 + r + e) * 64;
@@ -335,6 +382,18 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant
                             make_uint4(half_pair(y[e].x), half_pair(y[e].y), half_pair(y[e].z), half_pair(y[e].w));
                 }
             }
+            most = __reduce_max_sync(0xffffffffu, max(most & 0xffff, most >> 16));
+            if (lane == 0) atomicMax(a.c.c_max + b, most << 16);
+        } else if (u >= heads) {
+            const long row = (u - heads) * 8;   // of all heads' W_V
+            const int h = (int)(row / 128);
+            const uint4 *w = (const uint4 *)p.w + ((long)h * 256 + 128 + row % 128) * 64;
+            uint4 x[8][2];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e >> 1][e & 1] = __ldcg(w + (e >> 1) * 64 + (e & 1) * 32 + lane);
+            float top = largest_sum<false>(x);
+            if (!(top <= 3e38f)) top = fminf(largest_sum<true>(x), 3e38f);   // (seldom; the same in all lanes)
+            if (lane == 0) atomicMax(a.c.w_max + h, __float_as_uint(top));
         } else {
             const long i = u - R;
             const int t = (int)(i / per), h0 = (int)(i % per) * 32, h1 = min(h0 + 32, p.H);
@@ -394,7 +453,7 @@ long chunk_most_rows(int B, int n_tokens, long cap, int rows) {
 cudaError_t launch_paged_chunk(const PagedDecode &p, const PagedStep &s, const PagedChunk &c, cudaStream_t st) {
     cudaError_t e;
     {
-        const Chunk a{s, c, p.max_pages * p.page, c.key_rows, c.heads, chunk_item_rows(p)};
+        const Chunk a{s, c, p.max_pages * p.page, c.key_rows, c.heads, p.H, chunk_item_rows(p)};
         ProfScope ps("paged_chunk", st);
         const bool few = s.n_tokens <= 2048 && s.B <= 256;   // few warps come together sooner
         auto kern = few ? paged_chunk_kernel<256> : paged_chunk_kernel<PNT>;

@@ -55,6 +55,8 @@ struct TcStep {
     const int *limits, *done;      // [T]: keys seen; nonzero: computed here
     const uint32_t *held;          // a bit per key row
     const int *holes;              // [requests]
+    const int *block_of;           // [key_rows / 128]: the request of each 128 rows
+    const unsigned *w_max, *c_max; // [H], [requests]: bits of the largest sum |W_V row|, of the largest |c|
 };
 cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st);
 // Explicit prefill with the K_nope / V^T reconstruction inside the attention kernel

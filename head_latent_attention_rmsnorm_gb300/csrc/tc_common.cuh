@@ -479,6 +479,22 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     return false;
 }
 
+// Two fp32 products: one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*(uint64_t *)&a), "l"(*(uint64_t *)&b));
+    return *(float2 *)&d;
+}
+// 2^k, -126 <= k <= 127
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(127 + k) << 23); }
+// The power of two that brings the values V = W_V c of a head and a request into fp16's range, from bounds of their factors as
+// fp32 bits: w of the largest sum |W_V row|, c of the largest |c|.  With exponents e and f, |V| < 2^(e + 1) 2^(f + 1), so
+// |V| 2^(13 - e - f) < 2^15; at 2^-40 of that bound is half a step of fp16's smallest numbers.  (Cut so that a row's sum of
+// weights over the power of two stays a normal number.)
+__device__ __forceinline__ int value_shift(uint32_t w, uint32_t c) {
+    return max(min(13 + 2 * 127 - (int)(w >> 23) - (int)(c >> 23), 100), -126);
+}
+
 // ------------------------------------------------------------- descriptors ----
 // Shared-memory matrix descriptor, 128-byte swizzle.  `lbo`/`sbo` in bytes.
 //   bits  0-13 start address >> 4      bits 16-29 leading byte offset >> 4

@@ -312,6 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     uint64_t *acc_full = empty + PST, *acc_empty = acc_full + 2;
     uint32_t *tslot = (uint32_t *)(acc_empty + 2);
     volatile int *abort = (volatile int *)(tslot + 1);
+    float2 *scales = (float2 *)(tslot + 2);               // DYN: four tiles' factors, of their two blocks of 128 columns
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
@@ -323,7 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             mbar_init(&empty[s], 1);   // the issuer's commit
         }
         for (int a = 0; a < 2; ++a) {
-            mbar_init(&acc_full[a], 1);
+            mbar_init(&acc_full[a], DYN ? 2 : 1);   // the issuer's commit, and the tile's factors
             mbar_init(&acc_empty[a], 8);   // the epilogue warps of both CTAs
         }
         *abort = 0;
@@ -418,6 +419,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 __syncwarp();
             }
         }
+    } else if (DYN && warp == 6) {
+        // ------------------------------------ the tiles' factors, looked up ahead of the epilogue
+        if (lane == 0) {
+            int lt = 0;
+            for (int t = pair; t < k.total; t += pairs, ++lt) {
+                const Tile w = pair_tile_of(p, k, t);
+                float2 f = make_float2(1.f, 1.f);
+                if (w.prob == 1) {
+                    const unsigned wm = __ldcg(step.w_max + min(w.m0 + 128 * (int)rank, p.pr[1].M - 1) / 128);
+                    const int *b = step.block_of + w.n0 / 128;   // (behind the rows in use no matter what)
+                    f.x = pow2(value_shift(wm, __ldcg(step.c_max + __ldcg(b))));
+                    if (w.n0 + 128 < used) f.y = pow2(value_shift(wm, __ldcg(step.c_max + __ldcg(b + 1))));
+                }
+                // tile lt - 2 has been summed, so both CTAs have drained lt - 4, whose factors lay here
+                if (lt >= 2 && !mbar_wait(&acc_full[lt & 1], ((lt >> 1) - 1) & 1, abort, &g_tc_gemm_err)) break;
+                scales[lt & 3] = f;
+                mbar_arrive(&acc_full[lt & 1]);
+            }
+        }
     } else if (warp >= 2 && warp <= 5) {
         // ------------------------------------ epilogue (both CTAs): thread = row
         const int quad = warp & 3;
@@ -441,6 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 const long cbase = q.c_batch * w.batch, c_m = q.c_m;
                 int row0 = w.m0 + 128 * (int)rank + quad * 32, M = q.M;
                 const int N = q.N;
+                const float2 scale = DYN ? scales[lt & 3] : make_float2(1.f, 1.f);
                 const int rest = DYN && w.prob == 0 && row0 < used ? __ldcg(step.rest_of + row0 / 128) : -1;
                 const bool f16out = q.out_kind == 0;
                 const uint32_t sbuf0 = smem_u32(sC + (warp - 2) * 16384);
@@ -468,7 +489,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                         uint32_t o[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const float x0 = __uint_as_float(r[cc & 1][2 * i]), x1 = __uint_as_float(r[cc & 1][2 * i + 1]);
+                            float x0 = __uint_as_float(r[cc & 1][2 * i]), x1 = __uint_as_float(r[cc & 1][2 * i + 1]);
+                            if (DYN) {
+                                const float f = cc < 2 ? scale.x : scale.y;
+                                const float2 x = mul2(make_float2(x0, x1), make_float2(f, f));
+                                x0 = x.x;
+                                x1 = x.y;
+                            }
                             o[i] = f16out ? pack_f16(x0, x1) : pack_bf16(x0, x1);
                             if (DYN && pass) {
                                 const float2 f = __half22float2(*(const __half2 *)&o[i]);
@@ -682,7 +709,7 @@ cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaS
     switch (BN) {
         case 256:
             p.idesc = tc::idesc_f16(256, 256, f16);   // cta_group::2: M = 256 across the pair
-            if (step && !p.pr[0].c_stage) return cudaErrorInvalidValue;
+            if (step && !(p.pr[0].c_stage && p.pr[1].c_stage)) return cudaErrorInvalidValue;
             return launch_gemm_pair(maps, p, step, st);
         case 128:
             p.idesc = tc::idesc_f16(BM, 128, f16, false, p.a_mn != 0);

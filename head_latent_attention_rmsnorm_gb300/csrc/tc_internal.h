@@ -50,10 +50,13 @@ cudaError_t tc_gemm(const TmaOperand &A, const TmaOperand &B, int M, int N, int 
 // type): the explicit path's K_nope and V^T products share one launch.
 // With `step` (two problems of one batch on SM pairs, N >= 256): *rows (device memory) rows of problem 0 and columns of
 // problem 1 only; and what the rounding to fp16 leaves of the 128 rows i of problem 0, for those with rest_of[i] >= 0, to
-// rows 128 rest_of[i] .. of `rest` (fp16, row pitch c_m).
+// rows 128 rest_of[i] .. of `rest` (fp16, row pitch c_m).  Problem 1's rows 128 h .. and columns 128 i .. are written times
+// 2^value_shift(w_max[h], c_max[block_of[i]]).
 struct GemmStep {
     const int *rows, *rest_of;
     void *rest;
+    const int *block_of;
+    const unsigned *w_max, *c_max;
 };
 cudaError_t tc_gemm_group(const GemmProblem *probs, int n_probs, bool f16, cudaStream_t st, const GemmStep *step = nullptr);
 

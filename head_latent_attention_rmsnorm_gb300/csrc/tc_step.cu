@@ -17,7 +17,8 @@
 // rotated q_pe has its fp16 rest too (four score MMAs of 16): its rounding is the same for all keys, and shifted a
 // log-sum-exp by 1.5e-5 whatever their number.  K_nope's rounding errs by 1.6e-4 in each score, 1.6e-4 / sqrt(0.4 keys) in
 // a row's log-sum-exp: little but for rows of few keys, so the request's first 512 keys have K_nope's rest in the scores too
-// (eight MMAs more for those tiles, an entry of their own in the K ring).
+// (eight MMAs more for those tiles, an entry of their own in the K ring).  V is held times a power of two of its head and
+// request (value_shift), which each row's last division takes out again: fp16's narrow range bounds scores only.
 //
 // What bounds it.  2048 tokens over 16384 keys, 128 heads in shards of 64: 2.04 ms, 1265 TFLOP/s of the 640 a (token, key,
 // head) and 1520 of the MMAs that it issues (1.2 times those: the band's rest), where a product that runs for seconds under the
@@ -69,6 +70,7 @@ struct StepK {
     const int *limits, *done; // [tokens]: keys seen; nonzero: computed here
     const uint32_t *held;     // a bit per key row: there is such a key
     const int *holes;         // [requests]: nonzero: some page is missing
+    const unsigned *w_max, *c_max;   // [heads of the model], [requests]: V is held times 2^value_shift of the two
     int head_off, nh;         // first head, heads of this launch
     float scale_log2;
     __nv_bfloat16 *out;
@@ -358,6 +360,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // keys that the row, that every row of the warp sees (rows behind the tile's tokens: no matter what)
             const int sees = row < w.rows ? __ldcg(p.limits + w.q0 + row) : 2147483647;
             const int all_see = __reduce_min_sync(FULL, sees), holes = __ldcg(p.holes + w.request);
+            const float unscale = pow2(-value_shift(__ldcg(p.w_max + p.head_off + w.hl), __ldcg(p.c_max + w.request)));
             float m = -INFINITY, sum = 0.f;   // the row's maximum that this group last used; its part of the sum, relative to it
 #pragma unroll 1
             for (int j = 0; j < w.nt; ++j, ++T) {
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             row_sum[g][row] = sum;
             named_bar_sync(b_meet, 64);   // (and the last unit's sums were read before the first of the two)
             const float s2 = row_sum[g ^ 1][row], l = g ? s2 + sum : sum + s2;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float inv = l == 0.f ? 0.f : unscale / l;
             ok = __all_sync(FULL, ok && wait(B_OFINAL, n & 1));
             tc_fence_after();
             uint32_t o[2][32];
@@ -538,6 +541,8 @@ cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st) {
     a.done = p.done;
     a.held = p.held;
     a.holes = p.holes;
+    a.w_max = p.w_max;
+    a.c_max = p.c_max;
     a.scale_log2 = p.scale * 1.4426950408889634f;
     a.out = (__nv_bfloat16 *)p.out;
     a.H = p.H;
@@ -552,7 +557,7 @@ cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st) {
         TmaOperand wk{w, 512, 128, nh, 1024, 256 * 1024, 128, 0, 0}, wv{w + 128 * 1024, 512, 128, nh, 1024, 256 * 1024, 128, 0, 0};
         const GemmProblem kv[2] = {{latent, wk, (int)R, nh * 128, 512, 1, p.kws, (long)hs * 128, 1, 0, 0},
                                    {wv, latent, nh * 128, (int)R, 512, 1, p.vws, (long)R, 1, 0, 0}};
-        const GemmStep gs{p.ctl, p.rest_of, p.rest};
+        const GemmStep gs{p.ctl, p.rest_of, p.rest, p.block_of, p.w_max + h0, p.c_max};
         if ((e = tc_gemm_group(kv, 2, false, st, &gs)) != cudaSuccess) return e;
         a.head_off = h0;
         a.nh = nh;

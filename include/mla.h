@@ -350,8 +350,10 @@ size_t mla_paged_decode_workspace(const mla_dims *dims, mla_dtype dtype, int B, 
  * device from the lengths there.  Precision: absorbed as mla_paged_decode.  Explicit, the output's error over
  * that of an fp32 evaluation rounded to bf16 is 1.0 to 1.1; the log-sum-exp's, relative to its value and as a root mean
  * square, 2e-7 to 7e-7 at scores of standard deviation 1, 4e-6 at 2, 2e-5 at 4 and 4e-5 at 8 (a request's first 512 keys
- * alone: 9e-7 at most); and its operands are fp16: q_nope, the cached band and the rebuilt K_nope and V must lie inside
- * fp16's range (|x| < 65504).  key_rows 0 is for models where these do not do.
+ * alone: 9e-7 at most).  Its score operands are fp16: q_nope, the cached band and the rebuilt K_nope must lie inside fp16's
+ * range (|x| < 65504), and one of less than 6e-5 is held to 3e-8.  V is fp16 too, but times a power of two of its head and
+ * request, found from the rows of W_V and the request's largest cached value: it may have any size, and a value keeps 2^-12
+ * of itself or 2^-40 of the bound sum |W_V row| max |c|.  key_rows 0 is for models where these do not do.
  * A token that sees no key (a negative position, no pages) gives out 0 and lse -inf.  Rows of no request (in front of
  * cu_tokens[0], from cu_tokens[B] on) are left as they were.  Lengths, slots behind them and bad page ids are
  * treated as in mla_paged_decode, as are types, dimensions, determinism and the workspace.  What a token does not
