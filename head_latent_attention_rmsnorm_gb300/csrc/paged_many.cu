@@ -10,6 +10,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "paged_tc.cuh"
 #include "tc_internal.h"
@@ -595,7 +596,7 @@ cudaError_t paged_join_many(const PagedDecode &p, const __nv_bfloat16 *qlo, cons
     cudaError_t e;
     if ((e = cudaFuncSetAttribute(paged_join_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, JM_SMEM)) != cudaSuccess) return e;
     // the register split waits for ever where the launch has fewer to draw on: another compiler's choice is refused
-    static int regs = 0;
+    static std::atomic<int> regs{0};   // (of the kernel: the same from any host thread and device)
     if (regs == 0) {
         cudaFuncAttributes at;
         if ((e = cudaFuncGetAttributes(&at, paged_join_many_kernel)) != cudaSuccess) return e;

@@ -30,6 +30,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "mla_internal.h"
 #include "tc.h"
@@ -524,7 +525,7 @@ cudaError_t tc_step_prefill(const TcStep &p, cudaStream_t st) {
     }
     if ((e = cudaFuncSetAttribute(tc_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S_BYTES)) != cudaSuccess) return e;
     // the register split waits for ever where the launch has fewer to draw on: another compiler's choice is refused
-    static int regs = 0;
+    static std::atomic<int> regs{0};   // (of the kernel: the same from any host thread and device)
     if (regs == 0) {
         cudaFuncAttributes at;
         if ((e = cudaFuncGetAttributes(&at, tc_step_kernel)) != cudaSuccess) return e;
