@@ -838,6 +838,13 @@ PREFILL_HEAD_SHARD = 64
 PREFILL_ALL_HEADS = 5120 * 128
 
 
+def _int32(name: str, v: int) -> int:
+    """v, refused where the C call would get its low 32 bits only."""
+    if not -1 << 31 <= v < 1 << 31:
+        raise ValueError("%s: %d does not fit in 32 bits" % (name, v))
+    return v
+
+
 def _prefill_room(d, dt, n_tokens, table_shape, page, key_rows, head_shard):
     """The explicit form's (key_rows, head_shard): by default room for all that so many tokens can use of it, up to
     PREFILL_KEY_ROWS, all heads at once or in shards of PREFILL_HEAD_SHARD."""
@@ -846,7 +853,7 @@ def _prefill_room(d, dt, n_tokens, table_shape, page, key_rows, head_shard):
         key_rows = min(rows, PREFILL_KEY_ROWS)
     if head_shard is None:
         head_shard = 0 if key_rows * d.n_heads <= PREFILL_ALL_HEADS else PREFILL_HEAD_SHARD
-    return key_rows, head_shard
+    return _int32("key_rows", key_rows), _int32("head_shard", head_shard)
 
 
 def paged_prefill_workspace(d: Dims, n_tokens: int, c_cache, block_table, *, key_rows=None, head_shard=None) -> torch.Tensor:
@@ -970,6 +977,8 @@ def paged_evict(kv_lens, block_table, page_weights, *, page_size, keep_pages, fi
         return _on_stream(stream, paged_evict, kv_lens, block_table, page_weights, page_size=page_size, keep_pages=keep_pages,
                           first_pages=first_pages, last_pages=last_pages, table_out=table_out, weights_out=weights_out,
                           freed=freed, counts=counts, workspace=workspace)
+    for name, v in (("page_size", page_size), ("keep_pages", keep_pages), ("first_pages", first_pages), ("last_pages", last_pages)):
+        _int32(name, v)
     dev = _device(block_table)
     if block_table.dim() != 2 or block_table.shape[1] < 1:
         raise ValueError("block_table must be [B, max_pages]")

@@ -89,6 +89,18 @@ def test_default_workspace_of_a_decode_step():
     assert mla.mla_paged_prefill_workspace(*args, *room(128, 64, 64, 64, 2048)) <= 100 << 20
 
 
+@pytest.mark.parametrize("v", [1 << 31, 1 << 32, (1 << 32) + 256, -(1 << 31) - 1])
+def test_numbers_past_32_bits_are_refused(v):
+    """ctypes would pass their low halves: 2^32 pages to keep would be none."""
+    with pytest.raises(ValueError, match="key_rows: .* 32 bits"):
+        room(128, 4, 100, 64, 100, key_rows=v)
+    with pytest.raises(ValueError, match="head_shard: .* 32 bits"):
+        room(128, 4, 100, 64, 100, head_shard=v)
+    for name in ("page_size", "keep_pages", "first_pages", "last_pages"):
+        with pytest.raises(ValueError, match=name + ": .* 32 bits"):
+            mla.paged_evict(None, None, None, **{**dict(page_size=8, keep_pages=1), name: v})
+
+
 def test_refused_sizes_have_no_room():
     assert most(128, -1, 100, 64, 100) == 0 == most(128, 4, -1, 64, 100) == most(128, 4, 100, 0, 100) == most(128, 4, 100, 64, 0)
     assert most(128, 4, 100, 64, 100, dtype=9) == 0
