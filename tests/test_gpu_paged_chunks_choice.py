@@ -92,6 +92,21 @@ def test_by_the_room(heads, lens, key_rows, want):
         check_rows(d, s, out, lse, spread(cu, b, 4))
 
 
+def test_behind_more_keys_than_the_default_room():
+    """A request of more than 65536 keys goes absorbed by default, the one behind it explicit; both with the rows given."""
+    d = mla.dims(3, **V3)
+    lens = [(66000, 300), (0, 300)]
+    s = sref.step(ref.generator(3), d, BF, lens, 64)
+    a = sref.on_gpu(s)
+    assert rule(3, lens, mla.PREFILL_KEY_ROWS) == [1] and rule(3, lens, 68000) == [0, 1]
+    cu = s["cu_tokens"].tolist()
+    for rows, want in ((None, [1]), (68000, [0, 1])):
+        got = mla.paged_prefill(d, *a, key_rows=rows)
+        assert explicit(d, s, a, got, lens) == want
+        for b in range(2):
+            check_rows(d, s, *got, spread(cu, b, 5))
+
+
 def test_more_requests_than_a_block_has_threads():
     """Past 1024 requests the room is handed on from one part of them to the next."""
     d = mla.dims(16, **V3)
