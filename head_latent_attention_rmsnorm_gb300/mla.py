@@ -859,11 +859,13 @@ def _prefill_room(d, dt, n_tokens, table_shape, page, key_rows, head_shard):
 
 
 def paged_prefill_workspace(d: Dims, n_tokens: int, c_cache, block_table, *, key_rows=None, head_shard=None) -> torch.Tensor:
-    """A workspace for :func:`paged_prefill` calls of ``n_tokens`` rows with this cache and table (and the same
+    """A workspace for :func:`paged_prefill` calls of up to ``n_tokens`` rows with this cache and table (and the same
     ``key_rows`` and ``head_shard``), one call at a time."""
-    room = _prefill_room(d, _dt(c_cache), n_tokens, block_table.shape, c_cache.shape[1], key_rows, head_shard)
-    n = lib().mla_paged_prefill_workspace(ctypes.byref(d), _dt(c_cache), block_table.shape[0], n_tokens,
-                                          c_cache.shape[1], block_table.shape[1], *room)
+    dt, (B, max_pages), page = _dt(c_cache), block_table.shape, c_cache.shape[1]
+    rooms = [_prefill_room(d, dt, n_tokens, (B, max_pages), page, key_rows, head_shard)]
+    if head_shard is None:   # steps of fewer tokens and rows may take all heads at once
+        rooms.append((min(rooms[0][0], PREFILL_ALL_HEADS // d.n_heads), 0))
+    n = max(lib().mla_paged_prefill_workspace(ctypes.byref(d), dt, B, n_tokens, page, max_pages, *room) for room in rooms)
     return torch.empty(max(n, 1), dtype=torch.uint8, device=c_cache.device)
 
 
@@ -893,8 +895,9 @@ def paged_prefill(d: Dims, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_len
     ``cu_tokens[b]`` .. ``cu_tokens[b + 1] - 1`` of ``q_nope`` [n_tokens, n_heads, d_nope] and ``q_pe`` are request
     b's, each at its position, as :func:`paged_tables` gives them.  ``key_rows`` and ``head_shard`` are the room for
     the form that serves long chunks (0 rows: without it; by default what the step can use, up to ``PREFILL_KEY_ROWS``:
-    a chunk behind more keys than that is two to three times as fast with the rows for them).  Returns (out [n_tokens, n_heads, d_v],
-    lse [n_tokens, n_heads]); rows of no request are left as they were (zeros where this call allocates)."""
+    a chunk behind more keys than that is two to three times as fast with the rows for them).  Returns
+    (out [n_tokens, n_heads, d_v], lse [n_tokens, n_heads]); rows of no request are left as they were (zeros where this
+    call allocates)."""
     if stream is not None:
         return _on_stream(stream, paged_prefill, d, q_nope, q_pe, c_cache, kpe_cache, block_table, kv_lens, cu_tokens,
                           positions, w_kv_b, key_rows=key_rows, head_shard=head_shard, out=out, lse=lse, workspace=workspace)

@@ -357,7 +357,8 @@ size_t mla_paged_decode_workspace(const mla_dims *dims, mla_dtype dtype, int B, 
  * A token that sees no key (a negative position, no pages) gives out 0 and lse -inf.  Rows of no request (in front of
  * cu_tokens[0], from cu_tokens[B] on) are left as they were.  Lengths, slots behind them and bad page ids are
  * treated as in mla_paged_decode, as are types, dimensions, determinism and the workspace.  What a token does not
- * see does not matter, but for NaN and infinity in rows of its own request behind its position, in front of the length: they may show.
+ * see does not matter, but for NaN and infinity in rows of its own request behind its position and in front of the
+ * length: they may show.
  */
 mla_status mla_paged_prefill(const mla_dims *dims, mla_dtype dtype, int B, int n_tokens, int num_pages, int page_size,
                              int max_pages, int key_rows, int head_shard, const void *q_nope, const void *q_pe,

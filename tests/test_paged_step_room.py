@@ -89,6 +89,21 @@ def test_default_workspace_of_a_decode_step():
     assert mla.mla_paged_prefill_workspace(*args, *room(128, 64, 64, 64, 2048)) <= 100 << 20
 
 
+@pytest.mark.parametrize("heads,B,page,cols", [(128, 64, 64, 100), (128, 3, 64, 128), (16, 8, 64, 700), (130, 64, 8, 3000), (20, 1, 64, 512)])
+def test_a_workspace_does_for_steps_of_fewer_tokens(heads, B, page, cols):
+    """A server allocates one for its largest step; smaller ones, whose rows may allow all heads at once, fit in it."""
+    d = mla.dims(heads, **V3)
+    cache, table = torch.empty(1, page, 512, dtype=torch.bfloat16, device="meta"), torch.empty(B, cols, dtype=torch.int32, device="meta")
+    most = 0
+    for n in (1, 32, 63, 64, 65, 100, 150, 180, 200, 220, 232, 233, 250, 300, 400, 511, 700, 1024, 2048, 4096, 5000):
+        need = mla.mla_paged_prefill_workspace(ctypes.byref(d), mla.MLA_BF16, B, n, page, cols, *room(heads, B, n, page, cols))
+        most = max(most, need)
+        assert most <= mla.paged_prefill_workspace(d, n, cache, table).numel(), n
+    for kw in (dict(key_rows=4096), dict(head_shard=5), dict(key_rows=0, head_shard=0)):
+        want = mla.mla_paged_prefill_workspace(ctypes.byref(d), mla.MLA_BF16, B, 300, page, cols, *room(heads, B, 300, page, cols, **kw))
+        assert mla.paged_prefill_workspace(d, 300, cache, table, **kw).numel() >= want
+
+
 @pytest.mark.parametrize("v", [1 << 31, 1 << 32, (1 << 32) + 256, -(1 << 31) - 1])
 def test_numbers_past_32_bits_are_refused(v):
     """ctypes would pass their low halves: 2^32 pages to keep would be none."""
